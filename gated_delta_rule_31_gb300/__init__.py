@@ -22,17 +22,30 @@ from ._build import LIB as _LIB_PATH
 from ._build import build
 
 __all__ = ["build", "fwd_chunked", "bwd_chunked", "fwd_sequential", "bwd_sequential", "decode_step", "GdrError",
-           "fwd_workspace_bytes", "bwd_workspace_bytes", "lib", "Problem", "workspace_status", "selftest_wait_expiry", "trace"]
+           "fwd_workspace_bytes", "bwd_workspace_bytes", "lib", "Problem", "workspace_status", "selftest_wait_expiry", "trace",
+           "LinearProblem", "NormProblem", "linear_fwd", "linear_bwd", "linear_decode_step", "group_norm_fwd",
+           "group_norm_bwd"]
 
 GDR_F32, GDR_BF16 = 0, 1
 GDR_GATE_SCALAR, GDR_GATE_CHANNEL = 0, 1
 GDR_ERR_INVALID_ARG, GDR_ERR_UNSUPPORTED = 1, 2
+_ACTIVATIONS = {"none": 0, "silu": 1, "sigmoid": 2}
 
 
 class Problem(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("Hk", ctypes.c_int), ("Hv", ctypes.c_int),
                 ("Dk", ctypes.c_int), ("Dv", ctypes.c_int), ("dtype", ctypes.c_int), ("gate", ctypes.c_int),
                 ("scale", ctypes.c_float), ("use_qk_l2norm", ctypes.c_int)]
+
+
+class LinearProblem(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("Hk", ctypes.c_int), ("Hv", ctypes.c_int),
+                ("Dk", ctypes.c_int), ("Dv", ctypes.c_int), ("dtype", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class NormProblem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("groups", ctypes.c_int), ("D", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("activation", ctypes.c_int), ("center", ctypes.c_int), ("eps", ctypes.c_float)]
 
 
 class GdrError(RuntimeError):
@@ -94,6 +107,19 @@ def lib():
         L.gdr_trace_collect.argtypes = [ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(ctypes.c_float),
                                         ctypes.c_int]
         L.gdr_trace_collect.restype = ctypes.c_int
+        PL, PN = ctypes.POINTER(LinearProblem), ctypes.POINTER(NormProblem)
+        for name, at in (("gdr_linear_fwd_workspace", PL), ("gdr_linear_bwd_workspace", PL),
+                         ("gdr_group_norm_bwd_workspace", PN)):
+            getattr(L, name).argtypes = [at]
+            getattr(L, name).restype = sz
+        L.gdr_linear_fwd.argtypes = [PL] + [P] * 8 + [P, sz, st]
+        L.gdr_linear_bwd.argtypes = [PL] + [P] * 12 + [P, sz, st]
+        L.gdr_linear_decode_step.argtypes = [PL] + [P] * 6 + [st]
+        L.gdr_group_norm_fwd.argtypes = [PN] + [P] * 5 + [st]
+        L.gdr_group_norm_bwd.argtypes = [PN] + [P] * 9 + [P, sz, st]
+        for name in ("gdr_linear_fwd", "gdr_linear_bwd", "gdr_linear_decode_step", "gdr_group_norm_fwd",
+                     "gdr_group_norm_bwd"):
+            getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -303,6 +329,121 @@ def decode_step(q, k, v, g, beta, state, scale=None, use_qk_l2norm=True, out=Non
     _check(lib().gdr_decode_step(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state),
                                  _ptr(o), _stream(q.device)))
     return o
+
+
+def _linear_problem(q, k, v, g, scale, decode):
+    """Checks q, k, v, g of a linear attention call and describes them."""
+    dev, nd = q.device, 3 if decode else 4
+    _need(q, "q", device=dev)
+    if q.dim() != nd or v.dim() != nd:
+        raise ValueError(f"q and v must have {nd} dimensions")
+    _need(k, "k", dtype=q.dtype, device=dev, shape=q.shape)
+    _need(v, "v", dtype=q.dtype, device=dev, shape=tuple(q.shape[:-2]) + tuple(v.shape[-2:]))
+    dtype = {torch.float32: GDR_F32, torch.bfloat16: GDR_BF16}.get(q.dtype)
+    if dtype is None:
+        raise ValueError(f"q/k/v dtype must be float32 or bfloat16, got {q.dtype}")
+    Hv, Dk = v.shape[-2], q.shape[-1]
+    _need(g, "g", dtype=torch.float32, device=dev, shape=(Hv,))
+    return LinearProblem(q.shape[0], 1 if decode else q.shape[1], q.shape[-2], Hv, Dk, v.shape[-1], dtype,
+                         Dk ** -0.5 if scale is None else float(scale))
+
+
+def _linear_extras(p, dev, h0, lengths):
+    if h0 is not None:
+        _need(h0, "h0", dtype=torch.float32, device=dev, shape=(p.B, p.Hv, p.Dv, p.Dk))
+    if lengths is not None:
+        _need(lengths, "lengths", dtype=torch.int32, device=dev, shape=(p.B,))
+
+
+def linear_fwd(q, k, v, g, h0=None, scale=None, lengths=None, output_final_state=True, workspace=None):
+    """Linear attention with a constant decay per head over T tokens (gdr_linear_fwd):
+    S_t = exp(g) S_{t-1} + v_t k_t^T, o_t = scale S_t q_t. q, k [B,T,Hk,Dk] and v [B,T,Hv,Dv] bf16
+    or fp32; g [Hv] fp32 log-decay (<= 0); h0 [B,Hv,Dv,Dk] fp32 or None (zero); lengths [B] int32
+    (device) or None: entry b has lengths[b] tokens, o is zero past them and ht is the state after
+    the last one. scale defaults to Dk^-1/2. Returns (o, ht or None)."""
+    p = _linear_problem(q, k, v, g, scale, False)
+    _linear_extras(p, q.device, h0, lengths)
+    o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+    ht = torch.empty((p.B, p.Hv, p.Dv, p.Dk), dtype=torch.float32, device=v.device) if output_final_state else None
+    ws, nbytes = _workspace(lib().gdr_linear_fwd_workspace, p, q.device, workspace)
+    _check(lib().gdr_linear_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(h0), _ptr(lengths),
+                                _ptr(o), _ptr(ht), _ptr(ws), ctypes.c_size_t(nbytes), _stream(q.device)))
+    return o, ht
+
+
+def linear_bwd(q, k, v, g, h0, do, dht=None, scale=None, lengths=None, workspace=None):
+    """VJP of linear_fwd for the loss <do, o> + <dht, ht> (gdr_linear_bwd). Returns a dict of dq,
+    dk, dv in the inputs' dtype and dh0 fp32; the decay is a constant and has no gradient."""
+    p = _linear_problem(q, k, v, g, scale, False)
+    _linear_extras(p, q.device, h0, lengths)
+    _need(do, "do", dtype=v.dtype, device=v.device, shape=v.shape)
+    if dht is not None:
+        _need(dht, "dht", dtype=torch.float32, device=v.device, shape=(p.B, p.Hv, p.Dv, p.Dk))
+    out = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
+               dh0=torch.empty((p.B, p.Hv, p.Dv, p.Dk), dtype=torch.float32, device=v.device))
+    ws, nbytes = _workspace(lib().gdr_linear_bwd_workspace, p, q.device, workspace)
+    _check(lib().gdr_linear_bwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(h0), _ptr(lengths),
+                                _ptr(do), _ptr(dht), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
+                                _ptr(out["dh0"]), _ptr(ws), ctypes.c_size_t(nbytes), _stream(q.device)))
+    return out
+
+
+def linear_decode_step(q, k, v, g, state, scale=None, out=None):
+    """One token of linear attention (gdr_linear_decode_step): q, k [B,Hk,Dk]; v [B,Hv,Dv]; g [Hv];
+    state [B,Hv,Dv,Dk] fp32 updated in place. Returns o [B,Hv,Dv]."""
+    p = _linear_problem(q, k, v, g, scale, True)
+    _need(state, "state", dtype=torch.float32, device=q.device, shape=(p.B, p.Hv, p.Dv, p.Dk))
+    o = torch.empty_like(v) if out is None else _need(out, "out", dtype=v.dtype, device=v.device, shape=v.shape)
+    _check(lib().gdr_linear_decode_step(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state), _ptr(o),
+                                        _stream(q.device)))
+    return o
+
+
+def _norm_problem(x, groups, weight, bias, gate, activation, eps, center):
+    """Checks the inputs of a group norm call and describes them."""
+    _need(x, "x")
+    dtype = {torch.float32: GDR_F32, torch.bfloat16: GDR_BF16}.get(x.dtype)
+    if dtype is None:
+        raise ValueError(f"x dtype must be float32 or bfloat16, got {x.dtype}")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}, got {activation!r}")
+    C = x.shape[-1] if x.dim() > 0 else 0
+    if groups < 1 or C < 1 or C % groups:
+        raise ValueError(f"x's last dimension must be a positive multiple of groups = {groups}, got {tuple(x.shape)}")
+    if gate is not None:
+        _need(gate, "gate", dtype=x.dtype, device=x.device, shape=x.shape)
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _need(t, name, dtype=torch.float32, device=x.device, shape=(C,))
+    return NormProblem(x.numel() // C, groups, C // groups, dtype, _ACTIVATIONS[activation], int(bool(center)), eps)
+
+
+def group_norm_fwd(x, groups, weight=None, bias=None, gate=None, activation="none", eps=1e-5, center=True, out=None):
+    """Group norm over the channels of each token (gdr_group_norm_fwd): x [..., C] bf16 or fp32,
+    normalised by `groups` runs of C / groups channels with statistics of that token alone, then
+    n = weight h + bias and y = act(n), or n act(gate) with a gate of x's shape. weight, bias [C]
+    fp32 or None; activation "none", "silu" or "sigmoid"; center=False leaves the mean in (the
+    root-mean-square form). Returns y in x's dtype; `out` may be x or gate themselves."""
+    p = _norm_problem(x, groups, weight, bias, gate, activation, eps, center)
+    y = torch.empty_like(x) if out is None else _need(out, "out", dtype=x.dtype, device=x.device, shape=x.shape)
+    _check(lib().gdr_group_norm_fwd(ctypes.byref(p), _ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(y),
+                                    _stream(x.device)))
+    return y
+
+
+def group_norm_bwd(x, groups, weight, bias, gate, dy, activation="none", eps=1e-5, center=True, workspace=None):
+    """VJP of group_norm_fwd (gdr_group_norm_bwd). Returns a dict of dx, dgate (x's dtype; dgate None
+    without a gate), dweight and dbias (fp32; None where the parameter is)."""
+    p = _norm_problem(x, groups, weight, bias, gate, activation, eps, center)
+    _need(dy, "dy", dtype=x.dtype, device=x.device, shape=x.shape)
+    out = dict(dx=torch.empty_like(x), dgate=None if gate is None else torch.empty_like(gate),
+               dweight=None if weight is None else torch.empty_like(weight),
+               dbias=None if bias is None else torch.empty_like(bias))
+    ws, nbytes = _workspace(lib().gdr_group_norm_bwd_workspace, p, x.device, workspace)
+    _check(lib().gdr_group_norm_bwd(ctypes.byref(p), _ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(dy),
+                                    _ptr(out["dx"]), _ptr(out["dgate"]), _ptr(out["dweight"]), _ptr(out["dbias"]),
+                                    _ptr(ws), ctypes.c_size_t(nbytes), _stream(x.device)))
+    return out
 
 
 def workspace_status(ws) -> int:

@@ -22,9 +22,10 @@ from __future__ import annotations
 
 import torch
 
-from . import bwd_chunked, fwd_chunked
+from . import bwd_chunked, fwd_chunked, group_norm_bwd, group_norm_fwd, linear_bwd, linear_fwd
 
-__all__ = ["gated_delta_rule", "GatedDeltaRuleFunction"]
+__all__ = ["gated_delta_rule", "GatedDeltaRuleFunction", "linear_attention", "LinearAttentionFunction", "group_norm",
+           "GroupNormFunction"]
 
 
 class GatedDeltaRuleFunction(torch.autograd.Function):
@@ -67,3 +68,52 @@ def gated_delta_rule(q, k, v, g, beta, h0=None, scale=None, use_qk_l2norm=True, 
         scale = q.shape[-1] ** -0.5
     return GatedDeltaRuleFunction.apply(q, k, v, g, beta, h0, float(scale), bool(use_qk_l2norm),
                                         bool(keep_operators))
+
+
+class LinearAttentionFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, g, h0, scale, lengths):
+        ctx.scale = scale
+        ctx.save_for_backward(q, k, v, g, h0, lengths)
+        return linear_fwd(q, k, v, g, h0, scale=scale, lengths=lengths)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, do, dht):
+        q, k, v, g, h0, lengths = ctx.saved_tensors
+        do = torch.zeros_like(v) if do is None else do.to(v.dtype).contiguous()
+        dht = None if dht is None else dht.to(torch.float32).contiguous()
+        gr = linear_bwd(q, k, v, g, h0, do, dht, scale=ctx.scale, lengths=lengths)
+        return gr["dq"], gr["dk"], gr["dv"], None, None if h0 is None else gr["dh0"], None, None
+
+
+def linear_attention(q, k, v, g, h0=None, scale=None, lengths=None):
+    """Differentiable linear attention with a constant decay per head: (o [B,T,Hv,Dv] in v's dtype,
+    ht [B,Hv,Dv,Dk] fp32), differentiable in q, k, v and h0 (their gradients in the inputs' dtype).
+
+    Arguments as gated_delta_rule_31_gb300.linear_fwd; the decay g [Hv] is a constant of the head,
+    and one that requires a gradient is refused."""
+    if g.requires_grad:
+        raise ValueError("g is a constant decay and has no gradient: pass it detached")
+    return LinearAttentionFunction.apply(q, k, v, g, h0, None if scale is None else float(scale), lengths)
+
+
+class GroupNormFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, groups, weight, bias, gate, activation, eps, center):
+        ctx.groups, ctx.kw = groups, dict(activation=activation, eps=eps, center=center)
+        ctx.save_for_backward(x, weight, bias, gate)
+        return group_norm_fwd(x, groups, weight, bias, gate, **ctx.kw)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, weight, bias, gate = ctx.saved_tensors
+        gr = group_norm_bwd(x, ctx.groups, weight, bias, gate, dy.to(x.dtype).contiguous(), **ctx.kw)
+        return gr["dx"], None, gr["dweight"], gr["dbias"], gr["dgate"], None, None, None
+
+
+def group_norm(x, groups, weight=None, bias=None, gate=None, activation="none", eps=1e-5, center=True):
+    """Differentiable group norm over the channels of each token, in x, weight, bias and gate.
+    Arguments as gated_delta_rule_31_gb300.group_norm_fwd."""
+    return GroupNormFunction.apply(x, groups, weight, bias, gate, activation, float(eps), bool(center))

@@ -1,0 +1,73 @@
+// linear.h - launch interface of the linear attention with a constant decay per head
+// (gdr_linear_*), shared by its C ABI (api_linear.cu) and its kernels.
+//
+// Per (b, hv) the state S [Dv x Dk] evolves as S_t = l S_{t-1} + v_t k_t^T with l = exp(g[hv]),
+// and its adjoint D_t = l D_{t+1} + scale do_t q_t^T. The forward and each gradient are one
+// "mix" pass over the tokens,
+//
+//     out_t = sum_{j <= t} l^(t-j) (a_t . b_j) c_j + (decayed) a_t X,
+//
+// in token order for o (a, b, c = q, k, v; X = S) and dq (do, v, k; S), in reverse order for
+// dk (v, do, q; D) and dv (k, q, do; D). The tokens are cut into segments that run in parallel:
+// a summary pass forms what each segment adds to the state, a combine step the state that
+// enters each segment, and the mix pass starts from it.
+#pragma once
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace gdr {
+
+struct LinearShape {
+    int B, T, Hk, Hv, Dk, Dv, bf16;
+    int nseg, seg_tokens;  // tokens of batch entry b in segment s: [s * seg_tokens, ...) below its length
+    const float* g;        // [Hv] log-decay
+    const int* lengths;    // [B] valid tokens, or null (T)
+};
+
+// What the segments add to the state (reverse == 0: sum of w v k^T; reverse == 1: of w do q^T).
+struct LinearSummaryArgs {
+    LinearShape s;
+    const void* rows;  // v or do [B, T, Hv, Dv]
+    const void* cols;  // k or q  [B, T, Hk, Dk]
+    float factor;      // 1, or scale in reverse
+    int reverse;
+    float* z;  // [B, Hv, nseg, Dv, Dk]
+};
+
+// z -> the state entering each segment (in place), and the state after all of them.
+struct LinearCombineArgs {
+    LinearShape s;
+    const float* init;  // [B, Hv, Dv, Dk] or null (zero)
+    int reverse;
+    float* z;
+    float* last;  // [B, Hv, Dv, Dk] or null
+};
+
+enum LinearPass { LINEAR_O = 0, LINEAR_DQ = 1, LINEAR_DK = 2, LINEAR_DV = 3 };
+
+struct LinearMixArgs {
+    LinearShape s;
+    int pass;  // LinearPass
+    const void *q, *k, *v, *do_;
+    float scale;
+    float* starts;  // state entering each segment (scratch: passes that sum value heads update it)
+    void* out;
+};
+
+int linear_segments(int B, int T, int Hv, int Dk, int Dv, int bf16);
+cudaError_t launch_linear_summary(const LinearSummaryArgs& a, cudaStream_t st);
+cudaError_t launch_linear_combine(const LinearCombineArgs& a, cudaStream_t st);
+cudaError_t launch_linear_mix(const LinearMixArgs& a, cudaStream_t st);
+
+struct LinearStepArgs {
+    int B, Hk, Hv, Dk, Dv, bf16;
+    float scale;
+    const void *q, *k, *v;
+    const float* g;
+    float* state;
+    void* o;
+};
+cudaError_t launch_linear_step(const LinearStepArgs& a, cudaStream_t st);
+
+}  // namespace gdr

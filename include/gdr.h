@@ -240,6 +240,87 @@ gdr_status gdr_fwd_chunked_noalloc(const gdr_problem* p, const void* q, const vo
  * call has run on this device. */
 gdr_status gdr_noalloc_status(gdr_stream_t stream);
 
+/* ---- Linear attention with a constant decay per head --------------------------------------
+ *
+ * The layers beside the delta rule's in a hybrid model: no correction by the prediction, and a
+ * decay that is a constant of each value head. Per batch b and value head hv (key head
+ * hk = hv / (Hv / Hk)), with l = exp(g[hv]):
+ *
+ *     S_t = l S_{t-1} + v_t k_t^T,     o_t = scale * S_t q_t
+ *
+ * Layouts as above (q, k [B,T,Hk,Dk], v, o, do [B,T,Hv,Dv] of `dtype`, states [B,Hv,Dv,Dk] fp32),
+ * with g [Hv] fp32, the log-decay, g <= 0 (l = 0 for g = -infinity). The gradients dq, dk, dv are
+ * of `dtype`, each rounded once from fp32 sums (dq, dk over the value heads of their key head);
+ * the decay is not learned and has no gradient.
+ * `lengths` [B] int32 (device memory, or NULL: T everywhere; read clamped to [0, T]): batch entry
+ * b has lengths[b] tokens. What lies past them is never used, not even where it is not finite:
+ * o, dq, dk, dv are zero there, ht is the state after the last token and dht its adjoint.
+ * As in any blocked form a value that is not finite spreads within its block: a non-finite q, k,
+ * v or do may reach earlier outputs of the same 128 tokens. */
+typedef struct {
+    int B, T, Hk, Hv, Dk, Dv; /* Hv % Hk == 0; T >= 0 (T == 1 for the decode step); Dk, Dv in {32, 64, 128} */
+    gdr_dtype dtype;
+    float scale;
+} gdr_linear_problem;
+
+/* Forward over T tokens: o and, if ht != NULL, the state after them. h0 may be NULL (zero).
+ * Workspace: gdr_linear_fwd_workspace() bytes, 256-byte aligned (0: invalid problem).
+ * Pointers 16-byte aligned (g and lengths: 4). */
+size_t gdr_linear_fwd_workspace(const gdr_linear_problem* p);
+gdr_status gdr_linear_fwd(const gdr_linear_problem* p, const void* q, const void* k, const void* v, const float* g,
+                          const float* h0, const int* lengths, void* o, float* ht, void* ws, size_t ws_bytes,
+                          gdr_stream_t stream);
+
+/* VJP of gdr_linear_fwd for the loss <do, o> + <dht, ht>: dq, dk, dv and, if dh0 != NULL, dh0.
+ * h0 and dht may be NULL (zero). Deterministic: no floating-point atomics. */
+size_t gdr_linear_bwd_workspace(const gdr_linear_problem* p);
+gdr_status gdr_linear_bwd(const gdr_linear_problem* p, const void* q, const void* k, const void* v, const float* g,
+                          const float* h0, const int* lengths, const void* do_, const float* dht, void* dq, void* dk,
+                          void* dv, float* dh0, void* ws, size_t ws_bytes, gdr_stream_t stream);
+
+/* One token (p->T must be 1; layouts without the T axis): the state is updated in place, o written. */
+gdr_status gdr_linear_decode_step(const gdr_linear_problem* p, const void* q, const void* k, const void* v,
+                                  const float* g, float* state, void* o, gdr_stream_t stream);
+
+/* ---- Group norm over the channels of each token, with an activation -----------------------
+ *
+ * The output norm of linear attention and gated delta rule layers, channels last. Row x of
+ * [rows, groups * D] (a token) is normalised by groups of D channels, with statistics of that
+ * token alone (a causal model's token must not see later ones):
+ *
+ *     h = (x - mean) / sqrt(var + eps),   n = weight * h + bias,
+ *     y = act(n)              without a gate,
+ *     y = n * act(gate)       with one
+ *
+ * mean and var (of the D values, divided by D) are per row and group; with center == 0 the mean is
+ * taken as zero (the root-mean-square form). weight and bias are [groups * D] fp32 or NULL (1, 0).
+ * x, gate, y and the gradients dy, dx, dgate are dense and of `dtype`; dweight, dbias fp32. */
+typedef enum { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1, GDR_ACT_SIGMOID = 2 } gdr_activation;
+
+#define GDR_NORM_MAX_D 8192 /* largest group; groups * D is at most 2^24 */
+
+typedef struct {
+    long long rows; /* >= 0 */
+    int groups, D;
+    gdr_dtype dtype;
+    gdr_activation activation;
+    int center; /* 1: subtract the mean; 0: not */
+    float eps;  /* > 0 */
+} gdr_norm_problem;
+
+/* Any alignment of the element; 16-byte aligned pointers and D a multiple of 16 bytes are faster.
+ * y may be x or gate itself. */
+gdr_status gdr_group_norm_fwd(const gdr_norm_problem* p, const void* x, const void* gate, const float* weight,
+                              const float* bias, void* y, gdr_stream_t stream);
+
+/* VJP: dx, dgate (given exactly when gate is) and, where not NULL, dweight and dbias, from x and
+ * the parameters alone (no saved statistics). Deterministic: sums over rows in a fixed order.
+ * Workspace: gdr_group_norm_bwd_workspace() bytes, 256-byte aligned (0: invalid problem). */
+size_t gdr_group_norm_bwd_workspace(const gdr_norm_problem* p);
+gdr_status gdr_group_norm_bwd(const gdr_norm_problem* p, const void* x, const void* gate, const float* weight,
+                              const float* bias, const void* dy, void* dx, void* dgate, float* dweight, float* dbias,
+                              void* ws, size_t ws_bytes, gdr_stream_t stream);
+
 /* Launch tracing for profiling. While enabled, every kernel the library launches is
  * bracketed by two CUDA events recorded on its own stream (host-side events only; no
  * device memory). gdr_trace_collect() waits for the recorded events, writes up to `max`
