@@ -44,7 +44,7 @@ LinearShape shape_of(const gdr_linear_problem* p, const float* g, const int* len
     LinearShape s;
     s.B = p->B; s.T = p->T; s.Hk = p->Hk; s.Hv = p->Hv; s.Dk = p->Dk; s.Dv = p->Dv;
     s.bf16 = p->dtype == GDR_BF16;
-    s.nseg = linear_segments(p->B, p->T, p->Hv, p->Dk, p->Dv, s.bf16);
+    s.nseg = s.bf16 ? linear_tc_segments(p->B, p->T, p->Hv) : linear_segments(p->B, p->T, p->Hv, p->Dv);
     const int chunks = (p->T + 127) / 128;
     s.seg_tokens = (chunks + s.nseg - 1) / s.nseg * 128;
     s.nseg = chunks > 0 ? (p->T + s.seg_tokens - 1) / s.seg_tokens : 1;
@@ -73,6 +73,18 @@ cudaError_t states(const LinearShape& s, const void* rows, const void* cols, flo
     if (cudaError_t e = launch_linear_summary(a, st)) return e;
     LinearCombineArgs c{s, init, reverse, z, last};
     return launch_linear_combine(c, st);
+}
+
+// A mix pass on the tensor cores from the state `init` before it: with several segments, the states that
+// enter them first. The first kernel of a call clears its status word.
+cudaError_t mix_tc(const LinearMixArgs& m, const void* rows, const void* cols, float factor, int reverse,
+                   const float* init, float* z, float* last, int* status, bool clear, cudaStream_t st) {
+    if (m.s.nseg == 1) return launch_linear_tc_mix(m, init, 1, last, status, clear, st);
+    LinearSummaryArgs a{m.s, rows, cols, factor, reverse, z};
+    if (cudaError_t e = launch_linear_tc_summary(a, status, clear, st)) return e;
+    LinearCombineArgs c{m.s, init, reverse, z, nullptr};
+    if (cudaError_t e = launch_linear_combine(c, st)) return e;
+    return launch_linear_tc_mix(m, z, m.s.nseg, last, status, false, st);
 }
 
 // No token: the state passes through.
@@ -143,8 +155,9 @@ gdr_status gdr_linear_fwd(const gdr_linear_problem* p, const void* q, const void
     if (p->B == 0) return GDR_OK;
     if (p->T == 0) return pass_state(p, h0, ht, st);
     float* z = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256);
-    if (states(s, v, k, 1.f, 0, h0, z, ht, st) != cudaSuccess) return GDR_ERR_CUDA;
     LinearMixArgs m{s, LINEAR_O, q, k, v, nullptr, p->scale, z, o};
+    if (s.bf16) return of(mix_tc(m, v, k, 1.f, 0, h0, z, ht, static_cast<int*>(ws), true, st));
+    if (states(s, v, k, 1.f, 0, h0, z, ht, st) != cudaSuccess) return GDR_ERR_CUDA;
     return of(launch_linear_mix(m, st));
 }
 
@@ -163,12 +176,17 @@ gdr_status gdr_linear_bwd(const gdr_linear_problem* p, const void* q, const void
     if (p->T == 0) return pass_state(p, dht, dh0, st);
     uint8_t* w = static_cast<uint8_t*>(ws) + 256;
     float *zs = reinterpret_cast<float*>(w), *zd = reinterpret_cast<float*>(w + states_bytes(s));
+    if (s.bf16) {
+        LinearMixArgs m{s, LINEAR_DV, q, k, v, do_, p->scale, zd, dv};
+        if (mix_tc(m, do_, q, p->scale, 1, dht, zd, dh0, static_cast<int*>(ws), true, st) != cudaSuccess) return GDR_ERR_CUDA;
+    }
     if (states(s, v, k, 1.f, 0, h0, zs, nullptr, st) != cudaSuccess) return GDR_ERR_CUDA;
-    if (states(s, do_, q, p->scale, 1, dht, zd, dh0, st) != cudaSuccess) return GDR_ERR_CUDA;
+    if (states(s, do_, q, p->scale, 1, dht, zd, s.bf16 ? nullptr : dh0, st) != cudaSuccess) return GDR_ERR_CUDA;
     // dv reads the reverse states, which dk, summing over value heads, may update in place: dv first
     const struct { int pass; float* z; void* out; } passes[3] = {
         {LINEAR_DQ, zs, dq}, {LINEAR_DV, zd, dv}, {LINEAR_DK, zd, dk}};
     for (const auto& x : passes) {
+        if (s.bf16 && x.pass == LINEAR_DV) continue;
         LinearMixArgs m{s, x.pass, q, k, v, do_, p->scale, x.z, x.out};
         if (launch_linear_mix(m, st) != cudaSuccess) return GDR_ERR_CUDA;
     }

@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(256) linear_combine_kernel(LinearCombineArgs a
     for (int k = 0; k < s.nseg; k++) {
         const int seg = a.reverse ? s.nseg - 1 - k : k;
         float* p = a.z + (bh * s.nseg + seg) * D + i;
-        const float4 z = load4(p);
+        const bool need = k + 1 < s.nseg || a.last;
+        const float4 z = need ? load4(p) : x;
         store4(p, x);
         const float over = power(g, max(0, min(s.seg_tokens, n - seg * s.seg_tokens)));
         x = make_float4(over * x.x + z.x, over * x.y + z.y, over * x.z + z.z, over * x.w + z.w);
@@ -354,7 +355,7 @@ cudaError_t mix_of(const LinearMixArgs& a, cudaStream_t st) {
 }  // namespace
 
 // Segments: enough CTAs for two per SM, each of whole chunks.
-int linear_segments(int B, int T, int Hv, int Dk, int Dv, int bf16) {
+int linear_segments(int B, int T, int Hv, int Dv) {
     const long long chunks = (T + LC - 1) / LC, units = (long long)B * Hv * (Dv < 64 ? 1 : Dv / 64);
     if (chunks <= 1 || units <= 0) return 1;
     const long long want = (2 * 152 + units - 1) / units;

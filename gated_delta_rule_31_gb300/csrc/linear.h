@@ -35,7 +35,8 @@ struct LinearSummaryArgs {
     float* z;  // [B, Hv, nseg, Dv, Dk]
 };
 
-// z -> the state entering each segment (in place), and the state after all of them.
+// z -> the state entering each segment (in place), and the state after all of them (with last null
+// the z of the segment processed last is not read).
 struct LinearCombineArgs {
     LinearShape s;
     const float* init;  // [B, Hv, Dv, Dk] or null (zero)
@@ -55,10 +56,19 @@ struct LinearMixArgs {
     void* out;
 };
 
-int linear_segments(int B, int T, int Hv, int Dk, int Dv, int bf16);
+int linear_segments(int B, int T, int Hv, int Dv);
 cudaError_t launch_linear_summary(const LinearSummaryArgs& a, cudaStream_t st);
 cudaError_t launch_linear_combine(const LinearCombineArgs& a, cudaStream_t st);
 cudaError_t launch_linear_mix(const LinearMixArgs& a, cudaStream_t st);
+
+// bf16 on the tensor cores (linear_tc.cu): the summary of all segments but the last in processing
+// order, and the mix passes of o and dv, which carry the state through every segment and so give the
+// state after the last. start: the state entering each segment (start_segs = nseg), or before
+// all of them (1; may be null: zero). status: status word, cleared by the kernel if `clear`.
+int linear_tc_segments(int B, int T, int Hv);
+cudaError_t launch_linear_tc_summary(const LinearSummaryArgs& a, int* status, bool clear, cudaStream_t st);
+cudaError_t launch_linear_tc_mix(const LinearMixArgs& a, const float* start, int start_segs, float* last, int* status,
+                                 bool clear, cudaStream_t st);
 
 struct LinearStepArgs {
     int B, Hk, Hv, Dk, Dv, bf16;
