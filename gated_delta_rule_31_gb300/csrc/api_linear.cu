@@ -81,10 +81,10 @@ cudaError_t mix_tc(const LinearMixArgs& m, const void* rows, const void* cols, f
                    const float* init, float* z, float* last, int* status, bool clear, cudaStream_t st) {
     if (m.s.nseg == 1) return launch_linear_tc_mix(m, init, 1, last, status, clear, st);
     LinearSummaryArgs a{m.s, rows, cols, factor, reverse, z};
-    if (cudaError_t e = launch_linear_tc_summary(a, status, clear, st)) return e;
-    LinearCombineArgs c{m.s, init, reverse, z, nullptr};
+    if (cudaError_t e = launch_linear_tc_summary(a, last != nullptr, status, clear, st)) return e;
+    LinearCombineArgs c{m.s, init, reverse, z, last};
     if (cudaError_t e = launch_linear_combine(c, st)) return e;
-    return launch_linear_tc_mix(m, z, m.s.nseg, last, status, false, st);
+    return launch_linear_tc_mix(m, z, m.s.nseg, nullptr, status, false, st);
 }
 
 // No token: the state passes through.

@@ -113,14 +113,22 @@ __global__ void __launch_bounds__(256) linear_combine_kernel(LinearCombineArgs a
     const size_t bh = (size_t)blockIdx.z * s.Hv + blockIdx.y;
     const float g = s.g[blockIdx.y];
     float4 x = a.init ? load4(a.init + bh * D + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < s.nseg; k++) {
-        const int seg = a.reverse ? s.nseg - 1 - k : k;
-        float* p = a.z + (bh * s.nseg + seg) * D + i;
-        const bool need = k + 1 < s.nseg || a.last;
-        const float4 z = need ? load4(p) : x;
-        store4(p, x);
-        const float over = power(g, max(0, min(s.seg_tokens, n - seg * s.seg_tokens)));
-        x = make_float4(over * x.x + z.x, over * x.y + z.y, over * x.z + z.z, over * x.w + z.w);
+    for (int k0 = 0; k0 < s.nseg; k0 += 8) {  // eight segments' loads in flight
+        float4 z[8];
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            const int k = k0 + e, seg = a.reverse ? s.nseg - 1 - k : k;
+            if (k < s.nseg && (k + 1 < s.nseg || a.last)) z[e] = load4(a.z + (bh * s.nseg + seg) * D + i);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            const int k = k0 + e, seg = a.reverse ? s.nseg - 1 - k : k;
+            if (k >= s.nseg) break;
+            store4(a.z + (bh * s.nseg + seg) * D + i, x);
+            if (k + 1 == s.nseg && !a.last) break;
+            const float over = power(g, max(0, min(s.seg_tokens, n - seg * s.seg_tokens)));
+            x = make_float4(over * x.x + z[e].x, over * x.y + z[e].y, over * x.z + z[e].z, over * x.w + z[e].w);
+        }
     }
     if (a.last) store4(a.last + bh * D + i, x);
 }

@@ -61,12 +61,12 @@ cudaError_t launch_linear_summary(const LinearSummaryArgs& a, cudaStream_t st);
 cudaError_t launch_linear_combine(const LinearCombineArgs& a, cudaStream_t st);
 cudaError_t launch_linear_mix(const LinearMixArgs& a, cudaStream_t st);
 
-// bf16 on the tensor cores (linear_tc.cu): the summary of all segments but the last in processing
-// order, and the mix passes of o and dv, which carry the state through every segment and so give the
-// state after the last. start: the state entering each segment (start_segs = nseg), or before
-// all of them (1; may be null: zero). status: status word, cleared by the kernel if `clear`.
+// bf16 on the tensor cores (linear_tc.cu): the summary of the segments (all of them, or all but the
+// last in processing order), and the mix passes of o and dv. start: the state entering each
+// segment (start_segs = nseg), or before all of them (1; may be null: zero). last: the state after
+// the last segment, or null. status: status word, cleared by the kernel if `clear`.
 int linear_tc_segments(int B, int T, int Hv);
-cudaError_t launch_linear_tc_summary(const LinearSummaryArgs& a, int* status, bool clear, cudaStream_t st);
+cudaError_t launch_linear_tc_summary(const LinearSummaryArgs& a, bool all, int* status, bool clear, cudaStream_t st);
 cudaError_t launch_linear_tc_mix(const LinearMixArgs& a, const float* start, int start_segs, float* last, int* status,
                                  bool clear, cudaStream_t st);
 

@@ -10,21 +10,26 @@
 //     Y = P' c, P'_rj = f l^|r-j| P_rj for j <= r (reverse: j >= r)       128 x Dv x 128
 //     X = a S^T                       128 x Dv x Dk
 //     out_r = f' l^(r+1) X_r + Y_r    (reverse: l^(m-1-r))
-//     S <- l^m S + c^T B, B_j = f'' l^(m-1-j) b_j (reverse: l^(j+1))      Dv x Dk x 128
+//     S <- l^m S + c'^T b, c'_j = f'' l^(m-1-j) c_j (reverse: l^(j+1))    Dv x Dk x 128
 //
 // All four run as tcgen05 products with 128 rows. Rounding to bf16: P' (an operand kept in TMEM), the copy
-// of S that X reads, and the result, one rounding each. B would be a fourth, and the state is
-// returned in fp32, so it enters as the sum of three bf16 terms (B to 2^-26): three products in
-// place of one, which the tensor pipe has room for beside the memory traffic. Each chunk's sum
-// starts from zero in TMEM and is added to the fp32 registers there, so the tensor core's own
-// accumulation never runs over more than one chunk.
+// of S that X reads, and the result, one rounding each. c' would be a fourth, so it enters as the
+// sum of bf16 terms: two (2^-17 off, below the other roundings) where the state only feeds X,
+// three (exact: 24 bits) where it is returned in fp32. Each chunk's sum starts from zero in TMEM
+// and is added to the fp32 registers there, so the tensor core's own accumulation never runs over more than
+// one chunk. X is scaled by its rows' decays in TMEM and Y accumulates onto it.
 //
-// Warps: 0-3 turn P into P' and finish the output (a thread is a token row), 4-11 hold the state
-// (a thread is half a state row) and form B in 16-token pieces, 12 copies tiles in, 13 issues the
-// products. Input tiles (128 tokens, two 64-channel panels, 32 KB) go through a ring of five
-// slots in the order b, a, c; the a slot takes the output tile once its products are done.
-// Channels past a head size of 32 read as zero (out of the tensor map's range), sizes of 32 and 64
-// use one panel. With 512 TMEM columns and 217 KB of shared memory one CTA runs per SM.
+// c'^T is an operand in TMEM: transposing matrix loads give each thread two tokens of a channel,
+// which is the operand's own layout, so the terms go from registers to TMEM with no pass
+// through shared memory.
+//
+// Warps: 0-7 turn P into P' and finish the output (a thread is half a token row), 8-11 hold the
+// state (a thread is a state row), 12-19 form c' in pieces of PIECE tokens (in the summary 0-7 do
+// too), 20 copies tiles in, 21 issues the products. The state rows need the registers: warps
+// 12-23 give some up (setmaxnreg). Input tiles (128 tokens, two 64-channel panels, 32 KB) go
+// through a ring of six slots in the order b, a, c; the a slot takes the output tile once its
+// products are done. Channels past a head size of 32 read as zero (out of the tensor map's range),
+// sizes of 32 and 64 use one panel. With 512 TMEM columns and 225 KB of shared memory one CTA runs per SM.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -41,20 +46,20 @@ namespace gdr {
 namespace {
 
 constexpr int C = 128;     // tokens of a chunk
-constexpr int SLOTS = 5;   // input tiles
+constexpr int SLOTS = 6;   // input tiles
 constexpr uint32_t SLOT = 32768, PANEL = 16384;
-constexpr uint32_t AT_S = SLOTS * SLOT;      // bf16 state [128 x 128]
-constexpr uint32_t AT_B = AT_S + 32768;      // two pieces of B: three terms of [16 x 128]
-constexpr uint32_t TERM = 4096, PIECE = 3 * TERM;
-constexpr uint32_t AT_PW = AT_B + 2 * PIECE; // l^0 .. l^128, then l^31 .. l^0 (16-byte aligned)
-constexpr uint32_t BYTES = AT_PW + 1024;
-static_assert(BYTES + 1024 + 512 <= 232448, "shared memory");
-constexpr int THREADS = 448;
-constexpr uint32_t COL_P = 0, COL_X = 128, COL_Y = 256, COL_S = 384;
+constexpr uint32_t AT_S = SLOTS * SLOT;     // bf16 state [128 x 128]
+constexpr uint32_t AT_W = AT_S + 32768;     // tables: 32 and 64 floats, three of 128 bf16 pairs
+constexpr uint32_t BYTES = AT_W + 384 + 1536;
+static_assert(BYTES + 256 <= 232448, "shared memory");
+constexpr int THREADS = 768;
+// Registers a thread: 768 threads start with 80; 8 warps keep them, 4 go up, 8 and 4 go down.
+constexpr int REGS = 80, REGS_STATE = 176, REGS_DECAY = 48, REGS_REST = 48;
+static_assert(2 * REGS + REGS_STATE + 2 * REGS_DECAY + REGS_REST <= 6 * REGS, "registers of the launch");
 
 struct TcArgs {
     LinearShape s;
-    int reverse, panels_k, panels_v;
+    int reverse, panels_k, panels_v, first_seg;
     float fp, fx, fu;          // f, f', f''
     const float* start;        // state entering each segment [B, Hv, start_segs, Dv, Dk], or null (zero)
     int start_segs;
@@ -67,13 +72,38 @@ struct TcArgs {
 
 __device__ __forceinline__ float power(float g, int n) { return n == 0 ? 1.f : expf(g * (float)n); }
 
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// Products are issued by the elected lane of a converged warp, which keeps their operands in uniform
+// registers: the issue is what paces them. A descriptor is a fixed high word and a low word that
+// advances by a constant per 16-wide step. (Issued by a lone thread with descriptors built for
+// each step, a product took 140 to 240 cycles, not 70.)
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride 1024, version 1, 128-byte swizzle
+__device__ __forceinline__ uint32_t lo_kmajor(uint32_t tile) { return (tile >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t lo_mnmajor(uint32_t tile) { return (tile >> 4) | ((PANEL >> 4) << 16); }
+__device__ constexpr uint32_t step_kmajor(int k) { return (k >> 2) * (PANEL >> 4) + (k & 3) * 2; }
+__device__ constexpr uint32_t step_mnmajor(int k) { return k * (2048 >> 4); }
+
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t idesc,
+                                       uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(alo), "r"(blo), "r"(idesc), "r"(accumulate), "r"(DESC_HI)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\tmov.b64 y, {%2, %5};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(blo), "r"(idesc), "r"(accumulate), "r"(DESC_HI)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
         : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
@@ -84,33 +114,103 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
         "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-
-// x, as the sum of three bf16 terms: two values packed in each word.
-__device__ __forceinline__ void split3(float x0, float x1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-    hi = pack_bf16(x0, x1);
-    const float y0 = x0 - bf16lo(hi), y1 = x1 - bf16hi(hi);
-    mid = pack_bf16(y0, y1);
-    lo = pack_bf16(y0 - bf16lo(mid), y1 - bf16hi(mid));
+// 16 lanes x 16 columns: r[2 i], r[2 i + 1] hold column 4 i + t % 4 of lanes t / 4 and t / 4 + 8.
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// Four transposed 8 x 8 tiles of 16-bit values, rows at the addresses of lanes 8 i .. 8 i + 7: thread t
+// gets values (2 (t % 4), 2 (t % 4) + 1) of column t / 4 of each.
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
 }
 
-template <bool MIX>
+// Products and sums of two values at once: fp32 pairs, and bf16 pairs with one rounding.
+__device__ __forceinline__ void scale2(float* x, float f) {
+    uint64_t v, w;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x[0]), "f"(x[1]));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(w) : "f"(f));
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(w));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x[0]), "=f"(x[1]) : "l"(v));
+}
+__device__ __forceinline__ void scale2(float* x, float f0, float f1) {
+    uint64_t v, w;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x[0]), "f"(x[1]));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(w) : "f"(f0), "f"(f1));
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(w));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x[0]), "=f"(x[1]) : "l"(v));
+}
+__device__ __forceinline__ void axpy2(float* s, float f, const float* d) {  // s <- f s + d
+    uint64_t v, w, u;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(s[0]), "f"(s[1]));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(w) : "f"(f));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(u) : "f"(d[0]), "f"(d[1]));
+    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(v) : "l"(w), "l"(u));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(s[0]), "=f"(s[1]) : "l"(v));
+}
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t bf16x2_neg(uint32_t a) { return a ^ 0x80008000u; }
+
+// A wait that parks the warp in the barrier unit (polling 22 warps take issue slots from the ones that
+// work); the bounded wait takes over after a while.
+__device__ __forceinline__ bool wait_parked(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, int site) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+    return __all_sync(0xffffffffu, ok || mbar_wait(bar, parity, abort, status, site));
+}
+
+// TERMS: bf16 terms of c' (2 or 4). MIX: the output pass, else the summary.
+template <bool MIX, int TERMS>
 __global__ void __launch_bounds__(THREADS, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                      const __grid_constant__ CUtensorMap mc, const __grid_constant__ CUtensorMap mo, TcArgs a) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* sm = align1024(smem_raw);
+    extern __shared__ __align__(1024) uint8_t sm[];  // swizzled tiles: no room for rounding up
     const uint32_t sb = smem_u32(sm);
     __shared__ uint64_t full[SLOTS], empty[SLOTS], bfull[2], bfree[2];
-    __shared__ uint64_t pfull, pready, xdone, yfull, yfree, sfull, sfree, sready, drain;
+    __shared__ uint64_t pfull, pread, xfull, pready, xdone, yfull, yfree, sfull, sfree, sready, drain;
     __shared__ uint32_t tmem_sh;
     __shared__ int abort_sh;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const LinearShape& s = a.s;
-    const int seg = MIX || !a.reverse ? blockIdx.x : blockIdx.x + 1;  // the summary leaves out the last segment
+    const int seg = a.first_seg + blockIdx.x;
     const int hv = blockIdx.y, b = blockIdx.z, hk = hv / (s.Hv / s.Hk);
     const size_t bh = (size_t)b * s.Hv + hv;
+    if (sb & 1023u) {  // never on this layout; swizzled tiles would be read wrongly
+        if (tid == 0) a.status[0] = -1;
+        return;
+    }
     constexpr int TILES = MIX ? 3 : 2;  // b, a, c or b, c
-    constexpr uint32_t COLS = MIX ? 512 : 128, CS = MIX ? COL_S : 0;
+    // TMEM columns. Output pass: P, X (then the output), the chunk's sum of the state, P' and two pieces of c';
+    // with four terms P' is packed into P instead, the first half of each 64 columns. Summary: the
+    // sum and two pieces.
+    constexpr bool APART = MIX && TERMS == 2;              // P' has columns of its own
+    constexpr int PIECE = !MIX ? 64 : 32;                  // tokens of a piece
+    constexpr int STEPS = PIECE / 16;                      // products of a piece and term
+    constexpr uint32_t STEP = 8 * TERMS;                   // columns of a step: its terms, eight each
+    constexpr uint32_t COL_P = 0, COL_X = 128, COL_S = MIX ? 256 : 0, COL_PP = APART ? 384 : 0;
+    constexpr uint32_t PP_HALF = APART ? 32 : 64;          // from the first to the second 64 tokens of P'
+    constexpr uint32_t COL_C = !MIX ? 128 : APART ? 448 : 384;
+    static_assert(COL_C + 2 * STEPS * STEP <= 512 && (TERMS == 2 || TERMS == 4), "TMEM columns");
+    constexpr int DECAY_WARPS = MIX ? 8 : 16;
 
     const int n = s.lengths ? min(max(s.lengths[b], 0), s.T) : s.T;
     const int begin = seg * s.seg_tokens, end = min(begin + s.seg_tokens, s.T);
@@ -127,36 +227,131 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; i++) {
-            mbar_init(&bfull[i], 8);
+            mbar_init(&bfull[i], DECAY_WARPS);
             mbar_init(&bfree[i], 1);
         }
         mbar_init(&pfull, 1);
-        mbar_init(&pready, 4);
+        mbar_init(&pread, 8);
+        mbar_init(&xfull, 1);
+        mbar_init(&pready, 8);
         mbar_init(&xdone, 1);
         mbar_init(&yfull, 1);
-        mbar_init(&yfree, 4);
+        mbar_init(&yfree, 8);
         mbar_init(&sfull, 1);
-        mbar_init(&sfree, 8);
-        mbar_init(&sready, 8);
+        mbar_init(&sfree, 4);
+        mbar_init(&sready, 4);
         mbar_init(&drain, 1);
         fence_barrier_init();
     }
-    float* pw = reinterpret_cast<float*>(sm + AT_PW);  // pw[i] = l^i
-    float* pd = pw + 132;                              // pd[i] = l^(31-i)
-    if (tid <= C) pw[tid] = power(s.g[hv], tid);
-    if (tid < 32) pd[tid] = power(s.g[hv], 31 - tid);
-    if (warp == 12) {
-        tmem_alloc(&tmem_sh, COLS);
+    const float g = s.g[hv];
+    float* pd = reinterpret_cast<float*>(sm + AT_W);  // l^(31-i), in reverse l^i
+    float* tri = pd + 32;                             // tri[32 + r - j]: f l^|r-j| of a pair in order, else 0
+    // parts w1, w2, w3 of f'' l^e for two tokens in a row, the first of exponent e (the next e - 1, in
+    // reverse e + 1)
+    uint32_t* parts = reinterpret_cast<uint32_t*>(tri + 64);
+    if (tid < 32) pd[tid] = power(g, a.reverse ? tid : 31 - tid);
+    if (tid < 64) tri[tid] = (a.reverse ? tid <= 32 : tid >= 32) ? a.fp * power(g, abs(tid - 32)) : 0.f;
+    if (tid < 128) {
+        float x0 = a.fu * power(g, tid), x1 = a.fu * power(g, a.reverse ? tid + 1 : max(tid - 1, 0));
+#pragma unroll
+        for (int h = 0; h < 3; h++) {
+            const uint32_t w = pack_bf16(x0, x1);
+            parts[128 * h + tid] = w;
+            x0 -= bf16lo(w);
+            x1 -= bf16hi(w);
+        }
+    }
+    if (warp == 20) {
+        tmem_alloc(&tmem_sh, 512);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = tmem_sh;
-    int loaded = 0;  // tiles asked for (warp 12)
+    int loaded = 0;  // tiles asked for (warp 20)
 
-    if (warp == 12) {
-        if (lane == 0) {
+    // Pieces of c' into TMEM, by DECAY_WARPS warps of which this is number w (warp & 3 is its TMEM quarter).
+    auto decay_pieces = [&](const int w) {
+        const int quarter = w & 3, part = w >> 2;
+        const uint32_t lanes = tm + ((uint32_t)(32 * quarter) << 16);
+        constexpr int OWN = STEPS * 4 / DECAY_WARPS;  // steps of a piece for each warp
+        int piece = 0;
+        for (int i = 0; i < nc; i++) {
+            const int m = tokens_of(i), tb = i * TILES, tc = tb + TILES - 1, nj = (m + 15) / 16;
+            const uint32_t ct = sb + tc % SLOTS * SLOT;
+            bool ok = wait_parked(&full[tc % SLOTS], tc / SLOTS & 1, &abort_sh, a.status, 60);
+            if ((m & 15) && s.lengths) {
+                // rows past the last token that enter the last 16-token step: zero, whatever they hold
+                ok = ok && wait_parked(&full[tb % SLOTS], tb / SLOTS & 1, &abort_sh, a.status, 61);
+                const int z = m + 2 * w + (lane >> 4), ch = lane & 15;
+                if (ok && z < 16 * nj) {
+                    if (ch < 8 * a.panels_v) st_shared_v4(ct + sw128_chunk(z, ch, C), 0, 0, 0, 0);
+                    if (ch < 8 * a.panels_k) st_shared_v4(sb + tb % SLOTS * SLOT + sw128_chunk(z, ch, C), 0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+            }
+            for (int j = 0; j < nj && ok; j += STEPS, piece++) {
+                const int r = piece & 1;
+                if (piece >= 2)
+                    ok = wait_parked(&bfree[r], (piece / 2 + 1) & 1, &abort_sh, a.status, 62);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int e = 0; e < OWN; e++) {
+                    const int in = part * OWN + e, t = 16 * (j + in);  // step of the piece, its first token
+                    if (j + in >= nj || quarter >= 2 * a.panels_v) continue;
+                    uint32_t v[2][4];
+#pragma unroll
+                    for (int g2 = 0; g2 < 2; g2++)
+                        ldmatrix_x4_trans(
+                            ct + sw128_chunk(t + (lane >> 4) * 8 + (lane & 7), 4 * quarter + 2 * g2 + (lane >> 3 & 1), C), v[g2]);
+                    const int u = t + 2 * (lane & 3);  // first token of v[.][0], v[.][1]; that of the others is u + 8
+                    if (t + 16 > m) {                  // nothing past the last token, whatever it holds
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            const int x = u + 8 * (k >> 1);
+                            const uint32_t keep = x + 1 < m ? 0xffffffffu : x < m ? 0xffffu : 0u;
+                            v[0][k] &= keep;
+                            v[1][k] &= keep;
+                        }
+                    }
+                    const uint32_t* w0 = parts + (a.reverse ? u + 1 : max(m - 1 - u, 0));
+                    const uint32_t* w8 = parts + (a.reverse ? u + 9 : max(m - 9 - u, 0));
+                    const uint32_t w[2][3] = {{w0[0], w0[128], TERMS == 4 ? w0[256] : 0u}, {w8[0], w8[128], TERMS == 4 ? w8[256] : 0u}};
+#pragma unroll
+                    for (int g2 = 0; g2 < 2; g2++) {
+                        uint32_t y[4 * TERMS];
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            const uint32_t x = v[g2][k], *p = w[k >> 1];
+                            y[k] = bf16x2_mul(x, p[0]);
+                            const uint32_t rest = bf16x2_fma(x, p[0], bf16x2_neg(y[k]));
+                            if (TERMS == 2) {
+                                y[4 + k] = bf16x2_fma(x, p[1], rest);
+                            } else {
+                                y[4 + k] = rest;
+                                y[8 + k] = bf16x2_mul(x, p[1]);
+                                y[12 + k] = bf16x2_fma(x, p[2], bf16x2_fma(x, p[1], bf16x2_neg(y[8 + k])));
+                            }
+                        }
+                        const uint32_t to = lanes + ((uint32_t)(16 * g2) << 16) + COL_C + (r * STEPS + in) * STEP;
+                        tmem_st_16x128b_x4(to, y);
+                        if (TERMS == 4) tmem_st_16x128b_x4(to + 16, y + 4 * (TERMS - 2));
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bfull[r]);
+            }
+            if (!ok) break;
+        }
+    };
+
+    if (warp >= 20) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
+        if (warp == 20 && lane == 0) {
             bool ok = true;
             for (int i = 0; i < nc && ok; i++) {
                 const int t0 = first + chunk_of(i) * C;
@@ -176,139 +371,189 @@ __global__ void __launch_bounds__(THREADS, 1)
                     loaded++;
                 }
             }
-        }
-    } else if (warp == 13) {
-        if (lane == 0) {
-            const int dk = 64 * a.panels_k, dv = 64 * a.panels_v;
+        } else if (warp == 21) {
+            const int dk = 4 * a.panels_k, dv = 64 * a.panels_v;  // 16-channel steps, columns
             const uint32_t id_p = idesc_bf16(128, 128, 0, 0), id_x = idesc_bf16(128, dv, 0, 0);
-            const uint32_t id_y = idesc_bf16(128, dv, 0, 1), id_s = idesc_bf16(128, dk, 1, 1);
+            const uint32_t id_y = idesc_bf16(128, dv, 0, 1), id_s = idesc_bf16(128, 16 * dk, 0, 1);
             int piece = 0;
-            for (int i = 0; i < nc; i++) {
-                const int tb = i * TILES, ta = tb + 1, tc = tb + TILES - 1;
-                const uint32_t bt = sb + tb % SLOTS * SLOT, at = sb + ta % SLOTS * SLOT, ct = sb + tc % SLOTS * SLOT;
-                const int nj = (tokens_of(i) + 15) / 16;  // 16-token steps that hold tokens
-                if (!mbar_wait(&full[tb % SLOTS], tb / SLOTS & 1, &abort_sh, a.status, 41)) break;
-                if (MIX) {
-                    if (!mbar_wait(&full[ta % SLOTS], ta / SLOTS & 1, &abort_sh, a.status, 42)) break;
-                    tc_fence_after();
-                    // P takes the columns of the previous P', which the Y product before it has read
-                    for (int k0 = 0; k0 < dk; k0 += 16)
-                        mma_bf16(tm + COL_P, desc_kmajor(at, C, 0, k0), desc_kmajor(bt, C, 0, k0), id_p, k0 > 0);
-                    mma_commit(&pfull);
-                }
-                if (!mbar_wait(&full[tc % SLOTS], tc / SLOTS & 1, &abort_sh, a.status, 43)) break;
-                if (i > 0 && !mbar_wait(&sfree, (i - 1) & 1, &abort_sh, a.status, 44)) break;
-                bool ok = true;
-                for (int j = 0; j < nj; j++, piece++) {
+            auto slot = [&](int t) { return sb + t % SLOTS * SLOT; };
+            auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
+                return wait_parked(bar, parity, &abort_sh, a.status, site);
+            };
+            auto arrived = [&](int t, int site) { return wait(&full[t % SLOTS], t / SLOTS & 1, site); };
+            auto issue_p = [&](int i) {
+                if (!MIX) return true;
+                const int tb = i * TILES, ta = tb + 1;
+                if (!arrived(tb, 41) || !arrived(ta, 42)) return false;
+                // with P' apart: P is free once its rows have read it; else the Y product before has read P'
+                if (APART && i > 0 && !wait(&pread, (i - 1) & 1, 49)) return false;
+                tc_fence_after();
+                const uint32_t ad = lo_kmajor(slot(ta)), bd = lo_kmajor(slot(tb));
+#pragma unroll
+                for (int k = 0; k < 8; k++)
+                    if (k < dk) mma_ss(tm + COL_P, ad + step_kmajor(k), bd + step_kmajor(k), id_p, k > 0);
+                commit(&pfull);
+                return true;
+            };
+            auto issue_s = [&](int i) {
+                const int tb = i * TILES, nj = (tokens_of(i) + 15) / 16;  // 16-token steps that hold tokens
+                if (!MIX && !arrived(tb, 43)) return false;
+                if (i > 0 && !wait(&sfree, (i - 1) & 1, 44)) return false;
+                for (int j = 0; j < nj; j += STEPS, piece++) {
                     const int r = piece & 1;
-                    if (!(ok = mbar_wait(&bfull[r], piece / 2 & 1, &abort_sh, a.status, 45))) break;
+                    if (!wait(&bfull[r], piece / 2 & 1, 45)) return false;
                     tc_fence_after();
-                    const uint32_t p = sb + AT_B + r * PIECE;
-                    for (int t = 2; t >= 0; t--)  // the smallest term first
-                        mma_bf16(tm + CS, desc_mnmajor(ct, C, 0, 16 * j), desc_mnmajor(p + t * TERM, 16, 0, 0), id_s,
-                                 j > 0 || t < 2);
-                    mma_commit(&bfree[r]);
+                    const uint32_t from = tm + COL_C + r * STEPS * STEP, bd = lo_mnmajor(slot(tb)) + step_mnmajor(j);
+#pragma unroll
+                    for (int e = 0; e < STEPS; e++)
+#pragma unroll
+                        for (int t = TERMS - 1; t >= 0; t--)  // the smallest term first
+                            if (j + e < nj)
+                                mma_ts(tm + COL_S, from + e * STEP + 8 * t, bd + step_mnmajor(e), id_s,
+                                       e > 0 || t < TERMS - 1 ? 1u : j > 0);
+                    commit(&bfree[r]);
                 }
-                if (!ok) break;
-                mma_commit(&sfull);
-                mma_commit(&empty[tb % SLOTS]);  // every piece has been formed from b
+                commit(&sfull);
+                commit(&empty[tb % SLOTS]);
+                if (!MIX) commit(&empty[(tb + 1) % SLOTS]);
+                return true;
+            };
+            bool ok = nc > 0 && issue_p(0) && issue_s(0);
+            for (int i = 0; i < nc && ok; i++) {
+                const int ta = i * TILES + 1, tc = i * TILES + TILES - 1, nj = (tokens_of(i) + 15) / 16;
                 if (MIX) {
-                    if (!mbar_wait(&sready, i & 1, &abort_sh, a.status, 46)) break;
-                    if (i > 0 && !mbar_wait(&yfree, (i - 1) & 1, &abort_sh, a.status, 47)) break;
+                    if (!wait(&sready, i & 1, 46)) break;
+                    if (i > 0 && !wait(&yfree, (i - 1) & 1, 47)) break;
                     tc_fence_after();
-                    for (int k0 = 0; k0 < dk; k0 += 16)
-                        mma_bf16(tm + COL_X, desc_kmajor(at, C, 0, k0), desc_kmajor(sb + AT_S, C, 0, k0), id_x, k0 > 0);
-                    mma_commit(&xdone);
-                    if (!mbar_wait(&pready, i & 1, &abort_sh, a.status, 48)) break;
+                    const uint32_t ad = lo_kmajor(slot(ta)), sd = lo_kmajor(sb + AT_S);
+#pragma unroll
+                    for (int k = 0; k < 8; k++)
+                        if (k < dk) mma_ss(tm + COL_X, ad + step_kmajor(k), sd + step_kmajor(k), id_x, k > 0);
+                    commit(&xfull);
+                    commit(&xdone);
+                    if (APART && i + 1 < nc && !issue_p(i + 1)) break;  // while X is scaled
+                    if (!wait(&pready, i & 1, 48)) break;
                     tc_fence_after();
-                    for (int j = 0; j < nj; j++)
-                        mma_bf16_ts(tm + COL_Y, tm + COL_P + 8 * j, desc_mnmajor(ct, C, 0, 16 * j), id_y, j > 0);
-                    mma_commit(&yfull);
+                    const uint32_t cd = lo_mnmajor(slot(tc));
+#pragma unroll
+                    for (int j = 0; j < 8; j++)
+                        if (j < nj)
+                            mma_ts(tm + COL_X, tm + COL_PP + 8 * (j & 3) + (j >> 2) * PP_HALF, cd + step_mnmajor(j), id_y, 1);
+                    commit(&yfull);
+                    commit(&empty[tc % SLOTS]);
+                    if (!APART && i + 1 < nc && !issue_p(i + 1)) break;
                 }
-                mma_commit(&empty[tc % SLOTS]);
+                if (i + 1 < nc && !issue_s(i + 1)) break;
             }
-            mma_commit(&drain);  // every product issued so far has completed before TMEM is released
+            commit(&drain);  // every product issued so far has completed before TMEM is released
             volatile int never = 0;
             mbar_wait(&drain, 0, &never, nullptr, 0);
         }
-    } else if (warp < 4) {
-        if (MIX) {
+    } else if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_DECAY));
+        decay_pieces(warp - 12);
+    } else if (warp < 8) {
+        if (!MIX) {
+            decay_pieces(8 + warp);
+        } else {
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
-            for (int t = max(begin, first + nc * C) + warp; t < end; t += 4)  // past the last chunk: zero
+            for (int t = max(begin, first + nc * C) + warp; t < end; t += 8)  // past the last chunk: zero
                 for (int d = 8 * lane; d < s.Dv; d += 256)
                     *reinterpret_cast<uint4*>(out + (((size_t)b * s.T + t) * s.Hv + hv) * s.Dv + d) = make_uint4(0, 0, 0, 0);
-            const int r = tid;
-            const uint32_t row = tm + ((uint32_t)(32 * warp) << 16);
+            const int quarter = warp & 3, half = warp >> 2;
+            const int r = 32 * quarter + lane;  // token row; columns 64 half ..
+            const uint32_t row = tm + ((uint32_t)(32 * quarter) << 16);
             bool bad = false;
             for (int i = 0; i < nc && !bad; i++) {
                 const int m = tokens_of(i), ta = i * TILES + 1;
-                bool ok = __all_sync(0xffffffffu, mbar_wait(&pfull, i & 1, &abort_sh, a.status, 50));
+                bool ok = wait_parked(&pfull, i & 1, &abort_sh, a.status, 50);
                 tc_fence_after();
                 if (ok) {
 #pragma unroll 1
-                    for (int cb = 0; cb < 4; cb++) {
+                    for (int h = 0; h < 2; h++) {
+                        const int cb = 2 * half + h;  // columns 32 cb ..
                         uint32_t w[16];
-                        if (a.reverse ? cb < warp : cb > warp) {  // no pair of tokens in order
+                        if (a.reverse ? cb < quarter : cb > quarter) {  // no pair of tokens in order
 #pragma unroll
                             for (int e = 0; e < 16; e++) w[e] = 0;
                         } else {
                             float p[32];
                             tmem_ld32(row + COL_P + 32 * cb, p);
                             tmem_wait_ld();
-                            if (cb == warp) {
+                            if (32 * cb + 32 > m)  // past the last token, whatever was there
 #pragma unroll
-                                for (int e = 0; e < 32; e++) {
-                                    const int d = a.reverse ? e - lane : lane - e;
-                                    p[e] = d >= 0 && 32 * cb + e < m ? a.fp * pw[max(d, 0)] * p[e] : 0.f;
-                                }
+                                for (int e = 0; e < 32; e++) p[e] = 32 * cb + e < m ? p[e] : 0.f;
+                            if (cb == quarter) {
+                                const float* in = tri + 32 + lane;
+#pragma unroll
+                                for (int e = 0; e < 32; e++) p[e] *= in[-e];
                             } else {  // l^|r-j| as l to the tokens up to this block of columns, times l to those in it
-                                const float f = a.fp * (a.reverse ? pw[32 * cb - r] : pw[r - 32 * cb - 31]);
-                                const float* in = a.reverse ? pw : pd;
+                                const float f = a.fp * power(g, a.reverse ? 32 * cb - r : r - 32 * cb - 31);
 #pragma unroll
                                 for (int e = 0; e < 32; e += 4) {
-                                    const float4 x = *reinterpret_cast<const float4*>(in + e);
-                                    p[e] *= f * x.x;
-                                    p[e + 1] *= f * x.y;
-                                    p[e + 2] *= f * x.z;
-                                    p[e + 3] *= f * x.w;
+                                    const float4 x = *reinterpret_cast<const float4*>(pd + e);
+                                    scale2(p + e, x.x, x.y);
+                                    scale2(p + e + 2, x.z, x.w);
+                                    scale2(p + e, f);
+                                    scale2(p + e + 2, f);
                                 }
-                                if (32 * cb + 32 > m)
-#pragma unroll
-                                    for (int e = 0; e < 32; e++) p[e] = 32 * cb + e < m ? p[e] : 0.f;
                             }
 #pragma unroll
                             for (int e = 0; e < 16; e++) w[e] = pack_bf16(p[2 * e], p[2 * e + 1]);
                         }
-                        // the packed block lands on columns of P that this warp has already read
-                        tmem_st16(row + COL_P + 16 * cb, w);
+                        // P' apart, or onto columns of P that this warp alone reads, and has read
+                        tmem_st16(row + COL_PP + PP_HALF * half + 16 * h, w);
+                    }
+                    if (APART) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&pread);
+                    }
+                }
+                ok = ok && wait_parked(&xfull, i & 1, &abort_sh, a.status, 52);
+                tc_fence_after();
+                if (ok) {
+                    if (half < a.panels_v) {
+                        const float f = a.fx * power(g, a.reverse ? max(m - 1 - r, 0) : r + 1);
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+                            float x[32];
+                            tmem_ld32(row + COL_X + 64 * half + 32 * h, x);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) scale2(x + e, f);
+                            tmem_st32(row + COL_X + 64 * half + 32 * h, x);
+                        }
                     }
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&pready);
                 }
-                ok = ok && __all_sync(0xffffffffu, mbar_wait(&yfull, i & 1, &abort_sh, a.status, 51));
+                ok = ok && wait_parked(&yfull, i & 1, &abort_sh, a.status, 51);
                 tc_fence_after();
-                const uint32_t stage = sb + ta % SLOTS * SLOT;
                 if (ok) {
-                    const float f = a.fx * pw[a.reverse ? max(m - 1 - r, 0) : r + 1];
-#pragma unroll 1
-                    for (int cb = 0; cb < 2 * a.panels_v; cb++) {
-                        float x[32], y[32];
-                        tmem_ld32(row + COL_X + 32 * cb, x);
-                        tmem_ld32(row + COL_Y + 32 * cb, y);
-                        tmem_wait_ld();
+                    if (half < a.panels_v) {
+                        const uint32_t stage = sb + ta % SLOTS * SLOT;
 #pragma unroll
-                        for (int e = 0; e < 32; e++) x[e] = r < m ? f * x[e] + y[e] : 0.f;
+                        for (int h = 0; h < 2; h++) {
+                            float x[32];
+                            tmem_ld32(row + COL_X + 64 * half + 32 * h, x);
+                            tmem_wait_ld();
+                            if (r >= m)
 #pragma unroll
-                        for (int e = 0; e < 4; e++) st_chunk(stage + sw128_chunk(r, 4 * cb + e, C), x + 8 * e, 1.f);
+                                for (int e = 0; e < 32; e++) x[e] = 0.f;
+#pragma unroll
+                            for (int e = 0; e < 4; e++)
+                                st_chunk(stage + sw128_chunk(r, 8 * half + 4 * h + e, C), x + 8 * e, 1.f);
+                        }
                     }
                     tc_fence_before();
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&yfree);
                 }
-                bad = bar_sync_or(1, 128, !ok || abort_sh);
+                bad = bar_sync_or(1, 256, !ok || abort_sh);
                 if (!bad && tid == 0) {
                     for (int p = 0; p < a.panels_v; p++)
                         tma_store_4d(&mo, sm + ta % SLOTS * SLOT + p * PANEL, 64 * p, hv, first + chunk_of(i) * C, b);
@@ -320,108 +565,69 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (tid == 0) bulk_wait_all();
         }
     } else {
-        const int et = tid - 128, half = (warp - 4) >> 2;
-        const int row = 32 * (warp & 3) + lane;  // state row; columns 64 half ..
-        const bool mine = half < a.panels_k;
-        const uint32_t acc = tm + ((uint32_t)(32 * (warp & 3)) << 16) + CS + 64 * half;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_STATE));
+        const int row = tid - 256;  // state row
+        const uint32_t lanes = tm + ((uint32_t)(32 * (warp & 3)) << 16);
         const size_t state = (size_t)s.Dv * s.Dk;
-        float S[64];
+        float S[128];
         {
             const float* p = a.start ? a.start + (bh * a.start_segs + (a.start_segs > 1 ? seg : 0)) * state : nullptr;
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) {
-                const bool in = MIX && p && row < s.Dv && 64 * half + e < s.Dk;
-                const float4 x = in ? *reinterpret_cast<const float4*>(p + (size_t)row * s.Dk + 64 * half + e)
+            for (int e = 0; e < 128; e += 4) {
+                const bool in = MIX && p && row < s.Dv && e < s.Dk;
+                const float4 x = in ? *reinterpret_cast<const float4*>(p + (size_t)row * s.Dk + e)
                                     : make_float4(0.f, 0.f, 0.f, 0.f);
                 S[e] = x.x; S[e + 1] = x.y; S[e + 2] = x.z; S[e + 3] = x.w;
             }
         }
         auto write_state = [&]() {  // the bf16 copy that X reads
-            if (mine)
 #pragma unroll
-                for (int e = 0; e < 8; e++) st_chunk(sb + AT_S + sw128_chunk(row, 8 * half + e, C), S + 8 * e, 1.f);
+            for (int e = 0; e < 16; e++)
+                if (e < 8 * a.panels_k) st_chunk(sb + AT_S + sw128_chunk(row, e, C), S + 8 * e, 1.f);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sready);
         };
         if (MIX) write_state();
-        int piece = 0;
-        const int u = et >> 4, ch = et & 15;  // this thread's token row and 16-byte chunk of a piece
         for (int i = 0; i < nc; i++) {
-            const int m = tokens_of(i), tb = i * TILES, tc = tb + TILES - 1, nj = (m + 15) / 16;
-            bool ok = __all_sync(0xffffffffu, mbar_wait(&full[tb % SLOTS], tb / SLOTS & 1, &abort_sh, a.status, 60));
-            if (ok && (m & 15) && s.lengths) {
-                // rows of c past the last token enter the last 16-token step: zero, whatever they hold
-                ok = __all_sync(0xffffffffu, mbar_wait(&full[tc % SLOTS], tc / SLOTS & 1, &abort_sh, a.status, 61));
-                const int z = m + u;
-                if (ok && z < 16 * nj && ch < 8 * a.panels_v)
-                    st_shared_v4(sb + tc % SLOTS * SLOT + sw128_chunk(z, ch, C), 0, 0, 0, 0);
-            }
-            for (int j = 0; j < nj && ok; j++, piece++) {
-                const int r = piece & 1;
-                if (piece >= 2)
-                    ok = __all_sync(0xffffffffu, mbar_wait(&bfree[r], (piece / 2 + 1) & 1, &abort_sh, a.status, 62));
-                if (!ok) break;
-                if (ch < 8 * a.panels_k) {
-                    const int t = 16 * j + u;
-                    const uint4 v = ld_shared_v4(sb + tb % SLOTS * SLOT + sw128_chunk(t, ch, C));
-                    const float w = t < m ? a.fu * pw[a.reverse ? t + 1 : m - 1 - t] : 0.f;
-                    float x[8];
-                    unpack8(v, x);
-                    uint32_t h[4], d[4], l[4];
-#pragma unroll
-                    for (int e = 0; e < 4; e++)
-                        split3(t < m ? w * x[2 * e] : 0.f, t < m ? w * x[2 * e + 1] : 0.f, h[e], d[e], l[e]);
-                    const uint32_t to = sb + AT_B + r * PIECE + sw128_chunk(u, ch, 16);
-                    st_shared_v4(to, h[0], h[1], h[2], h[3]);
-                    st_shared_v4(to + TERM, d[0], d[1], d[2], d[3]);
-                    st_shared_v4(to + 2 * TERM, l[0], l[1], l[2], l[3]);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bfull[r]);
-            }
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&sfull, i & 1, &abort_sh, a.status, 63));
-            if (!ok) break;
+            if (!wait_parked(&sfull, i & 1, &abort_sh, a.status, 63)) break;
             tc_fence_after();
-            const float over = pw[m];
-            if (mine) {
+            const float over = power(g, tokens_of(i));
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    float d[32];
-                    tmem_ld32(acc + 32 * h, d);
-                    tmem_wait_ld();
+            for (int h = 0; h < 4; h++) {
+                if (h >= 2 * a.panels_k) continue;
+                float d[32];
+                tmem_ld32(lanes + COL_S + 32 * h, d);
+                tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; e++) S[32 * h + e] = over * S[32 * h + e] + d[e];
-                }
+                for (int e = 0; e < 32; e += 2) axpy2(S + 32 * h + e, over, d + e);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sfree);
             if (MIX && i + 1 < nc) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&xdone, i & 1, &abort_sh, a.status, 64))) break;
+                if (!wait_parked(&xdone, i & 1, &abort_sh, a.status, 64)) break;
                 write_state();
             }
         }
         float* to = nullptr;
         if (!MIX) to = a.z + (bh * s.nseg + seg) * state;
         else if (a.last && seg == (a.reverse ? 0 : s.nseg - 1)) to = a.last + bh * state;
-        if (to && mine && row < s.Dv)
+        if (to && row < s.Dv)
 #pragma unroll
-            for (int e = 0; e < 64; e += 4)
-                if (64 * half + e < s.Dk)
-                    *reinterpret_cast<float4*>(to + (size_t)row * s.Dk + 64 * half + e) =
-                        make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+            for (int e = 0; e < 128; e += 4)
+                if (e < s.Dk)
+                    *reinterpret_cast<float4*>(to + (size_t)row * s.Dk + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
     }
     tc_fence_before();
     __syncthreads();
-    if (abort_sh && warp == 12 && lane == 0) {  // copies still in flight must land first
+    if (abort_sh && warp == 20 && lane == 0) {  // copies still in flight must land first
         volatile int never = 0;
         for (int i = loaded > SLOTS ? loaded - SLOTS : 0; i < loaded; i++)
             mbar_wait(&full[i % SLOTS], i / SLOTS & 1, &never, nullptr, 0);
     }
     __syncthreads();
-    if (warp == 12) tmem_dealloc(tm, COLS);
+    if (warp == 20) tmem_dealloc(tm, 512);
 }
 
 // Tiles of one 64-channel panel and 128 tokens of a [B, T, H, D] tensor.
@@ -433,23 +639,23 @@ int panels(int d) { return d > 64 ? 2 : 1; }
 
 // Before the tensor maps: the first runtime call of a host thread (autograd's, say) makes the device's
 // context current there, which encoding a map needs.
-template <bool MIX>
+template <bool MIX, int TERMS>
 cudaError_t allow_smem() {
-    return cudaFuncSetAttribute(linear_tc_kernel<MIX>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES + 1024);
+    return cudaFuncSetAttribute(linear_tc_kernel<MIX, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
 }
 
-template <bool MIX>
+template <bool MIX, int TERMS>
 cudaError_t launch(const CUtensorMap* maps, const TcArgs& a, int segs, const char* name, cudaStream_t st) {
     trace_begin(name, st);
-    linear_tc_kernel<MIX><<<dim3(segs, a.s.Hv, a.s.B), THREADS, BYTES + 1024, st>>>(maps[0], maps[1], maps[2], maps[3], a);
+    linear_tc_kernel<MIX, TERMS><<<dim3(segs, a.s.Hv, a.s.B), THREADS, BYTES, st>>>(maps[0], maps[1], maps[2], maps[3], a);
     trace_end(st);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_linear_tc_summary(const LinearSummaryArgs& x, int* status, bool clear, cudaStream_t st) {
-    if (cudaError_t e = allow_smem<false>()) return e;
+cudaError_t launch_linear_tc_summary(const LinearSummaryArgs& x, bool all, int* status, bool clear, cudaStream_t st) {
+    if (cudaError_t e = allow_smem<false, 4>()) return e;
     CUtensorMap maps[4];
     memset(maps, 0, sizeof(maps));
     if (!tile_map(&maps[1], x.cols, x.s, x.s.Hk, x.s.Dk) || !tile_map(&maps[2], x.rows, x.s, x.s.Hv, x.s.Dv))
@@ -463,13 +669,15 @@ cudaError_t launch_linear_tc_summary(const LinearSummaryArgs& x, int* status, bo
     a.z = x.z;
     a.status = status;
     a.clear_status = clear;
-    return launch<false>(maps, a, x.s.nseg - 1, "linear_summary", st);
+    a.first_seg = all || !x.reverse ? 0 : 1;
+    return launch<false, 4>(maps, a, all ? x.s.nseg : x.s.nseg - 1, "linear_summary", st);
 }
 
 cudaError_t launch_linear_tc_mix(const LinearMixArgs& x, const float* start, int start_segs, float* last, int* status,
                                  bool clear, cudaStream_t st) {
     const bool rev = x.pass == LINEAR_DV;
-    if (cudaError_t e = allow_smem<true>()) return e;
+    // a state that leaves the call is carried with four terms, one that only feeds X with two
+    if (cudaError_t e = last ? allow_smem<true, 4>() : allow_smem<true, 2>()) return e;
     CUtensorMap maps[4];
     if (!tile_map(&maps[0], rev ? x.k : x.q, x.s, x.s.Hk, x.s.Dk) || !tile_map(&maps[1], rev ? x.q : x.k, x.s, x.s.Hk, x.s.Dk) ||
         !tile_map(&maps[2], rev ? x.do_ : x.v, x.s, x.s.Hv, x.s.Dv) || !tile_map(&maps[3], x.out, x.s, x.s.Hv, x.s.Dv))
@@ -488,7 +696,8 @@ cudaError_t launch_linear_tc_mix(const LinearMixArgs& x, const float* start, int
     a.out = x.out;
     a.status = status;
     a.clear_status = clear;
-    return launch<true>(maps, a, x.s.nseg, rev ? "linear_dv" : "linear_o", st);
+    const char* name = rev ? "linear_dv" : "linear_o";
+    return last ? launch<true, 4>(maps, a, x.s.nseg, name, st) : launch<true, 2>(maps, a, x.s.nseg, name, st);
 }
 
 // Segments of whole chunks, one CTA each, on 152 SMs. In units of one chunk of the mix pass: a wave
