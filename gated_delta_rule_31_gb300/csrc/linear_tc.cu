@@ -26,9 +26,10 @@
 // Warps: 0-7 turn P into P' and finish the output (a thread is half a token row), 8-11 hold the
 // state (a thread is a state row), 12-19 form c' in pieces of PIECE tokens (in the summary 0-7 do
 // too), 20 copies tiles in, 21 issues the products. The state rows need the registers: warps
-// 12-23 give some up (setmaxnreg). Input tiles (128 tokens, two 64-channel panels, 32 KB) go
-// through a ring of six slots in the order b, a, c; the a slot takes the output tile once its
-// products are done. Channels past a head size of 32 read as zero (out of the tensor map's range),
+// 12-23 give some up (setmaxnreg). The products of a chunk are issued as X, the next chunk's sum of the
+// state, Y, the next chunk's P: each has the others' time to wait for the warps that feed it. Input tiles (128 tokens,
+// two 64-channel panels, 32 KB) have three slots for c, which is wanted a chunk ahead and whose
+// slot then takes the output tile, two for b and one for a (three for b in the summary). Channels past a head size of 32 read as zero (out of the tensor map's range),
 // sizes of 32 and 64 use one panel. With 512 TMEM columns and 225 KB of shared memory one CTA runs per SM.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -46,7 +47,7 @@ namespace gdr {
 namespace {
 
 constexpr int C = 128;     // tokens of a chunk
-constexpr int SLOTS = 6;   // input tiles
+constexpr int SLOTS = 6, SLOTS_C = 3;  // input tiles, those of c
 constexpr uint32_t SLOT = 32768, PANEL = 16384;
 constexpr uint32_t AT_S = SLOTS * SLOT;     // bf16 state [128 x 128]
 constexpr uint32_t AT_W = AT_S + 32768;     // tables: 32 and 64 floats, three of 128 bf16 pairs
@@ -79,7 +80,6 @@ __device__ __forceinline__ float power(float g, int n) { return n == 0 ? 1.f : e
 constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride 1024, version 1, 128-byte swizzle
 __device__ __forceinline__ uint32_t lo_kmajor(uint32_t tile) { return (tile >> 4) | (1u << 16); }
 __device__ __forceinline__ uint32_t lo_mnmajor(uint32_t tile) { return (tile >> 4) | ((PANEL >> 4) << 16); }
-__device__ constexpr uint32_t step_kmajor(int k) { return (k >> 2) * (PANEL >> 4) + (k & 3) * 2; }
 __device__ constexpr uint32_t step_mnmajor(int k) { return k * (2048 >> 4); }
 
 __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t idesc,
@@ -164,18 +164,23 @@ __device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t 
 }
 __device__ __forceinline__ uint32_t bf16x2_neg(uint32_t a) { return a ^ 0x80008000u; }
 
-// A wait that parks the warp in the barrier unit (polling 22 warps take issue slots from the ones that
-// work); the bounded wait takes over after a while.
-__device__ __forceinline__ bool wait_parked(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, int site) {
+// Bounded wait of a whole warp for phase `parity`, in few instructions, since the warps' roles share the
+// instruction caches: the warp is parked in the barrier unit for up to a millisecond at a time. Gives
+// up after about a second, leaving the site in *failed, or as soon as another warp has.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* failed, int site) {
+    const long long t0 = clock64();
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
-        : "memory");
-    return __all_sync(0xffffffffu, ok || mbar_wait(bar, parity, abort, status, site));
+    do {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+            : "memory");
+        if (!ok && clock64() - t0 > kWaitCycles) *failed = site;
+    } while (!ok && !*failed);
+    return __all_sync(0xffffffffu, ok);
 }
 
 // TERMS: bf16 terms of c' (2 or 4). MIX: the output pass, else the summary.
@@ -185,10 +190,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                      const __grid_constant__ CUtensorMap mc, const __grid_constant__ CUtensorMap mo, TcArgs a) {
     extern __shared__ __align__(1024) uint8_t sm[];  // swizzled tiles: no room for rounding up
     const uint32_t sb = smem_u32(sm);
-    __shared__ uint64_t full[SLOTS], empty[SLOTS], bfull[2], bfree[2];
-    __shared__ uint64_t pfull, pread, xfull, pready, xdone, yfull, yfree, sfull, sfree, sready, drain;
+    __shared__ uint64_t full[SLOTS], empty[SLOTS], bfull[4], bfree[4];
+    __shared__ uint64_t pfull, xfull, pready, xdone, yfull, yfree, sfull[2], sfree[2], sready, drain;
     __shared__ uint32_t tmem_sh;
-    __shared__ int abort_sh;
+    __shared__ int failed, used[SLOTS];
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const LinearShape& s = a.s;
     const int seg = a.first_seg + blockIdx.x;
@@ -198,18 +203,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (tid == 0) a.status[0] = -1;
         return;
     }
-    constexpr int TILES = MIX ? 3 : 2;  // b, a, c or b, c
-    // TMEM columns. Output pass: P, X (then the output), the chunk's sum of the state, P' and two pieces of c';
-    // with four terms P' is packed into P instead, the first half of each 64 columns. Summary: the
-    // sum and two pieces.
-    constexpr bool APART = MIX && TERMS == 2;              // P' has columns of its own
-    constexpr int PIECE = !MIX ? 64 : 32;                  // tokens of a piece
-    constexpr int STEPS = PIECE / 16;                      // products of a piece and term
-    constexpr uint32_t STEP = 8 * TERMS;                   // columns of a step: its terms, eight each
-    constexpr uint32_t COL_P = 0, COL_X = 128, COL_S = MIX ? 256 : 0, COL_PP = APART ? 384 : 0;
-    constexpr uint32_t PP_HALF = APART ? 32 : 64;          // from the first to the second 64 tokens of P'
-    constexpr uint32_t COL_C = !MIX ? 128 : APART ? 448 : 384;
-    static_assert(COL_C + 2 * STEPS * STEP <= 512 && (TERMS == 2 || TERMS == 4), "TMEM columns");
+    // TMEM columns. Output pass: P (P' packed in the first half of each 64), X and then the output, the
+    // chunk's sum of the state, a ring of pieces of c'. Summary: two sums and the ring.
+    constexpr int PIECE = !MIX ? 64 : 32;              // tokens of a piece
+    constexpr int STEPS = PIECE / 16;                  // products of a piece and term
+    constexpr uint32_t STEP = 8 * TERMS;               // columns of a step: its terms, eight each
+    constexpr uint32_t COL_P = 0, COL_X = 128, COL_S = MIX ? 256 : 0, COL_C = MIX ? 384 : 256;
+    constexpr int SUMS = MIX ? 1 : 2, RING = (512 - COL_C) / (STEPS * STEP);
+    static_assert(RING >= 2 && RING <= 4 && (TERMS == 2 || TERMS == 4), "pieces");
+    constexpr int SLOTS_B = MIX ? 2 : 3;
+    auto slot_c = [](int i) { return i % SLOTS_C; };
+    auto slot_b = [](int i) { return SLOTS_C + i % SLOTS_B; };
+    constexpr int slot_a = SLOTS - 1;
     constexpr int DECAY_WARPS = MIX ? 8 : 16;
 
     const int n = s.lengths ? min(max(s.lengths[b], 0), s.T) : s.T;
@@ -221,24 +226,26 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (tid == 0) {
         if (a.clear_status && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
             for (int i = 0; i < 4; i++) a.status[i] = 0;  // a wait expires a second later at the earliest
-        abort_sh = 0;
+        failed = 0;
         for (int i = 0; i < SLOTS; i++) {
+            used[i] = 0;
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
-        for (int i = 0; i < 2; i++) {
+        for (int i = 0; i < RING; i++) {
             mbar_init(&bfull[i], DECAY_WARPS);
             mbar_init(&bfree[i], 1);
         }
+        for (int i = 0; i < SUMS; i++) {
+            mbar_init(&sfull[i], 1);
+            mbar_init(&sfree[i], 4);
+        }
         mbar_init(&pfull, 1);
-        mbar_init(&pread, 8);
         mbar_init(&xfull, 1);
         mbar_init(&pready, 8);
         mbar_init(&xdone, 1);
         mbar_init(&yfull, 1);
         mbar_init(&yfree, 8);
-        mbar_init(&sfull, 1);
-        mbar_init(&sfree, 4);
         mbar_init(&sready, 4);
         mbar_init(&drain, 1);
         fence_barrier_init();
@@ -269,7 +276,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = tmem_sh;
-    int loaded = 0;  // tiles asked for (warp 20)
 
     // Pieces of c' into TMEM, by DECAY_WARPS warps of which this is number w (warp & 3 is its TMEM quarter).
     auto decay_pieces = [&](const int w) {
@@ -278,23 +284,22 @@ __global__ void __launch_bounds__(THREADS, 1)
         constexpr int OWN = STEPS * 4 / DECAY_WARPS;  // steps of a piece for each warp
         int piece = 0;
         for (int i = 0; i < nc; i++) {
-            const int m = tokens_of(i), tb = i * TILES, tc = tb + TILES - 1, nj = (m + 15) / 16;
-            const uint32_t ct = sb + tc % SLOTS * SLOT;
-            bool ok = wait_parked(&full[tc % SLOTS], tc / SLOTS & 1, &abort_sh, a.status, 60);
+            const int m = tokens_of(i), nj = (m + 15) / 16;
+            const uint32_t ct = sb + slot_c(i) * SLOT, bt = sb + slot_b(i) * SLOT;
+            bool ok = wait_phase(&full[slot_c(i)], i / SLOTS_C & 1, &failed, 60);
             if ((m & 15) && s.lengths) {
                 // rows past the last token that enter the last 16-token step: zero, whatever they hold
-                ok = ok && wait_parked(&full[tb % SLOTS], tb / SLOTS & 1, &abort_sh, a.status, 61);
+                ok = ok && wait_phase(&full[slot_b(i)], i / SLOTS_B & 1, &failed, 61);
                 const int z = m + 2 * w + (lane >> 4), ch = lane & 15;
                 if (ok && z < 16 * nj) {
                     if (ch < 8 * a.panels_v) st_shared_v4(ct + sw128_chunk(z, ch, C), 0, 0, 0, 0);
-                    if (ch < 8 * a.panels_k) st_shared_v4(sb + tb % SLOTS * SLOT + sw128_chunk(z, ch, C), 0, 0, 0, 0);
+                    if (ch < 8 * a.panels_k) st_shared_v4(bt + sw128_chunk(z, ch, C), 0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
             }
             for (int j = 0; j < nj && ok; j += STEPS, piece++) {
-                const int r = piece & 1;
-                if (piece >= 2)
-                    ok = wait_parked(&bfree[r], (piece / 2 + 1) & 1, &abort_sh, a.status, 62);
+                const int r = piece % RING;
+                if (piece >= RING) ok = wait_phase(&bfree[r], (piece / RING + 1) & 1, &failed, 62);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
@@ -351,111 +356,120 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     if (warp >= 20) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
-        if (warp == 20 && lane == 0) {
-            bool ok = true;
-            for (int i = 0; i < nc && ok; i++) {
-                const int t0 = first + chunk_of(i) * C;
-#pragma unroll
-                for (int t = 0; t < TILES; t++) {
-                    const int k = loaded % SLOTS;
-                    if (loaded >= SLOTS && !mbar_wait(&empty[k], (loaded / SLOTS + 1) & 1, &abort_sh, a.status, 40)) {
-                        ok = false;
-                        break;
-                    }
-                    const bool is_c = t == TILES - 1;
-                    const int panels = is_c ? a.panels_v : a.panels_k;
-                    const CUtensorMap* map = is_c ? &mc : t == 0 ? &mb : &ma;
+        if (warp == 20) {
+            auto load = [&](const CUtensorMap* map, int panels, int head, int k, int use, int i) {  // use: tiles before
+                if (use > 0 && !wait_phase(&empty[k], (use + 1) & 1, &failed, 40)) return false;
+                if (lane == 0) {
                     mbar_expect_tx(&full[k], panels * PANEL);
                     for (int p = 0; p < panels; p++)
-                        tma_load_4d(sm + k * SLOT + p * PANEL, map, 64 * p, is_c ? hv : hk, t0, b, &full[k]);
-                    loaded++;
+                        tma_load_4d(sm + k * SLOT + p * PANEL, map, 64 * p, head, first + chunk_of(i) * C, b, &full[k]);
+                    used[k] = use + 1;
                 }
+                return true;
+            };
+            for (int i = -1; i < nc; i++) {
+                if (lane == 0 && i + 2 < nc) {  // into L2, two chunks before it is wanted
+                    const int t0 = first + chunk_of(i + 2) * C;
+                    for (int p = 0; p < a.panels_v; p++) tma_prefetch_4d(&mc, 64 * p, hv, t0, b);
+                    for (int p = 0; p < a.panels_k; p++) {
+                        tma_prefetch_4d(&mb, 64 * p, hk, t0, b);
+                        if (MIX) tma_prefetch_4d(&ma, 64 * p, hk, t0, b);
+                    }
+                }
+                if (MIX && i >= 0 && !load(&ma, a.panels_k, hk, slot_a, i, i)) break;
+                if (i + 1 < nc && (!load(&mc, a.panels_v, hv, slot_c(i + 1), (i + 1) / SLOTS_C, i + 1) ||
+                                   !load(&mb, a.panels_k, hk, slot_b(i + 1), (i + 1) / SLOTS_B, i + 1)))
+                    break;
             }
         } else if (warp == 21) {
-            const int dk = 4 * a.panels_k, dv = 64 * a.panels_v;  // 16-channel steps, columns
+            const int dk = 64 * a.panels_k, dv = 64 * a.panels_v;
             const uint32_t id_p = idesc_bf16(128, 128, 0, 0), id_x = idesc_bf16(128, dv, 0, 0);
-            const uint32_t id_y = idesc_bf16(128, dv, 0, 1), id_s = idesc_bf16(128, 16 * dk, 0, 1);
+            const uint32_t id_y = idesc_bf16(128, dv, 0, 1), id_s = idesc_bf16(128, dk, 0, 1);
             int piece = 0;
-            auto slot = [&](int t) { return sb + t % SLOTS * SLOT; };
             auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
-                return wait_parked(bar, parity, &abort_sh, a.status, site);
+                return wait_phase(bar, parity, &failed, site);
             };
-            auto arrived = [&](int t, int site) { return wait(&full[t % SLOTS], t / SLOTS & 1, site); };
-            auto issue_p = [&](int i) {
-                if (!MIX) return true;
-                const int tb = i * TILES, ta = tb + 1;
-                if (!arrived(tb, 41) || !arrived(ta, 42)) return false;
-                // with P' apart: P is free once its rows have read it; else the Y product before has read P'
-                if (APART && i > 0 && !wait(&pread, (i - 1) & 1, 49)) return false;
+            auto issue_p = [&](int i) {  // over P', which the Y product before has read
+                if (!wait(&full[slot_b(i)], i / SLOTS_B & 1, 41) || !wait(&full[slot_a], i & 1, 42)) return false;
                 tc_fence_after();
-                const uint32_t ad = lo_kmajor(slot(ta)), bd = lo_kmajor(slot(tb));
+                const uint32_t ad = lo_kmajor(sb + slot_a * SLOT), bd = lo_kmajor(sb + slot_b(i) * SLOT);
+#pragma unroll 1
+                for (int p = 0; p < a.panels_k; p++)
 #pragma unroll
-                for (int k = 0; k < 8; k++)
-                    if (k < dk) mma_ss(tm + COL_P, ad + step_kmajor(k), bd + step_kmajor(k), id_p, k > 0);
+                    for (int k = 0; k < 4; k++)
+                        mma_ss(tm + COL_P, ad + p * (PANEL >> 4) + 2 * k, bd + p * (PANEL >> 4) + 2 * k, id_p, k > 0 ? 1u : p);
                 commit(&pfull);
+                commit(&empty[slot_b(i)]);  // the sum of the state read it before
                 return true;
             };
             auto issue_s = [&](int i) {
-                const int tb = i * TILES, nj = (tokens_of(i) + 15) / 16;  // 16-token steps that hold tokens
-                if (!MIX && !arrived(tb, 43)) return false;
-                if (i > 0 && !wait(&sfree, (i - 1) & 1, 44)) return false;
+                const int nj = (tokens_of(i) + 15) / 16;  // 16-token steps that hold tokens
+                if (!wait(&full[slot_b(i)], i / SLOTS_B & 1, 43)) return false;
+                if (i >= SUMS && !wait(&sfree[i % SUMS], (i / SUMS + 1) & 1, 44)) return false;
+                const uint32_t sum = tm + COL_S + 128 * (i % SUMS);
                 for (int j = 0; j < nj; j += STEPS, piece++) {
-                    const int r = piece & 1;
-                    if (!wait(&bfull[r], piece / 2 & 1, 45)) return false;
+                    const int r = piece % RING;
+                    if (!wait(&bfull[r], piece / RING & 1, 45)) return false;
                     tc_fence_after();
-                    const uint32_t from = tm + COL_C + r * STEPS * STEP, bd = lo_mnmajor(slot(tb)) + step_mnmajor(j);
+                    const uint32_t from = tm + COL_C + r * STEPS * STEP, bd = lo_mnmajor(sb + slot_b(i) * SLOT) + step_mnmajor(j);
 #pragma unroll
                     for (int e = 0; e < STEPS; e++)
 #pragma unroll
                         for (int t = TERMS - 1; t >= 0; t--)  // the smallest term first
                             if (j + e < nj)
-                                mma_ts(tm + COL_S, from + e * STEP + 8 * t, bd + step_mnmajor(e), id_s,
+                                mma_ts(sum, from + e * STEP + 8 * t, bd + step_mnmajor(e), id_s,
                                        e > 0 || t < TERMS - 1 ? 1u : j > 0);
                     commit(&bfree[r]);
                 }
-                commit(&sfull);
-                commit(&empty[tb % SLOTS]);
-                if (!MIX) commit(&empty[(tb + 1) % SLOTS]);
+                commit(&sfull[i % SUMS]);
+                if (!MIX) {
+                    commit(&empty[slot_b(i)]);
+                    commit(&empty[slot_c(i)]);
+                }
                 return true;
             };
-            bool ok = nc > 0 && issue_p(0) && issue_s(0);
-            for (int i = 0; i < nc && ok; i++) {
-                const int ta = i * TILES + 1, tc = i * TILES + TILES - 1, nj = (tokens_of(i) + 15) / 16;
-                if (MIX) {
+#pragma unroll 1
+            for (int i = -1; i < nc; i++) {
+                const bool now = MIX && i >= 0;
+                if (now) {
                     if (!wait(&sready, i & 1, 46)) break;
                     if (i > 0 && !wait(&yfree, (i - 1) & 1, 47)) break;
                     tc_fence_after();
-                    const uint32_t ad = lo_kmajor(slot(ta)), sd = lo_kmajor(sb + AT_S);
+                    const uint32_t ad = lo_kmajor(sb + slot_a * SLOT), sd = lo_kmajor(sb + AT_S);
+#pragma unroll 1
+                    for (int p = 0; p < a.panels_k; p++)
 #pragma unroll
-                    for (int k = 0; k < 8; k++)
-                        if (k < dk) mma_ss(tm + COL_X, ad + step_kmajor(k), sd + step_kmajor(k), id_x, k > 0);
+                        for (int k = 0; k < 4; k++)
+                            mma_ss(tm + COL_X, ad + p * (PANEL >> 4) + 2 * k, sd + p * (PANEL >> 4) + 2 * k, id_x, k > 0 ? 1u : p);
                     commit(&xfull);
                     commit(&xdone);
-                    if (APART && i + 1 < nc && !issue_p(i + 1)) break;  // while X is scaled
-                    if (!wait(&pready, i & 1, 48)) break;
-                    tc_fence_after();
-                    const uint32_t cd = lo_mnmajor(slot(tc));
-#pragma unroll
-                    for (int j = 0; j < 8; j++)
-                        if (j < nj)
-                            mma_ts(tm + COL_X, tm + COL_PP + 8 * (j & 3) + (j >> 2) * PP_HALF, cd + step_mnmajor(j), id_y, 1);
-                    commit(&yfull);
-                    commit(&empty[tc % SLOTS]);
-                    if (!APART && i + 1 < nc && !issue_p(i + 1)) break;
+                    commit(&empty[slot_a]);  // P read it before
                 }
                 if (i + 1 < nc && !issue_s(i + 1)) break;
+                if (now) {
+                    const int nj = (tokens_of(i) + 15) / 16;
+                    if (!wait(&pready, i & 1, 48)) break;
+                    tc_fence_after();
+                    const uint32_t cd = lo_mnmajor(sb + slot_c(i) * SLOT);
+#pragma unroll 1
+                    for (int h = 0; 4 * h < nj; h++)  // P' of tokens 64 .. starts at column 64
+#pragma unroll
+                        for (int j = 0; j < 4; j++)
+                            if (4 * h + j < nj)
+                                mma_ts(tm + COL_X, tm + COL_P + 64 * h + 8 * j, cd + h * step_mnmajor(4) + step_mnmajor(j), id_y, 1);
+                    commit(&yfull);
+                }
+                if (MIX && i + 1 < nc && !issue_p(i + 1)) break;
             }
             commit(&drain);  // every product issued so far has completed before TMEM is released
-            volatile int never = 0;
-            mbar_wait(&drain, 0, &never, nullptr, 0);
+            int never = 0;
+            wait_phase(&drain, 0, &never, 1);
         }
-    } else if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_DECAY));
-        decay_pieces(warp - 12);
+    } else if (warp >= 12 || (!MIX && warp < 8)) {
+        if (warp >= 12) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_DECAY));
+        decay_pieces(warp >= 12 ? warp - 12 : 8 + warp);
     } else if (warp < 8) {
-        if (!MIX) {
-            decay_pieces(8 + warp);
-        } else {
+        if (MIX) {
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
             for (int t = max(begin, first + nc * C) + warp; t < end; t += 8)  // past the last chunk: zero
                 for (int d = 8 * lane; d < s.Dv; d += 256)
@@ -465,8 +479,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             const uint32_t row = tm + ((uint32_t)(32 * quarter) << 16);
             bool bad = false;
             for (int i = 0; i < nc && !bad; i++) {
-                const int m = tokens_of(i), ta = i * TILES + 1;
-                bool ok = wait_parked(&pfull, i & 1, &abort_sh, a.status, 50);
+                const int m = tokens_of(i);
+                bool ok = wait_phase(&pfull, i & 1, &failed, 50);
                 tc_fence_after();
                 if (ok) {
 #pragma unroll 1
@@ -501,21 +515,16 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                             for (int e = 0; e < 16; e++) w[e] = pack_bf16(p[2 * e], p[2 * e + 1]);
                         }
-                        // P' apart, or onto columns of P that this warp alone reads, and has read
-                        tmem_st16(row + COL_PP + PP_HALF * half + 16 * h, w);
-                    }
-                    if (APART) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&pread);
+                        // onto columns of P that this warp alone reads, and has read
+                        tmem_st16(row + COL_P + 64 * half + 16 * h, w);
                     }
                 }
-                ok = ok && wait_parked(&xfull, i & 1, &abort_sh, a.status, 52);
+                ok = ok && wait_phase(&xfull, i & 1, &failed, 52);
                 tc_fence_after();
                 if (ok) {
                     if (half < a.panels_v) {
                         const float f = a.fx * power(g, a.reverse ? max(m - 1 - r, 0) : r + 1);
-#pragma unroll
+#pragma unroll 1
                         for (int h = 0; h < 2; h++) {
                             float x[32];
                             tmem_ld32(row + COL_X + 64 * half + 32 * h, x);
@@ -530,12 +539,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&pready);
                 }
-                ok = ok && wait_parked(&yfull, i & 1, &abort_sh, a.status, 51);
+                ok = ok && wait_phase(&yfull, i & 1, &failed, 51);
                 tc_fence_after();
                 if (ok) {
                     if (half < a.panels_v) {
-                        const uint32_t stage = sb + ta % SLOTS * SLOT;
-#pragma unroll
+                        const uint32_t stage = sb + slot_c(i) * SLOT;
+#pragma unroll 1
                         for (int h = 0; h < 2; h++) {
                             float x[32];
                             tmem_ld32(row + COL_X + 64 * half + 32 * h, x);
@@ -553,13 +562,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&yfree);
                 }
-                bad = bar_sync_or(1, 256, !ok || abort_sh);
+                bad = bar_sync_or(1, 256, !ok || failed);
                 if (!bad && tid == 0) {
                     for (int p = 0; p < a.panels_v; p++)
-                        tma_store_4d(&mo, sm + ta % SLOTS * SLOT + p * PANEL, 64 * p, hv, first + chunk_of(i) * C, b);
+                        tma_store_4d(&mo, sm + slot_c(i) * SLOT + p * PANEL, 64 * p, hv, first + chunk_of(i) * C, b);
                     bulk_commit();
                     bulk_wait_read_all();
-                    mbar_arrive(&empty[ta % SLOTS]);
+                    mbar_arrive(&empty[slot_c(i)]);
                 }
             }
             if (tid == 0) bulk_wait_all();
@@ -590,23 +599,23 @@ __global__ void __launch_bounds__(THREADS, 1)
         };
         if (MIX) write_state();
         for (int i = 0; i < nc; i++) {
-            if (!wait_parked(&sfull, i & 1, &abort_sh, a.status, 63)) break;
+            if (!wait_phase(&sfull[i % SUMS], i / SUMS & 1, &failed, 63)) break;
             tc_fence_after();
             const float over = power(g, tokens_of(i));
 #pragma unroll
             for (int h = 0; h < 4; h++) {
                 if (h >= 2 * a.panels_k) continue;
                 float d[32];
-                tmem_ld32(lanes + COL_S + 32 * h, d);
+                tmem_ld32(lanes + COL_S + 128 * (i % SUMS) + 32 * h, d);
                 tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) axpy2(S + 32 * h + e, over, d + e);
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sfree);
+            if (lane == 0) mbar_arrive(&sfree[i % SUMS]);
             if (MIX && i + 1 < nc) {
-                if (!wait_parked(&xdone, i & 1, &abort_sh, a.status, 64)) break;
+                if (!wait_phase(&xdone, i & 1, &failed, 64)) break;
                 write_state();
             }
         }
@@ -621,10 +630,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (abort_sh && warp == 20 && lane == 0) {  // copies still in flight must land first
-        volatile int never = 0;
-        for (int i = loaded > SLOTS ? loaded - SLOTS : 0; i < loaded; i++)
-            mbar_wait(&full[i % SLOTS], i / SLOTS & 1, &never, nullptr, 0);
+    if (failed && tid == 0) {
+        if (atomicCAS(a.status, 0, DEV_TIMEOUT) == 0) {
+            a.status[1] = blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z);
+            a.status[2] = failed;
+        }
+        int never = 0;
+        for (int k = 0; k < SLOTS; k++)  // copies still in flight must land first
+            if (used[k]) mbar_wait(&full[k], (used[k] - 1) & 1, &never, nullptr, 0);
     }
     __syncthreads();
     if (warp == 20) tmem_dealloc(tm, 512);
