@@ -109,16 +109,19 @@ def lib():
         L.gdr_trace_collect.restype = ctypes.c_int
         PL, PN = ctypes.POINTER(LinearProblem), ctypes.POINTER(NormProblem)
         for name, at in (("gdr_linear_fwd_workspace", PL), ("gdr_linear_bwd_workspace", PL),
+                         ("gdr_linear_states_bytes", PL), ("gdr_linear_bwd_states_workspace", PL),
                          ("gdr_group_norm_bwd_workspace", PN)):
             getattr(L, name).argtypes = [at]
             getattr(L, name).restype = sz
         L.gdr_linear_fwd.argtypes = [PL] + [P] * 8 + [P, sz, st]
         L.gdr_linear_bwd.argtypes = [PL] + [P] * 12 + [P, sz, st]
+        L.gdr_linear_fwd_states.argtypes = [PL] + [P] * 8 + [P, sz, P, sz, st]
+        L.gdr_linear_bwd_states.argtypes = [PL] + [P] * 6 + [P, sz] + [P] * 6 + [P, sz, st]
         L.gdr_linear_decode_step.argtypes = [PL] + [P] * 6 + [st]
         L.gdr_group_norm_fwd.argtypes = [PN] + [P] * 5 + [st]
         L.gdr_group_norm_bwd.argtypes = [PN] + [P] * 9 + [P, sz, st]
-        for name in ("gdr_linear_fwd", "gdr_linear_bwd", "gdr_linear_decode_step", "gdr_group_norm_fwd",
-                     "gdr_group_norm_bwd"):
+        for name in ("gdr_linear_fwd", "gdr_linear_bwd", "gdr_linear_fwd_states", "gdr_linear_bwd_states",
+                     "gdr_linear_decode_step", "gdr_group_norm_fwd", "gdr_group_norm_bwd"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -355,24 +358,34 @@ def _linear_extras(p, dev, h0, lengths):
         _need(lengths, "lengths", dtype=torch.int32, device=dev, shape=(p.B,))
 
 
-def linear_fwd(q, k, v, g, h0=None, scale=None, lengths=None, output_final_state=True, workspace=None):
+def linear_fwd(q, k, v, g, h0=None, scale=None, lengths=None, output_final_state=True, workspace=None,
+               save_states=False):
     """Linear attention with a constant decay per head over T tokens (gdr_linear_fwd):
     S_t = exp(g) S_{t-1} + v_t k_t^T, o_t = scale S_t q_t. q, k [B,T,Hk,Dk] and v [B,T,Hv,Dv] bf16
     or fp32; g [Hv] fp32 log-decay (<= 0); h0 [B,Hv,Dv,Dk] fp32 or None (zero); lengths [B] int32
     (device) or None: entry b has lengths[b] tokens, o is zero past them and ht is the state after
-    the last one. scale defaults to Dk^-1/2. Returns (o, ht or None)."""
+    the last one. scale defaults to Dk^-1/2. Returns (o, ht or None), or (o, ht, states) with
+    save_states=True (gdr_linear_fwd_states: what linear_bwd(..., states=states) need not form again)."""
     p = _linear_problem(q, k, v, g, scale, False)
     _linear_extras(p, q.device, h0, lengths)
     o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
     ht = torch.empty((p.B, p.Hv, p.Dv, p.Dk), dtype=torch.float32, device=v.device) if output_final_state else None
-    ws, nbytes = _workspace(lib().gdr_linear_fwd_workspace, p, q.device, workspace)
-    _check(lib().gdr_linear_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(h0), _ptr(lengths),
+    L = lib()
+    ws, nbytes = _workspace(L.gdr_linear_fwd_workspace, p, q.device, workspace)
+    if not save_states:
+        _check(L.gdr_linear_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(h0), _ptr(lengths),
                                 _ptr(o), _ptr(ht), _ptr(ws), ctypes.c_size_t(nbytes), _stream(q.device)))
-    return o, ht
+        return o, ht
+    states = torch.empty(max(int(L.gdr_linear_states_bytes(ctypes.byref(p))), 256), dtype=torch.uint8, device=q.device)
+    _check(L.gdr_linear_fwd_states(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(h0), _ptr(lengths),
+                                   _ptr(o), _ptr(ht), _ptr(states), ctypes.c_size_t(states.numel()), _ptr(ws),
+                                   ctypes.c_size_t(nbytes), _stream(q.device)))
+    return o, ht, states
 
 
-def linear_bwd(q, k, v, g, h0, do, dht=None, scale=None, lengths=None, workspace=None):
-    """VJP of linear_fwd for the loss <do, o> + <dht, ht> (gdr_linear_bwd). Returns a dict of dq,
+def linear_bwd(q, k, v, g, h0, do, dht=None, scale=None, lengths=None, workspace=None, states=None):
+    """VJP of linear_fwd for the loss <do, o> + <dht, ht> (gdr_linear_bwd, or gdr_linear_bwd_states
+    with the `states` of linear_fwd(save_states=True) on the same inputs). Returns a dict of dq,
     dk, dv in the inputs' dtype and dh0 fp32; the decay is a constant and has no gradient."""
     p = _linear_problem(q, k, v, g, scale, False)
     _linear_extras(p, q.device, h0, lengths)
@@ -381,10 +394,18 @@ def linear_bwd(q, k, v, g, h0, do, dht=None, scale=None, lengths=None, workspace
         _need(dht, "dht", dtype=torch.float32, device=v.device, shape=(p.B, p.Hv, p.Dv, p.Dk))
     out = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
                dh0=torch.empty((p.B, p.Hv, p.Dv, p.Dk), dtype=torch.float32, device=v.device))
-    ws, nbytes = _workspace(lib().gdr_linear_bwd_workspace, p, q.device, workspace)
-    _check(lib().gdr_linear_bwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(h0), _ptr(lengths),
-                                _ptr(do), _ptr(dht), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
-                                _ptr(out["dh0"]), _ptr(ws), ctypes.c_size_t(nbytes), _stream(q.device)))
+    grads = [_ptr(out[n]) for n in ("dq", "dk", "dv", "dh0")]
+    ins = [_ptr(t) for t in (q, k, v, g, h0, lengths)]
+    L = lib()
+    if states is None:
+        ws, nbytes = _workspace(L.gdr_linear_bwd_workspace, p, q.device, workspace)
+        _check(L.gdr_linear_bwd(ctypes.byref(p), *ins, _ptr(do), _ptr(dht), *grads, _ptr(ws), ctypes.c_size_t(nbytes),
+                                _stream(q.device)))
+        return out
+    _need(states, "states", dtype=torch.uint8, device=q.device)
+    ws, nbytes = _workspace(L.gdr_linear_bwd_states_workspace, p, q.device, workspace)
+    _check(L.gdr_linear_bwd_states(ctypes.byref(p), *ins, _ptr(states), ctypes.c_size_t(states.numel()), _ptr(do),
+                                   _ptr(dht), *grads, _ptr(ws), ctypes.c_size_t(nbytes), _stream(q.device)))
     return out
 
 

@@ -74,16 +74,19 @@ class LinearAttentionFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, g, h0, scale, lengths):
         ctx.scale = scale
-        ctx.save_for_backward(q, k, v, g, h0, lengths)
-        return linear_fwd(q, k, v, g, h0, scale=scale, lengths=lengths)
+        if not any(ctx.needs_input_grad):
+            return linear_fwd(q, k, v, g, h0, scale=scale, lengths=lengths)
+        o, ht, states = linear_fwd(q, k, v, g, h0, scale=scale, lengths=lengths, save_states=True)
+        ctx.save_for_backward(q, k, v, g, h0, lengths, states)
+        return o, ht
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, do, dht):
-        q, k, v, g, h0, lengths = ctx.saved_tensors
+        q, k, v, g, h0, lengths, states = ctx.saved_tensors
         do = torch.zeros_like(v) if do is None else do.to(v.dtype).contiguous()
         dht = None if dht is None else dht.to(torch.float32).contiguous()
-        gr = linear_bwd(q, k, v, g, h0, do, dht, scale=ctx.scale, lengths=lengths)
+        gr = linear_bwd(q, k, v, g, h0, do, dht, scale=ctx.scale, lengths=lengths, states=states)
         return gr["dq"], gr["dk"], gr["dv"], None, None if h0 is None else gr["dh0"], None, None
 
 
@@ -92,7 +95,8 @@ def linear_attention(q, k, v, g, h0=None, scale=None, lengths=None):
     ht [B,Hv,Dv,Dk] fp32), differentiable in q, k, v and h0 (their gradients in the inputs' dtype).
 
     Arguments as gated_delta_rule_31_gb300.linear_fwd; the decay g [Hv] is a constant of the head,
-    and one that requires a gradient is refused."""
+    and one that requires a gradient is refused. With bf16 inputs the forward keeps the state that
+    each 128-token chunk starts from for the backward (32 KB per chunk and value head)."""
     if g.requires_grad:
         raise ValueError("g is a constant decay and has no gradient: pass it detached")
     return LinearAttentionFunction.apply(q, k, v, g, h0, None if scale is None else float(scale), lengths)

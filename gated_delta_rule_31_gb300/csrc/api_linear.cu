@@ -16,6 +16,7 @@ using namespace gdr;
 namespace {
 
 bool on(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+size_t round_up(size_t x, size_t to) { return (x + to - 1) / to * to; }
 bool dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
 
 gdr_status check_problem(const gdr_linear_problem* p, bool decode) {
@@ -57,12 +58,25 @@ LinearShape shape_of(const gdr_linear_problem* p, const float* g, const int* len
 size_t states_bytes(const LinearShape& s) {
     return (size_t)s.B * s.Hv * s.nseg * s.Dv * s.Dk * sizeof(float);
 }
+// Kept chunk states (bf16 only): a 32 KB tile for each (b, hv, 128-token chunk).
+size_t kept_bytes(const LinearShape& s) { return s.bf16 ? (size_t)s.B * s.Hv * ((s.T + 127) / 128) * 32768 : 0; }
+size_t tokens_bytes(const LinearShape& s) { return round_up((size_t)s.B * s.T * s.Hv * s.Dv * 2, 256); }
 size_t fwd_bytes(const LinearShape& s) { return 256 + states_bytes(s); }
-size_t bwd_bytes(const LinearShape& s) { return 256 + 2 * states_bytes(s); }
+// bf16: segment states, the adjoints of the chunks' states and, unless the forward kept them, their
+// states, formed again by an output pass whose output goes nowhere else. fp32: both segment states.
+size_t bwd_bytes(const LinearShape& s, bool kept) {
+    if (!s.bf16) return 256 + 2 * states_bytes(s);
+    return 256 + states_bytes(s) + kept_bytes(s) + (kept ? 0 : kept_bytes(s) + tokens_bytes(s));
+}
 
 gdr_status check_ws(const void* ws, size_t have, size_t need) {
     if (!ws || have < need) return GDR_ERR_WORKSPACE;
     return on(ws, 256) ? GDR_OK : GDR_ERR_INVALID_ARG;
+}
+gdr_status check_kept(const void* kept, size_t have, const LinearShape& s) {
+    const size_t need = kept_bytes(s);
+    if (need && (!kept || have < need)) return GDR_ERR_WORKSPACE;
+    return on(kept, 256) ? GDR_OK : GDR_ERR_INVALID_ARG;
 }
 gdr_status of(cudaError_t e) { return e == cudaSuccess ? GDR_OK : GDR_ERR_CUDA; }
 
@@ -136,61 +150,110 @@ size_t gdr_linear_fwd_workspace(const gdr_linear_problem* p) {
     return fwd_bytes(shape_of(p, nullptr, nullptr));
 }
 
-size_t gdr_linear_bwd_workspace(const gdr_linear_problem* p) {
+size_t gdr_linear_states_bytes(const gdr_linear_problem* p) {
     if (check_problem(p, false) != GDR_OK) return 0;
-    return bwd_bytes(shape_of(p, nullptr, nullptr));
+    return kept_bytes(shape_of(p, nullptr, nullptr));
 }
 
-gdr_status gdr_linear_fwd(const gdr_linear_problem* p, const void* q, const void* k, const void* v, const float* g,
-                          const float* h0, const int* lengths, void* o, float* ht, void* ws, size_t ws_bytes,
-                          gdr_stream_t stream) {
+size_t gdr_linear_bwd_workspace(const gdr_linear_problem* p) {
+    if (check_problem(p, false) != GDR_OK) return 0;
+    return bwd_bytes(shape_of(p, nullptr, nullptr), false);
+}
+
+size_t gdr_linear_bwd_states_workspace(const gdr_linear_problem* p) {
+    if (check_problem(p, false) != GDR_OK) return 0;
+    return bwd_bytes(shape_of(p, nullptr, nullptr), true);
+}
+
+static gdr_status linear_fwd_impl(const gdr_linear_problem* p, const void* q, const void* k, const void* v,
+                                  const float* g, const float* h0, const int* lengths, void* o, float* ht, bool keep,
+                                  void* kept, size_t have, void* ws, size_t ws_bytes, cudaStream_t st) {
     gdr_status r = check_problem(p, false);
     if (r != GDR_OK) return r;
     const bool empty = p->B == 0 || p->T == 0;
     if ((r = check_ptrs(empty, {q, k, v, o}, {h0, ht})) != GDR_OK) return r;
     if (!g || !on(g, 4) || !on(lengths, 4)) return GDR_ERR_INVALID_ARG;
     const LinearShape s = shape_of(p, g, lengths);
+    if (keep && (r = check_kept(kept, have, s)) != GDR_OK) return r;
     if ((r = check_ws(ws, ws_bytes, fwd_bytes(s))) != GDR_OK) return r;
-    cudaStream_t st = (cudaStream_t)stream;
     if (p->B == 0) return GDR_OK;
     if (p->T == 0) return pass_state(p, h0, ht, st);
     float* z = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256);
-    LinearMixArgs m{s, LINEAR_O, q, k, v, nullptr, p->scale, z, o};
+    LinearMixArgs m{s, LINEAR_O, q, k, v, nullptr, p->scale, z, o, keep ? kept : nullptr};
     if (s.bf16) return of(mix_tc(m, v, k, 1.f, 0, h0, z, ht, static_cast<int*>(ws), true, st));
     if (states(s, v, k, 1.f, 0, h0, z, ht, st) != cudaSuccess) return GDR_ERR_CUDA;
     return of(launch_linear_mix(m, st));
 }
 
-gdr_status gdr_linear_bwd(const gdr_linear_problem* p, const void* q, const void* k, const void* v, const float* g,
-                          const float* h0, const int* lengths, const void* do_, const float* dht, void* dq, void* dk,
-                          void* dv, float* dh0, void* ws, size_t ws_bytes, gdr_stream_t stream) {
+static gdr_status linear_bwd_impl(const gdr_linear_problem* p, const void* q, const void* k, const void* v,
+                                  const float* g, const float* h0, const int* lengths, const void* do_,
+                                  const float* dht, void* dq, void* dk, void* dv, float* dh0, bool keep,
+                                  const void* kept, size_t have, void* ws, size_t ws_bytes, cudaStream_t st) {
     gdr_status r = check_problem(p, false);
     if (r != GDR_OK) return r;
     const bool empty = p->B == 0 || p->T == 0;
     if ((r = check_ptrs(empty, {q, k, v, do_, dq, dk, dv}, {h0, dht, dh0})) != GDR_OK) return r;
     if (!g || !on(g, 4) || !on(lengths, 4)) return GDR_ERR_INVALID_ARG;
     const LinearShape s = shape_of(p, g, lengths);
-    if ((r = check_ws(ws, ws_bytes, bwd_bytes(s))) != GDR_OK) return r;
-    cudaStream_t st = (cudaStream_t)stream;
+    if (keep && (r = check_kept(kept, have, s)) != GDR_OK) return r;
+    if ((r = check_ws(ws, ws_bytes, bwd_bytes(s, keep))) != GDR_OK) return r;
     if (p->B == 0) return GDR_OK;
     if (p->T == 0) return pass_state(p, dht, dh0, st);
     uint8_t* w = static_cast<uint8_t*>(ws) + 256;
-    float *zs = reinterpret_cast<float*>(w), *zd = reinterpret_cast<float*>(w + states_bytes(s));
+    float* z = reinterpret_cast<float*>(w);
     if (s.bf16) {
-        LinearMixArgs m{s, LINEAR_DV, q, k, v, do_, p->scale, zd, dv};
-        if (mix_tc(m, do_, q, p->scale, 1, dht, zd, dh0, static_cast<int*>(ws), true, st) != cudaSuccess) return GDR_ERR_CUDA;
+        int* status = static_cast<int*>(ws);
+        uint8_t* adjoints = w + states_bytes(s);
+        if (!keep) {  // the chunks' states, formed again
+            uint8_t* again = adjoints + kept_bytes(s);
+            LinearMixArgs m{s, LINEAR_O, q, k, v, nullptr, p->scale, z, again + kept_bytes(s), again};
+            if (mix_tc(m, v, k, 1.f, 0, h0, z, nullptr, status, true, st) != cudaSuccess) return GDR_ERR_CUDA;
+            kept = again;
+        }
+        LinearMixArgs m{s, LINEAR_DV, q, k, v, do_, p->scale, z, dv, adjoints};
+        if (mix_tc(m, do_, q, p->scale, 1, dht, z, dh0, status, keep, st) != cudaSuccess) return GDR_ERR_CUDA;
+        LinearGradArgs a{s, q, k, v, do_, p->scale, kept, adjoints, dq, dk, status};
+        return of(launch_linear_tc_grad(a, st));
     }
-    if (states(s, v, k, 1.f, 0, h0, zs, nullptr, st) != cudaSuccess) return GDR_ERR_CUDA;
-    if (states(s, do_, q, p->scale, 1, dht, zd, s.bf16 ? nullptr : dh0, st) != cudaSuccess) return GDR_ERR_CUDA;
+    float* zd = reinterpret_cast<float*>(w + states_bytes(s));
+    if (states(s, v, k, 1.f, 0, h0, z, nullptr, st) != cudaSuccess) return GDR_ERR_CUDA;
+    if (states(s, do_, q, p->scale, 1, dht, zd, dh0, st) != cudaSuccess) return GDR_ERR_CUDA;
     // dv reads the reverse states, which dk, summing over value heads, may update in place: dv first
     const struct { int pass; float* z; void* out; } passes[3] = {
-        {LINEAR_DQ, zs, dq}, {LINEAR_DV, zd, dv}, {LINEAR_DK, zd, dk}};
+        {LINEAR_DQ, z, dq}, {LINEAR_DV, zd, dv}, {LINEAR_DK, zd, dk}};
     for (const auto& x : passes) {
-        if (s.bf16 && x.pass == LINEAR_DV) continue;
-        LinearMixArgs m{s, x.pass, q, k, v, do_, p->scale, x.z, x.out};
+        LinearMixArgs m{s, x.pass, q, k, v, do_, p->scale, x.z, x.out, nullptr};
         if (launch_linear_mix(m, st) != cudaSuccess) return GDR_ERR_CUDA;
     }
     return GDR_OK;
+}
+
+gdr_status gdr_linear_fwd(const gdr_linear_problem* p, const void* q, const void* k, const void* v, const float* g,
+                          const float* h0, const int* lengths, void* o, float* ht, void* ws, size_t ws_bytes,
+                          gdr_stream_t stream) {
+    return linear_fwd_impl(p, q, k, v, g, h0, lengths, o, ht, false, nullptr, 0, ws, ws_bytes, (cudaStream_t)stream);
+}
+
+gdr_status gdr_linear_fwd_states(const gdr_linear_problem* p, const void* q, const void* k, const void* v,
+                                 const float* g, const float* h0, const int* lengths, void* o, float* ht, void* states,
+                                 size_t states_bytes, void* ws, size_t ws_bytes, gdr_stream_t stream) {
+    return linear_fwd_impl(p, q, k, v, g, h0, lengths, o, ht, true, states, states_bytes, ws, ws_bytes,
+                           (cudaStream_t)stream);
+}
+
+gdr_status gdr_linear_bwd(const gdr_linear_problem* p, const void* q, const void* k, const void* v, const float* g,
+                          const float* h0, const int* lengths, const void* do_, const float* dht, void* dq, void* dk,
+                          void* dv, float* dh0, void* ws, size_t ws_bytes, gdr_stream_t stream) {
+    return linear_bwd_impl(p, q, k, v, g, h0, lengths, do_, dht, dq, dk, dv, dh0, false, nullptr, 0, ws, ws_bytes,
+                           (cudaStream_t)stream);
+}
+
+gdr_status gdr_linear_bwd_states(const gdr_linear_problem* p, const void* q, const void* k, const void* v,
+                                 const float* g, const float* h0, const int* lengths, const void* states,
+                                 size_t states_bytes, const void* do_, const float* dht, void* dq, void* dk, void* dv,
+                                 float* dh0, void* ws, size_t ws_bytes, gdr_stream_t stream) {
+    return linear_bwd_impl(p, q, k, v, g, h0, lengths, do_, dht, dq, dk, dv, dh0, true, states, states_bytes, ws,
+                           ws_bytes, (cudaStream_t)stream);
 }
 
 gdr_status gdr_linear_decode_step(const gdr_linear_problem* p, const void* q, const void* k, const void* v,

@@ -54,6 +54,9 @@ struct LinearMixArgs {
     float scale;
     float* starts;  // state entering each segment (scratch: passes that sum value heads update it)
     void* out;
+    void* images;   // bf16 o and dv: the state that each 128-token chunk starts from (dv: the adjoint of
+                    // the one it ends in) is kept there as a swizzled bf16 tile, 32 KB for each
+                    // (b, hv, chunk), for launch_linear_tc_grad; or null
 };
 
 int linear_segments(int B, int T, int Hv, int Dv);
@@ -69,6 +72,17 @@ int linear_tc_segments(int B, int T, int Hv);
 cudaError_t launch_linear_tc_summary(const LinearSummaryArgs& a, bool all, int* status, bool clear, cudaStream_t st);
 cudaError_t launch_linear_tc_mix(const LinearMixArgs& a, const float* start, int start_segs, float* last, int* status,
                                  bool clear, cudaStream_t st);
+
+// dq and dk of bf16 problems from the kept states (linear_grad.cu).
+struct LinearGradArgs {
+    LinearShape s;
+    const void *q, *k, *v, *do_;
+    float scale;
+    const void *states, *adjoints;  // images of the o and dv passes
+    void *dq, *dk;
+    int* status;
+};
+cudaError_t launch_linear_tc_grad(const LinearGradArgs& a, cudaStream_t st);
 
 struct LinearStepArgs {
     int B, Hk, Hv, Dk, Dv, bf16;

@@ -36,19 +36,19 @@
 #include <stdint.h>
 #include <string.h>
 
-#include "chunk_dev.cuh"
-#include "common.cuh"
 #include "kernels.h"
 #include "linear.h"
-#include "tma_host.h"
+#include "linear_dev.cuh"
+#include "linear_host.h"
 
 namespace gdr {
 
+using namespace linear;
+
 namespace {
 
-constexpr int C = 128;     // tokens of a chunk
 constexpr int SLOTS = 6, SLOTS_C = 3;  // input tiles, those of c
-constexpr uint32_t SLOT = 32768, PANEL = 16384;
+constexpr uint32_t SLOT = TILE;
 constexpr uint32_t AT_S = SLOTS * SLOT;     // bf16 state [128 x 128]
 constexpr uint32_t AT_W = AT_S + 32768;     // tables: 32 and 64 floats, three of 128 bf16 pairs
 constexpr uint32_t BYTES = AT_W + 384 + 1536;
@@ -67,53 +67,11 @@ struct TcArgs {
     float* z;                  // summary: what the segment adds to the state [B, Hv, nseg, Dv, Dk]
     float* last;               // mix: the state after all segments, or null
     void* out;                 // mix: [B, T, Hv, Dv]
+    uint8_t* images;           // mix: the bf16 state that each chunk's X reads, or null (linear.h)
     int* status;
     int clear_status;          // the first kernel of a call clears the status word
 };
 
-__device__ __forceinline__ float power(float g, int n) { return n == 0 ? 1.f : expf(g * (float)n); }
-
-// Products are issued by the elected lane of a converged warp, which keeps their operands in uniform
-// registers: the issue is what paces them. A descriptor is a fixed high word and a low word that
-// advances by a constant per 16-wide step. (Issued by a lone thread with descriptors built for
-// each step, a product took 140 to 240 cycles, not 70.)
-constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride 1024, version 1, 128-byte swizzle
-__device__ __forceinline__ uint32_t lo_kmajor(uint32_t tile) { return (tile >> 4) | (1u << 16); }
-__device__ __forceinline__ uint32_t lo_mnmajor(uint32_t tile) { return (tile >> 4) | ((PANEL >> 4) << 16); }
-__device__ constexpr uint32_t step_mnmajor(int k) { return k * (2048 >> 4); }
-
-__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t idesc,
-                                       uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t"
-        "setp.ne.u32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(alo), "r"(blo), "r"(idesc), "r"(accumulate), "r"(DESC_HI)
-        : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t idesc,
-                                       uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\t"
-        "setp.ne.u32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\tmov.b64 y, {%2, %5};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "r"(blo), "r"(idesc), "r"(accumulate), "r"(DESC_HI)
-        : "memory");
-}
-__device__ __forceinline__ void commit(uint64_t* bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
-        : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
 // 16 lanes x 16 columns: r[2 i], r[2 i + 1] hold column 4 i + t % 4 of lanes t / 4 and t / 4 + 8.
 __device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t* r) {
     asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
@@ -127,60 +85,6 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t* r) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr)
                  : "memory");
-}
-
-// Products and sums of two values at once: fp32 pairs, and bf16 pairs with one rounding.
-__device__ __forceinline__ void scale2(float* x, float f) {
-    uint64_t v, w;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x[0]), "f"(x[1]));
-    asm("mov.b64 %0, {%1, %1};" : "=l"(w) : "f"(f));
-    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(w));
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x[0]), "=f"(x[1]) : "l"(v));
-}
-__device__ __forceinline__ void scale2(float* x, float f0, float f1) {
-    uint64_t v, w;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x[0]), "f"(x[1]));
-    asm("mov.b64 %0, {%1, %2};" : "=l"(w) : "f"(f0), "f"(f1));
-    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(w));
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x[0]), "=f"(x[1]) : "l"(v));
-}
-__device__ __forceinline__ void axpy2(float* s, float f, const float* d) {  // s <- f s + d
-    uint64_t v, w, u;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(s[0]), "f"(s[1]));
-    asm("mov.b64 %0, {%1, %1};" : "=l"(w) : "f"(f));
-    asm("mov.b64 %0, {%1, %2};" : "=l"(u) : "f"(d[0]), "f"(d[1]));
-    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(v) : "l"(w), "l"(u));
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(s[0]), "=f"(s[1]) : "l"(v));
-}
-__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-__device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
-    uint32_t d;
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-    return d;
-}
-__device__ __forceinline__ uint32_t bf16x2_neg(uint32_t a) { return a ^ 0x80008000u; }
-
-// Bounded wait of a whole warp for phase `parity`, in few instructions, since the warps' roles share the
-// instruction caches: the warp is parked in the barrier unit for up to a millisecond at a time. Gives
-// up after about a second, leaving the site in *failed, or as soon as another warp has.
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* failed, int site) {
-    const long long t0 = clock64();
-    uint32_t ok;
-    do {
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
-            : "memory");
-        if (!ok && clock64() - t0 > kWaitCycles) *failed = site;
-    } while (!ok && !*failed);
-    return __all_sync(0xffffffffu, ok);
 }
 
 // TERMS: bf16 terms of c' (2 or 4). MIX: the output pass, else the summary.
@@ -597,28 +501,47 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&sready);
         };
-        if (MIX) write_state();
-        for (int i = 0; i < nc; i++) {
-            if (!wait_phase(&sfull[i % SUMS], i / SUMS & 1, &failed, 63)) break;
-            tc_fence_after();
-            const float over = power(g, tokens_of(i));
-#pragma unroll
-            for (int h = 0; h < 4; h++) {
-                if (h >= 2 * a.panels_k) continue;
-                float d[32];
-                tmem_ld32(lanes + COL_S + 128 * (i % SUMS) + 32 * h, d);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) axpy2(S + 32 * h + e, over, d + e);
+        // The copy of chunk i, and its image. The four warps decide together whether to go on.
+        auto share_state = [&](int i, bool ok) {
+            if (a.images && row == 0) bulk_wait_read_all();  // the last image has been read
+            if (bar_sync_or(2, 128, !ok)) return false;
+            write_state();
+            if (a.images) {
+                bar_sync_or(2, 128, false);
+                if (row == 0) {
+                    const size_t chunk = (bh * ((s.T + C - 1) / C) + first / C + chunk_of(i)) * TILE;
+                    bulk_store(a.images + chunk, sm + AT_S, a.panels_k * PANEL);
+                    bulk_commit();
+                }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sfree[i % SUMS]);
+            return true;
+        };
+        bool go = !MIX || nc == 0 || share_state(0, true);
+        for (int i = 0; i < nc && go; i++) {
+            bool ok = wait_phase(&sfull[i % SUMS], i / SUMS & 1, &failed, 63);
+            if (ok) {
+                tc_fence_after();
+                const float over = power(g, tokens_of(i));
+#pragma unroll
+                for (int h = 0; h < 4; h++) {
+                    if (h >= 2 * a.panels_k) continue;
+                    float d[32];
+                    tmem_ld32(lanes + COL_S + 128 * (i % SUMS) + 32 * h, d);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) axpy2(S + 32 * h + e, over, d + e);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sfree[i % SUMS]);
+            }
             if (MIX && i + 1 < nc) {
-                if (!wait_phase(&xdone, i & 1, &failed, 64)) break;
-                write_state();
+                ok = ok && wait_phase(&xdone, i & 1, &failed, 64);
+                ok = share_state(i + 1, ok);
             }
+            go = ok;
         }
+        if (MIX && a.images && row == 0) bulk_wait_all();
         float* to = nullptr;
         if (!MIX) to = a.z + (bh * s.nseg + seg) * state;
         else if (a.last && seg == (a.reverse ? 0 : s.nseg - 1)) to = a.last + bh * state;
@@ -642,13 +565,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     if (warp == 20) tmem_dealloc(tm, 512);
 }
-
-// Tiles of one 64-channel panel and 128 tokens of a [B, T, H, D] tensor.
-bool tile_map(CUtensorMap* m, const void* p, const LinearShape& s, int H, int D) {
-    return make_map_4d_bf16(m, p, D, H, s.T, s.B, 64, C, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
-int panels(int d) { return d > 64 ? 2 : 1; }
 
 // Before the tensor maps: the first runtime call of a host thread (autograd's, say) makes the device's
 // context current there, which encoding a map needs.
@@ -689,8 +605,10 @@ cudaError_t launch_linear_tc_summary(const LinearSummaryArgs& x, bool all, int* 
 cudaError_t launch_linear_tc_mix(const LinearMixArgs& x, const float* start, int start_segs, float* last, int* status,
                                  bool clear, cudaStream_t st) {
     const bool rev = x.pass == LINEAR_DV;
-    // a state that leaves the call is carried with four terms, one that only feeds X with two
-    if (cudaError_t e = last ? allow_smem<true, 4>() : allow_smem<true, 2>()) return e;
+    // One segment carries the state that leaves the call, with four terms (also where the caller does not
+    // want it, so that the kept states are the same); with several it comes from the summary.
+    const bool one = x.s.nseg == 1;
+    if (cudaError_t e = one ? allow_smem<true, 4>() : allow_smem<true, 2>()) return e;
     CUtensorMap maps[4];
     if (!tile_map(&maps[0], rev ? x.k : x.q, x.s, x.s.Hk, x.s.Dk) || !tile_map(&maps[1], rev ? x.q : x.k, x.s, x.s.Hk, x.s.Dk) ||
         !tile_map(&maps[2], rev ? x.do_ : x.v, x.s, x.s.Hv, x.s.Dv) || !tile_map(&maps[3], x.out, x.s, x.s.Hv, x.s.Dv))
@@ -707,10 +625,11 @@ cudaError_t launch_linear_tc_mix(const LinearMixArgs& x, const float* start, int
     a.start_segs = start_segs;
     a.last = last;
     a.out = x.out;
+    a.images = static_cast<uint8_t*>(x.images);
     a.status = status;
     a.clear_status = clear;
     const char* name = rev ? "linear_dv" : "linear_o";
-    return last ? launch<true, 4>(maps, a, x.s.nseg, name, st) : launch<true, 2>(maps, a, x.s.nseg, name, st);
+    return one ? launch<true, 4>(maps, a, x.s.nseg, name, st) : launch<true, 2>(maps, a, x.s.nseg, name, st);
 }
 
 // Segments of whole chunks, one CTA each, on 152 SMs. In units of one chunk of the mix pass: a wave

@@ -278,6 +278,21 @@ gdr_status gdr_linear_bwd(const gdr_linear_problem* p, const void* q, const void
                           const float* h0, const int* lengths, const void* do_, const float* dht, void* dq, void* dk,
                           void* dv, float* dh0, void* ws, size_t ws_bytes, gdr_stream_t stream);
 
+/* Saved-state handoff: the forward keeps the state that each 128-token chunk starts from, in the bf16 that
+ * its own output reads (opaque layout, gdr_linear_states_bytes() bytes: 32 KB for each (b, hv,
+ * chunk) of a BF16 problem, 0 for F32, whose backward keeps to gdr_linear_bwd's work; caller-owned, 256-byte
+ * aligned), and the backward of the same inputs reads them instead of forming them again; its h0
+ * is then not needed by BF16. Results are those of the calls without it, bit for bit. */
+size_t gdr_linear_states_bytes(const gdr_linear_problem* p);
+size_t gdr_linear_bwd_states_workspace(const gdr_linear_problem* p);
+gdr_status gdr_linear_fwd_states(const gdr_linear_problem* p, const void* q, const void* k, const void* v,
+                                 const float* g, const float* h0, const int* lengths, void* o, float* ht, void* states,
+                                 size_t states_bytes, void* ws, size_t ws_bytes, gdr_stream_t stream);
+gdr_status gdr_linear_bwd_states(const gdr_linear_problem* p, const void* q, const void* k, const void* v,
+                                 const float* g, const float* h0, const int* lengths, const void* states,
+                                 size_t states_bytes, const void* do_, const float* dht, void* dq, void* dk, void* dv,
+                                 float* dh0, void* ws, size_t ws_bytes, gdr_stream_t stream);
+
 /* One token (p->T must be 1; layouts without the T axis): the state is updated in place, o written. */
 gdr_status gdr_linear_decode_step(const gdr_linear_problem* p, const void* q, const void* k, const void* v,
                                   const float* g, float* state, void* o, gdr_stream_t stream);

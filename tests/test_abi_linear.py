@@ -81,6 +81,27 @@ def test_linear_workspace(L):
         assert f(p, *put(n), ctypes.c_void_p(0x100010), BIG, None) == INVALID
 
 
+def test_kept_states(L):
+    p = ctypes.byref(prob(T=129))
+    need = L.gdr_linear_states_bytes(p)
+    assert need == 4 * 2 * 32768  # value heads x chunks of 128 tokens
+    assert L.gdr_linear_states_bytes(ctypes.byref(prob(dtype=0))) == 0
+    assert 0 < L.gdr_linear_bwd_states_workspace(p) < L.gdr_linear_bwd_workspace(p)
+    assert L.gdr_linear_states_bytes(ctypes.byref(prob(Hv=3))) == 0
+
+    def fwd(states, n):
+        return L.gdr_linear_fwd_states(p, *put(8), states, ctypes.c_size_t(n), FAKE, BIG, None)
+
+    def bwd(states, n):
+        return L.gdr_linear_bwd_states(p, *put(6), states, ctypes.c_size_t(n), *put(6), FAKE, BIG, None)
+
+    for f in (fwd, bwd):
+        assert f(FAKE, need - 1) == WORKSPACE and f(None, need) == WORKSPACE
+        assert f(ctypes.c_void_p(0x100010), need) == INVALID
+    small = ctypes.c_size_t(L.gdr_linear_bwd_states_workspace(p) - 1)
+    assert L.gdr_linear_bwd_states(p, *put(6), FAKE, BIG, *put(6), FAKE, small, None) == WORKSPACE
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(rows=-1), INVALID), (dict(groups=0), INVALID), (dict(D=0), INVALID), (dict(dtype=2), INVALID),
     (dict(activation=3), INVALID), (dict(center=2), INVALID), (dict(eps=0.0), INVALID), (dict(eps=-1.0), INVALID),

@@ -152,6 +152,20 @@ def test_repeats_bitwise_on_another_stream(dtype):
     assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_kept_states_give_the_same_gradients(dtype):
+    dev = cuda_device()
+    for n in (None, [500, 0, 129]):
+        d = to_dev(make(3, 500, 2, 4, 64, 128, TYPES[dtype], seed=13, lengths=n), dev)
+        args = d["q"], d["k"], d["v"], d["g"], d["h0"]
+        o, ht = gdr.linear_fwd(*args, lengths=d["lengths"])
+        o2, ht2, states = gdr.linear_fwd(*args, lengths=d["lengths"], save_states=True)
+        assert torch.equal(o, o2) and torch.equal(ht, ht2)
+        want = gdr.linear_bwd(*args, d["do"], d["dht"], lengths=d["lengths"])
+        got = gdr.linear_bwd(*args, d["do"], d["dht"], lengths=d["lengths"], states=states)
+        assert all(torch.equal(want[x], got[x]) for x in want)
+
+
 def test_runs_in_a_captured_graph():
     dev = cuda_device()
     d = to_dev(make(1, 300, 2, 4, 128, 128, torch.bfloat16, seed=6), dev)
