@@ -14,6 +14,7 @@ fp32; states [B,Hv,Dv,Dk] fp32.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -334,28 +335,70 @@ def decode_step(q, k, v, g, beta, state, scale=None, use_qk_l2norm=True, out=Non
     return o
 
 
+# The calls below are short enough for the host's part to matter: tensors are compared with what they
+# have to be in one expression each (_need only words the refusal), pointers go as plain integers, and the
+# problem with its buffer sizes is built once for each set of sizes.
+_DTYPES = {torch.float32: GDR_F32, torch.bfloat16: GDR_BF16}
+
+
+def _is(t, name, dtype, device, shape):
+    if not (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+        _need(t, name, dtype=dtype, device=device, shape=shape)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(device):
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+@functools.lru_cache(maxsize=1024)
+def _linear_spec(B, T, Hk, Hv, Dk, Dv, dtype, scale):
+    """(by-reference problem, bytes: forward workspace, kept states, backward workspace without and with them)."""
+    p, L = LinearProblem(B, T, Hk, Hv, Dk, Dv, dtype, scale), lib()
+    at = ctypes.byref(p)
+    return at, tuple(int(f(at)) for f in (L.gdr_linear_fwd_workspace, L.gdr_linear_states_bytes,
+                                          L.gdr_linear_bwd_workspace, L.gdr_linear_bwd_states_workspace))
+
+
 def _linear_problem(q, k, v, g, scale, decode):
-    """Checks q, k, v, g of a linear attention call and describes them."""
-    dev, nd = q.device, 3 if decode else 4
-    _need(q, "q", device=dev)
-    if q.dim() != nd or v.dim() != nd:
+    """Checks q, k, v, g of a linear attention call: (problem, its buffer sizes, device, state shape)."""
+    qs, vs, dev, dtype = q.shape, v.shape, q.device, q.dtype
+    nd = 3 if decode else 4
+    if not (q.is_cuda and q.is_contiguous()):
+        _need(q, "q")
+    if len(qs) != nd or len(vs) != nd:
         raise ValueError(f"q and v must have {nd} dimensions")
-    _need(k, "k", dtype=q.dtype, device=dev, shape=q.shape)
-    _need(v, "v", dtype=q.dtype, device=dev, shape=tuple(q.shape[:-2]) + tuple(v.shape[-2:]))
-    dtype = {torch.float32: GDR_F32, torch.bfloat16: GDR_BF16}.get(q.dtype)
-    if dtype is None:
-        raise ValueError(f"q/k/v dtype must be float32 or bfloat16, got {q.dtype}")
-    Hv, Dk = v.shape[-2], q.shape[-1]
-    _need(g, "g", dtype=torch.float32, device=dev, shape=(Hv,))
-    return LinearProblem(q.shape[0], 1 if decode else q.shape[1], q.shape[-2], Hv, Dk, v.shape[-1], dtype,
-                         Dk ** -0.5 if scale is None else float(scale))
+    if dtype not in _DTYPES:
+        raise ValueError(f"q/k/v dtype must be float32 or bfloat16, got {dtype}")
+    _is(k, "k", dtype, dev, qs)
+    _is(v, "v", dtype, dev, qs[:-2] + vs[-2:])
+    Hv, Dk, Dv = vs[-2], qs[-1], vs[-1]
+    _is(g, "g", torch.float32, dev, (Hv,))
+    at, sizes = _linear_spec(qs[0], 1 if decode else qs[1], qs[-2], Hv, Dk, Dv, _DTYPES[dtype],
+                             Dk ** -0.5 if scale is None else float(scale))
+    return at, sizes, dev, (qs[0], Hv, Dv, Dk)
 
 
-def _linear_extras(p, dev, h0, lengths):
+def _linear_extras(dev, state, h0, lengths):
     if h0 is not None:
-        _need(h0, "h0", dtype=torch.float32, device=dev, shape=(p.B, p.Hv, p.Dv, p.Dk))
+        _is(h0, "h0", torch.float32, dev, state)
     if lengths is not None:
-        _need(lengths, "lengths", dtype=torch.int32, device=dev, shape=(p.B,))
+        _is(lengths, "lengths", torch.int32, dev, state[:1])
+
+
+def _scratch(nbytes, device, workspace):
+    """The caller's workspace after checking it, else a new buffer; no size means an unsupported problem."""
+    if nbytes == 0:
+        _check(GDR_ERR_UNSUPPORTED)
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    _need(workspace, "workspace", device=device)
+    if workspace.numel() * workspace.element_size() < nbytes:
+        raise ValueError(f"workspace too small: {workspace.numel() * workspace.element_size()} < {nbytes} bytes")
+    return workspace
 
 
 def linear_fwd(q, k, v, g, h0=None, scale=None, lengths=None, output_final_state=True, workspace=None,
@@ -366,20 +409,18 @@ def linear_fwd(q, k, v, g, h0=None, scale=None, lengths=None, output_final_state
     (device) or None: entry b has lengths[b] tokens, o is zero past them and ht is the state after
     the last one. scale defaults to Dk^-1/2. Returns (o, ht or None), or (o, ht, states) with
     save_states=True (gdr_linear_fwd_states: what linear_bwd(..., states=states) need not form again)."""
-    p = _linear_problem(q, k, v, g, scale, False)
-    _linear_extras(p, q.device, h0, lengths)
-    o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
-    ht = torch.empty((p.B, p.Hv, p.Dv, p.Dk), dtype=torch.float32, device=v.device) if output_final_state else None
-    L = lib()
-    ws, nbytes = _workspace(L.gdr_linear_fwd_workspace, p, q.device, workspace)
+    at, sizes, dev, state = _linear_problem(q, k, v, g, scale, False)
+    _linear_extras(dev, state, h0, lengths)
+    o = torch.empty_like(v)
+    ht = torch.empty(state, dtype=torch.float32, device=dev) if output_final_state else None
+    ws = _scratch(sizes[0], dev, workspace)
+    ins = (at, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _at(h0), _at(lengths), o.data_ptr(), _at(ht))
     if not save_states:
-        _check(L.gdr_linear_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(h0), _ptr(lengths),
-                                _ptr(o), _ptr(ht), _ptr(ws), ctypes.c_size_t(nbytes), _stream(q.device)))
+        _check(lib().gdr_linear_fwd(*ins, ws.data_ptr(), sizes[0], _raw_stream(dev)))
         return o, ht
-    states = torch.empty(max(int(L.gdr_linear_states_bytes(ctypes.byref(p))), 256), dtype=torch.uint8, device=q.device)
-    _check(L.gdr_linear_fwd_states(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(h0), _ptr(lengths),
-                                   _ptr(o), _ptr(ht), _ptr(states), ctypes.c_size_t(states.numel()), _ptr(ws),
-                                   ctypes.c_size_t(nbytes), _stream(q.device)))
+    states = torch.empty(max(sizes[1], 256), dtype=torch.uint8, device=dev)
+    _check(lib().gdr_linear_fwd_states(*ins, states.data_ptr(), states.numel(), ws.data_ptr(), sizes[0],
+                                       _raw_stream(dev)))
     return o, ht, states
 
 
@@ -387,56 +428,68 @@ def linear_bwd(q, k, v, g, h0, do, dht=None, scale=None, lengths=None, workspace
     """VJP of linear_fwd for the loss <do, o> + <dht, ht> (gdr_linear_bwd, or gdr_linear_bwd_states
     with the `states` of linear_fwd(save_states=True) on the same inputs). Returns a dict of dq,
     dk, dv in the inputs' dtype and dh0 fp32; the decay is a constant and has no gradient."""
-    p = _linear_problem(q, k, v, g, scale, False)
-    _linear_extras(p, q.device, h0, lengths)
-    _need(do, "do", dtype=v.dtype, device=v.device, shape=v.shape)
+    at, sizes, dev, state = _linear_problem(q, k, v, g, scale, False)
+    _linear_extras(dev, state, h0, lengths)
+    _is(do, "do", v.dtype, dev, v.shape)
     if dht is not None:
-        _need(dht, "dht", dtype=torch.float32, device=v.device, shape=(p.B, p.Hv, p.Dv, p.Dk))
-    out = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
-               dh0=torch.empty((p.B, p.Hv, p.Dv, p.Dk), dtype=torch.float32, device=v.device))
-    grads = [_ptr(out[n]) for n in ("dq", "dk", "dv", "dh0")]
-    ins = [_ptr(t) for t in (q, k, v, g, h0, lengths)]
-    L = lib()
+        _is(dht, "dht", torch.float32, dev, state)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    dh0 = torch.empty(state, dtype=torch.float32, device=dev)
+    need = sizes[2] if states is None else sizes[3]
+    ws = _scratch(need, dev, workspace)
+    ins = (at, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _at(h0), _at(lengths))
+    rest = (do.data_ptr(), _at(dht), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dh0.data_ptr(), ws.data_ptr(), need,
+            _raw_stream(dev))
     if states is None:
-        ws, nbytes = _workspace(L.gdr_linear_bwd_workspace, p, q.device, workspace)
-        _check(L.gdr_linear_bwd(ctypes.byref(p), *ins, _ptr(do), _ptr(dht), *grads, _ptr(ws), ctypes.c_size_t(nbytes),
-                                _stream(q.device)))
-        return out
-    _need(states, "states", dtype=torch.uint8, device=q.device)
-    ws, nbytes = _workspace(L.gdr_linear_bwd_states_workspace, p, q.device, workspace)
-    _check(L.gdr_linear_bwd_states(ctypes.byref(p), *ins, _ptr(states), ctypes.c_size_t(states.numel()), _ptr(do),
-                                   _ptr(dht), *grads, _ptr(ws), ctypes.c_size_t(nbytes), _stream(q.device)))
-    return out
+        _check(lib().gdr_linear_bwd(*ins, *rest))
+    else:
+        _need(states, "states", dtype=torch.uint8, device=dev)
+        _check(lib().gdr_linear_bwd_states(*ins, states.data_ptr(), states.numel(), *rest))
+    return dict(dq=dq, dk=dk, dv=dv, dh0=dh0)
 
 
 def linear_decode_step(q, k, v, g, state, scale=None, out=None):
     """One token of linear attention (gdr_linear_decode_step): q, k [B,Hk,Dk]; v [B,Hv,Dv]; g [Hv];
     state [B,Hv,Dv,Dk] fp32 updated in place. Returns o [B,Hv,Dv]."""
-    p = _linear_problem(q, k, v, g, scale, True)
-    _need(state, "state", dtype=torch.float32, device=q.device, shape=(p.B, p.Hv, p.Dv, p.Dk))
-    o = torch.empty_like(v) if out is None else _need(out, "out", dtype=v.dtype, device=v.device, shape=v.shape)
-    _check(lib().gdr_linear_decode_step(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state), _ptr(o),
-                                        _stream(q.device)))
-    return o
+    at, _, dev, shape = _linear_problem(q, k, v, g, scale, True)
+    _is(state, "state", torch.float32, dev, shape)
+    if out is None:
+        out = torch.empty_like(v)
+    else:
+        _is(out, "out", v.dtype, dev, v.shape)
+    _check(lib().gdr_linear_decode_step(at, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), state.data_ptr(),
+                                        out.data_ptr(), _raw_stream(dev)))
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_spec(rows, groups, D, dtype, activation, center, eps):
+    """(by-reference problem, bytes of the backward's workspace)."""
+    at = ctypes.byref(NormProblem(rows, groups, D, dtype, activation, center, eps))
+    return at, int(lib().gdr_group_norm_bwd_workspace(at))
 
 
 def _norm_problem(x, groups, weight, bias, gate, activation, eps, center):
-    """Checks the inputs of a group norm call and describes them."""
-    _need(x, "x")
-    dtype = {torch.float32: GDR_F32, torch.bfloat16: GDR_BF16}.get(x.dtype)
-    if dtype is None:
-        raise ValueError(f"x dtype must be float32 or bfloat16, got {x.dtype}")
+    """Checks the inputs of a group norm call: (problem, backward workspace bytes, device)."""
+    shape, dev, dtype = x.shape, x.device, x.dtype
+    if not (x.is_cuda and x.is_contiguous()):
+        _need(x, "x")
+    if dtype not in _DTYPES:
+        raise ValueError(f"x dtype must be float32 or bfloat16, got {dtype}")
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}, got {activation!r}")
-    C = x.shape[-1] if x.dim() > 0 else 0
+    C = shape[-1] if len(shape) > 0 else 0
     if groups < 1 or C < 1 or C % groups:
-        raise ValueError(f"x's last dimension must be a positive multiple of groups = {groups}, got {tuple(x.shape)}")
+        raise ValueError(f"x's last dimension must be a positive multiple of groups = {groups}, got {tuple(shape)}")
     if gate is not None:
-        _need(gate, "gate", dtype=x.dtype, device=x.device, shape=x.shape)
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is not None:
-            _need(t, name, dtype=torch.float32, device=x.device, shape=(C,))
-    return NormProblem(x.numel() // C, groups, C // groups, dtype, _ACTIVATIONS[activation], int(bool(center)), eps)
+        _is(gate, "gate", dtype, dev, shape)
+    if weight is not None:
+        _is(weight, "weight", torch.float32, dev, shape[-1:])
+    if bias is not None:
+        _is(bias, "bias", torch.float32, dev, shape[-1:])
+    at, nbytes = _norm_spec(x.numel() // C, groups, C // groups, _DTYPES[dtype], _ACTIVATIONS[activation],
+                            int(bool(center)), float(eps))
+    return at, nbytes, dev
 
 
 def group_norm_fwd(x, groups, weight=None, bias=None, gate=None, activation="none", eps=1e-5, center=True, out=None):
@@ -445,26 +498,29 @@ def group_norm_fwd(x, groups, weight=None, bias=None, gate=None, activation="non
     n = weight h + bias and y = act(n), or n act(gate) with a gate of x's shape. weight, bias [C]
     fp32 or None; activation "none", "silu" or "sigmoid"; center=False leaves the mean in (the
     root-mean-square form). Returns y in x's dtype; `out` may be x or gate themselves."""
-    p = _norm_problem(x, groups, weight, bias, gate, activation, eps, center)
-    y = torch.empty_like(x) if out is None else _need(out, "out", dtype=x.dtype, device=x.device, shape=x.shape)
-    _check(lib().gdr_group_norm_fwd(ctypes.byref(p), _ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(y),
-                                    _stream(x.device)))
-    return y
+    at, _, dev = _norm_problem(x, groups, weight, bias, gate, activation, eps, center)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _is(out, "out", x.dtype, dev, x.shape)
+    _check(lib().gdr_group_norm_fwd(at, x.data_ptr(), _at(gate), _at(weight), _at(bias), out.data_ptr(),
+                                    _raw_stream(dev)))
+    return out
 
 
 def group_norm_bwd(x, groups, weight, bias, gate, dy, activation="none", eps=1e-5, center=True, workspace=None):
     """VJP of group_norm_fwd (gdr_group_norm_bwd). Returns a dict of dx, dgate (x's dtype; dgate None
     without a gate), dweight and dbias (fp32; None where the parameter is)."""
-    p = _norm_problem(x, groups, weight, bias, gate, activation, eps, center)
-    _need(dy, "dy", dtype=x.dtype, device=x.device, shape=x.shape)
-    out = dict(dx=torch.empty_like(x), dgate=None if gate is None else torch.empty_like(gate),
-               dweight=None if weight is None else torch.empty_like(weight),
-               dbias=None if bias is None else torch.empty_like(bias))
-    ws, nbytes = _workspace(lib().gdr_group_norm_bwd_workspace, p, x.device, workspace)
-    _check(lib().gdr_group_norm_bwd(ctypes.byref(p), _ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(dy),
-                                    _ptr(out["dx"]), _ptr(out["dgate"]), _ptr(out["dweight"]), _ptr(out["dbias"]),
-                                    _ptr(ws), ctypes.c_size_t(nbytes), _stream(x.device)))
-    return out
+    at, nbytes, dev = _norm_problem(x, groups, weight, bias, gate, activation, eps, center)
+    _is(dy, "dy", x.dtype, dev, x.shape)
+    dx = torch.empty_like(x)
+    dgate = None if gate is None else torch.empty_like(gate)
+    dweight = None if weight is None else torch.empty_like(weight)
+    dbias = None if bias is None else torch.empty_like(bias)
+    ws = _scratch(nbytes, dev, workspace)
+    _check(lib().gdr_group_norm_bwd(at, x.data_ptr(), _at(gate), _at(weight), _at(bias), dy.data_ptr(), dx.data_ptr(),
+                                    _at(dgate), _at(dweight), _at(dbias), ws.data_ptr(), nbytes, _raw_stream(dev)))
+    return dict(dx=dx, dgate=dgate, dweight=dweight, dbias=dbias)
 
 
 def workspace_status(ws) -> int:

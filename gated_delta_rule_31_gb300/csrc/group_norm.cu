@@ -30,21 +30,27 @@ namespace {
 
 constexpr int THREADS = 256;
 
+// VEC values as loaded: 16 bytes, or a single value.
 template <int VEC, typename T>
-__device__ __forceinline__ void load_vec(const T* p, float* x) {
-    if constexpr (VEC == 8) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
-        x[0] = bf16lo(u.x); x[1] = bf16hi(u.x); x[2] = bf16lo(u.y); x[3] = bf16hi(u.y);
-        x[4] = bf16lo(u.z); x[5] = bf16hi(u.z); x[6] = bf16lo(u.w); x[7] = bf16hi(u.w);
-    } else if constexpr (VEC == 4) {
-        const float4 u = *reinterpret_cast<const float4*>(p);
-        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-    } else if constexpr (sizeof(T) == 2) {
-        x[0] = __bfloat162float(*p);
-    } else {
-        x[0] = *p;
-    }
+struct RawOf { using type = T; };
+template <>
+struct RawOf<8, __nv_bfloat16> { using type = uint4; };
+template <>
+struct RawOf<4, float> { using type = float4; };
+
+template <int VEC, typename T>
+__device__ __forceinline__ typename RawOf<VEC, T>::type load_raw(const T* p) {
+    return *reinterpret_cast<const typename RawOf<VEC, T>::type*>(p);
 }
+__device__ __forceinline__ void values(const uint4& u, float* x) {
+    x[0] = bf16lo(u.x); x[1] = bf16hi(u.x); x[2] = bf16lo(u.y); x[3] = bf16hi(u.y);
+    x[4] = bf16lo(u.z); x[5] = bf16hi(u.z); x[6] = bf16lo(u.w); x[7] = bf16hi(u.w);
+}
+__device__ __forceinline__ void values(const float4& u, float* x) {
+    x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+}
+__device__ __forceinline__ void values(const __nv_bfloat16& u, float* x) { x[0] = __bfloat162float(u); }
+__device__ __forceinline__ void values(const float& u, float* x) { x[0] = u; }
 template <int VEC, typename T>
 __device__ __forceinline__ void store_vec(T* p, const float* x) {
     if constexpr (VEC == 8)
@@ -59,11 +65,11 @@ __device__ __forceinline__ void store_vec(T* p, const float* x) {
 }
 template <int VEC>
 __device__ __forceinline__ void load_param(const float* p, float* x) {
-    if constexpr (VEC == 8) {
-        load_vec<4>(p, x);
-        load_vec<4>(p + 4, x + 4);
+    if constexpr (VEC == 1) {
+        x[0] = *p;
     } else {
-        load_vec<VEC>(p, x);
+#pragma unroll
+        for (int i = 0; i < VEC; i += 4) values(*reinterpret_cast<const float4*>(p + i), x + i);
     }
 }
 template <int VEC>
@@ -112,27 +118,31 @@ __device__ __forceinline__ float2 activate2(float x, int act) {
     return make_float2(x * s, s * (1.f + x * (1.f - s)));
 }
 
-// Which token rows and group a lane works on. A block covers `per` groups (blockIdx.x) and RL
-// token rows at a time; lanes past per * RL slots or past the last group only join the sums.
+// Which token rows and group a lane works on. A block covers `per` groups (blockIdx.x) and `rl` token
+// rows at a time, LPG lanes each; lanes past the last row or group only join the sums.
 struct Place {
-    int group, lane, row0, row_step, slot_row;
+    int group, lane, slot_row;
+    long long row0, row_step;
     bool live;
 };
 template <int LPG>
 __device__ __forceinline__ Place place(int groups, int per) {
     Place p;
-    const int slot = threadIdx.x / LPG, rl = (THREADS / LPG) / per;
+    const int slot = threadIdx.x / LPG, rl = blockDim.x / (LPG * per);
     p.lane = threadIdx.x % LPG;
     p.group = blockIdx.x * per + slot % per;
     p.slot_row = slot / per;
-    p.live = p.slot_row < rl && p.group < groups;
-    p.row0 = blockIdx.y * rl + p.slot_row;
-    p.row_step = gridDim.y * rl;
+    p.live = p.group < groups && p.slot_row < rl;
+    p.row0 = (long long)blockIdx.y * rl + p.slot_row;
+    p.row_step = (long long)gridDim.y * rl;
     return p;
 }
 
+// A lane asks for its next row before it works on the current one: a row a lane in flight is too little
+// to keep HBM busy (T = 32768 rows of 4096 bf16, gated: forward 147 us without).
 template <int LPG, int VEC, int NV, typename T>
-__global__ void __launch_bounds__(THREADS) group_norm_fwd_kernel(GroupNormArgs a, int per) {
+__global__ void __launch_bounds__(THREADS, NV == 1 ? 4 : 1) group_norm_fwd_kernel(GroupNormArgs a, int per) {
+    using Raw = typename RawOf<VEC, T>::type;
     __shared__ float2 red[THREADS / 32];
     const Place at = place<LPG>(a.groups, per);
     const size_t C = (size_t)a.groups * a.D;
@@ -156,19 +166,26 @@ __global__ void __launch_bounds__(THREADS) group_norm_fwd_kernel(GroupNormArgs a
         if (in[i] && a.weight) load_param<VEC>(a.weight + e[i], w[i]);
         if (in[i] && a.bias) load_param<VEC>(a.bias + e[i], b[i]);
     }
+    Raw nx[NV] = {}, nz[NV] = {};
+    auto ask = [&](long long row) {
+        if (row >= a.rows) return;
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            if (in[i]) nx[i] = load_raw<VEC>(x + row * C + e[i]);
+            if (in[i] && z) nz[i] = load_raw<VEC>(z + row * C + e[i]);
+        }
+    };
     const long long steps = (a.rows + at.row_step - 1) / at.row_step;
+    ask(at.row0);
     for (long long s = 0; s < steps; s++) {
         const long long row = at.row0 + s * at.row_step;
         float v[NV][VEC], u[NV][VEC];
-        bool use[NV];
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            use[i] = in[i] && row < a.rows;
-#pragma unroll
-            for (int j = 0; j < VEC; j++) v[i][j] = 0.f;
-            if (use[i]) load_vec<VEC>(x + row * C + e[i], v[i]);
-            if (use[i] && z) load_vec<VEC>(z + row * C + e[i], u[i]);
+            values(nx[i], v[i]);
+            values(nz[i], u[i]);
         }
+        ask(row + at.row_step);
         float sum = 0.f, none = 0.f;
         if (a.center) {
 #pragma unroll
@@ -181,7 +198,7 @@ __global__ void __launch_bounds__(THREADS) group_norm_fwd_kernel(GroupNormArgs a
         float sq = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; i++)
-            if (use[i])
+            if (in[i])
 #pragma unroll
                 for (int j = 0; j < VEC; j++) {
                     v[i][j] -= mean;
@@ -189,21 +206,23 @@ __global__ void __launch_bounds__(THREADS) group_norm_fwd_kernel(GroupNormArgs a
                 }
         group_sum2<LPG>(sq, none, red);
         const float r = 1.f / sqrtf(sq * inv + a.eps);
+        if (row < a.rows)
 #pragma unroll
-        for (int i = 0; i < NV; i++)
-            if (use[i]) {
+            for (int i = 0; i < NV; i++)
+                if (in[i]) {
 #pragma unroll
-                for (int j = 0; j < VEC; j++) {
-                    const float n = w[i][j] * (v[i][j] * r) + b[i][j];
-                    v[i][j] = z ? n * activate(u[i][j], a.act) : activate(n, a.act);
+                    for (int j = 0; j < VEC; j++) {
+                        const float n = w[i][j] * (v[i][j] * r) + b[i][j];
+                        v[i][j] = z ? n * activate(u[i][j], a.act) : activate(n, a.act);
+                    }
+                    store_vec<VEC>(y + row * C + e[i], v[i]);
                 }
-                store_vec<VEC>(y + row * C + e[i], v[i]);
-            }
     }
 }
 
 template <int LPG, int VEC, int NV, typename T>
-__global__ void __launch_bounds__(THREADS) group_norm_bwd_kernel(GroupNormArgs a, int per, float* part) {
+__global__ void __launch_bounds__(THREADS, NV == 1 ? 3 : 1) group_norm_bwd_kernel(GroupNormArgs a, int per, float* part) {
+    using Raw = typename RawOf<VEC, T>::type;
     __shared__ float2 red[THREADS / 32];
     const Place at = place<LPG>(a.groups, per);
     const size_t C = (size_t)a.groups * a.D;
@@ -229,20 +248,28 @@ __global__ void __launch_bounds__(THREADS) group_norm_bwd_kernel(GroupNormArgs a
         if (in[i] && a.weight) load_param<VEC>(a.weight + e[i], w[i]);
         if (in[i] && a.bias) load_param<VEC>(a.bias + e[i], b[i]);
     }
+    Raw nx[NV] = {}, nz[NV] = {}, ng[NV] = {};
+    auto ask = [&](long long row) {
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const bool use = in[i] && row < a.rows;
+            if (use) nx[i] = load_raw<VEC>(x + row * C + e[i]);
+            if (use && z) nz[i] = load_raw<VEC>(z + row * C + e[i]);
+            ng[i] = use ? load_raw<VEC>(dy + row * C + e[i]) : Raw{};  // no row adds nothing to dw and db
+        }
+    };
     const long long steps = (a.rows + at.row_step - 1) / at.row_step;
+    ask(at.row0);
     for (long long s = 0; s < steps; s++) {
         const long long row = at.row0 + s * at.row_step;
         float h[NV][VEC], u[NV][VEC], g[NV][VEC];
-        bool use[NV];
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            use[i] = in[i] && row < a.rows;
-#pragma unroll
-            for (int j = 0; j < VEC; j++) h[i][j] = g[i][j] = 0.f;
-            if (use[i]) load_vec<VEC>(x + row * C + e[i], h[i]);
-            if (use[i]) load_vec<VEC>(dy + row * C + e[i], g[i]);
-            if (use[i] && z) load_vec<VEC>(z + row * C + e[i], u[i]);
+            values(nx[i], h[i]);
+            values(nz[i], u[i]);
+            values(ng[i], g[i]);
         }
+        ask(row + at.row_step);
         float sum = 0.f, none = 0.f;
         if (a.center) {
 #pragma unroll
@@ -255,7 +282,7 @@ __global__ void __launch_bounds__(THREADS) group_norm_bwd_kernel(GroupNormArgs a
         float sq = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; i++)
-            if (use[i])
+            if (in[i])
 #pragma unroll
                 for (int j = 0; j < VEC; j++) {
                     h[i][j] -= mean;
@@ -266,14 +293,13 @@ __global__ void __launch_bounds__(THREADS) group_norm_bwd_kernel(GroupNormArgs a
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; i++)
-            if (use[i]) {
-                float dg[VEC];
+            if (in[i]) {
 #pragma unroll
                 for (int j = 0; j < VEC; j++) {
                     h[i][j] *= r;
                     const float n = w[i][j] * h[i][j] + b[i][j];
                     const float2 f = activate2(z ? u[i][j] : n, a.act);
-                    dg[j] = g[i][j] * n * f.y;
+                    u[i][j] = g[i][j] * n * f.y;  // dz
                     const float dn = g[i][j] * (z ? f.x : f.y);
                     dw[i][j] += dn * h[i][j];
                     db[i][j] += dn;
@@ -281,20 +307,20 @@ __global__ void __launch_bounds__(THREADS) group_norm_bwd_kernel(GroupNormArgs a
                     s1 += g[i][j];
                     s2 += g[i][j] * h[i][j];
                 }
-                if (z) store_vec<VEC>(dz + row * C + e[i], dg);
+                if (z && row < a.rows) store_vec<VEC>(dz + row * C + e[i], u[i]);
             }
         group_sum2<LPG>(s1, s2, red);
         const float m1 = a.center ? s1 * inv : 0.f, m2 = s2 * inv;
 #pragma unroll
         for (int i = 0; i < NV; i++)
-            if (use[i]) {
+            if (in[i] && row < a.rows) {
 #pragma unroll
                 for (int j = 0; j < VEC; j++) g[i][j] = r * (g[i][j] - m1 - h[i][j] * m2);
                 store_vec<VEC>(dx + row * C + e[i], g[i]);
             }
     }
     if (!part) return;
-    const int rl = (THREADS / LPG) / per;
+    const int rl = blockDim.x / (LPG * per);
     float* pw = part + ((size_t)blockIdx.y * rl + at.slot_row) * 2 * C;
 #pragma unroll
     for (int i = 0; i < NV; i++)
@@ -304,44 +330,46 @@ __global__ void __launch_bounds__(THREADS) group_norm_bwd_kernel(GroupNormArgs a
         }
 }
 
-// grid ceil(2 C / 32): 32 columns a block, 8 threads a column over the partial rows, joined in order.
-__global__ void __launch_bounds__(256) group_norm_params_kernel(const float* part, int n, int C, float* dw, float* db) {
-    __shared__ float sh[8][33];
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), y = threadIdx.x >> 5;
+// grid ceil(2 C / 32): 32 columns a block, 32 threads a column over the partial rows, joined in order.
+__global__ void __launch_bounds__(1024) group_norm_params_kernel(const float* part, int n, int C, float* dw, float* db) {
+    __shared__ float sh[32][33];
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
     float s = 0.f;
     if (c < 2 * C)
-        for (int i = y; i < n; i += 8) s += part[(size_t)i * 2 * C + c];
-    sh[y][threadIdx.x & 31] = s;
+#pragma unroll 8
+        for (int i = y; i < n; i += 32) s += part[(size_t)i * 2 * C + c];
+    sh[y][x] = s;
     __syncthreads();
-    if (y == 0 && c < 2 * C) {
-        float t = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; i++) t += sh[i][threadIdx.x];
-        float* out = c < C ? dw : db;
-        if (out) out[c < C ? c : c - C] = t;
+    s = warp_sum(sh[x][y]);  // column y of this block
+    const int d = blockIdx.x * 32 + y;
+    if (x == 0 && d < 2 * C) {
+        float* out = d < C ? dw : db;
+        if (out) out[d < C ? d : d - C] = s;
     }
 }
 
 struct Grid {
-    int per, rl, x, y;
+    int per, rl, threads, x, y;
 };
-// A block takes as many whole groups as its THREADS / lpg slots hold, then several token rows at a
-// time; the rows are spread over enough blocks for eight per SM, each with the same row count.
+// A block takes as many whole groups as THREADS lanes hold, then several token rows at a time; the
+// rows are spread evenly over about as many blocks as run at once.
 Grid grid_of(const GroupNormArgs& a, int lpg, int blocks_per_sm) {
     Grid g;
     const int slots = THREADS / lpg;
     g.per = a.groups < slots ? a.groups : slots;
     g.rl = slots / g.per;
+    g.threads = (g.per * g.rl * lpg + 31) / 32 * 32;
     g.x = (a.groups + g.per - 1) / g.per;
     const long long rows = (a.rows + g.rl - 1) / g.rl;
-    long long y = (152LL * blocks_per_sm + g.x - 1) / g.x;
+    long long y = (152LL * blocks_per_sm * THREADS / g.threads + g.x - 1) / g.x;
     if (y > rows) y = rows;
+    if (y > 65535) y = 65535;
     const long long each = (rows + y - 1) / y;  // row steps of a block
     g.y = (int)((rows + each - 1) / each);
     return g;
 }
 
-constexpr int kFwdBlocks = 8, kBwdBlocks = 4;  // blocks per SM
+constexpr int kFwdBlocks = 4, kBwdBlocks = 3;  // blocks of THREADS per SM that run at once
 
 // Lanes and vectors for a group of D values: 16-byte vectors where every row of every tensor starts
 // on 16 bytes (D a multiple of the vector and aligned pointers), else single values.
@@ -388,7 +416,7 @@ struct Forward {
     cudaError_t run() const {
         const Grid g = grid_of(a, LPG, kFwdBlocks);
         trace_begin("group_norm_fwd", st);
-        group_norm_fwd_kernel<LPG, VEC, NV, T><<<dim3(g.x, g.y), THREADS, 0, st>>>(a, g.per);
+        group_norm_fwd_kernel<LPG, VEC, NV, T><<<dim3(g.x, g.y), g.threads, 0, st>>>(a, g.per);
         trace_end(st);
         return cudaGetLastError();
     }
@@ -402,13 +430,13 @@ struct Backward {
         const Grid g = grid_of(a, LPG, kBwdBlocks);
         float* p = a.dweight || a.dbias ? part : nullptr;
         trace_begin("group_norm_bwd", st);
-        group_norm_bwd_kernel<LPG, VEC, NV, T><<<dim3(g.x, g.y), THREADS, 0, st>>>(a, g.per, p);
+        group_norm_bwd_kernel<LPG, VEC, NV, T><<<dim3(g.x, g.y), g.threads, 0, st>>>(a, g.per, p);
         trace_end(st);
         if (cudaError_t e = cudaGetLastError()) return e;
         if (!p) return cudaSuccess;
         const int C = a.groups * a.D;
         trace_begin("group_norm_params", st);
-        group_norm_params_kernel<<<(2 * C + 31) / 32, 256, 0, st>>>(p, g.y * g.rl, C, a.dweight, a.dbias);
+        group_norm_params_kernel<<<(2 * C + 31) / 32, 1024, 0, st>>>(p, g.y * g.rl, C, a.dweight, a.dbias);
         trace_end(st);
         return cudaGetLastError();
     }
