@@ -90,15 +90,18 @@ __device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t 
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
-__device__ __forceinline__ uint32_t bf16x2_neg(uint32_t a) { return a ^ 0x80008000u; }
+__device__ __forceinline__ uint32_t bf16x2_neg(uint32_t a) {
+    uint32_t d;
+    asm("neg.bf16x2 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
 
 // Bounded wait of a whole warp for phase `parity`, in few instructions, since the warps' roles share the
 // instruction caches: the warp is parked in the barrier unit for up to a millisecond at a time. Gives
 // up after about a second, leaving the site in *failed, or as soon as another warp has.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* failed, int site) {
-    const long long t0 = clock64();
-    uint32_t ok;
-    do {
+    auto parked = [&]() {
+        uint32_t ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
             "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
@@ -106,9 +109,17 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volat
             : "=r"(ok)
             : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
             : "memory");
-        if (!ok && clock64() - t0 > kWaitCycles) *failed = site;
-    } while (!ok && !*failed);
-    return __all_sync(0xffffffffu, ok);
+        return __all_sync(0xffffffffu, ok) != 0;
+    };
+    bool ok = parked();
+    if (!ok) {
+        const long long t0 = clock64();
+        while (!(ok = parked())) {
+            if (clock64() - t0 > kWaitCycles) *failed = site;
+            if (__any_sync(0xffffffffu, *failed)) break;
+        }
+    }
+    return ok;
 }
 
 }  // namespace linear

@@ -25,7 +25,7 @@
 //
 // Warps: 0-7 turn P into P' and finish the output (a thread is half a token row), 8-11 hold the
 // state (a thread is a state row), 12-19 form c' in pieces of PIECE tokens (in the summary 0-7 do
-// too), 20 copies tiles in, 21 issues the products. The state rows need the registers: warps
+// too), 20 and 23 copy tiles in, 21 issues the products, 22 stores the output tiles. The state rows need the registers: warps
 // 12-23 give some up (setmaxnreg). The products of a chunk are issued as X, the next chunk's sum of the
 // state, Y, the next chunk's P: each has the others' time to wait for the warps that feed it. Input tiles (128 tokens,
 // two 64-channel panels, 32 KB) have three slots for c, which is wanted a chunk ahead and whose
@@ -50,9 +50,9 @@ namespace {
 constexpr int SLOTS = 6, SLOTS_C = 3;  // input tiles, those of c
 constexpr uint32_t SLOT = TILE;
 constexpr uint32_t AT_S = SLOTS * SLOT;     // bf16 state [128 x 128]
-constexpr uint32_t AT_W = AT_S + 32768;     // tables: 32 and 64 floats, three of 128 bf16 pairs
-constexpr uint32_t BYTES = AT_W + 384 + 1536;
-static_assert(BYTES + 256 <= 232448, "shared memory");
+constexpr uint32_t AT_W = AT_S + 32768;     // decays: three tables of 128 bf16 pairs
+constexpr uint32_t BYTES = AT_W + 1536;
+static_assert(BYTES + 1024 <= 232448, "shared memory");
 constexpr int THREADS = 768;
 // Registers a thread: 768 threads start with 80; 8 warps keep them, 4 go up, 8 and 4 go down.
 constexpr int REGS = 80, REGS_STATE = 176, REGS_DECAY = 48, REGS_REST = 48;
@@ -95,7 +95,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     extern __shared__ __align__(1024) uint8_t sm[];  // swizzled tiles: no room for rounding up
     const uint32_t sb = smem_u32(sm);
     __shared__ uint64_t full[SLOTS], empty[SLOTS], bfull[4], bfree[4];
-    __shared__ uint64_t pfull, xfull, pready, xdone, yfull, yfree, sfull[2], sfree[2], sready, drain;
+    __shared__ uint64_t pfull, xfull, pready, yfull, xready, staged, sfull[2], sfree[2], drain;
+    __shared__ float tri[160];
     __shared__ uint32_t tmem_sh;
     __shared__ int failed, used[SLOTS];
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     // TMEM columns. Output pass: P (P' packed in the first half of each 64), X and then the output, the
     // chunk's sum of the state, a ring of pieces of c'. Summary: two sums and the ring.
-    constexpr int PIECE = !MIX ? 64 : 32;              // tokens of a piece
+    constexpr int PIECE = MIX ? 32 : 64;               // tokens of a piece
     constexpr int STEPS = PIECE / 16;                  // products of a piece and term
     constexpr uint32_t STEP = 8 * TERMS;               // columns of a step: its terms, eight each
     constexpr uint32_t COL_P = 0, COL_X = 128, COL_S = MIX ? 256 : 0, COL_C = MIX ? 384 : 256;
@@ -147,21 +148,22 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_init(&pfull, 1);
         mbar_init(&xfull, 1);
         mbar_init(&pready, 8);
-        mbar_init(&xdone, 1);
+        mbar_init(&staged, 8);
         mbar_init(&yfull, 1);
-        mbar_init(&yfree, 8);
-        mbar_init(&sready, 4);
+        mbar_init(&xready, 12);  // the copy of the state is written (4) and the last output read (8)
         mbar_init(&drain, 1);
         fence_barrier_init();
     }
     const float g = s.g[hv];
-    float* pd = reinterpret_cast<float*>(sm + AT_W);  // l^(31-i), in reverse l^i
-    float* tri = pd + 32;                             // tri[32 + r - j]: f l^|r-j| of a pair in order, else 0
+    // tri[31 + r - j] = f l^(r-j) of a pair in order, else 0; in reverse tri[127 + r - j] = f l^(j-r)
+    const int tri_zero = a.reverse ? 127 : 31;
+    if (tid < 160) {
+        const int d = a.reverse ? tri_zero - tid : tid - tri_zero;
+        tri[tid] = d >= 0 ? a.fp * power(g, d) : 0.f;
+    }
     // parts w1, w2, w3 of f'' l^e for two tokens in a row, the first of exponent e (the next e - 1, in
     // reverse e + 1)
-    uint32_t* parts = reinterpret_cast<uint32_t*>(tri + 64);
-    if (tid < 32) pd[tid] = power(g, a.reverse ? tid : 31 - tid);
-    if (tid < 64) tri[tid] = (a.reverse ? tid <= 32 : tid >= 32) ? a.fp * power(g, abs(tid - 32)) : 0.f;
+    uint32_t* parts = reinterpret_cast<uint32_t*>(sm + AT_W);
     if (tid < 128) {
         float x0 = a.fu * power(g, tid), x1 = a.fu * power(g, a.reverse ? tid + 1 : max(tid - 1, 0));
 #pragma unroll
@@ -186,35 +188,38 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int quarter = w & 3, part = w >> 2;
         const uint32_t lanes = tm + ((uint32_t)(32 * quarter) << 16);
         constexpr int OWN = STEPS * 4 / DECAY_WARPS;  // steps of a piece for each warp
+        // where this lane's matrix row lies in a step's 16 tokens of the tile of c
+        const uint32_t at_row = sw128_chunk((lane >> 4) * 8 + (lane & 7), 4 * quarter + (lane >> 3 & 1), C);
         int piece = 0;
         for (int i = 0; i < nc; i++) {
             const int m = tokens_of(i), nj = (m + 15) / 16;
             const uint32_t ct = sb + slot_c(i) * SLOT, bt = sb + slot_b(i) * SLOT;
             bool ok = wait_phase(&full[slot_c(i)], i / SLOTS_C & 1, &failed, 60);
-            if ((m & 15) && s.lengths) {
-                // rows past the last token that enter the last 16-token step: zero, whatever they hold
+            if (m < C && s.lengths) {
                 ok = ok && wait_phase(&full[slot_b(i)], i / SLOTS_B & 1, &failed, 61);
-                const int z = m + 2 * w + (lane >> 4), ch = lane & 15;
-                if (ok && z < 16 * nj) {
-                    if (ch < 8 * a.panels_v) st_shared_v4(ct + sw128_chunk(z, ch, C), 0, 0, 0, 0);
+                // rows past the last token: zero in b, and in c where they enter the last 16-token step,
+                // whatever they hold
+                const int ch = lane & 15;
+#pragma unroll 1
+                for (int z = m + 2 * w + (lane >> 4); ok && z < C; z += 2 * DECAY_WARPS) {
+                    if (z < 16 * nj && ch < 8 * a.panels_v) st_shared_v4(ct + sw128_chunk(z, ch, C), 0, 0, 0, 0);
                     if (ch < 8 * a.panels_k) st_shared_v4(bt + sw128_chunk(z, ch, C), 0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
             }
+#pragma unroll 1
             for (int j = 0; j < nj && ok; j += STEPS, piece++) {
                 const int r = piece % RING;
                 if (piece >= RING) ok = wait_phase(&bfree[r], (piece / RING + 1) & 1, &failed, 62);
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                 for (int e = 0; e < OWN; e++) {
                     const int in = part * OWN + e, t = 16 * (j + in);  // step of the piece, its first token
-                    if (j + in >= nj || quarter >= 2 * a.panels_v) continue;
+                    if (t >= m || quarter >= 2 * a.panels_v) continue;
                     uint32_t v[2][4];
-#pragma unroll
-                    for (int g2 = 0; g2 < 2; g2++)
-                        ldmatrix_x4_trans(
-                            ct + sw128_chunk(t + (lane >> 4) * 8 + (lane & 7), 4 * quarter + 2 * g2 + (lane >> 3 & 1), C), v[g2]);
+                    ldmatrix_x4_trans(ct + t * 128 + at_row, v[0]);
+                    ldmatrix_x4_trans(ct + t * 128 + (at_row ^ 32u), v[1]);
                     const int u = t + 2 * (lane & 3);  // first token of v[.][0], v[.][1]; that of the others is u + 8
                     if (t + 16 > m) {                  // nothing past the last token, whatever it holds
 #pragma unroll
@@ -260,30 +265,34 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     if (warp >= 20) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
-        if (warp == 20) {
-            auto load = [&](const CUtensorMap* map, int panels, int head, int k, int use, int i) {  // use: tiles before
-                if (use > 0 && !wait_phase(&empty[k], (use + 1) & 1, &failed, 40)) return false;
+        if (warp == 20 || warp == 23) {
+            // Tiles are asked for as their slots come free: c by one warp, since it is wanted first and kept
+            // longest, b and a by another (its steps: b of chunk 0, b 1, a 0, b 2, a 1, ..). In the output
+            // pass, whose one slot for a is free for a short time only, a step also brings its tile two chunks
+            // on into L2 (further ahead costs more than it hides: 227 us at six chunks, T = 32768).
+            const bool for_c = warp == 20;
+            const int steps = for_c ? nc : 2 * nc;
+#pragma unroll 1
+            for (int t = 0; t < steps; t++) {
+                const bool is_a = MIX && !for_c && t > 0 && (t % 2 == 0 || t == 2 * nc - 1);
+                if (!MIX && !for_c && t >= nc) break;
+                const int i = for_c || !MIX ? t : is_a ? (t - 1) / 2 : (t + 1) / 2;
+                const CUtensorMap* map = for_c ? &mc : is_a ? &ma : &mb;
+                const int panels = for_c ? a.panels_v : a.panels_k, head = for_c ? hv : hk;
+                const int k = for_c ? slot_c(i) : is_a ? slot_a : slot_b(i);
+                const int use = for_c ? i / SLOTS_C : is_a ? i : i / SLOTS_B;  // tiles that the slot had before
+                if (use > 0 && !wait_phase(&empty[k], (use + 1) & 1, &failed, 40)) break;
                 if (lane == 0) {
+                    const int t0 = first + chunk_of(i) * C, far = first + chunk_of(min(i + 2, nc - 1)) * C;
                     mbar_expect_tx(&full[k], panels * PANEL);
-                    for (int p = 0; p < panels; p++)
-                        tma_load_4d(sm + k * SLOT + p * PANEL, map, 64 * p, head, first + chunk_of(i) * C, b, &full[k]);
                     used[k] = use + 1;
-                }
-                return true;
-            };
-            for (int i = -1; i < nc; i++) {
-                if (lane == 0 && i + 2 < nc) {  // into L2, two chunks before it is wanted
-                    const int t0 = first + chunk_of(i + 2) * C;
-                    for (int p = 0; p < a.panels_v; p++) tma_prefetch_4d(&mc, 64 * p, hv, t0, b);
-                    for (int p = 0; p < a.panels_k; p++) {
-                        tma_prefetch_4d(&mb, 64 * p, hk, t0, b);
-                        if (MIX) tma_prefetch_4d(&ma, 64 * p, hk, t0, b);
+#pragma unroll 1
+                    for (int p = 0; p < panels; p++) {
+                        tma_load_4d(sm + k * SLOT + p * PANEL, map, 64 * p, head, t0, b, &full[k]);
+                        if (MIX) tma_prefetch_4d(map, 64 * p, head, far, b);
                     }
                 }
-                if (MIX && i >= 0 && !load(&ma, a.panels_k, hk, slot_a, i, i)) break;
-                if (i + 1 < nc && (!load(&mc, a.panels_v, hv, slot_c(i + 1), (i + 1) / SLOTS_C, i + 1) ||
-                                   !load(&mb, a.panels_k, hk, slot_b(i + 1), (i + 1) / SLOTS_B, i + 1)))
-                    break;
+                __syncwarp();
             }
         } else if (warp == 21) {
             const int dk = 64 * a.panels_k, dv = 64 * a.panels_v;
@@ -294,7 +303,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 return wait_phase(bar, parity, &failed, site);
             };
             auto issue_p = [&](int i) {  // over P', which the Y product before has read
-                if (!wait(&full[slot_b(i)], i / SLOTS_B & 1, 41) || !wait(&full[slot_a], i & 1, 42)) return false;
+                if (!wait(&full[slot_a], i & 1, 42)) return false;  // b has been there for the sum
                 tc_fence_after();
                 const uint32_t ad = lo_kmajor(sb + slot_a * SLOT), bd = lo_kmajor(sb + slot_b(i) * SLOT);
 #pragma unroll 1
@@ -336,8 +345,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int i = -1; i < nc; i++) {
                 const bool now = MIX && i >= 0;
                 if (now) {
-                    if (!wait(&sready, i & 1, 46)) break;
-                    if (i > 0 && !wait(&yfree, (i - 1) & 1, 47)) break;
+                    if (!wait(&xready, i & 1, 46)) break;
                     tc_fence_after();
                     const uint32_t ad = lo_kmajor(sb + slot_a * SLOT), sd = lo_kmajor(sb + AT_S);
 #pragma unroll 1
@@ -346,7 +354,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                         for (int k = 0; k < 4; k++)
                             mma_ss(tm + COL_X, ad + p * (PANEL >> 4) + 2 * k, sd + p * (PANEL >> 4) + 2 * k, id_x, k > 0 ? 1u : p);
                     commit(&xfull);
-                    commit(&xdone);
                     commit(&empty[slot_a]);  // P read it before
                 }
                 if (i + 1 < nc && !issue_s(i + 1)) break;
@@ -368,6 +375,19 @@ __global__ void __launch_bounds__(THREADS, 1)
             commit(&drain);  // every product issued so far has completed before TMEM is released
             int never = 0;
             wait_phase(&drain, 0, &never, 1);
+        } else if (MIX && warp == 22) {
+            for (int i = 0; i < nc; i++) {
+                if (!wait_phase(&staged, i & 1, &failed, 48)) break;
+                if (lane == 0) {
+                    for (int p = 0; p < a.panels_v; p++)
+                        tma_store_4d(&mo, sm + slot_c(i) * SLOT + p * PANEL, 64 * p, hv, first + chunk_of(i) * C, b);
+                    bulk_commit();
+                    bulk_wait_read_all();
+                    mbar_arrive(&empty[slot_c(i)]);
+                }
+                __syncwarp();
+            }
+            if (lane == 0) bulk_wait_all();
         }
     } else if (warp >= 12 || (!MIX && warp < 8)) {
         if (warp >= 12) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_DECAY));
@@ -381,8 +401,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int quarter = warp & 3, half = warp >> 2;
             const int r = 32 * quarter + lane;  // token row; columns 64 half ..
             const uint32_t row = tm + ((uint32_t)(32 * quarter) << 16);
-            bool bad = false;
-            for (int i = 0; i < nc && !bad; i++) {
+            if (lane == 0) mbar_arrive(&xready);
+            for (int i = 0; i < nc; i++) {
                 const int m = tokens_of(i);
                 bool ok = wait_phase(&pfull, i & 1, &failed, 50);
                 tc_fence_after();
@@ -398,24 +418,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                             float p[32];
                             tmem_ld32(row + COL_P + 32 * cb, p);
                             tmem_wait_ld();
-                            if (32 * cb + 32 > m)  // past the last token, whatever was there
+                            const float* in = tri + tri_zero + r - 32 * cb;
 #pragma unroll
-                                for (int e = 0; e < 32; e++) p[e] = 32 * cb + e < m ? p[e] : 0.f;
-                            if (cb == quarter) {
-                                const float* in = tri + 32 + lane;
-#pragma unroll
-                                for (int e = 0; e < 32; e++) p[e] *= in[-e];
-                            } else {  // l^|r-j| as l to the tokens up to this block of columns, times l to those in it
-                                const float f = a.fp * power(g, a.reverse ? 32 * cb - r : r - 32 * cb - 31);
-#pragma unroll
-                                for (int e = 0; e < 32; e += 4) {
-                                    const float4 x = *reinterpret_cast<const float4*>(pd + e);
-                                    scale2(p + e, x.x, x.y);
-                                    scale2(p + e + 2, x.z, x.w);
-                                    scale2(p + e, f);
-                                    scale2(p + e + 2, f);
-                                }
-                            }
+                            for (int e = 0; e < 32; e++) p[e] *= in[-e];
 #pragma unroll
                             for (int e = 0; e < 16; e++) w[e] = pack_bf16(p[2 * e], p[2 * e + 1]);
                         }
@@ -464,18 +469,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tc_fence_before();
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&yfree);
+                    if (lane == 0) {
+                        mbar_arrive(&xready);
+                        mbar_arrive(&staged);
+                    }
                 }
-                bad = bar_sync_or(1, 256, !ok || failed);
-                if (!bad && tid == 0) {
-                    for (int p = 0; p < a.panels_v; p++)
-                        tma_store_4d(&mo, sm + slot_c(i) * SLOT + p * PANEL, 64 * p, hv, first + chunk_of(i) * C, b);
-                    bulk_commit();
-                    bulk_wait_read_all();
-                    mbar_arrive(&empty[slot_c(i)]);
-                }
+                if (!ok) break;
             }
-            if (tid == 0) bulk_wait_all();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_STATE));
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (e < 8 * a.panels_k) st_chunk(sb + AT_S + sw128_chunk(row, e, C), S + 8 * e, 1.f);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sready);
+            if (lane == 0) mbar_arrive(&xready);
         };
         // The copy of chunk i, and its image. The four warps decide together whether to go on.
         auto share_state = [&](int i, bool ok) {
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (lane == 0) mbar_arrive(&sfree[i % SUMS]);
             }
             if (MIX && i + 1 < nc) {
-                ok = ok && wait_phase(&xdone, i & 1, &failed, 64);
+                ok = ok && wait_phase(&xfull, i & 1, &failed, 64);  // X has read the last copy
                 ok = share_state(i + 1, ok);
             }
             go = ok;
@@ -632,9 +632,10 @@ cudaError_t launch_linear_tc_mix(const LinearMixArgs& x, const float* start, int
     return one ? launch<true, 4>(maps, a, x.s.nseg, name, st) : launch<true, 2>(maps, a, x.s.nseg, name, st);
 }
 
-// Segments of whole chunks, one CTA each, on 152 SMs. In units of one chunk of the mix pass: a wave
-// of it takes a segment's chunks and about three for its start, with several segments there is
-// the summary too, at about 0.6 a chunk, and the combine step reads every segment's state.
+// Segments of whole chunks, one CTA each, on 152 SMs. In units of one chunk of the output pass (2.7 us): a
+// wave of it takes a segment's chunks and about four for its start and end; with several segments there is
+// the summary too, at about 0.6 a chunk, and the combine step, which reads every segment's state. At
+// T = 32768 and 32 heads 4 segments take 105 + 8 + 170 us, 9 take 109 + 10 + 174, 19 take 121 + 16 + 190.
 int linear_tc_segments(int B, int T, int Hv) {
     const long long chunks = (T + C - 1) / C, heads = (long long)B * Hv;
     if (chunks <= 1 || heads <= 0) return 1;
@@ -642,8 +643,8 @@ int linear_tc_segments(int B, int T, int Hv) {
     double least = 1e300;
     for (long long n = 1; n <= chunks && (n == 1 || heads * n <= 8 * 152); n++) {
         const long long len = (chunks + n - 1) / n, real = (chunks + len - 1) / len;
-        const double mix = (double)((heads * real + 151) / 152) * (len + 3);
-        const double sum = real > 1 ? (double)((heads * (real - 1) + 151) / 152) * (0.6 * len + 3) + 3 + 0.2 * real : 0.0;
+        const double mix = (double)((heads * real + 151) / 152) * (len + 4);
+        const double sum = real > 1 ? (double)((heads * (real - 1) + 151) / 152) * (0.6 * len + 5) + 3 + 0.2 * real : 0.0;
         if (mix + sum < least) {
             least = mix + sum;
             best = (int)real;
