@@ -110,12 +110,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     // TMEM columns. Output pass: P (P' packed in the first half of each 64), X and then the output, the
     // chunk's sum of the state, a ring of pieces of c'. Summary: two sums and the ring.
-    constexpr int PIECE = MIX ? 32 : 64;               // tokens of a piece
+    constexpr int PIECE = MIX && TERMS == 4 ? 32 : 64; // tokens of a piece
     constexpr int STEPS = PIECE / 16;                  // products of a piece and term
     constexpr uint32_t STEP = 8 * TERMS;               // columns of a step: its terms, eight each
     constexpr uint32_t COL_P = 0, COL_X = 128, COL_S = MIX ? 256 : 0, COL_C = MIX ? 384 : 256;
     constexpr int SUMS = MIX ? 1 : 2, RING = (512 - COL_C) / (STEPS * STEP);
-    static_assert(RING >= 2 && RING <= 4 && (TERMS == 2 || TERMS == 4), "pieces");
+    static_assert(RING == 2 && (TERMS == 2 || TERMS == 4), "pieces");
     constexpr int SLOTS_B = MIX ? 2 : 3;
     auto slot_c = [](int i) { return i % SLOTS_C; };
     auto slot_b = [](int i) { return SLOTS_C + i % SLOTS_B; };
