@@ -86,19 +86,19 @@ cudaError_t states(const LinearShape& s, const void* rows, const void* cols, flo
     LinearSummaryArgs a{s, rows, cols, factor, reverse, z};
     if (cudaError_t e = launch_linear_summary(a, st)) return e;
     LinearCombineArgs c{s, init, reverse, z, last};
-    return launch_linear_combine(c, st);
+    return launch_linear_combine(c, false, st);
 }
 
 // A mix pass on the tensor cores from the state `init` before it: with several segments, the states that
 // enter them first. The first kernel of a call clears its status word.
 cudaError_t mix_tc(const LinearMixArgs& m, const void* rows, const void* cols, float factor, int reverse,
                    const float* init, float* z, float* last, int* status, bool clear, cudaStream_t st) {
-    if (m.s.nseg == 1) return launch_linear_tc_mix(m, init, 1, last, status, clear, st);
+    if (m.s.nseg == 1) return launch_linear_tc_mix(m, init, 1, last, status, clear, false, st);
     LinearSummaryArgs a{m.s, rows, cols, factor, reverse, z};
     if (cudaError_t e = launch_linear_tc_summary(a, last != nullptr, status, clear, st)) return e;
     LinearCombineArgs c{m.s, init, reverse, z, last};
-    if (cudaError_t e = launch_linear_combine(c, st)) return e;
-    return launch_linear_tc_mix(m, z, m.s.nseg, nullptr, status, false, st);
+    if (cudaError_t e = launch_linear_combine(c, true, st)) return e;
+    return launch_linear_tc_mix(m, z, m.s.nseg, nullptr, status, false, true, st);
 }
 
 // No token: the state passes through.

@@ -15,6 +15,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "linear.h"
+#include "linear_dev.cuh"
 
 namespace gdr {
 
@@ -22,7 +23,7 @@ namespace {
 
 constexpr int LC = 64;  // tokens of a chunk
 
-__device__ __forceinline__ float power(float g, int n) { return n == 0 ? 1.f : expf(g * (float)n); }
+using linear::power;
 
 __device__ __forceinline__ int valid_tokens(const LinearShape& s, int b) {
     return s.lengths ? min(max(s.lengths[b], 0), s.T) : s.T;
@@ -108,6 +109,8 @@ __global__ void __launch_bounds__(256) linear_summary_kernel(LinearSummaryArgs a
 __global__ void __launch_bounds__(256) linear_combine_kernel(LinearCombineArgs a) {
     const LinearShape& s = a.s;
     const int i = (blockIdx.x * 256 + threadIdx.x) * 4, D = s.Dv * s.Dk;
+    linear::next_kernel_may_start();
+    linear::wait_kernel_before();
     if (i >= D) return;
     const int n = valid_tokens(s, blockIdx.z);
     const size_t bh = (size_t)blockIdx.z * s.Hv + blockIdx.y;
@@ -374,11 +377,12 @@ cudaError_t launch_linear_summary(const LinearSummaryArgs& a, cudaStream_t st) {
     return a.s.bf16 ? summary_of<__nv_bfloat16>(a, st) : summary_of<float>(a, st);
 }
 
-cudaError_t launch_linear_combine(const LinearCombineArgs& a, cudaStream_t st) {
+cudaError_t launch_linear_combine(const LinearCombineArgs& a, bool overlap, cudaStream_t st) {
     trace_begin("linear_combine", st);
-    linear_combine_kernel<<<dim3((a.s.Dv * a.s.Dk + 1023) / 1024, a.s.Hv, a.s.B), 256, 0, st>>>(a);
+    const dim3 grid((a.s.Dv * a.s.Dk + 1023) / 1024, a.s.Hv, a.s.B);
+    const cudaError_t e = launch_after(linear_combine_kernel, grid, 256, 0, st, overlap, a);
     trace_end(st);
-    return cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_linear_mix(const LinearMixArgs& a, cudaStream_t st) {

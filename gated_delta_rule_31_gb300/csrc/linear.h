@@ -59,19 +59,38 @@ struct LinearMixArgs {
                     // (b, hv, chunk), for launch_linear_tc_grad; or null
 };
 
+// A launch that may begin while the kernel before it on the stream, one of the same call, still runs; that
+// kernel lets it (griddepcontrol.launch_dependents), and the new one waits before it reads its results.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t st, bool overlap, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = overlap ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 int linear_segments(int B, int T, int Hv, int Dv);
 cudaError_t launch_linear_summary(const LinearSummaryArgs& a, cudaStream_t st);
-cudaError_t launch_linear_combine(const LinearCombineArgs& a, cudaStream_t st);
+cudaError_t launch_linear_combine(const LinearCombineArgs& a, bool overlap, cudaStream_t st);
 cudaError_t launch_linear_mix(const LinearMixArgs& a, cudaStream_t st);
 
 // bf16 on the tensor cores (linear_tc.cu): the summary of the segments (all of them, or all but the
 // last in processing order), and the mix passes of o and dv. start: the state entering each
 // segment (start_segs = nseg), or before all of them (1; may be null: zero). last: the state after
-// the last segment, or null. status: status word, cleared by the kernel if `clear`.
+// the last segment, or null. status: status word, cleared by the kernel if `clear`. overlap: the kernel
+// before it on the stream is of the same call (launch_after).
 int linear_tc_segments(int B, int T, int Hv);
 cudaError_t launch_linear_tc_summary(const LinearSummaryArgs& a, bool all, int* status, bool clear, cudaStream_t st);
 cudaError_t launch_linear_tc_mix(const LinearMixArgs& a, const float* start, int start_segs, float* last, int* status,
-                                 bool clear, cudaStream_t st);
+                                 bool clear, bool overlap, cudaStream_t st);
 
 // dq and dk of bf16 problems from the kept states (linear_grad.cu).
 struct LinearGradArgs {

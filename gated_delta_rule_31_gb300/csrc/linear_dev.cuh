@@ -72,12 +72,14 @@ __device__ __forceinline__ void scale2(float* x, float f0, float f1) {
     asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(w));
     asm("mov.b64 {%0, %1}, %2;" : "=f"(x[0]), "=f"(x[1]) : "l"(v));
 }
-__device__ __forceinline__ void axpy2(float* s, float f, const float* d) {  // s <- f s + d
+template <bool FADE>  // s <- f s + d, or s + f d
+__device__ __forceinline__ void axpy2(float* s, float f, const float* d) {
     uint64_t v, w, u;
     asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(s[0]), "f"(s[1]));
     asm("mov.b64 %0, {%1, %1};" : "=l"(w) : "f"(f));
     asm("mov.b64 %0, {%1, %2};" : "=l"(u) : "f"(d[0]), "f"(d[1]));
-    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(v) : "l"(w), "l"(u));
+    if (FADE) asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(v) : "l"(w), "l"(u));
+    else asm("fma.rn.f32x2 %0, %2, %1, %0;" : "+l"(v) : "l"(w), "l"(u));
     asm("mov.b64 {%0, %1}, %2;" : "=f"(s[0]), "=f"(s[1]) : "l"(v));
 }
 __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
@@ -95,6 +97,11 @@ __device__ __forceinline__ uint32_t bf16x2_neg(uint32_t a) {
     asm("neg.bf16x2 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
+
+// Kernels of one call start while the one before still runs (programmatic dependent launch): each lets the
+// next begin at once and waits for the one before to complete just ahead of what it reads of it.
+__device__ __forceinline__ void next_kernel_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Bounded wait of a whole warp for phase `parity`, in few instructions, since the warps' roles share the
 // instruction caches: the warp is parked in the barrier unit for up to a millisecond at a time. Gives

@@ -127,6 +127,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp >= 16) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
         if (warp == 16) {
+            wait_kernel_before();  // the adjoints
             int t = 0, k = 0;  // heads and units so far
             bool ok = true;
 #pragma unroll 1
@@ -404,9 +405,10 @@ cudaError_t launch_linear_tc_grad(const LinearGradArgs& x, cudaStream_t st) {
     a.status = x.status;
     trace_begin("linear_grad", st);
     const long long units = (long long)s.B * ((s.T + C - 1) / C) * s.Hk;
-    linear_grad_kernel<<<(unsigned)(units < 152 ? units : 152), THREADS, BYTES, st>>>(mq, mk, mv, mdo, mdq, mdk, a);
+    const cudaError_t e = launch_after(linear_grad_kernel, dim3((unsigned)(units < 152 ? units : 152)), THREADS, BYTES, st,
+                                       true, mq, mk, mv, mdo, mdq, mdk, a);
     trace_end(st);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace gdr

@@ -125,7 +125,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int n = s.lengths ? min(max(s.lengths[b], 0), s.T) : s.T;
     const int begin = seg * s.seg_tokens, end = min(begin + s.seg_tokens, s.T);
     const int first = min(begin, n), last = min(end, n), nc = (last - first + C - 1) / C;
-    auto chunk_of = [&](int i) { return a.reverse ? nc - 1 - i : i; };
+    // The summary, which may take a segment's chunks in any order, ends with those that the output pass begins
+    // with: part of them it then finds in L2.
+    auto chunk_of = [&](int i) { return (a.reverse != 0) == MIX ? nc - 1 - i : i; };
     auto tokens_of = [&](int i) { return min(C, last - first - chunk_of(i) * C); };
 
     if (tid == 0) {
@@ -181,6 +183,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    next_kernel_may_start();
     const uint32_t tm = tmem_sh;
 
     // Pieces of c' into TMEM, by DECAY_WARPS warps of which this is number w (warp & 3 is its TMEM quarter).
@@ -483,6 +486,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t lanes = tm + ((uint32_t)(32 * (warp & 3)) << 16);
         const size_t state = (size_t)s.Dv * s.Dk;
         float S[128];
+        wait_kernel_before();  // the states that enter the segments; the inputs come from before the call
         {
             const float* p = a.start ? a.start + (bh * a.start_segs + (a.start_segs > 1 ? seg : 0)) * state : nullptr;
 #pragma unroll
@@ -521,7 +525,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             bool ok = wait_phase(&sfull[i % SUMS], i / SUMS & 1, &failed, 63);
             if (ok) {
                 tc_fence_after();
-                const float over = power(g, tokens_of(i));
+                // output pass: S <- l^m S + sum; summary: S <- S + l^(tokens of the segment after the chunk) sum
+                const int t0 = chunk_of(i) * C, tokens = last - first;
+                const float over = power(g, MIX ? tokens_of(i) : a.reverse ? t0 : max(tokens - t0 - C, 0));
 #pragma unroll
                 for (int h = 0; h < 4; h++) {
                     if (h >= 2 * a.panels_k) continue;
@@ -529,7 +535,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tmem_ld32(lanes + COL_S + 128 * (i % SUMS) + 32 * h, d);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) axpy2(S + 32 * h + e, over, d + e);
+                    for (int e = 0; e < 32; e += 2) axpy2<MIX>(S + 32 * h + e, over, d + e);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -574,11 +580,12 @@ cudaError_t allow_smem() {
 }
 
 template <bool MIX, int TERMS>
-cudaError_t launch(const CUtensorMap* maps, const TcArgs& a, int segs, const char* name, cudaStream_t st) {
+cudaError_t launch(const CUtensorMap* maps, const TcArgs& a, int segs, const char* name, bool overlap, cudaStream_t st) {
     trace_begin(name, st);
-    linear_tc_kernel<MIX, TERMS><<<dim3(segs, a.s.Hv, a.s.B), THREADS, BYTES, st>>>(maps[0], maps[1], maps[2], maps[3], a);
+    const cudaError_t e = launch_after(linear_tc_kernel<MIX, TERMS>, dim3(segs, a.s.Hv, a.s.B), THREADS, BYTES, st, overlap,
+                                       maps[0], maps[1], maps[2], maps[3], a);
     trace_end(st);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace
@@ -599,11 +606,11 @@ cudaError_t launch_linear_tc_summary(const LinearSummaryArgs& x, bool all, int* 
     a.status = status;
     a.clear_status = clear;
     a.first_seg = all || !x.reverse ? 0 : 1;
-    return launch<false, 4>(maps, a, all ? x.s.nseg : x.s.nseg - 1, "linear_summary", st);
+    return launch<false, 4>(maps, a, all ? x.s.nseg : x.s.nseg - 1, "linear_summary", false, st);
 }
 
 cudaError_t launch_linear_tc_mix(const LinearMixArgs& x, const float* start, int start_segs, float* last, int* status,
-                                 bool clear, cudaStream_t st) {
+                                 bool clear, bool overlap, cudaStream_t st) {
     const bool rev = x.pass == LINEAR_DV;
     // One segment carries the state that leaves the call, with four terms (also where the caller does not
     // want it, so that the kept states are the same); with several it comes from the summary.
@@ -629,7 +636,7 @@ cudaError_t launch_linear_tc_mix(const LinearMixArgs& x, const float* start, int
     a.status = status;
     a.clear_status = clear;
     const char* name = rev ? "linear_dv" : "linear_o";
-    return one ? launch<true, 4>(maps, a, x.s.nseg, name, st) : launch<true, 2>(maps, a, x.s.nseg, name, st);
+    return one ? launch<true, 4>(maps, a, x.s.nseg, name, overlap, st) : launch<true, 2>(maps, a, x.s.nseg, name, overlap, st);
 }
 
 // Segments of whole chunks, one CTA each, on 152 SMs. In units of one chunk of the output pass (2.7 us): a
