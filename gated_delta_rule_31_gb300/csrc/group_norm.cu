@@ -42,45 +42,96 @@ template <int VEC, typename T>
 __device__ __forceinline__ typename RawOf<VEC, T>::type load_raw(const T* p) {
     return *reinterpret_cast<const typename RawOf<VEC, T>::type*>(p);
 }
-__device__ __forceinline__ void values(const uint4& u, float* x) {
-    x[0] = bf16lo(u.x); x[1] = bf16hi(u.x); x[2] = bf16lo(u.y); x[3] = bf16hi(u.y);
-    x[4] = bf16lo(u.z); x[5] = bf16hi(u.z); x[6] = bf16lo(u.w); x[7] = bf16hi(u.w);
+// Values are worked on in pairs, one instruction for two (fp32 pairs), or singly where VEC is 1.
+struct Pair {
+    uint64_t v;
+};
+__device__ __forceinline__ Pair pair(float a, float b) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(a), "f"(b));
+    return p;
 }
-__device__ __forceinline__ void values(const float4& u, float* x) {
-    x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+__device__ __forceinline__ float2 split(Pair p) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p.v));
+    return f;
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+    Pair d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+    Pair d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return d;
+}
+__device__ __forceinline__ float total(Pair p) {
+    const float2 f = split(p);
+    return f.x + f.y;
+}
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float total(float x) { return x; }
+__device__ __forceinline__ void fill(Pair& p, float x) { p = pair(x, x); }
+__device__ __forceinline__ void fill(float& p, float x) { p = x; }
+template <typename V>
+__device__ __forceinline__ V all(float x) {
+    V v;
+    fill(v, x);
+    return v;
+}
+
+template <int VEC>
+struct Lanes {  // VEC values as N units of type V
+    using V = Pair;
+    static constexpr int N = VEC / 2;
+};
+template <>
+struct Lanes<1> {
+    using V = float;
+    static constexpr int N = 1;
+};
+
+__device__ __forceinline__ Pair bf16_pair(uint32_t u) { return pair(bf16lo(u), bf16hi(u)); }
+__device__ __forceinline__ void values(const uint4& u, Pair* x) {
+    x[0] = bf16_pair(u.x); x[1] = bf16_pair(u.y); x[2] = bf16_pair(u.z); x[3] = bf16_pair(u.w);
+}
+__device__ __forceinline__ void values(const float4& u, Pair* x) {
+    x[0] = pair(u.x, u.y); x[1] = pair(u.z, u.w);
 }
 __device__ __forceinline__ void values(const __nv_bfloat16& u, float* x) { x[0] = __bfloat162float(u); }
 __device__ __forceinline__ void values(const float& u, float* x) { x[0] = u; }
-template <int VEC, typename T>
-__device__ __forceinline__ void store_vec(T* p, const float* x) {
-    if constexpr (VEC == 8)
-        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                                                  pack_bf16(x[6], x[7]));
-    else if constexpr (VEC == 4)
-        *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    else if constexpr (sizeof(T) == 2)
-        *p = __float2bfloat16_rn(x[0]);
-    else
-        *p = x[0];
+__device__ __forceinline__ uint32_t pack(Pair p) {
+    const float2 f = split(p);
+    return pack_bf16(f.x, f.y);
 }
-template <int VEC>
-__device__ __forceinline__ void load_param(const float* p, float* x) {
-    if constexpr (VEC == 1) {
-        x[0] = *p;
-    } else {
-#pragma unroll
-        for (int i = 0; i < VEC; i += 4) values(*reinterpret_cast<const float4*>(p + i), x + i);
-    }
+__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const Pair (&x)[4]) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack(x[0]), pack(x[1]), pack(x[2]), pack(x[3]));
 }
-template <int VEC>
-__device__ __forceinline__ void store_param(float* p, const float* x) {
-    if constexpr (VEC == 8) {
-        store_vec<4>(p, x);
-        store_vec<4>(p + 4, x + 4);
-    } else {
-        store_vec<VEC>(p, x);
-    }
+__device__ __forceinline__ void store_vec(float* p, const Pair (&x)[2]) {
+    const float2 a = split(x[0]), b = split(x[1]);
+    *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y);
 }
+__device__ __forceinline__ void store_vec(float* p, const Pair (&x)[4]) {
+    const float2 a = split(x[0]), b = split(x[1]), c = split(x[2]), d = split(x[3]);
+    *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(c.x, c.y, d.x, d.y);
+}
+__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&x)[1]) { *p = __float2bfloat16_rn(x[0]); }
+__device__ __forceinline__ void store_vec(float* p, const float (&x)[1]) { *p = x[0]; }
+__device__ __forceinline__ void load_param(const float* p, Pair (&x)[4]) {
+    values(*reinterpret_cast<const float4*>(p), x);
+    values(*reinterpret_cast<const float4*>(p + 4), x + 2);
+}
+__device__ __forceinline__ void load_param(const float* p, Pair (&x)[2]) { values(*reinterpret_cast<const float4*>(p), x); }
+__device__ __forceinline__ void load_param(const float* p, float (&x)[1]) { x[0] = *p; }
 
 // Sums of two values over the LPG lanes of a group. Groups wider than a warp go through shared memory.
 template <int LPG>
@@ -106,16 +157,65 @@ __device__ __forceinline__ void group_sum2(float& a, float& b, float2* red) {
     }
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-__device__ __forceinline__ float activate(float x, int act) {
-    return act == GDR_ACT_NONE ? x : act == GDR_ACT_SILU ? x * sigmoid(x) : sigmoid(x);
+// The sum of one value.
+template <int LPG>
+__device__ __forceinline__ float group_sum(float a, float2* red) {
+    float none = 0.f;
+    if constexpr (LPG > 32) {
+        group_sum2<LPG>(a, none, red);
+    } else {
+#pragma unroll
+        for (int o = LPG / 2; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    }
+    return a;
 }
-// act(x) and act'(x)
-__device__ __forceinline__ float2 activate2(float x, int act) {
-    if (act == GDR_ACT_NONE) return make_float2(x, 1.f);
-    const float s = sigmoid(x);
-    if (act == GDR_ACT_SIGMOID) return make_float2(s, s * (1.f - s));
-    return make_float2(x * s, s * (1.f + x * (1.f - s)));
+
+// 1 / (1 + 2^(-x log2 e)) by the hardware's approximate power of two and reciprocal, each good to a few units
+// in the last place; results below the smallest normal number are zero. (Through __expf and
+// __fdividef, which look after those, the backward was bound by its 462 instructions for each 8 values.)
+__device__ __forceinline__ float sigmoid(float x) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
+__device__ __forceinline__ Pair sigmoid(Pair x) {
+    const float2 f = split(x);
+    return pair(sigmoid(f.x), sigmoid(f.y));
+}
+// x <- act(x)
+template <typename V, int N>
+__device__ __forceinline__ void activate(V (&x)[N], int act) {
+    if (act == GDR_ACT_SILU) {
+#pragma unroll
+        for (int j = 0; j < N; j++) x[j] = mul(x[j], sigmoid(x[j]));
+    } else if (act == GDR_ACT_SIGMOID) {
+#pragma unroll
+        for (int j = 0; j < N; j++) x[j] = sigmoid(x[j]);
+    }
+}
+// x <- act(x), d = act'(x)
+template <typename V, int N>
+__device__ __forceinline__ void activate2(V (&x)[N], V (&d)[N], int act) {
+    const V one = all<V>(1.f), minus = all<V>(-1.f);
+    if (act == GDR_ACT_SILU) {
+#pragma unroll
+        for (int j = 0; j < N; j++) {
+            const V s = sigmoid(x[j]), f = mul(x[j], s);
+            d[j] = fma(f, fma(s, minus, one), s);  // s + x s (1 - s)
+            x[j] = f;
+        }
+    } else if (act == GDR_ACT_SIGMOID) {
+#pragma unroll
+        for (int j = 0; j < N; j++) {
+            const V s = sigmoid(x[j]);
+            d[j] = mul(s, fma(s, minus, one));
+            x[j] = s;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; j++) d[j] = one;
+    }
 }
 
 // Which token rows and group a lane works on. A block covers `per` groups (blockIdx.x) and `rl` token
@@ -143,6 +243,8 @@ __device__ __forceinline__ Place place(int groups, int per) {
 template <int LPG, int VEC, int NV, typename T>
 __global__ void __launch_bounds__(THREADS, NV == 1 ? 4 : 1) group_norm_fwd_kernel(GroupNormArgs a, int per) {
     using Raw = typename RawOf<VEC, T>::type;
+    using V = typename Lanes<VEC>::V;
+    constexpr int N = Lanes<VEC>::N;
     __shared__ float2 red[THREADS / 32];
     const Place at = place<LPG>(a.groups, per);
     const size_t C = (size_t)a.groups * a.D;
@@ -152,19 +254,19 @@ __global__ void __launch_bounds__(THREADS, NV == 1 ? 4 : 1) group_norm_fwd_kerne
     T* y = static_cast<T*>(a.y);
     int e[NV];
     bool in[NV];
-    float w[NV][VEC], b[NV][VEC];
+    V w[NV][N], b[NV][N];
 #pragma unroll
     for (int i = 0; i < NV; i++) {
         const int d = (i * LPG + at.lane) * VEC;
         in[i] = at.live && d < a.D;
         e[i] = at.group * a.D + d;
 #pragma unroll
-        for (int j = 0; j < VEC; j++) {
-            w[i][j] = 1.f;
-            b[i][j] = 0.f;
+        for (int j = 0; j < N; j++) {
+            w[i][j] = all<V>(1.f);
+            b[i][j] = all<V>(0.f);
         }
-        if (in[i] && a.weight) load_param<VEC>(a.weight + e[i], w[i]);
-        if (in[i] && a.bias) load_param<VEC>(a.bias + e[i], b[i]);
+        if (in[i] && a.weight) load_param(a.weight + e[i], w[i]);
+        if (in[i] && a.bias) load_param(a.bias + e[i], b[i]);
     }
     Raw nx[NV] = {}, nz[NV] = {};
     auto ask = [&](long long row) {
@@ -179,50 +281,52 @@ __global__ void __launch_bounds__(THREADS, NV == 1 ? 4 : 1) group_norm_fwd_kerne
     ask(at.row0);
     for (long long s = 0; s < steps; s++) {
         const long long row = at.row0 + s * at.row_step;
-        float v[NV][VEC], u[NV][VEC];
+        V v[NV][N], u[NV][N];
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             values(nx[i], v[i]);
             values(nz[i], u[i]);
         }
         ask(row + at.row_step);
-        float sum = 0.f, none = 0.f;
         if (a.center) {
+            V sum = all<V>(0.f);
 #pragma unroll
             for (int i = 0; i < NV; i++)
 #pragma unroll
-                for (int j = 0; j < VEC; j++) sum += v[i][j];
-            group_sum2<LPG>(sum, none, red);
+                for (int j = 0; j < N; j++) sum = add(sum, v[i][j]);
+            const V mean = all<V>(-inv * group_sum<LPG>(total(sum), red));
+#pragma unroll
+            for (int i = 0; i < NV; i++)
+                if (in[i])
+#pragma unroll
+                    for (int j = 0; j < N; j++) v[i][j] = add(v[i][j], mean);
         }
-        const float mean = sum * inv;
-        float sq = 0.f;
+        V sq = all<V>(0.f);
 #pragma unroll
         for (int i = 0; i < NV; i++)
-            if (in[i])
 #pragma unroll
-                for (int j = 0; j < VEC; j++) {
-                    v[i][j] -= mean;
-                    sq += v[i][j] * v[i][j];
-                }
-        group_sum2<LPG>(sq, none, red);
-        const float r = 1.f / sqrtf(sq * inv + a.eps);
+            for (int j = 0; j < N; j++) sq = fma(v[i][j], v[i][j], sq);
+        const V r = all<V>(rsqrtf(group_sum<LPG>(total(sq), red) * inv + a.eps));
         if (row < a.rows)
 #pragma unroll
             for (int i = 0; i < NV; i++)
                 if (in[i]) {
 #pragma unroll
-                    for (int j = 0; j < VEC; j++) {
-                        const float n = w[i][j] * (v[i][j] * r) + b[i][j];
-                        v[i][j] = z ? n * activate(u[i][j], a.act) : activate(n, a.act);
-                    }
-                    store_vec<VEC>(y + row * C + e[i], v[i]);
+                    for (int j = 0; j < N; j++) v[i][j] = fma(w[i][j], mul(v[i][j], r), b[i][j]);
+                    activate(z ? u[i] : v[i], a.act);
+                    if (z)
+#pragma unroll
+                        for (int j = 0; j < N; j++) v[i][j] = mul(v[i][j], u[i][j]);
+                    store_vec(y + row * C + e[i], v[i]);
                 }
     }
 }
 
 template <int LPG, int VEC, int NV, typename T>
-__global__ void __launch_bounds__(THREADS, NV == 1 ? 3 : 1) group_norm_bwd_kernel(GroupNormArgs a, int per, float* part) {
+__global__ void __launch_bounds__(THREADS, NV == 1 ? 2 : 1) group_norm_bwd_kernel(GroupNormArgs a, int per, float* part) {
     using Raw = typename RawOf<VEC, T>::type;
+    using V = typename Lanes<VEC>::V;
+    constexpr int N = Lanes<VEC>::N;
     __shared__ float2 red[THREADS / 32];
     const Place at = place<LPG>(a.groups, per);
     const size_t C = (size_t)a.groups * a.D;
@@ -234,19 +338,19 @@ __global__ void __launch_bounds__(THREADS, NV == 1 ? 3 : 1) group_norm_bwd_kerne
     T* dz = static_cast<T*>(a.dgate);
     int e[NV];
     bool in[NV];
-    float w[NV][VEC], b[NV][VEC], dw[NV][VEC], db[NV][VEC];
+    V w[NV][N], b[NV][N], dw[NV][N], db[NV][N];
 #pragma unroll
     for (int i = 0; i < NV; i++) {
         const int d = (i * LPG + at.lane) * VEC;
         in[i] = at.live && d < a.D;
         e[i] = at.group * a.D + d;
 #pragma unroll
-        for (int j = 0; j < VEC; j++) {
-            w[i][j] = 1.f;
-            b[i][j] = dw[i][j] = db[i][j] = 0.f;
+        for (int j = 0; j < N; j++) {
+            w[i][j] = all<V>(1.f);
+            b[i][j] = dw[i][j] = db[i][j] = all<V>(0.f);
         }
-        if (in[i] && a.weight) load_param<VEC>(a.weight + e[i], w[i]);
-        if (in[i] && a.bias) load_param<VEC>(a.bias + e[i], b[i]);
+        if (in[i] && a.weight) load_param(a.weight + e[i], w[i]);
+        if (in[i] && a.bias) load_param(a.bias + e[i], b[i]);
     }
     Raw nx[NV] = {}, nz[NV] = {}, ng[NV] = {};
     auto ask = [&](long long row) {
@@ -262,7 +366,7 @@ __global__ void __launch_bounds__(THREADS, NV == 1 ? 3 : 1) group_norm_bwd_kerne
     ask(at.row0);
     for (long long s = 0; s < steps; s++) {
         const long long row = at.row0 + s * at.row_step;
-        float h[NV][VEC], u[NV][VEC], g[NV][VEC];
+        V h[NV][N], u[NV][N], g[NV][N];
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             values(nx[i], h[i]);
@@ -270,53 +374,69 @@ __global__ void __launch_bounds__(THREADS, NV == 1 ? 3 : 1) group_norm_bwd_kerne
             values(ng[i], g[i]);
         }
         ask(row + at.row_step);
-        float sum = 0.f, none = 0.f;
         if (a.center) {
+            V sum = all<V>(0.f);
 #pragma unroll
             for (int i = 0; i < NV; i++)
 #pragma unroll
-                for (int j = 0; j < VEC; j++) sum += h[i][j];
-            group_sum2<LPG>(sum, none, red);
+                for (int j = 0; j < N; j++) sum = add(sum, h[i][j]);
+            const V mean = all<V>(-inv * group_sum<LPG>(total(sum), red));
+#pragma unroll
+            for (int i = 0; i < NV; i++)
+                if (in[i])
+#pragma unroll
+                    for (int j = 0; j < N; j++) h[i][j] = add(h[i][j], mean);
         }
-        const float mean = sum * inv;
-        float sq = 0.f;
+        V sq = all<V>(0.f);
 #pragma unroll
         for (int i = 0; i < NV; i++)
-            if (in[i])
 #pragma unroll
-                for (int j = 0; j < VEC; j++) {
-                    h[i][j] -= mean;
-                    sq += h[i][j] * h[i][j];
-                }
-        group_sum2<LPG>(sq, none, red);
-        const float r = 1.f / sqrtf(sq * inv + a.eps);
-        float s1 = 0.f, s2 = 0.f;
+            for (int j = 0; j < N; j++) sq = fma(h[i][j], h[i][j], sq);
+        const float r = rsqrtf(group_sum<LPG>(total(sq), red) * inv + a.eps);
+        V s1 = all<V>(0.f), s2 = all<V>(0.f);
 #pragma unroll
         for (int i = 0; i < NV; i++)
             if (in[i]) {
+                V n[N], d[N];
 #pragma unroll
-                for (int j = 0; j < VEC; j++) {
-                    h[i][j] *= r;
-                    const float n = w[i][j] * h[i][j] + b[i][j];
-                    const float2 f = activate2(z ? u[i][j] : n, a.act);
-                    u[i][j] = g[i][j] * n * f.y;  // dz
-                    const float dn = g[i][j] * (z ? f.x : f.y);
-                    dw[i][j] += dn * h[i][j];
-                    db[i][j] += dn;
-                    g[i][j] = dn * w[i][j];
-                    s1 += g[i][j];
-                    s2 += g[i][j] * h[i][j];
+                for (int j = 0; j < N; j++) {
+                    h[i][j] = mul(h[i][j], all<V>(r));
+                    n[j] = fma(w[i][j], h[i][j], b[i][j]);
                 }
-                if (z && row < a.rows) store_vec<VEC>(dz + row * C + e[i], u[i]);
+                if (z) {  // u: act(z), then dz = dy n act'(z); g: dn = dy act(z)
+                    activate2(u[i], d, a.act);
+#pragma unroll
+                    for (int j = 0; j < N; j++) {
+                        const V dy1 = g[i][j];
+                        g[i][j] = mul(dy1, u[i][j]);
+                        u[i][j] = mul(mul(dy1, n[j]), d[j]);
+                    }
+                } else {  // dn = dy act'(n)
+                    activate2(n, d, a.act);
+#pragma unroll
+                    for (int j = 0; j < N; j++) g[i][j] = mul(g[i][j], d[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < N; j++) {
+                    const V dn = g[i][j];
+                    dw[i][j] = fma(dn, h[i][j], dw[i][j]);
+                    db[i][j] = add(db[i][j], dn);
+                    g[i][j] = mul(dn, w[i][j]);
+                    s1 = add(s1, g[i][j]);
+                    s2 = fma(g[i][j], h[i][j], s2);
+                }
+                if (z && row < a.rows) store_vec(dz + row * C + e[i], u[i]);
             }
-        group_sum2<LPG>(s1, s2, red);
-        const float m1 = a.center ? s1 * inv : 0.f, m2 = s2 * inv;
+        float t1 = total(s1), t2 = total(s2);
+        group_sum2<LPG>(t1, t2, red);
+        // dx = r g - r m1 - h r m2
+        const V vr = all<V>(r), m1 = all<V>(a.center ? -t1 * inv * r : 0.f), m2 = all<V>(-t2 * inv * r);
 #pragma unroll
         for (int i = 0; i < NV; i++)
             if (in[i] && row < a.rows) {
 #pragma unroll
-                for (int j = 0; j < VEC; j++) g[i][j] = r * (g[i][j] - m1 - h[i][j] * m2);
-                store_vec<VEC>(dx + row * C + e[i], g[i]);
+                for (int j = 0; j < N; j++) g[i][j] = fma(g[i][j], vr, fma(h[i][j], m2, m1));
+                store_vec(dx + row * C + e[i], g[i]);
             }
     }
     if (!part) return;
@@ -325,8 +445,8 @@ __global__ void __launch_bounds__(THREADS, NV == 1 ? 3 : 1) group_norm_bwd_kerne
 #pragma unroll
     for (int i = 0; i < NV; i++)
         if (in[i]) {
-            store_param<VEC>(pw + e[i], dw[i]);
-            store_param<VEC>(pw + C + e[i], db[i]);
+            store_vec(pw + e[i], dw[i]);
+            store_vec(pw + C + e[i], db[i]);
         }
 }
 
@@ -369,7 +489,7 @@ Grid grid_of(const GroupNormArgs& a, int lpg, int blocks_per_sm) {
     return g;
 }
 
-constexpr int kFwdBlocks = 4, kBwdBlocks = 3;  // blocks of THREADS per SM that run at once
+constexpr int kFwdBlocks = 4, kBwdBlocks = 2;  // blocks of THREADS per SM that run at once
 
 // Lanes and vectors for a group of D values: 16-byte vectors where every row of every tensor starts
 // on 16 bytes (D a multiple of the vector and aligned pointers), else single values.
