@@ -179,9 +179,9 @@ static gdr_status linear_fwd_impl(const gdr_linear_problem* p, const void* q, co
     if (p->B == 0) return GDR_OK;
     if (p->T == 0) return pass_state(p, h0, ht, st);
     float* z = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256);
-    LinearMixArgs m{s, LINEAR_O, q, k, v, nullptr, p->scale, z, o, keep ? kept : nullptr};
+    LinearMixArgs m{s, LINEAR_O, q, k, v, nullptr, p->scale, z, o, h0, ht, keep ? kept : nullptr};
     if (s.bf16) return of(mix_tc(m, v, k, 1.f, 0, h0, z, ht, static_cast<int*>(ws), true, st));
-    if (states(s, v, k, 1.f, 0, h0, z, ht, st) != cudaSuccess) return GDR_ERR_CUDA;
+    if (s.nseg > 1 && states(s, v, k, 1.f, 0, h0, z, ht, st) != cudaSuccess) return GDR_ERR_CUDA;
     return of(launch_linear_mix(m, st));
 }
 
@@ -206,23 +206,25 @@ static gdr_status linear_bwd_impl(const gdr_linear_problem* p, const void* q, co
         uint8_t* adjoints = w + states_bytes(s);
         if (!keep) {  // the chunks' states, formed again
             uint8_t* again = adjoints + kept_bytes(s);
-            LinearMixArgs m{s, LINEAR_O, q, k, v, nullptr, p->scale, z, again + kept_bytes(s), again};
+            LinearMixArgs m{s, LINEAR_O, q, k, v, nullptr, p->scale, z, again + kept_bytes(s), nullptr, nullptr, again};
             if (mix_tc(m, v, k, 1.f, 0, h0, z, nullptr, status, true, st) != cudaSuccess) return GDR_ERR_CUDA;
             kept = again;
         }
-        LinearMixArgs m{s, LINEAR_DV, q, k, v, do_, p->scale, z, dv, adjoints};
+        LinearMixArgs m{s, LINEAR_DV, q, k, v, do_, p->scale, z, dv, nullptr, nullptr, adjoints};
         if (mix_tc(m, do_, q, p->scale, 1, dht, z, dh0, status, keep, st) != cudaSuccess) return GDR_ERR_CUDA;
         LinearGradArgs a{s, q, k, v, do_, p->scale, kept, adjoints, dq, dk, status};
         return of(launch_linear_tc_grad(a, st));
     }
     float* zd = reinterpret_cast<float*>(w + states_bytes(s));
-    if (states(s, v, k, 1.f, 0, h0, z, nullptr, st) != cudaSuccess) return GDR_ERR_CUDA;
-    if (states(s, do_, q, p->scale, 1, dht, zd, dh0, st) != cudaSuccess) return GDR_ERR_CUDA;
+    if (s.nseg > 1) {
+        if (states(s, v, k, 1.f, 0, h0, z, nullptr, st) != cudaSuccess) return GDR_ERR_CUDA;
+        if (states(s, do_, q, p->scale, 1, dht, zd, dh0, st) != cudaSuccess) return GDR_ERR_CUDA;
+    }
     // dv reads the reverse states, which dk, summing over value heads, may update in place: dv first
-    const struct { int pass; float* z; void* out; } passes[3] = {
-        {LINEAR_DQ, z, dq}, {LINEAR_DV, zd, dv}, {LINEAR_DK, zd, dk}};
+    const struct { int pass; float* z; void* out; const float* init; float* last; } passes[3] = {
+        {LINEAR_DQ, z, dq, h0, nullptr}, {LINEAR_DV, zd, dv, dht, dh0}, {LINEAR_DK, zd, dk, dht, nullptr}};
     for (const auto& x : passes) {
-        LinearMixArgs m{s, x.pass, q, k, v, do_, p->scale, x.z, x.out, nullptr};
+        LinearMixArgs m{s, x.pass, q, k, v, do_, p->scale, x.z, x.out, x.init, x.last, nullptr};
         if (launch_linear_mix(m, st) != cudaSuccess) return GDR_ERR_CUDA;
     }
     return GDR_OK;

@@ -1,18 +1,23 @@
-// linear.cu - linear attention with a constant decay per head on the CUDA cores, in fp32: the
-// segment summary, the combine step and the mix pass (linear.h).
+// linear.cu - linear attention with a constant decay per head on the CUDA cores, for fp32: the segment
+// summary and the mix pass (linear.h); and the combine step of both types.
 //
-// A chunk holds up to 64 tokens in processing order (u = 0 is the first token of the chunk, or
+// A chunk holds up to 32 tokens in processing order (u = 0 is the first token of the chunk, or
 // its last one in reverse), so both directions run the same sums over j <= r:
 //     P_rj = f l^(r-j) (a_r . b_j),   out_r = f' l^(r+1-s) a_r X + sum_{j<=r} P_rj c_j,
 //     X <- l^m X + f'' sum_j l^(m-1-j+s) b_j c_j^T          (m tokens in the chunk; s = reverse)
 // with f = scale, and (f', f'') = (scale, 1) forwards, (1, scale) in reverse: in reverse X is the
 // adjoint of the state after the chunk, which reaches token 0 (the last one) undecayed. Every
 // power of l has an exponent >= 0, so no decay overflows, and l^0 = 1 also where l = 0.
-#include <cuda_bf16.h>
+//
+// fp32 FMA bounds it (a chunk of 32 tokens and 64 of 128 columns: 721 thousand FMAs), then shared-memory
+// reads, so threads hold contiguous tiles that are read as 16-byte vectors, at least 3.2 FMAs a
+// wavefront, and the state stays in registers with a copy in shared memory for a X. Chunks of 32
+// need fewer FMAs than chunks of 64 (half of P is masked) and leave room for two CTAs per SM, one
+// loading while the other computes. (64-token chunks in strided scalar tiles, one CTA per SM:
+// T = 4096, 32 heads of 128: forward 1171 us.)
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "common.cuh"
 #include "kernels.h"
 #include "linear.h"
 #include "linear_dev.cuh"
@@ -21,7 +26,7 @@ namespace gdr {
 
 namespace {
 
-constexpr int LC = 64;  // tokens of a chunk
+constexpr int LC = 32;  // tokens of a chunk
 
 using linear::power;
 
@@ -30,49 +35,88 @@ __device__ __forceinline__ int valid_tokens(const LinearShape& s, int b) {
 }
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    return make_float4(bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y));
-}
 __device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+
+// N contiguous floats (N a multiple of 4, or 2).
+template <int N>
+__device__ __forceinline__ void load_n(const float* p, float* x) {
+    if constexpr (N == 2) {
+        const float2 v = *reinterpret_cast<const float2*>(p);
+        x[0] = v.x; x[1] = v.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const float4 v = load4(p + i);
+            x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
+        }
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_n(float* p, const float* x) {
+    if constexpr (N == 2) {
+        *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) store4(p + i, make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]));
+    }
 }
 
-// Columns [c0, c0 + D) of a chunk's tokens of one head, in processing order, as fp32 rows of
-// stride D + 4; rows m .. 63 are zero.
-template <int D, typename T>
-__device__ __forceinline__ void load_tile(float* dst, const T* src, size_t token0, size_t token_stride, int c0, int m,
+// The N columns of thread tx of 16 in a row: runs of four, 64 apart, so that neighbours read without conflicts.
+template <int N>
+__device__ __forceinline__ void load_cols(const float* row, int tx, float* x) {
+    if constexpr (N == 8) {
+        load_n<4>(row + 4 * tx, x);
+        load_n<4>(row + 64 + 4 * tx, x + 4);
+    } else {
+        load_n<N>(row + N * tx, x);
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_cols(float* row, int tx, const float* x) {
+    if constexpr (N == 8) {
+        store_n<4>(row + 4 * tx, x);
+        store_n<4>(row + 64 + 4 * tx, x + 4);
+    } else {
+        store_n<N>(row + N * tx, x);
+    }
+}
+
+// Columns [c0, c0 + D) of a chunk's tokens of one head, in processing order, as rows of stride D + 4;
+// rows m .. 31 are zero.
+template <int D>
+__device__ __forceinline__ void load_tile(float* dst, const float* src, size_t token0, size_t token_stride, int c0, int m,
                                           int reverse) {
     constexpr int V = D / 4;
-    for (int i = threadIdx.x; i < LC * V; i += blockDim.x) {
+#pragma unroll
+    for (int i = threadIdx.x; i < LC * V; i += 256) {
         const int u = i / V, c = 4 * (i % V);
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (u < m) x = load4(src + (token0 + (reverse ? m - 1 - u : u)) * token_stride + c0 + c);
-        *reinterpret_cast<float4*>(dst + u * (D + 4) + c) = x;
+        store4(dst + u * (D + 4) + c, x);
     }
 }
 
 __device__ __forceinline__ float at(const float4& x, int i) { return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w; }
 
-// grid (nseg * Dv / RS, Hv, B): rows [RS * i, ...) of the state's sum over one segment.
-template <int DK, int RS, typename T>
+// grid (nseg * Dv / RS, Hv, B): rows [RS * i, ...) of the state's sum over one segment; a thread holds
+// RS / 16 x DK / 16 of it.
+template <int DK, int RS>
 __global__ void __launch_bounds__(256) linear_summary_kernel(LinearSummaryArgs a) {
-    extern __shared__ float sm[];
-    float* X = sm;                      // [64][RS + 4]
-    float* Y = X + LC * (RS + 4);       // [64][DK + 4]
-    float* pw = Y + LC * (DK + 4);      // l^0 .. l^64
+    extern __shared__ __align__(16) float sm[];
+    float* X = sm;                 // [32][RS + 4]
+    float* Y = X + LC * (RS + 4);  // [32][DK + 4]
+    float* pw = Y + LC * (DK + 4); // l^0 .. l^32
     const LinearShape& s = a.s;
     const int nr = s.Dv / RS, seg = blockIdx.x / nr, r0 = (blockIdx.x % nr) * RS;
     const int hv = blockIdx.y, b = blockIdx.z, hk = hv / (s.Hv / s.Hk);
-    constexpr int TR = RS / 16, TC = DK / 16;  // rows and columns of a thread
+    constexpr int TR = RS / 16, TC = DK / 16;
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     if (threadIdx.x <= LC) pw[threadIdx.x] = power(s.g[hv], threadIdx.x);
     const int first = min(seg * s.seg_tokens, valid_tokens(s, b));
     const int last = min(first + s.seg_tokens, valid_tokens(s, b));
     const int nc = (last - first + LC - 1) / LC;
-    const T* rows = static_cast<const T*>(a.rows) + ((size_t)b * s.T * s.Hv + hv) * s.Dv;
-    const T* cols = static_cast<const T*>(a.cols) + ((size_t)b * s.T * s.Hk + hk) * s.Dk;
+    const float* rows = static_cast<const float*>(a.rows) + ((size_t)b * s.T * s.Hv + hv) * s.Dv;
+    const float* cols = static_cast<const float*>(a.cols) + ((size_t)b * s.T * s.Hk + hk) * s.Dk;
     float z[TR][TC] = {};
     for (int i = 0; i < nc; i++) {
         const int t0 = first + (a.reverse ? nc - 1 - i : i) * LC, m = min(LC, last - t0);
@@ -85,24 +129,23 @@ __global__ void __launch_bounds__(256) linear_summary_kernel(LinearSummaryArgs a
         for (int r = 0; r < TR; r++)
 #pragma unroll
             for (int c = 0; c < TC; c++) z[r][c] *= over;
+#pragma unroll 4
         for (int u = 0; u < m; u++) {
             const float w = a.factor * pw[m - 1 - u + a.reverse];
-            float y[TC];
-#pragma unroll
-            for (int c = 0; c < TC; c++) y[c] = Y[u * (DK + 4) + tx + 16 * c];
+            float x[TR], y[TC];
+            load_n<TR>(X + u * (RS + 4) + ty * TR, x);
+            load_cols<TC>(Y + u * (DK + 4), tx, y);
 #pragma unroll
             for (int r = 0; r < TR; r++) {
-                const float x = w * X[u * (RS + 4) + ty + 16 * r];
+                x[r] *= w;
 #pragma unroll
-                for (int c = 0; c < TC; c++) z[r][c] += x * y[c];
+                for (int c = 0; c < TC; c++) z[r][c] += x[r] * y[c];
             }
         }
     }
     float* out = a.z + ((((size_t)b * s.Hv + hv) * s.nseg + seg) * s.Dv + r0) * s.Dk;
 #pragma unroll
-    for (int r = 0; r < TR; r++)
-#pragma unroll
-        for (int c = 0; c < TC; c++) out[(size_t)(ty + 16 * r) * s.Dk + tx + 16 * c] = z[r][c];
+    for (int r = 0; r < TR; r++) store_cols<TC>(out + (size_t)(ty * TR + r) * s.Dk, tx, z[r]);
 }
 
 // grid (ceil(Dv Dk / 1024), Hv, B): four state elements a thread, the segments in processing order.
@@ -144,16 +187,17 @@ struct MixView {  // the roles of a pass (linear.h)
 };
 
 // grid (nseg * D2 / CS, output heads, B). D1: width of a and b; a CTA forms CS of the D2 output columns.
-// ROWS1: the state's rows (Dv) run along D1 (dq, dk), else along D2 (o, dv).
-template <int D1, int CS, bool ROWS1, typename T>
-__global__ void __launch_bounds__(256) linear_mix_kernel(LinearMixArgs args, MixView w) {
-    extern __shared__ float sm[];
-    float* A = sm;                         // [64][D1 + 4]
-    float* Bm = A + LC * (D1 + 4);         // [64][D1 + 4]
-    float* Cm = Bm + LC * (D1 + 4);        // [64][CS + 4]
-    float* X = Cm + LC * (CS + 4);         // [D1][CS + 4]
-    float* P = X + D1 * (CS + 4);          // [64][68]
-    float* pw = P + LC * (LC + 4);         // l^0 .. l^64
+// ROWS1: the state's rows (Dv) run along D1 (dq, dk), else along D2 (o, dv). A thread holds D1 / 16 x
+// CS / 16 of the state, 2 x CS / 16 of the output and 2 x 2 of P.
+template <int D1, int CS, bool ROWS1>
+__global__ void __launch_bounds__(256, 2) linear_mix_kernel(LinearMixArgs args, MixView w) {
+    extern __shared__ __align__(16) float sm[];
+    float* A = sm;                  // [32][D1 + 4]
+    float* Bm = A + LC * (D1 + 4);  // [32][D1 + 4]
+    float* Cm = Bm + LC * (D1 + 4); // [32][CS + 4]
+    float* X = Cm + LC * (CS + 4);  // [D1][CS + 4]
+    float* P = X + D1 * (CS + 4);   // [32][36]
+    float* pw = P + LC * (LC + 4);  // l^0 .. l^32
     const LinearShape& s = args.s;
     const int D2 = ROWS1 ? s.Dk : s.Dv;
     const int ns = D2 / CS, seg = blockIdx.x / ns, c0 = (blockIdx.x % ns) * CS;
@@ -164,139 +208,149 @@ __global__ void __launch_bounds__(256) linear_mix_kernel(LinearMixArgs args, Mix
     const int n = valid_tokens(s, b);
     const int begin = seg * s.seg_tokens, end = min(begin + s.seg_tokens, s.T);
     const int first = min(begin, n), last = min(end, n), nc = (last - first + LC - 1) / LC;
-    T* out = static_cast<T*>(args.out) + ((size_t)b * s.T * w.ho + ho) * D2 + c0;
+    float* out = static_cast<float*>(args.out) + ((size_t)b * s.T * w.ho + ho) * D2 + c0;
     const size_t out_stride = (size_t)w.ho * D2;
     for (int i = threadIdx.x; i < (end - max(begin, n)) * (CS / 4); i += 256)  // past the length: zero
         store4(out + (size_t)(max(begin, n) + i / (CS / 4)) * out_stride + 4 * (i % (CS / 4)),
                make_float4(0.f, 0.f, 0.f, 0.f));
     const size_t head_floats = (size_t)s.Dv * s.Dk;
     auto start_of = [&](int hv) { return args.starts + (((size_t)b * s.Hv + hv) * s.nseg + seg) * head_floats; };
-    auto move_state = [&](float* p, bool load) {
-        for (int i = threadIdx.x; i < D1 * CS; i += 256) {
-            // along the state's rows in memory, so that neighbouring threads touch neighbouring floats
-            const int d1 = ROWS1 ? i / CS : i % D1, d2 = ROWS1 ? i % CS : i / D1;
-            float* q = ROWS1 ? p + (size_t)d1 * s.Dk + c0 + d2 : p + (size_t)(c0 + d2) * s.Dk + d1;
-            if (load) X[d1 * (CS + 4) + d2] = *q;
-            else *q = X[d1 * (CS + 4) + d2];
-        }
+    float x[TK][TC];  // rows ty TK .., columns tx TC .. of X
+    // One segment: it starts from the state before the call, and ends with the one after it.
+    auto state_before = [&](int i, int hv) {
+        if (s.nseg > 1 || i > 0) return (const float*)start_of(hv);
+        return args.init ? args.init + ((size_t)b * s.Hv + hv) * head_floats : nullptr;
     };
-    if (heads == 1 && nc > 0) move_state(start_of(ho), true);
+    auto state_from = [&](const float* p) {
+#pragma unroll
+        for (int r = 0; r < TK; r++)
+#pragma unroll
+            for (int c = 0; c < TC; c++) {
+                const int d1 = ty * TK + r, d2 = c0 + tx * TC + c;
+                x[r][c] = !p ? 0.f : ROWS1 ? p[(size_t)d1 * s.Dk + d2] : p[(size_t)d2 * s.Dk + d1];
+            }
+    };
+    auto state_to = [&](float* p) {
+#pragma unroll
+        for (int r = 0; r < TK; r++)
+#pragma unroll
+            for (int c = 0; c < TC; c++) {
+                const int d1 = ty * TK + r, d2 = c0 + tx * TC + c;
+                (ROWS1 ? p[(size_t)d1 * s.Dk + d2] : p[(size_t)d2 * s.Dk + d1]) = x[r][c];
+            }
+    };
+    if (heads == 1) state_from(state_before(0, ho));
     for (int i = 0; i < nc; i++) {
         const int t0 = first + (w.reverse ? nc - 1 - i : i) * LC, m = min(LC, last - t0);
-        float acc[4][TC] = {};
+        float acc[2][TC] = {};
         for (int h = 0; h < heads; h++) {
             const int hv = ho * heads + h, hk = hv / G;
             const int ia = w.ha == s.Hv ? hv : hk, ic = w.hc == s.Hv ? hv : hk;
+            if (heads > 1) state_from(state_before(i, hv));
             __syncthreads();
-            if (heads > 1) move_state(start_of(hv), true);
+#pragma unroll
+            for (int r = 0; r < TK; r++) store_n<TC>(X + (ty * TK + r) * (CS + 4) + tx * TC, x[r]);
             if (threadIdx.x <= LC) pw[threadIdx.x] = power(s.g[hv], threadIdx.x);
-            load_tile<D1>(A, static_cast<const T*>(w.a) + ((size_t)b * s.T * w.ha + ia) * D1, t0, (size_t)w.ha * D1, 0, m,
-                          w.reverse);
-            load_tile<D1>(Bm, static_cast<const T*>(w.b) + ((size_t)b * s.T * w.ha + ia) * D1, t0, (size_t)w.ha * D1, 0,
+            load_tile<D1>(A, static_cast<const float*>(w.a) + ((size_t)b * s.T * w.ha + ia) * D1, t0, (size_t)w.ha * D1, 0,
                           m, w.reverse);
-            load_tile<CS>(Cm, static_cast<const T*>(w.c) + ((size_t)b * s.T * w.hc + ic) * D2, t0, (size_t)w.hc * D2, c0,
+            load_tile<D1>(Bm, static_cast<const float*>(w.b) + ((size_t)b * s.T * w.ha + ia) * D1, t0, (size_t)w.ha * D1, 0,
                           m, w.reverse);
+            load_tile<CS>(Cm, static_cast<const float*>(w.c) + ((size_t)b * s.T * w.hc + ic) * D2, t0, (size_t)w.hc * D2,
+                          c0, m, w.reverse);
             __syncthreads();
             {  // P: rows ty + 16 i, columns tx + 16 j
-                float p[4][4] = {};
+                float p[2][2] = {};
+#pragma unroll 4
                 for (int k = 0; k < D1; k += 4) {
-                    float4 x[4], y[4];
+                    float4 u[2], v[2];
 #pragma unroll
-                    for (int r = 0; r < 4; r++) {
-                        x[r] = load4(A + (ty + 16 * r) * (D1 + 4) + k);
-                        y[r] = load4(Bm + (tx + 16 * r) * (D1 + 4) + k);
+                    for (int r = 0; r < 2; r++) {
+                        u[r] = load4(A + (ty + 16 * r) * (D1 + 4) + k);
+                        v[r] = load4(Bm + (tx + 16 * r) * (D1 + 4) + k);
                     }
 #pragma unroll
-                    for (int r = 0; r < 4; r++)
+                    for (int r = 0; r < 2; r++)
 #pragma unroll
-                        for (int j = 0; j < 4; j++)
-                            p[r][j] += x[r].x * y[j].x + x[r].y * y[j].y + x[r].z * y[j].z + x[r].w * y[j].w;
+                        for (int j = 0; j < 2; j++)
+                            p[r][j] += u[r].x * v[j].x + u[r].y * v[j].y + u[r].z * v[j].z + u[r].w * v[j].w;
                 }
 #pragma unroll
-                for (int r = 0; r < 4; r++)
+                for (int r = 0; r < 2; r++)
 #pragma unroll
-                    for (int j = 0; j < 4; j++) {
+                    for (int j = 0; j < 2; j++) {
                         const int u = ty + 16 * r, v = tx + 16 * j;
                         P[u * (LC + 4) + v] = v <= u ? w.fp * pw[u - v] * p[r][j] : 0.f;
                     }
             }
-            {  // a X
-                float x[4][TC] = {};
+            {  // a X: rows ty + 16 i, columns tx TC ..
+                float y[2][TC] = {};
+#pragma unroll 2
                 for (int k = 0; k < D1; k += 4) {
-                    float4 av[4];
+                    float4 av[2];
 #pragma unroll
-                    for (int r = 0; r < 4; r++) av[r] = load4(A + (ty + 16 * r) * (D1 + 4) + k);
+                    for (int r = 0; r < 2; r++) av[r] = load4(A + (ty + 16 * r) * (D1 + 4) + k);
 #pragma unroll
-                    for (int e = 0; e < 4; e++)
+                    for (int e = 0; e < 4; e++) {
+                        float xv[TC];
+                        load_n<TC>(X + (k + e) * (CS + 4) + tx * TC, xv);
 #pragma unroll
-                        for (int c = 0; c < TC; c++) {
-                            const float xv = X[(k + e) * (CS + 4) + tx + 16 * c];
+                        for (int c = 0; c < TC; c++)
 #pragma unroll
-                            for (int r = 0; r < 4; r++) x[r][c] += at(av[r], e) * xv;
-                        }
+                            for (int r = 0; r < 2; r++) y[r][c] += at(av[r], e) * xv[c];
+                    }
                 }
 #pragma unroll
-                for (int r = 0; r < 4; r++) {
+                for (int r = 0; r < 2; r++) {
                     const float f = w.fx * pw[ty + 16 * r + 1 - w.reverse];
 #pragma unroll
-                    for (int c = 0; c < TC; c++) acc[r][c] += f * x[r][c];
+                    for (int c = 0; c < TC; c++) acc[r][c] += f * y[r][c];
                 }
             }
-            __syncthreads();  // P is written, X is read
-            for (int k = 0; k < m; k += 4) {  // P c
-                float4 pv[4];
+            __syncthreads();  // P is written
+#pragma unroll 2
+            for (int k = 0; k < LC; k += 4) {  // P c
+                float4 pv[2];
 #pragma unroll
-                for (int r = 0; r < 4; r++) pv[r] = load4(P + (ty + 16 * r) * (LC + 4) + k);
+                for (int r = 0; r < 2; r++) pv[r] = load4(P + (ty + 16 * r) * (LC + 4) + k);
 #pragma unroll
-                for (int e = 0; e < 4; e++)
+                for (int e = 0; e < 4; e++) {
+                    float cv[TC];
+                    load_n<TC>(Cm + (k + e) * (CS + 4) + tx * TC, cv);
 #pragma unroll
-                    for (int c = 0; c < TC; c++) {
-                        const float cv = Cm[(k + e) * (CS + 4) + tx + 16 * c];
+                    for (int c = 0; c < TC; c++)
 #pragma unroll
-                        for (int r = 0; r < 4; r++) acc[r][c] += at(pv[r], e) * cv;
-                    }
+                        for (int r = 0; r < 2; r++) acc[r][c] += at(pv[r], e) * cv[c];
+                }
             }
-            {  // the state over this chunk: rows ty + 16 r, columns tx + 16 c
-                float x[TK][TC];
+            {  // the state over this chunk
                 const float over = pw[m];
 #pragma unroll
                 for (int r = 0; r < TK; r++)
 #pragma unroll
-                    for (int c = 0; c < TC; c++) x[r][c] = over * X[(ty + 16 * r) * (CS + 4) + tx + 16 * c];
+                    for (int c = 0; c < TC; c++) x[r][c] *= over;
+#pragma unroll 2
                 for (int u = 0; u < m; u++) {
                     const float f = w.fu * pw[m - 1 - u + w.reverse];
-                    float cv[TC];
+                    float bv[TK], cv[TC];
+                    load_n<TK>(Bm + u * (D1 + 4) + ty * TK, bv);
+                    load_n<TC>(Cm + u * (CS + 4) + tx * TC, cv);
 #pragma unroll
-                    for (int c = 0; c < TC; c++) cv[c] = f * Cm[u * (CS + 4) + tx + 16 * c];
+                    for (int c = 0; c < TC; c++) {
+                        cv[c] *= f;
 #pragma unroll
-                    for (int r = 0; r < TK; r++) {
-                        const float bv = Bm[u * (D1 + 4) + ty + 16 * r];
-#pragma unroll
-                        for (int c = 0; c < TC; c++) x[r][c] += bv * cv[c];
+                        for (int r = 0; r < TK; r++) x[r][c] += bv[r] * cv[c];
                     }
                 }
-#pragma unroll
-                for (int r = 0; r < TK; r++)
-#pragma unroll
-                    for (int c = 0; c < TC; c++) X[(ty + 16 * r) * (CS + 4) + tx + 16 * c] = x[r][c];
             }
-            if (heads > 1) {
-                __syncthreads();
-                move_state(start_of(hv), false);
-            }
+            if (heads > 1) state_to(start_of(hv));
         }
 #pragma unroll
-        for (int r = 0; r < 4; r++) {
+        for (int r = 0; r < 2; r++) {
             const int u = ty + 16 * r;
-            if (u >= m) continue;
-            T* row = out + (size_t)(t0 + (w.reverse ? m - 1 - u : u)) * out_stride;
-#pragma unroll
-            for (int c = 0; c < TC; c++) {
-                if constexpr (sizeof(T) == 4) row[tx + 16 * c] = acc[r][c];
-                else row[tx + 16 * c] = __float2bfloat16_rn(acc[r][c]);
-            }
+            if (u < m) store_n<TC>(out + (size_t)(t0 + (w.reverse ? m - 1 - u : u)) * out_stride + tx * TC, acc[r]);
         }
     }
+    if (s.nseg == 1 && args.last) state_to(args.last + ((size_t)b * s.Hv + ho) * head_floats);  // heads == 1
 }
 
 template <typename K>
@@ -304,31 +358,19 @@ cudaError_t allow_smem(K kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <int DK, int RS, typename T>
+template <int DK, int RS>
 cudaError_t summary(const LinearSummaryArgs& a, cudaStream_t st) {
     const int bytes = 4 * (LC * (RS + 4) + LC * (DK + 4) + LC + 1);
-    auto kernel = linear_summary_kernel<DK, RS, T>;
-    if (cudaError_t e = allow_smem(kernel, bytes)) return e;
     trace_begin("linear_summary", st);
-    kernel<<<dim3(a.s.nseg * (a.s.Dv / RS), a.s.Hv, a.s.B), 256, bytes, st>>>(a);
+    linear_summary_kernel<DK, RS><<<dim3(a.s.nseg * (a.s.Dv / RS), a.s.Hv, a.s.B), 256, bytes, st>>>(a);
     trace_end(st);
     return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t summary_of(const LinearSummaryArgs& a, cudaStream_t st) {
-    const bool narrow = a.s.Dv == 32;
-    switch (a.s.Dk) {
-        case 32: return narrow ? summary<32, 32, T>(a, st) : summary<32, 64, T>(a, st);
-        case 64: return narrow ? summary<64, 32, T>(a, st) : summary<64, 64, T>(a, st);
-        default: return narrow ? summary<128, 32, T>(a, st) : summary<128, 64, T>(a, st);
-    }
-}
-
-template <int D1, int CS, bool ROWS1, typename T>
+template <int D1, int CS, bool ROWS1>
 cudaError_t mix(const LinearMixArgs& a, const MixView& w, int D2, cudaStream_t st) {
     const int bytes = 4 * (2 * LC * (D1 + 4) + LC * (CS + 4) + D1 * (CS + 4) + LC * (LC + 4) + LC + 1);
-    auto kernel = linear_mix_kernel<D1, CS, ROWS1, T>;
+    auto kernel = linear_mix_kernel<D1, CS, ROWS1>;
     if (cudaError_t e = allow_smem(kernel, bytes)) return e;
     trace_begin("linear_mix", st);
     kernel<<<dim3(a.s.nseg * (D2 / CS), w.ho, a.s.B), 256, bytes, st>>>(a, w);
@@ -336,45 +378,33 @@ cudaError_t mix(const LinearMixArgs& a, const MixView& w, int D2, cudaStream_t s
     return cudaGetLastError();
 }
 
-template <int CS, bool ROWS1, typename T>
+template <int CS, bool ROWS1>
 cudaError_t mix_d1(const LinearMixArgs& a, const MixView& w, int D1, int D2, cudaStream_t st) {
     switch (D1) {
-        case 32: return mix<32, CS, ROWS1, T>(a, w, D2, st);
-        case 64: return mix<64, CS, ROWS1, T>(a, w, D2, st);
-        default: return mix<128, CS, ROWS1, T>(a, w, D2, st);
+        case 32: return mix<32, CS, ROWS1>(a, w, D2, st);
+        case 64: return mix<64, CS, ROWS1>(a, w, D2, st);
+        default: return mix<128, CS, ROWS1>(a, w, D2, st);
     }
-}
-
-template <typename T>
-cudaError_t mix_of(const LinearMixArgs& a, cudaStream_t st) {
-    const LinearShape& s = a.s;
-    const int Hk = s.Hk, Hv = s.Hv;
-    MixView w;
-    switch (a.pass) {
-        case LINEAR_O: w = {a.q, a.k, a.v, Hk, Hv, Hv, 0, a.scale, a.scale, 1.f}; break;
-        case LINEAR_DQ: w = {a.do_, a.v, a.k, Hv, Hk, Hk, 0, a.scale, a.scale, 1.f}; break;
-        case LINEAR_DK: w = {a.v, a.do_, a.q, Hv, Hk, Hk, 1, a.scale, 1.f, a.scale}; break;
-        default: w = {a.k, a.q, a.do_, Hk, Hv, Hv, 1, a.scale, 1.f, a.scale}; break;
-    }
-    const bool rows1 = a.pass == LINEAR_DQ || a.pass == LINEAR_DK;
-    const int D1 = rows1 ? s.Dv : s.Dk, D2 = rows1 ? s.Dk : s.Dv;
-    if (rows1)
-        return D2 == 32 ? mix_d1<32, true, T>(a, w, D1, D2, st) : mix_d1<64, true, T>(a, w, D1, D2, st);
-    return D2 == 32 ? mix_d1<32, false, T>(a, w, D1, D2, st) : mix_d1<64, false, T>(a, w, D1, D2, st);
 }
 
 }  // namespace
 
-// Segments: enough CTAs for two per SM, each of whole chunks.
+// Segments of whole 128-token blocks: as many as give two CTAs per SM, and none where the heads alone do,
+// since a second pass over the tokens for the segments' sums takes about 0.4 of the mix pass's time.
 int linear_segments(int B, int T, int Hv, int Dv) {
-    const long long chunks = (T + LC - 1) / LC, units = (long long)B * Hv * (Dv < 64 ? 1 : Dv / 64);
-    if (chunks <= 1 || units <= 0) return 1;
-    const long long want = (2 * 152 + units - 1) / units;
-    return (int)(want < chunks ? want : chunks);
+    const long long blocks = (T + 127) / 128, units = (long long)B * Hv * (Dv < 64 ? 1 : Dv / 64);
+    if (blocks <= 1 || units <= 0) return 1;
+    const long long want = units >= 304 ? 1 : 304 / units;
+    return (int)(want < blocks ? want : blocks);
 }
 
 cudaError_t launch_linear_summary(const LinearSummaryArgs& a, cudaStream_t st) {
-    return a.s.bf16 ? summary_of<__nv_bfloat16>(a, st) : summary_of<float>(a, st);
+    const bool narrow = a.s.Dv == 32;
+    switch (a.s.Dk) {
+        case 32: return narrow ? summary<32, 32>(a, st) : summary<32, 64>(a, st);
+        case 64: return narrow ? summary<64, 32>(a, st) : summary<64, 64>(a, st);
+        default: return narrow ? summary<128, 32>(a, st) : summary<128, 64>(a, st);
+    }
 }
 
 cudaError_t launch_linear_combine(const LinearCombineArgs& a, bool overlap, cudaStream_t st) {
@@ -386,7 +416,19 @@ cudaError_t launch_linear_combine(const LinearCombineArgs& a, bool overlap, cuda
 }
 
 cudaError_t launch_linear_mix(const LinearMixArgs& a, cudaStream_t st) {
-    return a.s.bf16 ? mix_of<__nv_bfloat16>(a, st) : mix_of<float>(a, st);
+    const LinearShape& s = a.s;
+    const int Hk = s.Hk, Hv = s.Hv;
+    MixView w;
+    switch (a.pass) {
+        case LINEAR_O: w = {a.q, a.k, a.v, Hk, Hv, Hv, 0, a.scale, a.scale, 1.f}; break;
+        case LINEAR_DQ: w = {a.do_, a.v, a.k, Hv, Hk, Hk, 0, a.scale, a.scale, 1.f}; break;
+        case LINEAR_DK: w = {a.v, a.do_, a.q, Hv, Hk, Hk, 1, a.scale, 1.f, a.scale}; break;
+        default: w = {a.k, a.q, a.do_, Hk, Hv, Hv, 1, a.scale, 1.f, a.scale}; break;
+    }
+    const bool rows1 = a.pass == LINEAR_DQ || a.pass == LINEAR_DK;
+    const int D1 = rows1 ? s.Dv : s.Dk, D2 = rows1 ? s.Dk : s.Dv;
+    if (rows1) return D2 == 32 ? mix_d1<32, true>(a, w, D1, D2, st) : mix_d1<64, true>(a, w, D1, D2, st);
+    return D2 == 32 ? mix_d1<32, false>(a, w, D1, D2, st) : mix_d1<64, false>(a, w, D1, D2, st);
 }
 
 }  // namespace gdr

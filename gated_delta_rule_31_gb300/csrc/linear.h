@@ -54,6 +54,8 @@ struct LinearMixArgs {
     float scale;
     float* starts;  // state entering each segment (scratch: passes that sum value heads update it)
     void* out;
+    const float* init;  // fp32, one segment: the state before all tokens, or null (zero); and
+    float* last;        // o and dv: the state after them, or null
     void* images;   // bf16 o and dv: the state that each 128-token chunk starts from (dv: the adjoint of
                     // the one it ends in) is kept there as a swizzled bf16 tile, 32 KB for each
                     // (b, hv, chunk), for launch_linear_tc_grad; or null
