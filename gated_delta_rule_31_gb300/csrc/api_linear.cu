@@ -46,10 +46,10 @@ LinearShape shape_of(const gdr_linear_problem* p, const float* g, const int* len
     s.B = p->B; s.T = p->T; s.Hk = p->Hk; s.Hv = p->Hv; s.Dk = p->Dk; s.Dv = p->Dv;
     s.bf16 = p->dtype == GDR_BF16;
     s.nseg = s.bf16 ? linear_tc_segments(p->B, p->T, p->Hv) : linear_segments(p->B, p->T, p->Hv, p->Dv);
-    const int chunks = (p->T + 127) / 128;
-    s.seg_tokens = (chunks + s.nseg - 1) / s.nseg * 128;
-    s.nseg = chunks > 0 ? (p->T + s.seg_tokens - 1) / s.seg_tokens : 1;
-    if (s.seg_tokens == 0) s.seg_tokens = 128;
+    const int block = s.bf16 ? kLinearBlockTc : kLinearBlock;  // segments are whole blocks of tokens
+    const int blocks = p->T / block + (p->T % block != 0);
+    s.seg_tokens = blocks > 0 ? (blocks + s.nseg - 1) / s.nseg * block : block;
+    s.nseg = blocks > 0 ? p->T / s.seg_tokens + (p->T % s.seg_tokens != 0) : 1;
     s.g = g;
     s.lengths = lengths;
     return s;

@@ -389,10 +389,10 @@ cudaError_t mix_d1(const LinearMixArgs& a, const MixView& w, int D1, int D2, cud
 
 }  // namespace
 
-// Segments of whole 128-token blocks: as many as give two CTAs per SM, and none where the heads alone do,
+// Segments of whole blocks: as many as give two CTAs per SM, and none where the heads alone do,
 // since a second pass over the tokens for the segments' sums takes about 0.4 of the mix pass's time.
 int linear_segments(int B, int T, int Hv, int Dv) {
-    const long long blocks = (T + 127) / 128, units = (long long)B * Hv * (Dv < 64 ? 1 : Dv / 64);
+    const long long blocks = (T + kLinearBlock - 1) / kLinearBlock, units = (long long)B * Hv * (Dv < 64 ? 1 : Dv / 64);
     if (blocks <= 1 || units <= 0) return 1;
     const long long want = units >= 304 ? 1 : 304 / units;
     return (int)(want < blocks ? want : blocks);

@@ -79,6 +79,7 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int smem,
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+constexpr int kLinearBlock = 64, kLinearBlockTc = 128;  // tokens that segments are made of: fp32, bf16
 int linear_segments(int B, int T, int Hv, int Dv);
 cudaError_t launch_linear_summary(const LinearSummaryArgs& a, cudaStream_t st);
 cudaError_t launch_linear_combine(const LinearCombineArgs& a, bool overlap, cudaStream_t st);
