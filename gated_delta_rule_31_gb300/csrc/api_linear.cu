@@ -86,7 +86,7 @@ cudaError_t states(const LinearShape& s, const void* rows, const void* cols, flo
     LinearSummaryArgs a{s, rows, cols, factor, reverse, z};
     if (cudaError_t e = launch_linear_summary(a, st)) return e;
     LinearCombineArgs c{s, init, reverse, z, last};
-    return launch_linear_combine(c, false, st);
+    return launch_linear_combine(c, true, st);
 }
 
 // A mix pass on the tensor cores from the state `init` before it: with several segments, the states that
@@ -179,7 +179,8 @@ static gdr_status linear_fwd_impl(const gdr_linear_problem* p, const void* q, co
     if (p->B == 0) return GDR_OK;
     if (p->T == 0) return pass_state(p, h0, ht, st);
     float* z = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256);
-    LinearMixArgs m{s, LINEAR_O, q, k, v, nullptr, p->scale, z, o, h0, ht, keep ? kept : nullptr};
+    LinearMixArgs m{s, LINEAR_O, q, k, v, nullptr, p->scale, z, o, h0, ht, keep ? kept : nullptr,
+                    s.nseg > 1};
     if (s.bf16) return of(mix_tc(m, v, k, 1.f, 0, h0, z, ht, static_cast<int*>(ws), true, st));
     if (s.nseg > 1 && states(s, v, k, 1.f, 0, h0, z, ht, st) != cudaSuccess) return GDR_ERR_CUDA;
     return of(launch_linear_mix(m, st));
@@ -206,11 +207,11 @@ static gdr_status linear_bwd_impl(const gdr_linear_problem* p, const void* q, co
         uint8_t* adjoints = w + states_bytes(s);
         if (!keep) {  // the chunks' states, formed again
             uint8_t* again = adjoints + kept_bytes(s);
-            LinearMixArgs m{s, LINEAR_O, q, k, v, nullptr, p->scale, z, again + kept_bytes(s), nullptr, nullptr, again};
+            LinearMixArgs m{s, LINEAR_O, q, k, v, nullptr, p->scale, z, again + kept_bytes(s), nullptr, nullptr, again, false};
             if (mix_tc(m, v, k, 1.f, 0, h0, z, nullptr, status, true, st) != cudaSuccess) return GDR_ERR_CUDA;
             kept = again;
         }
-        LinearMixArgs m{s, LINEAR_DV, q, k, v, do_, p->scale, z, dv, nullptr, nullptr, adjoints};
+        LinearMixArgs m{s, LINEAR_DV, q, k, v, do_, p->scale, z, dv, nullptr, nullptr, adjoints, false};
         if (mix_tc(m, do_, q, p->scale, 1, dht, z, dh0, status, keep, st) != cudaSuccess) return GDR_ERR_CUDA;
         LinearGradArgs a{s, q, k, v, do_, p->scale, kept, adjoints, dq, dk, status};
         return of(launch_linear_tc_grad(a, st));
@@ -224,7 +225,7 @@ static gdr_status linear_bwd_impl(const gdr_linear_problem* p, const void* q, co
     const struct { int pass; float* z; void* out; const float* init; float* last; } passes[3] = {
         {LINEAR_DQ, z, dq, h0, nullptr}, {LINEAR_DV, zd, dv, dht, dh0}, {LINEAR_DK, zd, dk, dht, nullptr}};
     for (const auto& x : passes) {
-        LinearMixArgs m{s, x.pass, q, k, v, do_, p->scale, x.z, x.out, x.init, x.last, nullptr};
+        LinearMixArgs m{s, x.pass, q, k, v, do_, p->scale, x.z, x.out, x.init, x.last, nullptr, false};
         if (launch_linear_mix(m, st) != cudaSuccess) return GDR_ERR_CUDA;
     }
     return GDR_OK;

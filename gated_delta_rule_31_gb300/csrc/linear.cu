@@ -81,18 +81,16 @@ __device__ __forceinline__ void store_cols(float* row, int tx, const float* x) {
     }
 }
 
-// Columns [c0, c0 + D) of a chunk's tokens of one head, in processing order, as rows of stride D + 4;
-// rows m .. 31 are zero.
+// Starts the copies of columns [c0, c0 + D) of a chunk's tokens of one head, in processing order, to rows
+// of stride D + 4; rows m .. 31 become zero.
 template <int D>
-__device__ __forceinline__ void load_tile(float* dst, const float* src, size_t token0, size_t token_stride, int c0, int m,
-                                          int reverse) {
+__device__ __forceinline__ void fetch_tile(float* dst, const float* src, size_t token0, size_t token_stride, int c0, int m,
+                                           int reverse) {
     constexpr int V = D / 4;
 #pragma unroll
     for (int i = threadIdx.x; i < LC * V; i += 256) {
-        const int u = i / V, c = 4 * (i % V);
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (u < m) x = load4(src + (token0 + (reverse ? m - 1 - u : u)) * token_stride + c0 + c);
-        store4(dst + u * (D + 4) + c, x);
+        const int u = i / V, c = 4 * (i % V), row = u < m ? (reverse ? m - 1 - u : u) : 0;
+        cp_async16(dst + u * (D + 4) + c, src + (token0 + row) * token_stride + c0 + c, u < m);
     }
 }
 
@@ -103,9 +101,8 @@ __device__ __forceinline__ float at(const float4& x, int i) { return i == 0 ? x.
 template <int DK, int RS>
 __global__ void __launch_bounds__(256) linear_summary_kernel(LinearSummaryArgs a) {
     extern __shared__ __align__(16) float sm[];
-    float* X = sm;                 // [32][RS + 4]
-    float* Y = X + LC * (RS + 4);  // [32][DK + 4]
-    float* pw = Y + LC * (DK + 4); // l^0 .. l^32
+    constexpr int XS = LC * (RS + 4), YS = LC * (DK + 4);
+    float* pw = sm + 2 * (XS + YS);  // l^0 .. l^32, after two buffers of X [32][RS + 4] and Y [32][DK + 4]
     const LinearShape& s = a.s;
     const int nr = s.Dv / RS, seg = blockIdx.x / nr, r0 = (blockIdx.x % nr) * RS;
     const int hv = blockIdx.y, b = blockIdx.z, hk = hv / (s.Hv / s.Hk);
@@ -117,13 +114,22 @@ __global__ void __launch_bounds__(256) linear_summary_kernel(LinearSummaryArgs a
     const int nc = (last - first + LC - 1) / LC;
     const float* rows = static_cast<const float*>(a.rows) + ((size_t)b * s.T * s.Hv + hv) * s.Dv;
     const float* cols = static_cast<const float*>(a.cols) + ((size_t)b * s.T * s.Hk + hk) * s.Dk;
+    auto fetch = [&](int i) {
+        if (i >= nc) return;
+        const int t0 = first + (a.reverse ? nc - 1 - i : i) * LC, m = min(LC, last - t0);
+        float* X = sm + (i & 1) * (XS + YS);
+        fetch_tile<RS>(X, rows, t0, (size_t)s.Hv * s.Dv, r0, m, a.reverse);
+        fetch_tile<DK>(X + XS, cols, t0, (size_t)s.Hk * s.Dk, 0, m, a.reverse);
+    };
+    linear::next_kernel_may_start();
     float z[TR][TC] = {};
+    fetch(0);
     for (int i = 0; i < nc; i++) {
         const int t0 = first + (a.reverse ? nc - 1 - i : i) * LC, m = min(LC, last - t0);
-        __syncthreads();
-        load_tile<RS>(X, rows, t0, (size_t)s.Hv * s.Dv, r0, m, a.reverse);
-        load_tile<DK>(Y, cols, t0, (size_t)s.Hk * s.Dk, 0, m, a.reverse);
-        __syncthreads();
+        cp_async_wait_all();
+        __syncthreads();  // chunk i is there, and chunk i - 1's buffer is free
+        fetch(i + 1);
+        const float *X = sm + (i & 1) * (XS + YS), *Y = X + XS;
         const float over = pw[m];
 #pragma unroll
         for (int r = 0; r < TR; r++)
@@ -192,12 +198,13 @@ struct MixView {  // the roles of a pass (linear.h)
 template <int D1, int CS, bool ROWS1>
 __global__ void __launch_bounds__(256, 2) linear_mix_kernel(LinearMixArgs args, MixView w) {
     extern __shared__ __align__(16) float sm[];
-    float* A = sm;                  // [32][D1 + 4]
-    float* Bm = A + LC * (D1 + 4);  // [32][D1 + 4]
-    float* Cm = Bm + LC * (D1 + 4); // [32][CS + 4]
-    float* X = Cm + LC * (CS + 4);  // [D1][CS + 4]
+    constexpr int BS = LC * (D1 + 4), CZ = LC * (CS + 4);
+    float* A = sm;              // [32][D1 + 4]
+    float* Bs = A + BS;         // two of [32][D1 + 4]
+    float* Cs = Bs + 2 * BS;    // two of [32][CS + 4]
+    float* X = Cs + 2 * CZ;     // [D1][CS + 4]
     float* P = X + D1 * (CS + 4);   // [32][36]
-    float* pw = P + LC * (LC + 4);  // l^0 .. l^32
+    float* pws = P + LC * (LC + 4); // two of l^0 .. l^32
     const LinearShape& s = args.s;
     const int D2 = ROWS1 ? s.Dk : s.Dv;
     const int ns = D2 / CS, seg = blockIdx.x / ns, c0 = (blockIdx.x % ns) * CS;
@@ -210,9 +217,6 @@ __global__ void __launch_bounds__(256, 2) linear_mix_kernel(LinearMixArgs args, 
     const int first = min(begin, n), last = min(end, n), nc = (last - first + LC - 1) / LC;
     float* out = static_cast<float*>(args.out) + ((size_t)b * s.T * w.ho + ho) * D2 + c0;
     const size_t out_stride = (size_t)w.ho * D2;
-    for (int i = threadIdx.x; i < (end - max(begin, n)) * (CS / 4); i += 256)  // past the length: zero
-        store4(out + (size_t)(max(begin, n) + i / (CS / 4)) * out_stride + 4 * (i % (CS / 4)),
-               make_float4(0.f, 0.f, 0.f, 0.f));
     const size_t head_floats = (size_t)s.Dv * s.Dk;
     auto start_of = [&](int hv) { return args.starts + (((size_t)b * s.Hv + hv) * s.nseg + seg) * head_floats; };
     float x[TK][TC];  // rows ty TK .., columns tx TC .. of X
@@ -222,42 +226,74 @@ __global__ void __launch_bounds__(256, 2) linear_mix_kernel(LinearMixArgs args, 
         return args.init ? args.init + ((size_t)b * s.Hv + hv) * head_floats : nullptr;
     };
     auto state_from = [&](const float* p) {
+        if (ROWS1) {
 #pragma unroll
-        for (int r = 0; r < TK; r++)
+            for (int r = 0; r < TK; r++) {
+                if (p) load_n<TC>(p + (size_t)(ty * TK + r) * s.Dk + c0 + tx * TC, x[r]);
+#pragma unroll
+                for (int c = 0; c < TC; c++) x[r][c] = p ? x[r][c] : 0.f;
+            }
+        } else {
 #pragma unroll
             for (int c = 0; c < TC; c++) {
-                const int d1 = ty * TK + r, d2 = c0 + tx * TC + c;
-                x[r][c] = !p ? 0.f : ROWS1 ? p[(size_t)d1 * s.Dk + d2] : p[(size_t)d2 * s.Dk + d1];
+                float col[TK];
+                if (p) load_n<TK>(p + (size_t)(c0 + tx * TC + c) * s.Dk + ty * TK, col);
+#pragma unroll
+                for (int r = 0; r < TK; r++) x[r][c] = p ? col[r] : 0.f;
             }
+        }
     };
     auto state_to = [&](float* p) {
+        if (ROWS1) {
 #pragma unroll
-        for (int r = 0; r < TK; r++)
+            for (int r = 0; r < TK; r++) store_n<TC>(p + (size_t)(ty * TK + r) * s.Dk + c0 + tx * TC, x[r]);
+        } else {
 #pragma unroll
             for (int c = 0; c < TC; c++) {
-                const int d1 = ty * TK + r, d2 = c0 + tx * TC + c;
-                (ROWS1 ? p[(size_t)d1 * s.Dk + d2] : p[(size_t)d2 * s.Dk + d1]) = x[r][c];
+                float col[TK];
+#pragma unroll
+                for (int r = 0; r < TK; r++) col[r] = x[r][c];
+                store_n<TK>(p + (size_t)(c0 + tx * TC + c) * s.Dk + ty * TK, col);
             }
+        }
     };
-    if (heads == 1) state_from(state_before(0, ho));
+    auto share_state = [&] {
+#pragma unroll
+        for (int r = 0; r < TK; r++) store_n<TC>(X + (ty * TK + r) * (CS + 4) + tx * TC, x[r]);
+    };
+    // Step n: value head n % heads of chunk n / heads.
+    const int steps = nc * heads;
+    auto fetch = [&](int n, bool fetch_a) {
+        if (n >= steps) return;
+        const int i = n / heads, hv = ho * heads + n % heads, hk = hv / G;
+        const int ia = w.ha == s.Hv ? hv : hk, ic = w.hc == s.Hv ? hv : hk;
+        const int t0 = first + (w.reverse ? nc - 1 - i : i) * LC, m = min(LC, last - t0);
+        const size_t at1 = ((size_t)b * s.T * w.ha + ia) * D1, at2 = ((size_t)b * s.T * w.hc + ic) * D2;
+        if (fetch_a) {
+            fetch_tile<D1>(A, static_cast<const float*>(w.a) + at1, t0, (size_t)w.ha * D1, 0, m, w.reverse);
+        } else {
+            fetch_tile<D1>(Bs + (n & 1) * BS, static_cast<const float*>(w.b) + at1, t0, (size_t)w.ha * D1, 0, m, w.reverse);
+            fetch_tile<CS>(Cs + (n & 1) * CZ, static_cast<const float*>(w.c) + at2, t0, (size_t)w.hc * D2, c0, m, w.reverse);
+            if (threadIdx.x <= LC) pws[(n & 1) * (LC + 1) + threadIdx.x] = power(s.g[hv], threadIdx.x);
+        }
+    };
+    fetch(0, false);
+    fetch(0, true);
+    linear::wait_kernel_before();  // the states, and what the outputs' memory held
+    for (int i = threadIdx.x; i < (end - max(begin, n)) * (CS / 4); i += 256)  // past the length: zero
+        store4(out + (size_t)(max(begin, n) + i / (CS / 4)) * out_stride + 4 * (i % (CS / 4)),
+               make_float4(0.f, 0.f, 0.f, 0.f));
+    if (nc > 0 || heads == 1) state_from(state_before(0, ho * heads));
+    share_state();
+    float acc[2][TC] = {};
     for (int i = 0; i < nc; i++) {
         const int t0 = first + (w.reverse ? nc - 1 - i : i) * LC, m = min(LC, last - t0);
-        float acc[2][TC] = {};
         for (int h = 0; h < heads; h++) {
-            const int hv = ho * heads + h, hk = hv / G;
-            const int ia = w.ha == s.Hv ? hv : hk, ic = w.hc == s.Hv ? hv : hk;
-            if (heads > 1) state_from(state_before(i, hv));
-            __syncthreads();
-#pragma unroll
-            for (int r = 0; r < TK; r++) store_n<TC>(X + (ty * TK + r) * (CS + 4) + tx * TC, x[r]);
-            if (threadIdx.x <= LC) pw[threadIdx.x] = power(s.g[hv], threadIdx.x);
-            load_tile<D1>(A, static_cast<const float*>(w.a) + ((size_t)b * s.T * w.ha + ia) * D1, t0, (size_t)w.ha * D1, 0,
-                          m, w.reverse);
-            load_tile<D1>(Bm, static_cast<const float*>(w.b) + ((size_t)b * s.T * w.ha + ia) * D1, t0, (size_t)w.ha * D1, 0,
-                          m, w.reverse);
-            load_tile<CS>(Cm, static_cast<const float*>(w.c) + ((size_t)b * s.T * w.hc + ic) * D2, t0, (size_t)w.hc * D2,
-                          c0, m, w.reverse);
-            __syncthreads();
+            const int step = i * heads + h;
+            const float *Bm = Bs + (step & 1) * BS, *Cm = Cs + (step & 1) * CZ, *pw = pws + (step & 1) * (LC + 1);
+            cp_async_wait_all();
+            __syncthreads();  // the step's tiles and X are there, and the buffers of the step before are free
+            fetch(step + 1, false);
             {  // P: rows ty + 16 i, columns tx + 16 j
                 float p[2][2] = {};
 #pragma unroll 4
@@ -306,7 +342,8 @@ __global__ void __launch_bounds__(256, 2) linear_mix_kernel(LinearMixArgs args, 
                     for (int c = 0; c < TC; c++) acc[r][c] += f * y[r][c];
                 }
             }
-            __syncthreads();  // P is written
+            __syncthreads();  // P is written; A and X are free
+            fetch(step + 1, true);
 #pragma unroll 2
             for (int k = 0; k < LC; k += 4) {  // P c
                 float4 pv[2];
@@ -342,12 +379,18 @@ __global__ void __launch_bounds__(256, 2) linear_mix_kernel(LinearMixArgs args, 
                     }
                 }
             }
-            if (heads > 1) state_to(start_of(hv));
+            if (heads > 1) {
+                state_to(start_of(ho * heads + h));
+                if (step + 1 < steps) state_from(state_before((step + 1) / heads, ho * heads + (step + 1) % heads));
+            }
+            share_state();
         }
 #pragma unroll
         for (int r = 0; r < 2; r++) {
             const int u = ty + 16 * r;
             if (u < m) store_n<TC>(out + (size_t)(t0 + (w.reverse ? m - 1 - u : u)) * out_stride + tx * TC, acc[r]);
+#pragma unroll
+            for (int c = 0; c < TC; c++) acc[r][c] = 0.f;
         }
     }
     if (s.nseg == 1 && args.last) state_to(args.last + ((size_t)b * s.Hv + ho) * head_floats);  // heads == 1
@@ -360,7 +403,8 @@ cudaError_t allow_smem(K kernel, int bytes) {
 
 template <int DK, int RS>
 cudaError_t summary(const LinearSummaryArgs& a, cudaStream_t st) {
-    const int bytes = 4 * (LC * (RS + 4) + LC * (DK + 4) + LC + 1);
+    const int bytes = 4 * (2 * LC * (RS + 4) + 2 * LC * (DK + 4) + LC + 1);
+    if (cudaError_t e = allow_smem(linear_summary_kernel<DK, RS>, bytes)) return e;
     trace_begin("linear_summary", st);
     linear_summary_kernel<DK, RS><<<dim3(a.s.nseg * (a.s.Dv / RS), a.s.Hv, a.s.B), 256, bytes, st>>>(a);
     trace_end(st);
@@ -369,13 +413,13 @@ cudaError_t summary(const LinearSummaryArgs& a, cudaStream_t st) {
 
 template <int D1, int CS, bool ROWS1>
 cudaError_t mix(const LinearMixArgs& a, const MixView& w, int D2, cudaStream_t st) {
-    const int bytes = 4 * (2 * LC * (D1 + 4) + LC * (CS + 4) + D1 * (CS + 4) + LC * (LC + 4) + LC + 1);
+    const int bytes = 4 * (3 * LC * (D1 + 4) + 2 * LC * (CS + 4) + D1 * (CS + 4) + LC * (LC + 4) + 2 * (LC + 1));
     auto kernel = linear_mix_kernel<D1, CS, ROWS1>;
     if (cudaError_t e = allow_smem(kernel, bytes)) return e;
     trace_begin("linear_mix", st);
-    kernel<<<dim3(a.s.nseg * (D2 / CS), w.ho, a.s.B), 256, bytes, st>>>(a, w);
+    const cudaError_t e = launch_after(kernel, dim3(a.s.nseg * (D2 / CS), w.ho, a.s.B), 256, bytes, st, a.overlap, a, w);
     trace_end(st);
-    return cudaGetLastError();
+    return e;
 }
 
 template <int CS, bool ROWS1>

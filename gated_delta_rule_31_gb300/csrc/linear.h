@@ -59,6 +59,7 @@ struct LinearMixArgs {
     void* images;   // bf16 o and dv: the state that each 128-token chunk starts from (dv: the adjoint of
                     // the one it ends in) is kept there as a swizzled bf16 tile, 32 KB for each
                     // (b, hv, chunk), for launch_linear_tc_grad; or null
+    bool overlap;   // fp32: the kernel before it on the stream is the combine step of its call (launch_after)
 };
 
 // A launch that may begin while the kernel before it on the stream, one of the same call, still runs; that
