@@ -424,21 +424,22 @@ def linear_fwd(q, k, v, g, h0=None, scale=None, lengths=None, output_final_state
     return o, ht, states
 
 
-def linear_bwd(q, k, v, g, h0, do, dht=None, scale=None, lengths=None, workspace=None, states=None):
+def linear_bwd(q, k, v, g, h0, do, dht=None, scale=None, lengths=None, workspace=None, states=None, need_dh0=True):
     """VJP of linear_fwd for the loss <do, o> + <dht, ht> (gdr_linear_bwd, or gdr_linear_bwd_states
     with the `states` of linear_fwd(save_states=True) on the same inputs). Returns a dict of dq,
-    dk, dv in the inputs' dtype and dh0 fp32; the decay is a constant and has no gradient."""
+    dk, dv in the inputs' dtype and dh0 fp32 (None with need_dh0=False); the decay is a constant and
+    has no gradient."""
     at, sizes, dev, state = _linear_problem(q, k, v, g, scale, False)
     _linear_extras(dev, state, h0, lengths)
     _is(do, "do", v.dtype, dev, v.shape)
     if dht is not None:
         _is(dht, "dht", torch.float32, dev, state)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    dh0 = torch.empty(state, dtype=torch.float32, device=dev)
+    dh0 = torch.empty(state, dtype=torch.float32, device=dev) if need_dh0 else None
     need = sizes[2] if states is None else sizes[3]
     ws = _scratch(need, dev, workspace)
     ins = (at, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _at(h0), _at(lengths))
-    rest = (do.data_ptr(), _at(dht), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dh0.data_ptr(), ws.data_ptr(), need,
+    rest = (do.data_ptr(), _at(dht), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _at(dh0), ws.data_ptr(), need,
             _raw_stream(dev))
     if states is None:
         _check(lib().gdr_linear_bwd(*ins, *rest))

@@ -74,6 +74,7 @@ class LinearAttentionFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, g, h0, scale, lengths):
         ctx.scale = scale
+        ctx.set_materialize_grads(False)  # an unused ht costs no zeros: the adjoint state starts from none
         if not any(ctx.needs_input_grad):
             return linear_fwd(q, k, v, g, h0, scale=scale, lengths=lengths)
         o, ht, states = linear_fwd(q, k, v, g, h0, scale=scale, lengths=lengths, save_states=True)
@@ -86,8 +87,9 @@ class LinearAttentionFunction(torch.autograd.Function):
         q, k, v, g, h0, lengths, states = ctx.saved_tensors
         do = torch.zeros_like(v) if do is None else do.to(v.dtype).contiguous()
         dht = None if dht is None else dht.to(torch.float32).contiguous()
-        gr = linear_bwd(q, k, v, g, h0, do, dht, scale=ctx.scale, lengths=lengths, states=states)
-        return gr["dq"], gr["dk"], gr["dv"], None, None if h0 is None else gr["dh0"], None, None
+        gr = linear_bwd(q, k, v, g, h0, do, dht, scale=ctx.scale, lengths=lengths, states=states,
+                        need_dh0=ctx.needs_input_grad[4])
+        return gr["dq"], gr["dk"], gr["dv"], None, gr["dh0"], None, None
 
 
 def linear_attention(q, k, v, g, h0=None, scale=None, lengths=None):

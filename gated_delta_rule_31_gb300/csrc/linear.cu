@@ -61,6 +61,11 @@ __device__ __forceinline__ void store_n(float* p, const float* x) {
     }
 }
 
+// Threads' places in a 16 x 16 grid of state tiles: a warp takes 4 x 8 of them, so that each of its reads
+// of a tile's row or column is one wavefront.
+__device__ __forceinline__ int grid_row() { return (threadIdx.x >> 5 & 3) * 4 + (threadIdx.x >> 3 & 3); }
+__device__ __forceinline__ int grid_col() { return (threadIdx.x >> 7) * 8 + (threadIdx.x & 7); }
+
 // The N columns of thread tx of 16 in a row: runs of four, 64 apart, so that neighbours read without conflicts.
 template <int N>
 __device__ __forceinline__ void load_cols(const float* row, int tx, float* x) {
@@ -107,7 +112,7 @@ __global__ void __launch_bounds__(256) linear_summary_kernel(LinearSummaryArgs a
     const int nr = s.Dv / RS, seg = blockIdx.x / nr, r0 = (blockIdx.x % nr) * RS;
     const int hv = blockIdx.y, b = blockIdx.z, hk = hv / (s.Hv / s.Hk);
     constexpr int TR = RS / 16, TC = DK / 16;
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    const int ty = grid_row(), tx = grid_col();
     if (threadIdx.x <= LC) pw[threadIdx.x] = power(s.g[hv], threadIdx.x);
     const int first = min(seg * s.seg_tokens, valid_tokens(s, b));
     const int last = min(first + s.seg_tokens, valid_tokens(s, b));
@@ -185,6 +190,39 @@ __global__ void __launch_bounds__(256) linear_combine_kernel(LinearCombineArgs a
     if (a.last) store4(a.last + bh * D + i, x);
 }
 
+// Rows of a thread's output tile, from its first: pairs, 8 apart, so that the four pairs of a warp and two
+// runs of k lie in different banks.
+__device__ __forceinline__ constexpr int row_of(int r) { return (r & 1) + 8 * (r >> 1); }
+
+// y[r] += sum over four k of a[row_of(r)][k] x[k], rows at strides sa, sx; a points to column k, x to row k.
+template <int R>
+__device__ __forceinline__ void add_product(float (&y)[R][4], const float* a, int sa, const float* x, int sx, int row) {
+    float4 av[R];
+#pragma unroll
+    for (int r = 0; r < R; r++) av[r] = load4(a + (row + row_of(r)) * sa);
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        const float4 xv = load4(x + e * sx);
+#pragma unroll
+        for (int r = 0; r < R; r++)
+#pragma unroll
+            for (int c = 0; c < 4; c++) y[r][c] += at(av[r], e) * at(xv, c);
+    }
+}
+
+// Adds lane pairs' sums of N rows: the lane with bit `mask` keeps the upper half of them, in y[0 .. N / 2).
+template <int N, int R>
+__device__ __forceinline__ void add_halves(float (&y)[R][4], int mask) {
+    const bool up = threadIdx.x & mask;
+#pragma unroll
+    for (int r = 0; r < N / 2; r++)
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+            const float send = up ? y[r][c] : y[r + N / 2][c], keep = up ? y[r + N / 2][c] : y[r][c];
+            y[r][c] = keep + __shfl_xor_sync(0xffffffffu, send, mask);
+        }
+}
+
 struct MixView {  // the roles of a pass (linear.h)
     const void *a, *b, *c;
     int ha, hc, ho;  // heads of a and b, of c, and of the output
@@ -194,7 +232,7 @@ struct MixView {  // the roles of a pass (linear.h)
 
 // grid (nseg * D2 / CS, output heads, B). D1: width of a and b; a CTA forms CS of the D2 output columns.
 // ROWS1: the state's rows (Dv) run along D1 (dq, dk), else along D2 (o, dv). A thread holds D1 / 16 x
-// CS / 16 of the state, 2 x CS / 16 of the output and 2 x 2 of P.
+// CS / 16 of the state, a lane pair CS / 16 x 4 of the output, and four lanes 4 x 4 of P.
 template <int D1, int CS, bool ROWS1>
 __global__ void __launch_bounds__(256, 2) linear_mix_kernel(LinearMixArgs args, MixView w) {
     extern __shared__ __align__(16) float sm[];
@@ -210,7 +248,7 @@ __global__ void __launch_bounds__(256, 2) linear_mix_kernel(LinearMixArgs args, 
     const int ns = D2 / CS, seg = blockIdx.x / ns, c0 = (blockIdx.x % ns) * CS;
     const int ho = blockIdx.y, b = blockIdx.z, heads = s.Hv / w.ho;  // value heads summed into this output
     const int G = s.Hv / s.Hk;
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    const int ty = grid_row(), tx = grid_col();
     constexpr int TC = CS / 16, TK = D1 / 16;
     const int n = valid_tokens(s, b);
     const int begin = seg * s.seg_tokens, end = min(begin + s.seg_tokens, s.T);
@@ -285,7 +323,13 @@ __global__ void __launch_bounds__(256, 2) linear_mix_kernel(LinearMixArgs args, 
                make_float4(0.f, 0.f, 0.f, 0.f));
     if (nc > 0 || heads == 1) state_from(state_before(0, ho * heads));
     share_state();
-    float acc[2][TC] = {};
+    // The output: a warp forms 4 RI x 16 of it.
+    constexpr int RI = CS / 16, OW = CS / 16;  // rows of a thread's tile; warps side by side
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int orow = 4 * RI * (warp / OW) + 2 * (lane >> 3), oc = 16 * (warp % OW) + 4 * (lane >> 1 & 3);
+    const int last_p = 4 * RI * (warp / OW + 1);  // P is zero from this column on in the warp's rows
+    auto out_row = [&](int r) { return orow + row_of(r); };
+    float acc[RI][4] = {};
     for (int i = 0; i < nc; i++) {
         const int t0 = first + (w.reverse ? nc - 1 - i : i) * LC, m = min(LC, last - t0);
         for (int h = 0; h < heads; h++) {
@@ -294,71 +338,49 @@ __global__ void __launch_bounds__(256, 2) linear_mix_kernel(LinearMixArgs args, 
             cp_async_wait_all();
             __syncthreads();  // the step's tiles and X are there, and the buffers of the step before are free
             fetch(step + 1, false);
-            {  // P: rows ty + 16 i, columns tx + 16 j
-                float p[2][2] = {};
-#pragma unroll 4
-                for (int k = 0; k < D1; k += 4) {
-                    float4 u[2], v[2];
-#pragma unroll
-                    for (int r = 0; r < 2; r++) {
-                        u[r] = load4(A + (ty + 16 * r) * (D1 + 4) + k);
-                        v[r] = load4(Bm + (tx + 16 * r) * (D1 + 4) + k);
-                    }
-#pragma unroll
-                    for (int r = 0; r < 2; r++)
-#pragma unroll
-                        for (int j = 0; j < 2; j++)
-                            p[r][j] += u[r].x * v[j].x + u[r].y * v[j].y + u[r].z * v[j].z + u[r].w * v[j].w;
-                }
-#pragma unroll
-                for (int r = 0; r < 2; r++)
-#pragma unroll
-                    for (int j = 0; j < 2; j++) {
-                        const int u = ty + 16 * r, v = tx + 16 * j;
-                        P[u * (LC + 4) + v] = v <= u ? w.fp * pw[u - v] * p[r][j] : 0.f;
-                    }
-            }
-            {  // a X: rows ty + 16 i, columns tx TC ..
-                float y[2][TC] = {};
+            // P: a warp forms 8 x 16 of it, in tiles of 4 x 4 whose sums four lanes share, every fourth
+            // run of four k each; what lies above the diagonal is not formed where no warp reads it.
+            if (16 * (warp & 1) <= 8 * (warp >> 1)) {
+                const int row = 8 * (warp >> 1) + 4 * (lane >> 4), col = 16 * (warp & 1) + 4 * (lane >> 2 & 3);
+                float p[4][4] = {};
 #pragma unroll 2
-                for (int k = 0; k < D1; k += 4) {
-                    float4 av[2];
+                for (int k = 4 * (lane & 3); k < D1; k += 16) {
+                    float4 u[4], v[4];
 #pragma unroll
-                    for (int r = 0; r < 2; r++) av[r] = load4(A + (ty + 16 * r) * (D1 + 4) + k);
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        float xv[TC];
-                        load_n<TC>(X + (k + e) * (CS + 4) + tx * TC, xv);
-#pragma unroll
-                        for (int c = 0; c < TC; c++)
-#pragma unroll
-                            for (int r = 0; r < 2; r++) y[r][c] += at(av[r], e) * xv[c];
+                    for (int r = 0; r < 4; r++) {
+                        u[r] = load4(A + (row + r) * (D1 + 4) + k);
+                        v[r] = load4(Bm + (col + r) * (D1 + 4) + k);
                     }
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+#pragma unroll
+                        for (int r = 0; r < 4; r++)
+#pragma unroll
+                            for (int j = 0; j < 4; j++) p[r][j] += at(u[r], e) * at(v[j], e);
                 }
+                add_halves<4>(p, 1);
+                add_halves<2>(p, 2);
+                const int u = row + 2 * (lane & 1) + (lane >> 1 & 1);
 #pragma unroll
-                for (int r = 0; r < 2; r++) {
-                    const float f = w.fx * pw[ty + 16 * r + 1 - w.reverse];
+                for (int j = 0; j < 4; j++) p[0][j] = col + j <= u ? w.fp * pw[u - col - j] * p[0][j] : 0.f;
+                store_n<4>(P + u * (LC + 4) + col, p[0]);
+            }
+            {  // a X: the sums of a tile of RI x 4 are shared by two lanes, every other run of four k each
+                float y[RI][4] = {};
+#pragma unroll 2
+                for (int k = 4 * (lane & 1); k < D1; k += 8) add_product<RI>(y, A + k, D1 + 4, X + k * (CS + 4) + oc, CS + 4, orow);
 #pragma unroll
-                    for (int c = 0; c < TC; c++) acc[r][c] += f * y[r][c];
+                for (int r = 0; r < RI; r++) {
+                    const float f = w.fx * pw[out_row(r) + 1 - w.reverse];
+#pragma unroll
+                    for (int c = 0; c < 4; c++) acc[r][c] += f * y[r][c];
                 }
             }
             __syncthreads();  // P is written; A and X are free
             fetch(step + 1, true);
 #pragma unroll 2
-            for (int k = 0; k < LC; k += 4) {  // P c
-                float4 pv[2];
-#pragma unroll
-                for (int r = 0; r < 2; r++) pv[r] = load4(P + (ty + 16 * r) * (LC + 4) + k);
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    float cv[TC];
-                    load_n<TC>(Cm + (k + e) * (CS + 4) + tx * TC, cv);
-#pragma unroll
-                    for (int c = 0; c < TC; c++)
-#pragma unroll
-                        for (int r = 0; r < 2; r++) acc[r][c] += at(pv[r], e) * cv[c];
-                }
-            }
+            for (int k = 4 * (lane & 1); k < last_p; k += 8)  // P c
+                add_product<RI>(acc, P + k, LC + 4, Cm + k * (CS + 4) + oc, CS + 4, orow);
             {  // the state over this chunk
                 const float over = pw[m];
 #pragma unroll
@@ -385,13 +407,16 @@ __global__ void __launch_bounds__(256, 2) linear_mix_kernel(LinearMixArgs args, 
             }
             share_state();
         }
+        add_halves<RI>(acc, 1);
 #pragma unroll
-        for (int r = 0; r < 2; r++) {
-            const int u = ty + 16 * r;
-            if (u < m) store_n<TC>(out + (size_t)(t0 + (w.reverse ? m - 1 - u : u)) * out_stride + tx * TC, acc[r]);
-#pragma unroll
-            for (int c = 0; c < TC; c++) acc[r][c] = 0.f;
+        for (int r = 0; r < RI / 2; r++) {
+            const int u = out_row(r + (lane & 1) * (RI / 2));
+            if (u < m) store_n<4>(out + (size_t)(t0 + (w.reverse ? m - 1 - u : u)) * out_stride + oc, acc[r]);
         }
+#pragma unroll
+        for (int r = 0; r < RI; r++)
+#pragma unroll
+            for (int c = 0; c < 4; c++) acc[r][c] = 0.f;
     }
     if (s.nseg == 1 && args.last) state_to(args.last + ((size_t)b * s.Hv + ho) * head_floats);  // heads == 1
 }

@@ -237,3 +237,24 @@ def test_more_than_two_to_the_31_values():
     assert rel(ht, ref["ht"]) <= FP32
     for n in ("dq", "dk", "dv"):
         assert rel(gr[n][:, -100:].cpu(), ref[n][:, -100:]) <= BF16, n
+
+
+@pytest.mark.parametrize("initial", [True, False])
+def test_autograd_with_an_unused_result(initial):
+    """A loss of ht alone, and one of o alone, without and with an initial state's gradient."""
+    from gated_delta_rule_31_gb300.autograd import linear_attention
+
+    d = make(1, 150, 1, 2, 64, 32, torch.bfloat16, seed=15, initial=initial)
+    dht = torch.randn(1, 2, 32, 64, generator=torch.Generator().manual_seed(16))
+    x = to_dev(d, cuda_device())
+    names = ("q", "k", "v", "h0") if initial else ("q", "k", "v")
+    leaves = [x[n].requires_grad_() for n in names]
+    o, ht = linear_attention(*leaves[:3], x["g"], leaves[3] if initial else None)
+    of_ht = torch.autograd.grad(ht, leaves, dht.to(ht.device), retain_graph=True)
+    ref = linear(**{**d, "do": torch.zeros_like(d["do"]), "dht": dht})
+    for g, n in zip(of_ht, names):
+        assert rel(g, ref["d" + n]) <= (FP32 if n == "h0" else BF16), n
+    of_o = torch.autograd.grad(o, leaves, x["do"])
+    ref = linear(**{**d, "dht": None})
+    for g, n in zip(of_o, names):
+        assert rel(g, ref["d" + n]) <= (FP32 if n == "h0" else BF16), n
