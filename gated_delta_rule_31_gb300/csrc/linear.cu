@@ -9,12 +9,15 @@
 // adjoint of the state after the chunk, which reaches token 0 (the last one) undecayed. Every
 // power of l has an exponent >= 0, so no decay overflows, and l^0 = 1 also where l = 0.
 //
-// fp32 FMA bounds it (a chunk of 32 tokens and 64 of 128 columns: 721 thousand FMAs), then shared-memory
-// reads, so threads hold contiguous tiles that are read as 16-byte vectors, at least 3.2 FMAs a
-// wavefront, and the state stays in registers with a copy in shared memory for a X. Chunks of 32
-// need fewer FMAs than chunks of 64 (half of P is masked) and leave room for two CTAs per SM, one
-// loading while the other computes. (64-token chunks in strided scalar tiles, one CTA per SM:
-// T = 4096, 32 heads of 128: forward 1171 us.)
+// fp32 FMA bounds it (a chunk of 32 tokens and 64 of 128 columns: 721 thousand FMAs, 0.15 ms in all at
+// T = 4096 and 32 heads of 128), then shared-memory reads, so threads hold tiles of 4 x 4 and more whose
+// operands are read as 16-byte vectors from different banks, lanes that share a tile's sum taking
+// different parts of k; and the state stays in registers with a copy in shared memory for a X. Arithmetic
+// is on fp32 pairs, along the direction in which they were loaded (for the state, the other direction
+// takes 352 us instead of 301). Tiles are copied asynchronously, one chunk ahead. Chunks of 32 need fewer
+// FMAs than chunks of 64 (half of P is masked) and leave room for two CTAs per SM. T = 4096, 32 heads of
+// 128: summary 111 us, mix pass 301. (With synchronous loads and P and a X in strided tiles of 2 x 2 and
+// 2 x 4: 209 and 604. With 64-token chunks, one CTA per SM: 1171 in all.)
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -150,7 +153,7 @@ __global__ void __launch_bounds__(256) linear_summary_kernel(LinearSummaryArgs a
             for (int r = 0; r < TR; r++) {
                 x[r] *= w;
 #pragma unroll
-                for (int c = 0; c < TC; c++) z[r][c] += x[r] * y[c];
+                for (int c = 0; c < TC; c += 2) linear::axpy2<false>(&z[r][c], x[r], y + c);
             }
         }
     }
@@ -202,11 +205,12 @@ __device__ __forceinline__ void add_product(float (&y)[R][4], const float* a, in
     for (int r = 0; r < R; r++) av[r] = load4(a + (row + row_of(r)) * sa);
 #pragma unroll
     for (int e = 0; e < 4; e++) {
-        const float4 xv = load4(x + e * sx);
+        float xv[4];
+        load_n<4>(x + e * sx, xv);
 #pragma unroll
         for (int r = 0; r < R; r++)
 #pragma unroll
-            for (int c = 0; c < 4; c++) y[r][c] += at(av[r], e) * at(xv, c);
+            for (int c = 0; c < 4; c += 2) linear::axpy2<false>(&y[r][c], at(av[r], e), xv + c);
     }
 }
 
@@ -394,11 +398,20 @@ __global__ void __launch_bounds__(256, 2) linear_mix_kernel(LinearMixArgs args, 
                     load_n<TK>(Bm + u * (D1 + 4) + ty * TK, bv);
                     load_n<TC>(Cm + u * (CS + 4) + tx * TC, cv);
 #pragma unroll
-                    for (int c = 0; c < TC; c++) {
-                        cv[c] *= f;
+                    for (int c = 0; c < TC; c++) cv[c] *= f;
 #pragma unroll
-                        for (int r = 0; r < TK; r++) x[r][c] += bv[r] * cv[c];
-                    }
+                    for (int r = 0; r < TK; r += ROWS1 ? 1 : 2)
+#pragma unroll
+                        for (int c = 0; c < TC; c += ROWS1 ? 2 : 1) {  // in pairs as loaded
+                            if (ROWS1) {
+                                linear::axpy2<false>(&x[r][c], bv[r], cv + c);
+                            } else {
+                                float pair[2] = {x[r][c], x[r + 1][c]};
+                                linear::axpy2<false>(pair, cv[c], bv + r);
+                                x[r][c] = pair[0];
+                                x[r + 1][c] = pair[1];
+                            }
+                        }
                 }
             }
             if (heads > 1) {
@@ -459,9 +472,9 @@ cudaError_t mix_d1(const LinearMixArgs& a, const MixView& w, int D1, int D2, cud
 }  // namespace
 
 // Segments of whole blocks: none where the heads alone give two CTAs per SM, since a second pass over the
-// tokens for the segments' sums takes about 0.3 of the mix pass's time; else as many as give two CTAs per
+// tokens for the segments' sums takes 0.4 of the mix pass's time; else as many as give two CTAs per
 // SM, or up to eight if segments stay four blocks long, so that the SMs end together (T = 4096, 32 heads
-// of 128: 137 + 465 us with one round of CTAs, 122 + 422 with four).
+// of 128: with one round of CTAs a mix pass of 422 us takes 465).
 int linear_segments(int B, int T, int Hv, int Dv) {
     const long long blocks = (T + kLinearBlock - 1) / kLinearBlock, units = (long long)B * Hv * (Dv < 64 ? 1 : Dv / 64);
     if (blocks <= 1 || units <= 0 || units >= 304) return 1;
