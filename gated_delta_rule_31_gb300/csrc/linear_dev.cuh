@@ -65,13 +65,6 @@ __device__ __forceinline__ void scale2(float* x, float f) {
     asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(w));
     asm("mov.b64 {%0, %1}, %2;" : "=f"(x[0]), "=f"(x[1]) : "l"(v));
 }
-__device__ __forceinline__ void scale2(float* x, float f0, float f1) {
-    uint64_t v, w;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x[0]), "f"(x[1]));
-    asm("mov.b64 %0, {%1, %2};" : "=l"(w) : "f"(f0), "f"(f1));
-    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(w));
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x[0]), "=f"(x[1]) : "l"(v));
-}
 template <bool FADE>  // s <- f s + d, or s + f d
 __device__ __forceinline__ void axpy2(float* s, float f, const float* d) {
     uint64_t v, w, u;

@@ -50,8 +50,8 @@ namespace {
 constexpr int SLOTS = 6, SLOTS_C = 3;  // input tiles, those of c
 constexpr uint32_t SLOT = TILE;
 constexpr uint32_t AT_S = SLOTS * SLOT;     // bf16 state [128 x 128]
-constexpr uint32_t AT_W = AT_S + 32768;     // decays: three tables of 128 bf16 pairs
-constexpr uint32_t BYTES = AT_W + 1536;
+constexpr uint32_t AT_W = AT_S + 32768;     // weights of c' for 128 exponents, 8 bytes each
+constexpr uint32_t BYTES = AT_W + 1024;
 static_assert(BYTES + 1024 <= 232448, "shared memory");
 constexpr int THREADS = 768;
 // Registers a thread: 768 threads start with 80; 8 warps keep them, 4 go up, 8 and 4 go down.
@@ -78,6 +78,15 @@ __device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
+__device__ __forceinline__ void tmem_st_16x128b_x2(uint32_t taddr, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+// The upper halves of two floats: bf16 values, rounded towards zero.
+__device__ __forceinline__ uint32_t high_halves(float lo, float hi) {
+    return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+}
 // Four transposed 8 x 8 tiles of 16-bit values, rows at the addresses of lanes 8 i .. 8 i + 7: thread t
 // gets values (2 (t % 4), 2 (t % 4) + 1) of column t / 4 of each.
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t* r) {
@@ -87,7 +96,7 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t* r) {
                  : "memory");
 }
 
-// TERMS: bf16 terms of c' (2 or 4). MIX: the output pass, else the summary.
+// TERMS: bf16 terms of c' (2 or 3). MIX: the output pass, else the summary.
 template <bool MIX, int TERMS>
 __global__ void __launch_bounds__(THREADS, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
@@ -110,12 +119,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     // TMEM columns. Output pass: P (P' packed in the first half of each 64), X and then the output, the
     // chunk's sum of the state, a ring of pieces of c'. Summary: two sums and the ring.
-    constexpr int PIECE = MIX && TERMS == 4 ? 32 : 64; // tokens of a piece
+    constexpr int PIECE = MIX && TERMS == 3 ? 32 : 64; // tokens of a piece
     constexpr int STEPS = PIECE / 16;                  // products of a piece and term
     constexpr uint32_t STEP = 8 * TERMS;               // columns of a step: its terms, eight each
     constexpr uint32_t COL_P = 0, COL_X = 128, COL_S = MIX ? 256 : 0, COL_C = MIX ? 384 : 256;
     constexpr int SUMS = MIX ? 1 : 2, RING = (512 - COL_C) / (STEPS * STEP);
-    static_assert(RING == 2 && (TERMS == 2 || TERMS == 4), "pieces");
+    static_assert(RING == 2 && (TERMS == 2 || TERMS == 3), "pieces");
     constexpr int SLOTS_B = MIX ? 2 : 3;
     auto slot_c = [](int i) { return i % SLOTS_C; };
     auto slot_b = [](int i) { return SLOTS_C + i % SLOTS_B; };
@@ -163,18 +172,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int d = a.reverse ? tri_zero - tid : tid - tri_zero;
         tri[tid] = d >= 0 ? a.fp * power(g, d) : 0.f;
     }
-    // parts w1, w2, w3 of f'' l^e for two tokens in a row, the first of exponent e (the next e - 1, in
-    // reverse e + 1)
-    uint32_t* parts = reinterpret_cast<uint32_t*>(sm + AT_W);
+    // f'' l^e for two tokens in a row, the first of exponent e (the next e - 1, in reverse e + 1): for three
+    // terms in fp32, for two as bf16 parts, w1 and w2
+    uint32_t* weights = reinterpret_cast<uint32_t*>(sm + AT_W);
     if (tid < 128) {
-        float x0 = a.fu * power(g, tid), x1 = a.fu * power(g, a.reverse ? tid + 1 : max(tid - 1, 0));
-#pragma unroll
-        for (int h = 0; h < 3; h++) {
-            const uint32_t w = pack_bf16(x0, x1);
-            parts[128 * h + tid] = w;
-            x0 -= bf16lo(w);
-            x1 -= bf16hi(w);
-        }
+        const float x0 = a.fu * power(g, tid), x1 = a.fu * power(g, a.reverse ? tid + 1 : max(tid - 1, 0));
+        const uint32_t w = pack_bf16(x0, x1);
+        weights[2 * tid] = TERMS == 3 ? __float_as_uint(x0) : w;
+        weights[2 * tid + 1] = TERMS == 3 ? __float_as_uint(x1) : pack_bf16(x0 - bf16lo(w), x1 - bf16hi(w));
     }
     if (warp == 20) {
         tmem_alloc(&tmem_sh, 512);
@@ -233,28 +238,31 @@ __global__ void __launch_bounds__(THREADS, 1)
                             v[1][k] &= keep;
                         }
                     }
-                    const uint32_t* w0 = parts + (a.reverse ? u + 1 : max(m - 1 - u, 0));
-                    const uint32_t* w8 = parts + (a.reverse ? u + 9 : max(m - 9 - u, 0));
-                    const uint32_t w[2][3] = {{w0[0], w0[128], TERMS == 4 ? w0[256] : 0u}, {w8[0], w8[128], TERMS == 4 ? w8[256] : 0u}};
+                    const uint2* table = reinterpret_cast<const uint2*>(weights);
+                    const uint2 w[2] = {table[a.reverse ? u + 1 : max(m - 1 - u, 0)], table[a.reverse ? u + 9 : max(m - 9 - u, 0)]};
 #pragma unroll
                     for (int g2 = 0; g2 < 2; g2++) {
                         uint32_t y[4 * TERMS];
 #pragma unroll
                         for (int k = 0; k < 4; k++) {
-                            const uint32_t x = v[g2][k], *p = w[k >> 1];
-                            y[k] = bf16x2_mul(x, p[0]);
-                            const uint32_t rest = bf16x2_fma(x, p[0], bf16x2_neg(y[k]));
+                            const uint32_t x = v[g2][k];
+                            const uint2 p = w[k >> 1];
                             if (TERMS == 2) {
-                                y[4 + k] = bf16x2_fma(x, p[1], rest);
-                            } else {
-                                y[4 + k] = rest;
-                                y[8 + k] = bf16x2_mul(x, p[1]);
-                                y[12 + k] = bf16x2_fma(x, p[2], bf16x2_fma(x, p[1], bf16x2_neg(y[8 + k])));
+                                y[k] = bf16x2_mul(x, p.x);
+                                y[4 + k] = bf16x2_fma(x, p.y, bf16x2_fma(x, p.x, bf16x2_neg(y[k])));
+                            } else {  // 24 bits cut into three times eight
+                                float f0 = bf16lo(x) * __uint_as_float(p.x), f1 = bf16hi(x) * __uint_as_float(p.y);
+#pragma unroll
+                                for (int h = 0; h < 3; h++) {
+                                    y[4 * h + k] = high_halves(f0, f1);
+                                    f0 -= bf16hi(__float_as_uint(f0));
+                                    f1 -= bf16hi(__float_as_uint(f1));
+                                }
                             }
                         }
                         const uint32_t to = lanes + ((uint32_t)(16 * g2) << 16) + COL_C + (r * STEPS + in) * STEP;
                         tmem_st_16x128b_x4(to, y);
-                        if (TERMS == 4) tmem_st_16x128b_x4(to + 16, y + 4 * (TERMS - 2));
+                        if (TERMS == 3) tmem_st_16x128b_x2(to + 16, y + 4 * (TERMS - 1));
                     }
                 }
                 tmem_wait_st();
@@ -591,7 +599,7 @@ cudaError_t launch(const CUtensorMap* maps, const TcArgs& a, int segs, const cha
 }  // namespace
 
 cudaError_t launch_linear_tc_summary(const LinearSummaryArgs& x, bool all, int* status, bool clear, cudaStream_t st) {
-    if (cudaError_t e = allow_smem<false, 4>()) return e;
+    if (cudaError_t e = allow_smem<false, 3>()) return e;
     CUtensorMap maps[4];
     memset(maps, 0, sizeof(maps));
     if (!tile_map(&maps[1], x.cols, x.s, x.s.Hk, x.s.Dk) || !tile_map(&maps[2], x.rows, x.s, x.s.Hv, x.s.Dv))
@@ -606,7 +614,7 @@ cudaError_t launch_linear_tc_summary(const LinearSummaryArgs& x, bool all, int* 
     a.status = status;
     a.clear_status = clear;
     a.first_seg = all || !x.reverse ? 0 : 1;
-    return launch<false, 4>(maps, a, all ? x.s.nseg : x.s.nseg - 1, "linear_summary", false, st);
+    return launch<false, 3>(maps, a, all ? x.s.nseg : x.s.nseg - 1, "linear_summary", false, st);
 }
 
 cudaError_t launch_linear_tc_mix(const LinearMixArgs& x, const float* start, int start_segs, float* last, int* status,
@@ -615,7 +623,7 @@ cudaError_t launch_linear_tc_mix(const LinearMixArgs& x, const float* start, int
     // One segment carries the state that leaves the call, with four terms (also where the caller does not
     // want it, so that the kept states are the same); with several it comes from the summary.
     const bool one = x.s.nseg == 1;
-    if (cudaError_t e = one ? allow_smem<true, 4>() : allow_smem<true, 2>()) return e;
+    if (cudaError_t e = one ? allow_smem<true, 3>() : allow_smem<true, 2>()) return e;
     CUtensorMap maps[4];
     if (!tile_map(&maps[0], rev ? x.k : x.q, x.s, x.s.Hk, x.s.Dk) || !tile_map(&maps[1], rev ? x.q : x.k, x.s, x.s.Hk, x.s.Dk) ||
         !tile_map(&maps[2], rev ? x.do_ : x.v, x.s, x.s.Hv, x.s.Dv) || !tile_map(&maps[3], x.out, x.s, x.s.Hv, x.s.Dv))
@@ -636,7 +644,7 @@ cudaError_t launch_linear_tc_mix(const LinearMixArgs& x, const float* start, int
     a.status = status;
     a.clear_status = clear;
     const char* name = rev ? "linear_dv" : "linear_o";
-    return one ? launch<true, 4>(maps, a, x.s.nseg, name, overlap, st) : launch<true, 2>(maps, a, x.s.nseg, name, overlap, st);
+    return one ? launch<true, 3>(maps, a, x.s.nseg, name, overlap, st) : launch<true, 2>(maps, a, x.s.nseg, name, overlap, st);
 }
 
 // Segments of whole chunks, one CTA each, on 152 SMs. In units of one chunk of the output pass (2.7 us): a
