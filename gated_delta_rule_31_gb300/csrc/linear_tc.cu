@@ -15,7 +15,7 @@
 // All four run as tcgen05 products with 128 rows. Rounding to bf16: P' (an operand kept in TMEM), the copy
 // of S that X reads, and the result, one rounding each. c' would be a fourth, so it enters as the
 // sum of bf16 terms: two (2^-17 off, below the other roundings) where the state only feeds X,
-// three (exact: 24 bits) where it is returned in fp32. Each chunk's sum starts from zero in TMEM
+// three (the 24 bits of an fp32 product) where it is returned in fp32. Each chunk's sum starts from zero in TMEM
 // and is added to the fp32 registers there, so the tensor core's own accumulation never runs over more than
 // one chunk. X is scaled by its rows' decays in TMEM and Y accumulates onto it.
 //
@@ -25,12 +25,19 @@
 //
 // Warps: 0-7 turn P into P' and finish the output (a thread is half a token row), 8-11 hold the
 // state (a thread is a state row), 12-19 form c' in pieces of PIECE tokens (in the summary 0-7 do
-// too), 20 and 23 copy tiles in, 21 issues the products, 22 stores the output tiles. The state rows need the registers: warps
-// 12-23 give some up (setmaxnreg). The products of a chunk are issued as X, the next chunk's sum of the
-// state, Y, the next chunk's P: each has the others' time to wait for the warps that feed it. Input tiles (128 tokens,
-// two 64-channel panels, 32 KB) have three slots for c, which is wanted a chunk ahead and whose
-// slot then takes the output tile, two for b and one for a (three for b in the summary). Channels past a head size of 32 read as zero (out of the tensor map's range),
-// sizes of 32 and 64 use one panel. With 512 TMEM columns and 225 KB of shared memory one CTA runs per SM.
+// too), 20 and 23 copy tiles in, 21 issues the products, 22 stores the output tiles. The state rows need
+// the registers: warps 12-23 give some up (setmaxnreg). The products of a chunk are issued as X, the next
+// chunk's sum of the state, Y, the next chunk's P: each has the others' time to wait for the warps that
+// feed it. Input tiles (128 tokens, two 64-channel panels, 32 KB) have three slots for c, which is wanted
+// a chunk ahead and whose slot then takes the output tile, two for b and one for a (three for b in the
+// summary). Channels past a head size of 32 read as zero (out of the tensor map's range), sizes of 32 and
+// 64 use one panel. With 512 TMEM columns and 224 KB of shared memory one CTA runs per SM.
+//
+// T = 32768, Hk 16, Hv 32, D 128, four segments a head: the output pass 160 us (187 with the states kept),
+// bound by the copies in and out (805 MB, 74% of a plain copy's rate, from 128 CTAs with about one chunk's
+// tiles in flight each); the summary 101 us, bound by the waits between copy, decay, product and sum of a chunk (1.45 us;
+// 85 us in all with two terms). Pieces of 32 tokens in a ring of five take 111 us for the summary, of 128
+// with one sum 118; the output tile in b's slot takes 198 us for the output pass where c's took 172.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -647,10 +654,10 @@ cudaError_t launch_linear_tc_mix(const LinearMixArgs& x, const float* start, int
     return one ? launch<true, 3>(maps, a, x.s.nseg, name, overlap, st) : launch<true, 2>(maps, a, x.s.nseg, name, overlap, st);
 }
 
-// Segments of whole chunks, one CTA each, on 152 SMs. In units of one chunk of the output pass (2.7 us): a
+// Segments of whole chunks, one CTA each, on 152 SMs. In units of one chunk of the output pass (2.4 us): a
 // wave of it takes a segment's chunks and about four for its start and end; with several segments there is
 // the summary too, at about 0.6 a chunk, and the combine step, which reads every segment's state. At
-// T = 32768 and 32 heads 4 segments take 105 + 8 + 170 us, 9 take 109 + 10 + 174, 19 take 121 + 16 + 190.
+// T = 32768 and 32 heads 4 segments take 101 + 8 + 160 us, 9 take 104 + 10 + 162, 19 take 114 + 16 + 180.
 int linear_tc_segments(int B, int T, int Hv) {
     const long long chunks = (T + C - 1) / C, heads = (long long)B * Hv;
     if (chunks <= 1 || heads <= 0) return 1;
