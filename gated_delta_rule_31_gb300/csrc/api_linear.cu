@@ -28,6 +28,7 @@ gdr_status check_problem(const gdr_linear_problem* p, bool decode) {
     if (!isfinite(p->scale)) return GDR_ERR_INVALID_ARG;
     if (!dim_ok(p->Dk) || !dim_ok(p->Dv)) return GDR_ERR_UNSUPPORTED;
     if (p->B > 65535 || p->Hv > 65535) return GDR_ERR_UNSUPPORTED;  // grid y/z limits
+    if ((long long)p->B * p->Hv * p->Dv >= 1LL << 32) return GDR_ERR_UNSUPPORTED;  // a state of 512 GB or more
     return GDR_OK;
 }
 

@@ -2,16 +2,16 @@
 // (gdr_linear_decode_step): S <- exp(g) S + v k^T in place, o = scale S q.
 //
 // The state is read and written once, 8 bytes an element against 4 operations, so HBM bounds a
-// batch and latency a single sequence. Neighbouring CTAs take neighbouring rows of the state: B = 128 of 32
+// batch and latency a single sequence. Neighbouring CTAs take neighbouring parts of the state: B = 128 of 32
 // heads, 128 x 128, 540 MB, in 80.0 us, the rate of a plain copy, against 89.7 with the heads
-// fastest. A warp has ROWS state rows in flight (2: 83.6, 8: 88.7 us), and their dot products with q
-// are reduced together: each exchange halves the rows a lane still holds. A step is launched so that it may start
-// while the kernel before it on the stream ends (programmatic dependent launch), and reads and writes only
-// after that kernel is complete.
+// fastest. A warp reads 512 contiguous bytes at a time, one to four state rows, LINES of them in flight
+// (eight: 88.7 us; for heads of 64 x 64 a row at a time, 256 bytes, takes 20.1 us at B = 128 in L2 instead
+// of 16.0), and the rows' dot products with q are reduced together: each exchange halves
+// those that a lane still holds. A step is launched so that it may start while the kernel before it on the
+// stream ends (programmatic dependent launch), and reads and writes only after that kernel is complete.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
-#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -22,52 +22,52 @@ namespace gdr {
 
 namespace {
 
+__device__ __forceinline__ void get4(const float* p, float* x) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+}
+__device__ __forceinline__ void get4(const __nv_bfloat16* p, float* x) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    x[0] = bf16lo(v.x); x[1] = bf16hi(v.x); x[2] = bf16lo(v.y); x[3] = bf16hi(v.y);
+}
 __device__ __forceinline__ float as_float(float x) { return x; }
 __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// grid (Dv / (4 ROWS), Hv, B), 4 warps of ROWS (4 or 2) state rows; a row is DK / 32 floats a lane.
-template <int DK, int ROWS, typename T>
+// 4 warps, each LINES (4 or 2) lines of 128 floats: 128 / DK state rows of one head in a line, LANES lanes a row.
+template <int DK, int LINES, typename T>
 __global__ void __launch_bounds__(128) linear_step_kernel(LinearStepArgs a) {
-    constexpr int EL = DK / 32;
-    using Vec = typename std::conditional<EL == 4, float4, typename std::conditional<EL == 2, float2, float>::type>::type;
+    constexpr int LANES = DK / 4, PER = 32 / LANES;
     linear::next_kernel_may_start();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int hv = blockIdx.y, b = blockIdx.z, hk = hv / (a.Hv / a.Hk);
-    const size_t bh = (size_t)b * a.Hv + hv;
-    const int r0 = (blockIdx.x * 4 + warp) * ROWS;
-    const T* q = static_cast<const T*>(a.q) + ((size_t)b * a.Hk + hk) * DK + lane * EL;
-    const T* k = static_cast<const T*>(a.k) + ((size_t)b * a.Hk + hk) * DK + lane * EL;
-    const T* v = static_cast<const T*>(a.v) + bh * a.Dv + r0;
-    T* o = static_cast<T*>(a.o) + bh * a.Dv + r0;
-    Vec* S = reinterpret_cast<Vec*>(a.state + (bh * a.Dv + r0) * DK) + lane;
+    const unsigned row0 = (blockIdx.x * 4 + warp) * (LINES * PER), rows = (unsigned)a.B * a.Hv * a.Dv;
+    if (row0 >= rows) return;  // a head has whole warps of rows, not whole CTAs
+    float4* S = reinterpret_cast<float4*>(a.state + (size_t)row0 * DK) + lane;
+    const unsigned bh = row0 / a.Dv, b = bh / a.Hv, hv = bh - b * a.Hv, hk = hv / ((unsigned)a.Hv / a.Hk);
+    const size_t at = ((size_t)b * a.Hk + hk) * DK + lane % LANES * 4, row = row0 + lane / LANES;  // and every PER-th row
     linear::wait_kernel_before();
-    __align__(16) float x[ROWS][EL];
+    float4 x[LINES];
 #pragma unroll
-    for (int r = 0; r < ROWS; r++) *reinterpret_cast<Vec*>(x[r]) = __ldcs(S + r * 32);
-    float kf[EL], qf[EL];
-#pragma unroll
-    for (int e = 0; e < EL; e++) {
-        kf[e] = as_float(k[e]);
-        qf[e] = as_float(q[e]);
-    }
+    for (int r = 0; r < LINES; r++) x[r] = __ldcs(S + r * 32);
+    float kf[4], qf[4];
+    get4(static_cast<const T*>(a.k) + at, kf);
+    get4(static_cast<const T*>(a.q) + at, qf);
     const float l = expf(a.g[hv]);
-    float acc[ROWS];
+    float acc[LINES];
 #pragma unroll
-    for (int r = 0; r < ROWS; r++) {
-        const float vr = as_float(v[r]);
-        acc[r] = 0.f;
-#pragma unroll
-        for (int e = 0; e < EL; e++) {
-            x[r][e] = l * x[r][e] + vr * kf[e];
-            acc[r] += x[r][e] * qf[e];
-        }
-        __stcs(S + r * 32, *reinterpret_cast<Vec*>(x[r]));
+    for (int r = 0; r < LINES; r++) {
+        const float vr = as_float(static_cast<const T*>(a.v)[row + r * PER]);
+        x[r].x = l * x[r].x + vr * kf[0];
+        x[r].y = l * x[r].y + vr * kf[1];
+        x[r].z = l * x[r].z + vr * kf[2];
+        x[r].w = l * x[r].w + vr * kf[3];
+        acc[r] = x[r].x * qf[0] + x[r].y * qf[1] + x[r].z * qf[2] + x[r].w * qf[3];
+        __stcs(S + r * 32, x[r]);
     }
-    int off = 16;
+    int off = LANES / 2;
 #pragma unroll
-    for (int n = ROWS / 2; n > 0; n /= 2, off /= 2) {  // lanes with bit `off` keep the upper half of the rows
+    for (int n = LINES / 2; n > 0; n /= 2, off /= 2) {  // lanes with bit `off` keep the upper half of the rows
         const bool up = lane & off;
 #pragma unroll
         for (int r = 0; r < n; r++) {
@@ -75,30 +75,34 @@ __global__ void __launch_bounds__(128) linear_step_kernel(LinearStepArgs a) {
             acc[r] = keep + __shfl_xor_sync(0xffffffffu, send, off);
         }
     }
-    constexpr int LEFT = 32 / ROWS;  // lanes that share a row now
+    constexpr int LEFT = LANES / LINES;  // lanes that share a row now
 #pragma unroll
     for (int m = LEFT / 2; m > 0; m /= 2) acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], m);
-    if (lane % LEFT == 0) put(o + lane / LEFT, a.scale * acc[0]);
+    if (lane % LEFT == 0) put(static_cast<T*>(a.o) + row + lane % LANES / LEFT * PER, a.scale * acc[0]);
 }
 
-template <int DK, int ROWS, typename T>
+template <int DK, int LINES, typename T>
 cudaError_t step(const LinearStepArgs& a, cudaStream_t st) {
+    constexpr int ROWS = 4 * LINES * 128 / DK;  // of a CTA
+    const long long rows = (long long)a.B * a.Hv * a.Dv;
     trace_begin("linear_step", st);
     const cudaError_t e =
-        launch_after(linear_step_kernel<DK, ROWS, T>, dim3(a.Dv / (4 * ROWS), a.Hv, a.B), 128, 0, st, true, a);
+        launch_after(linear_step_kernel<DK, LINES, T>, dim3((unsigned)((rows + ROWS - 1) / ROWS)), 128, 0, st, true, a);
     trace_end(st);
     return e;
 }
 
-// Few states (less than two CTAs per SM) are spread over twice the warps.
+// Two lines a warp while that gives no more than two rounds of 16 CTAs per SM (32 heads of 128 x 128, states
+// in L2: B = 1 2.7 us with either, B = 4 3.2 with two, 4.6 with four; from HBM: B = 8 7.2 and 7.6), else
+// four (in L2: B = 16 9.9 with two, 8.6 with four; B = 128 82.6 and 79.8).
 template <int DK, typename T>
-cudaError_t step_rows(const LinearStepArgs& a, cudaStream_t st) {
-    return (long long)a.B * a.Hv * a.Dv < 2 * 152 * 16 ? step<DK, 2, T>(a, st) : step<DK, 4, T>(a, st);
+cudaError_t step_lines(const LinearStepArgs& a, cudaStream_t st) {
+    return (long long)a.B * a.Hv * a.Dv * DK / 128 < 2 * 152 * 128 ? step<DK, 2, T>(a, st) : step<DK, 4, T>(a, st);
 }
 
 template <typename T>
 cudaError_t step_of(const LinearStepArgs& a, cudaStream_t st) {
-    return a.Dk == 32 ? step_rows<32, T>(a, st) : a.Dk == 64 ? step_rows<64, T>(a, st) : step_rows<128, T>(a, st);
+    return a.Dk == 32 ? step_lines<32, T>(a, st) : a.Dk == 64 ? step_lines<64, T>(a, st) : step_lines<128, T>(a, st);
 }
 
 }  // namespace

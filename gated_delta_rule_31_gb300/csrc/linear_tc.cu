@@ -34,10 +34,11 @@
 // 64 use one panel. With 512 TMEM columns and 224 KB of shared memory one CTA runs per SM.
 //
 // T = 32768, Hk 16, Hv 32, D 128, four segments a head: the output pass 160 us (187 with the states kept),
-// bound by the copies in and out (805 MB, 74% of a plain copy's rate, from 128 CTAs with about one chunk's
-// tiles in flight each); the summary 101 us, bound by the waits between copy, decay, product and sum of a chunk (1.45 us;
-// 85 us in all with two terms). Pieces of 32 tokens in a ring of five take 111 us for the summary, of 128
-// with one sum 118; the output tile in b's slot takes 198 us for the output pass where c's took 172.
+// bound by the copies in and out (805 MB, 74% of a plain copy's rate, from 128 CTAs with about one
+// chunk's tiles in flight each); the summary 101 us, bound by the waits between copy, decay, product and
+// sum of a chunk (1.45 us; 85 us in all with two terms). Pieces of 32 tokens in a ring of five take 111 us
+// for the summary, of 128 with one sum 118; the output tile in b's slot took 198 us for the output pass
+// where c's took 172.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
