@@ -170,3 +170,33 @@ def test_more_than_two_to_the_31_values():
     leaf = last.clone().requires_grad_()
     (want,) = torch.autograd.grad(group_norm(leaf, 32, activation="silu"), leaf, y[-8:].cpu().double())
     assert rel(gr["dx"][-8:], want) <= TOL["bf16"]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("groups,D", [(8, 1), (8, 33), (4, 6), (12, 10), (4, 514), (2, 1500), (8, 257), (8, 1025), (2, 4100), (8, 8191)])
+def test_groups_that_start_inside_a_vector(groups, D, dtype):
+    """Rows start on 16 bytes, groups between: the results, and a group whose neighbour holds NaN. (Not the
+    gradients of single values: x / sqrt(x^2 + eps) leaves dx = g r (1 - h^2), a difference of equals that
+    loses x^2 / eps times fp32's precision.)"""
+    dev = cuda_device()
+    kw = dict(activation="silu", center=D > 1)
+    d = make(19, groups * D, TYPES[dtype], True, True, seed=D)
+    x = {n: t.to(dev) for n, t in d.items()}
+    if D > 1:
+        y, got = check(d, groups, dev, dtype, **kw)
+    else:
+        y = gdr.group_norm_fwd(x["x"], groups, x["weight"], x["bias"], x["gate"], **kw)
+        assert rel(y, group_norm(*(d[n].double() if n else groups for n in ("x", "", "weight", "bias", "gate")), **kw)) <= TOL[dtype]
+        got = gdr.group_norm_bwd(x["x"], groups, x["weight"], x["bias"], x["gate"], x["dy"], **kw)
+    bad = slice(D, 2 * D)
+    for n in ("x", "gate", "dy"):
+        x[n][3, bad] = float("nan")
+    y2 = gdr.group_norm_fwd(x["x"], groups, x["weight"], x["bias"], x["gate"], **kw)
+    got2 = gdr.group_norm_bwd(x["x"], groups, x["weight"], x["bias"], x["gate"], x["dy"], **kw)
+    here = torch.zeros(19, groups * D, dtype=torch.bool, device=dev)
+    here[3, bad] = True
+    for a, b in ((y2, y), (got2["dx"], got["dx"]), (got2["dgate"], got["dgate"])):
+        assert a[here].isnan().all() and torch.equal(a[~here], b[~here])
+    for n in ("dweight", "dbias"):
+        assert got2[n][bad].isnan().all()
+        assert torch.equal(got2[n][:D], got[n][:D]) and torch.equal(got2[n][2 * D:], got[n][2 * D:])
