@@ -173,7 +173,8 @@ def test_more_than_two_to_the_31_values():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-@pytest.mark.parametrize("groups,D", [(8, 1), (8, 33), (4, 6), (12, 10), (4, 514), (2, 1500), (8, 257), (8, 1025), (2, 4100), (8, 8191)])
+@pytest.mark.parametrize("groups,D", [(8, 1), (8, 33), (4, 6), (12, 10), (4, 514), (2, 1500), (8, 257), (8, 1025), (2, 4100), (8, 8191),
+                                      (4, 33), (12, 301), (4, 2051)])
 def test_groups_that_start_inside_a_vector(groups, D, dtype):
     """Rows start on 16 bytes, groups between: the results, and a group whose neighbour holds NaN. (Not the
     gradients of single values: x / sqrt(x^2 + eps) leaves dx = g r (1 - h^2), a difference of equals that
