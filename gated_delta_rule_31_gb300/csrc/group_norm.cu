@@ -14,9 +14,9 @@
 // works on: w and b are read once, and dw and db are sums in registers, written as one partial row for
 // each (block row, lane row) and added up in a fixed order by a second kernel. Groups that start between
 // vectors are read in the row's vectors all the same, and what a vector holds of a neighbour is masked.
-// 32768 rows of 32 groups of 128, bf16, gated: forward 123 us (805 MB, 96% of a plain copy's rate;
-// centered, with offsets, 128), backward 233 + 6 us (1.34 GB, 85%). Wider groups wait at a barrier for each
-// sum: one group of 4096, 24414 rows: forward 112 us (79%), backward 338 (44%).
+// 32768 rows of 32 groups of 128, bf16, gated: forward 128 us (805 MB, 93% of a plain copy's rate;
+// centered, with offsets, 130), backward 235 + 6 us (1.34 GB, 84%). Wider groups wait at a barrier for each
+// sum: one group of 4096, 24414 rows: forward 110 us (80%), backward 246 (60%).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -172,9 +172,17 @@ __device__ __forceinline__ void store_valid(T* p, const V (&x)[N], uint32_t vali
     }
     store_vec(p, x);
 }
-// The valid values of a weight's or offset's vector, which need no alignment; the others stay.
+// The valid values of a weight's or offset's vector, which need no alignment; the others stay. (Read for each
+// row a value at a time, the backward of groups of 4096 takes 338 us, by 16 bytes 246.)
 template <bool CUT, int N>
 __device__ __forceinline__ void load_param(const float* p, uint32_t valid, Pair (&x)[N]) {
+    if constexpr (!CUT && N % 2 == 0) {
+        if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+#pragma unroll
+            for (int j = 0; j < N; j += 2) values(*reinterpret_cast<const float4*>(p + 2 * j), x + j);
+            return;
+        }
+    }
 #pragma unroll
     for (int j = 0; j < N; j++) {
         float2 f = split(x[j]);
@@ -409,7 +417,7 @@ __global__ void __launch_bounds__(THREADS, VEC == 1 ? 1 : VEC > 2 && VEC * NV <=
 }
 
 // With 16 values a lane or more, the sums of dw and db lie in shared memory, in places of the lane's own,
-// and w and b are read for each row: registers hold what a row needs (24414 rows of 4096, bf16: 338 us; all
+// and w and b are read for each row: registers hold what a row needs (24414 rows of 4096, bf16: 246 us; all
 // in registers 395).
 template <int VEC, int NV, int L, bool CUT, typename T>
 __global__ void __launch_bounds__(THREADS, VEC * NV <= 16 ? 2 : 1)
