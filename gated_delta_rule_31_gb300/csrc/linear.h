@@ -62,8 +62,9 @@ struct LinearMixArgs {
     bool overlap;   // fp32: the kernel before it on the stream is the combine step of its call (launch_after)
 };
 
-// A launch that may begin while the kernel before it on the stream, one of the same call, still runs; that
-// kernel lets it (griddepcontrol.launch_dependents), and the new one waits before it reads its results.
+// A launch that, with `overlap`, may begin while the kernel before it on the stream still runs; that kernel
+// lets it (griddepcontrol.launch_dependents), and the new one waits before it reads its results
+// (linear_dev.cuh). Of a call's kernels the first is launched without, but for the decode step.
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t st, bool overlap, A... args) {
     cudaLaunchConfig_t cfg = {};

@@ -180,9 +180,14 @@ __global__ void __launch_bounds__(WARPS * 32) recurrent_rows_kernel(RecurrentArg
 // keeps four to eight 128-bit loads in flight for the whole CTA life. With one wave of
 // CTAs (B*Hv of them) the grid has no tail. The step is launched as a programmatic dependent
 // of the kernel before it on the stream: it lets the next launch begin at once
-// (griddepcontrol.launch_dependents), loads q, k, v, g, beta and forms the norms, and only then
-// waits for the previous kernel to complete (griddepcontrol.wait) before it reads the state or
-// writes anything. Back-to-back steps so overlap one step's start with the previous one's end.
+// (griddepcontrol.launch_dependents) and waits for the previous kernel to complete
+// (griddepcontrol.wait) before it reads or writes anything. Back-to-back steps so overlap one
+// step's launch with the previous one's end. Nothing can be read ahead of the wait: a kernel
+// that starts early has not waited yet when it lets the next one begin, so while this one starts,
+// the kernel before the previous one may still be writing what it reads. What is read first is
+// brought into L2, where later writes reach it, ahead of the wait (B = 32, 32 heads, D = 128, fp32,
+// per-channel decay, four states in turn: 24.2 us; without 25.9. One sequence, replayed from a graph:
+// 8.8 and 9.2 us. With q, k, g and the norms taken ahead of the wait they were 24.9 and 7.7).
 #ifndef GDR_DECODE_GROUP
 #define GDR_DECODE_GROUP 4
 #endif
@@ -211,6 +216,17 @@ __global__ void __launch_bounds__(128) decode_kernel(RecurrentArgs a) {
     const size_t qk_off = ((size_t)b * a.Hk + hk) * DK + c0;
     float kh[EL], qh[EL], dec[EL];
     float sk = 0.f, sq = 0.f;
+    auto to_l2 = [](const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); };
+    to_l2(k + qk_off);
+    to_l2(q + qk_off);
+    to_l2(a.g + (a.channel ? bh * DK + c0 : bh));
+    to_l2(a.beta + bh);
+    to_l2(v + bh * (size_t)a.Dv + r0);
+#pragma unroll
+    for (int i = 0; i < G; i++) to_l2(Sin + (size_t)(r0 + i) * DK + c0);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the previous kernel's writes are complete
+#pragma unroll
+    for (int i = 0; i < G; i++) ld_row<EL>(Sin + (size_t)(r0 + i) * DK + c0, cur[i]);
 #pragma unroll
     for (int e = 0; e < EL; e++) {
         kh[e] = to_f(k[qk_off + e]);
@@ -241,9 +257,6 @@ __global__ void __launch_bounds__(128) decode_kernel(RecurrentArgs a) {
     for (int e = 0; e < EL; e++) ak[e] = dec[e] * kh[e];
     const float beta = a.beta[bh];
     const size_t vo = bh * (size_t)a.Dv;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the previous kernel's writes are complete
-#pragma unroll
-    for (int i = 0; i < G; i++) ld_row<EL>(Sin + (size_t)(r0 + i) * DK + c0, cur[i]);
 
     for (int gi = 0; gi < ngroups; gi++) {
         const int rg = r0 + gi * G;
