@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(THREADS, VEC * NV <= 16 ? 2 : 1)
             const bool use = in[i] && row < a.rows;
             if (use) nx[i] = load_raw<VEC>(x + row * C + e[i]);
             if (use && z) nz[i] = load_raw<VEC>(z + row * C + e[i]);
-            ng[i] = use ? load_raw<VEC>(dy + row * C + e[i]) : Raw{};  // no row adds nothing to dw and db
+            if (use) ng[i] = load_raw<VEC>(dy + row * C + e[i]);
         }
     };
     const long long steps = (a.rows + at.row_step - 1) / at.row_step;
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(THREADS, VEC * NV <= 16 ? 2 : 1)
         V s1 = all<V>(0.f), s2 = all<V>(0.f);
 #pragma unroll
         for (int i = 0; i < NV; i++)
-            if (in[i]) {
+            if (in[i] && row < a.rows) {  // no row adds nothing to dw and db: what its registers hold may not be finite
                 V n[N], d[N];
                 if (WIDE) params(i);
                 const int k = WIDE ? 0 : i;
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(THREADS, VEC * NV <= 16 ? 2 : 1)
                     s1 = add(s1, g[i][j]);
                     s2 = fma(g[i][j], h[i][j], s2);
                 }
-                if (z && row < a.rows) store_valid<CUT>(dz + row * C + e[i], u[i], in[i]);
+                if (z) store_valid<CUT>(dz + row * C + e[i], u[i], in[i]);
             }
         float t1 = total(s1), t2 = total(s2);
         group_sum2(t1, t2, at, sums);
