@@ -525,7 +525,7 @@ def group_norm_bwd(x, groups, weight, bias, gate, dy, activation="none", eps=1e-
 
 
 def workspace_status(ws) -> int:
-    """Reads and clears the status word of a chunked workspace (0 = ok, 5 = a wait expired)."""
+    """Reads and clears the status word of a chunked or linear attention workspace (0 = ok, 5 = a wait expired)."""
     return int(lib().gdr_workspace_status(_ptr(ws), ctypes.c_size_t(ws.numel()), _stream(ws.device)))
 
 

@@ -83,8 +83,8 @@ gdr_status of(cudaError_t e) { return e == cudaSuccess ? GDR_OK : GDR_ERR_CUDA; 
 
 // The state that enters each segment, forwards (rows = v, cols = k) or in reverse (do, q).
 cudaError_t states(const LinearShape& s, const void* rows, const void* cols, float factor, int reverse,
-                   const float* init, float* z, float* last, cudaStream_t st) {
-    LinearSummaryArgs a{s, rows, cols, factor, reverse, z};
+                   const float* init, float* z, float* last, int* clear, cudaStream_t st) {
+    LinearSummaryArgs a{s, rows, cols, factor, reverse, z, clear};
     if (cudaError_t e = launch_linear_summary(a, st)) return e;
     LinearCombineArgs c{s, init, reverse, z, last};
     return launch_linear_combine(c, true, st);
@@ -95,16 +95,17 @@ cudaError_t states(const LinearShape& s, const void* rows, const void* cols, flo
 cudaError_t mix_tc(const LinearMixArgs& m, const void* rows, const void* cols, float factor, int reverse,
                    const float* init, float* z, float* last, int* status, bool clear, cudaStream_t st) {
     if (m.s.nseg == 1) return launch_linear_tc_mix(m, init, 1, last, status, clear, false, st);
-    LinearSummaryArgs a{m.s, rows, cols, factor, reverse, z};
+    LinearSummaryArgs a{m.s, rows, cols, factor, reverse, z, nullptr};
     if (cudaError_t e = launch_linear_tc_summary(a, last != nullptr, status, clear, st)) return e;
     LinearCombineArgs c{m.s, init, reverse, z, last};
     if (cudaError_t e = launch_linear_combine(c, true, st)) return e;
     return launch_linear_tc_mix(m, z, m.s.nseg, nullptr, status, false, true, st);
 }
 
-// No token: the state passes through.
-gdr_status pass_state(const gdr_linear_problem* p, const float* from, float* to, cudaStream_t st) {
-    if (!to) return GDR_OK;
+// No token or no sequence: nothing can fail, and the state passes through.
+gdr_status pass_state(const gdr_linear_problem* p, const float* from, float* to, void* status, cudaStream_t st) {
+    if (cudaMemsetAsync(status, 0, 256, st) != cudaSuccess) return GDR_ERR_CUDA;
+    if (p->B == 0 || !to) return GDR_OK;
     const size_t bytes = (size_t)p->B * p->Hv * p->Dv * p->Dk * sizeof(float);
     return of(from ? cudaMemcpyAsync(to, from, bytes, cudaMemcpyDeviceToDevice, st) : cudaMemsetAsync(to, 0, bytes, st));
 }
@@ -177,13 +178,13 @@ static gdr_status linear_fwd_impl(const gdr_linear_problem* p, const void* q, co
     const LinearShape s = shape_of(p, g, lengths);
     if (keep && (r = check_kept(kept, have, s)) != GDR_OK) return r;
     if ((r = check_ws(ws, ws_bytes, fwd_bytes(s))) != GDR_OK) return r;
-    if (p->B == 0) return GDR_OK;
-    if (p->T == 0) return pass_state(p, h0, ht, st);
+    if (empty) return pass_state(p, h0, ht, ws, st);
+    int* status = static_cast<int*>(ws);
     float* z = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256);
     LinearMixArgs m{s, LINEAR_O, q, k, v, nullptr, p->scale, z, o, h0, ht, keep ? kept : nullptr,
-                    s.nseg > 1};
-    if (s.bf16) return of(mix_tc(m, v, k, 1.f, 0, h0, z, ht, static_cast<int*>(ws), true, st));
-    if (s.nseg > 1 && states(s, v, k, 1.f, 0, h0, z, ht, st) != cudaSuccess) return GDR_ERR_CUDA;
+                    s.nseg > 1, s.nseg > 1 ? nullptr : status};
+    if (s.bf16) return of(mix_tc(m, v, k, 1.f, 0, h0, z, ht, status, true, st));
+    if (s.nseg > 1 && states(s, v, k, 1.f, 0, h0, z, ht, status, st) != cudaSuccess) return GDR_ERR_CUDA;
     return of(launch_linear_mix(m, st));
 }
 
@@ -199,34 +200,34 @@ static gdr_status linear_bwd_impl(const gdr_linear_problem* p, const void* q, co
     const LinearShape s = shape_of(p, g, lengths);
     if (keep && (r = check_kept(kept, have, s)) != GDR_OK) return r;
     if ((r = check_ws(ws, ws_bytes, bwd_bytes(s, keep))) != GDR_OK) return r;
-    if (p->B == 0) return GDR_OK;
-    if (p->T == 0) return pass_state(p, dht, dh0, st);
+    if (empty) return pass_state(p, dht, dh0, ws, st);
+    int* status = static_cast<int*>(ws);
     uint8_t* w = static_cast<uint8_t*>(ws) + 256;
     float* z = reinterpret_cast<float*>(w);
     if (s.bf16) {
-        int* status = static_cast<int*>(ws);
         uint8_t* adjoints = w + states_bytes(s);
         if (!keep) {  // the chunks' states, formed again
             uint8_t* again = adjoints + kept_bytes(s);
-            LinearMixArgs m{s, LINEAR_O, q, k, v, nullptr, p->scale, z, again + kept_bytes(s), nullptr, nullptr, again, false};
+            LinearMixArgs m{s, LINEAR_O, q, k, v, nullptr, p->scale, z, again + kept_bytes(s), nullptr, nullptr, again, false, nullptr};
             if (mix_tc(m, v, k, 1.f, 0, h0, z, nullptr, status, true, st) != cudaSuccess) return GDR_ERR_CUDA;
             kept = again;
         }
-        LinearMixArgs m{s, LINEAR_DV, q, k, v, do_, p->scale, z, dv, nullptr, nullptr, adjoints, false};
+        LinearMixArgs m{s, LINEAR_DV, q, k, v, do_, p->scale, z, dv, nullptr, nullptr, adjoints, false, nullptr};
         if (mix_tc(m, do_, q, p->scale, 1, dht, z, dh0, status, keep, st) != cudaSuccess) return GDR_ERR_CUDA;
         LinearGradArgs a{s, q, k, v, do_, p->scale, kept, adjoints, dq, dk, status};
         return of(launch_linear_tc_grad(a, st));
     }
     float* zd = reinterpret_cast<float*>(w + states_bytes(s));
     if (s.nseg > 1) {
-        if (states(s, v, k, 1.f, 0, h0, z, nullptr, st) != cudaSuccess) return GDR_ERR_CUDA;
-        if (states(s, do_, q, p->scale, 1, dht, zd, dh0, st) != cudaSuccess) return GDR_ERR_CUDA;
+        if (states(s, v, k, 1.f, 0, h0, z, nullptr, status, st) != cudaSuccess) return GDR_ERR_CUDA;
+        if (states(s, do_, q, p->scale, 1, dht, zd, dh0, nullptr, st) != cudaSuccess) return GDR_ERR_CUDA;
     }
     // dv reads the reverse states, which dk, summing over value heads, may update in place: dv first
     const struct { int pass; float* z; void* out; const float* init; float* last; } passes[3] = {
         {LINEAR_DQ, z, dq, h0, nullptr}, {LINEAR_DV, zd, dv, dht, dh0}, {LINEAR_DK, zd, dk, dht, nullptr}};
     for (const auto& x : passes) {
-        LinearMixArgs m{s, x.pass, q, k, v, do_, p->scale, x.z, x.out, x.init, x.last, nullptr, false};
+        LinearMixArgs m{s, x.pass, q, k, v, do_, p->scale, x.z, x.out, x.init, x.last, nullptr, false,
+                        s.nseg == 1 && x.pass == LINEAR_DQ ? status : nullptr};
         if (launch_linear_mix(m, st) != cudaSuccess) return GDR_ERR_CUDA;
     }
     return GDR_OK;

@@ -37,6 +37,12 @@ __device__ __forceinline__ int valid_tokens(const LinearShape& s, int b) {
     return s.lengths ? min(max(s.lengths[b], 0), s.T) : s.T;
 }
 
+// Clears the status word of a call, from one of the blocks of its first kernel. (No wait of the fp32 kernels
+// is one that could expire, so nothing else is ever written there.)
+__device__ __forceinline__ void clear_status(int* status) {
+    if (status && threadIdx.x < 4 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) status[threadIdx.x] = 0;
+}
+
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
 
@@ -130,6 +136,7 @@ __global__ void __launch_bounds__(256) linear_summary_kernel(LinearSummaryArgs a
         fetch_tile<DK>(X + XS, cols, t0, (size_t)s.Hk * s.Dk, 0, m, a.reverse);
     };
     linear::next_kernel_may_start();
+    clear_status(a.clear);
     float z[TR][TC] = {};
     fetch(0);
     for (int i = 0; i < nc; i++) {
@@ -321,6 +328,7 @@ __global__ void __launch_bounds__(256, 2) linear_mix_kernel(LinearMixArgs args, 
     };
     fetch(0, false);
     fetch(0, true);
+    clear_status(args.clear);
     linear::wait_kernel_before();  // the states, and what the outputs' memory held
     for (int i = threadIdx.x; i < (end - max(begin, n)) * (CS / 4); i += 256)  // past the length: zero
         store4(out + (size_t)(max(begin, n) + i / (CS / 4)) * out_stride + 4 * (i % (CS / 4)),

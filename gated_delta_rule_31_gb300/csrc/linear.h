@@ -33,6 +33,7 @@ struct LinearSummaryArgs {
     float factor;      // 1, or scale in reverse
     int reverse;
     float* z;  // [B, Hv, nseg, Dv, Dk]
+    int* clear;  // fp32: the call's status word, which its first kernel clears, or null
 };
 
 // z -> the state entering each segment (in place), and the state after all of them (with last null
@@ -60,6 +61,7 @@ struct LinearMixArgs {
                     // the one it ends in) is kept there as a swizzled bf16 tile, 32 KB for each
                     // (b, hv, chunk), for launch_linear_tc_grad; or null
     bool overlap;   // fp32: the kernel before it on the stream is the combine step of its call (launch_after)
+    int* clear;     // fp32: as LinearSummaryArgs
 };
 
 // A launch that, with `overlap`, may begin while the kernel before it on the stream still runs; that kernel

@@ -198,7 +198,7 @@ gdr_status gdr_decode_step(const gdr_problem* p, const void* q, const void* k, c
                            gdr_stream_t stream);
 
 /* Reads (synchronising on `stream`) and clears the workspace status word written by the
- * chunked kernels: GDR_OK, or GDR_ERR_TIMEOUT if a bounded wait expired. */
+ * chunked and the linear attention calls: GDR_OK, or GDR_ERR_TIMEOUT if a bounded wait expired. */
 gdr_status gdr_workspace_status(void* ws, size_t ws_bytes, gdr_stream_t stream);
 
 /* Check of the library's own failure handling (not an operation of the gated delta rule):
@@ -263,7 +263,9 @@ typedef struct {
 } gdr_linear_problem;
 
 /* Forward over T tokens: o and, if ht != NULL, the state after them. h0 may be NULL (zero).
- * Workspace: gdr_linear_fwd_workspace() bytes, 256-byte aligned (0: invalid problem).
+ * Workspace: gdr_linear_fwd_workspace() bytes, 256-byte aligned (0: invalid problem). As with the
+ * chunked calls its first 256 bytes hold the status word, which this call and those of the VJP
+ * clear and then set, and gdr_workspace_status() reads: the bf16 kernels bound every wait.
  * Pointers 16-byte aligned (g and lengths: 4). */
 size_t gdr_linear_fwd_workspace(const gdr_linear_problem* p);
 gdr_status gdr_linear_fwd(const gdr_linear_problem* p, const void* q, const void* k, const void* v, const float* g,
