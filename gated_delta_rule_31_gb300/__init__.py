@@ -141,6 +141,13 @@ def _stream(device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _written(*tensors):
+    """Tells autograd that a call wrote these tensors of the caller's: a graph that saved one refuses its backward."""
+    for t in tensors:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
+
+
 def _need(t, name, dtype=None, device=None, shape=None):
     if t is None:
         raise ValueError(f"{name} is required")
@@ -332,6 +339,7 @@ def decode_step(q, k, v, g, beta, state, scale=None, use_qk_l2norm=True, out=Non
     o = out if out is not None else torch.empty(v.shape, dtype=v.dtype, device=v.device)
     _check(lib().gdr_decode_step(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state),
                                  _ptr(o), _stream(q.device)))
+    _written(state, out)
     return o
 
 
@@ -454,13 +462,13 @@ def linear_decode_step(q, k, v, g, state, scale=None, out=None):
     state [B,Hv,Dv,Dk] fp32 updated in place. Returns o [B,Hv,Dv]."""
     at, _, dev, shape = _linear_problem(q, k, v, g, scale, True)
     _is(state, "state", torch.float32, dev, shape)
-    if out is None:
-        out = torch.empty_like(v)
-    else:
+    o = torch.empty_like(v) if out is None else out
+    if out is not None:
         _is(out, "out", v.dtype, dev, v.shape)
     _check(lib().gdr_linear_decode_step(at, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), state.data_ptr(),
-                                        out.data_ptr(), _raw_stream(dev)))
-    return out
+                                        o.data_ptr(), _raw_stream(dev)))
+    _written(state, out)
+    return o
 
 
 @functools.lru_cache(maxsize=1024)
@@ -500,13 +508,13 @@ def group_norm_fwd(x, groups, weight=None, bias=None, gate=None, activation="non
     fp32 or None; activation "none", "silu" or "sigmoid"; center=False leaves the mean in (the
     root-mean-square form). Returns y in x's dtype; `out` may be x or gate themselves."""
     at, _, dev = _norm_problem(x, groups, weight, bias, gate, activation, eps, center)
-    if out is None:
-        out = torch.empty_like(x)
-    else:
+    y = torch.empty_like(x) if out is None else out
+    if out is not None:
         _is(out, "out", x.dtype, dev, x.shape)
-    _check(lib().gdr_group_norm_fwd(at, x.data_ptr(), _at(gate), _at(weight), _at(bias), out.data_ptr(),
+    _check(lib().gdr_group_norm_fwd(at, x.data_ptr(), _at(gate), _at(weight), _at(bias), y.data_ptr(),
                                     _raw_stream(dev)))
-    return out
+    _written(out)
+    return y
 
 
 def group_norm_bwd(x, groups, weight, bias, gate, dy, activation="none", eps=1e-5, center=True, workspace=None):
