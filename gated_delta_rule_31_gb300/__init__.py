@@ -398,10 +398,9 @@ def _linear_extras(dev, state, h0, lengths):
 
 
 def _scratch(nbytes, device, workspace):
-    """The caller's workspace after checking it, else a new buffer; no size means an unsupported problem."""
-    if nbytes == 0:
-        _check(GDR_ERR_UNSUPPORTED)
-    if workspace is None:
+    """The caller's workspace after checking it, else a new buffer: an empty one for a problem without a
+    size, which the call itself refuses with the status that says why."""
+    if workspace is None or nbytes == 0:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
     _need(workspace, "workspace", device=device)
     if workspace.numel() * workspace.element_size() < nbytes:
