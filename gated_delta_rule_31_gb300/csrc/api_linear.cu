@@ -29,6 +29,8 @@ gdr_status check_problem(const gdr_linear_problem* p, bool decode) {
     if (!dim_ok(p->Dk) || !dim_ok(p->Dv)) return GDR_ERR_UNSUPPORTED;
     if (p->B > 65535 || p->Hv > 65535) return GDR_ERR_UNSUPPORTED;  // grid y/z limits
     if ((long long)p->B * p->Hv * p->Dv >= 1LL << 32) return GDR_ERR_UNSUPPORTED;  // a state of 512 GB or more
+    // Positions past the end of a sequence, by less than a block of tokens for each of up to 1216 segments, are ints.
+    if (p->T > GDR_LINEAR_MAX_T) return GDR_ERR_UNSUPPORTED;
     return GDR_OK;
 }
 

@@ -256,8 +256,11 @@ gdr_status gdr_noalloc_status(gdr_stream_t stream);
  * o, dq, dk, dv are zero there, ht is the state after the last token and dht its adjoint.
  * As in any blocked form a value that is not finite spreads within its block: a non-finite q, k,
  * v or do may reach earlier outputs of the same 128 tokens. */
+#define GDR_LINEAR_MAX_T 0x7ff00000 /* 2^31 - 2^20 */
+
 typedef struct {
-    int B, T, Hk, Hv, Dk, Dv; /* Hv % Hk == 0; T >= 0 (T == 1 for the decode step); Dk, Dv in {32, 64, 128} */
+    int B, T, Hk, Hv, Dk, Dv; /* Hv % Hk == 0; 0 <= T <= GDR_LINEAR_MAX_T (T == 1 for the decode step);
+                                 Dk, Dv in {32, 64, 128} */
     gdr_dtype dtype;
     float scale;
 } gdr_linear_problem;
