@@ -121,6 +121,7 @@ gdr_status check_norm(const gdr_norm_problem* p) {
     if (p->center != 0 && p->center != 1) return GDR_ERR_INVALID_ARG;
     if (!isfinite(p->eps) || p->eps <= 0.f) return GDR_ERR_INVALID_ARG;
     if (p->D > GDR_NORM_MAX_D || (long long)p->groups * p->D > (1 << 24)) return GDR_ERR_UNSUPPORTED;
+    if (p->rows > (1LL << 60) / (p->groups * p->D)) return GDR_ERR_UNSUPPORTED;  // sizes in bytes are 64-bit
     return GDR_OK;
 }
 

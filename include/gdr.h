@@ -319,7 +319,7 @@ typedef enum { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1, GDR_ACT_SIGMOID = 2 } gdr_act
 #define GDR_NORM_MAX_D 8192 /* largest group; groups * D is at most 2^24 */
 
 typedef struct {
-    long long rows; /* >= 0 */
+    long long rows; /* >= 0; rows * groups * D is at most 2^60 */
     int groups, D;
     gdr_dtype dtype;
     gdr_activation activation;

@@ -39,3 +39,15 @@ def test_as_many_tokens_as_there_can_be(L, T, heads):
     assert segments % (heads * 65536) == 0 and 1 <= segments // (heads * 65536) <= 1216
     assert kept == 256 + segments + chunks * heads * 32768
     assert both == kept + chunks * heads * 32768 + T * heads * 256
+
+
+@pytest.mark.parametrize("rows,groups,D", [(2 ** 63 - 1, 1, 1), (2 ** 63 - 1, 2, 64), (2 ** 60 + 1, 1, 1), (2 ** 53 + 1, 2, 64)])
+def test_too_many_rows(L, rows, groups, D):
+    p = ctypes.byref(NormProblem(rows, groups, D, 1, 1, 1, 1e-5))
+    assert L.gdr_group_norm_bwd_workspace(p) == 0
+    assert L.gdr_group_norm_fwd(p, *[FAKE] * 5, None) == UNSUPPORTED
+    assert L.gdr_group_norm_bwd(p, *[FAKE] * 9, FAKE, BIG, None) == UNSUPPORTED
+
+
+def test_many_rows(L):
+    assert 256 < L.gdr_group_norm_bwd_workspace(ctypes.byref(NormProblem(2 ** 40, 2, 64, 1, 1, 1, 1e-5))) < 2 ** 24
