@@ -336,6 +336,8 @@ def decode_step(q, k, v, g, beta, state, scale=None, use_qk_l2norm=True, out=Non
     _check_inputs(q, k, v, g, beta)
     p = _problem(q, v, g, scale, use_qk_l2norm)
     _need(state, "state", dtype=torch.float32, device=q.device, shape=(p.B, p.Hv, p.Dv, p.Dk))
+    if out is not None:
+        _need(out, "out", dtype=v.dtype, device=v.device, shape=v.shape)
     o = out if out is not None else torch.empty(v.shape, dtype=v.dtype, device=v.device)
     _check(lib().gdr_decode_step(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state),
                                  _ptr(o), _stream(q.device)))

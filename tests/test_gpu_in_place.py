@@ -61,6 +61,16 @@ def test_norm(which):
     refuses(y)
 
 
+@pytest.mark.parametrize("step", [delta_step, linear_step])
+def test_out_is_checked(step):
+    state = randn(2, 2, 64, 64)
+    want = state.clone()
+    for out in (randn(2, 2, 32), randn(1, 2, 64), randn(2, 2, 64, dtype=torch.bfloat16), randn(2, 2, 64, 2)[..., 0], torch.zeros(2, 2, 64)):
+        with pytest.raises(ValueError, match="out"):
+            step(state, out=out)
+    assert torch.equal(state, want)
+
+
 def test_inference_tensors():
     """Tensors made in inference mode have no version to raise, inside it or outside."""
     with torch.inference_mode():
