@@ -11,7 +11,8 @@
 // with do, v as [tokens, Dv] and S, D as [Dv, Dk]. A CTA owns one (b, key head, chunk), so
 // the sum over value heads needs no atomics and its order is fixed: the P' products accumulate
 // over the heads in TMEM, the state products, which every row scales by its own decay, in fp32
-// registers. Rounding to bf16: P', the kept states and the results.
+// registers. Rounding to bf16: P', the kept states (operands of the products; the states themselves are
+// carried in fp32 by the passes that keep these copies) and the results, one rounding each.
 //
 // HBM bounds it: per value head do, v and the two states (128 KB), per key head q, k, dq, dk. One CTA per
 // SM takes the (b, chunk, key head) units in turn, key heads fastest, so that the CTAs at work read

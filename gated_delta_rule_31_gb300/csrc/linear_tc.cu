@@ -13,8 +13,10 @@
 //     S <- l^m S + c'^T b, c'_j = f'' l^(m-1-j) c_j (reverse: l^(j+1))    Dv x Dk x 128
 //
 // All four run as tcgen05 products with 128 rows. Rounding to bf16: P' (an operand kept in TMEM), the copy
-// of S that X reads, and the result, one rounding each. c' would be a fourth, so it enters as the
-// sum of bf16 terms: two (2^-17 off, below the other roundings) where the state only feeds X,
+// of S that X reads, and the result, one rounding each: the products take bf16 operands, and a second
+// term of either would need as many products again and, for S, 32 KB of shared memory that the tiles
+// have. (Error of o, relative to its norm: 0.0023; the result's rounding alone 0.0017.) c' would be a fourth, so
+// it enters as the sum of bf16 terms: two (2^-17 off, below the other roundings) where the state only feeds X,
 // three (the 24 bits of an fp32 product) where it is returned in fp32. Each chunk's sum starts from zero in TMEM
 // and is added to the fp32 registers there, so the tensor core's own accumulation never runs over more than
 // one chunk. X is scaled by its rows' decays in TMEM and Y accumulates onto it.
@@ -628,8 +630,8 @@ cudaError_t launch_linear_tc_summary(const LinearSummaryArgs& x, bool all, int* 
 cudaError_t launch_linear_tc_mix(const LinearMixArgs& x, const float* start, int start_segs, float* last, int* status,
                                  bool clear, bool overlap, cudaStream_t st) {
     const bool rev = x.pass == LINEAR_DV;
-    // One segment carries the state that leaves the call, with four terms (also where the caller does not
-    // want it, so that the kept states are the same); with several it comes from the summary.
+    // One segment carries the state that leaves the call, with three terms (also where the caller does not
+    // want it, so that the kept states are the same); with several it comes from the summary, with three too.
     const bool one = x.s.nseg == 1;
     if (cudaError_t e = one ? allow_smem<true, 3>() : allow_smem<true, 2>()) return e;
     CUtensorMap maps[4];

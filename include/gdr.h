@@ -249,8 +249,13 @@ gdr_status gdr_noalloc_status(gdr_stream_t stream);
  *
  * Layouts as above (q, k [B,T,Hk,Dk], v, o, do [B,T,Hv,Dv] of `dtype`, states [B,Hv,Dv,Dk] fp32),
  * with g [Hv] fp32, the log-decay, g <= 0 (l = 0 for g = -infinity). The gradients dq, dk, dv are
- * of `dtype`, each rounded once from fp32 sums (dq, dk over the value heads of their key head);
- * the decay is not learned and has no gradient.
+ * of `dtype` (dq, dk summed over the value heads of their key head); the decay is not learned and
+ * has no gradient.
+ * Rounding: sums and states are fp32, ht and dh0 to fp32's precision. With F32 nothing is rounded to
+ * less. With BF16 each of o, dq, dk, dv is rounded once, and so are, as operands of the tensor cores, the
+ * weights between tokens of a 128-token chunk and the state (or its adjoint) at its start: three
+ * roundings of about 2^-9 in all (o off by 0.0023 of its norm, 0.0017 of that by its own). The
+ * decode step rounds o alone.
  * `lengths` [B] int32 (device memory, or NULL: T everywhere; read clamped to [0, T]): batch entry
  * b has lengths[b] tokens. What lies past them is never used, not even where it is not finite:
  * o, dq, dk, dv are zero there, ht is the state after the last token and dht its adjoint.
@@ -284,7 +289,7 @@ gdr_status gdr_linear_bwd(const gdr_linear_problem* p, const void* q, const void
 
 /* Saved-state handoff: the forward keeps the state that each 128-token chunk starts from, in the bf16 that
  * its own output reads (opaque layout, gdr_linear_states_bytes() bytes: 32 KB for each (b, hv,
- * chunk) of a BF16 problem, 0 for F32, whose backward keeps to gdr_linear_bwd's work; caller-owned, 256-byte
+ * chunk) of a BF16 problem, whatever the head sizes, 0 for F32, whose backward keeps to gdr_linear_bwd's work; caller-owned, 256-byte
  * aligned), and the backward of the same inputs reads them instead of forming them again; its h0
  * is then not needed by BF16. Results are those of the calls without it, bit for bit. */
 size_t gdr_linear_states_bytes(const gdr_linear_problem* p);
