@@ -92,10 +92,11 @@ __device__ __forceinline__ uint32_t bf16x2_neg(uint32_t a) {
 }
 
 // Programmatic dependent launch: a kernel lets the next one on the stream begin at once, and one launched to
-// do so (launch_after) waits for the kernel before it ahead of the first access to what any kernel of the
-// same call reads or writes. A call's first kernel starts when all work before the call is complete, so its
-// kernels may read the call's inputs before they wait; the decode steps, each a call's only kernel, wait
-// first of all. What follows a call can begin early as well, so that rule binds every kernel of the library.
+// do so (launch_after) waits for the kernel before it ahead of its first access to memory that another kernel
+// of the same call writes, or reads and it writes. A call's first kernel starts when all work before the call is
+// complete, so its kernels may read the call's inputs, and write outputs that are theirs alone, before they
+// wait; the decode steps, each a call's only kernel, wait first of all. What follows a call can begin
+// early as well, so whatever kernel is launched that way as a call's first has to wait first of all.
 __device__ __forceinline__ void next_kernel_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
