@@ -25,7 +25,8 @@ from ._build import build
 __all__ = ["build", "fwd_chunked", "bwd_chunked", "fwd_sequential", "bwd_sequential", "decode_step", "GdrError",
            "fwd_workspace_bytes", "bwd_workspace_bytes", "lib", "Problem", "workspace_status", "selftest_wait_expiry", "trace",
            "LinearProblem", "NormProblem", "linear_fwd", "linear_bwd", "linear_decode_step", "group_norm_fwd",
-           "group_norm_bwd"]
+           "group_norm_bwd", "WindowProblem", "RotaryProblem", "AppendProblem", "PagedProblem", "window_attention_fwd",
+           "window_attention_bwd", "rotary", "kv_append", "paged_decode_step"]
 
 GDR_F32, GDR_BF16 = 0, 1
 GDR_GATE_SCALAR, GDR_GATE_CHANNEL = 0, 1
@@ -47,6 +48,29 @@ class LinearProblem(ctypes.Structure):
 class NormProblem(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_longlong), ("groups", ctypes.c_int), ("D", ctypes.c_int), ("dtype", ctypes.c_int),
                 ("activation", ctypes.c_int), ("center", ctypes.c_int), ("eps", ctypes.c_float)]
+
+
+class WindowProblem(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("Hq", ctypes.c_int), ("Hk", ctypes.c_int), ("D", ctypes.c_int),
+                ("window", ctypes.c_int), ("sinks", ctypes.c_int), ("dtype", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class RotaryProblem(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int), ("D", ctypes.c_int), ("pairs", ctypes.c_int),
+                ("axes", ctypes.c_int), ("sections", ctypes.c_int * 4), ("interleaved", ctypes.c_int),
+                ("inverse", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+class AppendProblem(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("Hq", ctypes.c_int), ("Hk", ctypes.c_int), ("D", ctypes.c_int),
+                ("pages", ctypes.c_int), ("page_size", ctypes.c_int), ("table_pages", ctypes.c_int), ("pairs", ctypes.c_int),
+                ("axes", ctypes.c_int), ("sections", ctypes.c_int * 4), ("interleaved", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+class PagedProblem(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hk", ctypes.c_int), ("D", ctypes.c_int),
+                ("pages", ctypes.c_int), ("page_size", ctypes.c_int), ("table_pages", ctypes.c_int),
+                ("window", ctypes.c_int), ("sinks", ctypes.c_int), ("dtype", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
 class GdrError(RuntimeError):
@@ -123,6 +147,17 @@ def lib():
         L.gdr_group_norm_bwd.argtypes = [PN] + [P] * 9 + [P, sz, st]
         for name in ("gdr_linear_fwd", "gdr_linear_bwd", "gdr_linear_fwd_states", "gdr_linear_bwd_states",
                      "gdr_linear_decode_step", "gdr_group_norm_fwd", "gdr_group_norm_bwd"):
+            getattr(L, name).restype = ctypes.c_int
+        PW, PR, PA, PG = (ctypes.POINTER(s) for s in (WindowProblem, RotaryProblem, AppendProblem, PagedProblem))
+        for name, at in (("gdr_window_fwd_workspace", PW), ("gdr_window_bwd_workspace", PW), ("gdr_paged_decode_workspace", PG)):
+            getattr(L, name).argtypes = [at]
+            getattr(L, name).restype = sz
+        L.gdr_window_fwd.argtypes = [PW] + [P] * 6 + [P, sz, st]
+        L.gdr_window_bwd.argtypes = [PW] + [P] * 10 + [P, sz, st]
+        L.gdr_rotary.argtypes = [PR] + [P] * 4 + [st]
+        L.gdr_kv_append.argtypes = [PA] + [P] * 11 + [st]
+        L.gdr_paged_decode_step.argtypes = [PG] + [P] * 6 + [P, sz, st]
+        for name in ("gdr_window_fwd", "gdr_window_bwd", "gdr_rotary", "gdr_kv_append", "gdr_paged_decode_step"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -533,8 +568,223 @@ def group_norm_bwd(x, groups, weight, bias, gate, dy, activation="none", eps=1e-
     return dict(dx=dx, dgate=dgate, dweight=dweight, dbias=dbias)
 
 
+# The softmax attention layers of a mixed model. As above, checks in one expression each and problems built once; the
+# calls run on their tensors' device, whichever is current.
+def _call(dev, f, *args):
+    if torch._C._cuda_getDevice() == dev.index:
+        _check(f(*args, _raw_stream(dev)))
+    else:
+        with torch.cuda.device(dev):
+            _check(f(*args, _raw_stream(dev)))
+
+
+def _int(x, name):
+    if not isinstance(x, int) or not 0 <= x < 2 ** 31:
+        raise ValueError(f"{name} must be an int of 0 or more (below 2^31), got {x!r}")
+    return int(x)
+
+
+@functools.lru_cache(maxsize=1024)
+def _window_spec(B, T, Hq, Hk, D, window, sinks, dtype, scale):
+    """(by-reference problem, bytes of the forward's and of the backward's workspace)."""
+    at, L = ctypes.byref(WindowProblem(B, T, Hq, Hk, D, window, sinks, dtype, scale)), lib()
+    return at, int(L.gdr_window_fwd_workspace(at)), int(L.gdr_window_bwd_workspace(at))
+
+
+def _window_problem(q, k, v, window, sinks, scale, lengths):
+    """Checks the inputs of a window attention call: (problem, its workspace sizes, device, shape of lse)."""
+    qs, ks, dev, dtype = q.shape, k.shape, q.device, q.dtype
+    if not (q.is_cuda and q.is_contiguous()):
+        _need(q, "q")
+    if len(qs) != 4 or len(ks) != 4:
+        raise ValueError("q and k must have 4 dimensions")
+    if dtype not in _DTYPES:
+        raise ValueError(f"q/k/v dtype must be float32 or bfloat16, got {dtype}")
+    B, T, Hq, D = qs
+    _is(k, "k", dtype, dev, (B, T, ks[2], D))
+    _is(v, "v", dtype, dev, ks)
+    if lengths is not None:
+        _is(lengths, "lengths", torch.int32, dev, (B,))
+    at, *sizes = _window_spec(B, T, Hq, ks[2], D, _int(window, "window"), _int(sinks, "sinks"), _DTYPES[dtype],
+                              D ** -0.5 if scale is None else float(scale))
+    return at, sizes, dev, (B, Hq, T)
+
+
+def window_attention_fwd(q, k, v, window=0, sinks=0, scale=None, lengths=None, save_lse=False, out=None, workspace=None):
+    """Causal softmax attention with a sliding window and visible first tokens (gdr_window_fwd): query t sees token
+    j <= t if t - j < window (0: any) or j < sinks. q [B,T,Hq,D] and k, v [B,T,Hk,D] bf16 or fp32, query head h with
+    key head h // (Hq / Hk); lengths [B] int32 (device) or None: entry b has lengths[b] tokens and o is zero past them.
+    scale defaults to D^-1/2. Returns (o, lse), lse [B,Hq,T] fp32 (the log of the softmax's sums) with
+    save_lse=True, else None."""
+    at, sizes, dev, rows = _window_problem(q, k, v, window, sinks, scale, lengths)
+    o = torch.empty_like(q) if out is None else out
+    if out is not None:
+        _is(out, "out", q.dtype, dev, q.shape)
+    lse = torch.empty(rows, dtype=torch.float32, device=dev) if save_lse else None
+    ws = _scratch(sizes[0], dev, workspace)
+    _call(dev, lib().gdr_window_fwd, at, q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(lengths), o.data_ptr(), _at(lse),
+          ws.data_ptr(), sizes[0])
+    _written(out)
+    return o, lse
+
+
+def window_attention_bwd(q, k, v, o, lse, do, window=0, sinks=0, scale=None, lengths=None, workspace=None):
+    """VJP of window_attention_fwd for the loss <do, o> (gdr_window_bwd), from its o and lse. Returns a dict of dq, dk, dv
+    in the inputs' dtype."""
+    at, sizes, dev, rows = _window_problem(q, k, v, window, sinks, scale, lengths)
+    _is(o, "o", q.dtype, dev, q.shape)
+    _is(lse, "lse", torch.float32, dev, rows)
+    _is(do, "do", q.dtype, dev, q.shape)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    ws = _scratch(sizes[1], dev, workspace)
+    _call(dev, lib().gdr_window_bwd, at, q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(lengths), o.data_ptr(), lse.data_ptr(),
+          do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), sizes[1])
+    return dict(dq=dq, dk=dk, dv=dv)
+
+
+def _sections(sections, pairs):
+    sections = (pairs,) if sections is None else tuple(sections)
+    if not 1 <= len(sections) <= 4 or any(_int(s, "a section") > pairs for s in sections) or sum(sections) != pairs:
+        raise ValueError(f"sections must be 1 to 4 numbers that sum to len(inv_freq) = {pairs}, got {sections}")
+    return sections
+
+
+@functools.lru_cache(maxsize=1024)
+def _rotary_spec(tokens, H, D, pairs, sections, interleaved, inverse, dtype):
+    return ctypes.byref(RotaryProblem(1, tokens, H, D, pairs, len(sections), (ctypes.c_int * 4)(*sections), interleaved,
+                                      inverse, dtype))
+
+
+def rotary(x, positions, inv_freq, sections=None, interleaved=False, inverse=False, out=None):
+    """Rotary positions, on several axes where there are sections (gdr_rotary): the first 2 R channels of x [..., H, D]
+    (bf16 or fp32), R = len(inv_freq), are turned by pairs, (i, i + R) or with interleaved=True (2 i, 2 i + 1), by the
+    angle position * inv_freq[i]. sections: how many pairs each axis has, in order (None: one axis for all); positions
+    int32 of x's leading shape, with a last dimension of the axes (which one axis may leave out); inv_freq [R] fp32. inverse=True turns
+    back (the VJP). Angles are exact at any position. Returns y in x's dtype; `out` may be x itself."""
+    shape, dev, dtype = x.shape, x.device, x.dtype
+    if not (x.is_cuda and x.is_contiguous()):
+        _need(x, "x")
+    if len(shape) < 2 or inv_freq.dim() != 1:
+        raise ValueError("x must have at least 2 dimensions (heads, channels) and inv_freq 1")
+    if dtype not in _DTYPES:
+        raise ValueError(f"x dtype must be float32 or bfloat16, got {dtype}")
+    pairs = inv_freq.shape[0]
+    _is(inv_freq, "inv_freq", torch.float32, dev, (pairs,))
+    sections = _sections(sections, pairs)
+    lead = shape[:-2]
+    _is(positions, "positions", torch.int32, dev, lead if len(sections) == 1 and positions.dim() == len(lead) else (*lead, len(sections)))
+    y = torch.empty_like(x) if out is None else out
+    if out is not None:
+        _is(out, "out", dtype, dev, shape)
+    at = _rotary_spec(lead.numel(), shape[-2], shape[-1], pairs, sections, int(bool(interleaved)), int(bool(inverse)), _DTYPES[dtype])
+    _call(dev, lib().gdr_rotary, at, x.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), y.data_ptr())
+    _written(out)
+    return y
+
+
+@functools.lru_cache(maxsize=1024)
+def _append_spec(B, T, Hq, Hk, D, pages, page_size, table_pages, pairs, sections, interleaved, dtype):
+    return ctypes.byref(AppendProblem(B, T, Hq, Hk, D, pages, page_size, table_pages, pairs, len(sections),
+                                      (ctypes.c_int * 4)(*sections), interleaved, dtype))
+
+
+def _cache(k_cache, v_cache, page_table, lengths, dtype, dev, B, Hk, D):
+    """Checks a paged cache: (pages, page size, pages of a table row)."""
+    cs, ts = k_cache.shape, page_table.shape
+    if len(cs) != 4 or len(ts) != 2:
+        raise ValueError("k_cache must have 4 dimensions and page_table 2")
+    _is(k_cache, "k_cache", dtype, dev, (cs[0], cs[1], Hk, D))
+    _is(v_cache, "v_cache", dtype, dev, cs)
+    _is(page_table, "page_table", torch.int32, dev, (B, ts[1]))
+    _is(lengths, "lengths", torch.int32, dev, (B,))
+    return cs[0], cs[1], ts[1]
+
+
+def kv_append(k, v, k_cache, v_cache, page_table, lengths, inv_freq=None, positions=None, sections=None, interleaved=False,
+              counts=None, q=None, q_out=None):
+    """Appends tokens to a paged cache, rotated on the way (gdr_kv_append). k, v [B,T,Hk,D] (or [B,Hk,D]: one token) bf16 or
+    fp32; k_cache, v_cache [pages,page_size,Hk,D]; token t < counts[b] (None: all) of entry b becomes token lengths[b] + t,
+    in page page_table[b, place // page_size] (int32; a number outside the cache is no page, nothing is written there).
+    inv_freq, sections, interleaved as in rotary (None: no rotation); positions [B,T] or [B,T,axes] int32, or None:
+    the place in the sequence. lengths and counts [B] int32 are not changed. Queries q [B,T,Hq,D] (or [B,Hq,D]) are
+    rotated along; returns them (in q_out where given, which may be q; zero past counts), or None without q."""
+    ks, dev, dtype = k.shape, k.device, k.dtype
+    if not (k.is_cuda and k.is_contiguous()):
+        _need(k, "k")
+    if len(ks) not in (3, 4):
+        raise ValueError("k must have 4 dimensions, or 3 for one token")
+    if dtype not in _DTYPES:
+        raise ValueError(f"q/k/v dtype must be float32 or bfloat16, got {dtype}")
+    lead, (Hk, D) = ks[:-2], ks[-2:]
+    B, T = lead if len(lead) == 2 else (lead[0], 1)
+    _is(v, "v", dtype, dev, ks)
+    sizes = _cache(k_cache, v_cache, page_table, lengths, dtype, dev, B, Hk, D)
+    if counts is not None:
+        _is(counts, "counts", torch.int32, dev, (B,))
+    pairs = 0
+    if inv_freq is not None:
+        pairs = inv_freq.numel()
+        _is(inv_freq, "inv_freq", torch.float32, dev, (pairs,))
+    sections = _sections(sections, pairs)
+    if positions is not None:
+        if inv_freq is None:
+            raise ValueError("positions without inv_freq")
+        _is(positions, "positions", torch.int32, dev, lead if len(sections) == 1 and positions.dim() == len(lead) else (*lead, len(sections)))
+    elif len(sections) > 1:
+        raise ValueError("several axes need positions")
+    Hq, y = 0, None
+    if q is not None:
+        if q.dim() != len(ks):
+            raise ValueError(f"q must have {len(ks)} dimensions, as k")
+        Hq = q.shape[-2]
+        _is(q, "q", dtype, dev, (*lead, Hq, D))
+        y = torch.empty_like(q) if q_out is None else q_out
+        if q_out is not None:
+            _is(q_out, "q_out", dtype, dev, q.shape)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    at = _append_spec(B, T, Hq, Hk, D, *sizes, pairs, sections, int(bool(interleaved)), _DTYPES[dtype])
+    _call(dev, lib().gdr_kv_append, at, _at(q), k.data_ptr(), v.data_ptr(), _at(positions), _at(inv_freq), lengths.data_ptr(),
+          _at(counts), page_table.data_ptr(), _at(y), k_cache.data_ptr(), v_cache.data_ptr())
+    _written(k_cache, v_cache, q_out)
+    return y
+
+
+@functools.lru_cache(maxsize=1024)
+def _paged_spec(B, Hq, Hk, D, pages, page_size, table_pages, window, sinks, dtype, scale):
+    """(by-reference problem, bytes of its workspace)."""
+    at = ctypes.byref(PagedProblem(B, Hq, Hk, D, pages, page_size, table_pages, window, sinks, dtype, scale))
+    return at, int(lib().gdr_paged_decode_workspace(at))
+
+
+def paged_decode_step(q, k_cache, v_cache, page_table, lengths, window=0, sinks=0, scale=None, out=None, workspace=None):
+    """Attention of one token of each sequence over a paged cache (gdr_paged_decode_step): q [B,Hq,D] bf16 or fp32 is the
+    query of token lengths[b] - 1, the last one in the cache (kv_append, then lengths + 1). k_cache, v_cache
+    [pages,page_size,Hk,D], page_table [B,pages of a row] int32, lengths [B] int32; window and sinks as in
+    window_attention_fwd. scale defaults to D^-1/2. Returns o [B,Hq,D], zero for an empty sequence."""
+    qs, dev, dtype = q.shape, q.device, q.dtype
+    if not (q.is_cuda and q.is_contiguous()):
+        _need(q, "q")
+    if len(qs) != 3:
+        raise ValueError("q must have 3 dimensions")
+    if dtype not in _DTYPES:
+        raise ValueError(f"q dtype must be float32 or bfloat16, got {dtype}")
+    B, Hq, D = qs
+    sizes = _cache(k_cache, v_cache, page_table, lengths, dtype, dev, B, k_cache.shape[-2] if k_cache.dim() > 1 else 0, D)
+    o = torch.empty_like(q) if out is None else out
+    if out is not None:
+        _is(out, "out", dtype, dev, qs)
+    at, nbytes = _paged_spec(B, Hq, k_cache.shape[2], D, *sizes, _int(window, "window"), _int(sinks, "sinks"), _DTYPES[dtype],
+                             D ** -0.5 if scale is None else float(scale))
+    ws = _scratch(nbytes, dev, workspace)
+    _call(dev, lib().gdr_paged_decode_step, at, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
+          lengths.data_ptr(), o.data_ptr(), ws.data_ptr(), nbytes)
+    _written(out)
+    return o
+
+
 def workspace_status(ws) -> int:
-    """Reads and clears the status word of a chunked or linear attention workspace (0 = ok, 5 = a wait expired)."""
+    """Reads and clears the status word of a chunked, linear or window attention workspace (0 = ok, 5 = a wait expired)."""
     return int(lib().gdr_workspace_status(_ptr(ws), ctypes.c_size_t(ws.numel()), _stream(ws.device)))
 
 

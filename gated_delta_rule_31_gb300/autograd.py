@@ -22,10 +22,11 @@ from __future__ import annotations
 
 import torch
 
-from . import bwd_chunked, fwd_chunked, group_norm_bwd, group_norm_fwd, linear_bwd, linear_fwd
+from . import (bwd_chunked, fwd_chunked, group_norm_bwd, group_norm_fwd, linear_bwd, linear_fwd, rotary as _rotary,
+               window_attention_bwd, window_attention_fwd)
 
 __all__ = ["gated_delta_rule", "GatedDeltaRuleFunction", "linear_attention", "LinearAttentionFunction", "group_norm",
-           "GroupNormFunction"]
+           "GroupNormFunction", "window_attention", "WindowAttentionFunction", "rotary", "RotaryFunction"]
 
 
 class GatedDeltaRuleFunction(torch.autograd.Function):
@@ -123,3 +124,49 @@ def group_norm(x, groups, weight=None, bias=None, gate=None, activation="none", 
     """Differentiable group norm over the channels of each token, in x, weight, bias and gate.
     Arguments as gated_delta_rule_31_gb300.group_norm_fwd."""
     return GroupNormFunction.apply(x, groups, weight, bias, gate, activation, float(eps), bool(center))
+
+
+class WindowAttentionFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, window, sinks, scale, lengths):
+        ctx.kw = dict(window=window, sinks=sinks, scale=scale)
+        keep = any(ctx.needs_input_grad)
+        o, lse = window_attention_fwd(q, k, v, lengths=lengths, save_lse=keep, **ctx.kw)
+        if keep:
+            ctx.save_for_backward(q, k, v, o, lse, lengths)
+        return o
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, do):
+        q, k, v, o, lse, lengths = ctx.saved_tensors
+        gr = window_attention_bwd(q, k, v, o, lse, do.to(q.dtype).contiguous(), lengths=lengths, **ctx.kw)
+        return gr["dq"], gr["dk"], gr["dv"], None, None, None, None
+
+
+def window_attention(q, k, v, window=0, sinks=0, scale=None, lengths=None):
+    """Differentiable causal softmax attention with a sliding window and visible first tokens, in q, k and v (their
+    gradients in the inputs' dtype): o [B,T,Hq,D]. Arguments as gated_delta_rule_31_gb300.window_attention_fwd."""
+    return WindowAttentionFunction.apply(q, k, v, window, sinks, None if scale is None else float(scale), lengths)
+
+
+class RotaryFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, positions, inv_freq, sections, interleaved):
+        ctx.kw = dict(sections=sections, interleaved=interleaved)
+        ctx.save_for_backward(positions, inv_freq)
+        return _rotary(x, positions, inv_freq, **ctx.kw)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        positions, inv_freq = ctx.saved_tensors
+        return _rotary(dy.contiguous(), positions, inv_freq, inverse=True, **ctx.kw), None, None, None, None
+
+
+def rotary(x, positions, inv_freq, sections=None, interleaved=False):
+    """Differentiable rotary positions, in x. Arguments as gated_delta_rule_31_gb300.rotary; the frequencies are constants,
+    and ones that require a gradient are refused."""
+    if inv_freq.requires_grad:
+        raise ValueError("inv_freq is constant and has no gradient: pass it detached")
+    return RotaryFunction.apply(x, positions, inv_freq, sections, bool(interleaved))

@@ -1,0 +1,191 @@
+// turn.cu - rotary positions on several axes (gdr_rotary) and the append of keys and values to a paged cache with the
+// rotation on the way (gdr_kv_append).
+//
+// Pair i of a head's first 2 pairs channels, (x_i, x_{i + pairs}) or (x_2i, x_2i+1) if interleaved, is turned by the angle
+// p f, p the token's position on the pair's axis and f = inv_freq[i]; the other channels are copied.
+//
+// The angle: p f in fp32 would be off by half a radian at p = 2^22, and fp64 is slow here, so f is taken as a
+// fixed-point fraction of a turn of 64 bits, F = f / 2 pi * 2^64 mod 2^64, and p F mod 2^64 in integers is the angle as a
+// fraction of a turn, off by at most |p| 2^-62 of a turn for |f| <= 1 (and f times that above). Its upper 32 bits, signed, are
+// in [-1/2, 1/2] turns, for sincospif.
+//
+// Bound by HBM: every element is read and written once. A thread takes two vectors of a token (8 pairs of bf16), forms
+// their sines once and goes over up to HEADS heads with all loads in flight.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "attention.h"
+#include "common.cuh"
+#include "kernels.h"
+
+namespace gdr {
+
+namespace {
+
+constexpr int HEADS = 4, THREADS = 128;
+
+template <int BYTES>
+struct Raw;
+template <>
+struct Raw<2> { using type = uint16_t; };
+template <>
+struct Raw<4> { using type = uint32_t; };
+template <>
+struct Raw<8> { using type = uint2; };
+template <>
+struct Raw<16> { using type = uint4; };
+
+template <typename T, int VEC>
+union Vec {
+    typename Raw<sizeof(T) * VEC>::type raw;
+    T x[VEC];
+    __device__ Vec() {}
+};
+__device__ __forceinline__ float as_float(float x) { return x; }
+__device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void set(float& y, float x) { y = x; }
+__device__ __forceinline__ void set(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
+
+// f / 2 pi of a turn, mod 1, as a 64-bit fraction: the mantissa's product with 2^64 / 2 pi, shifted by the exponent.
+__device__ __forceinline__ uint64_t turns_of(float f) {
+    const uint32_t u = __float_as_uint(f), e = u >> 23 & 255;
+    const uint64_t m = (uint64_t)((u & 0x7fffffu) | (e ? 0x800000u : 0u)) << 40;
+    const uint64_t h = __umul64hi(m, 0x28BE60DB9391054Aull);  // m 2^-40 / 2 pi 2^40
+    const int up = (int)(e ? e : 1) - 126;                    // f = m 2^-64 2^up
+    const uint64_t t = up <= -64 || up >= 64 ? 0 : up < 0 ? h >> -up : h << up;
+    return u >> 31 ? 0ull - t : t;
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(THREADS) turn_kernel(TurnArgs a) {
+    const int units = a.D / (2 * VEC);
+    const unsigned index = blockIdx.x * THREADS + threadIdx.x;
+    const size_t token = index / (unsigned)units;
+    const int unit = index - (unsigned)token * units;
+    if (token >= (size_t)a.B * a.T) return;
+    const int b = token / a.T, t = token - (size_t)b * a.T;
+    int chunk = blockIdx.y, which = 0;
+    while (chunk >= (a.part[which].H + HEADS - 1) / HEADS) chunk -= (a.part[which++].H + HEADS - 1) / HEADS;
+    const TurnPart& part = a.part[which];
+    const int h0 = chunk * HEADS, nh = min(HEADS, part.H - h0);
+    const bool live = !a.counts || t < a.counts[b];
+    size_t row = token;  // of the destination
+    if (part.cached) {
+        const long long at = (long long)a.lengths[b] + t;
+        const long long place = at / a.page_size;
+        if (!live || at < 0 || place >= a.table_pages) return;
+        const int page = a.table[(size_t)b * a.table_pages + place];
+        if ((unsigned)page >= (unsigned)a.pages) return;  // nowhere to write
+        row = (size_t)page * a.page_size + at % a.page_size;
+    }
+    const int pairs = part.turned ? a.pairs : 0;
+    const bool turn = unit * VEC < pairs;  // pairs unit VEC ..; other units copy
+    const int c0 = turn && !a.interleaved ? unit * VEC : 2 * unit * VEC;
+    const int c1 = turn && !a.interleaved ? c0 + pairs : c0 + VEC;
+    const T* src = static_cast<const T*>(part.src) + (token * part.H + h0) * a.D;
+    T* dst = static_cast<T*>(part.dst) + (row * part.H + h0) * a.D;
+    Vec<T, VEC> x[HEADS], y[HEADS];
+#pragma unroll
+    for (int h = 0; h < HEADS; h++)
+        if (h < nh && live) {
+            x[h].raw = *reinterpret_cast<const decltype(x[h].raw)*>(src + h * a.D + c0);
+            y[h].raw = *reinterpret_cast<const decltype(y[h].raw)*>(src + h * a.D + c1);
+        }
+    float co[VEC], si[VEC];
+    if (turn)
+#pragma unroll
+        for (int e = 0; e < VEC; e++) {
+            const int i = unit * VEC + e;
+            int axis = 0, first = 0;
+#pragma unroll
+            for (int k = 0; k < 3; k++)
+                if (axis == k && k + 1 < a.axes && i >= first + a.sections[k]) {
+                    first += a.sections[k];
+                    axis = k + 1;
+                }
+            const long long p = a.positions ? a.positions[token * a.axes + axis] : (long long)a.lengths[b] + t;
+            uint64_t turns = turns_of(a.inv_freq[i]) * (uint64_t)p;
+            if (a.inverse) turns = 0ull - turns;
+            sincospif((float)(int)((turns + 0x80000000ull) >> 32) * 0x1p-31f, &si[e], &co[e]);
+        }
+#pragma unroll
+    for (int h = 0; h < HEADS; h++) {
+        if (h >= nh) break;
+        if (!live) {
+#pragma unroll
+            for (int e = 0; e < VEC; e++) {
+                set(x[h].x[e], 0.f);
+                set(y[h].x[e], 0.f);
+            }
+        } else if (turn) {
+            if (a.interleaved) {
+                T z[2 * VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; e++) {
+                    z[e] = x[h].x[e];
+                    z[VEC + e] = y[h].x[e];
+                }
+#pragma unroll
+                for (int e = 0; e < VEC; e++) {
+                    const float p = as_float(z[2 * e]), q = as_float(z[2 * e + 1]);
+                    set(z[2 * e], p * co[e] - q * si[e]);
+                    set(z[2 * e + 1], q * co[e] + p * si[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < VEC; e++) {
+                    x[h].x[e] = z[e];
+                    y[h].x[e] = z[VEC + e];
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; e++) {
+                    const float p = as_float(x[h].x[e]), q = as_float(y[h].x[e]);
+                    set(x[h].x[e], p * co[e] - q * si[e]);
+                    set(y[h].x[e], q * co[e] + p * si[e]);
+                }
+            }
+        }
+        *reinterpret_cast<decltype(x[h].raw)*>(dst + h * a.D + c0) = x[h].raw;
+        *reinterpret_cast<decltype(y[h].raw)*>(dst + h * a.D + c1) = y[h].raw;
+    }
+}
+
+template <typename T, int VEC>
+cudaError_t turn(const TurnArgs& a, cudaStream_t st) {
+    const long long threads = (long long)a.B * a.T * (a.D / (2 * VEC));
+    unsigned chunks = 0;
+    for (int i = 0; i < a.parts; i++) chunks += (a.part[i].H + HEADS - 1) / HEADS;
+    trace_begin("turn", st);
+    turn_kernel<T, VEC><<<dim3((unsigned)((threads + THREADS - 1) / THREADS), chunks), THREADS, 0, st>>>(a);
+    trace_end(st);
+    return cudaGetLastError();
+}
+
+// The widest vectors that the channels and every pointer are aligned to.
+template <typename T>
+int widest(const TurnArgs& a) {
+    uintptr_t all = 0;
+    for (int i = 0; i < a.parts; i++) all |= reinterpret_cast<uintptr_t>(a.part[i].src) | reinterpret_cast<uintptr_t>(a.part[i].dst);
+    int vec = 16 / sizeof(T);
+    while (vec > 1 && ((all & (vec * sizeof(T) - 1)) || a.D % (2 * vec) || a.pairs % vec)) vec /= 2;
+    return vec;
+}
+
+}  // namespace
+
+cudaError_t launch_turn(const TurnArgs& a, cudaStream_t st) {
+    if (a.bf16) switch (widest<__nv_bfloat16>(a)) {
+        case 8: return turn<__nv_bfloat16, 8>(a, st);
+        case 4: return turn<__nv_bfloat16, 4>(a, st);
+        case 2: return turn<__nv_bfloat16, 2>(a, st);
+        default: return turn<__nv_bfloat16, 1>(a, st);
+    }
+    switch (widest<float>(a)) {
+        case 4: return turn<float, 4>(a, st);
+        case 2: return turn<float, 2>(a, st);
+        default: return turn<float, 1>(a, st);
+    }
+}
+
+}  // namespace gdr

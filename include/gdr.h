@@ -345,6 +345,102 @@ gdr_status gdr_group_norm_bwd(const gdr_norm_problem* p, const void* x, const vo
                               const float* bias, const void* dy, void* dx, void* dgate, float* dweight, float* dbias,
                               void* ws, size_t ws_bytes, gdr_stream_t stream);
 
+/* ---- Softmax attention layers ---------------------------------------------------------------
+ *
+ * The layers of a mixed model that see its tokens directly: window attention for training and
+ * prompts, rotary positions, and, token by token, a paged cache with the append to it and the
+ * decode step over it.
+ *
+ * Window attention. Query t of entry b and query head h (key head h / (Hq / Hk)) sees token j if
+ * j <= t, j < lengths[b], and t - j < window or j < sinks; with window == 0 every j <= t:
+ *
+ *     s_tj = scale q_t . k_j,   o_t = sum_j p_tj v_j,   p_t = softmax of s_t over the seen j,
+ *     lse_t = log sum_j exp(s_tj)
+ *
+ * q, o, do, dq [B, T, Hq, D] and k, v, dk, dv [B, T, Hk, D] of `dtype` (dk, dv summed over the
+ * query heads of their key head), lse [B, Hq, T] fp32, all 16-byte aligned (lse and lengths: 4).
+ * `lengths` [B] int32 as for linear attention: what lies past an entry's tokens is never used, not
+ * even where it is not finite; o, dq, dk, dv are zero and lse is -infinity there. A value that is
+ * not finite at a token that is there may reach every query of the blocks of 128 that a query seeing it
+ * is in, also those that do not see it.
+ * Rounding: sums, maxima and softmax statistics are fp32. With BF16 each result is rounded once, and
+ * so are p and the scores' gradient as operands of the tensor cores; the VJP takes o as rounded. */
+#define GDR_WINDOW_MAX_T (1 << 24)
+
+typedef struct {
+    int B, T, Hq, Hk, D; /* Hq % Hk == 0; 0 <= T <= GDR_WINDOW_MAX_T; D in {32, 64, 128} */
+    int window, sinks;   /* >= 0 */
+    gdr_dtype dtype;
+    float scale; /* > 0 */
+} gdr_window_problem;
+
+/* Forward: o and, if lse != NULL, lse. Workspace: gdr_window_fwd_workspace() bytes, 256-byte aligned (0:
+ * invalid problem); its first 256 bytes hold the status word, which this call and the VJP clear and then
+ * set, and gdr_workspace_status() reads. */
+size_t gdr_window_fwd_workspace(const gdr_window_problem* p);
+gdr_status gdr_window_fwd(const gdr_window_problem* p, const void* q, const void* k, const void* v, const int* lengths,
+                          void* o, float* lse, void* ws, size_t ws_bytes, gdr_stream_t stream);
+
+/* VJP for the loss <do, o>, from the forward's o and lse. Deterministic: no floating-point atomics. */
+size_t gdr_window_bwd_workspace(const gdr_window_problem* p);
+gdr_status gdr_window_bwd(const gdr_window_problem* p, const void* q, const void* k, const void* v, const int* lengths,
+                          const void* o, const float* lse, const void* do_, void* dq, void* dk, void* dv, void* ws,
+                          size_t ws_bytes, gdr_stream_t stream);
+
+/* Rotary positions. Of the D channels of each head the first 2 * pairs are turned by pairs: (i, i + pairs), or
+ * (2 i, 2 i + 1) with interleaved, by the angle positions[b, t, axis of i] * inv_freq[i] (its negative with
+ * inverse, which is the VJP); the first sections[0] pairs belong to axis 0, the next sections[1] to axis 1, and so
+ * on. The others are copied. The angle is formed in 64-bit fixed point: exact to 2^-62 |position|
+ * max(1, |inv_freq|) of a turn at any position, for finite inv_freq.
+ * x, y [B, T, H, D], positions [B, T, axes] int32, inv_freq [pairs] fp32. D even, B * T * D at most 2^32.
+ * Any alignment of the element; vectors of up to 16 bytes are used as far as pointers, D and pairs
+ * are aligned to them. y may be x itself. */
+typedef struct {
+    int B, T, H, D;
+    int pairs;                /* 0 <= 2 * pairs <= D */
+    int axes, sections[4];    /* 1 <= axes <= 4, sections sum to pairs (not read with pairs == 0) */
+    int interleaved, inverse; /* 0 or 1 */
+    gdr_dtype dtype;
+} gdr_rotary_problem;
+gdr_status gdr_rotary(const gdr_rotary_problem* p, const void* x, const int* positions, const float* inv_freq, void* y,
+                      gdr_stream_t stream);
+
+/* Paged cache: k_cache, v_cache [pages, page_size, Hk, D] of `dtype`; token j of entry b lies in page
+ * page_table[b, j / page_size] ([B, table_pages] int32), row j % page_size. A number outside [0, pages)
+ * is no page: nothing is written there, and its tokens are not seen. Entries may share pages that are
+ * only read.
+ *
+ * Append: token t < counts[b] (NULL: T) of entry b, rotated (pairs as above; 0: not), becomes token
+ * lengths[b] + t of the cache, unless the table ends before it. positions as above, or NULL: that place
+ * in the sequence (one axis). Two tokens of a call must not go to one row. With Hq > 0 the queries
+ * q [B, T, Hq, D] are rotated into q_out (which may be q), zero past counts[b]. Alignment as gdr_rotary. */
+typedef struct {
+    int B, T, Hq, Hk, D; /* Hq == 0: no queries */
+    int pages, page_size, table_pages;
+    int pairs, axes, sections[4], interleaved;
+    gdr_dtype dtype;
+} gdr_append_problem;
+gdr_status gdr_kv_append(const gdr_append_problem* p, const void* q, const void* k, const void* v, const int* positions,
+                         const float* inv_freq, const int* lengths, const int* counts, const int* page_table,
+                         void* q_out, void* k_cache, void* v_cache, gdr_stream_t stream);
+
+/* Decode step: q [B, Hq, D] is the query of token lengths[b] - 1 of entry b, the last one in the cache
+ * (lengths read clamped to [0, table_pages * page_size]); it sees tokens as in window attention. o [B, Hq, D] is
+ * zero for an entry that sees none. Rows of the cache that no entry sees may hold anything. Deterministic.
+ * Workspace: gdr_paged_decode_workspace() bytes, 256-byte aligned (0: invalid problem); calls that may run
+ * at the same time need one each. q, o and the caches 16-byte aligned. */
+typedef struct {
+    int B, Hq, Hk, D; /* as gdr_window_problem */
+    int pages, page_size, table_pages;
+    int window, sinks;
+    gdr_dtype dtype;
+    float scale; /* > 0 */
+} gdr_paged_problem;
+size_t gdr_paged_decode_workspace(const gdr_paged_problem* p);
+gdr_status gdr_paged_decode_step(const gdr_paged_problem* p, const void* q, const void* k_cache, const void* v_cache,
+                                 const int* page_table, const int* lengths, void* o, void* ws, size_t ws_bytes,
+                                 gdr_stream_t stream);
+
 /* Launch tracing for profiling. While enabled, every kernel the library launches is
  * bracketed by two CUDA events recorded on its own stream (host-side events only; no
  * device memory). gdr_trace_collect() waits for the recorded events, writes up to `max`

@@ -1,0 +1,181 @@
+"""The decode step over a paged cache on the GPU against its formula in 64 bits.
+
+Bounds, on ||x - ref|| / ||ref|| for each head. bf16: the weights and the result are rounded once each, 2 x 2^-8; fp32:
+sums of up to 256 products and weights in a row (longer ones are cut), 256 x 2^-24."""
+import pytest
+import torch
+
+import gated_delta_rule_31_gb300 as gdr
+from attention_ref import decode, make_cache, rows
+from linear_ref import rel_heads
+from util import cuda_device
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": torch.bfloat16, "fp32": torch.float32}
+TOL = {"bf16": 2 * 2.0 ** -8, "fp32": 256 * 2.0 ** -24}
+
+
+def make(B, lengths, Hq, Hk, D, page, dtype, seed=0, fill=float("nan"), room=0):
+    """q, caches, table, lengths; rows that hold no token hold `fill`."""
+    gen = torch.Generator().manual_seed(seed)
+    table, kc, vc = make_cache(B, max(lengths) + room, page, Hk, D, dtype, seed=seed, fill=fill)
+    for b, n in enumerate(lengths):
+        pg, r = rows(table, b, n, page)
+        kc[pg, r], vc[pg, r] = (torch.randn(n, Hk, D, generator=gen).to(dtype) for _ in range(2))
+    return torch.randn(B, Hq, D, generator=gen).to(dtype), kc, vc, table, torch.tensor(lengths, dtype=torch.int32)
+
+
+def check(x, dtype, **kw):
+    dev = cuda_device()
+    ref = decode(*x, **kw)
+    o = gdr.paged_decode_step(*(t.to(dev) for t in x), **kw)
+    assert o.dtype == x[0].dtype and o.shape == x[0].shape
+    assert rel_heads(o, ref, 1) <= TOL[dtype]
+    for b in range(len(ref)):
+        if not ref[b].any():
+            assert not o[b].any()
+    return o
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 63, 64, 65, 127, 129, 255, 1000, 5000])
+def test_lengths(n, dtype):
+    check(make(1, [n], 8, 2, 128, 16, TYPES[dtype], seed=n), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("page", [1, 3, 16, 24, 64, 100, 256])
+def test_pages(page, dtype):
+    check(make(4, [300, 0, 1, 123], 4, 2, 64, page, TYPES[dtype], seed=page, room=70), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("Hk,G", [(1, 1), (5, 1), (2, 2), (1, 3), (2, 7), (1, 8), (1, 9), (2, 16), (1, 17), (1, 40)])
+def test_heads(Hk, G, D, dtype):
+    check(make(2, [200, 77], Hk * G, Hk, D, 16, TYPES[dtype], seed=G), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (10, 4), (16, 16), (63, 0), (64, 4), (65, 1), (100, 130), (1000, 3), (2 ** 31 - 1, 2 ** 31 - 1), (0, 5)])
+def test_windows_and_sinks(window, sinks, dtype):
+    check(make(5, [400, 64, 65, 3, 110], 4, 1, 64, 16, TYPES[dtype], seed=sinks % 100), dtype, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_many_sequences(dtype):
+    """More than the threads that sum up the lengths, most of them short, one long."""
+    n = [(7 * i) % 50 for i in range(300)]
+    n[150] = 3000
+    check(make(300, n, 4, 2, 32, 8, TYPES[dtype], seed=1), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_enough_sequences_for_every_run(dtype):
+    check(make(70, [130 + (37 * i) % 90 for i in range(70)], 16, 8, 64, 16, TYPES[dtype], seed=2), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_pages_that_are_none(dtype):
+    """Tokens on pages outside the cache are not seen: freed pages before the window, and others."""
+    x = list(make(3, [200, 150, 90], 4, 2, 64, 16, TYPES[dtype], seed=4))
+    t = x[3]
+    t[0, :3] = -1
+    t[1, 4] = 2 ** 30
+    t[2, :] = -2 ** 31
+    check(x, dtype)
+    check(x, dtype, window=100, sinks=20)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_no_sequence_sees_anything(dtype):
+    check(make(3, [0, 0, 0], 4, 2, 64, 16, TYPES[dtype]), dtype)
+    dev = cuda_device()
+    q = torch.randn(2, 4, 64, device=dev).to(TYPES[dtype])
+    cache = torch.empty(0, 16, 2, 64, device=dev, dtype=TYPES[dtype])
+    n = torch.tensor([5, 9], dtype=torch.int32, device=dev)
+    for table in (torch.zeros(2, 3, dtype=torch.int32, device=dev), torch.zeros(2, 0, dtype=torch.int32, device=dev)):
+        assert not gdr.paged_decode_step(q, cache, cache, table, n).any()
+    e = torch.empty(0, 4, 64, device=dev, dtype=TYPES[dtype])
+    assert gdr.paged_decode_step(e, cache, cache, torch.zeros(0, 3, dtype=torch.int32, device=dev), n[:0]).shape == (0, 4, 64)
+
+
+def test_lengths_are_clamped():
+    x = list(make(3, [48, 48, 48], 2, 1, 64, 16, torch.bfloat16, seed=5))
+    x[4] = torch.tensor([-3, 10 ** 9, 2 ** 31 - 1], dtype=torch.int32)
+    check(x, "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_scores_that_grow_and_fall_along_the_keys(dtype):
+    for up in (1, -1):
+        q, kc, vc, table, n = make(1, [4000], 4, 1, 64, 16, TYPES[dtype], seed=6)
+        q.zero_()
+        q[..., 0] = 8.0
+        pg, r = rows(table, 0, 4000, 16)
+        kc[pg, r, :, 0] = (torch.linspace(-100, 100, 4000)[:, None] * up).to(TYPES[dtype])
+        check((q, kc, vc, table, n), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_entries_that_share_pages_and_a_scale(dtype):
+    q, kc, vc, table, n = make(4, [100] * 4, 4, 2, 64, 16, TYPES[dtype], seed=7)
+    table[1:, :4] = table[0, :4]
+    check((q, kc, vc, table, n), dtype, scale=0.3)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_repeats_bitwise_on_another_stream_and_in_a_graph(dtype):
+    dev = cuda_device()
+    x = [t.to(dev) for t in make(3, [900, 30, 1], 8, 2, 128, 16, TYPES[dtype], seed=8, room=50)]
+    first = gdr.paged_decode_step(*x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        second = gdr.paged_decode_step(*x)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        third = gdr.paged_decode_step(*x)
+    graph.replay()
+    assert torch.equal(first, second) and torch.equal(first, third)
+    x[4].add_(-1)  # the lengths are read on the device
+    graph.replay()
+    assert torch.equal(third, gdr.paged_decode_step(*x)) and not torch.equal(first, third)
+
+
+def test_offsets_past_32_bits():
+    """A cache of 2^31 elements and more: rows at its end."""
+    dev = cuda_device()
+    D, Hk, page = 128, 8, 64
+    pages = (1 << 31) // (D * Hk * page) + 3
+    q, kc, vc, table, n = make(1, [150], 8, Hk, D, page, torch.bfloat16, seed=9, fill=0.0)
+    ref = decode(q, kc, vc, table, n)
+    big = [torch.empty(pages, page, Hk, D, dtype=torch.bfloat16, device=dev) for _ in range(2)]
+    far = torch.arange(pages - 3, pages, device=dev)
+    for b, c in zip(big, (kc, vc)):
+        b[far] = c[table[0].long()].to(dev)
+    o = gdr.paged_decode_step(q.to(dev), *big, far.to(torch.int32)[None], n.to(dev))
+    assert rel_heads(o, ref, 1) <= TOL["bf16"]
+    new = torch.randn(1, 1, Hk, D, device=dev).bfloat16()
+    gdr.kv_append(new, new, *big, far.to(torch.int32)[None], n.to(dev))
+    assert torch.equal(big[0][pages - 1, 150 - 128], new[0, 0]) and torch.equal(big[1][pages - 1, 150 - 128], new[0, 0])
+
+
+def test_refusals():
+    dev = cuda_device()
+    q, kc, vc, table, n = (t.to(dev) for t in make(2, [20, 5], 4, 2, 64, 16, torch.bfloat16))
+    f = gdr.paged_decode_step
+    for bad in (lambda: f(q.cpu(), kc, vc, table, n), lambda: f(q, kc, vc[:1], table, n), lambda: f(q, kc.float(), vc.float(), table, n),
+                lambda: f(q, kc, vc, table.long(), n), lambda: f(q, kc, vc, table, n.long()), lambda: f(q, kc, vc, table[:1], n),
+                lambda: f(q, kc, vc, table, n, window=-1), lambda: f(q, kc, vc, table, n, out=q[:, :2]), lambda: f(q[0], kc, vc, table, n),
+                lambda: f(q, kc, vc, table, n, workspace=torch.empty(8, dtype=torch.uint8, device=dev)), lambda: f(q, kc[0], vc, table, n),
+                lambda: f(q, kc[..., :32].contiguous(), vc[..., :32].contiguous(), table, n)):
+        with pytest.raises(ValueError):
+            bad()
+    for call, code in ((lambda: f(q, kc, vc, table, n, scale=float("inf")), 1), (lambda: f(q[:, :3].contiguous(), kc, vc, table, n), 1),
+                       (lambda: f(q, kc, vc, table, n, scale=-0.1), 1)):
+        with pytest.raises(gdr.GdrError) as e:
+            call()
+        assert e.value.code == code
