@@ -107,8 +107,7 @@ gdr_status gdr_window_fwd(const gdr_window_problem* p, const void* q, const void
     if (!on(lse, 4) || !on(lengths, 4)) return GDR_ERR_INVALID_ARG;
     if ((r = check_ws(ws, ws_bytes, gdr_window_fwd_workspace(p))) != GDR_OK) return r;
     cudaStream_t st = (cudaStream_t)stream;
-    if (cudaMemsetAsync(ws, 0, 256, st) != cudaSuccess) return GDR_ERR_CUDA;
-    if (empty) return GDR_OK;
+    if (empty) return of(cudaMemsetAsync(ws, 0, 256, st));
     WindowArgs a = window_args(p, lengths);
     a.q = q; a.k = k; a.v = v; a.o = o; a.lse = lse;
     a.status = static_cast<int*>(ws);
@@ -129,8 +128,7 @@ gdr_status gdr_window_bwd(const gdr_window_problem* p, const void* q, const void
     if ((!lse && !empty) || !on(lse, 4) || !on(lengths, 4)) return GDR_ERR_INVALID_ARG;
     if ((r = check_ws(ws, ws_bytes, gdr_window_bwd_workspace(p))) != GDR_OK) return r;
     cudaStream_t st = (cudaStream_t)stream;
-    if (cudaMemsetAsync(ws, 0, 256, st) != cudaSuccess) return GDR_ERR_CUDA;
-    if (empty) return GDR_OK;
+    if (empty) return of(cudaMemsetAsync(ws, 0, 256, st));
     WindowArgs a = window_args(p, lengths);
     a.q = q; a.k = k; a.v = v; a.o = const_cast<void*>(o); a.lse = const_cast<float*>(lse);
     a.do_ = do_; a.dq = dq; a.dk = dk; a.dv = dv;

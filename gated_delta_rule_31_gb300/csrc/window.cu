@@ -16,6 +16,7 @@
 #include "attention.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "window_host.h"
 
 namespace gdr {
 
@@ -139,6 +140,7 @@ __global__ void __launch_bounds__(THREADS) window_fwd_kernel(WindowArgs a) {
     const WindowShape& s = a.s;
     const int t0 = (gridDim.x - 1 - blockIdx.x) * N, h = blockIdx.y, b = blockIdx.z, hk = h / (s.Hq / s.Hk), n = s.tokens(b);
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    if (blockIdx.x + blockIdx.y + blockIdx.z == 0 && threadIdx.x < 4) a.status[threadIdx.x] = 0;
     const KeyTiles tiles(N, s.window, s.sinks, t0, min(t0 + N, n));
     load_tile<D, T>(Q, a.q, s.T, s.Hq, b, h, t0, n);
     float m[4], l[4], acc[4][D / 16] = {};
@@ -197,6 +199,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) window_delta_kernel(WindowArgs a) {
     const WindowShape& s = a.s;
     const size_t row = ((size_t)blockIdx.x * 256 + threadIdx.x) / 8, rows = (size_t)s.B * s.T * s.Hq;
+    if (blockIdx.x == 0 && threadIdx.x < 4) a.status[threadIdx.x] = 0;
     if (row >= rows) return;  // whole groups of 8 lanes
     const int h = row % s.Hq, lane = threadIdx.x % 8;
     const size_t bt = row / s.Hq;
@@ -326,7 +329,7 @@ cudaError_t bwd_of(const WindowArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_window_fwd(const WindowArgs& a, cudaStream_t st) {
-    return a.s.bf16 ? fwd_of<__nv_bfloat16>(a, st) : fwd_of<float>(a, st);
+    return a.s.bf16 ? launch_window_fwd_tc(a, st) : fwd_of<float>(a, st);
 }
 
 cudaError_t launch_window_delta(const WindowArgs& a, cudaStream_t st) {

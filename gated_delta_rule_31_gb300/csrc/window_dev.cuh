@@ -1,0 +1,76 @@
+// window_dev.cuh - device helpers of the tensor-core kernels of window attention: which pairs of a tile are seen, the
+// exponentials, zeroing of rows past the end, and arithmetic on fp32 pairs.
+#pragma once
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "attention.h"
+#include "linear_dev.cuh"
+
+namespace gdr {
+namespace window {
+
+using namespace linear;  // C = 128 tokens of a tile, TILE, PANEL, products and waits
+
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Whether every query of t0 .. t0 + 127 sees every key of j0 .. j0 + 127.
+__device__ __forceinline__ bool all_seen(const WindowShape& s, int t0, int j0, int n) {
+    return j0 + C - 1 <= t0 && t0 + C <= n && (t0 + C - 1 - j0 < s.window || j0 + C <= s.sinks);
+}
+__device__ __forceinline__ uint32_t below(int c) { return c <= 0 ? 0u : c >= 32 ? 0xffffffffu : (1u << c) - 1; }
+// Which of keys j .. j + 31 query t sees, as bits.
+__device__ __forceinline__ uint32_t keys_seen(const WindowShape& s, int t, int j, int n) {
+    const uint32_t upto = t < n ? below(t + 1 - j) : 0u;
+    return upto & (~below(t - s.window + 1 - j) | below(s.sinks - j));
+}
+// Which of queries t .. t + 31 see key j.
+__device__ __forceinline__ uint32_t seen_by(const WindowShape& s, int t, int j, int n) {
+    const uint32_t from = j < n ? below(n - t) & ~below(j - t) : 0u;
+    return j < s.sinks ? from : from & below(j + s.window - t);
+}
+
+// Rows m .. 127 of a 128-token tile in shared memory to zero, by a whole warp: operands of products must be finite there.
+__device__ __forceinline__ void zero_rows(uint32_t tile, int m, int panels, int lane) {
+    const int ch = lane & 15;
+    if (ch < 8 * panels)
+#pragma unroll 1
+        for (int z = m + (lane >> 4); z < C; z += 2) st_shared_v4(tile + sw128_chunk(z, ch, C), 0, 0, 0, 0);
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+}  // namespace window
+}  // namespace gdr

@@ -1,0 +1,440 @@
+// window_tc.cu - forward of window attention on the tensor cores, for bf16 (gdr_window_fwd).
+//
+// A CTA stays on its SM and takes units in turn, each two tiles of 128 query rows against the same keys: two heads that share
+// a key head, or, where the sharing heads are odd in number, neighbouring row tiles. Per tile of 128 keys and query tile
+//
+//     S = Q K^T                      128 x 128 x D
+//     P = 2^(c S - c m), c = scale log2 e, m a maximum of the row so far; l += sum P
+//     O += P V                       128 x D x 128
+//
+// as tcgen05 products with S, then P in bf16 over it, and O in TMEM. Four warps, a thread for each row, form a query
+// tile's P, so a row's maximum and sum need no exchange; while they do, the tensor core works for the other query tile: in
+// order P0 V, the next S0, P1 V, the next S1. m is moved, and O and l scaled by 2^(c m - c m'), only when the row's
+// maximum has grown by more than 8 / c: until then P is at most 2^8, as exact in bf16 as below one, and the sums in
+// fp32 have the room; most tiles then need no pass over O. The order of tiles and units is fixed by the shape.
+// Rounding to bf16: P, and the result.
+//
+// Warps 0-3 and 4-7 take the query tiles, 8 copies tiles in (Q of the next unit as soon as the last S of this one has read it,
+// K and V in a ring of five slots), 9 issues the products. The stream of tiles runs through the units without a
+// break: while the rows of one unit are written, the next unit's S is formed.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "kernels.h"
+#include "linear.h"
+#include "window_dev.cuh"
+#include "window_host.h"
+
+namespace gdr {
+
+using namespace window;
+
+namespace {
+
+constexpr int THREADS = 384, SLOTS = 5, SMS = 152;
+constexpr uint32_t AT_KV = 2 * TILE, BYTES = AT_KV + SLOTS * TILE;
+static_assert(BYTES + 1024 <= 232448, "shared memory");
+// Registers a thread: three times 128 threads start with 168.
+constexpr int REGS_ROWS = 216, REGS_REST = 64;
+static_assert(2 * REGS_ROWS + REGS_REST <= 3 * 168, "registers of the launch");
+constexpr float GROWTH = 8.f;  // of c m before O is scaled
+
+struct FwdArgs {
+    WindowShape s;
+    int pair_heads;     // a unit's two tiles are heads h, h + 1 of a row tile; else row tiles 2 i, 2 i + 1 of a head
+    int row_tiles;      // of the sequence
+    long long units;
+    void* o;
+    float* lse;
+    int* status;
+};
+
+// A unit: its two query tiles and the key tiles that either sees.
+struct Unit {
+    int b, hk, n, h[2], t0[2];
+    KeyTiles tiles[2], both;
+    __device__ __forceinline__ void set(const FwdArgs& a, long long u) {
+        const WindowShape& s = a.s;
+        // the longest rows first, the heads of a row tile next to one another
+        const int cols = a.pair_heads ? s.Hq / 2 : s.Hq, rows = a.pair_heads ? a.row_tiles : (a.row_tiles + 1) / 2;
+        const long long per = (long long)cols * s.B;
+        const int r = rows - 1 - (int)(u / per), rest = (int)(u % per), col = rest % cols;
+        b = rest / cols;
+        n = s.tokens(b);
+        h[0] = a.pair_heads ? 2 * col : col;
+        h[1] = a.pair_heads ? 2 * col + 1 : col;
+        hk = h[0] / (s.Hq / s.Hk);
+        t0[0] = (a.pair_heads ? r : 2 * r) * C;
+        t0[1] = a.pair_heads ? t0[0] : t0[0] + C;
+#pragma unroll
+        for (int i = 0; i < 2; i++) tiles[i] = KeyTiles(C, s.window, s.sinks, t0[i], min(t0[i] + C, n));
+        both = tiles[0];
+        if (!a.pair_heads && tiles[1].hi > 0) {  // the later rows see at least as far
+            both.hi = tiles[1].hi;
+            both.lo = min(tiles[0].lo, tiles[1].lo);
+            both.first = min(max(tiles[0].first, tiles[1].first), both.lo);
+        }
+    }
+    __device__ __forceinline__ bool first(int i, int tile) const { return tile == tiles[i].at(0); }
+    __device__ __forceinline__ bool last(int i, int tile) const { return tile == tiles[i].hi - 1; }
+};
+
+// The units of a CTA: every other round in reverse order, so that long and short ones even out.
+__device__ __forceinline__ long long unit_of(long long round) {
+    return round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
+__global__ void __launch_bounds__(THREADS, 1)
+    window_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                         const __grid_constant__ CUtensorMap mv, FwdArgs a) {
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const uint32_t sb = smem_u32(sm);
+    __shared__ uint64_t qfull[2], qfree[2], full[SLOTS], empty[SLOTS], sfull[2], pready[2], ofull[2], ofree[2], drain;
+    __shared__ uint32_t tmem_sh;
+    __shared__ int failed, used[SLOTS], used_q[2];
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const WindowShape& s = a.s;
+    if (sb & 1023u) {  // never on this layout; swizzled tiles would be read wrongly
+        if (tid == 0) a.status[0] = -1;
+        return;
+    }
+    if (tid == 0) {
+        if (blockIdx.x == 0)
+            for (int i = 0; i < 4; i++) a.status[i] = 0;  // a wait expires a second later at the earliest
+        failed = 0;
+        for (int i = 0; i < SLOTS; i++) {
+            used[i] = 0;
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            used_q[i] = 0;
+            mbar_init(&qfull[i], 1);
+            mbar_init(&qfree[i], 1);
+            mbar_init(&sfull[i], 1);
+            mbar_init(&pready[i], 4);
+            mbar_init(&ofull[i], 1);
+            mbar_init(&ofree[i], 4);
+        }
+        mbar_init(&drain, 1);
+        fence_barrier_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(&tmem_sh, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = tmem_sh;
+    const int panels = s.D > 64 ? 2 : 1;
+    constexpr uint32_t COL_S = 0, COL_O = 256;
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
+        if (warp == 8) {
+            int pos = 0, nq[2] = {0, 0};
+            bool ok = true;
+            auto load = [&](const CUtensorMap* map, int head, int t, int b) {
+                const int k = pos % SLOTS, use = pos / SLOTS;
+                if (use > 0) ok = wait_phase(&empty[k], (use + 1) & 1, &failed, 70);
+                if (ok && lane == 0) {
+                    mbar_expect_tx(&full[k], panels * PANEL);
+                    used[k] = use + 1;
+                    for (int p = 0; p < panels; p++) tma_load_4d(sm + AT_KV + k * TILE + p * PANEL, map, 64 * p, head, t, b, &full[k]);
+                }
+                __syncwarp();
+                pos++;
+            };
+#pragma unroll 1
+            for (long long round = 0; ok; round++) {
+                const long long u = unit_of(round);
+                if (u >= a.units) {
+                    if (round * gridDim.x >= a.units) break;
+                    continue;
+                }
+                Unit x;
+                x.set(a, u);
+                const int count = x.both.count();
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    if (!ok || x.tiles[i].count() == 0) continue;
+                    if (nq[i] > 0) ok = wait_phase(&qfree[i], (nq[i] + 1) & 1, &failed, 71);
+                    if (ok && lane == 0) {
+                        mbar_expect_tx(&qfull[i], panels * PANEL);
+                        used_q[i] = nq[i] + 1;
+                        for (int p = 0; p < panels; p++) tma_load_4d(sm + i * TILE + p * PANEL, &mq, 64 * p, x.h[i], x.t0[i], x.b, &qfull[i]);
+                    }
+                    __syncwarp();
+                    nq[i]++;
+                    if (i == 0 && ok) load(&mk, x.hk, x.both.at(0) * C, x.b);
+                }
+#pragma unroll 1
+                for (int i = 0; i < count && ok; i++) {
+                    const int t = x.both.at(i) * C;
+                    if (i > 0) load(&mk, x.hk, t, x.b);
+                    if (ok) load(&mv, x.hk, t, x.b);
+                }
+            }
+        } else if (warp == 9) {
+            const uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, s.D, 0, 1);
+            const int ksteps = s.D / 16;
+            int npv[2] = {0, 0}, nq[2] = {0, 0}, nu[2] = {0, 0};  // P V products; units begun by S; by P V
+            long long round = -1;
+            Unit cur, nxt;
+            int ci = 0, ni = 0, count = 0;  // places in the key tiles of cur and nxt
+            long long pos = 0;              // key tiles whose S has been issued
+            bool have = true, ok = true;
+            auto advance = [&]() {  // nxt, ni to the next key tile of the stream
+                if (ni + 1 < count) {
+                    ni++;
+                    return;
+                }
+                ni = 0;
+                count = 0;
+                while (have && count == 0) {
+                    round++;
+                    if (round * gridDim.x >= a.units) {
+                        have = false;
+                        break;
+                    }
+                    const long long u = unit_of(round);
+                    if (u >= a.units) continue;
+                    nxt.set(a, u);
+                    count = nxt.both.count();
+                }
+            };
+            auto issue_s = [&](int i) {
+                const int tile = nxt.both.at(ni);
+                if (!nxt.tiles[i].has(tile)) return true;
+                if (nxt.first(i, tile)) {
+                    if (!wait_phase(&qfull[i], nq[i] & 1, &failed, 72)) return false;
+                    nq[i]++;
+                }
+                const int kp = (int)((2 * pos) % SLOTS);
+                if (!wait_phase(&full[kp], (int)((2 * pos) / SLOTS & 1), &failed, 73)) return false;
+                tc_fence_after();
+                const uint32_t ad = lo_kmajor(sb + i * TILE), bd = lo_kmajor(sb + AT_KV + kp * TILE);
+#pragma unroll
+                for (int k = 0; k < 8; k++)
+                    if (k < ksteps)
+                        mma_ss(tm + COL_S + 128 * i, ad + (k >> 2) * (PANEL >> 4) + 2 * (k & 3), bd + (k >> 2) * (PANEL >> 4) + 2 * (k & 3), id_s, k > 0);
+                commit(&sfull[i]);
+                if (nxt.last(i, tile)) commit(&qfree[i]);
+                return true;
+            };
+            auto ring_done = [&](long long p) { commit(&empty[(int)(p % SLOTS)]); };
+            advance();
+            if (have) {
+                ok = issue_s(0) && issue_s(1);
+                ring_done(2 * pos);
+                pos++;
+            }
+#pragma unroll 1
+            while (have && ok) {
+                cur = nxt;
+                ci = ni;
+                const int tile = cur.both.at(ci);
+                const long long vp = 2 * (pos - 1) + 1;
+                const uint32_t vt = sb + AT_KV + (int)(vp % SLOTS) * TILE;
+                advance();
+                if (!wait_phase(&full[(int)(vp % SLOTS)], (int)(vp / SLOTS & 1), &failed, 74)) break;
+                const int m = cur.n - tile * C;
+                if (m < C && cur.n < s.T) zero_rows(vt, m, panels, lane);  // past the end, whatever it holds
+                const int steps = m < C ? (m + 15) / 16 : 8;
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    if (cur.tiles[i].has(tile)) {
+                        const bool begin = cur.first(i, tile);
+                        if (begin && nu[i]++ > 0) ok = ok && wait_phase(&ofree[i], nu[i] & 1, &failed, 75);
+                        ok = ok && wait_phase(&pready[i], npv[i] & 1, &failed, 76);
+                        npv[i]++;
+                        if (ok) {
+                            tc_fence_after();
+                            const uint32_t bd = lo_mnmajor(vt);
+#pragma unroll
+                            for (int k = 0; k < 8; k++)
+                                if (k < steps) mma_ts(tm + COL_O + 128 * i, tm + COL_S + 128 * i + 8 * k, bd + step_mnmajor(k), id_o, k > 0 || !begin);
+                            commit(&ofull[i]);
+                        }
+                    }
+                    if (ok && have) ok = issue_s(i);
+                }
+                if (!ok) break;
+                ring_done(vp);
+                if (have) {
+                    ring_done(2 * pos);
+                    pos++;
+                }
+            }
+            commit(&drain);  // every product issued so far has completed before TMEM is released
+            int never = 0;
+            wait_phase(&drain, 0, &never, 1);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_ROWS));
+        const int i = warp >> 2, row = 32 * (warp & 3) + lane;
+        const uint32_t lanes = tm + ((uint32_t)(32 * (warp & 3)) << 16), at_s = lanes + COL_S + 128 * i, at_o = lanes + COL_O + 128 * i;
+        const float c = s.scale * LOG2E;
+        int np = 0;  // tiles so far
+        bool ok = true;
+#pragma unroll 1
+        for (long long round = 0; ok; round++) {
+            const long long u = unit_of(round);
+            if (u >= a.units) {
+                if (round * gridDim.x >= a.units) break;
+                continue;
+            }
+            Unit x;
+            x.set(a, u);
+            const int t0 = i ? x.t0[1] : x.t0[0], t = t0 + row, head = i ? x.h[1] : x.h[0], n = x.n;
+            const KeyTiles tiles = i ? x.tiles[1] : x.tiles[0];
+            const int count = tiles.count();
+            float m = -INFINITY, l = 0.f;  // m as it is used; l of this thread's row
+#pragma unroll 1
+            for (int it = 0; it < count; it++, np++) {
+                const int j0 = tiles.at(it) * C;
+                ok = wait_phase(&sfull[i], np & 1, &failed, 77);
+                if (!ok) break;
+                tc_fence_after();
+                float v[128];
+#pragma unroll
+                for (int e = 0; e < 4; e++) tmem_ld32(at_s + 32 * e, v + 32 * e);
+                tmem_wait_ld();
+                if (!all_seen(s, t0, j0, n)) {
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const uint32_t w = keys_seen(s, t, j0 + 32 * e, n);
+#pragma unroll
+                        for (int k = 0; k < 32; k++)
+                            if (!(w >> k & 1)) v[32 * e + k] = -INFINITY;
+                    }
+                }
+                float top[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) top[e] = fmaxf(v[2 * e], v[2 * e + 1]);
+#pragma unroll
+                for (int k = 8; k < 128; k += 8)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) top[e] = max3(top[e], v[k + 2 * e], v[k + 2 * e + 1]);
+                const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                // a row that has seen no token (l = 0, O = 0) takes any maximum as it is
+                if (l == 0.f) m = now;
+                const bool grown = (now - m) * c > GROWTH;
+                if (__any_sync(0xffffffffu, grown)) {
+                    const float to = fmaxf(m, now), f = to == m ? 1.f : exp2_fast((m - to) * c);
+                    m = to;
+                    l *= f;
+                    ok = wait_phase(&ofull[i], (np + 1) & 1, &failed, 78);  // the product before
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int e = 0; e < s.D; e += 32) {
+                        float o[32];
+                        tmem_ld32(at_o + e, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) scale2(o + k, f);
+                        tmem_st32(at_o + e, o);
+                    }
+                }
+                const float base = m == -INFINITY ? 0.f : m * c;
+                const uint64_t c2 = pair(c, c), b2 = pair(-base, -base);
+                uint64_t sum[2] = {0, 0};
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int k = 0; k < 16; k++) {
+                        float p0, p1;
+                        unpair(fma2(pair(v[32 * e + 2 * k], v[32 * e + 2 * k + 1]), c2, b2), p0, p1);
+                        p0 = exp2_fast(p0);
+                        p1 = exp2_fast(p1);
+                        sum[k & 1] = add2(sum[k & 1], pair(p0, p1));
+                        w[k] = pack_bf16(p0, p1);
+                    }
+                    tmem_st16(at_s + 16 * e, w);
+                }
+                float s0, s1;
+                unpair(add2(sum[0], sum[1]), s0, s1);
+                l += s0 + s1;
+                // the product before: complete, since S came after it, and its phase is taken before the next one's can end
+                ok = np == 0 || wait_phase(&ofull[i], (np + 1) & 1, &failed, 80);
+                if (!ok) break;
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&pready[i]);
+            }
+            if (!ok) break;
+            if (t0 >= s.T) continue;  // no such row tile
+            if (count > 0) {
+                ok = wait_phase(&ofull[i], (np + 1) & 1, &failed, 79);
+                if (!ok) break;
+                tc_fence_after();
+            }
+            const bool there = t < n;
+            const float f = there ? 1.f / l : 0.f;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + (((size_t)x.b * s.T + t) * s.Hq + head) * s.D;
+#pragma unroll 1
+            for (int e = 0; e < s.D; e += 32) {
+                float o[32];
+                if (count > 0) {
+                    tmem_ld32(at_o + e, o);
+                    tmem_wait_ld();
+                }
+                if (t < s.T)
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8)
+                        *reinterpret_cast<uint4*>(out + e + k) = there ? pack8(o + k, f) : make_uint4(0, 0, 0, 0);
+            }
+            if (count > 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ofree[i]);
+            }
+            if (a.lse && t < s.T) a.lse[((size_t)x.b * s.Hq + head) * s.T + t] = there ? LN2 * (m * c + log2f(l)) : -INFINITY;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (failed && tid == 0) {
+        if (atomicCAS(a.status, 0, DEV_TIMEOUT) == 0) {
+            a.status[1] = blockIdx.x;
+            a.status[2] = failed;
+        }
+        int never = 0;
+        for (int k = 0; k < SLOTS; k++)  // copies still in flight must land first
+            if (used[k]) mbar_wait(&full[k], (used[k] - 1) & 1, &never, nullptr, 0);
+        for (int k = 0; k < 2; k++)
+            if (used_q[k]) mbar_wait(&qfull[k], (used_q[k] - 1) & 1, &never, nullptr, 0);
+    }
+    __syncthreads();
+    if (warp == 8) tmem_dealloc(tm, 512);
+}
+
+}  // namespace
+
+cudaError_t launch_window_fwd_tc(const WindowArgs& x, cudaStream_t st) {
+    // before the tensor maps: the first runtime call of a host thread makes the device's context current there
+    if (cudaError_t e = cudaFuncSetAttribute(window_fwd_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES)) return e;
+    CUtensorMap mq, mk, mv;
+    if (!rows_map(&mq, x.q, x.s, x.s.Hq) || !rows_map(&mk, x.k, x.s, x.s.Hk) || !rows_map(&mv, x.v, x.s, x.s.Hk)) return cudaErrorInvalidValue;
+    FwdArgs a = {};
+    a.s = x.s;
+    a.pair_heads = x.s.Hq / x.s.Hk % 2 == 0;
+    a.row_tiles = (x.s.T + C - 1) / C;
+    a.units = (long long)x.s.B * (a.pair_heads ? (long long)x.s.Hq / 2 * a.row_tiles : (long long)x.s.Hq * ((a.row_tiles + 1) / 2));
+    a.o = x.o;
+    a.lse = x.lse;
+    a.status = x.status;
+    trace_begin("window_fwd_tc", st);
+    window_fwd_tc_kernel<<<(unsigned)(a.units < SMS ? a.units : SMS), THREADS, BYTES, st>>>(mq, mk, mv, a);
+    trace_end(st);
+    return cudaGetLastError();
+}
+
+}  // namespace gdr
