@@ -14,7 +14,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgdr.so")
 SOURCES = ["api.cu", "recurrent.cu", "recurrent_bwd.cu", "chunk_fwd.cu", "chunk_fwd_ch.cu", "chunk_bwd.cu", "chunk_bwd_ch.cu", "scan.cu", "pad.cu", "noalloc.cu", "chunk_f32.cu",
            "api_linear.cu", "linear.cu", "linear_tc.cu", "linear_grad.cu", "linear_step.cu", "group_norm.cu",
-           "api_attention.cu", "window.cu", "window_tc.cu", "turn.cu", "paged.cu"]
+           "api_attention.cu", "window.cu", "window_tc.cu", "window_grad.cu", "turn.cu", "paged.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
                 "-I", INCLUDE, "-I", CSRC]

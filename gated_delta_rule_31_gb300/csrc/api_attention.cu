@@ -115,7 +115,7 @@ gdr_status gdr_window_fwd(const gdr_window_problem* p, const void* q, const void
 }
 
 size_t gdr_window_bwd_workspace(const gdr_window_problem* p) {
-    return check_window(p) == GDR_OK ? 256 + rows_bytes(p) : 0;
+    return check_window(p) == GDR_OK ? 256 + rows_bytes(p) + window_parts_bytes(window_args(p, nullptr).s) : 0;
 }
 
 gdr_status gdr_window_bwd(const gdr_window_problem* p, const void* q, const void* k, const void* v, const int* lengths,
@@ -134,6 +134,7 @@ gdr_status gdr_window_bwd(const gdr_window_problem* p, const void* q, const void
     a.do_ = do_; a.dq = dq; a.dk = dk; a.dv = dv;
     a.status = static_cast<int*>(ws);
     a.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256);
+    a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256 + rows_bytes(p));
     if (launch_window_delta(a, st) != cudaSuccess) return GDR_ERR_CUDA;
     return of(launch_window_bwd(a, st));
 }

@@ -55,10 +55,11 @@ struct WindowArgs {
     const void *do_;
     float* delta;  // [B, Hq, T] sum of do o over the channels
     void *dq, *dk, *dv;
-    float* parts;  // partial sums of dk and dv, where tiles of keys are cut (window_grad_pieces)
+    float* parts;  // sums of dk and dv over parts of the queries (window_parts_bytes)
     int* status;
 };
 cudaError_t launch_window_fwd(const WindowArgs& a, cudaStream_t st);
+size_t window_parts_bytes(const WindowShape& s);
 cudaError_t launch_window_delta(const WindowArgs& a, cudaStream_t st);
 cudaError_t launch_window_bwd(const WindowArgs& a, cudaStream_t st);
 

@@ -1,5 +1,5 @@
-// window.cu - softmax attention with a sliding window and visible first tokens on the CUDA cores (gdr_window_fwd,
-// gdr_window_bwd): tiles of 64 queries and 64 keys in shared memory, all arithmetic in fp32.
+// window.cu - softmax attention with a sliding window and visible first tokens (gdr_window_fwd, gdr_window_bwd): the launches,
+// delta, and fp32 problems on the CUDA cores: tiles of 64 queries and 64 keys in shared memory, all arithmetic in fp32.
 //
 // Forward, a CTA for each (64 queries, head, entry): with the running maximum m and sum l of each row, per tile
 //     S = scale Q K^T,  m' = max(m, max S),  P = exp(S - m'),  l <- exp(m - m') l + sum P,  O <- exp(m - m') O + P V.
@@ -29,16 +29,14 @@ __device__ __forceinline__ float4 get4(const __nv_bfloat16* p) {
     const uint2 v = *reinterpret_cast<const uint2*>(p);
     return make_float4(bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y));
 }
-__device__ __forceinline__ void put(float* p, float x) { *p = x; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
 // Rows t0 .. t0 + 63 of one head of x [B, T, H, D] into shared memory; rows from n on are zero.
-template <int D, typename T>
+template <int D>
 __device__ __forceinline__ void load_tile(float* to, const void* x, int len, int H, int b, int h, int t0, int n) {
     for (int i = threadIdx.x; i < N * D / 4; i += THREADS) {
         const int r = i / (D / 4), c = i % (D / 4) * 4;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (t0 + r < n) v = get4(static_cast<const T*>(x) + (((size_t)b * len + t0 + r) * H + h) * D + c);
+        if (t0 + r < n) v = get4(static_cast<const float*>(x) + (((size_t)b * len + t0 + r) * H + h) * D + c);
         *reinterpret_cast<float4*>(to + r * (D + 4) + c) = v;
     }
 }
@@ -114,7 +112,7 @@ __device__ __forceinline__ float over16(float x, bool max) {
     return x;
 }
 
-template <int D, typename T>
+template <int D>
 __device__ __forceinline__ void put_rows(void* x, int len, int H, int b, int h, int t0, const float (&acc)[4][D / 16],
                                          const float* f) {
     using C = Cols<D>;
@@ -122,18 +120,18 @@ __device__ __forceinline__ void put_rows(void* x, int len, int H, int b, int h, 
     for (int i = 0; i < 4; i++) {
         const int t = t0 + threadIdx.x / 16 * 4 + i;
         if (t >= len) continue;
-        T* row = static_cast<T*>(x) + (((size_t)b * len + t) * H + h) * D;
+        float* row = static_cast<float*>(x) + (((size_t)b * len + t) * H + h) * D;
 #pragma unroll
         for (int g = 0; g < C::NW; g++)
 #pragma unroll
-            for (int c = 0; c < C::W; c++) put(row + C::at(g) + c, f[i] * acc[i][g * C::W + c]);
+            for (int c = 0; c < C::W; c++) row[C::at(g) + c] = f[i] * acc[i][g * C::W + c];
     }
 }
 
 template <int D>
 constexpr int tile_bytes() { return N * (D + 4) * 4; }
 
-template <int D, typename T>
+template <int D>
 __global__ void __launch_bounds__(THREADS) window_fwd_kernel(WindowArgs a) {
     extern __shared__ __align__(16) float sh[];
     float *Q = sh, *K = Q + tile_bytes<D>() / 4, *V = K + tile_bytes<D>() / 4, *P = V + tile_bytes<D>() / 4;
@@ -142,7 +140,7 @@ __global__ void __launch_bounds__(THREADS) window_fwd_kernel(WindowArgs a) {
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     if (blockIdx.x + blockIdx.y + blockIdx.z == 0 && threadIdx.x < 4) a.status[threadIdx.x] = 0;
     const KeyTiles tiles(N, s.window, s.sinks, t0, min(t0 + N, n));
-    load_tile<D, T>(Q, a.q, s.T, s.Hq, b, h, t0, n);
+    load_tile<D>(Q, a.q, s.T, s.Hq, b, h, t0, n);
     float m[4], l[4], acc[4][D / 16] = {};
 #pragma unroll
     for (int i = 0; i < 4; i++) {
@@ -152,8 +150,8 @@ __global__ void __launch_bounds__(THREADS) window_fwd_kernel(WindowArgs a) {
     for (int it = 0; it < tiles.count(); it++) {
         const int j0 = tiles.at(it) * N;
         __syncthreads();
-        load_tile<D, T>(K, a.k, s.T, s.Hk, b, hk, j0, n);
-        load_tile<D, T>(V, a.v, s.T, s.Hk, b, hk, j0, n);
+        load_tile<D>(K, a.k, s.T, s.Hk, b, hk, j0, n);
+        load_tile<D>(V, a.v, s.T, s.Hk, b, hk, j0, n);
         __syncthreads();
         float S[4][4];
         rows_by_rows<D>(Q, K, S);
@@ -186,7 +184,7 @@ __global__ void __launch_bounds__(THREADS) window_fwd_kernel(WindowArgs a) {
     float f[4];
 #pragma unroll
     for (int i = 0; i < 4; i++) f[i] = l[i] == 0.f ? 0.f : 1.f / l[i];
-    put_rows<D, T>(a.o, s.T, s.Hq, b, h, t0, acc, f);
+    put_rows<D>(a.o, s.T, s.Hq, b, h, t0, acc, f);
     if (a.lse && tx == 0)
 #pragma unroll
         for (int i = 0; i < 4; i++)
@@ -215,7 +213,7 @@ __global__ void __launch_bounds__(256) window_delta_kernel(WindowArgs a) {
     if (lane == 0) a.delta[((size_t)b * s.Hq + h) * s.T + t] = x;
 }
 
-template <int D, typename T>
+template <int D>
 __global__ void __launch_bounds__(THREADS) window_dq_kernel(WindowArgs a) {
     extern __shared__ __align__(16) float sh[];
     constexpr int TILE = tile_bytes<D>() / 4;
@@ -224,8 +222,8 @@ __global__ void __launch_bounds__(THREADS) window_dq_kernel(WindowArgs a) {
     const int t0 = (gridDim.x - 1 - blockIdx.x) * N, h = blockIdx.y, b = blockIdx.z, hk = h / (s.Hq / s.Hk), n = s.tokens(b);
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const KeyTiles tiles(N, s.window, s.sinks, t0, min(t0 + N, n));
-    load_tile<D, T>(Q, a.q, s.T, s.Hq, b, h, t0, n);
-    load_tile<D, T>(G, a.do_, s.T, s.Hq, b, h, t0, n);
+    load_tile<D>(Q, a.q, s.T, s.Hq, b, h, t0, n);
+    load_tile<D>(G, a.do_, s.T, s.Hq, b, h, t0, n);
     float lse[4], delta[4], acc[4][D / 16] = {};
 #pragma unroll
     for (int i = 0; i < 4; i++) {
@@ -237,8 +235,8 @@ __global__ void __launch_bounds__(THREADS) window_dq_kernel(WindowArgs a) {
     for (int it = 0; it < tiles.count(); it++) {
         const int j0 = tiles.at(it) * N;
         __syncthreads();
-        load_tile<D, T>(K, a.k, s.T, s.Hk, b, hk, j0, n);
-        load_tile<D, T>(V, a.v, s.T, s.Hk, b, hk, j0, n);
+        load_tile<D>(K, a.k, s.T, s.Hk, b, hk, j0, n);
+        load_tile<D>(V, a.v, s.T, s.Hk, b, hk, j0, n);
         __syncthreads();
         float S[4][4], dP[4][4];
         rows_by_rows<D>(Q, K, S);
@@ -254,10 +252,10 @@ __global__ void __launch_bounds__(THREADS) window_dq_kernel(WindowArgs a) {
         rows_by_cols<D>(P, K, acc);
     }
     const float f[4] = {s.scale, s.scale, s.scale, s.scale};
-    put_rows<D, T>(a.dq, s.T, s.Hq, b, h, t0, acc, f);
+    put_rows<D>(a.dq, s.T, s.Hq, b, h, t0, acc, f);
 }
 
-template <int D, typename T>
+template <int D>
 __global__ void __launch_bounds__(THREADS) window_dkv_kernel(WindowArgs a) {
     extern __shared__ __align__(16) float sh[];
     constexpr int TILE = tile_bytes<D>() / 4;
@@ -265,15 +263,15 @@ __global__ void __launch_bounds__(THREADS) window_dkv_kernel(WindowArgs a) {
     const WindowShape& s = a.s;
     const int j0 = blockIdx.x * N, hk = blockIdx.y, b = blockIdx.z, group = s.Hq / s.Hk, n = s.tokens(b);
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    load_tile<D, T>(K, a.k, s.T, s.Hk, b, hk, j0, n);
-    load_tile<D, T>(V, a.v, s.T, s.Hk, b, hk, j0, n);
+    load_tile<D>(K, a.k, s.T, s.Hk, b, hk, j0, n);
+    load_tile<D>(V, a.v, s.T, s.Hk, b, hk, j0, n);
     float dk[4][D / 16] = {}, dv[4][D / 16] = {};
     const int end = j0 < n ? queries_end(N, s.window, s.sinks, j0, n) : 0;
     for (int h = hk * group; h < (hk + 1) * group; h++)
         for (int t0 = j0; t0 < end; t0 += N) {
             __syncthreads();
-            load_tile<D, T>(Q, a.q, s.T, s.Hq, b, h, t0, n);
-            load_tile<D, T>(G, a.do_, s.T, s.Hq, b, h, t0, n);
+            load_tile<D>(Q, a.q, s.T, s.Hq, b, h, t0, n);
+            load_tile<D>(G, a.do_, s.T, s.Hq, b, h, t0, n);
             __syncthreads();
             float S[4][4], dP[4][4];  // rows: keys, columns: queries
             rows_by_rows<D>(K, Q, S);
@@ -296,8 +294,8 @@ __global__ void __launch_bounds__(THREADS) window_dkv_kernel(WindowArgs a) {
             rows_by_cols<D>(dS, Q, dk);
         }
     const float f[4] = {s.scale, s.scale, s.scale, s.scale}, one[4] = {1.f, 1.f, 1.f, 1.f};
-    put_rows<D, T>(a.dk, s.T, s.Hk, b, hk, j0, dk, f);
-    put_rows<D, T>(a.dv, s.T, s.Hk, b, hk, j0, dv, one);
+    put_rows<D>(a.dk, s.T, s.Hk, b, hk, j0, dk, f);
+    put_rows<D>(a.dv, s.T, s.Hk, b, hk, j0, dv, one);
 }
 
 template <typename K>
@@ -308,28 +306,21 @@ cudaError_t launch(K kernel, const char* name, int heads, int smem, const Window
     trace_end(st);
     return cudaGetLastError();
 }
-template <int D, typename T>
+template <int D>
 cudaError_t fwd(const WindowArgs& a, cudaStream_t st) {
-    return launch(window_fwd_kernel<D, T>, "window_fwd", a.s.Hq, 3 * tile_bytes<D>() + N * LP * 4, a, st);
+    return launch(window_fwd_kernel<D>, "window_fwd", a.s.Hq, 3 * tile_bytes<D>() + N * LP * 4, a, st);
 }
-template <int D, typename T>
+template <int D>
 cudaError_t bwd(const WindowArgs& a, cudaStream_t st) {
-    if (cudaError_t e = launch(window_dq_kernel<D, T>, "window_dq", a.s.Hq, 4 * tile_bytes<D>() + N * LP * 4, a, st)) return e;
-    return launch(window_dkv_kernel<D, T>, "window_dkv", a.s.Hk, 4 * tile_bytes<D>() + 2 * N * LP * 4, a, st);
-}
-template <typename T>
-cudaError_t fwd_of(const WindowArgs& a, cudaStream_t st) {
-    return a.s.D == 32 ? fwd<32, T>(a, st) : a.s.D == 64 ? fwd<64, T>(a, st) : fwd<128, T>(a, st);
-}
-template <typename T>
-cudaError_t bwd_of(const WindowArgs& a, cudaStream_t st) {
-    return a.s.D == 32 ? bwd<32, T>(a, st) : a.s.D == 64 ? bwd<64, T>(a, st) : bwd<128, T>(a, st);
+    if (cudaError_t e = launch(window_dq_kernel<D>, "window_dq", a.s.Hq, 4 * tile_bytes<D>() + N * LP * 4, a, st)) return e;
+    return launch(window_dkv_kernel<D>, "window_dkv", a.s.Hk, 4 * tile_bytes<D>() + 2 * N * LP * 4, a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_window_fwd(const WindowArgs& a, cudaStream_t st) {
-    return a.s.bf16 ? launch_window_fwd_tc(a, st) : fwd_of<float>(a, st);
+    if (a.s.bf16) return launch_window_fwd_tc(a, st);
+    return a.s.D == 32 ? fwd<32>(a, st) : a.s.D == 64 ? fwd<64>(a, st) : fwd<128>(a, st);
 }
 
 cudaError_t launch_window_delta(const WindowArgs& a, cudaStream_t st) {
@@ -343,7 +334,8 @@ cudaError_t launch_window_delta(const WindowArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_window_bwd(const WindowArgs& a, cudaStream_t st) {
-    return a.s.bf16 ? bwd_of<__nv_bfloat16>(a, st) : bwd_of<float>(a, st);
+    if (a.s.bf16) return launch_window_bwd_tc(a, st);
+    return a.s.D == 32 ? bwd<32>(a, st) : a.s.D == 64 ? bwd<64>(a, st) : bwd<128>(a, st);
 }
 
 }  // namespace gdr
