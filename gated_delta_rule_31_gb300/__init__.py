@@ -152,8 +152,8 @@ def lib():
         for name, at in (("gdr_window_fwd_workspace", PW), ("gdr_window_bwd_workspace", PW), ("gdr_paged_decode_workspace", PG)):
             getattr(L, name).argtypes = [at]
             getattr(L, name).restype = sz
-        L.gdr_window_fwd.argtypes = [PW] + [P] * 6 + [P, sz, st]
-        L.gdr_window_bwd.argtypes = [PW] + [P] * 10 + [P, sz, st]
+        L.gdr_window_fwd.argtypes = [PW] + [P] * 7 + [P, sz, st]
+        L.gdr_window_bwd.argtypes = [PW] + [P] * 11 + [P, sz, st]
         L.gdr_rotary.argtypes = [PR] + [P] * 4 + [st]
         L.gdr_kv_append.argtypes = [PA] + [P] * 11 + [st]
         L.gdr_paged_decode_step.argtypes = [PG] + [P] * 6 + [P, sz, st]
@@ -614,31 +614,34 @@ def window_attention_fwd(q, k, v, window=0, sinks=0, scale=None, lengths=None, s
     """Causal softmax attention with a sliding window and visible first tokens (gdr_window_fwd): query t sees token
     j <= t if t - j < window (0: any) or j < sinks. q [B,T,Hq,D] and k, v [B,T,Hk,D] bf16 or fp32, query head h with
     key head h // (Hq / Hk); lengths [B] int32 (device) or None: entry b has lengths[b] tokens and o is zero past them.
-    scale defaults to D^-1/2. Returns (o, lse), lse [B,Hq,T] fp32 (the log of the softmax's sums) with
-    save_lse=True, else None."""
+    scale defaults to D^-1/2. Returns (o, lse, rest), None for the last two unless save_lse=True: lse [B,Hq,T] fp32, the log
+    of the softmax's sums, and for bf16 rest, what the rounding of o left, both for window_attention_bwd."""
     at, sizes, dev, rows = _window_problem(q, k, v, window, sinks, scale, lengths)
     o = torch.empty_like(q) if out is None else out
     if out is not None:
         _is(out, "out", q.dtype, dev, q.shape)
     lse = torch.empty(rows, dtype=torch.float32, device=dev) if save_lse else None
+    rest = torch.empty_like(q) if save_lse and q.dtype is torch.bfloat16 else None
     ws = _scratch(sizes[0], dev, workspace)
     _call(dev, lib().gdr_window_fwd, at, q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(lengths), o.data_ptr(), _at(lse),
-          ws.data_ptr(), sizes[0])
+          _at(rest), ws.data_ptr(), sizes[0])
     _written(out)
-    return o, lse
+    return o, lse, rest
 
 
-def window_attention_bwd(q, k, v, o, lse, do, window=0, sinks=0, scale=None, lengths=None, workspace=None):
-    """VJP of window_attention_fwd for the loss <do, o> (gdr_window_bwd), from its o and lse. Returns a dict of dq, dk, dv
-    in the inputs' dtype."""
+def window_attention_bwd(q, k, v, o, lse, do, window=0, sinks=0, scale=None, lengths=None, rest=None, workspace=None):
+    """VJP of window_attention_fwd for the loss <do, o> (gdr_window_bwd), from its o, lse and, for bf16, rest (None: from o
+    as rounded). Returns a dict of dq, dk, dv in the inputs' dtype."""
     at, sizes, dev, rows = _window_problem(q, k, v, window, sinks, scale, lengths)
     _is(o, "o", q.dtype, dev, q.shape)
     _is(lse, "lse", torch.float32, dev, rows)
     _is(do, "do", q.dtype, dev, q.shape)
+    if rest is not None:
+        _is(rest, "rest", torch.bfloat16, dev, q.shape)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     ws = _scratch(sizes[1], dev, workspace)
     _call(dev, lib().gdr_window_bwd, at, q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(lengths), o.data_ptr(), lse.data_ptr(),
-          do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), sizes[1])
+          _at(rest), do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), sizes[1])
     return dict(dq=dq, dk=dk, dv=dv)
 
 

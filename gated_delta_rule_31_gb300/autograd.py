@@ -131,16 +131,16 @@ class WindowAttentionFunction(torch.autograd.Function):
     def forward(ctx, q, k, v, window, sinks, scale, lengths):
         ctx.kw = dict(window=window, sinks=sinks, scale=scale)
         keep = any(ctx.needs_input_grad)
-        o, lse = window_attention_fwd(q, k, v, lengths=lengths, save_lse=keep, **ctx.kw)
+        o, lse, rest = window_attention_fwd(q, k, v, lengths=lengths, save_lse=keep, **ctx.kw)
         if keep:
-            ctx.save_for_backward(q, k, v, o, lse, lengths)
+            ctx.save_for_backward(q, k, v, o, lse, rest, lengths)
         return o
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, do):
-        q, k, v, o, lse, lengths = ctx.saved_tensors
-        gr = window_attention_bwd(q, k, v, o, lse, do.to(q.dtype).contiguous(), lengths=lengths, **ctx.kw)
+        q, k, v, o, lse, rest, lengths = ctx.saved_tensors
+        gr = window_attention_bwd(q, k, v, o, lse, do.to(q.dtype).contiguous(), lengths=lengths, rest=rest, **ctx.kw)
         return gr["dq"], gr["dk"], gr["dv"], None, None, None, None
 
 

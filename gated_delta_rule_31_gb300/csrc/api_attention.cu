@@ -99,17 +99,18 @@ extern "C" {
 size_t gdr_window_fwd_workspace(const gdr_window_problem* p) { return check_window(p) == GDR_OK ? 256 : 0; }
 
 gdr_status gdr_window_fwd(const gdr_window_problem* p, const void* q, const void* k, const void* v, const int* lengths,
-                          void* o, float* lse, void* ws, size_t ws_bytes, gdr_stream_t stream) {
+                          void* o, float* lse, void* rest, void* ws, size_t ws_bytes, gdr_stream_t stream) {
     gdr_status r = check_window(p);
     if (r != GDR_OK) return r;
     const bool empty = p->B == 0 || p->T == 0;
-    if ((r = check_ptrs(empty, 16, {q, k, v, o}, {})) != GDR_OK) return r;
+    if ((r = check_ptrs(empty, 16, {q, k, v, o}, {rest})) != GDR_OK) return r;
+    if (rest && p->dtype != GDR_BF16) return GDR_ERR_INVALID_ARG;
     if (!on(lse, 4) || !on(lengths, 4)) return GDR_ERR_INVALID_ARG;
     if ((r = check_ws(ws, ws_bytes, gdr_window_fwd_workspace(p))) != GDR_OK) return r;
     cudaStream_t st = (cudaStream_t)stream;
     if (empty) return of(cudaMemsetAsync(ws, 0, 256, st));
     WindowArgs a = window_args(p, lengths);
-    a.q = q; a.k = k; a.v = v; a.o = o; a.lse = lse;
+    a.q = q; a.k = k; a.v = v; a.o = o; a.lse = lse; a.rest = rest;
     a.status = static_cast<int*>(ws);
     return of(launch_window_fwd(a, st));
 }
@@ -119,23 +120,23 @@ size_t gdr_window_bwd_workspace(const gdr_window_problem* p) {
 }
 
 gdr_status gdr_window_bwd(const gdr_window_problem* p, const void* q, const void* k, const void* v, const int* lengths,
-                          const void* o, const float* lse, const void* do_, void* dq, void* dk, void* dv, void* ws,
-                          size_t ws_bytes, gdr_stream_t stream) {
+                          const void* o, const float* lse, const void* rest, const void* do_, void* dq, void* dk,
+                          void* dv, void* ws, size_t ws_bytes, gdr_stream_t stream) {
     gdr_status r = check_window(p);
     if (r != GDR_OK) return r;
     const bool empty = p->B == 0 || p->T == 0;
-    if ((r = check_ptrs(empty, 16, {q, k, v, o, do_, dq, dk, dv}, {})) != GDR_OK) return r;
+    if ((r = check_ptrs(empty, 16, {q, k, v, o, do_, dq, dk, dv}, {rest})) != GDR_OK) return r;
+    if (rest && p->dtype != GDR_BF16) return GDR_ERR_INVALID_ARG;
     if ((!lse && !empty) || !on(lse, 4) || !on(lengths, 4)) return GDR_ERR_INVALID_ARG;
     if ((r = check_ws(ws, ws_bytes, gdr_window_bwd_workspace(p))) != GDR_OK) return r;
     cudaStream_t st = (cudaStream_t)stream;
     if (empty) return of(cudaMemsetAsync(ws, 0, 256, st));
     WindowArgs a = window_args(p, lengths);
-    a.q = q; a.k = k; a.v = v; a.o = const_cast<void*>(o); a.lse = const_cast<float*>(lse);
+    a.q = q; a.k = k; a.v = v; a.o = const_cast<void*>(o); a.lse = const_cast<float*>(lse); a.rest = const_cast<void*>(rest);
     a.do_ = do_; a.dq = dq; a.dk = dk; a.dv = dv;
     a.status = static_cast<int*>(ws);
     a.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256);
     a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256 + rows_bytes(p));
-    if (launch_window_delta(a, st) != cudaSuccess) return GDR_ERR_CUDA;
     return of(launch_window_bwd(a, st));
 }
 

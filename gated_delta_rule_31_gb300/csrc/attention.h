@@ -51,6 +51,7 @@ struct WindowArgs {
     const void *q, *k, *v;
     void* o;
     float* lse;   // [B, Hq, T], or null (forward)
+    void* rest;   // bf16: what the rounding of o left [B, T, Hq, D], or null
     // VJP
     const void *do_;
     float* delta;  // [B, Hq, T] sum of do o over the channels
@@ -60,7 +61,6 @@ struct WindowArgs {
 };
 cudaError_t launch_window_fwd(const WindowArgs& a, cudaStream_t st);
 size_t window_parts_bytes(const WindowShape& s);
-cudaError_t launch_window_delta(const WindowArgs& a, cudaStream_t st);
 cudaError_t launch_window_bwd(const WindowArgs& a, cudaStream_t st);
 
 // Rows of heads: q (and k) with their first 2 `pairs` channels turned, v as it is.

@@ -1,5 +1,5 @@
 // window.cu - softmax attention with a sliding window and visible first tokens (gdr_window_fwd, gdr_window_bwd): the launches,
-// delta, and fp32 problems on the CUDA cores: tiles of 64 queries and 64 keys in shared memory, all arithmetic in fp32.
+// and fp32 problems on the CUDA cores: tiles of 64 queries and 64 keys in shared memory, all arithmetic in fp32.
 //
 // Forward, a CTA for each (64 queries, head, entry): with the running maximum m and sum l of each row, per tile
 //     S = scale Q K^T,  m' = max(m, max S),  P = exp(S - m'),  l <- exp(m - m') l + sum P,  O <- exp(m - m') O + P V.
@@ -8,7 +8,6 @@
 //     dv = P^T do, dk = scale dS^T q over the queries that see a tile of keys, of all heads that share it.
 // The two walk the pairs separately, 7 products for the 5 that one walk would need, so that neither adds into
 // memory that another CTA adds into: the order of every sum is fixed.
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -25,10 +24,6 @@ namespace {
 constexpr int N = 64, THREADS = 256, LP = N + 4;  // tokens of a tile, row stride of P
 
 __device__ __forceinline__ float4 get4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 get4(const __nv_bfloat16* p) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    return make_float4(bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y));
-}
 
 // Rows t0 .. t0 + 63 of one head of x [B, T, H, D] into shared memory; rows from n on are zero.
 template <int D>
@@ -193,7 +188,6 @@ __global__ void __launch_bounds__(THREADS) window_fwd_kernel(WindowArgs a) {
 }
 
 // delta [B, Hq, T]: 8 lanes a row.
-template <typename T>
 __global__ void __launch_bounds__(256) window_delta_kernel(WindowArgs a) {
     const WindowShape& s = a.s;
     const size_t row = ((size_t)blockIdx.x * 256 + threadIdx.x) / 8, rows = (size_t)s.B * s.T * s.Hq;
@@ -205,7 +199,7 @@ __global__ void __launch_bounds__(256) window_delta_kernel(WindowArgs a) {
     float x = 0.f;
     if (t < s.tokens(b))
         for (int d = 4 * lane; d < s.D; d += 32) {
-            const float4 u = get4(static_cast<const T*>(a.do_) + row * s.D + d), v = get4(static_cast<const T*>(a.o) + row * s.D + d);
+            const float4 u = get4(static_cast<const float*>(a.do_) + row * s.D + d), v = get4(static_cast<const float*>(a.o) + row * s.D + d);
             x += u.x * v.x + u.y * v.y + u.z * v.z + u.w * v.w;
         }
     const uint32_t group = 0xffu << (threadIdx.x & 24);
@@ -310,6 +304,13 @@ template <int D>
 cudaError_t fwd(const WindowArgs& a, cudaStream_t st) {
     return launch(window_fwd_kernel<D>, "window_fwd", a.s.Hq, 3 * tile_bytes<D>() + N * LP * 4, a, st);
 }
+cudaError_t delta(const WindowArgs& a, cudaStream_t st) {
+    const size_t rows = (size_t)a.s.B * a.s.T * a.s.Hq;
+    trace_begin("window_delta", st);
+    window_delta_kernel<<<(unsigned)((rows + 31) / 32), 256, 0, st>>>(a);
+    trace_end(st);
+    return cudaGetLastError();
+}
 template <int D>
 cudaError_t bwd(const WindowArgs& a, cudaStream_t st) {
     if (cudaError_t e = launch(window_dq_kernel<D>, "window_dq", a.s.Hq, 4 * tile_bytes<D>() + N * LP * 4, a, st)) return e;
@@ -323,18 +324,9 @@ cudaError_t launch_window_fwd(const WindowArgs& a, cudaStream_t st) {
     return a.s.D == 32 ? fwd<32>(a, st) : a.s.D == 64 ? fwd<64>(a, st) : fwd<128>(a, st);
 }
 
-cudaError_t launch_window_delta(const WindowArgs& a, cudaStream_t st) {
-    const size_t rows = (size_t)a.s.B * a.s.T * a.s.Hq;
-    trace_begin("window_delta", st);
-    const unsigned blocks = (unsigned)((rows + 31) / 32);
-    if (a.s.bf16) window_delta_kernel<__nv_bfloat16><<<blocks, 256, 0, st>>>(a);
-    else window_delta_kernel<float><<<blocks, 256, 0, st>>>(a);
-    trace_end(st);
-    return cudaGetLastError();
-}
-
 cudaError_t launch_window_bwd(const WindowArgs& a, cudaStream_t st) {
     if (a.s.bf16) return launch_window_bwd_tc(a, st);
+    if (cudaError_t e = delta(a, st)) return e;
     return a.s.D == 32 ? bwd<32>(a, st) : a.s.D == 64 ? bwd<64>(a, st) : bwd<128>(a, st);
 }
 

@@ -10,6 +10,7 @@
 // dkv forms S^T and dP^T (rows: keys), so that P^T and dS^T, over them in TMEM as bf16, are the operands of the sums as
 // they are. In order per pair: dV, the next pair's S^T, dK, the next dP^T: each half has the other's time to wait for the
 // rows' arithmetic. dq keeps two S, and puts dS over the one that is done with: dP of the next pair, dQ, S of the pair after it.
+// dq comes first and forms delta too, from the copy of do that it has.
 // Eight warps do the arithmetic, a thread for a row and half of the columns; 8 copies tiles in, 9 issues products, and in dkv 10 fetches
 // lse and delta, which lie along the columns there. Units are taken in turn by CTAs that stay, longest first, as one stream.
 //
@@ -47,7 +48,9 @@ struct GradArgs {
     int cut, pieces_cut;  // key tiles from the start, pieces of each
     int pieces;           // pieces of the others
     long long units;
-    const float *lse, *delta;
+    const float* lse;
+    const void *o, *rest;
+    float* delta;
     void *dq, *dk, *dv;
     float* parts;  // of a cut key tile's pieces: dv, dk [2, 128, D] each
     int* status;
@@ -176,6 +179,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t sb = smem_u32(sm);
     __shared__ Bars bar;
     __shared__ __align__(16) float2 stats[KEYS ? 2 : 1][KEYS ? C : 1];  // (- log2 e lse, - delta) of the queries
+    __shared__ float half_sums[KEYS ? 1 : 2][2][KEYS ? 1 : C];  // of do o over the channels
     __shared__ uint32_t tmem_sh;
     __shared__ int failed, used[SLOTS], used_keep[2];
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -185,6 +189,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         return;
     }
     if (tid == 0) {
+        if (!KEYS && blockIdx.x == 0)
+            for (int i = 0; i < 4; i++) a.status[i] = 0;  // a wait expires a second later at the earliest
         failed = 0;
         for (int i = 0; i < SLOTS; i++) {
             used[i] = 0;
@@ -194,7 +200,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int i = 0; i < 2; i++) {
             used_keep[i] = 0;
             mbar_init(&bar.keep[i], 1);
-            mbar_init(&bar.kept[i], 1);
+            mbar_init(&bar.kept[i], !KEYS && i == 1 ? 9 : 1);  // dq: do is read by the rows' warps too
             mbar_init(&bar.sfull[i], 1);
             mbar_init(&bar.lfull[i], 32);
             mbar_init(&bar.lfree[i], 8);
@@ -394,9 +400,36 @@ __global__ void __launch_bounds__(THREADS, 1)
             if constexpr (!KEYS) {
                 const int t = x.t0 + row;
                 const size_t at = ((size_t)x.b * s.Hq + x.h) * s.T + t;
-                const float l = t < n ? -LOG2E * a.lse[at] : 0.f, d = t < n ? -a.delta[at] : 0.f;
+                const float l = t < n ? -LOG2E * a.lse[at] : 0.f;
                 b2 = pair(l, l);
-                d2 = pair(d, d);
+                if (count > 0) {
+                    // a thread's half of the row's do o: channels 64 half .. (32 half .. of at most 64)
+                    const int width = s.D > 64 ? 64 : s.D / 2, from = width * half;
+                    const size_t to = (((size_t)x.b * s.T + t) * s.Hq + x.h) * s.D + from;
+                    const __nv_bfloat16 *o = static_cast<const __nv_bfloat16*>(a.o) + to, *rest = static_cast<const __nv_bfloat16*>(a.rest) + to;
+                    float sum = 0.f;
+                    ok = wait_phase(&bar.keep[1], units & 1, &failed, 101);
+                    if (ok && t < n)
+#pragma unroll 4
+                        for (int e = 0; e < width; e += 8) {
+                            float y[8], z[8] = {}, g[8];
+                            unpack8(*reinterpret_cast<const uint4*>(o + e), y);
+                            if (a.rest) unpack8(*reinterpret_cast<const uint4*>(rest + e), z);
+                            unpack8(ld_shared_v4(sb + TILE + sw128_chunk(row, (from + e) / 8, C)), g);
+#pragma unroll
+                            for (int k = 0; k < 8; k++) sum = fmaf(g[k], y[k] + z[k], sum);
+                        }
+                    half_sums[units & 1][half][row] = sum;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.kept[1]);
+                    if (bar_sync_or(1, 256, !ok)) {  // all go on, or none
+                        ok = false;
+                        break;
+                    }
+                    const float d = -(half_sums[units & 1][0][row] + half_sums[units & 1][1][row]);
+                    d2 = pair(d, d);
+                    if (half == 0 && t < n) a.delta[at] = -d;
+                }
             }
 #pragma unroll 1
             for (int i = 0; i < count; i++, np++) {
@@ -618,6 +651,8 @@ cudaError_t launch_window_bwd_tc(const WindowArgs& x, cudaStream_t st) {
     a.pieces_cut = cut.pieces_cut;
     a.pieces = cut.pieces;
     a.lse = x.lse;
+    a.o = x.o;
+    a.rest = x.rest;
     a.delta = x.delta;
     a.dq = x.dq;
     a.dk = x.dk;

@@ -12,7 +12,7 @@
 // order P0 V, the next S0, P1 V, the next S1. m is moved, and O and l scaled by 2^(c m - c m'), only when the row's
 // maximum has grown by more than 8 / c: until then P is at most 2^8, as exact in bf16 as below one, and the sums in
 // fp32 have the room; most tiles then need no pass over O. The order of tiles and units is fixed by the shape.
-// Rounding to bf16: P, and the result.
+// Rounding to bf16: P, and the result (what that leaves may be kept for the VJP).
 //
 // Warps 0-3 and 4-7 take the query tiles, 8 copies tiles in (Q of the next unit as soon as the last S of this one has read it,
 // K and V in a ring of five slots), 9 issues the products. The stream of tiles runs through the units without a
@@ -47,7 +47,7 @@ struct FwdArgs {
     int pair_heads;     // a unit's two tiles are heads h, h + 1 of a row tile; else row tiles 2 i, 2 i + 1 of a head
     int row_tiles;      // of the sequence
     long long units;
-    void* o;
+    void *o, *rest;
     float* lse;
     int* status;
 };
@@ -378,7 +378,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             const bool there = t < n;
             const float f = there ? 1.f / l : 0.f;
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + (((size_t)x.b * s.T + t) * s.Hq + head) * s.D;
+            const size_t at = (((size_t)x.b * s.T + t) * s.Hq + head) * s.D;
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16*>(a.o) + at, *rest = static_cast<__nv_bfloat16*>(a.rest) + at;
 #pragma unroll 1
             for (int e = 0; e < s.D; e += 32) {
                 float o[32];
@@ -388,8 +389,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 if (t < s.T)
 #pragma unroll
-                    for (int k = 0; k < 32; k += 8)
-                        *reinterpret_cast<uint4*>(out + e + k) = there ? pack8(o + k, f) : make_uint4(0, 0, 0, 0);
+                    for (int k = 0; k < 32; k += 8) {
+                        const uint4 y = there ? pack8(o + k, f) : make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(out + e + k) = y;
+                        if (a.rest) {
+                            float z[8];
+                            unpack8(y, z);
+#pragma unroll
+                            for (int d = 0; d < 8; d++) z[d] = there ? fmaf(f, o[k + d], -z[d]) : 0.f;
+                            *reinterpret_cast<uint4*>(rest + e + k) = pack8(z, 1.f);
+                        }
+                    }
             }
             if (count > 0) {
                 tc_fence_before();
@@ -430,6 +440,7 @@ cudaError_t launch_window_fwd_tc(const WindowArgs& x, cudaStream_t st) {
     a.units = (long long)x.s.B * (a.pair_heads ? (long long)x.s.Hq / 2 * a.row_tiles : (long long)x.s.Hq * ((a.row_tiles + 1) / 2));
     a.o = x.o;
     a.lse = x.lse;
+    a.rest = x.rest;
     a.status = x.status;
     trace_begin("window_fwd_tc", st);
     window_fwd_tc_kernel<<<(unsigned)(a.units < SMS ? a.units : SMS), THREADS, BYTES, st>>>(mq, mk, mv, a);

@@ -364,7 +364,7 @@ gdr_status gdr_group_norm_bwd(const gdr_norm_problem* p, const void* x, const vo
  * not finite at a token that is there may reach every query of the blocks of 128 that a query seeing it
  * is in, also those that do not see it.
  * Rounding: sums, maxima and softmax statistics are fp32. With BF16 each result is rounded once, and
- * so are p and the scores' gradient as operands of the tensor cores; the VJP takes o as rounded. */
+ * so are p and the scores' gradient as operands of the tensor cores. */
 #define GDR_WINDOW_MAX_T (1 << 24)
 
 typedef struct {
@@ -374,18 +374,20 @@ typedef struct {
     float scale; /* > 0 */
 } gdr_window_problem;
 
-/* Forward: o and, if lse != NULL, lse. Workspace: gdr_window_fwd_workspace() bytes, 256-byte aligned (0:
- * invalid problem); its first 256 bytes hold the status word, which this call and the VJP clear and then
- * set, and gdr_workspace_status() reads. */
+/* Forward: o and, if lse != NULL, lse, and if rest != NULL (BF16 only), rest [B, T, Hq, D] of `dtype`, what the
+ * rounding of o left: the VJP's row sums of do o come from o + rest, without it from o as rounded, which alone
+ * takes dq and dk of short sequences from 0.0024 of their norm off to 0.0029.
+ * Workspace: gdr_window_fwd_workspace() bytes, 256-byte aligned (0: invalid problem); its first 256 bytes hold
+ * the status word, which this call and the VJP clear and then set, and gdr_workspace_status() reads. */
 size_t gdr_window_fwd_workspace(const gdr_window_problem* p);
 gdr_status gdr_window_fwd(const gdr_window_problem* p, const void* q, const void* k, const void* v, const int* lengths,
-                          void* o, float* lse, void* ws, size_t ws_bytes, gdr_stream_t stream);
+                          void* o, float* lse, void* rest, void* ws, size_t ws_bytes, gdr_stream_t stream);
 
-/* VJP for the loss <do, o>, from the forward's o and lse. Deterministic: no floating-point atomics. */
+/* VJP for the loss <do, o>, from the forward's o, lse and rest (or NULL). Deterministic: no floating-point atomics. */
 size_t gdr_window_bwd_workspace(const gdr_window_problem* p);
 gdr_status gdr_window_bwd(const gdr_window_problem* p, const void* q, const void* k, const void* v, const int* lengths,
-                          const void* o, const float* lse, const void* do_, void* dq, void* dk, void* dv, void* ws,
-                          size_t ws_bytes, gdr_stream_t stream);
+                          const void* o, const float* lse, const void* rest, const void* do_, void* dq, void* dk,
+                          void* dv, void* ws, size_t ws_bytes, gdr_stream_t stream);
 
 /* Rotary positions. Of the D channels of each head the first 2 * pairs are turned by pairs: (i, i + pairs), or
  * (2 i, 2 i + 1) with interleaved, by the angle positions[b, t, axis of i] * inv_freq[i] (its negative with

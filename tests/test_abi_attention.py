@@ -59,25 +59,29 @@ HEADS = [(dict(Hq=3), INVALID), (dict(Hk=0), INVALID), (dict(Hq=0), INVALID), (d
                                              (dict(B=60000, T=1 << 24, Hq=64, Hk=64), UNSUPPORTED)])
 def test_window_problem(L, kw, code):
     p = window(**kw)
-    assert L.gdr_window_fwd(p, *put(6), FAKE, BIG, None) == code
-    assert L.gdr_window_bwd(p, *put(10), FAKE, BIG, None) == code
+    assert L.gdr_window_fwd(p, *put(7), FAKE, BIG, None) == code
+    assert L.gdr_window_bwd(p, *put(11), FAKE, BIG, None) == code
     assert L.gdr_window_fwd_workspace(p) == 0 and L.gdr_window_bwd_workspace(p) == 0
 
 
 def test_window_pointers(L):
     p = window()
-    assert L.gdr_window_fwd(None, *put(6), FAKE, BIG, None) == INVALID
+    assert L.gdr_window_fwd(None, *put(7), FAKE, BIG, None) == INVALID
     assert L.gdr_window_fwd_workspace(None) == 0
     for i in (0, 1, 2, 4):  # q, k, v, o
         for bad in (None, MISALIGNED):
-            assert L.gdr_window_fwd(p, *put(6, **{f"p{i}": bad}), FAKE, BIG, None) == INVALID, i
+            assert L.gdr_window_fwd(p, *put(7, **{f"p{i}": bad}), FAKE, BIG, None) == INVALID, i
     for i in (3, 5):  # lengths, lse
-        assert L.gdr_window_fwd(p, *put(6, **{f"p{i}": ODD}), FAKE, BIG, None) == INVALID, i
-    for i in (0, 1, 2, 4, 6, 7, 8, 9):  # q, k, v, o, do, dq, dk, dv
+        assert L.gdr_window_fwd(p, *put(7, **{f"p{i}": ODD}), FAKE, BIG, None) == INVALID, i
+    assert L.gdr_window_fwd(p, *put(7, p6=MISALIGNED), FAKE, BIG, None) == INVALID  # rest
+    assert L.gdr_window_bwd(p, *put(11, p6=MISALIGNED), FAKE, BIG, None) == INVALID
+    assert L.gdr_window_fwd(window(dtype=0), *put(7), FAKE, BIG, None) == INVALID  # of bf16 only
+    assert L.gdr_window_bwd(window(dtype=0), *put(11), FAKE, BIG, None) == INVALID
+    for i in (0, 1, 2, 4, 7, 8, 9, 10):  # q, k, v, o, do, dq, dk, dv
         for bad in (None, MISALIGNED):
-            assert L.gdr_window_bwd(p, *put(10, **{f"p{i}": bad}), FAKE, BIG, None) == INVALID, i
-    assert L.gdr_window_bwd(p, *put(10, p5=None), FAKE, BIG, None) == INVALID  # lse
-    for f, n, need in ((L.gdr_window_fwd, 6, L.gdr_window_fwd_workspace(p)), (L.gdr_window_bwd, 10, L.gdr_window_bwd_workspace(p))):
+            assert L.gdr_window_bwd(p, *put(11, **{f"p{i}": bad}), FAKE, BIG, None) == INVALID, i
+    assert L.gdr_window_bwd(p, *put(11, p5=None), FAKE, BIG, None) == INVALID  # lse
+    for f, n, need in ((L.gdr_window_fwd, 7, L.gdr_window_fwd_workspace(p)), (L.gdr_window_bwd, 11, L.gdr_window_bwd_workspace(p))):
         assert need > 0
         assert f(p, *put(n), FAKE, ctypes.c_size_t(need - 1), None) == WORKSPACE
         assert f(p, *put(n), None, BIG, None) == WORKSPACE
