@@ -200,7 +200,7 @@ gdr_status gdr_kv_append(const gdr_append_problem* p, const void* q, const void*
 }
 
 size_t gdr_paged_decode_workspace(const gdr_paged_problem* p) {
-    return check_paged(p) == GDR_OK ? 256 + paged_parts_bytes(p->B, p->Hq, p->Hk, p->D) : 0;
+    return check_paged(p) == GDR_OK ? 256 + paged_parts_bytes(p->D) : 0;
 }
 
 gdr_status gdr_paged_decode_step(const gdr_paged_problem* p, const void* q, const void* k_cache, const void* v_cache,

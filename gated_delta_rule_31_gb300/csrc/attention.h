@@ -92,7 +92,7 @@ struct PagedArgs {
     void* o;
     float* parts;
 };
-size_t paged_parts_bytes(int B, int Hq, int Hk, int D);
+size_t paged_parts_bytes(int D);
 cudaError_t launch_paged_step(const PagedArgs& a, cudaStream_t st);
 
 }  // namespace gdr

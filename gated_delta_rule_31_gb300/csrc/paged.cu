@@ -1,11 +1,20 @@
 // paged.cu - attention of one new token of each sequence over a paged cache (gdr_paged_decode_step).
 //
 // Entry b with n tokens sees tokens j >= n - window and j < sinks: a list of `first` tokens from the start and those
-// from lo on, cut into tiles of 64. The tiles of all entries and key heads in a row (entries outermost) are dealt
-// out evenly, a run of neighbouring tiles to each CTA, whatever the lengths, which only the device knows. A CTA
-// walks its run with the running maximum m and sum l of a softmax and the sum O of exp(s - m) v for the heads that share a key
-// head; a head whose tiles lie in one run is written at once, of one that is cut each run leaves (m, l, O), and a second
-// kernel joins them, runs in order: o = sum exp(m_i - m) O_i / sum exp(m_i - m) l_i.
+// from lo on, cut into tiles. The tiles of all entries and key heads in a row (entries outermost) are dealt out evenly, a run
+// of neighbouring tiles to each CTA, whatever the lengths, which only the device knows. A CTA walks its run with the running
+// maximum m and sum l of a softmax and the sum O of 2^(s - m) v (s in units of log 2) for the heads that share a key head, 8 at a
+// time; a walk whose tiles lie in one run is written at once, of one that is cut each run leaves (m, l, O), and a second
+// kernel joins them, runs in order: o = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i.
+//
+// bf16: each of the four warps takes every fourth 8 KB of K and of V (16 tokens at D = 128) on its own, copied three steps
+// ahead into its own part of shared memory, across walks too, so no warp waits for another before a walk ends. A row's
+// place comes from the page table a step before that. Products by mma.m16n8k16 with the 8 heads as columns, S^T = K q^T and
+// O^T += V^T P^T: the tokens are rows, so no row is spent on heads that are not there, and a thread keeps the same two heads
+// in S, m, l and O. m moves when a score has grown past it by 8 (a weight is at most 2^8 then, exact to bf16 as any), which
+// one vote tells; otherwise lanes exchange nothing. HBM bounds it: 4 operations a byte and head, a few percent of the
+// products' rate. (tcgen05 would take 128 rows for the 8.)
+// fp32: a CTA for each run as well, products on the CUDA cores.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -21,16 +30,12 @@ namespace gdr {
 
 namespace {
 
-constexpr int TILE = 64, THREADS = 128, HEADS = 8;  // tokens of a tile, heads that share a walk
-constexpr int RUNS = 2 * 152;                        // CTAs
+constexpr int THREADS = 128, HEADS = 8;  // heads that share a walk
+constexpr int RUNS = 2 * 152;            // CTAs
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr int kTile32 = 64;  // tokens of a tile of fp32
 
 __device__ __forceinline__ float4 get4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 get4(const __nv_bfloat16* p) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    return make_float4(bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y));
-}
-__device__ __forceinline__ float as_float(float x) { return x; }
-__device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
@@ -45,22 +50,22 @@ struct Seen {
         count = first + n - lo;
     }
     __device__ int at(int i) const { return i < first ? i : lo + (i - first); }
-    __device__ int tiles() const { return (count + TILE - 1) / TILE; }
+    __device__ int tiles(int tile) const { return (count + tile - 1) / tile; }
 };
 
-// Which entry and how far into it: entry, tiles before it per walk (a walk is a key head's block of heads).
+// An entry, and the tiles of the entries before it for each walk (a walk is a key head's block of heads).
 struct Place {
     int b;
     long long before;
 };
 
-// Tiles of all entries, per walk, and the places of two tiles (numbered over all entries and walks), by all threads of a CTA of THREADS.
-__device__ long long find(const PagedArgs& a, int walks, int run, int runs, Place& from, long long& begin, long long& end) {
+// The tiles of all entries and walks, those of a run among them and the entry where it begins, by all THREADS threads.
+__device__ long long find(const PagedArgs& a, int tile, int walks, int run, int runs, Place& from, long long& begin, long long& end) {
     __shared__ long long total_sh, part[THREADS / 32];
     __shared__ Place from_sh;
     const int tid = threadIdx.x, per = (a.B + THREADS - 1) / THREADS;
     long long mine = 0;
-    for (int b = tid * per; b < min(a.B, (tid + 1) * per); b++) mine += Seen(a, b).tiles();
+    for (int b = tid * per; b < min(a.B, (tid + 1) * per); b++) mine += Seen(a, b).tiles(tile);
     long long scan = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -78,7 +83,7 @@ __device__ long long find(const PagedArgs& a, int walks, int run, int runs, Plac
     end = total * (run + 1) / runs;
     if (before * walks <= begin && begin < (before + mine) * walks)
         for (int b = tid * per; b < min(a.B, (tid + 1) * per); b++) {
-            const long long t = Seen(a, b).tiles();
+            const long long t = Seen(a, b).tiles(tile);
             if (begin < (before + t) * walks) {
                 from_sh = Place{b, before};
                 break;
@@ -90,22 +95,24 @@ __device__ long long find(const PagedArgs& a, int walks, int run, int runs, Plac
     return total;
 }
 
-template <int D, typename T>
-__global__ void __launch_bounds__(THREADS) paged_kernel(PagedArgs a, int blocks) {
+// ---- fp32
+
+template <int D>
+__global__ void __launch_bounds__(THREADS) paged_f32_kernel(PagedArgs a, int blocks) {
     extern __shared__ __align__(16) float sh[];
     constexpr int LD = D + 4;
-    float *K = sh, *V = K + TILE * LD, *Q = V + TILE * LD, *P = Q + HEADS * LD;
+    float *K = sh, *V = K + kTile32 * LD, *Q = V + kTile32 * LD, *P = Q + HEADS * LD;
     __shared__ float m_sh[HEADS], l_sh[HEADS], fade_sh[HEADS];
     linear::next_kernel_may_start();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = a.Hq / a.Hk, walks = a.Hk * blocks;
     Place at;
     long long begin, end;
-    find(a, walks, blockIdx.x, gridDim.x, at, begin, end);
+    find(a, kTile32, walks, blockIdx.x, gridDim.x, at, begin, end);
     long long tile = begin;
     int segment = 0;
     while (tile < end) {
         const Seen seen(a, at.b);
-        const int tiles = seen.tiles();
+        const int tiles = seen.tiles(kTile32);
         if (tile >= (at.before + tiles) * walks) {
             at.before += tiles;
             at.b++;
@@ -117,7 +124,7 @@ __global__ void __launch_bounds__(THREADS) paged_kernel(PagedArgs a, int blocks)
         const size_t q0 = (size_t)at.b * a.Hq + hk * group + g0;
         __syncthreads();
         for (int i = tid; i < HEADS * D; i += THREADS)
-            Q[i / D * LD + i % D] = i / D < ng ? a.scale * as_float(static_cast<const T*>(a.q)[q0 * D + i]) : 0.f;
+            Q[i / D * LD + i % D] = i / D < ng ? LOG2E * a.scale * static_cast<const float*>(a.q)[q0 * D + i] : 0.f;
         if (tid < HEADS) {
             m_sh[tid] = -INFINITY;
             l_sh[tid] = 0.f;
@@ -127,8 +134,8 @@ __global__ void __launch_bounds__(THREADS) paged_kernel(PagedArgs a, int blocks)
         for (int i = 0; i < HEADS * D / THREADS; i++) acc[i] = 0.f;
         for (int t = t0; t < t1; t++) {
             __syncthreads();
-            for (int i = tid; i < TILE * D / 4; i += THREADS) {
-                const int r = i / (D / 4), c = i % (D / 4) * 4, x = t * TILE + r;
+            for (int i = tid; i < kTile32 * D / 4; i += THREADS) {
+                const int r = i / (D / 4), c = i % (D / 4) * 4, x = t * kTile32 + r;
                 float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
                 bool on = x < seen.count;
                 if (on) {
@@ -136,8 +143,8 @@ __global__ void __launch_bounds__(THREADS) paged_kernel(PagedArgs a, int blocks)
                     on = (unsigned)page < (unsigned)a.pages;
                     if (on) {
                         const size_t row = (((size_t)page * a.page_size + j % a.page_size) * a.Hk + hk) * D + c;
-                        k = get4(static_cast<const T*>(a.k) + row);
-                        v = get4(static_cast<const T*>(a.v) + row);
+                        k = get4(static_cast<const float*>(a.k) + row);
+                        v = get4(static_cast<const float*>(a.v) + row);
                     }
                 }
                 *reinterpret_cast<float4*>(K + r * LD + c) = k;
@@ -146,10 +153,10 @@ __global__ void __launch_bounds__(THREADS) paged_kernel(PagedArgs a, int blocks)
             }
             __syncthreads();
             for (int g = warp; g < ng; g += THREADS / 32) {  // a warp per head, two tokens a lane
-                float s[TILE / 32];
+                float s[kTile32 / 32];
                 float top = m_sh[g], sum = 0.f;
 #pragma unroll
-                for (int i = 0; i < TILE / 32; i++) {
+                for (int i = 0; i < kTile32 / 32; i++) {
                     const float* k = K + (lane + 32 * i) * LD;
                     float x = 0.f;
 #pragma unroll 8
@@ -164,14 +171,14 @@ __global__ void __launch_bounds__(THREADS) paged_kernel(PagedArgs a, int blocks)
                 for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                 const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll
-                for (int i = 0; i < TILE / 32; i++) {
-                    const float p = expf(s[i] - base);
-                    P[g * TILE + lane + 32 * i] = p;
+                for (int i = 0; i < kTile32 / 32; i++) {
+                    const float p = exp2f(s[i] - base);
+                    P[g * kTile32 + lane + 32 * i] = p;
                     sum += p;
                 }
                 sum = warp_sum(sum);
                 if (lane == 0) {
-                    fade_sh[g] = expf(m_sh[g] - base);
+                    fade_sh[g] = exp2f(m_sh[g] - base);
                     l_sh[g] = fade_sh[g] * l_sh[g] + sum;
                     m_sh[g] = top;
                 }
@@ -183,7 +190,7 @@ __global__ void __launch_bounds__(THREADS) paged_kernel(PagedArgs a, int blocks)
                 if (g >= ng) continue;
                 float x = fade_sh[g] * acc[i];
 #pragma unroll 8
-                for (int j = 0; j < TILE; j++) x = fmaf(P[g * TILE + j], V[j * LD + tid % D], x);
+                for (int j = 0; j < kTile32; j++) x = fmaf(P[g * kTile32 + j], V[j * LD + tid % D], x);
                 acc[i] = x;
             }
         }
@@ -194,7 +201,7 @@ __global__ void __launch_bounds__(THREADS) paged_kernel(PagedArgs a, int blocks)
         for (int i = 0; i < HEADS * D / THREADS; i++) {
             const int g = tid / D + THREADS / D * i;
             if (g >= ng) continue;
-            if (whole) put(static_cast<T*>(a.o) + (q0 + g) * D + tid % D, l_sh[g] > 0.f ? acc[i] / l_sh[g] : 0.f);
+            if (whole) static_cast<float*>(a.o)[(q0 + g) * D + tid % D] = l_sh[g] > 0.f ? acc[i] / l_sh[g] : 0.f;
             else part[g * (D + 2) + tid % D] = acc[i];
         }
         if (!whole && tid < ng) {
@@ -207,20 +214,277 @@ __global__ void __launch_bounds__(THREADS) paged_kernel(PagedArgs a, int blocks)
     // entries without a token: zero
     for (int b = blockIdx.x; b < a.B; b += gridDim.x)
         if (Seen(a, b).count == 0)
-            for (int i = tid; i < a.Hq * D; i += THREADS) put(static_cast<T*>(a.o) + (size_t)b * a.Hq * D + i, 0.f);
+            for (int i = tid; i < a.Hq * D; i += THREADS) static_cast<float*>(a.o)[(size_t)b * a.Hq * D + i] = 0.f;
+}
+
+// ---- bf16
+
+constexpr int STAGES = 3, WARPS = THREADS / 32;
+constexpr uint32_t STEP_BYTES = 8192;  // K and V of a warp's step
+template <int D>
+constexpr int step_tokens() { return (int)STEP_BYTES / (4 * D); }
+template <int D>
+constexpr int merge_bytes() { return WARPS * HEADS * (D + 2) * 4; }
+
+template <int N>
+__device__ __forceinline__ void cp_async_wait_but() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// The transpose of an 8 x 8 tile: thread t holds values 2 (t % 4), + 1 of row t / 4, before and after.
+__device__ __forceinline__ uint32_t transpose(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A walk's tiles in a run, as one goes over them.
+struct Cursor {
+    Place at;
+    long long tile;              // the next one, numbered over all walks
+    int walk, t, t1, tiles;      // the walk, its tiles t .. t1 - 1 in this run, and how many it has
+    int first, lo, count;        // the entry's seen tokens
+    bool whole;
+    // to the walk that `tile` lies in
+    __device__ __forceinline__ void open(const PagedArgs& a, int size, int walks, long long end) {
+        for (;; at.b++) {
+            const Seen s(a, at.b);
+            tiles = s.tiles(size);
+            first = s.first;
+            lo = s.lo;
+            count = s.count;
+            if (tile < (at.before + tiles) * walks) break;
+            at.before += tiles;
+        }
+        const long long in = tile - at.before * walks;
+        walk = (int)(in / tiles);
+        t = (int)(in - (long long)walk * tiles);
+        t1 = (int)min((long long)tiles, t + end - tile);
+        whole = t == 0 && t1 == tiles;
+    }
+    __device__ __forceinline__ int token(int x) const { return x < first ? x : lo + (x - first); }
+};
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 2) paged_bf16_kernel(PagedArgs a, int blocks) {
+    constexpr int STEP = step_tokens<D>(), TILE = WARPS * STEP, CHUNKS = D / 8, M = STEP / 16;
+    extern __shared__ __align__(128) uint8_t sm[];
+    __shared__ uint32_t there[WARPS][STAGES][2];  // which tokens of a step are there, as bits
+    linear::next_kernel_may_start();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = a.Hq / a.Hk, walks = a.Hk * blocks;
+    const uint32_t ring = smem_u32(sm) + warp * STAGES * STEP_BYTES;
+    float* merge = reinterpret_cast<float*>(sm + WARPS * STAGES * STEP_BYTES);
+    Cursor in, out;
+    long long end;
+    find(a, TILE, walks, blockIdx.x, gridDim.x, in.at, in.tile, end);
+    const bool some = in.tile < end;
+    if (some) in.open(a, TILE, walks, end);
+    out = in;
+
+    // Rows of the cache that hold the warp's tokens of the cursor's tile: a lane's token, and its token 32 on.
+    constexpr uint32_t NONE = 0xffffffffu;
+    uint32_t row[2];
+    auto look_up = [&]() {
+#pragma unroll
+        for (int i = 0; i < (STEP + 31) / 32; i++) {
+            const int s = lane + 32 * i, x = in.t * TILE + warp * STEP + s;
+            row[i] = NONE;
+            if (in.tile < end && s < STEP && x < in.count) {
+                const int j = in.token(x), place = j / a.page_size, page = a.table[(size_t)in.at.b * a.table_pages + place];
+                if ((unsigned)page < (unsigned)a.pages) row[i] = (uint32_t)page * a.page_size + (j - place * a.page_size);
+            }
+        }
+    };
+    int put_at = 0;
+    auto fetch = [&]() {  // the looked up rows into the next stage; the cursor to the next tile, and its rows looked up
+        if (in.tile < end) {
+            const uint32_t to = ring + put_at * STEP_BYTES;
+            const int hk = in.walk / blocks;
+#pragma unroll
+            for (int i = 0; i < STEP * CHUNKS / 32; i++) {
+                const int r = (i * 32 + lane) / CHUNKS, ch = lane % CHUNKS;
+                const uint32_t at = __shfl_sync(0xffffffffu, row[i * (32 / CHUNKS) / 32], r & 31);
+                const bool on = at != NONE;
+                const size_t src = on ? (((size_t)at * a.Hk + hk) * D + ch * 8) * 2 : 0;
+                const uint32_t dst = to + r * (2 * D) + ((ch ^ (D == 32 ? (r >> 1) & 3 : r & 7)) << 4);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(static_cast<const uint8_t*>(a.k) + src), "r"(on ? 16 : 0) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + STEP_BYTES / 2), "l"(static_cast<const uint8_t*>(a.v) + src), "r"(on ? 16 : 0)
+                             : "memory");
+            }
+#pragma unroll
+            for (int i = 0; i < (STEP + 31) / 32; i++) {
+                const uint32_t bits = __ballot_sync(0xffffffffu, row[i] != NONE);
+                if (lane == 0) there[warp][put_at][i] = bits;
+            }
+            in.tile++;
+            if (++in.t == in.t1 && in.tile < end) in.open(a, TILE, walks, end);
+            look_up();
+        }
+        cp_async_commit();
+        put_at = put_at + 1 == STAGES ? 0 : put_at + 1;
+    };
+    if (some) {
+        look_up();
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; i++) fetch();
+    }
+
+    const float c = a.scale * LOG2E;
+    int get_at = 0, segment = 0;
+    // where this lane's rows of the products' operands lie: K rows (its 8 x 8 tiles: tokens 0-7, 8-15, then channels 8 on), V
+    // rows (tokens 0-7 twice, then 8-15)
+    const int krow = lane & 15, kch = lane >> 4, vrow = (lane & 7) + (lane >> 4) * 8, vch = lane >> 3 & 1;
+    auto swizzled = [](int r, int ch) { return (uint32_t)(r * (2 * D) + ((ch ^ (D == 32 ? (r >> 1) & 3 : r & 7)) << 4)); };
+    while (out.tile < end) {
+        const int hk = out.walk / blocks, g0 = out.walk % blocks * HEADS, ng = min(HEADS, group - g0);
+        const size_t q0 = (size_t)out.at.b * a.Hq + hk * group + g0;
+        uint32_t q[D / 8];  // column lane / 4 of q^T: channels 16 k + 2 (lane % 4), + 1, and 8 on
+#pragma unroll
+        for (int k = 0; k < D / 8; k++)
+            q[k] = lane / 4 < ng ? *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q) + (q0 + lane / 4) * D + 8 * k + 2 * (lane % 4)) : 0u;
+        float o[D / 16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // of heads 2 (lane % 4), + 1
+#pragma unroll
+        for (int d = 0; d < D / 16; d++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) o[d][e] = 0.f;
+        for (; out.t < out.t1; out.t++, out.tile++) {
+            cp_async_wait_but<STAGES - 2>();
+            __syncwarp();
+            fetch();  // over the stage that the step before has read
+            const uint32_t kt = ring + get_at * STEP_BYTES, vt = kt + STEP_BYTES / 2;
+            float s[M][4];
+#pragma unroll
+            for (int i = 0; i < M; i++) {
+#pragma unroll
+                for (int e = 0; e < 4; e++) s[i][e] = 0.f;
+#pragma unroll
+                for (int k = 0; k < D / 16; k++) {
+                    uint32_t x[4];
+                    ldmatrix_x4(kt + swizzled(16 * i + krow, 2 * k + kch), x);
+                    mma(s[i], x, q[2 * k], q[2 * k + 1]);
+                }
+            }
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < M; i++) {
+                const uint32_t bits = there[warp][get_at][i / 2] >> (i % 2 * 16 + lane / 4);
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    s[i][e] = bits >> (e / 2 * 8) & 1 ? c * s[i][e] : -INFINITY;
+                    top[e & 1] = fmaxf(top[e & 1], s[i][e]);
+                }
+            }
+            if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+#pragma unroll
+                    for (int x = 4; x < 32; x *= 2) top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], x));
+                    const float to = fmaxf(m[h], top[h]), f = to == m[h] ? 1.f : exp2_fast(m[h] - to);
+                    m[h] = to;
+                    l[h] *= f;
+#pragma unroll
+                    for (int d = 0; d < D / 16; d++) {
+                        o[d][h] *= f;
+                        o[d][2 + h] *= f;
+                    }
+                }
+            }
+            const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+            for (int i = 0; i < M; i++) {
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    s[i][e] = exp2_fast(s[i][e] - base[e & 1]);
+                    l[e & 1] += s[i][e];
+                }
+                const uint32_t p0 = transpose(pack_bf16(s[i][0], s[i][1])), p1 = transpose(pack_bf16(s[i][2], s[i][3]));
+#pragma unroll
+                for (int d = 0; d < D / 16; d++) {
+                    uint32_t x[4];
+                    ldmatrix_x4_trans(vt + swizzled(16 * i + vrow, 2 * d + vch), x);
+                    mma(o[d], x, p0, p1);
+                }
+            }
+            get_at = get_at + 1 == STAGES ? 0 : get_at + 1;
+        }
+        // the warps' sums: each to shared memory under the common maximum, then added in order
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+            for (int x = 4; x < 32; x *= 2) l[h] += __shfl_xor_sync(0xffffffffu, l[h], x);
+        __syncthreads();  // the walk before has been read
+        float* mine = merge + warp * HEADS * (D + 2);
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            float* to = mine + (2 * (lane % 4) + h) * (D + 2);
+#pragma unroll
+            for (int d = 0; d < D / 16; d++) {
+                to[16 * d + lane / 4] = o[d][h];
+                to[16 * d + 8 + lane / 4] = o[d][2 + h];
+            }
+            if (lane < 4) {
+                to[D] = m[h];
+                to[D + 1] = l[h];
+            }
+        }
+        __syncthreads();
+        float* part = a.parts + (size_t)(2 * blockIdx.x + (segment > 0)) * HEADS * (D + 2);
+        for (int i = tid; i < ng * D; i += THREADS) {
+            const int g = i / D, d = i % D;
+            const float* from = merge + g * (D + 2);
+            float mw[WARPS], top = -INFINITY, x = 0.f, sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < WARPS; w++) top = fmaxf(top, mw[w] = from[w * HEADS * (D + 2) + D]);
+            const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+            for (int w = 0; w < WARPS; w++) {
+                const float f = exp2_fast(mw[w] - base);
+                x = fmaf(f, from[w * HEADS * (D + 2) + d], x);
+                sum = fmaf(f, from[w * HEADS * (D + 2) + D + 1], sum);
+            }
+            if (out.whole) {
+                put(static_cast<__nv_bfloat16*>(a.o) + (q0 + g) * D + d, sum > 0.f ? x / sum : 0.f);
+            } else {
+                part[g * (D + 2) + d] = x;
+                if (d == 0) {
+                    part[g * (D + 2) + D] = top;
+                    part[g * (D + 2) + D + 1] = sum;
+                }
+            }
+        }
+        segment++;
+        if (out.tile < end) out.open(a, TILE, walks, end);
+    }
+    // entries that see no token: zero
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x)
+        if (Seen(a, b).count == 0)
+            for (int i = tid; i < a.Hq * D; i += THREADS) put(static_cast<__nv_bfloat16*>(a.o) + (size_t)b * a.Hq * D + i, 0.f);
 }
 
 // Joins the walk that the border before run blockIdx.x + 1 cuts, if that border is the first in it.
 template <int D, typename T>
-__global__ void __launch_bounds__(THREADS) paged_join_kernel(PagedArgs a, int blocks) {
+__global__ void __launch_bounds__(THREADS) paged_join_kernel(PagedArgs a, int blocks, int tile) {
     linear::next_kernel_may_start();
     const int tid = threadIdx.x, group = a.Hq / a.Hk, walks = a.Hk * blocks, run = blockIdx.x + 1, runs = gridDim.x + 1;
     Place at;
     long long begin, end;
-    const long long total = find(a, walks, run, runs, at, begin, end);
+    const long long total = find(a, tile, walks, run, runs, at, begin, end);
     linear::wait_kernel_before();
     if (begin >= total) return;
-    const long long tiles = Seen(a, at.b).tiles(), start = at.before * walks;
+    const long long tiles = Seen(a, at.b).tiles(tile), start = at.before * walks;
     const int walk = (int)((begin - start) / tiles);
     const long long w0 = start + walk * tiles, w1 = w0 + tiles;
     if (w0 == begin || total * (run - 1) / runs > w0) return;
@@ -236,7 +500,7 @@ __global__ void __launch_bounds__(THREADS) paged_join_kernel(PagedArgs a, int bl
             const float* part = a.parts + (size_t)(2 * r + (rb < w0)) * HEADS * (D + 2) + g * (D + 2);
             const float mr = part[D], top = fmaxf(m, mr);
             if (mr == -INFINITY) continue;
-            const float f0 = expf(m - top), f1 = expf(mr - top);
+            const float f0 = exp2f(m - top), f1 = exp2f(mr - top);
             x = f0 * x + f1 * part[d];
             l = f0 * l + f1 * part[D + 1];
             m = top;
@@ -246,29 +510,31 @@ __global__ void __launch_bounds__(THREADS) paged_join_kernel(PagedArgs a, int bl
 }
 
 template <int D, typename T>
-cudaError_t step(const PagedArgs& a, cudaStream_t st) {
-    const int blocks = (a.Hq / a.Hk + HEADS - 1) / HEADS, smem = (2 * TILE * (D + 4) + HEADS * (D + 4) + HEADS * TILE) * 4;
-    if (cudaError_t e = cudaFuncSetAttribute(paged_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
+cudaError_t step(void (*kernel)(PagedArgs, int), int smem, int tile, const PagedArgs& a, cudaStream_t st) {
+    const int blocks = (a.Hq / a.Hk + HEADS - 1) / HEADS;
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
     trace_begin("paged_step", st);
-    cudaError_t e = launch_after(paged_kernel<D, T>, dim3(RUNS), THREADS, smem, st, false, a, blocks);
+    cudaError_t e = launch_after(kernel, dim3(RUNS), THREADS, smem, st, false, a, blocks);
     trace_end(st);
     if (e != cudaSuccess) return e;
     trace_begin("paged_join", st);
-    e = launch_after(paged_join_kernel<D, T>, dim3(RUNS - 1), THREADS, 0, st, true, a, blocks);
+    e = launch_after(paged_join_kernel<D, T>, dim3(RUNS - 1), THREADS, 0, st, true, a, blocks, tile);
     trace_end(st);
     return e;
 }
-template <typename T>
+template <int D>
 cudaError_t step_of(const PagedArgs& a, cudaStream_t st) {
-    return a.D == 32 ? step<32, T>(a, st) : a.D == 64 ? step<64, T>(a, st) : step<128, T>(a, st);
+    if (a.bf16)
+        return step<D, __nv_bfloat16>(paged_bf16_kernel<D>, WARPS * STAGES * STEP_BYTES + merge_bytes<D>(), WARPS * step_tokens<D>(), a, st);
+    return step<D, float>(paged_f32_kernel<D>, (2 * kTile32 * (D + 4) + HEADS * (D + 4) + HEADS * kTile32) * 4, kTile32, a, st);
 }
 
 }  // namespace
 
-size_t paged_parts_bytes(int, int, int, int D) { return (size_t)2 * RUNS * HEADS * (D + 2) * sizeof(float); }
+size_t paged_parts_bytes(int D) { return (size_t)2 * RUNS * HEADS * (D + 2) * sizeof(float); }
 
 cudaError_t launch_paged_step(const PagedArgs& a, cudaStream_t st) {
-    return a.bf16 ? step_of<__nv_bfloat16>(a, st) : step_of<float>(a, st);
+    return a.D == 32 ? step_of<32>(a, st) : a.D == 64 ? step_of<64>(a, st) : step_of<128>(a, st);
 }
 
 }  // namespace gdr
