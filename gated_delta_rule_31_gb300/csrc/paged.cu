@@ -59,11 +59,12 @@ struct Place {
     long long before;
 };
 
-// The tiles of all entries and walks, those of a run among them and the entry where it begins, by all THREADS threads.
+// The tiles of all entries and walks, those of a run among them and the entry where it begins, by all N threads of a CTA.
+template <int N>
 __device__ long long find(const PagedArgs& a, int tile, int walks, int run, int runs, Place& from, long long& begin, long long& end) {
-    __shared__ long long total_sh, part[THREADS / 32];
+    __shared__ long long total_sh, part[N / 32];
     __shared__ Place from_sh;
-    const int tid = threadIdx.x, per = (a.B + THREADS - 1) / THREADS;
+    const int tid = threadIdx.x, per = (a.B + N - 1) / N;
     long long mine = 0;
     for (int b = tid * per; b < min(a.B, (tid + 1) * per); b++) mine += Seen(a, b).tiles(tile);
     long long scan = mine;
@@ -76,7 +77,7 @@ __device__ long long find(const PagedArgs& a, int tile, int walks, int run, int 
     __syncthreads();
     long long before = scan - mine;
     for (int w = 0; w < tid >> 5; w++) before += part[w];
-    if (tid == THREADS - 1) total_sh = before + mine;
+    if (tid == N - 1) total_sh = before + mine;
     __syncthreads();
     const long long total = total_sh * walks;
     begin = total * run / runs;
@@ -107,7 +108,7 @@ __global__ void __launch_bounds__(THREADS) paged_f32_kernel(PagedArgs a, int blo
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = a.Hq / a.Hk, walks = a.Hk * blocks;
     Place at;
     long long begin, end;
-    find(a, kTile32, walks, blockIdx.x, gridDim.x, at, begin, end);
+    find<THREADS>(a, kTile32, walks, blockIdx.x, gridDim.x, at, begin, end);
     long long tile = begin;
     int segment = 0;
     while (tile < end) {
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(THREADS, 2) paged_bf16_kernel(PagedArgs a, int
     float* merge = reinterpret_cast<float*>(sm + WARPS * STAGES * STEP_BYTES);
     Cursor in, out;
     long long end;
-    find(a, TILE, walks, blockIdx.x, gridDim.x, in.at, in.tile, end);
+    find<THREADS>(a, TILE, walks, blockIdx.x, gridDim.x, in.at, in.tile, end);
     const bool some = in.tile < end;
     if (some) in.open(a, TILE, walks, end);
     out = in;
@@ -474,38 +475,70 @@ __global__ void __launch_bounds__(THREADS, 2) paged_bf16_kernel(PagedArgs a, int
             for (int i = tid; i < a.Hq * D; i += THREADS) put(static_cast<__nv_bfloat16*>(a.o) + (size_t)b * a.Hq * D + i, 0.f);
 }
 
-// Joins the walk that the border before run blockIdx.x + 1 cuts, if that border is the first in it.
+// Joins the walk that the border before run blockIdx.x + 1 cuts, if that border is the first in it: the maximum of each
+// head over the runs by a warp, then the sums by four groups of threads, each every fourth run, in the same order always.
+constexpr int JOIN_THREADS = 512, JOIN_GROUPS = 4;
+
 template <int D, typename T>
-__global__ void __launch_bounds__(THREADS) paged_join_kernel(PagedArgs a, int blocks, int tile) {
+__global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(PagedArgs a, int blocks, int tile) {
+    __shared__ float weight[HEADS][RUNS], sum[HEADS], acc[JOIN_GROUPS][HEADS][D];
+    __shared__ int slot[RUNS];
     linear::next_kernel_may_start();
-    const int tid = threadIdx.x, group = a.Hq / a.Hk, walks = a.Hk * blocks, run = blockIdx.x + 1, runs = gridDim.x + 1;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int group = a.Hq / a.Hk, walks = a.Hk * blocks, run = blockIdx.x + 1, runs = gridDim.x + 1;
     Place at;
     long long begin, end;
-    const long long total = find(a, tile, walks, run, runs, at, begin, end);
-    linear::wait_kernel_before();
-    if (begin >= total) return;
-    const long long tiles = Seen(a, at.b).tiles(tile), start = at.before * walks;
+    const long long total = find<JOIN_THREADS>(a, tile, walks, run, runs, at, begin, end);
+    const long long tiles = begin < total ? Seen(a, at.b).tiles(tile) : 1, start = at.before * walks;
     const int walk = (int)((begin - start) / tiles);
     const long long w0 = start + walk * tiles, w1 = w0 + tiles;
-    if (w0 == begin || total * (run - 1) / runs > w0) return;
+    const bool ours = begin < total && w0 < begin && total * (run - 1) / runs <= w0;
+    const int n = ours ? (int)((w1 * runs - 1) / total) - (run - 1) + 1 : 0;  // runs that hold tiles of the walk, from run - 1 on
+    for (int i = tid; i < n; i += JOIN_THREADS) {
+        const int r = run - 1 + i;
+        const long long rb = total * r / runs, re = total * (r + 1) / runs;
+        slot[i] = rb < re ? 2 * r + (rb < w0) : -1;
+    }
+    linear::wait_kernel_before();
+    __syncthreads();
+    if (!ours) return;
     const int hk = walk / blocks, g0 = walk % blocks * HEADS, ng = min(HEADS, group - g0);
     const size_t q0 = (size_t)at.b * a.Hq + hk * group + g0;
-    for (int i = tid; i < ng * D; i += THREADS) {
-        const int g = i / D, d = i % D;
-        float m = -INFINITY, l = 0.f, x = 0.f;
-        for (int r = run - 1; r < runs; r++) {
-            const long long rb = total * r / runs, re = total * (r + 1) / runs;
-            if (rb >= w1) break;
-            if (rb == re) continue;
-            const float* part = a.parts + (size_t)(2 * r + (rb < w0)) * HEADS * (D + 2) + g * (D + 2);
-            const float mr = part[D], top = fmaxf(m, mr);
-            if (mr == -INFINITY) continue;
-            const float f0 = exp2f(m - top), f1 = exp2f(mr - top);
-            x = f0 * x + f1 * part[d];
-            l = f0 * l + f1 * part[D + 1];
-            m = top;
+    for (int g = warp; g < ng; g += JOIN_THREADS / 32) {
+        float top = -INFINITY, all = 0.f;
+        for (int i = lane; i < n; i += 32) {
+            const float m = slot[i] < 0 ? -INFINITY : a.parts[((size_t)slot[i] * HEADS + g) * (D + 2) + D];
+            weight[g][i] = m;
+            top = fmaxf(top, m);
         }
-        put(static_cast<T*>(a.o) + (q0 + g) * D + d, l > 0.f ? x / l : 0.f);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int i = lane; i < n; i += 32) {
+            const float m = weight[g][i], f = m == -INFINITY ? 0.f : exp2f(m - top);
+            weight[g][i] = f;
+            if (f != 0.f) all = fmaf(f, a.parts[((size_t)slot[i] * HEADS + g) * (D + 2) + D + 1], all);
+        }
+        all = warp_sum(all);
+        if (lane == 0) sum[g] = all;
+    }
+    __syncthreads();
+    constexpr int COLS = JOIN_THREADS / JOIN_GROUPS;
+    const int part = tid / COLS;
+    for (int e = tid % COLS; e < ng * D; e += COLS) {
+        const int g = e / D, d = e % D;
+        float x = 0.f;
+#pragma unroll 4
+        for (int i = part; i < n; i += JOIN_GROUPS) {
+            const float f = weight[g][i];
+            if (f != 0.f) x = fmaf(f, a.parts[((size_t)slot[i] * HEADS + g) * (D + 2) + d], x);  // a run without tokens left no sums
+        }
+        acc[part][g][d] = x;
+    }
+    __syncthreads();
+    for (int e = tid; e < ng * D; e += JOIN_THREADS) {
+        const int g = e / D, d = e % D;
+        const float x = (acc[0][g][d] + acc[1][g][d]) + (acc[2][g][d] + acc[3][g][d]);
+        put(static_cast<T*>(a.o) + (q0 + g) * D + d, sum[g] > 0.f ? x / sum[g] : 0.f);
     }
 }
 
@@ -518,7 +551,7 @@ cudaError_t step(void (*kernel)(PagedArgs, int), int smem, int tile, const Paged
     trace_end(st);
     if (e != cudaSuccess) return e;
     trace_begin("paged_join", st);
-    e = launch_after(paged_join_kernel<D, T>, dim3(RUNS - 1), THREADS, 0, st, true, a, blocks, tile);
+    e = launch_after(paged_join_kernel<D, T>, dim3(RUNS - 1), JOIN_THREADS, 0, st, true, a, blocks, tile);
     trace_end(st);
     return e;
 }
