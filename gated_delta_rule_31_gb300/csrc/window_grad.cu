@@ -1,5 +1,5 @@
-// window_grad.cu - VJP of window attention on the tensor cores, for bf16 (gdr_window_bwd), from lse and
-// delta = sum do o: with c = scale log2 e, per pair of 128-token tiles of queries and keys
+// window_grad.cu - VJP of window attention on the tensor cores, for bf16 (gdr_window_bwd), from lse and o: with delta = sum do o,
+// c = scale log2 e, per pair of 128-token tiles of queries and keys
 //
 //     P = 2^(c Q K^T - log2 e lse),  dS = P (dO V^T - delta),  dQ += scale dS K,  dV += P^T dO,  dK += scale dS^T Q.
 //
@@ -7,12 +7,18 @@
 // but add one of its results into memory in an order that changes, or hand it on in fp32 through memory. Here each result
 // is summed in TMEM, over the heads that share a key head too, and written once.
 //
+// Eight warps do the arithmetic, a thread for a row and half of a pair's columns.
+//
 // dkv forms S^T and dP^T (rows: keys), so that P^T and dS^T, over them in TMEM as bf16, are the operands of the sums as
-// they are. In order per pair: dV, the next pair's S^T, dK, the next dP^T: each half has the other's time to wait for the
-// rows' arithmetic. dq keeps two S, and puts dS over the one that is done with: dP of the next pair, dQ, S of the pair after it.
-// dq comes first and forms delta too, from the copy of do that it has.
-// Eight warps do the arithmetic, a thread for a row and half of the columns; 8 copies tiles in, 9 issues products, and in dkv 10 fetches
-// lse and delta, which lie along the columns there. Units are taken in turn by CTAs that stay, longest first, as one stream.
+// they are. In order per pair: dV, the next pair's S^T; dK, the next dP^T: each half has the other's time to wait for the
+// rows' arithmetic. 2080 cycles of products a pair. (By halves of 64 columns with barriers of their own, as in dq, a product of two
+// operands in shared memory takes 49 cycles a 16-channel step, not 33, bound by reading K or V again.)
+// dq has Q and dO in TMEM, where there is no such bound, and goes by halves: in order, for each, the next S, dQ, the next dP, so one
+// group of four warps has the other's time. 1560 cycles a pair. It comes first and forms delta for both, from tiles of o and what
+// its rounding left that come through the ring ahead of a unit's keys.
+//
+// Warp 8 copies tiles in, 9 issues products, and in dkv 10 brings lse and delta, which lie along the columns there. Units are taken
+// in turn by CTAs that stay, longest first, as one stream.
 //
 // Where a key tile's queries are many (first tokens that all see) or the units few, a key tile is cut: its pieces leave fp32 sums,
 // which a third kernel adds in order.
@@ -49,7 +55,7 @@ struct GradArgs {
     int pieces;           // pieces of the others
     long long units;
     const float* lse;
-    const void *o, *rest;
+    int rest;  // dq: what the rounding of o left is there
     float* delta;
     void *dq, *dk, *dv;
     float* parts;  // of a cut key tile's pieces: dv, dk [2, 128, D] each
@@ -100,8 +106,22 @@ struct KeyUnit {
         part = pieces == 1 ? -1 : in_cut || a.pieces_cut == 1 ? v : u;
     }
     __device__ __forceinline__ int count() const { return end - begin; }
-    __device__ __forceinline__ int head(const WindowShape& s, int i) const { return hk * (s.Hq / s.Hk) + (begin + i) / per; }
-    __device__ __forceinline__ int query(int i) const { return j0 + (begin + i) % per * C; }
+};
+// The pairs of a KeyUnit in order: query head (of those that share the key head) and tile.
+struct Queries {
+    int g, tile;
+    __device__ __forceinline__ void begin(const KeyUnit& x) {
+        g = x.per > 0 ? x.begin / x.per : 0;
+        tile = x.begin - g * x.per;
+    }
+    __device__ __forceinline__ void next(const KeyUnit& x) {
+        if (++tile == x.per) {
+            tile = 0;
+            g++;
+        }
+    }
+    __device__ __forceinline__ int head(const WindowShape& s, const KeyUnit& x) const { return x.hk * (s.Hq / s.Hk) + g; }
+    __device__ __forceinline__ int query(const KeyUnit& x) const { return x.j0 + tile * C; }
 };
 
 // A pair of tiles as the product warp needs it.
@@ -114,10 +134,13 @@ struct Pair {
 template <typename U>
 struct Stream {
     U x;
+    Queries at;
     long long round = -1;
     int i = 0, count = 0;
     __device__ __forceinline__ Pair next(const GradArgs& a) {
-        i++;
+        if (++i < count) {
+            if constexpr (std::is_same<U, KeyUnit>::value) at.next(x);
+        }
         while (i >= count) {
             round++;
             if (round * gridDim.x >= a.units) return Pair{false, false, false, 0};
@@ -126,40 +149,25 @@ struct Stream {
             x.set(a, u);
             i = 0;
             count = x.count();
+            if constexpr (std::is_same<U, KeyUnit>::value) at.begin(x);
         }
         return Pair{true, i == 0, i + 1 == count, x.n - row0()};
     }
-    __device__ __forceinline__ int row0() const;
+    __device__ __forceinline__ int row0() const {  // of the streamed tiles
+        if constexpr (std::is_same<U, KeyUnit>::value) return at.query(x);
+        else return x.tiles.at(i) * C;
+    }
 };
-template <>
-__device__ __forceinline__ int Stream<QueryUnit>::row0() const { return x.tiles.at(i) * C; }
-template <>
-__device__ __forceinline__ int Stream<KeyUnit>::row0() const { return x.query(i); }
-
-__device__ __forceinline__ void product_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t id, int ksteps) {  // a b^T over channels
-    const uint32_t ad = lo_kmajor(a), bd = lo_kmajor(b);
-#pragma unroll
-    for (int k = 0; k < 8; k++)
-        if (k < ksteps)
-            mma_ss(d, ad + (k >> 2) * (PANEL >> 4) + 2 * (k & 3), bd + (k >> 2) * (PANEL >> 4) + 2 * (k & 3), id, k > 0);
-}
-// += p b over the rows of b, p in TMEM: the columns of each half of 64 start at column 64 of it
-__device__ __forceinline__ void product_sum(uint32_t d, uint32_t p, uint32_t b, uint32_t id, int m, bool begin) {
-    const uint32_t bd = lo_mnmajor(b);
-    const int steps = m < C ? (m + 15) / 16 : 8;
-#pragma unroll
-    for (int k = 0; k < 8; k++)
-        if (k < steps) mma_ts(d, p + 64 * (k >> 2) + 8 * (k & 3), bd + step_mnmajor(k), id, k > 0 || !begin);
-}
 
 struct Bars {
     uint64_t keep[2], kept[2];  // operands that stay for a unit: there; free
     uint64_t full[SLOTS], empty[SLOTS];
-    uint64_t sfull[2], dpfull, pready, dsready, sumfull, sumfree, drain;
-    uint64_t lfull[2], lfree[2];
+    uint64_t sfull[2], dpfull[2], pready, dsready[2], sumfull, sumfree, drain;  // dq: of each half
+    uint64_t aready;              // dq: the operands that stay are in TMEM
+    uint64_t lfull[2], lfree[2];  // dkv: statistics
 };
 
-// 64 columns of p - or of their seen part - as bf16 to TMEM
+// 64 columns as bf16 to TMEM
 __device__ __forceinline__ void put_half(uint32_t at, const float (&x)[64]) {
 #pragma unroll
     for (int e = 0; e < 2; e++) {
@@ -173,13 +181,14 @@ __device__ __forceinline__ void put_half(uint32_t at, const float (&x)[64]) {
 template <bool KEYS>
 __global__ void __launch_bounds__(THREADS, 1)
     window_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-                       const __grid_constant__ CUtensorMap mg, GradArgs a) {
+                       const __grid_constant__ CUtensorMap mg, const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap mr,
+                       GradArgs a) {
     using U = typename std::conditional<KEYS, KeyUnit, QueryUnit>::type;
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     __shared__ Bars bar;
-    __shared__ __align__(16) float2 stats[KEYS ? 2 : 1][KEYS ? C : 1];  // (- log2 e lse, - delta) of the queries
-    __shared__ float half_sums[KEYS ? 1 : 2][2][KEYS ? 1 : C];  // of do o over the channels
+    // dkv: - log2 e lse and - delta of a pair's queries; dq: the halves of delta
+    __shared__ __align__(16) float lse_sh[2][C], delta_sh[2][C];
     __shared__ uint32_t tmem_sh;
     __shared__ int failed, used[SLOTS], used_keep[2];
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -200,16 +209,17 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int i = 0; i < 2; i++) {
             used_keep[i] = 0;
             mbar_init(&bar.keep[i], 1);
-            mbar_init(&bar.kept[i], !KEYS && i == 1 ? 9 : 1);  // dq: do is read by the rows' warps too
+            mbar_init(&bar.kept[i], KEYS ? 1 : 4 + 4 * i);  // dq: both halves read dO
             mbar_init(&bar.sfull[i], 1);
-            mbar_init(&bar.lfull[i], 32);
+            mbar_init(&bar.dpfull[i], 1);
+            mbar_init(&bar.dsready[i], KEYS ? 8 : 4);
+            mbar_init(&bar.lfull[i], 1);
             mbar_init(&bar.lfree[i], 8);
         }
-        mbar_init(&bar.dpfull, 1);
         mbar_init(&bar.pready, 8);
-        mbar_init(&bar.dsready, 8);
         mbar_init(&bar.sumfull, 1);
         mbar_init(&bar.sumfree, 8);
+        mbar_init(&bar.aready, 8);
         mbar_init(&bar.drain, 1);
         fence_barrier_init();
     }
@@ -222,8 +232,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_after();
     const uint32_t tm = tmem_sh;
     const int panels = s.D > 64 ? 2 : 1;
-    // TMEM columns. dkv: S^T (P^T), dP^T (dS^T), dV, dK. dq: two S (dS), dP, dQ.
-    constexpr uint32_t COL_S = 0, COL_DP = KEYS ? 128 : 256, COL_V = 256, COL_SUM = 384;
+    // TMEM columns, S and dP in halves of 64. dkv: S^T (P^T), dP^T (dS^T), dV, dK. dq: Q, dO, S, dP (dS), dQ.
+    constexpr uint32_t COL_Q = 0, COL_G = 64, COL_S = KEYS ? 0 : 128, COL_DP = KEYS ? 128 : 256, COL_V = 256, COL_SUM = 384;
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
@@ -255,12 +265,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                 U x;
                 x.set(a, u);
                 const int count = x.count();
+                Queries at;
+                if constexpr (KEYS) at.begin(x);
 #pragma unroll 1
                 for (int i = 0; i < count && ok; i++) {
                     int head, t;
                     if constexpr (KEYS) {
-                        head = x.head(s, i);
-                        t = x.query(i);
+                        head = at.head(s, x);
+                        t = at.query(x);
+                        at.next(x);
                     } else {
                         head = x.hk;
                         t = x.tiles.at(i) * C;
@@ -269,8 +282,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int w = 0; w < 2; w++) {
                         if (i == 0) {
                             if (units > 0) ok = ok && wait_phase(&bar.kept[w], (units + 1) & 1, &failed, 91);
-                            if constexpr (KEYS) put(w * TILE, w ? &mv : &mk, x.hk, x.j0, x.b, &bar.keep[w], &used_keep[w]);
-                            else put(w * TILE, w ? &mg : &mq, x.h, x.t0, x.b, &bar.keep[w], &used_keep[w]);
+                            if constexpr (KEYS) {
+                                put(w * TILE, w ? &mv : &mk, x.hk, x.j0, x.b, &bar.keep[w], &used_keep[w]);
+                            } else {
+                                put(w * TILE, w ? &mg : &mq, x.h, x.t0, x.b, &bar.keep[w], &used_keep[w]);
+                                if (w == 0) {
+                                    stream(&mo, x.h, x.t0, x.b);
+                                    if (a.rest) stream(&mr, x.h, x.t0, x.b);
+                                }
+                            }
                         }
                         stream(KEYS ? (w ? &mg : &mq) : (w ? &mv : &mk), head, t, x.b);
                     }
@@ -278,78 +298,115 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (count > 0) units++;
             }
         } else if (warp == 9) {
-            const uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, s.D, 0, 1);
-            const int ksteps = s.D / 16;
+            const uint32_t id_s = idesc_bf16(128, KEYS ? 128 : 64, 0, 0), id_o = idesc_bf16(128, s.D, 0, 1);
+            const int extra = KEYS ? 0 : a.rest ? 2 : 1;  // tiles of the ring ahead of a unit's pairs
             Stream<U> stream;
-            int started[2] = {0, 0}, summed = 0;  // units begun by S, by dP, by the sums
+            int started = 0, summed = 0;  // units begun by S and dP, by the sums
+            int pos = 0;                  // pairs so far
+            int ring = 0;                 // place in the ring of the current pair's first tile
             bool ok = true;
             const bool ragged = s.lengths != nullptr;
-            auto slot = [&](int pos, int w) { return sb + AT_RING + (2 * pos + w) % SLOTS * TILE; };
-            auto there = [&](int pos, int w, int m) {  // the streamed tile, finite past its tokens
-                ok = ok && wait_phase(&bar.full[(2 * pos + w) % SLOTS], (2 * pos + w) / SLOTS & 1, &failed, 92);
-                if (ok && ragged && m < C) zero_rows(slot(pos, w), m, panels, lane);
+            auto slot = [&](int at) { return sb + AT_RING + at % SLOTS * TILE; };
+            auto there = [&](int at, int m) {  // the streamed tile, finite past its tokens
+                ok = ok && wait_phase(&bar.full[at % SLOTS], at / SLOTS & 1, &failed, 92);
+                if (ok && ragged && m < C) zero_rows(slot(at), m, panels, lane);
             };
-            auto done = [&](int pos, int w) { commit(&bar.empty[(2 * pos + w) % SLOTS]); };
-            // w 0: S, w 1: dP, of pair p, the pos-th
-            auto issue = [&](int w, const Pair& p, int pos, uint32_t to, uint64_t* full) {
-                if (!ok || !p.some) return;
-                if (p.first) ok = wait_phase(&bar.keep[w], started[w]++ & 1, &failed, 93);
-                there(pos, w, p.m);
-                if (!ok) return;
+            auto done = [&](int at) { commit(&bar.empty[at % SLOTS]); };
+            auto rows_ready = [&](uint64_t* b, int site) {
+                ok = ok && wait_phase(b, pos & 1, &failed, site);
                 tc_fence_after();
-                // the rows are those of the operand that stays
-                product_rows(tm + to, sb + w * TILE, slot(pos, w), id_s, ksteps);
-                commit(full);
-                if (p.last) commit(&bar.kept[w]);
+                return ok;
             };
             auto sums_begin = [&](const Pair& p) {
                 if (p.first && summed++ > 0) ok = ok && wait_phase(&bar.sumfree, summed & 1, &failed, 94);
             };
             Pair cur = stream.next(a);
             if constexpr (KEYS) {
-                issue(0, cur, 0, COL_S, &bar.sfull[0]);
-                issue(1, cur, 0, COL_DP, &bar.dpfull);
+                // w 0: S^T, w 1: dP^T, of a pair whose tile is at `at`
+                auto issue = [&](int w, const Pair& p, int at) {
+                    if (!ok || !p.some) return;
+                    if (p.first) {
+                        ok = wait_phase(&bar.keep[w], started & 1, &failed, 93);
+                        started += w;
+                    }
+                    there(at, p.m);
+                    if (!ok) return;
+                    tc_fence_after();
+                    product_ss(tm + (w ? COL_DP : COL_S), lo_kmajor(sb + w * TILE), lo_kmajor(slot(at)), id_s, s.D);
+                    commit(w ? &bar.dpfull[0] : &bar.sfull[0]);
+                    if (p.last) commit(&bar.kept[w]);
+                };
+                auto sum = [&](int w, uint32_t from, int at) {  // both halves' columns, each from its column 64
+                    const uint32_t d = tm + (w ? COL_SUM : COL_V), bd = lo_mnmajor(slot(at));
+                    product_sum64(d, tm + from, bd, id_o, cur.m, cur.first);
+                    product_sum64(d, tm + from + 64, bd + step_mnmajor(4), id_o, cur.m - 64, false);
+                    done(at);
+                };
+                issue(0, cur, 0);
+                issue(1, cur, 1);
 #pragma unroll 1
-                for (int pos = 0; cur.some && ok; pos++) {
+                for (; cur.some && ok; pos++, ring += 2) {
                     const Pair nxt = stream.next(a);
                     sums_begin(cur);
-                    ok = ok && wait_phase(&bar.pready, pos & 1, &failed, 95);
-                    if (!ok) break;
-                    tc_fence_after();
-                    product_sum(tm + COL_V, tm + COL_S, slot(pos, 1), id_o, cur.m, cur.first);
-                    done(pos, 1);
-                    issue(0, nxt, pos + 1, COL_S, &bar.sfull[0]);
-                    ok = ok && wait_phase(&bar.dsready, pos & 1, &failed, 96);
-                    if (!ok) break;
-                    tc_fence_after();
-                    product_sum(tm + COL_SUM, tm + COL_DP, slot(pos, 0), id_o, cur.m, cur.first);
-                    done(pos, 0);
+                    if (!rows_ready(&bar.pready, 95)) break;
+                    sum(0, COL_S, ring + 1);
+                    issue(0, nxt, ring + 2);
+                    if (!rows_ready(&bar.dsready[0], 96)) break;
+                    sum(1, COL_DP, ring);
                     if (cur.last) commit(&bar.sumfull);
-                    issue(1, nxt, pos + 1, COL_DP, &bar.dpfull);
+                    issue(1, nxt, ring + 3);
                     cur = nxt;
                 }
             } else {
-                Pair nxt = cur.some ? stream.next(a) : cur;
-                issue(0, cur, 0, COL_S, &bar.sfull[0]);
-                issue(1, cur, 0, COL_DP, &bar.dpfull);
-                if (cur.some) done(0, 1);
-                issue(0, nxt, 1, COL_S + 128, &bar.sfull[1]);
+                auto issue = [&](int w, int half, int at) {  // w 0: S, w 1: dP
+                    product_ts(tm + (w ? COL_DP : COL_S) + 64 * half, tm + (w ? COL_G : COL_Q), lo_kmajor(slot(at)) + half * (64 * 128 >> 4), id_s, s.D);
+                    commit(w ? &bar.dpfull[half] : &bar.sfull[half]);
+                };
+                auto begin_unit = [&]() {  // S and dP of a unit's first pair
+                    if (!ok || !cur.some) return;
+                    ring += extra;
+                    ok = wait_phase(&bar.aready, started++ & 1, &failed, 93);
 #pragma unroll 1
-                for (int pos = 0; cur.some && ok; pos++) {
-                    const Pair far = nxt.some ? stream.next(a) : nxt;
-                    const uint32_t at = COL_S + 128 * (pos & 1);
-                    ok = wait_phase(&bar.dsready, pos & 1, &failed, 96);
-                    issue(1, nxt, pos + 1, COL_DP, &bar.dpfull);
-                    if (ok && nxt.some) done(pos + 1, 1);
+                    for (int w = 0; w < 2 && ok; w++) {
+                        there(ring + w, cur.m);
+                        if (!ok) return;
+                        tc_fence_after();
+                        issue(w, 0, ring + w);
+                        issue(w, 1, ring + w);
+                    }
+                    done(ring + 1);
+                };
+                begin_unit();
+#pragma unroll 1
+                for (; cur.some && ok; pos++) {
+                    const Pair nxt = stream.next(a);
+                    const bool on = nxt.some && !nxt.first;
                     sums_begin(cur);
-                    if (!ok) break;
-                    tc_fence_after();
-                    product_sum(tm + COL_SUM, tm + at, slot(pos, 0), id_o, cur.m, cur.first);
-                    done(pos, 0);
-                    if (cur.last) commit(&bar.sumfull);
-                    issue(0, far, pos + 2, at, &bar.sfull[pos & 1]);
+#pragma unroll 1
+                    for (int h = 0; h < 2 && ok; h++) {
+                        if (!rows_ready(&bar.dsready[h], 96)) break;
+                        if (on) {
+                            if (h == 0) there(ring + 2, nxt.m);
+                            if (!ok) break;
+                            tc_fence_after();
+                            issue(0, h, ring + 2);
+                        }
+                        product_sum64(tm + COL_SUM, tm + COL_DP + 64 * h, lo_mnmajor(slot(ring)) + h * step_mnmajor(4), id_o, cur.m - 64 * h, cur.first && h == 0);
+                        if (h == 1) {
+                            done(ring);
+                            if (cur.last) commit(&bar.sumfull);
+                        }
+                        if (on) {
+                            if (h == 0) there(ring + 3, nxt.m);
+                            if (!ok) break;
+                            tc_fence_after();
+                            issue(1, h, ring + 3);
+                        }
+                    }
+                    if (ok && on) done(ring + 3);
+                    ring += 2;
                     cur = nxt;
-                    nxt = far;
+                    if (!on) begin_unit();
                 }
             }
             commit(&bar.drain);  // every product issued so far has completed before TMEM is released
@@ -361,20 +418,22 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int pos = 0;; pos++) {
                     const Pair p = stream.next(a);
                     if (!p.some) break;
-                    const int t0 = stream.row0();
-                    const size_t row = ((size_t)stream.x.b * s.Hq + stream.x.head(s, stream.i)) * s.T + t0;
-                    float2 x[4];
+                    const size_t row = ((size_t)stream.x.b * s.Hq + stream.at.head(s, stream.x)) * s.T + stream.row0();
+                    float l[4], d[4];
 #pragma unroll
-                    for (int e = 0; e < 4; e++) {
+                    for (int e = 0; e < 4; e++) {  // queries past the end weigh nothing: 2^-inf
                         const int r = lane + 32 * e;
-                        // queries past the end weigh nothing: 2^-inf
-                        x[e] = r < p.m ? make_float2(-LOG2E * a.lse[row + r], -a.delta[row + r]) : make_float2(-INFINITY, 0.f);
+                        l[e] = r < p.m ? -LOG2E * a.lse[row + r] : -INFINITY;
+                        d[e] = r < p.m ? -a.delta[row + r] : 0.f;
                     }
                     if (pos >= 2 && !wait_phase(&bar.lfree[pos & 1], (pos / 2 + 1) & 1, &failed, 97)) break;
 #pragma unroll
-                    for (int e = 0; e < 4; e++) stats[pos & 1][lane + 32 * e] = x[e];
-                    mbar_arrive(&bar.lfull[pos & 1]);
+                    for (int e = 0; e < 4; e++) {
+                        lse_sh[pos & 1][lane + 32 * e] = l[e];
+                        delta_sh[pos & 1][lane + 32 * e] = d[e];
+                    }
                     __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.lfull[pos & 1]);
                 }
             }
         }
@@ -382,10 +441,36 @@ __global__ void __launch_bounds__(THREADS, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_ROWS));
         const int half = warp >> 2, row = 32 * (warp & 3) + lane;
         const uint32_t lanes = tm + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t at_s = lanes + COL_S + 64 * half, at_dp = lanes + COL_DP + 64 * half;
         const float c = s.scale * LOG2E;
         const uint64_t c2 = pair(c, c);
         int np = 0, units = 0;
         bool ok = true;
+        // dq: the rows that are still to be written, a unit later
+        int late_t = 0, late_n = 0, late_b = 0, late_h = 0;
+        auto write_dq = [&](bool sums, int t, int n, int b, int h) {
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.dq) + (((size_t)b * s.T + t) * s.Hq + h) * s.D;
+#pragma unroll 1
+            for (int e = 32 * half; e < s.D; e += 64) {  // every other 32 channels for each half
+                float o[32];
+                if (sums) {
+                    tmem_ld32(lanes + COL_SUM + e, o);
+                    tmem_wait_ld();
+                }
+                if (t < s.T)
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8) *reinterpret_cast<uint4*>(out + e + k) = t < n ? pack8(o + k, s.scale) : make_uint4(0, 0, 0, 0);
+            }
+        };
+        auto write_late = [&]() {  // of unit number `units`, counted from 1
+            ok = wait_phase(&bar.sumfull, (units + 1) & 1, &failed, 100);
+            if (!ok) return;
+            tc_fence_after();
+            write_dq(true, late_t, late_n, late_b, late_h);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.sumfree);
+        };
 #pragma unroll 1
         for (long long round = 0; ok; round++) {
             const long long u = unit_of(round);
@@ -398,45 +483,81 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int count = x.count(), n = x.n;
             uint64_t b2 = 0, d2 = 0;  // dq: - log2 e lse and - delta of the thread's row, twice
             if constexpr (!KEYS) {
-                const int t = x.t0 + row;
-                const size_t at = ((size_t)x.b * s.Hq + x.h) * s.T + t;
-                const float l = t < n ? -LOG2E * a.lse[at] : 0.f;
-                b2 = pair(l, l);
-                if (count > 0) {
-                    // a thread's half of the row's do o: channels 64 half .. (32 half .. of at most 64)
-                    const int width = s.D > 64 ? 64 : s.D / 2, from = width * half;
-                    const size_t to = (((size_t)x.b * s.T + t) * s.Hq + x.h) * s.D + from;
-                    const __nv_bfloat16 *o = static_cast<const __nv_bfloat16*>(a.o) + to, *rest = static_cast<const __nv_bfloat16*>(a.rest) + to;
-                    float sum = 0.f;
-                    ok = wait_phase(&bar.keep[1], units & 1, &failed, 101);
-                    if (ok && t < n)
-#pragma unroll 4
-                        for (int e = 0; e < width; e += 8) {
-                            float y[8], z[8] = {}, g[8];
-                            unpack8(*reinterpret_cast<const uint4*>(o + e), y);
-                            if (a.rest) unpack8(*reinterpret_cast<const uint4*>(rest + e), z);
-                            unpack8(ld_shared_v4(sb + TILE + sw128_chunk(row, (from + e) / 8, C)), g);
-#pragma unroll
-                            for (int k = 0; k < 8; k++) sum = fmaf(g[k], y[k] + z[k], sum);
-                        }
-                    half_sums[units & 1][half][row] = sum;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.kept[1]);
-                    if (bar_sync_or(1, 256, !ok)) {  // all go on, or none
-                        ok = false;
-                        break;
-                    }
-                    const float d = -(half_sums[units & 1][0][row] + half_sums[units & 1][1][row]);
-                    d2 = pair(d, d);
-                    if (half == 0 && t < n) a.delta[at] = -d;
+                if (count == 0) {
+                    write_dq(false, x.t0 + row, n, x.b, x.h);
+                    continue;
                 }
+                const int t = x.t0 + row;
+                const size_t stat = ((size_t)x.b * s.Hq + x.h) * s.T + t;
+                const float l = t < n ? -LOG2E * a.lse[stat] : 0.f;
+                // the row of Q (first half) or dO into TMEM: the unit before has done with it, on both sides
+                ok = wait_phase(&bar.keep[half], units & 1, &failed, 101);
+                if (bar_sync_or(1, 256, !ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll 1
+                for (int e = 0; e < s.D / 2; e += 16) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        const uint4 y = ld_shared_v4(sb + half * TILE + sw128_chunk(row, e / 4 + k, C));
+                        w[4 * k] = y.x; w[4 * k + 1] = y.y; w[4 * k + 2] = y.z; w[4 * k + 3] = y.w;
+                    }
+                    tmem_st16(lanes + (half ? COL_G : COL_Q) + e, w);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bar.aready);
+                    if (half == 0) mbar_arrive(&bar.kept[0]);
+                }
+                // half of the row's sum of do o, o with what its rounding left
+                const int extra = a.rest ? 2 : 1, width = s.D / 16, o_at = 2 * np + extra * units;  // chunks of 8 channels; place in the ring
+                ok = wait_phase(&bar.keep[1], units & 1, &failed, 102);
+                for (int k = 0; k < extra; k++) ok = ok && wait_phase(&bar.full[(o_at + k) % SLOTS], (o_at + k) / SLOTS & 1, &failed, 103);
+                float d = 0.f;
+                if (ok && t < n) {
+                    const uint32_t at_o = sb + AT_RING + o_at % SLOTS * TILE, at_r = sb + AT_RING + (o_at + 1) % SLOTS * TILE;
+#pragma unroll 2
+                    for (int e = half * width; e < (half + 1) * width; e++) {
+                        const uint32_t chunk = sw128_chunk(row, e, C);
+                        float y[8], z[8] = {}, g[8];
+                        unpack8(ld_shared_v4(at_o + chunk), y);
+                        if (a.rest) unpack8(ld_shared_v4(at_r + chunk), z);
+                        unpack8(ld_shared_v4(sb + TILE + chunk), g);
+#pragma unroll
+                        for (int k = 0; k < 8; k++) d = fmaf(g[k], y[k] + z[k], d);
+                    }
+                }
+                float(*halves)[C] = units & 1 ? lse_sh : delta_sh;
+                halves[half][row] = d;
+                if (bar_sync_or(1, 256, !ok)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) mbar_arrive(&bar.kept[1]);
+                if (tid == 0)
+                    for (int k = 0; k < extra; k++) mbar_arrive(&bar.empty[(o_at + k) % SLOTS]);
+                d = halves[0][row] + halves[1][row];
+                if (half == 0 && t < n) a.delta[stat] = d;
+                b2 = pair(l, l);
+                d2 = pair(-d, -d);
+                if (units > 0) write_late();
+                if (!ok) break;
+                late_t = x.t0 + row;
+                late_n = n;
+                late_b = x.b;
+                late_h = x.h;
             }
+            Queries at;
+            if constexpr (KEYS) at.begin(x);
 #pragma unroll 1
             for (int i = 0; i < count; i++, np++) {
-                const int buffer = KEYS ? 0 : np & 1;
-                const uint32_t at_s = lanes + COL_S + 128 * buffer + 64 * half, at_dp = lanes + COL_DP + 64 * half;
                 if (KEYS) ok = wait_phase(&bar.lfull[np & 1], np / 2 & 1, &failed, 97);
-                ok = ok && wait_phase(&bar.sfull[buffer], (KEYS ? np : np / 2) & 1, &failed, 98);
+                ok = ok && wait_phase(&bar.sfull[KEYS ? 0 : half], np & 1, &failed, 98);
                 if (!ok) break;
                 tc_fence_after();
                 float p[64];
@@ -444,23 +565,26 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tmem_ld32(at_s + 32, p + 32);
                 int t0, j0;
                 if constexpr (KEYS) {
-                    t0 = x.query(i);
+                    t0 = at.query(x);
                     j0 = x.j0;
+                    at.next(x);
                 } else {
                     t0 = x.t0;
                     j0 = x.tiles.at(i) * C;
                 }
                 const bool all = all_seen(s, t0, j0, n);
-                const float4* st = reinterpret_cast<const float4*>(stats[KEYS ? np & 1 : 0]) + (KEYS ? 32 * half : 0);  // two queries each
+                const float4* st = reinterpret_cast<const float4*>(lse_sh[np & 1]) + 16 * half;  // dkv: four columns each
                 tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 32; k++) {
-                    uint64_t lse = b2;
+                for (int k = 0; k < 16; k++) {
+                    uint64_t l0 = b2, l1 = b2;
                     if (KEYS) {
                         const float4 f = st[k];
-                        lse = pair(f.x, f.z);
+                        l0 = pair(f.x, f.y);
+                        l1 = pair(f.z, f.w);
                     }
-                    unpair(fma2(pair(p[2 * k], p[2 * k + 1]), c2, lse), p[2 * k], p[2 * k + 1]);
+                    unpair(fma2(pair(p[4 * k], p[4 * k + 1]), c2, l0), p[4 * k], p[4 * k + 1]);
+                    unpair(fma2(pair(p[4 * k + 2], p[4 * k + 3]), c2, l1), p[4 * k + 2], p[4 * k + 3]);
                 }
 #pragma unroll
                 for (int k = 0; k < 64; k++) p[k] = exp2_fast(p[k]);
@@ -481,46 +605,48 @@ __global__ void __launch_bounds__(THREADS, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.pready);
                 }
-                ok = wait_phase(&bar.dpfull, np & 1, &failed, 99);
+                ok = wait_phase(&bar.dpfull[KEYS ? 0 : half], np & 1, &failed, 99);
                 if (!ok) break;
                 tc_fence_after();
+                const float4* dt = reinterpret_cast<const float4*>(delta_sh[np & 1]) + 16 * half;
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
                     float d[32];
                     tmem_ld32(at_dp + 32 * e, d);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 16; k++) {
-                        uint64_t delta = d2;
+                    for (int k = 0; k < 8; k++) {
+                        uint64_t d0 = d2, d1 = d2;
                         if (KEYS) {
-                            const float4 f = st[16 * e + k];
-                            delta = pair(f.y, f.w);
+                            const float4 f = dt[8 * e + k];
+                            d0 = pair(f.x, f.y);
+                            d1 = pair(f.z, f.w);
                         }
-                        float* q = p + 32 * e + 2 * k;
-                        unpair(mul2(pair(q[0], q[1]), add2(pair(d[2 * k], d[2 * k + 1]), delta)), q[0], q[1]);
+                        float* q = p + 32 * e + 4 * k;
+                        unpair(mul2(pair(q[0], q[1]), add2(pair(d[4 * k], d[4 * k + 1]), d0)), q[0], q[1]);
+                        unpair(mul2(pair(q[2], q[3]), add2(pair(d[4 * k + 2], d[4 * k + 3]), d1)), q[2], q[3]);
                     }
                 }
-                put_half(KEYS ? at_dp : at_s, p);
+                put_half(at_dp, p);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&bar.dsready);
+                    mbar_arrive(&bar.dsready[KEYS ? 0 : half]);
                     if (KEYS) mbar_arrive(&bar.lfree[np & 1]);
                 }
             }
             if (!ok) break;
-            if (count > 0) {
-                ok = wait_phase(&bar.sumfull, units & 1, &failed, 100);
-                if (!ok) break;
-                tc_fence_after();
-                units++;
-            }
-            // dkv: the first four warps write dv, the others dk; dq: every other 32 channels each
-            const float f = KEYS && half == 0 ? 1.f : s.scale;
-            if constexpr (KEYS) {
+            if (count > 0) units++;
+            if constexpr (KEYS) {  // the first four warps write dv, the others dk
+                if (count > 0) {
+                    ok = wait_phase(&bar.sumfull, (units + 1) & 1, &failed, 100);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
                 const int j = x.j0 + row;
                 const bool there = j < n;
+                const float f = half ? s.scale : 1.f;
                 __nv_bfloat16* out = static_cast<__nv_bfloat16*>(half ? a.dk : a.dv) + (((size_t)x.b * s.T + j) * s.Hk + x.hk) * s.D;
                 float* part = a.parts + (((size_t)x.part * 2 + half) * C + row) * s.D;
 #pragma unroll 1
@@ -541,28 +667,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                         for (int k = 0; k < 32; k += 8) *reinterpret_cast<uint4*>(out + e + k) = pack8(o + k, f);
                     }
                 }
-            } else {
-                const int q = x.t0 + row;
-                const bool there = q < n;
-                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.dq) + (((size_t)x.b * s.T + q) * s.Hq + x.h) * s.D;
-#pragma unroll 1
-                for (int e = 32 * half; e < s.D; e += 64) {
-                    float o[32];
-                    if (count > 0) {
-                        tmem_ld32(lanes + COL_SUM + e, o);
-                        tmem_wait_ld();
-                    }
-                    if (q < s.T)
-#pragma unroll
-                        for (int k = 0; k < 32; k += 8) *reinterpret_cast<uint4*>(out + e + k) = there ? pack8(o + k, f) : make_uint4(0, 0, 0, 0);
+                if (count > 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.sumfree);
                 }
             }
-            if (count > 0) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.sumfree);
-            }
         }
+        if (!KEYS && ok && units > 0) write_late();
     }
     tc_fence_before();
     __syncthreads();
@@ -624,7 +736,7 @@ struct Cut {
 template <bool KEYS>
 cudaError_t launch(const CUtensorMap* maps, const GradArgs& a, const char* name, cudaStream_t st) {
     trace_begin(name, st);
-    window_grad_kernel<KEYS><<<(unsigned)(a.units < SMS ? a.units : SMS), THREADS, BYTES, st>>>(maps[0], maps[1], maps[2], maps[3], a);
+    window_grad_kernel<KEYS><<<(unsigned)(a.units < SMS ? a.units : SMS), THREADS, BYTES, st>>>(maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], a);
     trace_end(st);
     return cudaGetLastError();
 }
@@ -639,7 +751,8 @@ cudaError_t launch_window_bwd_tc(const WindowArgs& x, cudaStream_t st) {
     // before the tensor maps: the first runtime call of a host thread makes the device's context current there
     if (cudaError_t e = cudaFuncSetAttribute(window_grad_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES)) return e;
     if (cudaError_t e = cudaFuncSetAttribute(window_grad_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES)) return e;
-    CUtensorMap maps[4];
+    CUtensorMap maps[6];
+    if (!rows_map(&maps[4], x.o, x.s, x.s.Hq) || !rows_map(&maps[5], x.rest ? x.rest : x.o, x.s, x.s.Hq)) return cudaErrorInvalidValue;
     if (!rows_map(&maps[0], x.q, x.s, x.s.Hq) || !rows_map(&maps[1], x.k, x.s, x.s.Hk) || !rows_map(&maps[2], x.v, x.s, x.s.Hk) ||
         !rows_map(&maps[3], x.do_, x.s, x.s.Hq))
         return cudaErrorInvalidValue;
@@ -651,8 +764,7 @@ cudaError_t launch_window_bwd_tc(const WindowArgs& x, cudaStream_t st) {
     a.pieces_cut = cut.pieces_cut;
     a.pieces = cut.pieces;
     a.lse = x.lse;
-    a.o = x.o;
-    a.rest = x.rest;
+    a.rest = x.rest != nullptr;
     a.delta = x.delta;
     a.dq = x.dq;
     a.dk = x.dk;

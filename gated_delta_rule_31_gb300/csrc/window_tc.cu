@@ -181,7 +181,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         } else if (warp == 9) {
             const uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, s.D, 0, 1);
-            const int ksteps = s.D / 16;
             int npv[2] = {0, 0}, nq[2] = {0, 0}, nu[2] = {0, 0};  // P V products; units begun by S; by P V
             long long round = -1;
             Unit cur, nxt;
@@ -218,10 +217,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!wait_phase(&full[kp], (int)((2 * pos) / SLOTS & 1), &failed, 73)) return false;
                 tc_fence_after();
                 const uint32_t ad = lo_kmajor(sb + i * TILE), bd = lo_kmajor(sb + AT_KV + kp * TILE);
-#pragma unroll
-                for (int k = 0; k < 8; k++)
-                    if (k < ksteps)
-                        mma_ss(tm + COL_S + 128 * i, ad + (k >> 2) * (PANEL >> 4) + 2 * (k & 3), bd + (k >> 2) * (PANEL >> 4) + 2 * (k & 3), id_s, k > 0);
+                product_ss(tm + COL_S + 128 * i, ad, bd, id_s, s.D);
                 commit(&sfull[i]);
                 if (nxt.last(i, tile)) commit(&qfree[i]);
                 return true;
@@ -244,7 +240,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!wait_phase(&full[(int)(vp % SLOTS)], (int)(vp / SLOTS & 1), &failed, 74)) break;
                 const int m = cur.n - tile * C;
                 if (m < C && cur.n < s.T) zero_rows(vt, m, panels, lane);  // past the end, whatever it holds
-                const int steps = m < C ? (m + 15) / 16 : 8;
 #pragma unroll
                 for (int i = 0; i < 2; i++) {
                     if (cur.tiles[i].has(tile)) {
@@ -255,9 +250,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (ok) {
                             tc_fence_after();
                             const uint32_t bd = lo_mnmajor(vt);
-#pragma unroll
-                            for (int k = 0; k < 8; k++)
-                                if (k < steps) mma_ts(tm + COL_O + 128 * i, tm + COL_S + 128 * i + 8 * k, bd + step_mnmajor(k), id_o, k > 0 || !begin);
+                            product_sum64(tm + COL_O + 128 * i, tm + COL_S + 128 * i, bd, id_o, m, begin);
+                            product_sum64(tm + COL_O + 128 * i, tm + COL_S + 128 * i + 32, bd + step_mnmajor(4), id_o, m - 64, false);
                             commit(&ofull[i]);
                         }
                     }
