@@ -46,66 +46,24 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     return d;
 }
 
-// Four products in a row with one election: both operands in shared memory, 16 channels on each time (d accumulates but for
-// the first with begin); and the left one in TMEM, 8 columns on, against 16 rows of b on each time.
-__device__ __forceinline__ void mma_ss4(uint32_t d, uint32_t alo, uint32_t blo, uint32_t idesc, bool begin) {
-    asm volatile(
-        "{\n\t.reg .pred p, q, t;\n\t.reg .b64 x, y;\n\t.reg .b32 u, v;\n\t"
-        "setp.eq.u32 p, %4, 0;\n\tsetp.eq.u32 t, 0, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
-        "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t"
-        "add.u32 u, %1, 2;\n\tadd.u32 v, %2, 2;\n\tmov.b64 x, {u, %5};\n\tmov.b64 y, {v, %5};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-        "add.u32 u, %1, 4;\n\tadd.u32 v, %2, 4;\n\tmov.b64 x, {u, %5};\n\tmov.b64 y, {v, %5};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-        "add.u32 u, %1, 6;\n\tadd.u32 v, %2, 6;\n\tmov.b64 x, {u, %5};\n\tmov.b64 y, {v, %5};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t}" ::"r"(d),
-        "r"(alo), "r"(blo), "r"(idesc), "r"((uint32_t)begin), "r"(DESC_HI)
-        : "memory");
+// d = a b^T over D channels, of the rows that the instruction's shape says, tiles in shared memory (a: or in TMEM). Issued one by
+// one without loops: the compiler then keeps all operands in uniform registers (several products to an election, or loops over
+// them, took dq from 0.90 to 1.2 us a pair of tiles).
+template <int D>
+__device__ __forceinline__ void product_ss(uint32_t d, uint32_t alo, uint32_t blo, uint32_t idesc) {
+#pragma unroll
+    for (int k = 0; k < D / 16; k++) mma_ss(d, alo + (k >> 2) * (PANEL >> 4) + 2 * (k & 3), blo + (k >> 2) * (PANEL >> 4) + 2 * (k & 3), idesc, k > 0);
 }
-template <int STEP>
-__device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a, uint32_t blo, uint32_t idesc, bool begin) {
-    asm volatile(
-        "{\n\t.reg .pred p, q, t;\n\t.reg .b64 y;\n\t.reg .b32 u, v;\n\t"
-        "setp.eq.u32 p, %4, 0;\n\tsetp.eq.u32 t, 0, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
-        "mov.b64 y, {%2, %5};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t"
-        "add.u32 u, %1, 8;\n\tadd.u32 v, %2, %6;\n\tmov.b64 y, {v, %5};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %3, t;\n\t"
-        "add.u32 u, %1, 16;\n\tadd.u32 v, %2, %7;\n\tmov.b64 y, {v, %5};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %3, t;\n\t"
-        "add.u32 u, %1, 24;\n\tadd.u32 v, %2, %8;\n\tmov.b64 y, {v, %5};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %3, t;\n\t}" ::"r"(d),
-        "r"(a), "r"(blo), "r"(idesc), "r"((uint32_t)begin), "r"(DESC_HI), "n"(STEP), "n"(2 * STEP), "n"(3 * STEP)
-        : "memory");
-}
-// d = a b^T over `channels` channels, of the rows that the instruction's shape says, tiles in shared memory (a: or in TMEM).
-__device__ __forceinline__ void product_ss(uint32_t d, uint32_t alo, uint32_t blo, uint32_t idesc, int channels) {
-    if (channels < 64) {
-        mma_ss(d, alo, blo, idesc, 0);
-        mma_ss(d, alo + 2, blo + 2, idesc, 1);
-    } else {
-#pragma unroll 1
-        for (int c = 0; c < channels; c += 64, alo += PANEL >> 4, blo += PANEL >> 4) mma_ss4(d, alo, blo, idesc, c == 0);
-    }
-}
-__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint32_t blo, uint32_t idesc, int channels) {
-    if (channels < 64) {
-        mma_ts(d, a, blo, idesc, 0);
-        mma_ts(d, a + 8, blo + 2, idesc, 1);
-    } else {
-#pragma unroll 1
-        for (int c = 0; c < channels; c += 64, a += 32, blo += PANEL >> 4) mma_ts4<2>(d, a, blo, idesc, c == 0);
-    }
+template <int D>
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint32_t blo, uint32_t idesc) {
+#pragma unroll
+    for (int k = 0; k < D / 16; k++) mma_ts(d, a + 8 * k, blo + (k >> 2) * (PANEL >> 4) + 2 * (k & 3), idesc, k > 0);
 }
 // d (+)= p b over 64 rows of b (blo: MN-major), p in TMEM; the first `rows` are enough, the others weigh nothing
 __device__ __forceinline__ void product_sum64(uint32_t d, uint32_t p, uint32_t blo, uint32_t idesc, int rows, bool begin) {
-    if (rows > 48) {
-        mma_ts4<step_mnmajor(1)>(d, p, blo, idesc, begin);
-    } else {
-#pragma unroll 1
-        for (int r = 0; r < rows; r += 16, p += 8, blo += step_mnmajor(1)) mma_ts(d, p, blo, idesc, r > 0 || !begin);
-    }
+#pragma unroll
+    for (int k = 0; k < 4; k++)
+        if (16 * k < rows) mma_ts(d, p + 8 * k, blo + step_mnmajor(k), idesc, k > 0 || !begin);
 }
 
 // Whether every query of t0 .. t0 + 127 sees every key of j0 .. j0 + 127.

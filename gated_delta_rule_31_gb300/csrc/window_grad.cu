@@ -178,7 +178,7 @@ __device__ __forceinline__ void put_half(uint32_t at, const float (&x)[64]) {
     }
 }
 
-template <bool KEYS>
+template <bool KEYS, int D>
 __global__ void __launch_bounds__(THREADS, 1)
     window_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                        const __grid_constant__ CUtensorMap mg, const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap mr,
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = tmem_sh;
-    const int panels = s.D > 64 ? 2 : 1;
+    constexpr int panels = D > 64 ? 2 : 1;
     // TMEM columns, S and dP in halves of 64. dkv: S^T (P^T), dP^T (dS^T), dV, dK. dq: Q, dO, S, dP (dS), dQ.
     constexpr uint32_t COL_Q = 0, COL_G = 64, COL_S = KEYS ? 0 : 128, COL_DP = KEYS ? 128 : 256, COL_V = 256, COL_SUM = 384;
 
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (count > 0) units++;
             }
         } else if (warp == 9) {
-            const uint32_t id_s = idesc_bf16(128, KEYS ? 128 : 64, 0, 0), id_o = idesc_bf16(128, s.D, 0, 1);
+            constexpr uint32_t id_s = idesc_bf16(128, KEYS ? 128 : 64, 0, 0), id_o = idesc_bf16(128, D, 0, 1);
             const int extra = KEYS ? 0 : a.rest ? 2 : 1;  // tiles of the ring ahead of a unit's pairs
             Stream<U> stream;
             int started = 0, summed = 0;  // units begun by S and dP, by the sums
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     there(at, p.m);
                     if (!ok) return;
                     tc_fence_after();
-                    product_ss(tm + (w ? COL_DP : COL_S), lo_kmajor(sb + w * TILE), lo_kmajor(slot(at)), id_s, s.D);
+                    product_ss<D>(tm + (w ? COL_DP : COL_S), lo_kmajor(sb + w * TILE), lo_kmajor(slot(at)), id_s);
                     commit(w ? &bar.dpfull[0] : &bar.sfull[0]);
                     if (p.last) commit(&bar.kept[w]);
                 };
@@ -359,15 +359,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             } else {
                 auto issue = [&](int w, int half, int at) {  // w 0: S, w 1: dP
-                    product_ts(tm + (w ? COL_DP : COL_S) + 64 * half, tm + (w ? COL_G : COL_Q), lo_kmajor(slot(at)) + half * (64 * 128 >> 4), id_s, s.D);
+                    product_ts<D>(tm + (w ? COL_DP : COL_S) + 64 * half, tm + (w ? COL_G : COL_Q), lo_kmajor(slot(at)) + half * (64 * 128 >> 4), id_s);
                     commit(w ? &bar.dpfull[half] : &bar.sfull[half]);
                 };
                 auto begin_unit = [&]() {  // S and dP of a unit's first pair
                     if (!ok || !cur.some) return;
                     ring += extra;
                     ok = wait_phase(&bar.aready, started++ & 1, &failed, 93);
-#pragma unroll 1
-                    for (int w = 0; w < 2 && ok; w++) {
+#pragma unroll
+                    for (int w = 0; w < 2; w++) {
                         there(ring + w, cur.m);
                         if (!ok) return;
                         tc_fence_after();
@@ -382,8 +382,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const Pair nxt = stream.next(a);
                     const bool on = nxt.some && !nxt.first;
                     sums_begin(cur);
-#pragma unroll 1
-                    for (int h = 0; h < 2 && ok; h++) {
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
                         if (!rows_ready(&bar.dsready[h], 96)) break;
                         if (on) {
                             if (h == 0) there(ring + 2, nxt.m);
@@ -449,9 +449,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         // dq: the rows that are still to be written, a unit later
         int late_t = 0, late_n = 0, late_b = 0, late_h = 0;
         auto write_dq = [&](bool sums, int t, int n, int b, int h) {
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.dq) + (((size_t)b * s.T + t) * s.Hq + h) * s.D;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.dq) + (((size_t)b * s.T + t) * s.Hq + h) * D;
 #pragma unroll 1
-            for (int e = 32 * half; e < s.D; e += 64) {  // every other 32 channels for each half
+            for (int e = 32 * half; e < D; e += 64) {  // every other 32 channels for each half
                 float o[32];
                 if (sums) {
                     tmem_ld32(lanes + COL_SUM + e, o);
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 tc_fence_after();
 #pragma unroll 1
-                for (int e = 0; e < s.D / 2; e += 16) {
+                for (int e = 0; e < D / 2; e += 16) {
                     uint32_t w[16];
 #pragma unroll
                     for (int k = 0; k < 4; k++) {
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (half == 0) mbar_arrive(&bar.kept[0]);
                 }
                 // half of the row's sum of do o, o with what its rounding left
-                const int extra = a.rest ? 2 : 1, width = s.D / 16, o_at = 2 * np + extra * units;  // chunks of 8 channels; place in the ring
+                const int extra = a.rest ? 2 : 1, width = D / 16, o_at = 2 * np + extra * units;  // chunks of 8 channels; place in the ring
                 ok = wait_phase(&bar.keep[1], units & 1, &failed, 102);
                 for (int k = 0; k < extra; k++) ok = ok && wait_phase(&bar.full[(o_at + k) % SLOTS], (o_at + k) / SLOTS & 1, &failed, 103);
                 float d = 0.f;
@@ -647,10 +647,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int j = x.j0 + row;
                 const bool there = j < n;
                 const float f = half ? s.scale : 1.f;
-                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(half ? a.dk : a.dv) + (((size_t)x.b * s.T + j) * s.Hk + x.hk) * s.D;
-                float* part = a.parts + (((size_t)x.part * 2 + half) * C + row) * s.D;
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(half ? a.dk : a.dv) + (((size_t)x.b * s.T + j) * s.Hk + x.hk) * D;
+                float* part = a.parts + (((size_t)x.part * 2 + half) * C + row) * D;
 #pragma unroll 1
-                for (int e = 0; e < s.D; e += 32) {
+                for (int e = 0; e < D; e += 32) {
                     float o[32];
                     if (count > 0) {
                         tmem_ld32(lanes + (half ? COL_SUM : COL_V) + e, o);
@@ -733,24 +733,24 @@ struct Cut {
     }
 };
 
-template <bool KEYS>
+// Before the tensor maps: the first runtime call of a host thread makes the device's context current there.
+template <int D>
+cudaError_t allow_smem() {
+    if (cudaError_t e = cudaFuncSetAttribute(window_grad_kernel<false, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES)) return e;
+    return cudaFuncSetAttribute(window_grad_kernel<true, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+}
+
+template <bool KEYS, int D>
 cudaError_t launch(const CUtensorMap* maps, const GradArgs& a, const char* name, cudaStream_t st) {
     trace_begin(name, st);
-    window_grad_kernel<KEYS><<<(unsigned)(a.units < SMS ? a.units : SMS), THREADS, BYTES, st>>>(maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], a);
+    window_grad_kernel<KEYS, D><<<(unsigned)(a.units < SMS ? a.units : SMS), THREADS, BYTES, st>>>(maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], a);
     trace_end(st);
     return cudaGetLastError();
 }
 
-}  // namespace
-
-size_t window_parts_bytes(const WindowShape& s) {
-    return s.bf16 && s.B > 0 && s.T > 0 ? (size_t)Cut(s).parts * 2 * C * s.D * sizeof(float) : 0;
-}
-
-cudaError_t launch_window_bwd_tc(const WindowArgs& x, cudaStream_t st) {
-    // before the tensor maps: the first runtime call of a host thread makes the device's context current there
-    if (cudaError_t e = cudaFuncSetAttribute(window_grad_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES)) return e;
-    if (cudaError_t e = cudaFuncSetAttribute(window_grad_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES)) return e;
+template <int D>
+cudaError_t launch_bwd(const WindowArgs& x, cudaStream_t st) {
+    if (cudaError_t e = allow_smem<D>()) return e;
     CUtensorMap maps[6];
     if (!rows_map(&maps[4], x.o, x.s, x.s.Hq) || !rows_map(&maps[5], x.rest ? x.rest : x.o, x.s, x.s.Hq)) return cudaErrorInvalidValue;
     if (!rows_map(&maps[0], x.q, x.s, x.s.Hq) || !rows_map(&maps[1], x.k, x.s, x.s.Hk) || !rows_map(&maps[2], x.v, x.s, x.s.Hk) ||
@@ -772,10 +772,10 @@ cudaError_t launch_window_bwd_tc(const WindowArgs& x, cudaStream_t st) {
     a.parts = x.parts;
     a.status = x.status;
     a.units = (long long)x.s.B * x.s.Hq * cut.tiles;
-    if (cudaError_t e = launch<false>(maps, a, "window_dq_tc", st)) return e;
+    if (cudaError_t e = launch<false, D>(maps, a, "window_dq_tc", st)) return e;
     const long long heads = (long long)x.s.B * x.s.Hk, first = heads * cut.cut * cut.pieces_cut;
     a.units = first + heads * (cut.tiles - cut.cut) * cut.pieces;
-    if (cudaError_t e = launch<true>(maps, a, "window_dkv_tc", st)) return e;
+    if (cudaError_t e = launch<true, D>(maps, a, "window_dkv_tc", st)) return e;
     const struct { int first, tiles, pieces; long long part0; } joins[2] = {
         {0, cut.cut, cut.pieces_cut, 0}, {cut.cut, cut.tiles - cut.cut, cut.pieces, cut.pieces_cut > 1 ? first : 0}};
     for (const auto& j : joins) {
@@ -786,6 +786,16 @@ cudaError_t launch_window_bwd_tc(const WindowArgs& x, cudaStream_t st) {
         if (cudaError_t e = cudaGetLastError()) return e;
     }
     return cudaSuccess;
+}
+
+}  // namespace
+
+size_t window_parts_bytes(const WindowShape& s) {
+    return s.bf16 && s.B > 0 && s.T > 0 ? (size_t)Cut(s).parts * 2 * C * s.D * sizeof(float) : 0;
+}
+
+cudaError_t launch_window_bwd_tc(const WindowArgs& x, cudaStream_t st) {
+    return x.s.D == 32 ? launch_bwd<32>(x, st) : x.s.D == 64 ? launch_bwd<64>(x, st) : launch_bwd<128>(x, st);
 }
 
 }  // namespace gdr

@@ -78,8 +78,6 @@ struct Unit {
             both.first = min(max(tiles[0].first, tiles[1].first), both.lo);
         }
     }
-    __device__ __forceinline__ bool first(int i, int tile) const { return tile == tiles[i].at(0); }
-    __device__ __forceinline__ bool last(int i, int tile) const { return tile == tiles[i].hi - 1; }
 };
 
 // The units of a CTA: every other round in reverse order, so that long and short ones even out.
@@ -87,6 +85,7 @@ __device__ __forceinline__ long long unit_of(long long round) {
     return round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
 
+template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
     window_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                          const __grid_constant__ CUtensorMap mv, FwdArgs a) {
@@ -130,7 +129,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = tmem_sh;
-    const int panels = s.D > 64 ? 2 : 1;
+    constexpr int panels = D > 64 ? 2 : 1;
     constexpr uint32_t COL_S = 0, COL_O = 256;
 
     if (warp >= 8) {
@@ -180,89 +179,89 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
         } else if (warp == 9) {
-            const uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, s.D, 0, 1);
-            int npv[2] = {0, 0}, nq[2] = {0, 0}, nu[2] = {0, 0};  // P V products; units begun by S; by P V
-            long long round = -1;
-            Unit cur, nxt;
-            int ci = 0, ni = 0, count = 0;  // places in the key tiles of cur and nxt
-            long long pos = 0;              // key tiles whose S has been issued
+            constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, D, 0, 1);
+            Unit x;
+            int tile = 0, i = 0, count = 0;  // a key tile of the stream, its place among the unit's
             bool have = true, ok = true;
-            auto advance = [&]() {  // nxt, ni to the next key tile of the stream
-                if (ni + 1 < count) {
-                    ni++;
-                    return;
-                }
-                ni = 0;
-                count = 0;
-                while (have && count == 0) {
+            int round = -1;
+            auto advance = [&]() {
+                i++;
+                while (i >= count) {
                     round++;
-                    if (round * gridDim.x >= a.units) {
+                    if ((long long)round * gridDim.x >= a.units) {
                         have = false;
-                        break;
+                        return;
                     }
                     const long long u = unit_of(round);
                     if (u >= a.units) continue;
-                    nxt.set(a, u);
-                    count = nxt.both.count();
+                    x.set(a, u);
+                    count = x.both.count();
+                    i = 0;
+                }
+                tile = x.both.at(i);
+            };
+            int slot = 0, lap = 0;  // of the next tile of the ring
+            auto next_slot = [&]() {
+                commit(&empty[slot]);
+                if (++slot == SLOTS) {
+                    slot = 0;
+                    lap ^= 1;
                 }
             };
-            auto issue_s = [&](int i) {
-                const int tile = nxt.both.at(ni);
-                if (!nxt.tiles[i].has(tile)) return true;
-                if (nxt.first(i, tile)) {
-                    if (!wait_phase(&qfull[i], nq[i] & 1, &failed, 72)) return false;
-                    nq[i]++;
-                }
-                const int kp = (int)((2 * pos) % SLOTS);
-                if (!wait_phase(&full[kp], (int)((2 * pos) / SLOTS & 1), &failed, 73)) return false;
+            int nq[2] = {0, 0}, np[2] = {0, 0};  // units begun, P V products
+            auto issue_s = [&](const int w) {
+                if (!x.tiles[w].has(tile)) return;
+                if (tile == x.tiles[w].at(0)) ok = ok && wait_phase(&qfull[w], nq[w]++ & 1, &failed, 72);
+                if (!ok) return;
                 tc_fence_after();
-                const uint32_t ad = lo_kmajor(sb + i * TILE), bd = lo_kmajor(sb + AT_KV + kp * TILE);
-                product_ss(tm + COL_S + 128 * i, ad, bd, id_s, s.D);
-                commit(&sfull[i]);
-                if (nxt.last(i, tile)) commit(&qfree[i]);
-                return true;
+                product_ss<D>(tm + COL_S + 128 * w, lo_kmajor(sb + w * TILE), lo_kmajor(sb + AT_KV + slot * TILE), id_s);
+                commit(&sfull[w]);
+                if (tile == x.tiles[w].hi - 1) commit(&qfree[w]);
             };
-            auto ring_done = [&](long long p) { commit(&empty[(int)(p % SLOTS)]); };
             advance();
             if (have) {
-                ok = issue_s(0) && issue_s(1);
-                ring_done(2 * pos);
-                pos++;
+                ok = wait_phase(&full[slot], lap, &failed, 73);
+                issue_s(0);
+                issue_s(1);
+                next_slot();
             }
 #pragma unroll 1
             while (have && ok) {
-                cur = nxt;
-                ci = ni;
-                const int tile = cur.both.at(ci);
-                const long long vp = 2 * (pos - 1) + 1;
-                const uint32_t vt = sb + AT_KV + (int)(vp % SLOTS) * TILE;
-                advance();
-                if (!wait_phase(&full[(int)(vp % SLOTS)], (int)(vp / SLOTS & 1), &failed, 74)) break;
-                const int m = cur.n - tile * C;
-                if (m < C && cur.n < s.T) zero_rows(vt, m, panels, lane);  // past the end, whatever it holds
+                bool now[2], begin[2];
 #pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    if (cur.tiles[i].has(tile)) {
-                        const bool begin = cur.first(i, tile);
-                        if (begin && nu[i]++ > 0) ok = ok && wait_phase(&ofree[i], nu[i] & 1, &failed, 75);
-                        ok = ok && wait_phase(&pready[i], npv[i] & 1, &failed, 76);
-                        npv[i]++;
+                for (int w = 0; w < 2; w++) {
+                    now[w] = x.tiles[w].has(tile);
+                    begin[w] = now[w] && tile == x.tiles[w].at(0);
+                }
+                const int m = x.n - tile * C;
+                const bool fill = m < C && x.n < s.T;
+                advance();
+                const uint32_t vt = sb + AT_KV + slot * TILE, bd = lo_mnmajor(vt);
+                ok = wait_phase(&full[slot], lap, &failed, 74);
+                if (ok && fill) zero_rows(vt, m, panels, lane);  // past the end, whatever it holds
+                uint64_t* v_empty = &empty[slot];
+                if (++slot == SLOTS) {
+                    slot = 0;
+                    lap ^= 1;
+                }
+#pragma unroll
+                for (int w = 0; w < 2; w++) {
+                    if (now[w]) {
+                        if (begin[w] && nq[w] > 1) ok = ok && wait_phase(&ofree[w], nq[w] & 1, &failed, 75);
+                        ok = ok && wait_phase(&pready[w], np[w]++ & 1, &failed, 76);
                         if (ok) {
                             tc_fence_after();
-                            const uint32_t bd = lo_mnmajor(vt);
-                            product_sum64(tm + COL_O + 128 * i, tm + COL_S + 128 * i, bd, id_o, m, begin);
-                            product_sum64(tm + COL_O + 128 * i, tm + COL_S + 128 * i + 32, bd + step_mnmajor(4), id_o, m - 64, false);
-                            commit(&ofull[i]);
+                            product_sum64(tm + COL_O + 128 * w, tm + COL_S + 128 * w, bd, id_o, m, begin[w]);
+                            product_sum64(tm + COL_O + 128 * w, tm + COL_S + 128 * w + 32, bd + step_mnmajor(4), id_o, m - 64, false);
+                            commit(&ofull[w]);
                         }
                     }
-                    if (ok && have) ok = issue_s(i);
+                    if (w == 0 && have) ok = ok && wait_phase(&full[slot], lap, &failed, 73);
+                    if (ok && have) issue_s(w);
                 }
                 if (!ok) break;
-                ring_done(vp);
-                if (have) {
-                    ring_done(2 * pos);
-                    pos++;
-                }
+                commit(v_empty);
+                if (have) next_slot();
             }
             commit(&drain);  // every product issued so far has completed before TMEM is released
             int never = 0;
@@ -326,7 +325,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int e = 0; e < s.D; e += 32) {
+                    for (int e = 0; e < D; e += 32) {
                         float o[32];
                         tmem_ld32(at_o + e, o);
                         tmem_wait_ld();
@@ -372,10 +371,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             const bool there = t < n;
             const float f = there ? 1.f / l : 0.f;
-            const size_t at = (((size_t)x.b * s.T + t) * s.Hq + head) * s.D;
+            const size_t at = (((size_t)x.b * s.T + t) * s.Hq + head) * D;
             __nv_bfloat16 *out = static_cast<__nv_bfloat16*>(a.o) + at, *rest = static_cast<__nv_bfloat16*>(a.rest) + at;
 #pragma unroll 1
-            for (int e = 0; e < s.D; e += 32) {
+            for (int e = 0; e < D; e += 32) {
                 float o[32];
                 if (count > 0) {
                     tmem_ld32(at_o + e, o);
@@ -420,11 +419,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == 8) tmem_dealloc(tm, 512);
 }
 
-}  // namespace
-
-cudaError_t launch_window_fwd_tc(const WindowArgs& x, cudaStream_t st) {
+template <int D>
+cudaError_t launch_fwd(const WindowArgs& x, cudaStream_t st) {
     // before the tensor maps: the first runtime call of a host thread makes the device's context current there
-    if (cudaError_t e = cudaFuncSetAttribute(window_fwd_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES)) return e;
+    if (cudaError_t e = cudaFuncSetAttribute(window_fwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES)) return e;
     CUtensorMap mq, mk, mv;
     if (!rows_map(&mq, x.q, x.s, x.s.Hq) || !rows_map(&mk, x.k, x.s, x.s.Hk) || !rows_map(&mv, x.v, x.s, x.s.Hk)) return cudaErrorInvalidValue;
     FwdArgs a = {};
@@ -437,9 +435,15 @@ cudaError_t launch_window_fwd_tc(const WindowArgs& x, cudaStream_t st) {
     a.rest = x.rest;
     a.status = x.status;
     trace_begin("window_fwd_tc", st);
-    window_fwd_tc_kernel<<<(unsigned)(a.units < SMS ? a.units : SMS), THREADS, BYTES, st>>>(mq, mk, mv, a);
+    window_fwd_tc_kernel<D><<<(unsigned)(a.units < SMS ? a.units : SMS), THREADS, BYTES, st>>>(mq, mk, mv, a);
     trace_end(st);
     return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_window_fwd_tc(const WindowArgs& x, cudaStream_t st) {
+    return x.s.D == 32 ? launch_fwd<32>(x, st) : x.s.D == 64 ? launch_fwd<64>(x, st) : launch_fwd<128>(x, st);
 }
 
 }  // namespace gdr
