@@ -46,7 +46,8 @@ gdr_status check_window(const gdr_window_problem* p) {
     const gdr_status r = check_heads(p->Hq, p->Hk, p->D, p->window, p->sinks, p->dtype, p->scale);
     if (r != GDR_OK) return r;
     if (p->B > 65535 || p->T > GDR_WINDOW_MAX_T) return GDR_ERR_UNSUPPORTED;        // grid z limit
-    if ((long long)p->B * p->T * p->Hq >= 1LL << 36) return GDR_ERR_UNSUPPORTED;  // a q of 4 TB or more
+    // units of 128 queries (or keys and their pieces, few more than that) of a head are counted in ints
+    if ((long long)p->B * p->Hq * ((p->T + 127) / 128) > 1 << 29) return GDR_ERR_UNSUPPORTED;
     return GDR_OK;
 }
 WindowArgs window_args(const gdr_window_problem* p, const int* lengths) {

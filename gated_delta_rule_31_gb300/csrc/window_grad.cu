@@ -53,7 +53,7 @@ struct GradArgs {
     int tiles;            // of the sequence
     int cut, pieces_cut;  // key tiles from the start, pieces of each
     int pieces;           // pieces of the others
-    long long units;
+    int units;
     const float* lse;
     int rest;  // dq: what the rounding of o left is there
     float* delta;
@@ -62,21 +62,20 @@ struct GradArgs {
     int* status;
 };
 
-__device__ __forceinline__ long long unit_of(long long round) {  // every other round in reverse
-    return round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+__device__ __forceinline__ int unit_of(int round) {  // every other round in reverse
+    return round * (int)gridDim.x + (int)(round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
 
 // dq: 128 queries of a head, and the key tiles that they see.
 struct QueryUnit {
     int b, h, hk, n, t0;
     KeyTiles tiles;
-    __device__ __forceinline__ void set(const GradArgs& a, long long u) {
+    __device__ __forceinline__ void set(const GradArgs& a, int u) {
         const WindowShape& s = a.s;
-        const long long per = (long long)s.Hq * s.B;
-        const int rest = (int)(u % per);
-        t0 = (a.tiles - 1 - (int)(u / per)) * C;
-        h = rest % s.Hq;
+        const int per = s.Hq * s.B, from_top = u / per, rest = u - from_top * per;
+        t0 = (a.tiles - 1 - from_top) * C;
         b = rest / s.Hq;
+        h = rest - b * s.Hq;
         hk = h / (s.Hq / s.Hk);
         n = s.tokens(b);
         tiles = KeyTiles(C, s.window, s.sinks, t0, min(t0 + C, n));
@@ -87,22 +86,22 @@ struct QueryUnit {
 // dkv: 128 keys of a head, a piece of the (query head, query tile) pairs that see them.
 struct KeyUnit {
     int b, hk, n, j0, per, begin, end;  // pairs begin .. end - 1, `per` query tiles a head
-    long long part;                     // index of its piece of `parts`, or -1
-    __device__ __forceinline__ void set(const GradArgs& a, long long u) {
+    int part;                           // index of its piece of `parts`, or -1
+    __device__ __forceinline__ void set(const GradArgs& a, int u) {
         const WindowShape& s = a.s;
-        const long long heads = (long long)s.Hk * s.B, cut = heads * a.cut * a.pieces_cut;
+        const int heads = s.Hk * s.B, cut = heads * a.cut * a.pieces_cut;
         const bool in_cut = u < cut;
         const int pieces = in_cut ? a.pieces_cut : a.pieces;
-        const long long v = in_cut ? u : u - cut;
-        const int head = (int)(v % heads), piece = (int)(v / heads % pieces), tile = (int)(v / heads / pieces) + (in_cut ? 0 : a.cut);
-        hk = head % s.Hk;
+        const int v = in_cut ? u : u - cut, of_heads = v / heads, head = v - of_heads * heads;
+        const int of_tile = of_heads / pieces, piece = of_heads - of_tile * pieces, tile = of_tile + (in_cut ? 0 : a.cut);
         b = head / s.Hk;
+        hk = head - b * s.Hk;
         n = s.tokens(b);
         j0 = tile * C;
         per = j0 < n ? (queries_end(C, s.window, s.sinks, j0, n) - j0 + C - 1) / C : 0;
-        const long long all = (long long)per * (s.Hq / s.Hk);
-        begin = (int)(all * piece / pieces);
-        end = (int)(all * (piece + 1) / pieces);
+        const int all = per * (s.Hq / s.Hk);
+        begin = pieces == 1 ? 0 : (int)((long long)all * piece / pieces);
+        end = pieces == 1 ? all : (int)((long long)all * (piece + 1) / pieces);
         part = pieces == 1 ? -1 : in_cut || a.pieces_cut == 1 ? v : u;
     }
     __device__ __forceinline__ int count() const { return end - begin; }
@@ -135,16 +134,15 @@ template <typename U>
 struct Stream {
     U x;
     Queries at;
-    long long round = -1;
-    int i = 0, count = 0;
+    int round = -1, i = 0, count = 0;
     __device__ __forceinline__ Pair next(const GradArgs& a) {
         if (++i < count) {
             if constexpr (std::is_same<U, KeyUnit>::value) at.next(x);
         }
         while (i >= count) {
             round++;
-            if (round * gridDim.x >= a.units) return Pair{false, false, false, 0};
-            const long long u = unit_of(round);
+            if (round * (int)gridDim.x >= a.units) return Pair{false, false, false, 0};
+            const int u = unit_of(round);
             if (u >= a.units) continue;
             x.set(a, u);
             i = 0;
@@ -256,10 +254,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 pos++;
             };
 #pragma unroll 1
-            for (long long round = 0; ok; round++) {
-                const long long u = unit_of(round);
+            for (int round = 0; ok; round++) {
+                const int u = unit_of(round);
                 if (u >= a.units) {
-                    if (round * gridDim.x >= a.units) break;
+                    if (round * (int)gridDim.x >= a.units) break;
                     continue;
                 }
                 U x;
@@ -444,6 +442,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t at_s = lanes + COL_S + 64 * half, at_dp = lanes + COL_DP + 64 * half;
         const float c = s.scale * LOG2E;
         const uint64_t c2 = pair(c, c);
+        const bool wide = on32(KEYS ? half ? a.dk : a.dv : a.dq);
         int np = 0, units = 0;
         bool ok = true;
         // dq: the rows that are still to be written, a unit later
@@ -457,9 +456,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tmem_ld32(lanes + COL_SUM + e, o);
                     tmem_wait_ld();
                 }
-                if (t < s.T)
+                if (t >= s.T) continue;
+                uint4 y[4];
 #pragma unroll
-                    for (int k = 0; k < 32; k += 8) *reinterpret_cast<uint4*>(out + e + k) = t < n ? pack8(o + k, s.scale) : make_uint4(0, 0, 0, 0);
+                for (int k = 0; k < 4; k++) y[k] = t < n ? pack8(o + 8 * k, s.scale) : make_uint4(0, 0, 0, 0);
+                st_row(out + e, y[0], y[1], wide);
+                st_row(out + e + 16, y[2], y[3], wide);
             }
         };
         auto write_late = [&]() {  // of unit number `units`, counted from 1
@@ -472,10 +474,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (lane == 0) mbar_arrive(&bar.sumfree);
         };
 #pragma unroll 1
-        for (long long round = 0; ok; round++) {
-            const long long u = unit_of(round);
+        for (int round = 0; ok; round++) {
+            const int u = unit_of(round);
             if (u >= a.units) {
-                if (round * gridDim.x >= a.units) break;
+                if (round * (int)gridDim.x >= a.units) break;
                 continue;
             }
             U x;
@@ -515,22 +517,30 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (half == 0) mbar_arrive(&bar.kept[0]);
                 }
                 // half of the row's sum of do o, o with what its rounding left
-                const int extra = a.rest ? 2 : 1, width = D / 16, o_at = 2 * np + extra * units;  // chunks of 8 channels; place in the ring
+                constexpr int width = D / 16;
+                const int extra = a.rest ? 2 : 1, o_at = 2 * np + extra * units;  // chunks of 8 channels; place in the ring
                 ok = wait_phase(&bar.keep[1], units & 1, &failed, 102);
                 for (int k = 0; k < extra; k++) ok = ok && wait_phase(&bar.full[(o_at + k) % SLOTS], (o_at + k) / SLOTS & 1, &failed, 103);
                 float d = 0.f;
                 if (ok && t < n) {
                     const uint32_t at_o = sb + AT_RING + o_at % SLOTS * TILE, at_r = sb + AT_RING + (o_at + 1) % SLOTS * TILE;
-#pragma unroll 2
-                    for (int e = half * width; e < (half + 1) * width; e++) {
-                        const uint32_t chunk = sw128_chunk(row, e, C);
-                        float y[8], z[8] = {}, g[8];
-                        unpack8(ld_shared_v4(at_o + chunk), y);
-                        if (a.rest) unpack8(ld_shared_v4(at_r + chunk), z);
-                        unpack8(ld_shared_v4(sb + TILE + chunk), g);
+                    uint64_t sum[2] = {0, 0};
 #pragma unroll
-                        for (int k = 0; k < 8; k++) d = fmaf(g[k], y[k] + z[k], d);
+                    for (int e = 0; e < width; e++) {
+                        const uint32_t chunk = sw128_chunk(row, half * width + e, C);
+                        const uint4 y = ld_shared_v4(at_o + chunk), g = ld_shared_v4(sb + TILE + chunk);
+                        const uint4 z = a.rest ? ld_shared_v4(at_r + chunk) : make_uint4(0, 0, 0, 0);
+                        const uint32_t ys[4] = {y.x, y.y, y.z, y.w}, zs[4] = {z.x, z.y, z.z, z.w}, gs[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            const uint64_t w = pair(bf16lo(gs[k]), bf16hi(gs[k]));
+                            sum[0] = fma2(w, pair(bf16lo(ys[k]), bf16hi(ys[k])), sum[0]);
+                            sum[1] = fma2(w, pair(bf16lo(zs[k]), bf16hi(zs[k])), sum[1]);
+                        }
                     }
+                    float s0, s1;
+                    unpair(add2(sum[0], sum[1]), s0, s1);
+                    d = s0 + s1;
                 }
                 float(*halves)[C] = units & 1 ? lse_sh : delta_sh;
                 halves[half][row] = d;
@@ -663,8 +673,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                         for (int k = 0; k < 32; k += 4) *reinterpret_cast<float4*>(part + e + k) = make_float4(f * o[k], f * o[k + 1], f * o[k + 2], f * o[k + 3]);
                     } else if (j < s.T) {
-#pragma unroll
-                        for (int k = 0; k < 32; k += 8) *reinterpret_cast<uint4*>(out + e + k) = pack8(o + k, f);
+                        st_row(out + e, pack8(o, f), pack8(o + 8, f), wide);
+                        st_row(out + e + 16, pack8(o + 16, f), pack8(o + 24, f), wide);
                     }
                 }
                 if (count > 0) {
@@ -771,12 +781,12 @@ cudaError_t launch_bwd(const WindowArgs& x, cudaStream_t st) {
     a.dv = x.dv;
     a.parts = x.parts;
     a.status = x.status;
-    a.units = (long long)x.s.B * x.s.Hq * cut.tiles;
+    a.units = x.s.B * x.s.Hq * cut.tiles;
     if (cudaError_t e = launch<false, D>(maps, a, "window_dq_tc", st)) return e;
-    const long long heads = (long long)x.s.B * x.s.Hk, first = heads * cut.cut * cut.pieces_cut;
+    const int heads = x.s.B * x.s.Hk, first = heads * cut.cut * cut.pieces_cut;
     a.units = first + heads * (cut.tiles - cut.cut) * cut.pieces;
     if (cudaError_t e = launch<true, D>(maps, a, "window_dkv_tc", st)) return e;
-    const struct { int first, tiles, pieces; long long part0; } joins[2] = {
+    const struct { int first, tiles, pieces, part0; } joins[2] = {
         {0, cut.cut, cut.pieces_cut, 0}, {cut.cut, cut.tiles - cut.cut, cut.pieces, cut.pieces_cut > 1 ? first : 0}};
     for (const auto& j : joins) {
         if (j.pieces == 1 || j.tiles == 0) continue;

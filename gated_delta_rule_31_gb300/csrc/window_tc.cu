@@ -46,7 +46,7 @@ struct FwdArgs {
     WindowShape s;
     int pair_heads;     // a unit's two tiles are heads h, h + 1 of a row tile; else row tiles 2 i, 2 i + 1 of a head
     int row_tiles;      // of the sequence
-    long long units;
+    int units;
     void *o, *rest;
     float* lse;
     int* status;
@@ -56,13 +56,13 @@ struct FwdArgs {
 struct Unit {
     int b, hk, n, h[2], t0[2];
     KeyTiles tiles[2], both;
-    __device__ __forceinline__ void set(const FwdArgs& a, long long u) {
+    __device__ __forceinline__ void set(const FwdArgs& a, int u) {
         const WindowShape& s = a.s;
         // the longest rows first, the heads of a row tile next to one another
         const int cols = a.pair_heads ? s.Hq / 2 : s.Hq, rows = a.pair_heads ? a.row_tiles : (a.row_tiles + 1) / 2;
-        const long long per = (long long)cols * s.B;
-        const int r = rows - 1 - (int)(u / per), rest = (int)(u % per), col = rest % cols;
+        const int per = cols * s.B, from_top = u / per, r = rows - 1 - from_top, rest = u - from_top * per;
         b = rest / cols;
+        const int col = rest - b * cols;
         n = s.tokens(b);
         h[0] = a.pair_heads ? 2 * col : col;
         h[1] = a.pair_heads ? 2 * col + 1 : col;
@@ -81,8 +81,8 @@ struct Unit {
 };
 
 // The units of a CTA: every other round in reverse order, so that long and short ones even out.
-__device__ __forceinline__ long long unit_of(long long round) {
-    return round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+__device__ __forceinline__ int unit_of(int round) {
+    return round * (int)gridDim.x + (int)(round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
 
 template <int D>
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                          const __grid_constant__ CUtensorMap mv, FwdArgs a) {
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
-    __shared__ uint64_t qfull[2], qfree[2], full[SLOTS], empty[SLOTS], sfull[2], pready[2], ofull[2], ofree[2], drain;
+    __shared__ uint64_t qfull[2], qfree[2], full[SLOTS], empty[SLOTS], sfull[2], pready[2], ofull[2][2], ofree[2], drain;  // ofull: of even and odd tiles
     __shared__ uint32_t tmem_sh;
     __shared__ int failed, used[SLOTS], used_q[2];
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -115,7 +115,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&qfree[i], 1);
             mbar_init(&sfull[i], 1);
             mbar_init(&pready[i], 4);
-            mbar_init(&ofull[i], 1);
+            mbar_init(&ofull[i][0], 1);
+            mbar_init(&ofull[i][1], 1);
             mbar_init(&ofree[i], 4);
         }
         mbar_init(&drain, 1);
@@ -149,10 +150,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 pos++;
             };
 #pragma unroll 1
-            for (long long round = 0; ok; round++) {
-                const long long u = unit_of(round);
+            for (int round = 0; ok; round++) {
+                const int u = unit_of(round);
                 if (u >= a.units) {
-                    if (round * gridDim.x >= a.units) break;
+                    if (round * (int)gridDim.x >= a.units) break;
                     continue;
                 }
                 Unit x;
@@ -188,11 +189,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                 i++;
                 while (i >= count) {
                     round++;
-                    if ((long long)round * gridDim.x >= a.units) {
+                    if (round * (int)gridDim.x >= a.units) {
                         have = false;
                         return;
                     }
-                    const long long u = unit_of(round);
+                    const int u = unit_of(round);
                     if (u >= a.units) continue;
                     x.set(a, u);
                     count = x.both.count();
@@ -248,13 +249,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int w = 0; w < 2; w++) {
                     if (now[w]) {
                         if (begin[w] && nq[w] > 1) ok = ok && wait_phase(&ofree[w], nq[w] & 1, &failed, 75);
-                        ok = ok && wait_phase(&pready[w], np[w]++ & 1, &failed, 76);
+                        ok = ok && wait_phase(&pready[w], np[w] & 1, &failed, 76);
                         if (ok) {
                             tc_fence_after();
                             product_sum64(tm + COL_O + 128 * w, tm + COL_S + 128 * w, bd, id_o, m, begin[w]);
                             product_sum64(tm + COL_O + 128 * w, tm + COL_S + 128 * w + 32, bd + step_mnmajor(4), id_o, m - 64, false);
-                            commit(&ofull[w]);
+                            commit(&ofull[w][np[w] & 1]);
                         }
+                        np[w]++;
                     }
                     if (w == 0 && have) ok = ok && wait_phase(&full[slot], lap, &failed, 73);
                     if (ok && have) issue_s(w);
@@ -272,13 +274,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int i = warp >> 2, row = 32 * (warp & 3) + lane;
         const uint32_t lanes = tm + ((uint32_t)(32 * (warp & 3)) << 16), at_s = lanes + COL_S + 128 * i, at_o = lanes + COL_O + 128 * i;
         const float c = s.scale * LOG2E;
+        const bool wide_o = on32(a.o), wide_rest = on32(a.rest);
         int np = 0;  // tiles so far
         bool ok = true;
 #pragma unroll 1
-        for (long long round = 0; ok; round++) {
-            const long long u = unit_of(round);
+        for (int round = 0; ok; round++) {
+            const int u = unit_of(round);
             if (u >= a.units) {
-                if (round * gridDim.x >= a.units) break;
+                if (round * (int)gridDim.x >= a.units) break;
                 continue;
             }
             Unit x;
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const float to = fmaxf(m, now), f = to == m ? 1.f : exp2_fast((m - to) * c);
                     m = to;
                     l *= f;
-                    ok = wait_phase(&ofull[i], (np + 1) & 1, &failed, 78);  // the product before
+                    ok = wait_phase(&ofull[i][(np + 1) & 1], (np - 1) >> 1 & 1, &failed, 78);  // the product before
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
@@ -354,9 +357,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 float s0, s1;
                 unpair(add2(sum[0], sum[1]), s0, s1);
                 l += s0 + s1;
-                // the product before: complete, since S came after it, and its phase is taken before the next one's can end
-                ok = np == 0 || wait_phase(&ofull[i], (np + 1) & 1, &failed, 80);
-                if (!ok) break;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!ok) break;
             if (t0 >= s.T) continue;  // no such row tile
             if (count > 0) {
-                ok = wait_phase(&ofull[i], (np + 1) & 1, &failed, 79);
+                ok = wait_phase(&ofull[i][(np + 1) & 1], (np - 1) >> 1 & 1, &failed, 79);
                 if (!ok) break;
                 tc_fence_after();
             }
@@ -380,19 +380,24 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tmem_ld32(at_o + e, o);
                     tmem_wait_ld();
                 }
-                if (t < s.T)
+                if (t >= s.T) continue;
+                uint4 y[4];
 #pragma unroll
-                    for (int k = 0; k < 32; k += 8) {
-                        const uint4 y = there ? pack8(o + k, f) : make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4*>(out + e + k) = y;
-                        if (a.rest) {
-                            float z[8];
-                            unpack8(y, z);
+                for (int k = 0; k < 4; k++) y[k] = there ? pack8(o + 8 * k, f) : make_uint4(0, 0, 0, 0);
+                st_row(out + e, y[0], y[1], wide_o);
+                st_row(out + e + 16, y[2], y[3], wide_o);
+                if (a.rest) {
 #pragma unroll
-                            for (int d = 0; d < 8; d++) z[d] = there ? fmaf(f, o[k + d], -z[d]) : 0.f;
-                            *reinterpret_cast<uint4*>(rest + e + k) = pack8(z, 1.f);
-                        }
+                    for (int k = 0; k < 4; k++) {
+                        float z[8];
+                        unpack8(y[k], z);
+#pragma unroll
+                        for (int d = 0; d < 8; d++) z[d] = there ? fmaf(f, o[8 * k + d], -z[d]) : 0.f;
+                        y[k] = pack8(z, 1.f);
                     }
+                    st_row(rest + e, y[0], y[1], wide_rest);
+                    st_row(rest + e + 16, y[2], y[3], wide_rest);
+                }
             }
             if (count > 0) {
                 tc_fence_before();
@@ -429,7 +434,7 @@ cudaError_t launch_fwd(const WindowArgs& x, cudaStream_t st) {
     a.s = x.s;
     a.pair_heads = x.s.Hq / x.s.Hk % 2 == 0;
     a.row_tiles = (x.s.T + C - 1) / C;
-    a.units = (long long)x.s.B * (a.pair_heads ? (long long)x.s.Hq / 2 * a.row_tiles : (long long)x.s.Hq * ((a.row_tiles + 1) / 2));
+    a.units = x.s.B * (a.pair_heads ? x.s.Hq / 2 * a.row_tiles : x.s.Hq * ((a.row_tiles + 1) / 2));
     a.o = x.o;
     a.lse = x.lse;
     a.rest = x.rest;
