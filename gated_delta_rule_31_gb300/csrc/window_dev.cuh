@@ -14,6 +14,21 @@ using namespace linear;  // C = 128 tokens of a tile, TILE, PANEL, products and 
 
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
+// Bounded wait of a whole warp for phase `parity`, as linear::wait_phase but parked for the machine's own short time at once: a
+// phase that is complete, as most are here, then takes 61 cycles and not 123. Gives up after about a second, leaving the site in
+// *failed, or as soon as another warp has.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* failed, int site) {
+    bool ok = __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) != 0;
+    if (!ok) {
+        const long long t0 = clock64();
+        while (!(ok = __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) != 0)) {
+            if (clock64() - t0 > kWaitCycles) *failed = site;
+            if (__any_sync(0xffffffffu, *failed)) break;
+        }
+    }
+    return ok;
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

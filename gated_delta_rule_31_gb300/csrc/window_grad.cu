@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             };
             auto stream = [&](const CUtensorMap* map, int head, int t, int b) {
                 const int k = pos % SLOTS, use = pos / SLOTS;
-                if (use > 0) ok = ok && wait_phase(&bar.empty[k], (use + 1) & 1, &failed, 90);
+                if (use > 0) ok = ok && wait_for(&bar.empty[k], (use + 1) & 1, &failed, 90);
                 put(AT_RING + k * TILE, map, head, t, b, &bar.full[k], &used[k]);
                 pos++;
             };
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int w = 0; w < 2; w++) {
                         if (i == 0) {
-                            if (units > 0) ok = ok && wait_phase(&bar.kept[w], (units + 1) & 1, &failed, 91);
+                            if (units > 0) ok = ok && wait_for(&bar.kept[w], (units + 1) & 1, &failed, 91);
                             if constexpr (KEYS) {
                                 put(w * TILE, w ? &mv : &mk, x.hk, x.j0, x.b, &bar.keep[w], &used_keep[w]);
                             } else {
@@ -306,17 +306,17 @@ __global__ void __launch_bounds__(THREADS, 1)
             const bool ragged = s.lengths != nullptr;
             auto slot = [&](int at) { return sb + AT_RING + at % SLOTS * TILE; };
             auto there = [&](int at, int m) {  // the streamed tile, finite past its tokens
-                ok = ok && wait_phase(&bar.full[at % SLOTS], at / SLOTS & 1, &failed, 92);
+                ok = ok && wait_for(&bar.full[at % SLOTS], at / SLOTS & 1, &failed, 92);
                 if (ok && ragged && m < C) zero_rows(slot(at), m, panels, lane);
             };
             auto done = [&](int at) { commit(&bar.empty[at % SLOTS]); };
             auto rows_ready = [&](uint64_t* b, int site) {
-                ok = ok && wait_phase(b, pos & 1, &failed, site);
+                ok = ok && wait_for(b, pos & 1, &failed, site);
                 tc_fence_after();
                 return ok;
             };
             auto sums_begin = [&](const Pair& p) {
-                if (p.first && summed++ > 0) ok = ok && wait_phase(&bar.sumfree, summed & 1, &failed, 94);
+                if (p.first && summed++ > 0) ok = ok && wait_for(&bar.sumfree, summed & 1, &failed, 94);
             };
             Pair cur = stream.next(a);
             if constexpr (KEYS) {
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 auto issue = [&](int w, const Pair& p, int at) {
                     if (!ok || !p.some) return;
                     if (p.first) {
-                        ok = wait_phase(&bar.keep[w], started & 1, &failed, 93);
+                        ok = wait_for(&bar.keep[w], started & 1, &failed, 93);
                         started += w;
                     }
                     there(at, p.m);
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 auto begin_unit = [&]() {  // S and dP of a unit's first pair
                     if (!ok || !cur.some) return;
                     ring += extra;
-                    ok = wait_phase(&bar.aready, started++ & 1, &failed, 93);
+                    ok = wait_for(&bar.aready, started++ & 1, &failed, 93);
 #pragma unroll
                     for (int w = 0; w < 2; w++) {
                         there(ring + w, cur.m);
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             commit(&bar.drain);  // every product issued so far has completed before TMEM is released
             int never = 0;
-            wait_phase(&bar.drain, 0, &never, 1);
+            wait_for(&bar.drain, 0, &never, 1);
         } else if (KEYS && warp == 10) {
             if constexpr (KEYS) {
                 Stream<KeyUnit> stream;
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         l[e] = r < p.m ? -LOG2E * a.lse[row + r] : -INFINITY;
                         d[e] = r < p.m ? -a.delta[row + r] : 0.f;
                     }
-                    if (pos >= 2 && !wait_phase(&bar.lfree[pos & 1], (pos / 2 + 1) & 1, &failed, 97)) break;
+                    if (pos >= 2 && !wait_for(&bar.lfree[pos & 1], (pos / 2 + 1) & 1, &failed, 97)) break;
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
                         lse_sh[pos & 1][lane + 32 * e] = l[e];
@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         };
         auto write_late = [&]() {  // of unit number `units`, counted from 1
-            ok = wait_phase(&bar.sumfull, (units + 1) & 1, &failed, 100);
+            ok = wait_for(&bar.sumfull, (units + 1) & 1, &failed, 100);
             if (!ok) return;
             tc_fence_after();
             write_dq(true, late_t, late_n, late_b, late_h);
@@ -493,13 +493,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const size_t stat = ((size_t)x.b * s.Hq + x.h) * s.T + t;
                 const float l = t < n ? -LOG2E * a.lse[stat] : 0.f;
                 // the row of Q (first half) or dO into TMEM: the unit before has done with it, on both sides
-                ok = wait_phase(&bar.keep[half], units & 1, &failed, 101);
+                ok = wait_for(&bar.keep[half], units & 1, &failed, 101);
                 if (bar_sync_or(1, 256, !ok)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-#pragma unroll 1
+#pragma unroll
                 for (int e = 0; e < D / 2; e += 16) {
                     uint32_t w[16];
 #pragma unroll
@@ -519,8 +519,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 // half of the row's sum of do o, o with what its rounding left
                 constexpr int width = D / 16;
                 const int extra = a.rest ? 2 : 1, o_at = 2 * np + extra * units;  // chunks of 8 channels; place in the ring
-                ok = wait_phase(&bar.keep[1], units & 1, &failed, 102);
-                for (int k = 0; k < extra; k++) ok = ok && wait_phase(&bar.full[(o_at + k) % SLOTS], (o_at + k) / SLOTS & 1, &failed, 103);
+                ok = wait_for(&bar.keep[1], units & 1, &failed, 102);
+                for (int k = 0; k < extra; k++) ok = ok && wait_for(&bar.full[(o_at + k) % SLOTS], (o_at + k) / SLOTS & 1, &failed, 103);
                 float d = 0.f;
                 if (ok && t < n) {
                     const uint32_t at_o = sb + AT_RING + o_at % SLOTS * TILE, at_r = sb + AT_RING + (o_at + 1) % SLOTS * TILE;
@@ -566,8 +566,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             if constexpr (KEYS) at.begin(x);
 #pragma unroll 1
             for (int i = 0; i < count; i++, np++) {
-                if (KEYS) ok = wait_phase(&bar.lfull[np & 1], np / 2 & 1, &failed, 97);
-                ok = ok && wait_phase(&bar.sfull[KEYS ? 0 : half], np & 1, &failed, 98);
+                if (KEYS) ok = wait_for(&bar.lfull[np & 1], np / 2 & 1, &failed, 97);
+                ok = ok && wait_for(&bar.sfull[KEYS ? 0 : half], np & 1, &failed, 98);
                 if (!ok) break;
                 tc_fence_after();
                 float p[64];
@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.pready);
                 }
-                ok = wait_phase(&bar.dpfull[KEYS ? 0 : half], np & 1, &failed, 99);
+                ok = wait_for(&bar.dpfull[KEYS ? 0 : half], np & 1, &failed, 99);
                 if (!ok) break;
                 tc_fence_after();
                 const float4* dt = reinterpret_cast<const float4*>(delta_sh[np & 1]) + 16 * half;
@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (count > 0) units++;
             if constexpr (KEYS) {  // the first four warps write dv, the others dk
                 if (count > 0) {
-                    ok = wait_phase(&bar.sumfull, (units + 1) & 1, &failed, 100);
+                    ok = wait_for(&bar.sumfull, (units + 1) & 1, &failed, 100);
                     if (!ok) break;
                     tc_fence_after();
                 }

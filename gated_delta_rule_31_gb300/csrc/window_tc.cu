@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             bool ok = true;
             auto load = [&](const CUtensorMap* map, int head, int t, int b) {
                 const int k = pos % SLOTS, use = pos / SLOTS;
-                if (use > 0) ok = wait_phase(&empty[k], (use + 1) & 1, &failed, 70);
+                if (use > 0) ok = wait_for(&empty[k], (use + 1) & 1, &failed, 70);
                 if (ok && lane == 0) {
                     mbar_expect_tx(&full[k], panels * PANEL);
                     used[k] = use + 1;
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < 2; i++) {
                     if (!ok || x.tiles[i].count() == 0) continue;
-                    if (nq[i] > 0) ok = wait_phase(&qfree[i], (nq[i] + 1) & 1, &failed, 71);
+                    if (nq[i] > 0) ok = wait_for(&qfree[i], (nq[i] + 1) & 1, &failed, 71);
                     if (ok && lane == 0) {
                         mbar_expect_tx(&qfull[i], panels * PANEL);
                         used_q[i] = nq[i] + 1;
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             int nq[2] = {0, 0}, np[2] = {0, 0};  // units begun, P V products
             auto issue_s = [&](const int w) {
                 if (!x.tiles[w].has(tile)) return;
-                if (tile == x.tiles[w].at(0)) ok = ok && wait_phase(&qfull[w], nq[w]++ & 1, &failed, 72);
+                if (tile == x.tiles[w].at(0)) ok = ok && wait_for(&qfull[w], nq[w]++ & 1, &failed, 72);
                 if (!ok) return;
                 tc_fence_after();
                 product_ss<D>(tm + COL_S + 128 * w, lo_kmajor(sb + w * TILE), lo_kmajor(sb + AT_KV + slot * TILE), id_s);
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             };
             advance();
             if (have) {
-                ok = wait_phase(&full[slot], lap, &failed, 73);
+                ok = wait_for(&full[slot], lap, &failed, 73);
                 issue_s(0);
                 issue_s(1);
                 next_slot();
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const bool fill = m < C && x.n < s.T;
                 advance();
                 const uint32_t vt = sb + AT_KV + slot * TILE, bd = lo_mnmajor(vt);
-                ok = wait_phase(&full[slot], lap, &failed, 74);
+                ok = wait_for(&full[slot], lap, &failed, 74);
                 if (ok && fill) zero_rows(vt, m, panels, lane);  // past the end, whatever it holds
                 uint64_t* v_empty = &empty[slot];
                 if (++slot == SLOTS) {
@@ -248,8 +248,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int w = 0; w < 2; w++) {
                     if (now[w]) {
-                        if (begin[w] && nq[w] > 1) ok = ok && wait_phase(&ofree[w], nq[w] & 1, &failed, 75);
-                        ok = ok && wait_phase(&pready[w], np[w] & 1, &failed, 76);
+                        if (begin[w] && nq[w] > 1) ok = ok && wait_for(&ofree[w], nq[w] & 1, &failed, 75);
+                        ok = ok && wait_for(&pready[w], np[w] & 1, &failed, 76);
                         if (ok) {
                             tc_fence_after();
                             product_sum64(tm + COL_O + 128 * w, tm + COL_S + 128 * w, bd, id_o, m, begin[w]);
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                         np[w]++;
                     }
-                    if (w == 0 && have) ok = ok && wait_phase(&full[slot], lap, &failed, 73);
+                    if (w == 0 && have) ok = ok && wait_for(&full[slot], lap, &failed, 73);
                     if (ok && have) issue_s(w);
                 }
                 if (!ok) break;
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             commit(&drain);  // every product issued so far has completed before TMEM is released
             int never = 0;
-            wait_phase(&drain, 0, &never, 1);
+            wait_for(&drain, 0, &never, 1);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_ROWS));
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll 1
             for (int it = 0; it < count; it++, np++) {
                 const int j0 = tiles.at(it) * C;
-                ok = wait_phase(&sfull[i], np & 1, &failed, 77);
+                ok = wait_for(&sfull[i], np & 1, &failed, 77);
                 if (!ok) break;
                 tc_fence_after();
                 float v[128];
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const float to = fmaxf(m, now), f = to == m ? 1.f : exp2_fast((m - to) * c);
                     m = to;
                     l *= f;
-                    ok = wait_phase(&ofull[i][(np + 1) & 1], (np - 1) >> 1 & 1, &failed, 78);  // the product before
+                    ok = wait_for(&ofull[i][(np + 1) & 1], (np - 1) >> 1 & 1, &failed, 78);  // the product before
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!ok) break;
             if (t0 >= s.T) continue;  // no such row tile
             if (count > 0) {
-                ok = wait_phase(&ofull[i][(np + 1) & 1], (np - 1) >> 1 & 1, &failed, 79);
+                ok = wait_for(&ofull[i][(np + 1) & 1], (np - 1) >> 1 & 1, &failed, 79);
                 if (!ok) break;
                 tc_fence_after();
             }
