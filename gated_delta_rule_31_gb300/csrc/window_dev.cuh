@@ -111,6 +111,31 @@ __device__ __forceinline__ void st_row(__nv_bfloat16* to, const uint4& a, const 
 }
 __device__ __forceinline__ bool on32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
 
+// A warp's 32 rows of W channels (32 or 64) from bf16 in shared memory, 128 bytes a row with swizzled 16-byte chunks, to memory,
+// `stride` elements from row to row, a row's by neighbouring lanes; the first `rows` of them, zero from row `live` on.
+// (Stored by the thread that has a row, 16 or 32 bytes a lane, 64 channels of 128 rows took 2200 cycles.)
+template <int W>
+__device__ __forceinline__ void store_rows(__nv_bfloat16* to, size_t stride, uint32_t stage, int rows, int live, int lane) {
+    constexpr int CH = W / 8, AT_ONCE = 32 / CH;  // lanes a row, rows at once
+    const int ch = lane % CH, r0 = lane / CH;
+    uint4 y[CH];
+#pragma unroll
+    for (int i = 0; i < CH; i++) {
+        const int r = r0 + i * AT_ONCE;
+        y[i] = ld_shared_v4(stage + r * 128 + ((ch ^ (r & 7)) << 4));
+        if (r >= live) y[i] = make_uint4(0, 0, 0, 0);
+    }
+    to += r0 * stride + 8 * ch;
+#pragma unroll
+    for (int i = 0; i < CH; i++)
+        if (r0 + i * AT_ONCE < rows) *reinterpret_cast<uint4*>(to + i * AT_ONCE * stride) = y[i];
+}
+// 32 channels e .. of the thread's row into that place.
+__device__ __forceinline__ void stage_row(uint32_t stage, int e, const uint4* y, int lane) {
+#pragma unroll
+    for (int k = 0; k < 4; k++) st_shared_v4(stage + lane * 128 + ((e / 8 + k ^ (lane & 7)) << 4), y[k].x, y[k].y, y[k].z, y[k].w);
+}
+
 // Rows m .. 127 of a 128-token tile in shared memory to zero, by a whole warp: operands of products must be finite there.
 __device__ __forceinline__ void zero_rows(uint32_t tile, int m, int panels, int lane) {
     const int ch = lane & 15;

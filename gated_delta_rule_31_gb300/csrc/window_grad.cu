@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int i = 0; i < 2; i++) {
             used_keep[i] = 0;
             mbar_init(&bar.keep[i], 1);
-            mbar_init(&bar.kept[i], KEYS ? 1 : 4 + 4 * i);  // dq: both halves read dO
+            mbar_init(&bar.kept[i], KEYS ? 1 : 8);  // dq: the rows' warps read dO, and write over Q
             mbar_init(&bar.sfull[i], 1);
             mbar_init(&bar.dpfull[i], 1);
             mbar_init(&bar.dsready[i], KEYS ? 8 : 4);
@@ -442,27 +442,30 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t at_s = lanes + COL_S + 64 * half, at_dp = lanes + COL_DP + 64 * half;
         const float c = s.scale * LOG2E;
         const uint64_t c2 = pair(c, c);
-        const bool wide = on32(KEYS ? half ? a.dk : a.dv : a.dq);
+        const bool wide = on32(half ? a.dk : a.dv);
         int np = 0, units = 0;
         bool ok = true;
         // dq: the rows that are still to be written, a unit later
         int late_t = 0, late_n = 0, late_b = 0, late_h = 0;
+        // Channels of the rows that this half writes, by way of Q's place in shared memory, 4 KB for each warp.
+        constexpr int WIDTH = D > 32 ? D / 2 : D;
         auto write_dq = [&](bool sums, int t, int n, int b, int h) {
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.dq) + (((size_t)b * s.T + t) * s.Hq + h) * D;
-#pragma unroll 1
-            for (int e = 32 * half; e < D; e += 64) {  // every other 32 channels for each half
-                float o[32];
-                if (sums) {
-                    tmem_ld32(lanes + COL_SUM + e, o);
-                    tmem_wait_ld();
-                }
-                if (t >= s.T) continue;
-                uint4 y[4];
+            if (D == 32 && half) return;
+            const uint32_t stage = sb + warp * 4096;
+            if (sums) {
 #pragma unroll
-                for (int k = 0; k < 4; k++) y[k] = t < n ? pack8(o + 8 * k, s.scale) : make_uint4(0, 0, 0, 0);
-                st_row(out + e, y[0], y[1], wide);
-                st_row(out + e + 16, y[2], y[3], wide);
+                for (int e = 0; e < WIDTH; e += 32) {
+                    float o[32];
+                    tmem_ld32(lanes + COL_SUM + WIDTH * half + e, o);
+                    tmem_wait_ld();
+                    const uint4 y[4] = {pack8(o, s.scale), pack8(o + 8, s.scale), pack8(o + 16, s.scale), pack8(o + 24, s.scale)};
+                    stage_row(stage, e, y, lane);
+                }
+                __syncwarp();
             }
+            const int first = t - lane;
+            store_rows<WIDTH>(static_cast<__nv_bfloat16*>(a.dq) + (((size_t)b * s.T + first) * s.Hq + h) * D + WIDTH * half, (size_t)s.Hq * D,
+                              stage, s.T - first, sums ? n - first : 0, lane);
         };
         auto write_late = [&]() {  // of unit number `units`, counted from 1
             ok = wait_for(&bar.sumfull, (units + 1) & 1, &failed, 100);
@@ -491,7 +494,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 const int t = x.t0 + row;
                 const size_t stat = ((size_t)x.b * s.Hq + x.h) * s.T + t;
-                const float l = t < n ? -LOG2E * a.lse[stat] : 0.f;
+                const float lse = t < n ? a.lse[stat] : 0.f;  // used, and waited for, only below
                 // the row of Q (first half) or dO into TMEM: the unit before has done with it, on both sides
                 ok = wait_for(&bar.keep[half], units & 1, &failed, 101);
                 if (bar_sync_or(1, 256, !ok)) {
@@ -514,7 +517,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&bar.aready);
-                    if (half == 0) mbar_arrive(&bar.kept[0]);
                 }
                 // half of the row's sum of do o, o with what its rounding left
                 constexpr int width = D / 16;
@@ -553,10 +555,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int k = 0; k < extra; k++) mbar_arrive(&bar.empty[(o_at + k) % SLOTS]);
                 d = halves[0][row] + halves[1][row];
                 if (half == 0 && t < n) a.delta[stat] = d;
-                b2 = pair(l, l);
-                d2 = pair(-d, -d);
                 if (units > 0) write_late();
                 if (!ok) break;
+                fence_proxy_async_smem();  // the next copy of Q comes over what was written there
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.kept[0]);
+                b2 = pair(-LOG2E * lse, -LOG2E * lse);
+                d2 = pair(-d, -d);
                 late_t = x.t0 + row;
                 late_n = n;
                 late_b = x.b;

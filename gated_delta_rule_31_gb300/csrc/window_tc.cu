@@ -15,7 +15,7 @@
 // Rounding to bf16: P, and the result (what that leaves may be kept for the VJP).
 //
 // Warps 0-3 and 4-7 take the query tiles, 8 copies tiles in (Q of the next unit as soon as the last S of this one has read it,
-// K and V in a ring of five slots), 9 issues the products. The stream of tiles runs through the units without a
+// K and V in a ring of four slots), 9 issues the products. The stream of tiles runs through the units without a
 // break: while the rows of one unit are written, the next unit's S is formed.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -34,8 +34,8 @@ using namespace window;
 
 namespace {
 
-constexpr int THREADS = 384, SLOTS = 5, SMS = 152;
-constexpr uint32_t AT_KV = 2 * TILE, BYTES = AT_KV + SLOTS * TILE;
+constexpr int THREADS = 384, SLOTS = 4, SMS = 152;
+constexpr uint32_t AT_KV = 2 * TILE, AT_OUT = AT_KV + SLOTS * TILE, BYTES = AT_OUT + 8 * 4096;  // 4 KB for each warp that writes rows
 static_assert(BYTES + 1024 <= 232448, "shared memory");
 // Registers a thread: three times 128 threads start with 168.
 constexpr int REGS_ROWS = 216, REGS_REST = 64;
@@ -274,7 +274,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int i = warp >> 2, row = 32 * (warp & 3) + lane;
         const uint32_t lanes = tm + ((uint32_t)(32 * (warp & 3)) << 16), at_s = lanes + COL_S + 128 * i, at_o = lanes + COL_O + 128 * i;
         const float c = s.scale * LOG2E;
-        const bool wide_o = on32(a.o), wide_rest = on32(a.rest);
         int np = 0;  // tiles so far
         bool ok = true;
 #pragma unroll 1
@@ -371,32 +370,42 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             const bool there = t < n;
             const float f = there ? 1.f / l : 0.f;
-            const size_t at = (((size_t)x.b * s.T + t) * s.Hq + head) * D;
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16*>(a.o) + at, *rest = static_cast<__nv_bfloat16*>(a.rest) + at;
+            const int first = t - lane;
+            const size_t at = (((size_t)x.b * s.T + first) * s.Hq + head) * D, stride = (size_t)s.Hq * D;
+            const uint32_t stage = sb + AT_OUT + warp * 4096;
+            constexpr int WIDTH = D > 64 ? 64 : D;  // channels staged at once
 #pragma unroll 1
-            for (int e = 0; e < D; e += 32) {
-                float o[32];
+            for (int e = 0; e < D; e += WIDTH) {
+                uint4 rest[WIDTH / 8];
                 if (count > 0) {
-                    tmem_ld32(at_o + e, o);
-                    tmem_wait_ld();
-                }
-                if (t >= s.T) continue;
-                uint4 y[4];
 #pragma unroll
-                for (int k = 0; k < 4; k++) y[k] = there ? pack8(o + 8 * k, f) : make_uint4(0, 0, 0, 0);
-                st_row(out + e, y[0], y[1], wide_o);
-                st_row(out + e + 16, y[2], y[3], wide_o);
+                    for (int k = 0; k < WIDTH; k += 32) {
+                        float o[32];
+                        tmem_ld32(at_o + e + k, o);
+                        tmem_wait_ld();
+                        uint4 y[4];
+#pragma unroll
+                        for (int c8 = 0; c8 < 4; c8++) {
+                            y[c8] = pack8(o + 8 * c8, f);
+                            float z[8];
+                            unpack8(y[c8], z);
+#pragma unroll
+                            for (int d = 0; d < 8; d++) z[d] = fmaf(f, o[8 * c8 + d], -z[d]);
+                            rest[k / 8 + c8] = pack8(z, 1.f);
+                        }
+                        stage_row(stage, k, y, lane);
+                    }
+                    __syncwarp();
+                }
+                const int live = count > 0 ? n - first : 0;
+                store_rows<WIDTH>(static_cast<__nv_bfloat16*>(a.o) + at + e, stride, stage, s.T - first, live, lane);
+                __syncwarp();
                 if (a.rest) {
 #pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        float z[8];
-                        unpack8(y[k], z);
-#pragma unroll
-                        for (int d = 0; d < 8; d++) z[d] = there ? fmaf(f, o[8 * k + d], -z[d]) : 0.f;
-                        y[k] = pack8(z, 1.f);
-                    }
-                    st_row(rest + e, y[0], y[1], wide_rest);
-                    st_row(rest + e + 16, y[2], y[3], wide_rest);
+                    for (int k = 0; k < WIDTH; k += 32) stage_row(stage, k, rest + k / 8, lane);
+                    __syncwarp();
+                    store_rows<WIDTH>(static_cast<__nv_bfloat16*>(a.rest) + at + e, stride, stage, s.T - first, live, lane);
+                    __syncwarp();
                 }
             }
             if (count > 0) {
