@@ -97,20 +97,6 @@ __device__ __forceinline__ uint32_t seen_by(const WindowShape& s, int t, int j, 
     return j < s.sinks ? from : from & below(j + s.window - t);
 }
 
-// 16 bf16 values of a row to 16-byte aligned memory: as one 32-byte sector where that is aligned to
-// it (`wide`), since a warp's rows are far apart and what its store costs goes by rows, not bytes.
-__device__ __forceinline__ void st_row(__nv_bfloat16* to, const uint4& a, const uint4& b, bool wide) {
-    if (wide) {
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y),
-                     "r"(b.z), "r"(b.w)
-                     : "memory");
-    } else {
-        reinterpret_cast<uint4*>(to)[0] = a;
-        reinterpret_cast<uint4*>(to)[1] = b;
-    }
-}
-__device__ __forceinline__ bool on32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
-
 // A warp's 32 rows of W channels (32 or 64) from bf16 in shared memory, 128 bytes a row with swizzled 16-byte chunks, to memory,
 // `stride` elements from row to row, a row's by neighbouring lanes; the first `rows` of them, zero from row `live` on.
 // (Stored by the thread that has a row, 16 or 32 bytes a lane, 64 channels of 128 rows took 2200 cycles.)

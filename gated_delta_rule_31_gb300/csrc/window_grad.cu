@@ -42,8 +42,11 @@ using namespace window;
 
 namespace {
 
-constexpr int THREADS = 384, SLOTS = 5, SMS = 152;
-constexpr uint32_t AT_RING = 2 * TILE, BYTES = AT_RING + SLOTS * TILE;  // two operands that stay, then the ring
+constexpr int THREADS = 384, SMS = 152;
+// Shared memory: two operands that stay, then the ring: five slots in dq (four: 5% slower), four in dkv, and there 4 KB for each
+// warp that writes rows (dq: where Q was).
+constexpr int slots(bool keys) { return keys ? 4 : 5; }
+constexpr uint32_t AT_RING = 2 * TILE, BYTES = AT_RING + 5 * TILE;
 static_assert(BYTES + 3072 <= 232448, "shared memory");
 constexpr int REGS_ROWS = 208, REGS_REST = 80;  // of 168 at the launch
 static_assert(2 * REGS_ROWS + REGS_REST <= 3 * 168, "registers of the launch");
@@ -157,6 +160,7 @@ struct Stream {
     }
 };
 
+template <int SLOTS>
 struct Bars {
     uint64_t keep[2], kept[2];  // operands that stay for a unit: there; free
     uint64_t full[SLOTS], empty[SLOTS];
@@ -182,9 +186,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                        const __grid_constant__ CUtensorMap mg, const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap mr,
                        GradArgs a) {
     using U = typename std::conditional<KEYS, KeyUnit, QueryUnit>::type;
+    constexpr int SLOTS = slots(KEYS);
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
-    __shared__ Bars bar;
+    __shared__ Bars<SLOTS> bar;
     // dkv: - log2 e lse and - delta of a pair's queries; dq: the halves of delta
     __shared__ __align__(16) float lse_sh[2][C], delta_sh[2][C];
     __shared__ uint32_t tmem_sh;
@@ -442,7 +447,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t at_s = lanes + COL_S + 64 * half, at_dp = lanes + COL_DP + 64 * half;
         const float c = s.scale * LOG2E;
         const uint64_t c2 = pair(c, c);
-        const bool wide = on32(half ? a.dk : a.dv);
         int np = 0, units = 0;
         bool ok = true;
         // dq: the rows that are still to be written, a unit later
@@ -659,28 +663,36 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (!ok) break;
                     tc_fence_after();
                 }
-                const int j = x.j0 + row;
-                const bool there = j < n;
+                const int first = x.j0 + row - lane;
                 const float f = half ? s.scale : 1.f;
-                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(half ? a.dk : a.dv) + (((size_t)x.b * s.T + j) * s.Hk + x.hk) * D;
+                const size_t stride = (size_t)s.Hk * D;
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(half ? a.dk : a.dv) + (((size_t)x.b * s.T + first) * s.Hk + x.hk) * D;
                 float* part = a.parts + (((size_t)x.part * 2 + half) * C + row) * D;
+                const uint32_t stage = sb + AT_RING + SLOTS * TILE + warp * 4096;
+                constexpr int WIDTH = D > 64 ? 64 : D;  // channels staged at once
 #pragma unroll 1
-                for (int e = 0; e < D; e += 32) {
-                    float o[32];
-                    if (count > 0) {
-                        tmem_ld32(lanes + (half ? COL_SUM : COL_V) + e, o);
-                        tmem_wait_ld();
-                    }
-                    if (count == 0 || !there)
+                for (int e = 0; e < D; e += WIDTH) {
 #pragma unroll
-                        for (int k = 0; k < 32; k++) o[k] = 0.f;
-                    if (x.part >= 0) {
+                    for (int k = 0; k < WIDTH; k += 32) {
+                        float o[32];
+                        if (count > 0) {
+                            tmem_ld32(lanes + (half ? COL_SUM : COL_V) + e + k, o);
+                            tmem_wait_ld();
+                        }
+                        if (x.part >= 0) {
+                            const bool there = count > 0 && first + lane < n;
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4) *reinterpret_cast<float4*>(part + e + k) = make_float4(f * o[k], f * o[k + 1], f * o[k + 2], f * o[k + 3]);
-                    } else if (j < s.T) {
-                        st_row(out + e, pack8(o, f), pack8(o + 8, f), wide);
-                        st_row(out + e + 16, pack8(o + 16, f), pack8(o + 24, f), wide);
+                            for (int d = 0; d < 32; d += 4)
+                                *reinterpret_cast<float4*>(part + e + k + d) =
+                                    there ? make_float4(f * o[d], f * o[d + 1], f * o[d + 2], f * o[d + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        } else {
+                            const uint4 y[4] = {pack8(o, f), pack8(o + 8, f), pack8(o + 16, f), pack8(o + 24, f)};
+                            stage_row(stage, k, y, lane);
+                        }
                     }
+                    __syncwarp();
+                    if (x.part < 0) store_rows<WIDTH>(out + e, stride, stage, s.T - first, count > 0 ? n - first : 0, lane);
+                    __syncwarp();
                 }
                 if (count > 0) {
                     tc_fence_before();
@@ -738,11 +750,14 @@ struct Cut {
         const long long reach = (C - 1 + (long long)s.window + C - 1) / C + 1, near_ = reach < tiles ? reach : tiles;
         const long long rest = tiles - cut, tail = rest < near_ ? rest : near_;  // of the others the last ones are seen by fewer
         const long long pairs = (long long)cut * tiles - (long long)cut * (cut - 1) / 2 + tail * (tail + 1) / 2 + (rest - tail) * near_;
-        // no piece longer than a third of a CTA's share, or shorter than 8 pairs, below which writing and adding its sums costs more
+        // no piece longer than a third of a CTA's share, or shorter than 8 pairs, below which writing and adding its sums costs more;
+        // and those of the first tiles no longer than another tile is: CTAs take the same number of units (with pieces of 171 pairs
+        // and tiles of 36 the training step of 32768 tokens took 180 us longer)
         long long most = heads * group * pairs / (3 * SMS);
         if (most < 8) most = 8;
-        pieces_cut = (int)((group * tiles + most - 1) / most);
         pieces = (int)((group * near_ + most - 1) / most);
+        if (most > group * near_) most = group * near_ > 8 ? group * near_ : 8;
+        pieces_cut = (int)((group * tiles + most - 1) / most);
         if (cut == 0) pieces_cut = 1;
         parts = (pieces_cut > 1 ? heads * cut * pieces_cut : 0) + (pieces > 1 ? heads * (tiles - cut) * pieces : 0);
     }
