@@ -75,6 +75,7 @@ struct TurnArgs {
     int B, T, D, bf16;
     int pairs, axes, sections[4], interleaved, inverse;
     const float* inv_freq;  // [pairs]
+    int freq16;             // set by launch_turn: inv_freq is 16-byte aligned
     const int* positions;   // [B, T, axes], or null: lengths[b] + t
     const int* counts;      // [B] tokens of each entry, or null (T)
     const int* lengths;     // [B] tokens in the cache before, or null

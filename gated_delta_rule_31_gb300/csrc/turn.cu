@@ -23,7 +23,7 @@ namespace gdr {
 
 namespace {
 
-constexpr int HEADS = 4, THREADS = 128;
+constexpr int THREADS = 128;
 
 template <int BYTES>
 struct Raw;
@@ -57,7 +57,11 @@ __device__ __forceinline__ uint64_t turns_of(float f) {
     return u >> 31 ? 0ull - t : t;
 }
 
-template <typename T, int VEC>
+// Sine and cosine of x half turns, |x| <= 1: for fp32 to its precision, for bf16 by the hardware's functions, 2^-21 off.
+__device__ __forceinline__ void sincos_of(float x, float* s, float* c, float) { sincospif(x, s, c); }
+__device__ __forceinline__ void sincos_of(float x, float* s, float* c, __nv_bfloat16) { __sincosf(3.14159265358979f * x, s, c); }
+
+template <typename T, int VEC, int HEADS>
 __global__ void __launch_bounds__(THREADS) turn_kernel(TurnArgs a) {
     const int units = a.D / (2 * VEC);
     const unsigned index = blockIdx.x * THREADS + threadIdx.x;
@@ -93,22 +97,32 @@ __global__ void __launch_bounds__(THREADS) turn_kernel(TurnArgs a) {
             y[h].raw = *reinterpret_cast<const decltype(y[h].raw)*>(src + h * a.D + c1);
         }
     float co[VEC], si[VEC];
-    if (turn)
+    if (turn) {
+        long long at[4];  // the token's position on each axis
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            if (k < a.axes) at[k] = a.positions ? a.positions[token * a.axes + k] : (long long)a.lengths[b] + t;
+        const int end0 = a.sections[0], end1 = end0 + a.sections[1], end2 = end1 + a.sections[2];
+        float f[VEC];
+        if (VEC >= 4 && a.freq16) {
+#pragma unroll
+            for (int e = 0; e < VEC / 4; e++) {
+                const float4 x4 = reinterpret_cast<const float4*>(a.inv_freq + unit * VEC)[e];
+                f[4 * e] = x4.x; f[(4 * e + 1) % VEC] = x4.y; f[(4 * e + 2) % VEC] = x4.z; f[(4 * e + 3) % VEC] = x4.w;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; e++) f[e] = a.inv_freq[unit * VEC + e];
+        }
 #pragma unroll
         for (int e = 0; e < VEC; e++) {
             const int i = unit * VEC + e;
-            int axis = 0, first = 0;
-#pragma unroll
-            for (int k = 0; k < 3; k++)
-                if (axis == k && k + 1 < a.axes && i >= first + a.sections[k]) {
-                    first += a.sections[k];
-                    axis = k + 1;
-                }
-            const long long p = a.positions ? a.positions[token * a.axes + axis] : (long long)a.lengths[b] + t;
-            uint64_t turns = turns_of(a.inv_freq[i]) * (uint64_t)p;
+            const long long p = i < end0 || a.axes == 1 ? at[0] : i < end1 || a.axes == 2 ? at[1] : i < end2 || a.axes == 3 ? at[2] : at[3];
+            uint64_t turns = turns_of(f[e]) * (uint64_t)p;
             if (a.inverse) turns = 0ull - turns;
-            sincospif((float)(int)((turns + 0x80000000ull) >> 32) * 0x1p-31f, &si[e], &co[e]);
+            sincos_of((float)(int)((turns + 0x80000000ull) >> 32) * 0x1p-31f, &si[e], &co[e], T());
         }
+    }
 #pragma unroll
     for (int h = 0; h < HEADS; h++) {
         if (h >= nh) break;
@@ -151,15 +165,24 @@ __global__ void __launch_bounds__(THREADS) turn_kernel(TurnArgs a) {
     }
 }
 
-template <typename T, int VEC>
-cudaError_t turn(const TurnArgs& a, cudaStream_t st) {
+template <typename T, int VEC, int HEADS>
+cudaError_t turn_heads(TurnArgs a, cudaStream_t st) {
     const long long threads = (long long)a.B * a.T * (a.D / (2 * VEC));
     unsigned chunks = 0;
     for (int i = 0; i < a.parts; i++) chunks += (a.part[i].H + HEADS - 1) / HEADS;
+    a.freq16 = (reinterpret_cast<uintptr_t>(a.inv_freq) & 15) == 0;
     trace_begin("turn", st);
-    turn_kernel<T, VEC><<<dim3((unsigned)((threads + THREADS - 1) / THREADS), chunks), THREADS, 0, st>>>(a);
+    turn_kernel<T, VEC, HEADS><<<dim3((unsigned)((threads + THREADS - 1) / THREADS), chunks), THREADS, 0, st>>>(a);
     trace_end(st);
     return cudaGetLastError();
+}
+
+// Eight heads a thread where that leaves two waves of threads (1024 an SM at 64 registers), else four.
+template <typename T, int VEC>
+cudaError_t turn(const TurnArgs& a, cudaStream_t st) {
+    long long rows = 0;
+    for (int i = 0; i < a.parts; i++) rows += (a.part[i].H + 7) / 8;
+    return rows * a.B * a.T * (a.D / (2 * VEC)) >= 2LL * 152 * 1024 ? turn_heads<T, VEC, 8>(a, st) : turn_heads<T, VEC, 4>(a, st);
 }
 
 // The widest vectors that the channels and every pointer are aligned to.
