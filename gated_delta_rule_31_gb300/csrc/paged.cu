@@ -33,6 +33,8 @@ namespace {
 constexpr int THREADS = 128, HEADS = 8;  // heads that share a walk
 constexpr int RUNS = 2 * 152;            // CTAs
 constexpr float LOG2E = 1.4426950408889634f;
+
+
 constexpr int kTile32 = 64;  // tokens of a tile of fp32
 
 __device__ __forceinline__ float4 get4(const float* p) { return *reinterpret_cast<const float4*>(p); }
@@ -104,6 +106,7 @@ __global__ void __launch_bounds__(THREADS) paged_f32_kernel(PagedArgs a, int blo
     constexpr int LD = D + 4;
     float *K = sh, *V = K + kTile32 * LD, *Q = V + kTile32 * LD, *P = Q + HEADS * LD;
     __shared__ float m_sh[HEADS], l_sh[HEADS], fade_sh[HEADS];
+    linear::wait_kernel_before();  // ahead of every read; the join, which may start then, has the same guarantee
     linear::next_kernel_may_start();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = a.Hq / a.Hk, walks = a.Hk * blocks;
     Place at;
@@ -220,12 +223,15 @@ __global__ void __launch_bounds__(THREADS) paged_f32_kernel(PagedArgs a, int blo
 
 // ---- bf16
 
-constexpr int STAGES = 3, WARPS = THREADS / 32;
+constexpr int STAGES = 3;
 constexpr uint32_t STEP_BYTES = 8192;  // K and V of a warp's step
 template <int D>
 constexpr int step_tokens() { return (int)STEP_BYTES / (4 * D); }
-template <int D>
-constexpr int merge_bytes() { return WARPS * HEADS * (D + 2) * 4; }
+// A part for each warp; with clusters, whose CTAs have one walk each, they and the CTA's go over the copied tiles.
+template <int D, int CLUSTER, int WARPS>
+constexpr int merge_bytes() { return (WARPS + (CLUSTER ? 1 : 0)) * HEADS * (D + 2) * 4; }
+template <int D, int CLUSTER, int WARPS>
+constexpr int smem_bytes() { return WARPS * STAGES * (int)STEP_BYTES + (CLUSTER ? 0 : merge_bytes<D, CLUSTER, WARPS>()); }
 
 template <int N>
 __device__ __forceinline__ void cp_async_wait_but() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -250,6 +256,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float x;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+    return x;
 }
 
 // A walk's tiles in a run, as one goes over them.
@@ -279,20 +291,42 @@ struct Cursor {
     __device__ __forceinline__ int token(int x) const { return x < first ? x : lo + (x - first); }
 };
 
-template <int D>
-__global__ void __launch_bounds__(THREADS, 2) paged_bf16_kernel(PagedArgs a, int blocks) {
-    constexpr int STEP = step_tokens<D>(), TILE = WARPS * STEP, CHUNKS = D / 8, M = STEP / 16;
+// CLUSTER: the walks' tiles are not dealt out in a row: each walk has a cluster of that many CTAs, which join through each other's
+// shared memory.
+template <int D, int CLUSTER, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) paged_bf16_kernel(PagedArgs a, int blocks) {
+    constexpr int THREADS = WARPS * 32, STEP = step_tokens<D>(), TILE = WARPS * STEP, CHUNKS = D / 8, M = STEP / 16;
+    static_assert(merge_bytes<D, CLUSTER, WARPS>() <= WARPS * STAGES * STEP_BYTES, "parts over the tiles");
     extern __shared__ __align__(128) uint8_t sm[];
     __shared__ uint32_t there[WARPS][STAGES][2];  // which tokens of a step are there, as bits
+    linear::wait_kernel_before();  // ahead of every read; the join, which may start then, has the same guarantee
     linear::next_kernel_may_start();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = a.Hq / a.Hk, walks = a.Hk * blocks;
     const uint32_t ring = smem_u32(sm) + warp * STAGES * STEP_BYTES;
-    float* merge = reinterpret_cast<float*>(sm + WARPS * STAGES * STEP_BYTES);
+    float* merge = reinterpret_cast<float*>(sm + (CLUSTER ? 0 : WARPS * STAGES * STEP_BYTES));
     Cursor in, out;
     long long end;
-    find<THREADS>(a, TILE, walks, blockIdx.x, gridDim.x, in.at, in.tile, end);
-    const bool some = in.tile < end;
-    if (some) in.open(a, TILE, walks, end);
+    bool some;
+    if constexpr (CLUSTER > 0) {
+        const int rank = blockIdx.x % CLUSTER, all = blockIdx.x / CLUSTER;
+        in.at = Place{all / walks, 0};
+        in.walk = all - in.at.b * walks;
+        const Seen seen(a, in.at.b);
+        in.first = seen.first;
+        in.lo = seen.lo;
+        in.count = seen.count;
+        in.tiles = seen.tiles(TILE);
+        in.t = (int)((long long)in.tiles * rank / CLUSTER);
+        in.t1 = (int)((long long)in.tiles * (rank + 1) / CLUSTER);
+        in.whole = false;
+        in.tile = in.t;
+        end = in.t1;
+        some = in.tile < end;
+    } else {
+        find<THREADS>(a, TILE, walks, blockIdx.x, gridDim.x, in.at, in.tile, end);
+        some = in.tile < end;
+        if (some) in.open(a, TILE, walks, end);
+    }
     out = in;
 
     // Rows of the cache that hold the warp's tokens of the cursor's tile: a lane's token, and its token 32 on.
@@ -349,7 +383,7 @@ __global__ void __launch_bounds__(THREADS, 2) paged_bf16_kernel(PagedArgs a, int
     // rows (tokens 0-7 twice, then 8-15)
     const int krow = lane & 15, kch = lane >> 4, vrow = (lane & 7) + (lane >> 4) * 8, vch = lane >> 3 & 1;
     auto swizzled = [](int r, int ch) { return (uint32_t)(r * (2 * D) + ((ch ^ (D == 32 ? (r >> 1) & 3 : r & 7)) << 4)); };
-    while (out.tile < end) {
+    while (CLUSTER ? segment == 0 : out.tile < end) {
         const int hk = out.walk / blocks, g0 = out.walk % blocks * HEADS, ng = min(HEADS, group - g0);
         const size_t q0 = (size_t)out.at.b * a.Hq + hk * group + g0;
         uint32_t q[D / 8];  // column lane / 4 of q^T: channels 16 k + 2 (lane % 4), + 1, and 8 on
@@ -369,14 +403,17 @@ __global__ void __launch_bounds__(THREADS, 2) paged_bf16_kernel(PagedArgs a, int
             float s[M][4];
 #pragma unroll
             for (int i = 0; i < M; i++) {
+                float odd[4] = {0.f, 0.f, 0.f, 0.f};  // two sums, so that products wait for one another half as long
 #pragma unroll
                 for (int e = 0; e < 4; e++) s[i][e] = 0.f;
 #pragma unroll
                 for (int k = 0; k < D / 16; k++) {
                     uint32_t x[4];
                     ldmatrix_x4(kt + swizzled(16 * i + krow, 2 * k + kch), x);
-                    mma(s[i], x, q[2 * k], q[2 * k + 1]);
+                    mma(k & 1 ? odd : s[i], x, q[2 * k], q[2 * k + 1]);
                 }
+#pragma unroll
+                for (int e = 0; e < 4; e++) s[i][e] += odd[e];
             }
             float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -426,7 +463,7 @@ __global__ void __launch_bounds__(THREADS, 2) paged_bf16_kernel(PagedArgs a, int
         for (int h = 0; h < 2; h++)
 #pragma unroll
             for (int x = 4; x < 32; x *= 2) l[h] += __shfl_xor_sync(0xffffffffu, l[h], x);
-        __syncthreads();  // the walk before has been read
+        __syncthreads();  // the walk before, or with clusters the tiles, have been read
         float* mine = merge + warp * HEADS * (D + 2);
 #pragma unroll
         for (int h = 0; h < 2; h++) {
@@ -442,7 +479,8 @@ __global__ void __launch_bounds__(THREADS, 2) paged_bf16_kernel(PagedArgs a, int
             }
         }
         __syncthreads();
-        float* part = a.parts + (size_t)(2 * blockIdx.x + (segment > 0)) * HEADS * (D + 2);
+        // of a cluster's CTA, or of a run that has a part of the walk: left to be joined
+        float* part = CLUSTER ? merge + WARPS * HEADS * (D + 2) : a.parts + (size_t)(2 * blockIdx.x + (segment > 0)) * HEADS * (D + 2);
         for (int i = tid; i < ng * D; i += THREADS) {
             const int g = i / D, d = i % D;
             const float* from = merge + g * (D + 2);
@@ -467,6 +505,33 @@ __global__ void __launch_bounds__(THREADS, 2) paged_bf16_kernel(PagedArgs a, int
             }
         }
         segment++;
+        if constexpr (CLUSTER > 0) {
+            cluster_sync();
+            // a CTA joins every CLUSTER-th channel, the CTAs' parts in order
+            const uint32_t mine = smem_u32(part);
+            for (int i = tid * CLUSTER + blockIdx.x % CLUSTER; i < ng * D; i += THREADS * CLUSTER) {
+                const int g = i / D, d = i % D;
+                float mr[CLUSTER], lr[CLUSTER], xr[CLUSTER], top = -INFINITY, x = 0.f, sum = 0.f;
+#pragma unroll
+                for (int r = 0; r < CLUSTER; r++) {
+                    const uint32_t at = mapa_shared(mine, r) + g * (D + 2) * 4;
+                    mr[r] = ld_cluster(at + D * 4);
+                    lr[r] = ld_cluster(at + D * 4 + 4);
+                    xr[r] = ld_cluster(at + d * 4);
+                    top = fmaxf(top, mr[r]);
+                }
+                const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+                for (int r = 0; r < CLUSTER; r++) {
+                    const float f = exp2_fast(mr[r] - base);
+                    x = fmaf(f, xr[r], x);
+                    sum = fmaf(f, lr[r], sum);
+                }
+                put(static_cast<__nv_bfloat16*>(a.o) + (q0 + g) * D + d, sum > 0.f ? x / sum : 0.f);
+            }
+            cluster_sync();  // the others have read this CTA's
+            return;
+        }
         if (out.tile < end) out.open(a, TILE, walks, end);
     }
     // entries that see no token: zero
@@ -547,7 +612,7 @@ cudaError_t step(void (*kernel)(PagedArgs, int), int smem, int tile, const Paged
     const int blocks = (a.Hq / a.Hk + HEADS - 1) / HEADS;
     if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
     trace_begin("paged_step", st);
-    cudaError_t e = launch_after(kernel, dim3(RUNS), THREADS, smem, st, false, a, blocks);
+    cudaError_t e = launch_after(kernel, dim3(RUNS), THREADS, smem, st, true, a, blocks);
     trace_end(st);
     if (e != cudaSuccess) return e;
     trace_begin("paged_join", st);
@@ -555,10 +620,47 @@ cudaError_t step(void (*kernel)(PagedArgs, int), int smem, int tile, const Paged
     trace_end(st);
     return e;
 }
+template <int D, int CLUSTER>
+cudaError_t clusters(const PagedArgs& a, cudaStream_t st) {
+    constexpr int WARPS = 8, smem = smem_bytes<D, CLUSTER, WARPS>();
+    const auto kernel = paged_bf16_kernel<D, CLUSTER, WARPS>;
+    const int blocks = (a.Hq / a.Hk + HEADS - 1) / HEADS;
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.B * a.Hk * blocks * CLUSTER);
+    cfg.blockDim = dim3(WARPS * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = CLUSTER;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    trace_begin("paged_step", st);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, blocks);
+    trace_end(st);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+constexpr long long CLUSTER_MOST = 4096 * 128;  // tokens x channels of a CTA
+// The CTAs of a cluster for each walk, where walks are few and sequences not long (one launch, and no lengths to sum up
+// first): the most of 8, 4, 2 that the SMs have room for; 0: runs.
+int cluster_of(const PagedArgs& a) {
+    const long long walks = (long long)a.B * a.Hk * ((a.Hq / a.Hk + HEADS - 1) / HEADS);
+    int n = 8;
+    while (n > 1 && walks * n > 152) n /= 2;
+    return a.bf16 && n > 1 && (long long)a.table_pages * a.page_size * a.D <= (long long)n * CLUSTER_MOST ? n : 0;
+}
+
 template <int D>
 cudaError_t step_of(const PagedArgs& a, cudaStream_t st) {
+    const int n = cluster_of(a);
+    if (n) return n == 8 ? clusters<D, 8>(a, st) : n == 4 ? clusters<D, 4>(a, st) : clusters<D, 2>(a, st);
     if (a.bf16)
-        return step<D, __nv_bfloat16>(paged_bf16_kernel<D>, WARPS * STAGES * STEP_BYTES + merge_bytes<D>(), WARPS * step_tokens<D>(), a, st);
+        return step<D, __nv_bfloat16>(paged_bf16_kernel<D, 0, 4>, smem_bytes<D, 0, 4>(), 4 * step_tokens<D>(), a, st);
     return step<D, float>(paged_f32_kernel<D>, (2 * kTile32 * (D + 4) + HEADS * (D + 4) + HEADS * kTile32) * 4, kTile32, a, st);
 }
 

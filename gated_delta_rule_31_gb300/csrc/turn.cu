@@ -18,6 +18,8 @@
 #include "attention.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "linear.h"
+#include "linear_dev.cuh"
 
 namespace gdr {
 
@@ -63,6 +65,8 @@ __device__ __forceinline__ void sincos_of(float x, float* s, float* c, __nv_bflo
 
 template <typename T, int VEC, int HEADS>
 __global__ void __launch_bounds__(THREADS) turn_kernel(TurnArgs a) {
+    linear::wait_kernel_before();  // ahead of every read and write: a call may start while the kernel before it ends
+    linear::next_kernel_may_start();
     const int units = a.D / (2 * VEC);
     const unsigned index = blockIdx.x * THREADS + threadIdx.x;
     const size_t token = index / (unsigned)units;
@@ -172,9 +176,9 @@ cudaError_t turn_heads(TurnArgs a, cudaStream_t st) {
     for (int i = 0; i < a.parts; i++) chunks += (a.part[i].H + HEADS - 1) / HEADS;
     a.freq16 = (reinterpret_cast<uintptr_t>(a.inv_freq) & 15) == 0;
     trace_begin("turn", st);
-    turn_kernel<T, VEC, HEADS><<<dim3((unsigned)((threads + THREADS - 1) / THREADS), chunks), THREADS, 0, st>>>(a);
+    const cudaError_t e = launch_after(turn_kernel<T, VEC, HEADS>, dim3((unsigned)((threads + THREADS - 1) / THREADS), chunks), THREADS, 0, st, true, a);
     trace_end(st);
-    return cudaGetLastError();
+    return e;
 }
 
 // Eight heads a thread where that leaves two waves of threads (1024 an SM at 64 registers), else four.
