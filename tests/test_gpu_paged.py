@@ -77,6 +77,35 @@ def test_enough_sequences_for_every_run(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 1), (63, 4), (200, 0), (130, 130)])
+@pytest.mark.parametrize("D,Hq,Hk", [(32, 6, 2), (64, 16, 8), (128, 8, 4), (128, 18, 1)])
+def test_more_walks_than_clusters_are_made_for(D, Hq, Hk, window, sinks, dtype):
+    """Tiles of all sequences dealt out in runs: walks whole, cut once and cut into many parts, empty ones between them."""
+    n = [(97 * i * i) % 400 for i in range(60)]
+    n[7], n[8], n[59] = 1900, 0, 700
+    x = make(60, n, Hq, Hk, D, 16, TYPES[dtype], seed=D + window)
+    x[3][11, :2] = -1  # pages given back
+    x[3][12] = 10 ** 6
+    check(x, dtype, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,Hq,Hk", [(1, 4, 1), (1, 8, 8), (3, 12, 12), (2, 72, 2)])
+def test_long_sequences(B, Hq, Hk, dtype):
+    check(make(B, [20000 + 777 * b for b in range(B)], Hq, Hk, 128, 64, TYPES[dtype], seed=B), dtype)
+
+
+def test_a_table_with_more_room_than_tokens():
+    """Short sequences in a table for long ones, over the sizes where clusters give way to runs."""
+    for room in (100, 30000, 40000, 300000):
+        q, kc, vc, table, n = make(2, [333, 65], 8, 2, 64, 16, torch.bfloat16, seed=room % 7)
+        wide = torch.full((2, -(-room // 16)), 2 ** 31 - 1, dtype=torch.int32)
+        wide[:, :table.shape[1]] = table[:, :wide.shape[1]]
+        n = n.clamp(max=wide.shape[1] * 16)
+        check((q, kc, vc, wide, n), "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_pages_that_are_none(dtype):
     """Tokens on pages outside the cache are not seen: freed pages before the window, and others."""
     x = list(make(3, [200, 150, 90], 4, 2, 64, 16, TYPES[dtype], seed=4))
@@ -143,6 +172,34 @@ def test_repeats_bitwise_on_another_stream_and_in_a_graph(dtype):
     x[4].add_(-1)  # the lengths are read on the device
     graph.replay()
     assert torch.equal(third, gdr.paged_decode_step(*x)) and not torch.equal(first, third)
+
+
+@pytest.mark.parametrize("B", [1, 40])
+def test_two_calls_at_once(B):
+    """On two streams, each with its own workspace; and two graphs replayed at once."""
+    dev = cuda_device()
+    xs = [[t.to(dev) for t in make(B, [600 + 5 * b for b in range(B)], 8, 4, 128, 16, torch.bfloat16, seed=s)] for s in (1, 2)]
+    want = [gdr.paged_decode_step(*x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    graphs, got = [torch.cuda.CUDAGraph() for _ in xs], [None, None]
+    for i, x in enumerate(xs):
+        with torch.cuda.graph(graphs[i]):
+            for _ in range(5):
+                got[i] = gdr.paged_decode_step(*x)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                graphs[i].replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    outs = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(gdr.paged_decode_step(*xs[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, want[i]) for i in range(2) for a in outs[i])
 
 
 def test_offsets_past_32_bits():
