@@ -7,14 +7,14 @@
 // time; a walk whose tiles lie in one run is written at once, of one that is cut each run leaves (m, l, O), and a second
 // kernel joins them, runs in order: o = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i.
 //
-// bf16: each of the four warps takes every fourth 8 KB of K and of V (16 tokens at D = 128) on its own, copied three steps
-// ahead into its own part of shared memory, across walks too, so no warp waits for another before a walk ends. A row's
-// place comes from the page table a step before that. Products by mma.m16n8k16 with the 8 heads as columns, S^T = K q^T and
-// O^T += V^T P^T: the tokens are rows, so no row is spent on heads that are not there, and a thread keeps the same two heads
-// in S, m, l and O. m moves when a score has grown past it by 8 (a weight is at most 2^8 then, exact to bf16 as any), which
-// one vote tells; otherwise lanes exchange nothing. HBM bounds it: 4 operations a byte and head, a few percent of the
-// products' rate. (tcgen05 would take 128 rows for the 8.)
-// fp32: a CTA for each run as well, products on the CUDA cores.
+// Each warp takes 8 KB of K and V at a time (16 tokens of 128 channels in bf16, 8 in fp32) on its own, copied three steps ahead
+// into its own part of shared memory, across walks too, so no warp waits for another before a walk ends. A row's place
+// comes from the page table a step before that. m moves when a score has grown past it by 8 (a weight is at most 2^8 then,
+// exact to bf16 as any), which one vote tells; otherwise lanes exchange little. HBM bounds it: 4 operations a byte and head.
+// bf16: products by mma.m16n8k16 with the 8 heads as columns, S^T = K q^T and O^T += V^T P^T: the tokens are rows, so no row is
+// spent on heads that are not there, and a thread keeps the same two heads in S, m, l and O. (tcgen05 would take 128 rows
+// for the 8.) fp32: products on the CUDA cores, for S 32 channels of one token a lane, for O 4 channels of 8 tokens a lane.
+//
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -30,14 +30,13 @@ namespace gdr {
 
 namespace {
 
-constexpr int THREADS = 128, HEADS = 8;  // heads that share a walk
-constexpr int RUNS = 2 * 152;            // CTAs
+constexpr int HEADS = 8;       // that share a walk
+constexpr int RUNS = 2 * 152;  // CTAs, of RUN_WARPS warps
+constexpr int RUN_WARPS = 4, CLUSTER_WARPS = 8;
 constexpr float LOG2E = 1.4426950408889634f;
 
 
-constexpr int kTile32 = 64;  // tokens of a tile of fp32
 
-__device__ __forceinline__ float4 get4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
@@ -51,7 +50,6 @@ struct Seen {
         first = min(a.sinks, lo);
         count = first + n - lo;
     }
-    __device__ int at(int i) const { return i < first ? i : lo + (i - first); }
     __device__ int tiles(int tile) const { return (count + tile - 1) / tile; }
 };
 
@@ -98,140 +96,21 @@ __device__ long long find(const PagedArgs& a, int tile, int walks, int run, int 
     return total;
 }
 
-// ---- fp32
-
-template <int D>
-__global__ void __launch_bounds__(THREADS) paged_f32_kernel(PagedArgs a, int blocks) {
-    extern __shared__ __align__(16) float sh[];
-    constexpr int LD = D + 4;
-    float *K = sh, *V = K + kTile32 * LD, *Q = V + kTile32 * LD, *P = Q + HEADS * LD;
-    __shared__ float m_sh[HEADS], l_sh[HEADS], fade_sh[HEADS];
-    linear::wait_kernel_before();  // ahead of every read; the join, which may start then, has the same guarantee
-    linear::next_kernel_may_start();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = a.Hq / a.Hk, walks = a.Hk * blocks;
-    Place at;
-    long long begin, end;
-    find<THREADS>(a, kTile32, walks, blockIdx.x, gridDim.x, at, begin, end);
-    long long tile = begin;
-    int segment = 0;
-    while (tile < end) {
-        const Seen seen(a, at.b);
-        const int tiles = seen.tiles(kTile32);
-        if (tile >= (at.before + tiles) * walks) {
-            at.before += tiles;
-            at.b++;
-            continue;
-        }
-        const int walk = (int)((tile - at.before * walks) / tiles), t0 = (int)(tile - at.before * walks - (long long)walk * tiles);
-        const int t1 = (int)min((long long)tiles, t0 + end - tile);
-        const int hk = walk / blocks, g0 = walk % blocks * HEADS, ng = min(HEADS, group - g0);
-        const size_t q0 = (size_t)at.b * a.Hq + hk * group + g0;
-        __syncthreads();
-        for (int i = tid; i < HEADS * D; i += THREADS)
-            Q[i / D * LD + i % D] = i / D < ng ? LOG2E * a.scale * static_cast<const float*>(a.q)[q0 * D + i] : 0.f;
-        if (tid < HEADS) {
-            m_sh[tid] = -INFINITY;
-            l_sh[tid] = 0.f;
-        }
-        float acc[HEADS * D / THREADS];  // heads tid / D + (THREADS / D) i, channel tid % D
-#pragma unroll
-        for (int i = 0; i < HEADS * D / THREADS; i++) acc[i] = 0.f;
-        for (int t = t0; t < t1; t++) {
-            __syncthreads();
-            for (int i = tid; i < kTile32 * D / 4; i += THREADS) {
-                const int r = i / (D / 4), c = i % (D / 4) * 4, x = t * kTile32 + r;
-                float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
-                bool on = x < seen.count;
-                if (on) {
-                    const int j = seen.at(x), page = a.table[(size_t)at.b * a.table_pages + j / a.page_size];
-                    on = (unsigned)page < (unsigned)a.pages;
-                    if (on) {
-                        const size_t row = (((size_t)page * a.page_size + j % a.page_size) * a.Hk + hk) * D + c;
-                        k = get4(static_cast<const float*>(a.k) + row);
-                        v = get4(static_cast<const float*>(a.v) + row);
-                    }
-                }
-                *reinterpret_cast<float4*>(K + r * LD + c) = k;
-                *reinterpret_cast<float4*>(V + r * LD + c) = v;
-                if (c == 0) K[r * LD + D] = on ? 0.f : -INFINITY;  // whether the token is there
-            }
-            __syncthreads();
-            for (int g = warp; g < ng; g += THREADS / 32) {  // a warp per head, two tokens a lane
-                float s[kTile32 / 32];
-                float top = m_sh[g], sum = 0.f;
-#pragma unroll
-                for (int i = 0; i < kTile32 / 32; i++) {
-                    const float* k = K + (lane + 32 * i) * LD;
-                    float x = 0.f;
-#pragma unroll 8
-                    for (int d = 0; d < D; d += 4) {
-                        const float4 u = get4(k + d), w = get4(Q + g * LD + d);
-                        x += u.x * w.x + u.y * w.y + u.z * w.z + u.w * w.w;
-                    }
-                    s[i] = k[D] == 0.f ? x : -INFINITY;
-                    top = fmaxf(top, s[i]);
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll
-                for (int i = 0; i < kTile32 / 32; i++) {
-                    const float p = exp2f(s[i] - base);
-                    P[g * kTile32 + lane + 32 * i] = p;
-                    sum += p;
-                }
-                sum = warp_sum(sum);
-                if (lane == 0) {
-                    fade_sh[g] = exp2f(m_sh[g] - base);
-                    l_sh[g] = fade_sh[g] * l_sh[g] + sum;
-                    m_sh[g] = top;
-                }
-            }
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < HEADS * D / THREADS; i++) {
-                const int g = tid / D + THREADS / D * i;
-                if (g >= ng) continue;
-                float x = fade_sh[g] * acc[i];
-#pragma unroll 8
-                for (int j = 0; j < kTile32; j++) x = fmaf(P[g * kTile32 + j], V[j * LD + tid % D], x);
-                acc[i] = x;
-            }
-        }
-        __syncthreads();
-        const bool whole = t0 == 0 && t1 == tiles;
-        float* part = a.parts + (size_t)(2 * blockIdx.x + (segment > 0)) * HEADS * (D + 2);
-#pragma unroll
-        for (int i = 0; i < HEADS * D / THREADS; i++) {
-            const int g = tid / D + THREADS / D * i;
-            if (g >= ng) continue;
-            if (whole) static_cast<float*>(a.o)[(q0 + g) * D + tid % D] = l_sh[g] > 0.f ? acc[i] / l_sh[g] : 0.f;
-            else part[g * (D + 2) + tid % D] = acc[i];
-        }
-        if (!whole && tid < ng) {
-            part[tid * (D + 2) + D] = m_sh[tid];
-            part[tid * (D + 2) + D + 1] = l_sh[tid];
-        }
-        tile += t1 - t0;
-        segment++;
-    }
-    // entries without a token: zero
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x)
-        if (Seen(a, b).count == 0)
-            for (int i = tid; i < a.Hq * D; i += THREADS) static_cast<float*>(a.o)[(size_t)b * a.Hq * D + i] = 0.f;
-}
-
-// ---- bf16
-
 constexpr int STAGES = 3;
 constexpr uint32_t STEP_BYTES = 8192;  // K and V of a warp's step
-template <int D>
-constexpr int step_tokens() { return (int)STEP_BYTES / (4 * D); }
+template <typename T, int D>
+constexpr int step_tokens() { return (int)STEP_BYTES / (2 * D * (int)sizeof(T)); }
 // A part for each warp; with clusters, whose CTAs have one walk each, they and the CTA's go over the copied tiles.
 template <int D, int CLUSTER, int WARPS>
 constexpr int merge_bytes() { return (WARPS + (CLUSTER ? 1 : 0)) * HEADS * (D + 2) * 4; }
-template <int D, int CLUSTER, int WARPS>
-constexpr int smem_bytes() { return WARPS * STAGES * (int)STEP_BYTES + (CLUSTER ? 0 : merge_bytes<D, CLUSTER, WARPS>()); }
+// fp32: the heads' q, and weights of a step's tokens for each warp; between the walks of a run the parts go over them.
+template <typename T, int D, int WARPS>
+constexpr int rows_bytes() { return sizeof(T) == 4 ? HEADS * D * 4 + WARPS * step_tokens<T, D>() * HEADS * 4 : 0; }
+template <typename T, int D, int CLUSTER, int WARPS>
+constexpr int smem_bytes() {
+    constexpr int parts = CLUSTER ? 0 : merge_bytes<D, CLUSTER, WARPS>(), rows = rows_bytes<T, D, WARPS>();
+    return WARPS * STAGES * (int)STEP_BYTES + (parts > rows ? parts : rows);
+}
 
 template <int N>
 __device__ __forceinline__ void cp_async_wait_but() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -258,6 +137,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
 __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     float x;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
@@ -293,9 +177,15 @@ struct Cursor {
 
 // CLUSTER: the walks' tiles are not dealt out in a row: each walk has a cluster of that many CTAs, which join through each other's
 // shared memory.
-template <int D, int CLUSTER, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) paged_bf16_kernel(PagedArgs a, int blocks) {
-    constexpr int THREADS = WARPS * 32, STEP = step_tokens<D>(), TILE = WARPS * STEP, CHUNKS = D / 8, M = STEP / 16;
+template <typename T, int D, int CLUSTER, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) paged_kernel(PagedArgs a, int blocks) {
+    constexpr bool BF16 = sizeof(T) == 2;
+    constexpr int ROW = D * sizeof(T), CHUNKS = ROW / 16;  // bytes of a row, and its 16-byte chunks
+    constexpr int THREADS = WARPS * 32, STEP = step_tokens<T, D>(), TILE = WARPS * STEP;
+    // Chunks of a row are permuted so that neither the copies in nor the products' reads (bf16: 8 rows of a chunk; fp32: of 8 lanes,
+    // 32 / STEP to a row) meet in a bank.
+    constexpr int PARTS = 32 / STEP > 0 ? 32 / STEP : 1;  // fp32: lanes that share a token's scores
+    auto flip = [](int r) { return BF16 ? (D == 32 ? (r >> 1) & 3 : r & 7) : (r & (8 / PARTS - 1)) * PARTS; };
     static_assert(merge_bytes<D, CLUSTER, WARPS>() <= WARPS * STAGES * STEP_BYTES, "parts over the tiles");
     extern __shared__ __align__(128) uint8_t sm[];
     __shared__ uint32_t there[WARPS][STAGES][2];  // which tokens of a step are there, as bits
@@ -353,8 +243,8 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) paged_bf16_kernel(Paged
                 const int r = (i * 32 + lane) / CHUNKS, ch = lane % CHUNKS;
                 const uint32_t at = __shfl_sync(0xffffffffu, row[i * (32 / CHUNKS) / 32], r & 31);
                 const bool on = at != NONE;
-                const size_t src = on ? (((size_t)at * a.Hk + hk) * D + ch * 8) * 2 : 0;
-                const uint32_t dst = to + r * (2 * D) + ((ch ^ (D == 32 ? (r >> 1) & 3 : r & 7)) << 4);
+                const size_t src = on ? ((size_t)at * a.Hk + hk) * ROW + ch * 16 : 0;
+                const uint32_t dst = to + r * ROW + ((ch ^ flip(r)) << 4);
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(static_cast<const uint8_t*>(a.k) + src), "r"(on ? 16 : 0) : "memory");
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + STEP_BYTES / 2), "l"(static_cast<const uint8_t*>(a.v) + src), "r"(on ? 16 : 0)
                              : "memory");
@@ -379,103 +269,206 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) paged_bf16_kernel(Paged
 
     const float c = a.scale * LOG2E;
     int get_at = 0, segment = 0;
-    // where this lane's rows of the products' operands lie: K rows (its 8 x 8 tiles: tokens 0-7, 8-15, then channels 8 on), V
-    // rows (tokens 0-7 twice, then 8-15)
+    // bf16: where this lane's rows of the products' operands lie: K rows (its 8 x 8 tiles: tokens 0-7, 8-15, then channels 8 on),
+    // V rows (tokens 0-7 twice, then 8-15)
     const int krow = lane & 15, kch = lane >> 4, vrow = (lane & 7) + (lane >> 4) * 8, vch = lane >> 3 & 1;
-    auto swizzled = [](int r, int ch) { return (uint32_t)(r * (2 * D) + ((ch ^ (D == 32 ? (r >> 1) & 3 : r & 7)) << 4)); };
+    auto at_chunk = [&](int r, int ch) { return (uint32_t)(r * ROW + ((ch ^ flip(r)) << 4)); };
+    // fp32: the token and the channels of the lane's scores, the tokens and the chunk of its sums
+    const int tok = lane / PARTS, sub = lane % PARTS, vtok = lane / CHUNKS, vchunk = lane % CHUNKS;
+    float* q_sh = reinterpret_cast<float*>(sm + WARPS * STAGES * STEP_BYTES);
+    float* p_sh = q_sh + HEADS * D + warp * STEP * HEADS;
     while (CLUSTER ? segment == 0 : out.tile < end) {
         const int hk = out.walk / blocks, g0 = out.walk % blocks * HEADS, ng = min(HEADS, group - g0);
         const size_t q0 = (size_t)out.at.b * a.Hq + hk * group + g0;
-        uint32_t q[D / 8];  // column lane / 4 of q^T: channels 16 k + 2 (lane % 4), + 1, and 8 on
+        constexpr int OWN = BF16 ? 2 : HEADS;  // heads of a thread: bf16 2 (lane % 4), + 1, fp32 all
+        float m[OWN], l[OWN];
 #pragma unroll
-        for (int k = 0; k < D / 8; k++)
-            q[k] = lane / 4 < ng ? *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q) + (q0 + lane / 4) * D + 8 * k + 2 * (lane % 4)) : 0u;
-        float o[D / 16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // of heads 2 (lane % 4), + 1
+        for (int h = 0; h < OWN; h++) {
+            m[h] = -INFINITY;
+            l[h] = 0.f;
+        }
+        uint32_t q[BF16 ? D / 8 : 1];
+        float o[BF16 ? D / 16 : HEADS][4];
 #pragma unroll
-        for (int d = 0; d < D / 16; d++)
+        for (int d = 0; d < (BF16 ? D / 16 : HEADS); d++)
 #pragma unroll
             for (int e = 0; e < 4; e++) o[d][e] = 0.f;
+        if constexpr (BF16) {  // column lane / 4 of q^T: channels 16 k + 2 (lane % 4), + 1, and 8 on
+#pragma unroll
+            for (int k = 0; k < D / 8; k++)
+                q[k] = lane / 4 < ng ? *reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.q) + (q0 + lane / 4) * D + 8 * k + 2 * (lane % 4)) : 0u;
+        } else {
+            __syncthreads();  // the parts of the walk before have been read
+            for (int i = tid; i < HEADS * D; i += THREADS) q_sh[i] = i < ng * D ? c * static_cast<const T*>(a.q)[q0 * D + i] : 0.f;
+            __syncthreads();
+        }
         for (; out.t < out.t1; out.t++, out.tile++) {
             cp_async_wait_but<STAGES - 2>();
             __syncwarp();
             fetch();  // over the stage that the step before has read
             const uint32_t kt = ring + get_at * STEP_BYTES, vt = kt + STEP_BYTES / 2;
-            float s[M][4];
+            // a move of the maxima: all lanes' largest scores, and what was summed under the old ones
+            auto move = [&](float (&top)[OWN]) {
 #pragma unroll
-            for (int i = 0; i < M; i++) {
-                float odd[4] = {0.f, 0.f, 0.f, 0.f};  // two sums, so that products wait for one another half as long
+                for (int h = 0; h < OWN; h++) {
 #pragma unroll
-                for (int e = 0; e < 4; e++) s[i][e] = 0.f;
-#pragma unroll
-                for (int k = 0; k < D / 16; k++) {
-                    uint32_t x[4];
-                    ldmatrix_x4(kt + swizzled(16 * i + krow, 2 * k + kch), x);
-                    mma(k & 1 ? odd : s[i], x, q[2 * k], q[2 * k + 1]);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; e++) s[i][e] += odd[e];
-            }
-            float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < M; i++) {
-                const uint32_t bits = there[warp][get_at][i / 2] >> (i % 2 * 16 + lane / 4);
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    s[i][e] = bits >> (e / 2 * 8) & 1 ? c * s[i][e] : -INFINITY;
-                    top[e & 1] = fmaxf(top[e & 1], s[i][e]);
-                }
-            }
-            if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
-#pragma unroll
-                for (int h = 0; h < 2; h++) {
-#pragma unroll
-                    for (int x = 4; x < 32; x *= 2) top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], x));
+                    for (int x = BF16 ? 4 : PARTS; x < 32; x *= 2) top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], x));
                     const float to = fmaxf(m[h], top[h]), f = to == m[h] ? 1.f : exp2_fast(m[h] - to);
                     m[h] = to;
                     l[h] *= f;
+                    if constexpr (BF16) {
 #pragma unroll
-                    for (int d = 0; d < D / 16; d++) {
-                        o[d][h] *= f;
-                        o[d][2 + h] *= f;
+                        for (int d = 0; d < D / 16; d++) {
+                            o[d][h] *= f;
+                            o[d][2 + h] *= f;
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; e++) o[h][e] *= f;
                     }
                 }
-            }
-            const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+            };
+            if constexpr (BF16) {
+                constexpr int M = STEP / 16;
+                float s[M][4];
 #pragma unroll
-            for (int i = 0; i < M; i++) {
+                for (int i = 0; i < M; i++) {
+                    float odd[4] = {0.f, 0.f, 0.f, 0.f};  // two sums, so that products wait for one another half as long
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    s[i][e] = exp2_fast(s[i][e] - base[e & 1]);
-                    l[e & 1] += s[i][e];
+                    for (int e = 0; e < 4; e++) s[i][e] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < D / 16; k++) {
+                        uint32_t x[4];
+                        ldmatrix_x4(kt + at_chunk(16 * i + krow, 2 * k + kch), x);
+                        mma(k & 1 ? odd : s[i], x, q[2 * k], q[2 * k + 1]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; e++) s[i][e] += odd[e];
                 }
-                const uint32_t p0 = transpose(pack_bf16(s[i][0], s[i][1])), p1 = transpose(pack_bf16(s[i][2], s[i][3]));
+                float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                for (int d = 0; d < D / 16; d++) {
-                    uint32_t x[4];
-                    ldmatrix_x4_trans(vt + swizzled(16 * i + vrow, 2 * d + vch), x);
-                    mma(o[d], x, p0, p1);
+                for (int i = 0; i < M; i++) {
+                    const uint32_t bits = there[warp][get_at][i / 2] >> (i % 2 * 16 + lane / 4);
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        s[i][e] = bits >> (e / 2 * 8) & 1 ? c * s[i][e] : -INFINITY;
+                        top[e & 1] = fmaxf(top[e & 1], s[i][e]);
+                    }
+                }
+                if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) move(top);
+                const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+                for (int i = 0; i < M; i++) {
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        s[i][e] = exp2_fast(s[i][e] - base[e & 1]);
+                        l[e & 1] += s[i][e];
+                    }
+                    const uint32_t p0 = transpose(pack_bf16(s[i][0], s[i][1])), p1 = transpose(pack_bf16(s[i][2], s[i][3]));
+#pragma unroll
+                    for (int d = 0; d < D / 16; d++) {
+                        uint32_t x[4];
+                        ldmatrix_x4_trans(vt + at_chunk(16 * i + vrow, 2 * d + vch), x);
+                        mma(o[d], x, p0, p1);
+                    }
+                }
+            } else {
+                float s[HEADS];
+#pragma unroll
+                for (int g = 0; g < HEADS; g++) s[g] = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const float4 k4 = ld_shared_f4(kt + at_chunk(tok, i * PARTS + sub));
+#pragma unroll
+                    for (int g = 0; g < HEADS; g++)
+                        if (g < ng) {
+                            const float4 q4 = *reinterpret_cast<const float4*>(q_sh + g * D + (i * PARTS + sub) * 4);
+                            s[g] = fmaf(k4.x, q4.x, fmaf(k4.y, q4.y, fmaf(k4.z, q4.z, fmaf(k4.w, q4.w, s[g]))));
+                        }
+                }
+                const bool here = there[warp][get_at][0] >> tok & 1;
+                bool grown = false;
+#pragma unroll
+                for (int g = 0; g < HEADS; g++) {
+#pragma unroll
+                    for (int x = 1; x < PARTS; x *= 2) s[g] += __shfl_xor_sync(0xffffffffu, s[g], x);
+                    if (!here) s[g] = -INFINITY;
+                    grown = grown || s[g] > m[g] + 8.f;
+                }
+                if (__any_sync(0xffffffffu, grown)) {
+                    float top[HEADS];
+#pragma unroll
+                    for (int g = 0; g < HEADS; g++) top[g] = s[g];
+                    move(top);
+                }
+#pragma unroll
+                for (int g = 0; g < HEADS; g++) {
+                    s[g] = exp2_fast(s[g] - (m[g] == -INFINITY ? 0.f : m[g]));
+                    if (sub == 0) l[g] += s[g];
+                }
+                if (sub == 0) {
+                    reinterpret_cast<float4*>(p_sh + tok * HEADS)[0] = make_float4(s[0], s[1], s[2], s[3]);
+                    reinterpret_cast<float4*>(p_sh + tok * HEADS)[1] = make_float4(s[4], s[5], s[6], s[7]);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const int r = i * (32 / CHUNKS) + vtok;
+                    const float4 v4 = ld_shared_f4(vt + at_chunk(r, vchunk));
+                    const float4 p0 = reinterpret_cast<const float4*>(p_sh + r * HEADS)[0], p1 = reinterpret_cast<const float4*>(p_sh + r * HEADS)[1];
+                    const float p[HEADS] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+#pragma unroll
+                    for (int g = 0; g < HEADS; g++)
+                        if (g < ng) {
+                            o[g][0] = fmaf(p[g], v4.x, o[g][0]);
+                            o[g][1] = fmaf(p[g], v4.y, o[g][1]);
+                            o[g][2] = fmaf(p[g], v4.z, o[g][2]);
+                            o[g][3] = fmaf(p[g], v4.w, o[g][3]);
+                        }
                 }
             }
             get_at = get_at + 1 == STAGES ? 0 : get_at + 1;
         }
         // the warps' sums: each to shared memory under the common maximum, then added in order
 #pragma unroll
-        for (int h = 0; h < 2; h++)
+        for (int h = 0; h < OWN; h++)
 #pragma unroll
-            for (int x = 4; x < 32; x *= 2) l[h] += __shfl_xor_sync(0xffffffffu, l[h], x);
+            for (int x = BF16 ? 4 : 1; x < 32; x *= 2) l[h] += __shfl_xor_sync(0xffffffffu, l[h], x);
+        if constexpr (!BF16) {  // lanes that took other tokens of the same channels
+#pragma unroll
+            for (int g = 0; g < HEADS; g++)
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+#pragma unroll
+                    for (int x = CHUNKS; x < 32; x *= 2) o[g][e] += __shfl_xor_sync(0xffffffffu, o[g][e], x);
+        }
         __syncthreads();  // the walk before, or with clusters the tiles, have been read
         float* mine = merge + warp * HEADS * (D + 2);
+        if constexpr (BF16) {
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            float* to = mine + (2 * (lane % 4) + h) * (D + 2);
+            for (int h = 0; h < 2; h++) {
+                float* to = mine + (2 * (lane % 4) + h) * (D + 2);
 #pragma unroll
-            for (int d = 0; d < D / 16; d++) {
-                to[16 * d + lane / 4] = o[d][h];
-                to[16 * d + 8 + lane / 4] = o[d][2 + h];
+                for (int d = 0; d < D / 16; d++) {
+                    to[16 * d + lane / 4] = o[d][h];
+                    to[16 * d + 8 + lane / 4] = o[d][2 + h];
+                }
+                if (lane < 4) {
+                    to[D] = m[h];
+                    to[D + 1] = l[h];
+                }
             }
-            if (lane < 4) {
-                to[D] = m[h];
-                to[D + 1] = l[h];
+        } else {
+#pragma unroll
+            for (int g = 0; g < HEADS; g++) {
+                float* to = mine + g * (D + 2);
+                if (lane < CHUNKS)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) to[4 * lane + e] = o[g][e];
+                if (lane == 0) {
+                    to[D] = m[g];
+                    to[D + 1] = l[g];
+                }
             }
         }
         __syncthreads();
@@ -495,7 +488,7 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) paged_bf16_kernel(Paged
                 sum = fmaf(f, from[w * HEADS * (D + 2) + D + 1], sum);
             }
             if (out.whole) {
-                put(static_cast<__nv_bfloat16*>(a.o) + (q0 + g) * D + d, sum > 0.f ? x / sum : 0.f);
+                put(static_cast<T*>(a.o) + (q0 + g) * D + d, sum > 0.f ? x / sum : 0.f);
             } else {
                 part[g * (D + 2) + d] = x;
                 if (d == 0) {
@@ -527,7 +520,7 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) paged_bf16_kernel(Paged
                     x = fmaf(f, xr[r], x);
                     sum = fmaf(f, lr[r], sum);
                 }
-                put(static_cast<__nv_bfloat16*>(a.o) + (q0 + g) * D + d, sum > 0.f ? x / sum : 0.f);
+                put(static_cast<T*>(a.o) + (q0 + g) * D + d, sum > 0.f ? x / sum : 0.f);
             }
             cluster_sync();  // the others have read this CTA's
             return;
@@ -537,7 +530,7 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) paged_bf16_kernel(Paged
     // entries that see no token: zero
     for (int b = blockIdx.x; b < a.B; b += gridDim.x)
         if (Seen(a, b).count == 0)
-            for (int i = tid; i < a.Hq * D; i += THREADS) put(static_cast<__nv_bfloat16*>(a.o) + (size_t)b * a.Hq * D + i, 0.f);
+            for (int i = tid; i < a.Hq * D; i += THREADS) put(static_cast<T*>(a.o) + (size_t)b * a.Hq * D + i, 0.f);
 }
 
 // Joins the walk that the border before run blockIdx.x + 1 cuts, if that border is the first in it: the maximum of each
@@ -607,28 +600,31 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(PagedArgs a, i
     }
 }
 
-template <int D, typename T>
-cudaError_t step(void (*kernel)(PagedArgs, int), int smem, int tile, const PagedArgs& a, cudaStream_t st) {
+template <typename T, int D>
+cudaError_t runs(const PagedArgs& a, cudaStream_t st) {
+    constexpr int smem = smem_bytes<T, D, 0, RUN_WARPS>();
+    const auto kernel = paged_kernel<T, D, 0, RUN_WARPS>;
     const int blocks = (a.Hq / a.Hk + HEADS - 1) / HEADS;
     if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
     trace_begin("paged_step", st);
-    cudaError_t e = launch_after(kernel, dim3(RUNS), THREADS, smem, st, true, a, blocks);
+    cudaError_t e = launch_after(kernel, dim3(RUNS), RUN_WARPS * 32, smem, st, true, a, blocks);
     trace_end(st);
     if (e != cudaSuccess) return e;
     trace_begin("paged_join", st);
-    e = launch_after(paged_join_kernel<D, T>, dim3(RUNS - 1), JOIN_THREADS, 0, st, true, a, blocks, tile);
+    e = launch_after(paged_join_kernel<D, T>, dim3(RUNS - 1), JOIN_THREADS, 0, st, true, a, blocks, RUN_WARPS * step_tokens<T, D>());
     trace_end(st);
     return e;
 }
-template <int D, int CLUSTER>
+
+template <typename T, int D, int CLUSTER>
 cudaError_t clusters(const PagedArgs& a, cudaStream_t st) {
-    constexpr int WARPS = 8, smem = smem_bytes<D, CLUSTER, WARPS>();
-    const auto kernel = paged_bf16_kernel<D, CLUSTER, WARPS>;
+    constexpr int smem = smem_bytes<T, D, CLUSTER, CLUSTER_WARPS>();
+    const auto kernel = paged_kernel<T, D, CLUSTER, CLUSTER_WARPS>;
     const int blocks = (a.Hq / a.Hk + HEADS - 1) / HEADS;
     if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.B * a.Hk * blocks * CLUSTER);
-    cfg.blockDim = dim3(WARPS * 32);
+    cfg.blockDim = dim3(CLUSTER_WARPS * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[2];
@@ -645,31 +641,36 @@ cudaError_t clusters(const PagedArgs& a, cudaStream_t st) {
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-constexpr long long CLUSTER_MOST = 4096 * 128;  // tokens x channels of a CTA
-// The CTAs of a cluster for each walk, where walks are few and sequences not long (one launch, and no lengths to sum up
-// first): the most of 8, 4, 2 that the SMs have room for; 0: runs.
+// The CTAs of a cluster for each walk, where walks are few and sequences not long (one launch, and no lengths to sum up first): the
+// most of 8, 4, 2 that the SMs have room for; 0: runs. On the GPU alone, 32 heads on 8, bf16, in us with clusters and with
+// runs: one sequence of 100 tokens 5 and 11, 4096 8 and 26, 16384 19 and 33, 32768 34 and 45; four of 4096 12 and 26, of 16384 43
+// and 62. One long sequence among short ones waits for its clusters alone, hence the limit on the table's room for a CTA: 2 MB.
 int cluster_of(const PagedArgs& a) {
     const long long walks = (long long)a.B * a.Hk * ((a.Hq / a.Hk + HEADS - 1) / HEADS);
     int n = 8;
     while (n > 1 && walks * n > 152) n /= 2;
-    return a.bf16 && n > 1 && (long long)a.table_pages * a.page_size * a.D <= (long long)n * CLUSTER_MOST ? n : 0;
+    const long long bytes = (long long)a.table_pages * a.page_size * a.D * (a.bf16 ? 4 : 8);  // K and V of the longest walk
+    return n > 1 && bytes <= (long long)n * (2 << 20) ? n : 0;
 }
 
-template <int D>
+template <typename T, int D>
 cudaError_t step_of(const PagedArgs& a, cudaStream_t st) {
-    const int n = cluster_of(a);
-    if (n) return n == 8 ? clusters<D, 8>(a, st) : n == 4 ? clusters<D, 4>(a, st) : clusters<D, 2>(a, st);
-    if (a.bf16)
-        return step<D, __nv_bfloat16>(paged_bf16_kernel<D, 0, 4>, smem_bytes<D, 0, 4>(), 4 * step_tokens<D>(), a, st);
-    return step<D, float>(paged_f32_kernel<D>, (2 * kTile32 * (D + 4) + HEADS * (D + 4) + HEADS * kTile32) * 4, kTile32, a, st);
+    switch (cluster_of(a)) {
+        case 8: return clusters<T, D, 8>(a, st);
+        case 4: return clusters<T, D, 4>(a, st);
+        case 2: return clusters<T, D, 2>(a, st);
+        default: return runs<T, D>(a, st);
+    }
+}
+template <typename T>
+cudaError_t step(const PagedArgs& a, cudaStream_t st) {
+    return a.D == 32 ? step_of<T, 32>(a, st) : a.D == 64 ? step_of<T, 64>(a, st) : step_of<T, 128>(a, st);
 }
 
 }  // namespace
 
 size_t paged_parts_bytes(int D) { return (size_t)2 * RUNS * HEADS * (D + 2) * sizeof(float); }
 
-cudaError_t launch_paged_step(const PagedArgs& a, cudaStream_t st) {
-    return a.D == 32 ? step_of<32>(a, st) : a.D == 64 ? step_of<64>(a, st) : step_of<128>(a, st);
-}
+cudaError_t launch_paged_step(const PagedArgs& a, cudaStream_t st) { return a.bf16 ? step<__nv_bfloat16>(a, st) : step<float>(a, st); }
 
 }  // namespace gdr
