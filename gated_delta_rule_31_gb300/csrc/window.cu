@@ -25,25 +25,40 @@ constexpr int N = 64, THREADS = 256, LP = N + 4;  // tokens of a tile, row strid
 
 __device__ __forceinline__ float4 get4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
-// Rows t0 .. t0 + 63 of one head of x [B, T, H, D] into shared memory; rows from n on are zero.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
+}
+__device__ __forceinline__ void fma2(uint64_t& c, uint64_t a, uint64_t b) { asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b)); }
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+
+// Rows t0 .. t0 + 63 of one head of x [B, T, H, D] into shared memory, asynchronously; rows from n on are zero.
 template <int D>
 __device__ __forceinline__ void load_tile(float* to, const void* x, int len, int H, int b, int h, int t0, int n) {
+#pragma unroll
     for (int i = threadIdx.x; i < N * D / 4; i += THREADS) {
         const int r = i / (D / 4), c = i % (D / 4) * 4;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (t0 + r < n) v = get4(static_cast<const float*>(x) + (((size_t)b * len + t0 + r) * H + h) * D + c);
-        *reinterpret_cast<float4*>(to + r * (D + 4) + c) = v;
+        const bool on = t0 + r < n;
+        cp_async16(to + r * (D + 4) + c, static_cast<const float*>(x) + (((size_t)b * len + (on ? t0 + r : 0)) * H + h) * D + c, on);
     }
 }
+// All copies but those of the last group have landed, for every thread of the CTA.
+__device__ __forceinline__ void tiles_there(bool but_last) {
+    if (but_last) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else cp_async_wait_all();
+    __syncthreads();
+}
 
-// acc[i][j] = a row 4 ty + i . b row tx + 16 j
+// acc[i][j] = a row 4 ty + i . b row tx + 16 j; two sums each, of even and odd channels
 template <int D>
 __device__ __forceinline__ void rows_by_rows(const float* a, const float* b, float (&acc)[4][4]) {
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    uint64_t s[4][4];
 #pragma unroll
     for (int i = 0; i < 4; i++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) acc[i][j] = 0.f;
+        for (int j = 0; j < 4; j++) s[i][j] = 0;
 #pragma unroll 4
     for (int d = 0; d < D; d += 4) {
         float4 x[4], y[4];
@@ -55,12 +70,18 @@ __device__ __forceinline__ void rows_by_rows(const float* a, const float* b, flo
         for (int i = 0; i < 4; i++)
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                acc[i][j] = fmaf(x[i].x, y[j].x, acc[i][j]);
-                acc[i][j] = fmaf(x[i].y, y[j].y, acc[i][j]);
-                acc[i][j] = fmaf(x[i].z, y[j].z, acc[i][j]);
-                acc[i][j] = fmaf(x[i].w, y[j].w, acc[i][j]);
+                fma2(s[i][j], pair(x[i].x, x[i].y), pair(y[j].x, y[j].y));
+                fma2(s[i][j], pair(x[i].z, x[i].w), pair(y[j].z, y[j].w));
             }
     }
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            float even, odd;
+            unpair(s[i][j], even, odd);
+            acc[i][j] = even + odd;
+        }
 }
 
 // Columns of an output row that a thread keeps: D / 16 of them, W together.
@@ -70,9 +91,9 @@ struct Cols {
     static __device__ __forceinline__ int at(int g) { return threadIdx.x % 16 * W + g * 16 * W; }
 };
 
-// acc[i][.] += sum over k of p[4 ty + i][k] b[k][columns]
+// acc[i][.] += sum over k of p[4 ty + i][k] b[k][columns], columns in pairs
 template <int D>
-__device__ __forceinline__ void rows_by_cols(const float* p, const float* b, float (&acc)[4][D / 16]) {
+__device__ __forceinline__ void rows_by_cols(const float* p, const float* b, uint64_t (&acc)[4][D / 32]) {
     using C = Cols<D>;
     const int ty = threadIdx.x / 16;
 #pragma unroll 2
@@ -84,15 +105,27 @@ __device__ __forceinline__ void rows_by_cols(const float* p, const float* b, flo
         for (int kk = 0; kk < 4; kk++)
 #pragma unroll
             for (int g = 0; g < C::NW; g++) {
-                float y[C::W];
-#pragma unroll
-                for (int c = 0; c < C::W; c++) y[c] = b[(k + kk) * (D + 4) + C::at(g) + c];
+                const float* at = b + (k + kk) * (D + 4) + C::at(g);
+                uint64_t y[C::W / 2];
+                if constexpr (C::W == 4) {
+                    const float4 v = get4(at);
+                    y[0] = pair(v.x, v.y);
+                    y[C::W / 2 - 1] = pair(v.z, v.w);
+                } else {
+                    const float2 v = *reinterpret_cast<const float2*>(at);
+                    y[0] = pair(v.x, v.y);
+                }
 #pragma unroll
                 for (int i = 0; i < 4; i++)
 #pragma unroll
-                    for (int c = 0; c < C::W; c++) acc[i][g * C::W + c] = fmaf(x[i][kk], y[c], acc[i][g * C::W + c]);
+                    for (int c = 0; c < C::W / 2; c++) fma2(acc[i][g * C::W / 2 + c], pair(x[i][kk], x[i][kk]), y[c]);
             }
     }
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 __device__ __forceinline__ bool sees(const WindowShape& s, int t, int j, int n) {
@@ -108,8 +141,7 @@ __device__ __forceinline__ float over16(float x, bool max) {
 }
 
 template <int D>
-__device__ __forceinline__ void put_rows(void* x, int len, int H, int b, int h, int t0, const float (&acc)[4][D / 16],
-                                         const float* f) {
+__device__ __forceinline__ void put_rows(void* x, int len, int H, int b, int h, int t0, const uint64_t (&acc)[4][D / 32], const float* f) {
     using C = Cols<D>;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
@@ -119,7 +151,11 @@ __device__ __forceinline__ void put_rows(void* x, int len, int H, int b, int h, 
 #pragma unroll
         for (int g = 0; g < C::NW; g++)
 #pragma unroll
-            for (int c = 0; c < C::W; c++) row[C::at(g) + c] = f[i] * acc[i][g * C::W + c];
+            for (int c = 0; c < C::W; c += 2) {
+                float u, v;
+                unpair(acc[i][(g * C::W + c) / 2], u, v);
+                *reinterpret_cast<float2*>(row + C::at(g) + c) = make_float2(f[i] * u, f[i] * v);
+            }
     }
 }
 
@@ -129,25 +165,37 @@ constexpr int tile_bytes() { return N * (D + 4) * 4; }
 template <int D>
 __global__ void __launch_bounds__(THREADS) window_fwd_kernel(WindowArgs a) {
     extern __shared__ __align__(16) float sh[];
-    float *Q = sh, *K = Q + tile_bytes<D>() / 4, *V = K + tile_bytes<D>() / 4, *P = V + tile_bytes<D>() / 4;
+    constexpr int TILE = tile_bytes<D>() / 4;
+    float *Q = sh, *KV = Q + TILE, *P = KV + 4 * TILE;  // two tiles each of K and V: the next ones come in meanwhile
     const WindowShape& s = a.s;
     const int t0 = (gridDim.x - 1 - blockIdx.x) * N, h = blockIdx.y, b = blockIdx.z, hk = h / (s.Hq / s.Hk), n = s.tokens(b);
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     if (blockIdx.x + blockIdx.y + blockIdx.z == 0 && threadIdx.x < 4) a.status[threadIdx.x] = 0;
     const KeyTiles tiles(N, s.window, s.sinks, t0, min(t0 + N, n));
+    const int count = tiles.count();
+    auto load = [&](int it) {
+        if (it < count) {
+            load_tile<D>(KV + (it & 1) * 2 * TILE, a.k, s.T, s.Hk, b, hk, tiles.at(it) * N, n);
+            load_tile<D>(KV + (it & 1) * 2 * TILE + TILE, a.v, s.T, s.Hk, b, hk, tiles.at(it) * N, n);
+        }
+        cp_async_commit();
+    };
     load_tile<D>(Q, a.q, s.T, s.Hq, b, h, t0, n);
-    float m[4], l[4], acc[4][D / 16] = {};
+    load(0);
+    const float c = s.scale * 1.4426950408889634f;  // scores in units of log 2
+    float m[4], l[4];
+    uint64_t acc[4][D / 32] = {};
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         m[i] = -INFINITY;
         l[i] = 0.f;
     }
-    for (int it = 0; it < tiles.count(); it++) {
+    for (int it = 0; it < count; it++) {
         const int j0 = tiles.at(it) * N;
-        __syncthreads();
-        load_tile<D>(K, a.k, s.T, s.Hk, b, hk, j0, n);
-        load_tile<D>(V, a.v, s.T, s.Hk, b, hk, j0, n);
-        __syncthreads();
+        const float *K = KV + (it & 1) * 2 * TILE, *V = K + TILE;
+        __syncthreads();  // the tiles before these have been read
+        load(it + 1);
+        tiles_there(true);
         float S[4][4];
         rows_by_rows<D>(Q, K, S);
 #pragma unroll
@@ -156,26 +204,28 @@ __global__ void __launch_bounds__(THREADS) window_fwd_kernel(WindowArgs a) {
             float top = m[i], sum = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                S[i][j] = sees(s, t, j0 + tx + 16 * j, n) ? s.scale * S[i][j] : -INFINITY;
+                S[i][j] = sees(s, t, j0 + tx + 16 * j, n) ? c * S[i][j] : -INFINITY;
                 top = fmaxf(top, S[i][j]);
             }
             top = over16(top, true);
             const float base = top == -INFINITY ? 0.f : top;  // no token seen yet
-            const float fade = expf(m[i] - base);
+            const float fade = exp2_fast(m[i] - base);
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                S[i][j] = expf(S[i][j] - base);
+                S[i][j] = exp2_fast(S[i][j] - base);
                 sum += S[i][j];
                 P[(4 * ty + i) * LP + tx + 16 * j] = S[i][j];
             }
             m[i] = top;
             l[i] = fade * l[i] + over16(sum, false);
+            const uint64_t f2 = pair(fade, fade);
 #pragma unroll
-            for (int c = 0; c < D / 16; c++) acc[i][c] *= fade;
+            for (int d = 0; d < D / 32; d++) asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(acc[i][d]) : "l"(f2));
         }
-        __syncthreads();
+        __syncwarp();  // a warp's rows of P are its own
         rows_by_cols<D>(P, V, acc);
     }
+    cp_async_wait_all();
     float f[4];
 #pragma unroll
     for (int i = 0; i < 4; i++) f[i] = l[i] == 0.f ? 0.f : 1.f / l[i];
@@ -184,7 +234,7 @@ __global__ void __launch_bounds__(THREADS) window_fwd_kernel(WindowArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; i++)
             if (t0 + 4 * ty + i < s.T)
-                a.lse[((size_t)b * s.Hq + h) * s.T + t0 + 4 * ty + i] = l[i] == 0.f ? -INFINITY : m[i] + logf(l[i]);
+                a.lse[((size_t)b * s.Hq + h) * s.T + t0 + 4 * ty + i] = l[i] == 0.f ? -INFINITY : 0.6931471805599453f * m[i] + logf(l[i]);
 }
 
 // delta [B, Hq, T]: 8 lanes a row.
@@ -211,27 +261,38 @@ template <int D>
 __global__ void __launch_bounds__(THREADS) window_dq_kernel(WindowArgs a) {
     extern __shared__ __align__(16) float sh[];
     constexpr int TILE = tile_bytes<D>() / 4;
-    float *Q = sh, *G = Q + TILE, *K = G + TILE, *V = K + TILE, *P = V + TILE;
+    float *Q = sh, *G = Q + TILE, *KV = G + TILE, *P = KV + 4 * TILE;
     const WindowShape& s = a.s;
     const int t0 = (gridDim.x - 1 - blockIdx.x) * N, h = blockIdx.y, b = blockIdx.z, hk = h / (s.Hq / s.Hk), n = s.tokens(b);
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const KeyTiles tiles(N, s.window, s.sinks, t0, min(t0 + N, n));
+    const int count = tiles.count();
+    auto load = [&](int it) {
+        if (it < count) {
+            load_tile<D>(KV + (it & 1) * 2 * TILE, a.k, s.T, s.Hk, b, hk, tiles.at(it) * N, n);
+            load_tile<D>(KV + (it & 1) * 2 * TILE + TILE, a.v, s.T, s.Hk, b, hk, tiles.at(it) * N, n);
+        }
+        cp_async_commit();
+    };
     load_tile<D>(Q, a.q, s.T, s.Hq, b, h, t0, n);
     load_tile<D>(G, a.do_, s.T, s.Hq, b, h, t0, n);
-    float lse[4], delta[4], acc[4][D / 16] = {};
+    load(0);
+    const float c = s.scale * 1.4426950408889634f;
+    float lse[4], delta[4];
+    uint64_t acc[4][D / 32] = {};
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         const int t = t0 + 4 * ty + i;
         const size_t at = ((size_t)b * s.Hq + h) * s.T + t;
-        lse[i] = t < n ? a.lse[at] : 0.f;
+        lse[i] = t < n ? 1.4426950408889634f * a.lse[at] : 0.f;
         delta[i] = t < n ? a.delta[at] : 0.f;
     }
-    for (int it = 0; it < tiles.count(); it++) {
+    for (int it = 0; it < count; it++) {
         const int j0 = tiles.at(it) * N;
-        __syncthreads();
-        load_tile<D>(K, a.k, s.T, s.Hk, b, hk, j0, n);
-        load_tile<D>(V, a.v, s.T, s.Hk, b, hk, j0, n);
-        __syncthreads();
+        const float *K = KV + (it & 1) * 2 * TILE, *V = K + TILE;
+        __syncthreads();  // the tiles before these have been read
+        load(it + 1);
+        tiles_there(true);
         float S[4][4], dP[4][4];
         rows_by_rows<D>(Q, K, S);
         rows_by_rows<D>(G, V, dP);
@@ -240,57 +301,110 @@ __global__ void __launch_bounds__(THREADS) window_dq_kernel(WindowArgs a) {
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 const bool on = sees(s, t0 + 4 * ty + i, j0 + tx + 16 * j, n);
-                P[(4 * ty + i) * LP + tx + 16 * j] = on ? expf(s.scale * S[i][j] - lse[i]) * (dP[i][j] - delta[i]) : 0.f;
+                P[(4 * ty + i) * LP + tx + 16 * j] = on ? exp2_fast(fmaf(c, S[i][j], -lse[i])) * (dP[i][j] - delta[i]) : 0.f;
             }
-        __syncthreads();
+        __syncwarp();  // a warp's rows are its own
         rows_by_cols<D>(P, K, acc);
     }
+    cp_async_wait_all();
     const float f[4] = {s.scale, s.scale, s.scale, s.scale};
     put_rows<D>(a.dq, s.T, s.Hq, b, h, t0, acc, f);
 }
 
-template <int D>
+// SPLIT: a CTA for each query head, whose sums go to parts [2][B, T, Hq, D] (dk, dv), to be added by window_heads_kernel.
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(THREADS) window_dkv_kernel(WindowArgs a) {
     extern __shared__ __align__(16) float sh[];
     constexpr int TILE = tile_bytes<D>() / 4;
-    float *Q = sh, *G = Q + TILE, *K = G + TILE, *V = K + TILE, *P = V + TILE, *dS = P + N * LP;
+    float *K = sh, *V = K + TILE, *QG = V + TILE, *P = QG + 4 * TILE;  // P and then dS
     const WindowShape& s = a.s;
-    const int j0 = blockIdx.x * N, hk = blockIdx.y, b = blockIdx.z, group = s.Hq / s.Hk, n = s.tokens(b);
+    const int j0 = blockIdx.x * N, share = s.Hq / s.Hk, hk = SPLIT ? blockIdx.y / share : blockIdx.y, b = blockIdx.z, n = s.tokens(b);
+    const int first = SPLIT ? blockIdx.y : hk * share, group = SPLIT ? 1 : share;  // query heads of this CTA
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const int end = j0 < n ? queries_end(N, s.window, s.sinks, j0, n) : j0, per = (end - j0 + N - 1) / N, count = per * group;
+    auto load = [&](int it, int g, int tile) {
+        if (it < count) {
+            load_tile<D>(QG + (it & 1) * 2 * TILE, a.q, s.T, s.Hq, b, first + g, j0 + tile * N, n);
+            load_tile<D>(QG + (it & 1) * 2 * TILE + TILE, a.do_, s.T, s.Hq, b, first + g, j0 + tile * N, n);
+        }
+        cp_async_commit();
+    };
     load_tile<D>(K, a.k, s.T, s.Hk, b, hk, j0, n);
     load_tile<D>(V, a.v, s.T, s.Hk, b, hk, j0, n);
-    float dk[4][D / 16] = {}, dv[4][D / 16] = {};
-    const int end = j0 < n ? queries_end(N, s.window, s.sinks, j0, n) : 0;
-    for (int h = hk * group; h < (hk + 1) * group; h++)
-        for (int t0 = j0; t0 < end; t0 += N) {
-            __syncthreads();
-            load_tile<D>(Q, a.q, s.T, s.Hq, b, h, t0, n);
-            load_tile<D>(G, a.do_, s.T, s.Hq, b, h, t0, n);
-            __syncthreads();
-            float S[4][4], dP[4][4];  // rows: keys, columns: queries
-            rows_by_rows<D>(K, Q, S);
-            rows_by_rows<D>(V, G, dP);
+    load(0, 0, 0);
+    const float c = s.scale * 1.4426950408889634f;
+    uint64_t dk[4][D / 32] = {}, dv[4][D / 32] = {};
+    int g = 0, tile = 0;
+    for (int it = 0; it < count; it++) {
+        const float *Q = QG + (it & 1) * 2 * TILE, *G = Q + TILE;
+        const int t0 = j0 + tile * N;
+        const size_t rows = ((size_t)b * s.Hq + first + g) * s.T + t0;
+        if (++tile == per) {
+            tile = 0;
+            g++;
+        }
+        __syncthreads();  // the tiles before these have been read
+        load(it + 1, g, tile);
+        float lse[4], delta[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const bool on = t0 + tx + 16 * j < n;
+            lse[j] = on ? 1.4426950408889634f * a.lse[rows + tx + 16 * j] : 0.f;
+            delta[j] = on ? a.delta[rows + tx + 16 * j] : 0.f;
+        }
+        tiles_there(true);
+        float S[4][4], dP[4][4];  // rows: keys, columns: queries
+        rows_by_rows<D>(K, Q, S);
+        rows_by_rows<D>(V, G, dP);
+#pragma unroll
+        for (int i = 0; i < 4; i++)
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                const int t = t0 + tx + 16 * j;
-                const size_t at = ((size_t)b * s.Hq + h) * s.T + t;
-                const float lse = t < n ? a.lse[at] : 0.f, delta = t < n ? a.delta[at] : 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const bool on = sees(s, t, j0 + 4 * ty + i, n);
-                    const float p = on ? expf(s.scale * S[i][j] - lse) : 0.f;
-                    P[(4 * ty + i) * LP + tx + 16 * j] = p;
-                    dS[(4 * ty + i) * LP + tx + 16 * j] = on ? p * (dP[i][j] - delta) : 0.f;
-                }
+                const bool on = sees(s, t0 + tx + 16 * j, j0 + 4 * ty + i, n);
+                S[i][j] = on ? exp2_fast(fmaf(c, S[i][j], -lse[j])) : 0.f;
+                dP[i][j] = on ? S[i][j] * (dP[i][j] - delta[j]) : 0.f;
+                P[(4 * ty + i) * LP + tx + 16 * j] = S[i][j];
             }
-            __syncthreads();
-            rows_by_cols<D>(P, G, dv);
-            rows_by_cols<D>(dS, Q, dk);
-        }
+        __syncwarp();  // a warp's rows are its own
+        rows_by_cols<D>(P, G, dv);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) P[(4 * ty + i) * LP + tx + 16 * j] = dP[i][j];
+        __syncwarp();
+        rows_by_cols<D>(P, Q, dk);
+    }
+    cp_async_wait_all();
     const float f[4] = {s.scale, s.scale, s.scale, s.scale}, one[4] = {1.f, 1.f, 1.f, 1.f};
-    put_rows<D>(a.dk, s.T, s.Hk, b, hk, j0, dk, f);
-    put_rows<D>(a.dv, s.T, s.Hk, b, hk, j0, dv, one);
+    if (SPLIT) {
+        put_rows<D>(a.parts, s.T, s.Hq, b, first, j0, dk, f);
+        put_rows<D>(a.parts + (size_t)s.B * s.T * s.Hq * D, s.T, s.Hq, b, first, j0, dv, one);
+    } else {
+        put_rows<D>(a.dk, s.T, s.Hk, b, hk, j0, dk, f);
+        put_rows<D>(a.dv, s.T, s.Hk, b, hk, j0, dv, one);
+    }
 }
+
+__global__ void __launch_bounds__(256) window_heads_kernel(WindowArgs a) {
+    const WindowShape& s = a.s;
+    const int share = s.Hq / s.Hk;
+    const size_t all = (size_t)s.B * s.T * s.Hk * s.D, i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4, row = i / s.D, d = i % s.D;
+    if (i >= all) return;
+#pragma unroll
+    for (int w = 0; w < 2; w++) {
+        const float* from = a.parts + w * all * share + row * share * s.D + d;
+        float4 x = get4(from);
+        for (int h = 1; h < share; h++) {
+            const float4 y = get4(from + (size_t)h * s.D);
+            x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+        }
+        *reinterpret_cast<float4*>(static_cast<float*>(w ? a.dv : a.dk) + i) = x;
+    }
+}
+
+// By query heads where tiles of the key heads are too few for two CTAs on each SM.
+bool split_heads(const WindowShape& s) { return s.Hq > s.Hk && (long long)(s.T + N - 1) / N * s.Hk * s.B < 2 * 152; }
 
 template <typename K>
 cudaError_t launch(K kernel, const char* name, int heads, int smem, const WindowArgs& a, cudaStream_t st) {
@@ -302,7 +416,7 @@ cudaError_t launch(K kernel, const char* name, int heads, int smem, const Window
 }
 template <int D>
 cudaError_t fwd(const WindowArgs& a, cudaStream_t st) {
-    return launch(window_fwd_kernel<D>, "window_fwd", a.s.Hq, 3 * tile_bytes<D>() + N * LP * 4, a, st);
+    return launch(window_fwd_kernel<D>, "window_fwd", a.s.Hq, 5 * tile_bytes<D>() + N * LP * 4, a, st);
 }
 cudaError_t delta(const WindowArgs& a, cudaStream_t st) {
     const size_t rows = (size_t)a.s.B * a.s.T * a.s.Hq;
@@ -313,11 +427,23 @@ cudaError_t delta(const WindowArgs& a, cudaStream_t st) {
 }
 template <int D>
 cudaError_t bwd(const WindowArgs& a, cudaStream_t st) {
-    if (cudaError_t e = launch(window_dq_kernel<D>, "window_dq", a.s.Hq, 4 * tile_bytes<D>() + N * LP * 4, a, st)) return e;
-    return launch(window_dkv_kernel<D>, "window_dkv", a.s.Hk, 4 * tile_bytes<D>() + 2 * N * LP * 4, a, st);
+    if (cudaError_t e = launch(window_dq_kernel<D>, "window_dq", a.s.Hq, 6 * tile_bytes<D>() + N * LP * 4, a, st)) return e;
+    const int smem = 6 * tile_bytes<D>() + N * LP * 4;
+    if (!split_heads(a.s)) return launch(window_dkv_kernel<D, false>, "window_dkv", a.s.Hk, smem, a, st);
+    if (cudaError_t e = launch(window_dkv_kernel<D, true>, "window_dkv", a.s.Hq, smem, a, st)) return e;
+    const size_t values = (size_t)a.s.B * a.s.T * a.s.Hk * D;
+    trace_begin("window_heads", st);
+    window_heads_kernel<<<(unsigned)((values + 1023) / 1024), 256, 0, st>>>(a);
+    trace_end(st);
+    return cudaGetLastError();
 }
 
 }  // namespace
+
+size_t window_parts_bytes(const WindowShape& s) {
+    if (s.bf16) return window_parts_bytes_tc(s);
+    return split_heads(s) ? 2 * (size_t)s.B * s.T * s.Hq * s.D * sizeof(float) : 0;
+}
 
 cudaError_t launch_window_fwd(const WindowArgs& a, cudaStream_t st) {
     if (a.s.bf16) return launch_window_fwd_tc(a, st);

@@ -820,8 +820,8 @@ cudaError_t launch_bwd(const WindowArgs& x, cudaStream_t st) {
 
 }  // namespace
 
-size_t window_parts_bytes(const WindowShape& s) {
-    return s.bf16 && s.B > 0 && s.T > 0 ? (size_t)Cut(s).parts * 2 * C * s.D * sizeof(float) : 0;
+size_t window_parts_bytes_tc(const WindowShape& s) {
+    return s.B > 0 && s.T > 0 ? (size_t)Cut(s).parts * 2 * C * s.D * sizeof(float) : 0;
 }
 
 cudaError_t launch_window_bwd_tc(const WindowArgs& x, cudaStream_t st) {

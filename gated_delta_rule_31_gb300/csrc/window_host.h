@@ -11,6 +11,7 @@ inline bool rows_map(CUtensorMap* m, const void* p, const WindowShape& s, int H)
 }
 
 cudaError_t launch_window_fwd_tc(const WindowArgs& a, cudaStream_t st);
+size_t window_parts_bytes_tc(const WindowShape& s);
 cudaError_t launch_window_bwd_tc(const WindowArgs& a, cudaStream_t st);
 
 }  // namespace gdr
