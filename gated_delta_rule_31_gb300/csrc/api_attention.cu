@@ -90,6 +90,7 @@ gdr_status check_paged(const gdr_paged_problem* p) {
     const gdr_status r = check_heads(p->Hq, p->Hk, p->D, p->window, p->sinks, p->dtype, p->scale);
     if (r != GDR_OK) return r;
     if (p->B > 65535) return GDR_ERR_UNSUPPORTED;
+    if ((long long)p->pages * p->page_size >= 0xffffffffLL) return GDR_ERR_UNSUPPORTED;  // rows are counted in 32 bits
     return GDR_OK;
 }
 

@@ -57,6 +57,7 @@ struct GradArgs {
     int cut, pieces_cut;  // key tiles from the start, pieces of each
     int pieces;           // pieces of the others
     int units;
+    int heavy, light;  // dkv with first tiles that are cut: pairs of a piece and of another tile; heavy 0: not
     const float* lse;
     int rest;  // dq: what the rounding of o left is there
     float* delta;
@@ -65,9 +66,39 @@ struct GradArgs {
     int* status;
 };
 
-__device__ __forceinline__ int unit_of(int round) {  // every other round in reverse
-    return round * (int)gridDim.x + (int)(round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-}
+// The units of a CTA, in turn: one of each round of them, every other round in reverse, so that long and short ones even out. Where
+// there are long ones first and then equal ones, the CTAs that get one long one more than others join the rounds of the equal ones
+// as many rounds later as that is worth. (CTAs that take neighbouring units instead share no tiles in L2: 1170 us for 865.)
+template <bool KEYS>
+struct Share {
+    int mine, pieces, more, late;  // this CTA's long ones; of all; CTAs with one more; rounds that they are late
+    __device__ __forceinline__ explicit Share(const GradArgs& a) : mine(0), pieces(0), more(0), late(0) {
+        if (KEYS && a.heavy) {
+            const int n = gridDim.x, c = blockIdx.x;
+            pieces = a.s.Hk * a.s.B * a.cut * a.pieces_cut;
+            more = pieces % n;
+            mine = pieces / n + (c < more);
+            late = more ? (a.heavy + a.light / 2) / a.light : 0;
+        }
+    }
+    // The unit of a round: -1 for none in this round; false after the last.
+    __device__ __forceinline__ bool unit(const GradArgs& a, int round, int& u) const {
+        const int n = gridDim.x, c = blockIdx.x;
+        if (KEYS && a.heavy) {
+            if (round < mine) {
+                u = round * n + c;
+                return true;
+            }
+            const int r = round - mine + (c < more ? late : 0);
+            u = pieces + (r < late ? r * (n - more) + c - more : late * (n - more) + (r - late) * n + c);
+            return u < a.units;
+        }
+        u = round * n + (round & 1 ? n - 1 - c : c);
+        if (u < a.units) return true;
+        u = -1;
+        return round * n < a.units;
+    }
+};
 
 // dq: 128 queries of a head, and the key tiles that they see.
 struct QueryUnit {
@@ -137,16 +168,17 @@ template <typename U>
 struct Stream {
     U x;
     Queries at;
+    Share<std::is_same<U, KeyUnit>::value> share;
     int round = -1, i = 0, count = 0;
+    __device__ __forceinline__ explicit Stream(const GradArgs& a) : share(a) {}
     __device__ __forceinline__ Pair next(const GradArgs& a) {
         if (++i < count) {
             if constexpr (std::is_same<U, KeyUnit>::value) at.next(x);
         }
         while (i >= count) {
-            round++;
-            if (round * (int)gridDim.x >= a.units) return Pair{false, false, false, 0};
-            const int u = unit_of(round);
-            if (u >= a.units) continue;
+            int u;
+            if (!share.unit(a, ++round, u)) return Pair{false, false, false, 0};
+            if (u < 0) continue;
             x.set(a, u);
             i = 0;
             count = x.count();
@@ -258,13 +290,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 put(AT_RING + k * TILE, map, head, t, b, &bar.full[k], &used[k]);
                 pos++;
             };
+            const Share<KEYS> share(a);
 #pragma unroll 1
-            for (int round = 0; ok; round++) {
-                const int u = unit_of(round);
-                if (u >= a.units) {
-                    if (round * (int)gridDim.x >= a.units) break;
-                    continue;
-                }
+            for (int round = 0, u; ok && share.unit(a, round, u); round++) {
+                if (u < 0) continue;
                 U x;
                 x.set(a, u);
                 const int count = x.count();
@@ -303,7 +332,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else if (warp == 9) {
             constexpr uint32_t id_s = idesc_bf16(128, KEYS ? 128 : 64, 0, 0), id_o = idesc_bf16(128, D, 0, 1);
             const int extra = KEYS ? 0 : a.rest ? 2 : 1;  // tiles of the ring ahead of a unit's pairs
-            Stream<U> stream;
+            Stream<U> stream(a);
             int started = 0, summed = 0;  // units begun by S and dP, by the sums
             int pos = 0;                  // pairs so far
             int ring = 0;                 // place in the ring of the current pair's first tile
@@ -417,7 +446,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             wait_for(&bar.drain, 0, &never, 1);
         } else if (KEYS && warp == 10) {
             if constexpr (KEYS) {
-                Stream<KeyUnit> stream;
+                Stream<KeyUnit> stream(a);
                 for (int pos = 0;; pos++) {
                     const Pair p = stream.next(a);
                     if (!p.some) break;
@@ -480,13 +509,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.sumfree);
         };
+        const Share<KEYS> share(a);
 #pragma unroll 1
-        for (int round = 0; ok; round++) {
-            const int u = unit_of(round);
-            if (u >= a.units) {
-                if (round * (int)gridDim.x >= a.units) break;
-                continue;
-            }
+        for (int round = 0, u; ok && share.unit(a, round, u); round++) {
+            if (u < 0) continue;
             U x;
             x.set(a, u);
             const int count = x.count(), n = x.n;
@@ -740,7 +766,7 @@ __global__ void __launch_bounds__(256) window_join_kernel(GradArgs a, int first,
 
 // How key tiles are cut.
 struct Cut {
-    int tiles, cut, pieces_cut, pieces;
+    int tiles, cut, pieces_cut, pieces, heavy, light;
     long long parts;  // pieces that leave sums, without and with those of the first tiles
     explicit Cut(const WindowShape& s) {
         const long long group = s.Hq / s.Hk, heads = (long long)s.B * s.Hk;
@@ -750,15 +776,15 @@ struct Cut {
         const long long reach = (C - 1 + (long long)s.window + C - 1) / C + 1, near_ = reach < tiles ? reach : tiles;
         const long long rest = tiles - cut, tail = rest < near_ ? rest : near_;  // of the others the last ones are seen by fewer
         const long long pairs = (long long)cut * tiles - (long long)cut * (cut - 1) / 2 + tail * (tail + 1) / 2 + (rest - tail) * near_;
-        // no piece longer than a third of a CTA's share, or shorter than 8 pairs, below which writing and adding its sums costs more;
-        // and those of the first tiles no longer than another tile is: CTAs take the same number of units (with pieces of 171 pairs
-        // and tiles of 36 the training step of 32768 tokens took 180 us longer)
-        long long most = heads * group * pairs / (3 * SMS);
-        if (most < 8) most = 8;
+        // No piece longer than a third of a CTA's share, those of the first tiles than an eighth; or shorter than 8 pairs, below which writing and adding its sums costs more.
+        const long long all = heads * group * pairs;
+        long long most = all / (3 * SMS) > 8 ? all / (3 * SMS) : 8;
         pieces = (int)((group * near_ + most - 1) / most);
-        if (most > group * near_) most = group * near_ > 8 ? group * near_ : 8;
+        most = all / (8 * SMS) > 8 ? all / (8 * SMS) : 8;
         pieces_cut = (int)((group * tiles + most - 1) / most);
-        if (cut == 0) pieces_cut = 1;
+        heavy = (int)((group * tiles + pieces_cut - 1) / pieces_cut);
+        light = (int)((group * near_ + pieces - 1) / pieces);
+        if (cut == 0) pieces_cut = 1, heavy = 0;
         parts = (pieces_cut > 1 ? heads * cut * pieces_cut : 0) + (pieces > 1 ? heads * (tiles - cut) * pieces : 0);
     }
 };
@@ -805,6 +831,8 @@ cudaError_t launch_bwd(const WindowArgs& x, cudaStream_t st) {
     if (cudaError_t e = launch<false, D>(maps, a, "window_dq_tc", st)) return e;
     const int heads = x.s.B * x.s.Hk, first = heads * cut.cut * cut.pieces_cut;
     a.units = first + heads * (cut.tiles - cut.cut) * cut.pieces;
+    a.heavy = cut.heavy;
+    a.light = cut.light;
     if (cudaError_t e = launch<true, D>(maps, a, "window_dkv_tc", st)) return e;
     const struct { int first, tiles, pieces, part0; } joins[2] = {
         {0, cut.cut, cut.pieces_cut, 0}, {cut.cut, cut.tiles - cut.cut, cut.pieces, cut.pieces_cut > 1 ? first : 0}};

@@ -128,7 +128,8 @@ def test_append_pointers(L):
     assert L.gdr_kv_append(append(Hq=0, pages=0), *put(11, p0=None, p8=None, p9=None, p10=None), None) == OK  # nowhere to write
 
 
-@pytest.mark.parametrize("kw,code", HEADS + [(dict(pages=-1), INVALID), (dict(page_size=0), INVALID), (dict(table_pages=-1), INVALID)])
+@pytest.mark.parametrize("kw,code", HEADS + [(dict(pages=-1), INVALID), (dict(page_size=0), INVALID), (dict(table_pages=-1), INVALID),
+                                             (dict(pages=1 << 20, page_size=1 << 12), UNSUPPORTED)])
 def test_paged_problem(L, kw, code):
     p = paged(**kw)
     assert L.gdr_paged_decode_step(p, *put(6), FAKE, BIG, None) == code
