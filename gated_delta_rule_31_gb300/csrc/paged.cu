@@ -13,7 +13,9 @@
 // exact to bf16 as any), which one vote tells; otherwise lanes exchange little. HBM bounds it: 4 operations a byte and head.
 // bf16: products by mma.m16n8k16 with the 8 heads as columns, S^T = K q^T and O^T += V^T P^T: the tokens are rows, so no row is
 // spent on heads that are not there, and a thread keeps the same two heads in S, m, l and O. (tcgen05 would take 128 rows
-// for the 8.) fp32: products on the CUDA cores, for S 32 channels of one token a lane, for O 4 channels of 8 tokens a lane.
+// for the 8.) 64 sequences of up to 16384 tokens, 8 key heads of 128: 2.1 GB in 335 us, 0.95 of a copy's rate; 128 with a window of 1024:
+// 90 us, 0.84; the sums of runs take 5 us of either, the lengths' sum and the first copies 5. Eight warps to a CTA and 152 runs: 340
+// and 99. fp32: products on the CUDA cores, for S 32 channels of one token a lane, for O 4 channels of 8 tokens a lane.
 //
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

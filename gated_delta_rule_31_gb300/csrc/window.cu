@@ -8,6 +8,8 @@
 //     dv = P^T do, dk = scale dS^T q over the queries that see a tile of keys, of all heads that share it.
 // The two walk the pairs separately, 7 products for the 5 that one walk would need, so that neither adds into
 // memory that another CTA adds into: the order of every sum is fixed.
+// Tiles come in asynchronously, one ahead; products by fp32 pairs. Bound by shared-memory reads (4 x 4 outputs a thread: 4 products
+// to a value read) and, at few tiles, by each CTA's chain: 2 x 777 tokens of 8 heads of 64, window 300: 61, 74 and 139 us.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
