@@ -313,34 +313,78 @@ __global__ void __launch_bounds__(THREADS) window_dq_kernel(WindowArgs a) {
     put_rows<D>(a.dq, s.T, s.Hq, b, h, t0, acc, f);
 }
 
-// SPLIT: a CTA for each query head, whose sums go to parts [2][B, T, Hq, D] (dk, dv), to be added by window_heads_kernel.
-template <int D, bool SPLIT>
-__global__ void __launch_bounds__(THREADS) window_dkv_kernel(WindowArgs a) {
+// A CTA for a piece of a tile of keys and the queries that see it (Cut): pieces of one leave their sums in parts, [2][N, D] each (dk,
+// dv), to be added by window_sum_kernel. Sums over more than 16 tiles of queries are kept in parts of 16 that are added up in memory,
+// so that a long sum's rounding stays that of a short one.
+struct CutArgs {
+    int tiles, cut, pieces_cut, pieces;
+    __device__ __forceinline__ int pieces_of(int tile) const { return tile < cut ? pieces_cut : pieces; }
+    // of piece 0 of a tile of head v (entry and key head) of `heads`
+    __device__ __forceinline__ long long part(int v, int tile, int heads) const {
+        if (tile < cut) return ((long long)v * cut + tile) * pieces_cut;
+        return (pieces_cut > 1 ? (long long)heads * cut * pieces_cut : 0) + ((long long)v * (tiles - cut) + tile - cut) * pieces;
+    }
+};
+
+// rows (+)= f acc
+template <int D>
+__device__ __forceinline__ void add_rows(float* rows, size_t stride, int live, const uint64_t (&acc)[4][D / 32], float f, bool add) {
+    using C = Cols<D>;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int r = threadIdx.x / 16 * 4 + i;
+        if (r >= live) continue;
+#pragma unroll
+        for (int g = 0; g < C::NW; g++)
+#pragma unroll
+            for (int c = 0; c < C::W; c += 2) {
+                float2* to = reinterpret_cast<float2*>(rows + r * stride + C::at(g) + c);
+                const float2 old = add ? *to : make_float2(0.f, 0.f);
+                float u, v;
+                unpair(acc[i][(g * C::W + c) / 2], u, v);
+                *to = make_float2(fmaf(f, u, old.x), fmaf(f, v, old.y));
+            }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS) window_dkv_kernel(WindowArgs a, CutArgs cut) {
     extern __shared__ __align__(16) float sh[];
     constexpr int TILE = tile_bytes<D>() / 4;
     float *K = sh, *V = K + TILE, *QG = V + TILE, *P = QG + 4 * TILE;  // P and then dS
     const WindowShape& s = a.s;
-    const int j0 = blockIdx.x * N, share = s.Hq / s.Hk, hk = SPLIT ? blockIdx.y / share : blockIdx.y, b = blockIdx.z, n = s.tokens(b);
-    const int first = SPLIT ? blockIdx.y : hk * share, group = SPLIT ? 1 : share;  // query heads of this CTA
+    const int of_cut = cut.cut * cut.pieces_cut, x = blockIdx.x, y = x - of_cut;
+    const int pieces = x < of_cut ? cut.pieces_cut : cut.pieces, kt = x < of_cut ? x / pieces : cut.cut + y / pieces;
+    const int piece = x < of_cut ? x - kt * pieces : y - (kt - cut.cut) * pieces;
+    const int j0 = kt * N, hk = blockIdx.y, b = blockIdx.z, group = s.Hq / s.Hk, n = s.tokens(b);
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    const int end = j0 < n ? queries_end(N, s.window, s.sinks, j0, n) : j0, per = (end - j0 + N - 1) / N, count = per * group;
+    const int end = j0 < n ? queries_end(N, s.window, s.sinks, j0, n) : j0, per = (end - j0 + N - 1) / N;
+    const int from = (int)((long long)per * group * piece / pieces), count = (int)((long long)per * group * (piece + 1) / pieces) - from;
+    int g = per ? from / per : 0, tile = from - g * per;
     auto load = [&](int it, int g, int tile) {
         if (it < count) {
-            load_tile<D>(QG + (it & 1) * 2 * TILE, a.q, s.T, s.Hq, b, first + g, j0 + tile * N, n);
-            load_tile<D>(QG + (it & 1) * 2 * TILE + TILE, a.do_, s.T, s.Hq, b, first + g, j0 + tile * N, n);
+            load_tile<D>(QG + (it & 1) * 2 * TILE, a.q, s.T, s.Hq, b, hk * group + g, j0 + tile * N, n);
+            load_tile<D>(QG + (it & 1) * 2 * TILE + TILE, a.do_, s.T, s.Hq, b, hk * group + g, j0 + tile * N, n);
         }
         cp_async_commit();
     };
     load_tile<D>(K, a.k, s.T, s.Hk, b, hk, j0, n);
     load_tile<D>(V, a.v, s.T, s.Hk, b, hk, j0, n);
-    load(0, 0, 0);
+    load(0, g, tile);
+    // where the sums go: rows of dk and dv, or of this piece's parts
+    const size_t row = (((size_t)b * s.T + j0) * s.Hk + hk) * D;
+    float* part = pieces > 1 ? a.parts + (size_t)(cut.part(b * s.Hk + hk, kt, s.B * s.Hk) + piece) * 2 * N * D : nullptr;
+    float* to_k = part ? part : static_cast<float*>(a.dk) + row;
+    float* to_v = part ? part + N * D : static_cast<float*>(a.dv) + row;
+    const size_t stride = part ? D : (size_t)s.Hk * D;
+    const int live = part ? N : s.T - j0;
     const float c = s.scale * 1.4426950408889634f;
     uint64_t dk[4][D / 32] = {}, dv[4][D / 32] = {};
-    int g = 0, tile = 0;
+    bool begun = false;
     for (int it = 0; it < count; it++) {
         const float *Q = QG + (it & 1) * 2 * TILE, *G = Q + TILE;
         const int t0 = j0 + tile * N;
-        const size_t rows = ((size_t)b * s.Hq + first + g) * s.T + t0;
+        const size_t rows = ((size_t)b * s.Hq + hk * group + g) * s.T + t0;
         if (++tile == per) {
             tile = 0;
             g++;
@@ -376,37 +420,41 @@ __global__ void __launch_bounds__(THREADS) window_dkv_kernel(WindowArgs a) {
             for (int j = 0; j < 4; j++) P[(4 * ty + i) * LP + tx + 16 * j] = dP[i][j];
         __syncwarp();
         rows_by_cols<D>(P, Q, dk);
+        if (it % 16 == 15 && it + 1 < count) {
+            add_rows<D>(to_k, stride, live, dk, s.scale, begun);
+            add_rows<D>(to_v, stride, live, dv, 1.f, begun);
+            begun = true;
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+#pragma unroll
+                for (int d = 0; d < D / 32; d++) dk[i][d] = dv[i][d] = 0;
+        }
     }
     cp_async_wait_all();
-    const float f[4] = {s.scale, s.scale, s.scale, s.scale}, one[4] = {1.f, 1.f, 1.f, 1.f};
-    if (SPLIT) {
-        put_rows<D>(a.parts, s.T, s.Hq, b, first, j0, dk, f);
-        put_rows<D>(a.parts + (size_t)s.B * s.T * s.Hq * D, s.T, s.Hq, b, first, j0, dv, one);
-    } else {
-        put_rows<D>(a.dk, s.T, s.Hk, b, hk, j0, dk, f);
-        put_rows<D>(a.dv, s.T, s.Hk, b, hk, j0, dv, one);
-    }
+    add_rows<D>(to_k, stride, live, dk, s.scale, begun);
+    add_rows<D>(to_v, stride, live, dv, 1.f, begun);
 }
 
-__global__ void __launch_bounds__(256) window_heads_kernel(WindowArgs a) {
+// The sums of the pieces of a tile, in order.
+__global__ void __launch_bounds__(256) window_sum_kernel(WindowArgs a, CutArgs cut) {
     const WindowShape& s = a.s;
-    const int share = s.Hq / s.Hk;
-    const size_t all = (size_t)s.B * s.T * s.Hk * s.D, i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4, row = i / s.D, d = i % s.D;
-    if (i >= all) return;
-#pragma unroll
-    for (int w = 0; w < 2; w++) {
-        const float* from = a.parts + w * all * share + row * share * s.D + d;
-        float4 x = get4(from);
-        for (int h = 1; h < share; h++) {
-            const float4 y = get4(from + (size_t)h * s.D);
-            x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+    const int kt = blockIdx.x, hk = blockIdx.y, b = blockIdx.z, pieces = cut.pieces_of(kt), rows = min(N, s.T - kt * N);
+    if (pieces == 1) return;
+    const float* part = a.parts + (size_t)cut.part(b * s.Hk + hk, kt, s.B * s.Hk) * 2 * N * s.D;
+    for (int w = 0; w < 2; w++)
+        for (int i = 4 * threadIdx.x; i < rows * s.D; i += 1024) {
+            float4 x = get4(part + (size_t)w * N * s.D + i);
+            for (int p = 1; p < pieces; p++) {
+                const float4 y = get4(part + (size_t)(2 * p + w) * N * s.D + i);
+                x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+            }
+            const int r = i / s.D, d = i - r * s.D;
+            *reinterpret_cast<float4*>(static_cast<float*>(w ? a.dv : a.dk) + (((size_t)b * s.T + kt * N + r) * s.Hk + hk) * s.D + d) = x;
         }
-        *reinterpret_cast<float4*>(static_cast<float*>(w ? a.dv : a.dk) + i) = x;
-    }
 }
 
-// By query heads where tiles of the key heads are too few for two CTAs on each SM.
-bool split_heads(const WindowShape& s) { return s.Hq > s.Hk && (long long)(s.T + N - 1) / N * s.Hk * s.B < 2 * 152; }
+// One CTA an SM (three of 32 channels); two pairs of tiles, some 25 us, are a piece at least.
+Cut cut_of(const WindowShape& s) { return Cut(s, N, s.D == 32 ? 3 * 152 : 152, 2); }
 
 template <typename K>
 cudaError_t launch(K kernel, const char* name, int heads, int smem, const WindowArgs& a, cudaStream_t st) {
@@ -431,11 +479,16 @@ template <int D>
 cudaError_t bwd(const WindowArgs& a, cudaStream_t st) {
     if (cudaError_t e = launch(window_dq_kernel<D>, "window_dq", a.s.Hq, 6 * tile_bytes<D>() + N * LP * 4, a, st)) return e;
     const int smem = 6 * tile_bytes<D>() + N * LP * 4;
-    if (!split_heads(a.s)) return launch(window_dkv_kernel<D, false>, "window_dkv", a.s.Hk, smem, a, st);
-    if (cudaError_t e = launch(window_dkv_kernel<D, true>, "window_dkv", a.s.Hq, smem, a, st)) return e;
-    const size_t values = (size_t)a.s.B * a.s.T * a.s.Hk * D;
-    trace_begin("window_heads", st);
-    window_heads_kernel<<<(unsigned)((values + 1023) / 1024), 256, 0, st>>>(a);
+    if (cudaError_t e = cudaFuncSetAttribute(window_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
+    const Cut cut = cut_of(a.s);
+    const CutArgs c{cut.tiles, cut.cut, cut.pieces_cut, cut.pieces};
+    trace_begin("window_dkv", st);
+    window_dkv_kernel<D><<<dim3(cut.cut * cut.pieces_cut + (cut.tiles - cut.cut) * cut.pieces, a.s.Hk, a.s.B), THREADS, smem, st>>>(a, c);
+    trace_end(st);
+    if (cudaError_t e = cudaGetLastError()) return e;
+    if (cut.parts == 0) return cudaSuccess;
+    trace_begin("window_sum", st);
+    window_sum_kernel<<<dim3(cut.tiles, a.s.Hk, a.s.B), 256, 0, st>>>(a, c);
     trace_end(st);
     return cudaGetLastError();
 }
@@ -444,7 +497,7 @@ cudaError_t bwd(const WindowArgs& a, cudaStream_t st) {
 
 size_t window_parts_bytes(const WindowShape& s) {
     if (s.bf16) return window_parts_bytes_tc(s);
-    return split_heads(s) ? 2 * (size_t)s.B * s.T * s.Hq * s.D * sizeof(float) : 0;
+    return s.B > 0 ? (size_t)cut_of(s).parts * 2 * N * s.D * sizeof(float) : 0;
 }
 
 cudaError_t launch_window_fwd(const WindowArgs& a, cudaStream_t st) {

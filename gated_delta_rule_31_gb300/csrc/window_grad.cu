@@ -770,31 +770,6 @@ __global__ void __launch_bounds__(256) window_join_kernel(GradArgs a, int first,
     }
 }
 
-// How key tiles are cut.
-struct Cut {
-    int tiles, cut, pieces_cut, pieces, heavy, light;
-    long long parts;  // pieces that leave sums, without and with those of the first tiles
-    explicit Cut(const WindowShape& s) {
-        const long long group = s.Hq / s.Hk, heads = (long long)s.B * s.Hk;
-        tiles = (s.T + C - 1) / C;
-        // a tile that holds first tokens is seen by all later queries, others by those within the window
-        cut = s.window < s.T ? (s.sinks + C - 1) / C : 0;
-        const long long reach = (C - 1 + (long long)s.window + C - 1) / C + 1, near_ = reach < tiles ? reach : tiles;
-        const long long rest = tiles - cut, tail = rest < near_ ? rest : near_;  // of the others the last ones are seen by fewer
-        const long long pairs = (long long)cut * tiles - (long long)cut * (cut - 1) / 2 + tail * (tail + 1) / 2 + (rest - tail) * near_;
-        // No piece longer than a third of a CTA's share, those of the first tiles than an eighth; or shorter than 8 pairs, below which writing and adding its sums costs more.
-        const long long all = heads * group * pairs;
-        long long most = all / (3 * SMS) > 8 ? all / (3 * SMS) : 8;
-        pieces = (int)((group * near_ + most - 1) / most);
-        most = all / (8 * SMS) > 8 ? all / (8 * SMS) : 8;
-        pieces_cut = (int)((group * tiles + most - 1) / most);
-        heavy = (int)((group * tiles + pieces_cut - 1) / pieces_cut);
-        light = (int)((group * near_ + pieces - 1) / pieces);
-        if (cut == 0) pieces_cut = 1, heavy = 0;
-        parts = (pieces_cut > 1 ? heads * cut * pieces_cut : 0) + (pieces > 1 ? heads * (tiles - cut) * pieces : 0);
-    }
-};
-
 // Before the tensor maps: the first runtime call of a host thread makes the device's context current there.
 template <int D>
 cudaError_t allow_smem() {
@@ -818,7 +793,7 @@ cudaError_t launch_bwd(const WindowArgs& x, cudaStream_t st) {
     if (!rows_map(&maps[0], x.q, x.s, x.s.Hq) || !rows_map(&maps[1], x.k, x.s, x.s.Hk) || !rows_map(&maps[2], x.v, x.s, x.s.Hk) ||
         !rows_map(&maps[3], x.do_, x.s, x.s.Hq))
         return cudaErrorInvalidValue;
-    const Cut cut(x.s);
+    const Cut cut(x.s, C, SMS, 8);
     GradArgs a = {};
     a.s = x.s;
     a.tiles = cut.tiles;
@@ -855,7 +830,7 @@ cudaError_t launch_bwd(const WindowArgs& x, cudaStream_t st) {
 }  // namespace
 
 size_t window_parts_bytes_tc(const WindowShape& s) {
-    return s.B > 0 && s.T > 0 ? (size_t)Cut(s).parts * 2 * C * s.D * sizeof(float) : 0;
+    return s.B > 0 && s.T > 0 ? (size_t)Cut(s, C, SMS, 8).parts * 2 * C * s.D * sizeof(float) : 0;
 }
 
 cudaError_t launch_window_bwd_tc(const WindowArgs& x, cudaStream_t st) {

@@ -10,6 +10,33 @@ inline bool rows_map(CUtensorMap* m, const void* p, const WindowShape& s, int H)
     return make_map_4d_bf16(m, p, s.D, H, s.T, s.B, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// How the walks over the queries that see a tile of N keys are cut for dk and dv: a list of (head, tile of queries) pairs for each key
+// tile. First tokens are seen by all later queries, others within the window.
+struct Cut {
+    int tiles, cut;             // key tiles, those that hold first tokens
+    int pieces_cut, pieces;     // pieces of these, and of the others
+    int heavy, light;           // pairs of such a piece; heavy 0: no first tokens
+    long long parts;            // pieces that leave sums
+    // No piece longer than a third of the share of one of `ctas` CTAs, those of the first tokens than an eighth; or shorter than `least`
+    // pairs, below which writing and adding its sums costs more.
+    Cut(const WindowShape& s, int N, int ctas, int least) {
+        const long long group = s.Hq / s.Hk, heads = (long long)s.B * s.Hk;
+        tiles = (s.T + N - 1) / N;
+        cut = s.window < s.T ? (s.sinks + N - 1) / N : 0;
+        const long long reach = (N - 1 + (long long)s.window + N - 1) / N + 1, near_ = reach < tiles ? reach : tiles;
+        const long long rest = tiles - cut, tail = rest < near_ ? rest : near_;  // of the others the last ones are seen by fewer
+        const long long pairs = (long long)cut * tiles - (long long)cut * (cut - 1) / 2 + tail * (tail + 1) / 2 + (rest - tail) * near_;
+        const long long all = heads * group * pairs;
+        long long most = all / (3 * ctas) > least ? all / (3 * ctas) : least;
+        pieces = (int)((group * near_ + most - 1) / most);
+        most = all / (8 * ctas) > least ? all / (8 * ctas) : least;
+        pieces_cut = cut ? (int)((group * tiles + most - 1) / most) : 1;
+        heavy = cut ? (int)((group * tiles + pieces_cut - 1) / pieces_cut) : 0;
+        light = (int)((group * near_ + pieces - 1) / pieces);
+        parts = (pieces_cut > 1 ? heads * cut * pieces_cut : 0) + (pieces > 1 ? heads * rest * pieces : 0);
+    }
+};
+
 cudaError_t launch_window_fwd_tc(const WindowArgs& a, cudaStream_t st);
 size_t window_parts_bytes_tc(const WindowShape& s);
 cudaError_t launch_window_bwd_tc(const WindowArgs& a, cudaStream_t st);

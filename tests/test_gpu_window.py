@@ -238,3 +238,18 @@ def test_a_saved_output_that_a_call_overwrites_is_noticed():
     gdr.window_attention_fwd(d["do"], d["k"], d["v"], out=o.detach())
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.backward()
+
+
+def test_long_sums_of_gradients_keep_their_precision():
+    """fp32: a key that thousands of queries see. Its gradients, sums of as many terms of either sign, are off by at most
+    256 x 2^-24 of what a sum of terms of one sign would be, as shorter ones are."""
+    dev = cuda_device()
+    d = make(1, 6000, 2, 1, 32, torch.float32, seed=1)
+    ref = attention(**d, window=64, sinks=3)
+    x = to_dev(d, dev)
+    o, lse, _ = gdr.window_attention_fwd(x["q"], x["k"], x["v"], window=64, sinks=3, save_lse=True)
+    gr = gdr.window_attention_bwd(x["q"], x["k"], x["v"], o, lse, x["do"], window=64, sinks=3)
+    for n in ("dq", "dk", "dv"):
+        assert rel_heads(gr[n], ref[n], 2) <= TOL["fp32"][n]
+    # the first tokens alone: 12000 terms each
+    assert rel(gr["dv"][0, :3], ref["dv"][0, :3]) <= 32 * 2.0 ** -24 and rel(gr["dk"][0, :3], ref["dk"][0, :3]) <= 32 * 2.0 ** -24
