@@ -81,6 +81,12 @@ __device__ __forceinline__ void product_sum64(uint32_t d, uint32_t p, uint32_t b
         if (16 * k < rows) mma_ts(d, p + 8 * k, blo + step_mnmajor(k), idesc, k > 0 || !begin);
 }
 
+// Weights as operands: one bf16 term, or two (2^-17 off) for sequences of up to 64 tokens, whose queries see too few keys for the
+// roundings to average out and whose time is the launch's (dq of pairs of tokens off by 0.0017 of its norm, 0.0025 with one term). The
+// second terms lie in the columns that the first leave free over the fp32 values.
+constexpr int kTwoTerms = 64;
+__device__ __forceinline__ uint32_t second_term(uint32_t first, float lo, float hi) { return pack_bf16(lo - bf16lo(first), hi - bf16hi(first)); }
+
 // Whether every query of t0 .. t0 + 127 sees every key of j0 .. j0 + 127.
 __device__ __forceinline__ bool all_seen(const WindowShape& s, int t0, int j0, int n) {
     return j0 + C - 1 <= t0 && t0 + C <= n && (t0 + C - 1 - j0 < s.window || j0 + C <= s.sinks);

@@ -28,7 +28,7 @@
 //
 // Where a key tile's queries are many (first tokens that all see) or the units few, a key tile is cut: its pieces leave fp32 sums,
 // which a third kernel adds in order.
-// Rounding to bf16: P and dS as operands, and the results.
+// Rounding to bf16: P and dS as operands (kTwoTerms), and the results.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -207,7 +207,8 @@ struct Bars {
     uint64_t lfull[2], lfree[2];  // dkv: statistics
 };
 
-// 64 columns as bf16 to TMEM
+// 64 columns as bf16 to TMEM, the second terms 32 columns on
+template <int TERMS>
 __device__ __forceinline__ void put_half(uint32_t at, const float (&x)[64]) {
 #pragma unroll
     for (int e = 0; e < 2; e++) {
@@ -215,10 +216,15 @@ __device__ __forceinline__ void put_half(uint32_t at, const float (&x)[64]) {
 #pragma unroll
         for (int k = 0; k < 16; k++) w[k] = pack_bf16(x[32 * e + 2 * k], x[32 * e + 2 * k + 1]);
         tmem_st16(at + 16 * e, w);
+        if (TERMS == 2) {
+#pragma unroll
+            for (int k = 0; k < 16; k++) w[k] = second_term(w[k], x[32 * e + 2 * k], x[32 * e + 2 * k + 1]);
+            tmem_st16(at + 32 + 16 * e, w);
+        }
     }
 }
 
-template <bool KEYS, int D>
+template <bool KEYS, int D, int TERMS>
 __global__ void __launch_bounds__(THREADS, 1)
     window_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                        const __grid_constant__ CUtensorMap mg, const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap mr,
@@ -378,6 +384,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const uint32_t d = tm + (w ? COL_SUM : COL_V), bd = lo_mnmajor(slot(at));
                     product_sum64(d, tm + from, bd, id_o, cur.m, cur.first);
                     product_sum64(d, tm + from + 64, bd + step_mnmajor(4), id_o, cur.m - 64, false);
+                    if (TERMS == 2) {
+                        product_sum64(d, tm + from + 32, bd, id_o, cur.m, false);
+                        product_sum64(d, tm + from + 96, bd + step_mnmajor(4), id_o, cur.m - 64, false);
+                    }
                     done(at);
                 };
                 issue(0, cur, 0);
@@ -430,6 +440,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             issue(0, h, ring + 2);
                         }
                         product_sum64(tm + COL_SUM, tm + COL_DP + 64 * h, lo_mnmajor(slot(ring)) + h * step_mnmajor(4), id_o, cur.m - 64 * h, cur.first && h == 0);
+                        if (TERMS == 2) product_sum64(tm + COL_SUM, tm + COL_DP + 64 * h + 32, lo_mnmajor(slot(ring)) + h * step_mnmajor(4), id_o, cur.m - 64 * h, false);
                         if (h == 1) {
                             done(ring);
                             if (cur.last) commit(&bar.sumfull);
@@ -650,7 +661,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
                 if (KEYS) {
-                    put_half(at_s, p);
+                    put_half<TERMS>(at_s, p);
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
@@ -678,7 +689,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         unpair(mul2(pair(q[2], q[3]), add2(pair(d[4 * k + 2], d[4 * k + 3]), d1)), q[2], q[3]);
                     }
                 }
-                put_half(at_dp, p);
+                put_half<TERMS>(at_dp, p);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -771,23 +782,23 @@ __global__ void __launch_bounds__(256) window_join_kernel(GradArgs a, int first,
 }
 
 // Before the tensor maps: the first runtime call of a host thread makes the device's context current there.
-template <int D>
+template <int D, int TERMS>
 cudaError_t allow_smem() {
-    if (cudaError_t e = cudaFuncSetAttribute(window_grad_kernel<false, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES)) return e;
-    return cudaFuncSetAttribute(window_grad_kernel<true, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+    if (cudaError_t e = cudaFuncSetAttribute(window_grad_kernel<false, D, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES)) return e;
+    return cudaFuncSetAttribute(window_grad_kernel<true, D, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
 }
 
-template <bool KEYS, int D>
+template <bool KEYS, int D, int TERMS>
 cudaError_t launch(const CUtensorMap* maps, const GradArgs& a, const char* name, cudaStream_t st) {
     trace_begin(name, st);
-    window_grad_kernel<KEYS, D><<<(unsigned)(a.units < SMS ? a.units : SMS), THREADS, BYTES, st>>>(maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], a);
+    window_grad_kernel<KEYS, D, TERMS><<<(unsigned)(a.units < SMS ? a.units : SMS), THREADS, BYTES, st>>>(maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], a);
     trace_end(st);
     return cudaGetLastError();
 }
 
-template <int D>
+template <int D, int TERMS>
 cudaError_t launch_bwd(const WindowArgs& x, cudaStream_t st) {
-    if (cudaError_t e = allow_smem<D>()) return e;
+    if (cudaError_t e = allow_smem<D, TERMS>()) return e;
     CUtensorMap maps[6];
     if (!rows_map(&maps[4], x.o, x.s, x.s.Hq) || !rows_map(&maps[5], x.rest ? x.rest : x.o, x.s, x.s.Hq)) return cudaErrorInvalidValue;
     if (!rows_map(&maps[0], x.q, x.s, x.s.Hq) || !rows_map(&maps[1], x.k, x.s, x.s.Hk) || !rows_map(&maps[2], x.v, x.s, x.s.Hk) ||
@@ -809,12 +820,12 @@ cudaError_t launch_bwd(const WindowArgs& x, cudaStream_t st) {
     a.parts = x.parts;
     a.status = x.status;
     a.units = x.s.B * x.s.Hq * cut.tiles;
-    if (cudaError_t e = launch<false, D>(maps, a, "window_dq_tc", st)) return e;
+    if (cudaError_t e = launch<false, D, TERMS>(maps, a, "window_dq_tc", st)) return e;
     const int heads = x.s.B * x.s.Hk, first = heads * cut.cut * cut.pieces_cut;
     a.units = first + heads * (cut.tiles - cut.cut) * cut.pieces;
     a.heavy = cut.heavy;
     a.light = cut.light;
-    if (cudaError_t e = launch<true, D>(maps, a, "window_dkv_tc", st)) return e;
+    if (cudaError_t e = launch<true, D, TERMS>(maps, a, "window_dkv_tc", st)) return e;
     const struct { int first, tiles, pieces, part0; } joins[2] = {
         {0, cut.cut, cut.pieces_cut, 0}, {cut.cut, cut.tiles - cut.cut, cut.pieces, cut.pieces_cut > 1 ? first : 0}};
     for (const auto& j : joins) {
@@ -834,7 +845,8 @@ size_t window_parts_bytes_tc(const WindowShape& s) {
 }
 
 cudaError_t launch_window_bwd_tc(const WindowArgs& x, cudaStream_t st) {
-    return x.s.D == 32 ? launch_bwd<32>(x, st) : x.s.D == 64 ? launch_bwd<64>(x, st) : launch_bwd<128>(x, st);
+    if (x.s.T <= kTwoTerms) return x.s.D == 32 ? launch_bwd<32, 2>(x, st) : x.s.D == 64 ? launch_bwd<64, 2>(x, st) : launch_bwd<128, 2>(x, st);
+    return x.s.D == 32 ? launch_bwd<32, 1>(x, st) : x.s.D == 64 ? launch_bwd<64, 1>(x, st) : launch_bwd<128, 1>(x, st);
 }
 
 }  // namespace gdr

@@ -12,7 +12,7 @@
 // order P0 V, the next S0, P1 V, the next S1. m is moved, and O and l scaled by 2^(c m - c m'), only when the row's
 // maximum has grown by more than 8 / c: until then P is at most 2^8, as exact in bf16 as below one, and the sums in
 // fp32 have the room; most tiles then need no pass over O. The order of tiles and units is fixed by the shape.
-// Rounding to bf16: P, and the result (what that leaves may be kept for the VJP).
+// Rounding to bf16: P (kTwoTerms), and the result (what that leaves may be kept for the VJP).
 //
 // Warps 0-3 and 4-7 take the query tiles, 8 copies tiles in (Q of the next unit as soon as the last S of this one has read it,
 // K and V in a ring of four slots), 9 issues the products. The stream of tiles runs through the units without a
@@ -90,7 +90,7 @@ __device__ __forceinline__ int unit_of(int round) {
     return round * (int)gridDim.x + (int)(round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
 
-template <int D>
+template <int D, int TERMS>
 __global__ void __launch_bounds__(THREADS, 1)
     window_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                          const __grid_constant__ CUtensorMap mv, FwdArgs a) {
@@ -258,6 +258,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (ok) {
                             tc_fence_after();
                             product_sum64(tm + COL_O + 128 * w, tm + COL_S + 128 * w, bd, id_o, m, begin[w]);
+                            if (TERMS == 2) {
+                                product_sum64(tm + COL_O + 128 * w, tm + COL_S + 128 * w + 64, bd, id_o, m, false);
+                                product_sum64(tm + COL_O + 128 * w, tm + COL_S + 128 * w + 96, bd + step_mnmajor(4), id_o, m - 64, false);
+                            }
                             product_sum64(tm + COL_O + 128 * w, tm + COL_S + 128 * w + 32, bd + step_mnmajor(4), id_o, m - 64, false);
                             commit(&ofull[w][np[w] & 1]);
                         }
@@ -346,7 +350,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 uint64_t sum[2] = {0, 0};
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
-                    uint32_t w[16];
+                    uint32_t w[16], w2[TERMS == 2 ? 16 : 1];
 #pragma unroll
                     for (int k = 0; k < 16; k++) {
                         float p0, p1;
@@ -355,8 +359,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                         p1 = exp2_fast(p1);
                         sum[k & 1] = add2(sum[k & 1], pair(p0, p1));
                         w[k] = pack_bf16(p0, p1);
+                        if (TERMS == 2) w2[k] = second_term(w[k], p0, p1);
                     }
                     tmem_st16(at_s + 16 * e, w);
+                    if (TERMS == 2) tmem_st16(at_s + 64 + 16 * e, w2);
                 }
                 float s0, s1;
                 unpair(add2(sum[0], sum[1]), s0, s1);
@@ -438,10 +444,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == 8) tmem_dealloc(tm, 512);
 }
 
-template <int D>
+template <int D, int TERMS>
 cudaError_t launch_fwd(const WindowArgs& x, cudaStream_t st) {
     // before the tensor maps: the first runtime call of a host thread makes the device's context current there
-    if (cudaError_t e = cudaFuncSetAttribute(window_fwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES)) return e;
+    if (cudaError_t e = cudaFuncSetAttribute(window_fwd_tc_kernel<D, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES)) return e;
     CUtensorMap mq, mk, mv;
     if (!rows_map(&mq, x.q, x.s, x.s.Hq) || !rows_map(&mk, x.k, x.s, x.s.Hk) || !rows_map(&mv, x.v, x.s, x.s.Hk)) return cudaErrorInvalidValue;
     FwdArgs a = {};
@@ -454,7 +460,7 @@ cudaError_t launch_fwd(const WindowArgs& x, cudaStream_t st) {
     a.rest = x.rest;
     a.status = x.status;
     trace_begin("window_fwd_tc", st);
-    window_fwd_tc_kernel<D><<<(unsigned)(a.units < SMS ? a.units : SMS), THREADS, BYTES, st>>>(mq, mk, mv, a);
+    window_fwd_tc_kernel<D, TERMS><<<(unsigned)(a.units < SMS ? a.units : SMS), THREADS, BYTES, st>>>(mq, mk, mv, a);
     trace_end(st);
     return cudaGetLastError();
 }
@@ -462,7 +468,8 @@ cudaError_t launch_fwd(const WindowArgs& x, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_window_fwd_tc(const WindowArgs& x, cudaStream_t st) {
-    return x.s.D == 32 ? launch_fwd<32>(x, st) : x.s.D == 64 ? launch_fwd<64>(x, st) : launch_fwd<128>(x, st);
+    if (x.s.T <= kTwoTerms) return x.s.D == 32 ? launch_fwd<32, 2>(x, st) : x.s.D == 64 ? launch_fwd<64, 2>(x, st) : launch_fwd<128, 2>(x, st);
+    return x.s.D == 32 ? launch_fwd<32, 1>(x, st) : x.s.D == 64 ? launch_fwd<64, 1>(x, st) : launch_fwd<128, 1>(x, st);
 }
 
 }  // namespace gdr

@@ -253,3 +253,18 @@ def test_long_sums_of_gradients_keep_their_precision():
         assert rel_heads(gr[n], ref[n], 2) <= TOL["fp32"][n]
     # the first tokens alone: 12000 terms each
     assert rel(gr["dv"][0, :3], ref["dv"][0, :3]) <= 32 * 2.0 ** -24 and rel(gr["dk"][0, :3], ref["dk"][0, :3]) <= 32 * 2.0 ** -24
+
+
+def test_few_tokens_round_once():
+    """bf16, up to 64 tokens: the weights enter to 2^-17, so each result is off by its own rounding, 2^-8 at most, alone."""
+    dev = cuda_device()
+    for T in (2, 3, 20, 64):
+        d = make(4, T, 4, 2, 64, torch.bfloat16, seed=T)
+        ref = attention(**d)
+        x = to_dev(d, dev)
+        o, lse, rest = gdr.window_attention_fwd(x["q"], x["k"], x["v"], save_lse=True)
+        gr = gdr.window_attention_bwd(x["q"], x["k"], x["v"], o, lse, x["do"], rest=rest)
+        for n, y in dict(o=o, **gr).items():
+            off = float((y.double().cpu() - ref[n]).norm() / ref[n].norm())
+            # a rounding's error is spread evenly over its step: 1 / sqrt 3 of the most, with room for few values
+            assert off <= 0.75 * 2.0 ** -8, (T, n, off)
