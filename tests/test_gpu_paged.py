@@ -236,3 +236,34 @@ def test_refusals():
         with pytest.raises(gdr.GdrError) as e:
             call()
         assert e.value.code == code
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_caches_on_the_16_byte_grid_only(dtype):
+    dev = cuda_device()
+    q, kc, vc, table, n = make(2, [70, 33], 4, 2, 64, 16, TYPES[dtype], seed=10)
+    ref = decode(q, kc, vc, table, n)
+    step = 16 // TYPES[dtype].itemsize
+
+    def view(x, by):
+        flat = torch.empty(x.numel() + 64, dtype=x.dtype, device=dev)
+        y = flat[by:by + x.numel()].view(x.shape)
+        y.copy_(x)
+        return y
+
+    args = table.to(dev), n.to(dev)
+    assert rel_heads(gdr.paged_decode_step(view(q, step), view(kc, step), view(vc, 3 * step), *args), ref, 1) <= TOL[dtype]
+    for bad in ((1, 0, 0), (0, 1, 0), (0, 0, 1)):
+        with pytest.raises(gdr.GdrError) as e:
+            gdr.paged_decode_step(view(q, bad[0]), view(kc, bad[1]), view(vc, bad[2]), *args)
+        assert e.value.code == 1
+
+
+def test_rows_behind_the_last_sequence_stay_as_they_were():
+    """Outputs in the first rows of a larger buffer."""
+    dev = cuda_device()
+    for B in (3, 50):
+        q, kc, vc, table, n = (t.to(dev) for t in make(B, [30 + i for i in range(B)], 4, 2, 64, 16, torch.bfloat16, seed=11))
+        buf = torch.full((B + 2, 4, 64), 3.0, dtype=torch.bfloat16, device=dev)
+        o = gdr.paged_decode_step(q, kc, vc, table, n, out=buf[:B])
+        assert torch.equal(o, gdr.paged_decode_step(q, kc, vc, table, n)) and (buf[B:] == 3.0).all()

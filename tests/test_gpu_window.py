@@ -268,3 +268,74 @@ def test_few_tokens_round_once():
             off = float((y.double().cpu() - ref[n]).norm() / ref[n].norm())
             # a rounding's error is spread evenly over its step: 1 / sqrt 3 of the most, with room for few values
             assert off <= 0.75 * 2.0 ** -8, (T, n, off)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_tensors_on_the_16_byte_grid_only(dtype):
+    """Views that begin 16 bytes into their storage, and ones off the grid, which are refused."""
+    dev = cuda_device()
+    d = make(2, 130, 4, 2, 64, TYPES[dtype], seed=12)
+    ref = attention(**d, window=50, sinks=1)
+    step = 16 // TYPES[dtype].itemsize
+
+    def view(x, by):
+        flat = torch.empty(x.numel() + 64, dtype=x.dtype, device=dev)
+        y = flat[by:by + x.numel()].view(x.shape)
+        y.copy_(x)
+        return y
+
+    q, k, v, do = (view(d[n], step) for n in ("q", "k", "v", "do"))
+    out = view(torch.zeros_like(d["q"]), 3 * step)
+    o, lse, rest = gdr.window_attention_fwd(q, k, v, window=50, sinks=1, save_lse=True, out=out)
+    assert o is out
+    gr = gdr.window_attention_bwd(q, k, v, o, lse, do, window=50, sinks=1, rest=rest)
+    for n, y in dict(o=o, **gr).items():
+        close(y, ref, n, dtype)
+    with pytest.raises(gdr.GdrError) as e:
+        gdr.window_attention_fwd(view(d["q"], 1), k, v)
+    assert e.value.code == 1
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_many_short_sequences(dtype):
+    n = [(i * 7) % 6 for i in range(700)]
+    check(make(700, 5, 3, 1, 32, TYPES[dtype], lengths=n, seed=13), dtype, cuda_device(), window=3, sinks=1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_workspaces_of_earlier_calls_and_two_graphs(dtype):
+    """Whatever a workspace holds; and two captured calls that share one, replayed one after the other."""
+    dev = cuda_device()
+    xs = [to_dev(make(1, 400, 4, 2, 64, TYPES[dtype], seed=s), dev) for s in (14, 15)]
+    kw = dict(window=100, sinks=5)
+    ws = torch.full((1 << 24,), 255, dtype=torch.uint8, device=dev)
+
+    def both(x, w=None):
+        o, lse, rest = gdr.window_attention_fwd(x["q"], x["k"], x["v"], save_lse=True, workspace=w, **kw)
+        return (o, *gdr.window_attention_bwd(x["q"], x["k"], x["v"], o, lse, x["do"], rest=rest, workspace=w, **kw).values())
+
+    want = [both(x) for x in xs]
+    graphs, got = [torch.cuda.CUDAGraph() for _ in xs], []
+    for g, x in zip(graphs, xs):
+        with torch.cuda.graph(g):
+            got.append(both(x, ws))
+    for order in ((0, 1), (1, 0)):
+        for i in order:
+            graphs[i].replay()
+        for a, b in zip(got, want):
+            assert all(torch.equal(u, w) for u, w in zip(a, b))
+
+
+def test_lengths_that_change_between_replays():
+    dev = cuda_device()
+    d = to_dev(make(2, 300, 2, 1, 64, torch.bfloat16, seed=16), dev)
+    n = torch.tensor([300, 10], dtype=torch.int32, device=dev)
+    graph = torch.cuda.CUDAGraph()
+    f = lambda: gdr.window_attention_fwd(d["q"], d["k"], d["v"], lengths=n, window=64)[0]  # noqa: E731
+    f()
+    with torch.cuda.graph(graph):
+        o = f()
+    for lengths in ([300, 10], [0, 300], [129, 1]):
+        n.copy_(torch.tensor(lengths, dtype=torch.int32))
+        graph.replay()
+        assert torch.equal(o, f())
