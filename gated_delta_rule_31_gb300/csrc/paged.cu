@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) paged_kernel(PagedArgs 
                 sum = fmaf(f, from[w * HEADS * (D + 2) + D + 1], sum);
             }
             if (out.whole) {
-                put(static_cast<T*>(a.o) + (q0 + g) * D + d, sum > 0.f ? x / sum : 0.f);
+                put(static_cast<T*>(a.o) + (q0 + g) * D + d, sum == 0.f ? 0.f : x / sum);
             } else {
                 part[g * (D + 2) + d] = x;
                 if (d == 0) {
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) paged_kernel(PagedArgs 
                     x = fmaf(f, xr[r], x);
                     sum = fmaf(f, lr[r], sum);
                 }
-                put(static_cast<T*>(a.o) + (q0 + g) * D + d, sum > 0.f ? x / sum : 0.f);
+                put(static_cast<T*>(a.o) + (q0 + g) * D + d, sum == 0.f ? 0.f : x / sum);
             }
             cluster_sync();  // the others have read this CTA's
             return;
@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(PagedArgs a, i
         for (int i = lane; i < n; i += 32) {
             const float m = weight[g][i], f = m == -INFINITY ? 0.f : exp2f(m - top);
             weight[g][i] = f;
-            if (f != 0.f) all = fmaf(f, a.parts[((size_t)slot[i] * HEADS + g) * (D + 2) + D + 1], all);
+            if (slot[i] >= 0) all = fmaf(f, a.parts[((size_t)slot[i] * HEADS + g) * (D + 2) + D + 1], all);
         }
         all = warp_sum(all);
         if (lane == 0) sum[g] = all;
@@ -589,8 +589,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(PagedArgs a, i
         float x = 0.f;
 #pragma unroll 4
         for (int i = part; i < n; i += JOIN_GROUPS) {
-            const float f = weight[g][i];
-            if (f != 0.f) x = fmaf(f, a.parts[((size_t)slot[i] * HEADS + g) * (D + 2) + d], x);  // a run without tokens left no sums
+            if (slot[i] >= 0) x = fmaf(weight[g][i], a.parts[((size_t)slot[i] * HEADS + g) * (D + 2) + d], x);
         }
         acc[part][g][d] = x;
     }
@@ -598,7 +597,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(PagedArgs a, i
     for (int e = tid; e < ng * D; e += JOIN_THREADS) {
         const int g = e / D, d = e % D;
         const float x = (acc[0][g][d] + acc[1][g][d]) + (acc[2][g][d] + acc[3][g][d]);
-        put(static_cast<T*>(a.o) + (q0 + g) * D + d, sum[g] > 0.f ? x / sum[g] : 0.f);
+        put(static_cast<T*>(a.o) + (q0 + g) * D + d, sum[g] == 0.f ? 0.f : x / sum[g]);
     }
 }
 

@@ -230,13 +230,13 @@ __global__ void __launch_bounds__(THREADS) window_fwd_kernel(WindowArgs a) {
     cp_async_wait_all();
     float f[4];
 #pragma unroll
-    for (int i = 0; i < 4; i++) f[i] = l[i] == 0.f ? 0.f : 1.f / l[i];
+    for (int i = 0; i < 4; i++) f[i] = t0 + 4 * ty + i < n ? 1.f / l[i] : 0.f;
     put_rows<D>(a.o, s.T, s.Hq, b, h, t0, acc, f);
     if (a.lse && tx == 0)
 #pragma unroll
         for (int i = 0; i < 4; i++)
             if (t0 + 4 * ty + i < s.T)
-                a.lse[((size_t)b * s.Hq + h) * s.T + t0 + 4 * ty + i] = l[i] == 0.f ? -INFINITY : 0.6931471805599453f * m[i] + logf(l[i]);
+                a.lse[((size_t)b * s.Hq + h) * s.T + t0 + 4 * ty + i] = t0 + 4 * ty + i < n ? 0.6931471805599453f * m[i] + logf(l[i]) : -INFINITY;
 }
 
 // delta [B, Hq, T]: 8 lanes a row.

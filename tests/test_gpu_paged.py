@@ -267,3 +267,29 @@ def test_rows_behind_the_last_sequence_stay_as_they_were():
         buf = torch.full((B + 2, 4, 64), 3.0, dtype=torch.bfloat16, device=dev)
         o = gdr.paged_decode_step(q, kc, vc, table, n, out=buf[:B])
         assert torch.equal(o, gdr.paged_decode_step(q, kc, vc, table, n)) and (buf[B:] == 3.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("B", [2, 60])
+def test_values_that_are_none_are_not_hidden(B, dtype):
+    """NaN in a query, a key or a value that is seen reaches the output, of that head alone; infinite keys as in the formula."""
+    dev = cuda_device()
+    q, kc, vc, table, n = make(B, [900 + b for b in range(B)], 4, 2, 64, 16, TYPES[dtype], seed=12)
+    ref = decode(q, kc, vc, table, n)
+    q[0, 1] = float("nan")
+    page = table[1].long()
+    kc[page[3], 5, 0, 7] = float("nan")  # heads 0 and 1 of entry 1
+    vc[page[50], 2, 1, 3] = float("nan")  # heads 2 and 3, channel 3
+    o = gdr.paged_decode_step(*(t.to(dev) for t in (q, kc, vc, table, n)))
+    bad = torch.zeros(B, 4, 64, dtype=torch.bool, device=dev)
+    bad[0, 1] = bad[1, :2] = bad[1, 2:, 3] = True
+    assert torch.equal(o.isnan(), bad)
+    bad = bad.cpu()
+    bad[0, 1] = bad[1, 2:] = True  # whole heads, as the bound is one on heads
+    good = ~bad[..., 0].flatten()
+    assert rel_heads(o.flatten(0, 1)[good.to(dev)], ref.flatten(0, 1)[good], 0) <= TOL[dtype]
+    q, kc, vc, table, n = make(B, [900 + b for b in range(B)], 4, 2, 64, 16, TYPES[dtype], seed=12)
+    q[1] = q[1].abs()
+    kc[table[1, 3].long(), 5] = -float("inf")  # a score of -inf: not seen
+    x = (q, kc, vc, table, n)
+    assert rel_heads(gdr.paged_decode_step(*(t.to(dev) for t in x)), decode(*x), 1) <= TOL[dtype]

@@ -339,3 +339,21 @@ def test_lengths_that_change_between_replays():
         n.copy_(torch.tensor(lengths, dtype=torch.int32))
         graph.replay()
         assert torch.equal(o, f())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_values_that_are_none_are_not_hidden(dtype):
+    """NaN in a query reaches its output, and that one alone; in a key every later query of its heads."""
+    dev = cuda_device()
+    d = make(1, 300, 4, 2, 64, TYPES[dtype], seed=17)
+    ref = attention(**d)
+    d["q"][0, 140, 3, 5] = float("nan")
+    o = gdr.window_attention_fwd(*(d[n].to(dev) for n in "qkv"))[0]
+    bad = torch.zeros_like(o, dtype=torch.bool)
+    bad[0, 140, 3] = True
+    assert torch.equal(o.isnan(), bad)
+    close(o[:, :, :3], {"o": ref["o"][:, :, :3]}, "o", dtype)
+    d["k"][0, 200, 0] = float("nan")
+    o, lse, _ = gdr.window_attention_fwd(*(d[n].to(dev) for n in "qkv"), save_lse=True)
+    assert o[0, 200:, :2].isnan().all() and lse[0, :2, 200:].isnan().all()
+    close(o[:, :, 2:3], {"o": ref["o"][:, :, 2:3]}, "o", dtype)
