@@ -91,6 +91,7 @@ gdr_status check_paged(const gdr_paged_problem* p) {
     if (r != GDR_OK) return r;
     if (p->B > 65535) return GDR_ERR_UNSUPPORTED;
     if ((long long)p->pages * p->page_size >= 0xffffffffLL) return GDR_ERR_UNSUPPORTED;  // rows are counted in 32 bits
+    if ((long long)p->table_pages * p->page_size > 0x7fff0000LL) return GDR_ERR_UNSUPPORTED;    // tokens, and a tile more, in 31
     return GDR_OK;
 }
 

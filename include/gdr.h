@@ -433,7 +433,7 @@ gdr_status gdr_kv_append(const gdr_append_problem* p, const void* q, const void*
  * at the same time need one each. q, o and the caches 16-byte aligned. */
 typedef struct {
     int B, Hq, Hk, D; /* as gdr_window_problem */
-    int pages, page_size, table_pages; /* pages * page_size < 2^32 - 1 */
+    int pages, page_size, table_pages; /* pages * page_size < 2^32 - 1, table_pages * page_size <= 2^31 - 2^16 */
     int window, sinks;
     gdr_dtype dtype;
     float scale; /* > 0 */

@@ -129,7 +129,8 @@ def test_append_pointers(L):
 
 
 @pytest.mark.parametrize("kw,code", HEADS + [(dict(pages=-1), INVALID), (dict(page_size=0), INVALID), (dict(table_pages=-1), INVALID),
-                                             (dict(pages=1 << 20, page_size=1 << 12), UNSUPPORTED)])
+                                             (dict(pages=1 << 20, page_size=1 << 12), UNSUPPORTED),
+                                             (dict(table_pages=1 << 27), UNSUPPORTED)])
 def test_paged_problem(L, kw, code):
     p = paged(**kw)
     assert L.gdr_paged_decode_step(p, *put(6), FAKE, BIG, None) == code
