@@ -207,7 +207,7 @@ struct Bars {
     uint64_t lfull[2], lfree[2];  // dkv: statistics
 };
 
-// 64 columns as bf16 to TMEM, the second terms 32 columns on
+// 64 columns as bf16 to TMEM, the second terms 32 columns on (both: of a second half, which is empty with two terms, none are read)
 template <int TERMS>
 __device__ __forceinline__ void put_half(uint32_t at, const float (&x)[64]) {
 #pragma unroll
@@ -383,11 +383,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 auto sum = [&](int w, uint32_t from, int at) {  // both halves' columns, each from its column 64
                     const uint32_t d = tm + (w ? COL_SUM : COL_V), bd = lo_mnmajor(slot(at));
                     product_sum64(d, tm + from, bd, id_o, cur.m, cur.first);
-                    product_sum64(d, tm + from + 64, bd + step_mnmajor(4), id_o, cur.m - 64, false);
-                    if (TERMS == 2) {
-                        product_sum64(d, tm + from + 32, bd, id_o, cur.m, false);
-                        product_sum64(d, tm + from + 96, bd + step_mnmajor(4), id_o, cur.m - 64, false);
-                    }
+                    if (TERMS == 2) product_sum64(d, tm + from + 32, bd, id_o, cur.m, false);
+                    else product_sum64(d, tm + from + 64, bd + step_mnmajor(4), id_o, cur.m - 64, false);
                     done(at);
                 };
                 issue(0, cur, 0);
@@ -439,8 +436,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                             tc_fence_after();
                             issue(0, h, ring + 2);
                         }
-                        product_sum64(tm + COL_SUM, tm + COL_DP + 64 * h, lo_mnmajor(slot(ring)) + h * step_mnmajor(4), id_o, cur.m - 64 * h, cur.first && h == 0);
-                        if (TERMS == 2) product_sum64(tm + COL_SUM, tm + COL_DP + 64 * h + 32, lo_mnmajor(slot(ring)) + h * step_mnmajor(4), id_o, cur.m - 64 * h, false);
+                        if (TERMS == 1 || h == 0)
+                            product_sum64(tm + COL_SUM, tm + COL_DP + 64 * h, lo_mnmajor(slot(ring)) + h * step_mnmajor(4), id_o, cur.m - 64 * h, cur.first && h == 0);
+                        if (TERMS == 2 && h == 0) product_sum64(tm + COL_SUM, tm + COL_DP + 32, lo_mnmajor(slot(ring)), id_o, cur.m, false);
                         if (h == 1) {
                             done(ring);
                             if (cur.last) commit(&bar.sumfull);

@@ -258,11 +258,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (ok) {
                             tc_fence_after();
                             product_sum64(tm + COL_O + 128 * w, tm + COL_S + 128 * w, bd, id_o, m, begin[w]);
-                            if (TERMS == 2) {
-                                product_sum64(tm + COL_O + 128 * w, tm + COL_S + 128 * w + 64, bd, id_o, m, false);
-                                product_sum64(tm + COL_O + 128 * w, tm + COL_S + 128 * w + 96, bd + step_mnmajor(4), id_o, m - 64, false);
-                            }
-                            product_sum64(tm + COL_O + 128 * w, tm + COL_S + 128 * w + 32, bd + step_mnmajor(4), id_o, m - 64, false);
+                            if (TERMS == 2) product_sum64(tm + COL_O + 128 * w, tm + COL_S + 128 * w + 64, bd, id_o, m, false);
+                            else product_sum64(tm + COL_O + 128 * w, tm + COL_S + 128 * w + 32, bd + step_mnmajor(4), id_o, m - 64, false);
                             commit(&ofull[w][np[w] & 1]);
                         }
                         np[w]++;
@@ -359,10 +356,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                         p1 = exp2_fast(p1);
                         sum[k & 1] = add2(sum[k & 1], pair(p0, p1));
                         w[k] = pack_bf16(p0, p1);
-                        if (TERMS == 2) w2[k] = second_term(w[k], p0, p1);
+                        if (TERMS == 2 && e < 2) w2[k] = second_term(w[k], p0, p1);
                     }
-                    tmem_st16(at_s + 16 * e, w);
-                    if (TERMS == 2) tmem_st16(at_s + 64 + 16 * e, w2);
+                    if (TERMS == 1 || e < 2) tmem_st16(at_s + 16 * e, w);
+                    if (TERMS == 2 && e < 2) tmem_st16(at_s + 64 + 16 * e, w2);
                 }
                 float s0, s1;
                 unpair(add2(sum[0], sum[1]), s0, s1);
