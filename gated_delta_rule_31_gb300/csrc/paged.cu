@@ -102,6 +102,9 @@ constexpr int STAGES = 3;
 constexpr uint32_t STEP_BYTES = 8192;  // K and V of a warp's step
 template <typename T, int D>
 constexpr int step_tokens() { return (int)STEP_BYTES / (2 * D * (int)sizeof(T)); }
+// Floats of a head's sums that a run leaves: O, m, l.
+template <int D>
+constexpr int part_stride() { return D + 4; }
 // A part for each warp; with clusters, whose CTAs have one walk each, they and the CTA's go over the copied tiles.
 template <int D, int CLUSTER, int WARPS>
 constexpr int merge_bytes() { return (WARPS + (CLUSTER ? 1 : 0)) * HEADS * (D + 2) * 4; }
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) paged_kernel(PagedArgs 
     auto flip = [](int r) { return BF16 ? (D == 32 ? (r >> 1) & 3 : r & 7) : (r & (8 / PARTS - 1)) * PARTS; };
     static_assert(merge_bytes<D, CLUSTER, WARPS>() <= WARPS * STAGES * STEP_BYTES, "parts over the tiles");
     extern __shared__ __align__(128) uint8_t sm[];
-    __shared__ uint32_t there[WARPS][STAGES][2];  // which tokens of a step are there, as bits
+    __shared__ uint32_t there[WARPS][STAGES][(STEP + 31) / 32];  // which tokens of a step are there, as bits
     linear::wait_kernel_before();  // ahead of every read; the join, which may start then, has the same guarantee
     linear::next_kernel_may_start();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = a.Hq / a.Hk, walks = a.Hk * blocks;
@@ -474,8 +477,9 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) paged_kernel(PagedArgs 
             }
         }
         __syncthreads();
+        constexpr int PART = CLUSTER ? D + 2 : part_stride<D>();
         // of a cluster's CTA, or of a run that has a part of the walk: left to be joined
-        float* part = CLUSTER ? merge + WARPS * HEADS * (D + 2) : a.parts + (size_t)(2 * blockIdx.x + (segment > 0)) * HEADS * (D + 2);
+        float* part = CLUSTER ? merge + WARPS * HEADS * (D + 2) : a.parts + (size_t)(2 * blockIdx.x + (segment > 0)) * HEADS * PART;
         for (int i = tid; i < ng * D; i += THREADS) {
             const int g = i / D, d = i % D;
             const float* from = merge + g * (D + 2);
@@ -492,10 +496,10 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) paged_kernel(PagedArgs 
             if (out.whole) {
                 put(static_cast<T*>(a.o) + (q0 + g) * D + d, sum == 0.f ? 0.f : x / sum);
             } else {
-                part[g * (D + 2) + d] = x;
+                part[g * PART + d] = x;
                 if (d == 0) {
-                    part[g * (D + 2) + D] = top;
-                    part[g * (D + 2) + D + 1] = sum;
+                    part[g * PART + D] = top;
+                    part[g * PART + D + 1] = sum;
                 }
             }
         }
@@ -535,69 +539,89 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) paged_kernel(PagedArgs 
             for (int i = tid; i < a.Hq * D; i += THREADS) put(static_cast<T*>(a.o) + (size_t)b * a.Hq * D + i, 0.f);
 }
 
-// Joins the walk that the border before run blockIdx.x + 1 cuts, if that border is the first in it: the maximum of each
-// head over the runs by a warp, then the sums by four groups of threads, each every fourth run, in the same order always.
-constexpr int JOIN_THREADS = 512, JOIN_GROUPS = 4;
+// Joins the walks that borders of runs cut, two borders to a CTA, four warps each. A walk in n runs has n - 1 borders, whose warps share
+// its heads and channels: a warp takes a head's maximum, its sum, and then a slice of its channels at a time, 128 where runs are few,
+// 16 and every eighth run to four lanes where they are many, 4 and every 32nd to one where very many; the order is always the same. It needs next to no shared memory, so that its
+// CTAs are there, with the lengths summed, when the last run ends (with 27 KB, after it: 1 to 2 us later). 30 sequences of 200 tokens 13.3
+// us in a graph (15.2), one of 524288 with a single key head, all runs in one walk, 69 (81 with groups of four lanes at least).
+constexpr int JOIN_THREADS = 256;
+static_assert(RUNS % 2 == 0, "borders");
 
 template <int D, typename T>
 __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(PagedArgs a, int blocks, int tile) {
-    __shared__ float weight[HEADS][RUNS], sum[HEADS], acc[JOIN_GROUPS][HEADS][D];
-    __shared__ int slot[RUNS];
     linear::next_kernel_may_start();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int group = a.Hq / a.Hk, walks = a.Hk * blocks, run = blockIdx.x + 1, runs = gridDim.x + 1;
-    Place at;
-    long long begin, end;
-    const long long total = find<JOIN_THREADS>(a, tile, walks, run, runs, at, begin, end);
-    const long long tiles = begin < total ? Seen(a, at.b).tiles(tile) : 1, start = at.before * walks;
-    const int walk = (int)((begin - start) / tiles);
-    const long long w0 = start + walk * tiles, w1 = w0 + tiles;
-    const bool ours = begin < total && w0 < begin && total * (run - 1) / runs <= w0;
-    const int n = ours ? (int)((w1 * runs - 1) / total) - (run - 1) + 1 : 0;  // runs that hold tiles of the walk, from run - 1 on
-    for (int i = tid; i < n; i += JOIN_THREADS) {
-        const int r = run - 1 + i;
-        const long long rb = total * r / runs, re = total * (r + 1) / runs;
-        slot[i] = rb < re ? 2 * r + (rb < w0) : -1;
+    const int lane = threadIdx.x & 31, which = threadIdx.x / 128, warp = threadIdx.x / 32 & 3;
+    const int group = a.Hq / a.Hk, walks = a.Hk * blocks, run = 2 * blockIdx.x + 1 + which;
+    Place at = {0, 0};
+    long long begin = 0, total = 0;
+#pragma unroll
+    for (int z = 0; z < 2; z++) {
+        Place p;
+        long long b, e;
+        total = find<JOIN_THREADS>(a, tile, walks, 2 * blockIdx.x + 1 + z, RUNS, p, b, e);
+        if (z == which && b < total) at = p;
+        if (z == which) begin = b;
     }
+    const bool some = begin < total;
+    const long long tiles = some ? Seen(a, at.b).tiles(tile) : 1, start = at.before * walks;
+    const int walk = some ? (int)((begin - start) / tiles) : 0;
+    const long long w0 = start + walk * tiles, w1 = w0 + tiles;
+    // runs r0 .. r0 + n - 1 hold tiles of the walk
+    const int r0 = some ? (int)(((w0 + 1) * RUNS - 1) / total) : 0, n = some ? (int)((w1 * RUNS - 1) / total) - r0 + 1 : 0;
     linear::wait_kernel_before();
-    __syncthreads();
-    if (!ours) return;
+    if (!some || begin == w0) return;  // nothing is cut here
     const int hk = walk / blocks, g0 = walk % blocks * HEADS, ng = min(HEADS, group - g0);
     const size_t q0 = (size_t)at.b * a.Hq + hk * group + g0;
-    for (int g = warp; g < ng; g += JOIN_THREADS / 32) {
-        float top = -INFINITY, all = 0.f;
-        for (int i = lane; i < n; i += 32) {
-            const float m = slot[i] < 0 ? -INFINITY : a.parts[((size_t)slot[i] * HEADS + g) * (D + 2) + D];
-            weight[g][i] = m;
-            top = fmaxf(top, m);
-        }
+    auto part = [&](int i, int g) -> const float* {  // null: a run without tiles
+        const int r = r0 + i;
+        const long long rb = total * r / RUNS, re = total * (r + 1) / RUNS;
+        return rb < re ? a.parts + ((size_t)(2 * r + (rb < w0)) * HEADS + g) * part_stride<D>() : nullptr;
+    };
+    const int groups = n > 64 ? 32 : n > 8 ? 8 : 128 / D, lanes = 32 / groups, slices = D / (4 * lanes), units = ng * slices, step = 4 * (n - 1);
+    for (int u = (run - r0 - 1) * 4 + warp; u < units; u += 2 * step) {
+        int g[2], c[2];
+        float m[2], l[2], top[2], all[2], x[2][4] = {};
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        for (int i = lane; i < n; i += 32) {
-            const float m = weight[g][i], f = m == -INFINITY ? 0.f : exp2f(m - top);
-            weight[g][i] = f;
-            if (slot[i] >= 0) all = fmaf(f, a.parts[((size_t)slot[i] * HEADS + g) * (D + 2) + D + 1], all);
+        for (int z = 0; z < 2; z++) {
+            const int v = u + z * step < units ? u + z * step : u;
+            g[z] = v / slices;
+            c[z] = (v % slices * lanes + lane % lanes) * 4;
+            const float* p = lane < n ? part(lane, g[z]) : nullptr;
+            top[z] = m[z] = p ? p[D] : -INFINITY;
+            l[z] = p ? p[D + 1] : 0.f;
+            for (int i = lane + 32; i < n; i += 32)
+                if (const float* y = part(i, g[z])) top[z] = fmaxf(top[z], y[D]);
         }
-        all = warp_sum(all);
-        if (lane == 0) sum[g] = all;
-    }
-    __syncthreads();
-    constexpr int COLS = JOIN_THREADS / JOIN_GROUPS;
-    const int part = tid / COLS;
-    for (int e = tid % COLS; e < ng * D; e += COLS) {
-        const int g = e / D, d = e % D;
-        float x = 0.f;
-#pragma unroll 4
-        for (int i = part; i < n; i += JOIN_GROUPS) {
-            if (slot[i] >= 0) x = fmaf(weight[g][i], a.parts[((size_t)slot[i] * HEADS + g) * (D + 2) + d], x);
+        auto weight = [&](float m, float top) { return m == -INFINITY ? 0.f : exp2f(m - top); };
+#pragma unroll
+        for (int z = 0; z < 2; z++) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top[z] = fmaxf(top[z], __shfl_xor_sync(0xffffffffu, top[z], o));
+            all[z] = weight(m[z], top[z]) * l[z];
+            for (int i = lane + 32; i < n; i += 32)
+                if (const float* y = part(i, g[z])) all[z] = fmaf(weight(y[D], top[z]), y[D + 1], all[z]);
+            all[z] = warp_sum(all[z]);
         }
-        acc[part][g][d] = x;
-    }
-    __syncthreads();
-    for (int e = tid; e < ng * D; e += JOIN_THREADS) {
-        const int g = e / D, d = e % D;
-        const float x = (acc[0][g][d] + acc[1][g][d]) + (acc[2][g][d] + acc[3][g][d]);
-        put(static_cast<T*>(a.o) + (q0 + g) * D + d, sum[g] == 0.f ? 0.f : x / sum[g]);
+#pragma unroll 2
+        for (int i = lane / lanes; i < n; i += groups)
+#pragma unroll
+            for (int z = 0; z < 2; z++)
+                if (const float* y = part(i, g[z])) {
+                    const float f = weight(y[D], top[z]);
+                    const float4 v = *reinterpret_cast<const float4*>(y + c[z]);
+                    x[z][0] = fmaf(f, v.x, x[z][0]);
+                    x[z][1] = fmaf(f, v.y, x[z][1]);
+                    x[z][2] = fmaf(f, v.z, x[z][2]);
+                    x[z][3] = fmaf(f, v.w, x[z][3]);
+                }
+        for (int o = lanes; o < 32; o *= 2)
+#pragma unroll
+            for (int e = 0; e < 8; e++) x[e / 4][e % 4] += __shfl_xor_sync(0xffffffffu, x[e / 4][e % 4], o);
+#pragma unroll
+        for (int z = 0; z < 2; z++)
+            if (lane < lanes && (z == 0 || u + step < units))
+#pragma unroll
+                for (int e = 0; e < 4; e++) put(static_cast<T*>(a.o) + (q0 + g[z]) * D + c[z] + e, all[z] == 0.f ? 0.f : x[z][e] / all[z]);
     }
 }
 
@@ -612,7 +636,7 @@ cudaError_t runs(const PagedArgs& a, cudaStream_t st) {
     trace_end(st);
     if (e != cudaSuccess) return e;
     trace_begin("paged_join", st);
-    e = launch_after(paged_join_kernel<D, T>, dim3(RUNS - 1), JOIN_THREADS, 0, st, true, a, blocks, RUN_WARPS * step_tokens<T, D>());
+    e = launch_after(paged_join_kernel<D, T>, dim3(RUNS / 2), JOIN_THREADS, 0, st, true, a, blocks, RUN_WARPS * step_tokens<T, D>());
     trace_end(st);
     return e;
 }
@@ -670,7 +694,7 @@ cudaError_t step(const PagedArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-size_t paged_parts_bytes(int D) { return (size_t)2 * RUNS * HEADS * (D + 2) * sizeof(float); }
+size_t paged_parts_bytes(int D) { return (size_t)2 * RUNS * HEADS * (D + 4) * sizeof(float); }
 
 cudaError_t launch_paged_step(const PagedArgs& a, cudaStream_t st) { return a.bf16 ? step<__nv_bfloat16>(a, st) : step<float>(a, st); }
 
