@@ -14,8 +14,8 @@
 // bf16: products by mma.m16n8k16 with the 8 heads as columns, S^T = K q^T and O^T += V^T P^T: the tokens are rows, so no row is
 // spent on heads that are not there, and a thread keeps the same two heads in S, m, l and O. (tcgen05 would take 128 rows
 // for the 8.) 64 sequences of up to 16384 tokens, 8 key heads of 128: 2.1 GB in 335 us, 0.95 of a copy's rate; 128 with a window of 1024:
-// 90 us, 0.84; the sums of runs take 5 us of either, the lengths' sum and the first copies 5. Eight warps to a CTA and 152 runs: 340
-// and 99. fp32: products on the CUDA cores, for S 32 channels of one token a lane, for O 4 channels of 8 tokens a lane.
+// 89 us, 0.85; the join takes 4 us of either, the lengths' sum and the first copies 5. Eight warps to a CTA and 152 runs: 340 and
+// 99; warps that pass over tiles without tokens of theirs: 0.5 us more. fp32: products on the CUDA cores, for S 32 channels of one token a lane, for O 4 channels of 8 tokens a lane.
 //
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -180,8 +180,8 @@ struct Cursor {
     __device__ __forceinline__ int token(int x) const { return x < first ? x : lo + (x - first); }
 };
 
-// CLUSTER: the walks' tiles are not dealt out in a row: each walk has a cluster of that many CTAs, which join through each other's
-// shared memory.
+// CLUSTER: the walks' tiles are not dealt out in a row: each walk has a cluster of that many CTAs (1: a CTA), which join through each
+// other's shared memory.
 template <typename T, int D, int CLUSTER, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) paged_kernel(PagedArgs a, int blocks) {
     constexpr bool BF16 = sizeof(T) == 2;
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) paged_kernel(PagedArgs 
         in.tiles = seen.tiles(TILE);
         in.t = (int)((long long)in.tiles * rank / CLUSTER);
         in.t1 = (int)((long long)in.tiles * (rank + 1) / CLUSTER);
-        in.whole = false;
+        in.whole = CLUSTER == 1;
         in.tile = in.t;
         end = in.t1;
         some = in.tile < end;
@@ -504,7 +504,8 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) paged_kernel(PagedArgs 
             }
         }
         segment++;
-        if constexpr (CLUSTER > 0) {
+        if constexpr (CLUSTER == 1) return;
+        if constexpr (CLUSTER > 1) {
             cluster_sync();
             // a CTA joins every CLUSTER-th channel, the CTAs' parts in order
             const uint32_t mine = smem_u32(part);
@@ -541,9 +542,9 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) paged_kernel(PagedArgs 
 
 // Joins the walks that borders of runs cut, two borders to a CTA, four warps each. A walk in n runs has n - 1 borders, whose warps share
 // its heads and channels: a warp takes a head's maximum, its sum, and then a slice of its channels at a time, 128 where runs are few,
-// 16 and every eighth run to four lanes where they are many, 4 and every 32nd to one where very many; the order is always the same. It needs next to no shared memory, so that its
-// CTAs are there, with the lengths summed, when the last run ends (with 27 KB, after it: 1 to 2 us later). 30 sequences of 200 tokens 13.3
-// us in a graph (15.2), one of 524288 with a single key head, all runs in one walk, 69 (81 with groups of four lanes at least).
+// 16 and every eighth run to four lanes where they are many, 4 and every 32nd to one where very many; the order is always the same. It
+// needs next to no shared memory, so that its CTAs are there, with the lengths summed, when the last run ends (with 27 KB, after it: 1
+// to 2 us later). One sequence of 524288 with a single key head, all runs in one walk: 69 us in a graph (four lanes at least: 81).
 constexpr int JOIN_THREADS = 256;
 static_assert(RUNS % 2 == 0, "borders");
 
@@ -666,16 +667,20 @@ cudaError_t clusters(const PagedArgs& a, cudaStream_t st) {
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// The CTAs of a cluster for each walk, where walks are few and sequences not long (one launch, and no lengths to sum up first): the
-// most of 8, 4, 2 that the SMs have room for; 0: runs. On the GPU alone, 32 heads on 8, bf16, in us with clusters and with
-// runs: one sequence of 100 tokens 5 and 11, 4096 8 and 26, 16384 19 and 33, 32768 34 and 45; four of 4096 12 and 26, of 16384 43
-// and 62. One long sequence among short ones waits for its clusters alone, hence the limit on the table's room for a CTA: 2 MB.
+// The CTAs for each walk, 1 or a cluster of 2, 4, 8, where walks are few and the table's sequences not long (one launch, and no lengths
+// to sum up first); 0: runs. A cluster starts and joins 1 to 1.5 us later than a lone CTA, so it has as many as leave a CTA 96 KB of K
+// and V or less, and as are there at once: 76 clusters of 2, 36 of 4, 15 of 8 (one more takes a second round). On the GPU alone, 32
+// heads on 8, bf16, in us with 1, 2, 4, 8 CTAs and with runs: one sequence of 64 tokens 3.2, 4.1, 4.6, 4.9 and 6.5, 512 6.1, 5.4, 4.8,
+// 5.2, 4096 32, 18, 11, 7.6 and 26. Lone CTAs: 30 sequences of 200 tokens 7.9 (runs 13.3), of 1000 24 (28), 76 of 200 15.4 (14.2).
+// One long sequence among short ones waits for its CTAs alone (64 KB a us), hence the limits on the table's room: 2 MB a CTA, 512 KB
+// with one.
 int cluster_of(const PagedArgs& a) {
     const long long walks = (long long)a.B * a.Hk * ((a.Hq / a.Hk + HEADS - 1) / HEADS);
-    int n = 8;
-    while (n > 1 && walks * n > 152) n /= 2;
     const long long bytes = (long long)a.table_pages * a.page_size * a.D * (a.bf16 ? 4 : 8);  // K and V of the longest walk
-    return n > 1 && bytes <= (long long)n * (2 << 20) ? n : 0;
+    auto fit = [](int n) { return n == 8 ? 15 : n == 4 ? 36 : n == 2 ? 76 : 2 * 152; };
+    int n = 1;
+    while (n < 8 && walks <= fit(2 * n) && bytes > (long long)n * (96 << 10)) n *= 2;
+    return walks <= fit(n) && bytes <= (n > 1 ? (long long)n * (2 << 20) : 512 << 10) ? n : 0;
 }
 
 template <typename T, int D>
@@ -684,6 +689,7 @@ cudaError_t step_of(const PagedArgs& a, cudaStream_t st) {
         case 8: return clusters<T, D, 8>(a, st);
         case 4: return clusters<T, D, 4>(a, st);
         case 2: return clusters<T, D, 2>(a, st);
+        case 1: return clusters<T, D, 1>(a, st);
         default: return runs<T, D>(a, st);
     }
 }

@@ -8,8 +8,10 @@
 //     dv = P^T do, dk = scale dS^T q over the queries that see a tile of keys, of all heads that share it.
 // The two walk the pairs separately, 7 products for the 5 that one walk would need, so that neither adds into
 // memory that another CTA adds into: the order of every sum is fixed.
-// Tiles come in asynchronously, one ahead; products by fp32 pairs. Bound by shared-memory reads (4 x 4 outputs a thread: 4 products
-// to a value read) and, at few tiles, by each CTA's chain: 2 x 777 tokens of 8 heads of 64, window 300: 61, 74 and 139 us.
+// Tiles come in asynchronously, one ahead; products by fp32 pairs. 4096 tokens of 32 heads on 8 of 128: forward 3.6 ms, dq 5.2, dkv 6.7, half
+// of the FMA units' rate: two warps to a scheduler wait for one another's results, and what feeds the products takes issue slots.
+// Not kept: threads with 4 x 8 outputs, four warps (5.1, 5.5, 7.4); warps of 4 x 8 threads, whose reads share addresses (the same, so
+// shared memory is not it). At few tiles each CTA's chain: 2 x 777 tokens of 8 heads of 64, window 300: 62 to 70, 74, 79 and the sums 18 us.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>

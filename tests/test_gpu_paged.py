@@ -293,3 +293,15 @@ def test_values_that_are_none_are_not_hidden(B, dtype):
     kc[table[1, 3].long(), 5] = -float("inf")  # a score of -inf: not seen
     x = (q, kc, vc, table, n)
     assert rel_heads(gdr.paged_decode_step(*(t.to(dev) for t in x)), decode(*x), 1) <= TOL[dtype]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("room", [0, 100, 390, 1300, 5000])
+@pytest.mark.parametrize("B,Hk", [(1, 1), (5, 3), (8, 2), (9, 4), (37, 1), (19, 4), (77, 1), (38, 8), (61, 5)])
+def test_walks_and_room(B, Hk, room, dtype):
+    """Across the numbers of walks and the lengths of tables where CTAs alone, clusters and runs take them."""
+    n = [(53 * i * i + 7) % 190 for i in range(B)]
+    q, kc, vc, table, lengths = make(B, n, 2 * Hk, Hk, 128, 16, TYPES[dtype], seed=B)
+    wide = torch.full((B, table.shape[1] + -(-room // 16)), -1, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    check((q, kc, vc, wide, lengths), dtype, window=150, sinks=3)
