@@ -437,22 +437,26 @@ __global__ void __launch_bounds__(THREADS) window_dkv_kernel(WindowArgs a, CutAr
     add_rows<D>(to_v, stride, live, dv, 1.f, begun);
 }
 
-// The sums of the pieces of a tile, in order.
+// The sums of the pieces of a tile, in order: a CTA for 8 of its 64 rows.
+constexpr int SUM_ROWS = 8;
 __global__ void __launch_bounds__(256) window_sum_kernel(WindowArgs a, CutArgs cut) {
     const WindowShape& s = a.s;
-    const int kt = blockIdx.x, hk = blockIdx.y, b = blockIdx.z, pieces = cut.pieces_of(kt), rows = min(N, s.T - kt * N);
-    if (pieces == 1) return;
-    const float* part = a.parts + (size_t)cut.part(b * s.Hk + hk, kt, s.B * s.Hk) * 2 * N * s.D;
-    for (int w = 0; w < 2; w++)
-        for (int i = 4 * threadIdx.x; i < rows * s.D; i += 1024) {
-            float4 x = get4(part + (size_t)w * N * s.D + i);
-            for (int p = 1; p < pieces; p++) {
-                const float4 y = get4(part + (size_t)(2 * p + w) * N * s.D + i);
-                x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
-            }
-            const int r = i / s.D, d = i - r * s.D;
-            *reinterpret_cast<float4*>(static_cast<float*>(w ? a.dv : a.dk) + (((size_t)b * s.T + kt * N + r) * s.Hk + hk) * s.D + d) = x;
+    const int kt = blockIdx.x / (N / SUM_ROWS), r0 = blockIdx.x % (N / SUM_ROWS) * SUM_ROWS, hk = blockIdx.y, b = blockIdx.z;
+    const int pieces = cut.pieces_of(kt), rows = min(SUM_ROWS, s.T - kt * N - r0);
+    if (pieces == 1 || rows <= 0) return;
+    const float* part = a.parts + (size_t)cut.part(b * s.Hk + hk, kt, s.B * s.Hk) * 2 * N * s.D + r0 * s.D;
+    const size_t out = (((size_t)b * s.T + kt * N + r0) * s.Hk + hk) * s.D;
+    for (int i = 4 * threadIdx.x; i < 2 * SUM_ROWS * s.D; i += 1024) {
+        const int w = i / (SUM_ROWS * s.D), at = i - w * SUM_ROWS * s.D, r = at / s.D;
+        if (r >= rows) continue;
+        float4 x = get4(part + (size_t)w * N * s.D + at);
+#pragma unroll 4
+        for (int p = 1; p < pieces; p++) {
+            const float4 y = get4(part + (size_t)(2 * p + w) * N * s.D + at);
+            x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
         }
+        *reinterpret_cast<float4*>(static_cast<float*>(w ? a.dv : a.dk) + out + (size_t)r * s.Hk * s.D + at - r * s.D) = x;
+    }
 }
 
 // One CTA an SM (three of 32 channels); two pairs of tiles, some 25 us, are a piece at least.
@@ -490,7 +494,7 @@ cudaError_t bwd(const WindowArgs& a, cudaStream_t st) {
     if (cudaError_t e = cudaGetLastError()) return e;
     if (cut.parts == 0) return cudaSuccess;
     trace_begin("window_sum", st);
-    window_sum_kernel<<<dim3(cut.tiles, a.s.Hk, a.s.B), 256, 0, st>>>(a, c);
+    window_sum_kernel<<<dim3(cut.tiles * (N / SUM_ROWS), a.s.Hk, a.s.B), 256, 0, st>>>(a, c);
     trace_end(st);
     return cudaGetLastError();
 }
